@@ -11,7 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, byref, c_char_p, c_float, c_int32, c_size_t, c_void_p
+from ctypes import POINTER, byref, c_char_p, c_float, c_int32, c_int64, c_size_t, c_void_p
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "lib", "libllama_block.so")
@@ -65,6 +65,16 @@ class llama_kv_cache(ctypes.Structure):
     _fields_ = [("k", c_void_p), ("v", c_void_p), ("max_batch", c_int32), ("max_seq_len", c_int32)]
 
 
+class llama_paged_kv_cache(ctypes.Structure):
+    _fields_ = [("k", c_void_p), ("v", c_void_p), ("page_table", c_void_p), ("n_pages", c_int32),
+                ("page_size", c_int32), ("max_pages", c_int32), ("table_stride", c_int32), ("page_stride", c_int64)]
+
+
+class llama_packed_batch(ctypes.Structure):
+    _fields_ = [("q_offsets", c_void_p), ("kv_lens", c_void_p), ("n_seqs", c_int32), ("n_tokens", c_int32),
+                ("max_kv_len", c_int32)]
+
+
 _lib = None
 
 
@@ -95,6 +105,8 @@ def load() -> ctypes.CDLL:
                                       POINTER(llama_kv_cache), c_void_p, c_void_p, c_void_p]),
         "llama_stack_forward": (st, [c_void_p, c_void_p, c_int32, c_int32, c_int32, POINTER(llama_kv_cache),
                                      c_void_p, c_void_p]),
+        "llama_stack_score": (st, [c_void_p, c_void_p, c_int32, c_int32, c_int32, POINTER(llama_kv_cache), c_void_p,
+                                   c_void_p, c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_void_p]),
         "llama_stack_destroy": (None, [c_void_p]),
         "llama_stack_device_status": (st, [c_void_p]),
         "llama_kv_cache_bytes": (c_size_t, [POINTER(llama_config), c_int32, c_int32]),
@@ -117,6 +129,20 @@ def load() -> ctypes.CDLL:
                                      c_void_p]),
         "llama_op_attention_decode_noalloc": (st, [c_void_p, POINTER(llama_kv_cache), c_void_p, c_int32, c_int32,
                                                    c_int32, c_int32, c_int32, c_void_p]),
+        "llama_op_rope_kv_write_paged": (st, [c_int32, c_void_p, c_void_p, POINTER(llama_paged_kv_cache),
+                                              POINTER(llama_packed_batch), c_void_p, c_int32, c_int32, c_int32, c_int32,
+                                              c_int32, c_void_p, c_void_p]),
+        "llama_op_attention_packed_workspace_bytes": (c_size_t, [c_int32, POINTER(llama_packed_batch), c_int32, c_int32,
+                                                                 c_int32]),
+        "llama_op_attention_packed": (st, [c_int32, c_void_p, POINTER(llama_paged_kv_cache),
+                                           POINTER(llama_packed_batch), c_void_p, c_int32, c_int32, c_int32, c_void_p,
+                                           c_size_t, c_void_p, c_void_p]),
+        "llama_op_attention_paged_decode_workspace_bytes": (c_size_t, [c_int32] * 6),
+        "llama_op_attention_paged_decode": (st, [c_int32, c_void_p, POINTER(llama_paged_kv_cache), c_void_p, c_int32,
+                                                 c_int32, c_void_p, c_int32, c_int32, c_int32, c_void_p, c_size_t,
+                                                 c_void_p, c_void_p]),
+        "llama_op_token_logprobs": (st, [c_int32, c_void_p, c_int64, c_void_p, c_int32, c_int32, c_void_p, c_void_p,
+                                         c_int32, c_void_p, c_void_p, c_void_p, c_void_p]),
         "llama_op_rope_kv_write": (st, [c_int32, c_void_p, c_void_p, POINTER(llama_kv_cache), c_void_p, c_int32,
                                         c_int32, c_int32, c_int32, c_int32, c_int32, c_int32, c_int32, c_void_p]),
     }
@@ -227,6 +253,16 @@ def llama_stack_generate(stk, prompt, B, S_prompt, start_pos, n_new, kv_list, ou
                                        _p(logits), _stream(stream))
 
 
+LLAMA_LOGPROBS_MAX_TOP = 32
+
+
+def llama_stack_score(stk, tokens, B, S, start_pos, kv_list, targets, logits, logprobs, entropy=None, top_k=0,
+                      top_ids=None, top_logprobs=None, stream=None) -> int:
+    arr = (llama_kv_cache * max(len(kv_list), 1))(*kv_list)
+    return load().llama_stack_score(stk, _p(tokens), B, S, start_pos, arr, _p(targets), _p(logits), _p(logprobs),
+                                    _p(entropy), top_k, _p(top_ids), _p(top_logprobs), _stream(stream))
+
+
 def llama_stack_destroy(stk) -> None:
     load().llama_stack_destroy(stk)
 
@@ -319,6 +355,53 @@ LLAMA_NOALLOC_SCRATCH_BYTES = 32 << 20
 def llama_op_attention_decode_noalloc(q, kv: llama_kv_cache, o, B, start_pos, H, G, D, stream=None) -> int:
     """Decode attention using the library's built-in scratch array (no device allocation)."""
     return load().llama_op_attention_decode_noalloc(_p(q), byref(kv), _p(o), B, start_pos, H, G, D, _stream(stream))
+
+
+LLAMA_PACKED_MAX_SEQS = 4096
+
+
+def make_paged_kv_cache(k, v, page_table) -> llama_paged_kv_cache:
+    """Struct of a page pool: k, v tensors [n_pages][n_kv_heads][page_size][d_head] (dense within a page, the same
+    stride from page to page), page_table int32 [n_seqs][max_pages] (dense rows)."""
+    return llama_paged_kv_cache(_p(k), _p(v), _p(page_table), k.shape[0], k.shape[2], page_table.shape[1],
+                                page_table.stride(0), k.stride(0))
+
+
+def make_packed_batch(q_offsets, kv_lens, n_tokens, max_kv_len) -> llama_packed_batch:
+    """Struct of a packed batch: q_offsets int32 [n_seqs + 1], kv_lens int32 [n_seqs] (device)."""
+    return llama_packed_batch(_p(q_offsets), _p(kv_lens), kv_lens.shape[0], n_tokens, max_kv_len)
+
+
+def llama_op_rope_kv_write_paged(dtype, qkv, q_out, kv: llama_paged_kv_cache, batch: llama_packed_batch, table,
+                                 table_max_seq, H, G, D, layout=0, status=None, stream=None) -> int:
+    return load().llama_op_rope_kv_write_paged(dtype, _p(qkv), _p(q_out), byref(kv), byref(batch), _p(table),
+                                               table_max_seq, H, G, D, layout, _p(status), _stream(stream))
+
+
+def llama_op_attention_packed_workspace_bytes(dtype, batch: llama_packed_batch, H, G, D) -> int:
+    return load().llama_op_attention_packed_workspace_bytes(dtype, byref(batch), H, G, D)
+
+
+def llama_op_attention_packed(dtype, q, kv: llama_paged_kv_cache, batch: llama_packed_batch, o, H, G, D,
+                              workspace=None, workspace_bytes=0, status=None, stream=None) -> int:
+    return load().llama_op_attention_packed(dtype, _p(q), byref(kv), byref(batch), _p(o), H, G, D, _p(workspace),
+                                            workspace_bytes, _p(status), _stream(stream))
+
+
+def llama_op_attention_paged_decode_workspace_bytes(dtype, n_seqs, max_kv_len, H, G, D) -> int:
+    return load().llama_op_attention_paged_decode_workspace_bytes(dtype, n_seqs, max_kv_len, H, G, D)
+
+
+def llama_op_attention_paged_decode(dtype, q, kv: llama_paged_kv_cache, kv_lens, n_seqs, max_kv_len, o, H, G, D,
+                                    workspace=None, workspace_bytes=0, status=None, stream=None) -> int:
+    return load().llama_op_attention_paged_decode(dtype, _p(q), byref(kv), _p(kv_lens), n_seqs, max_kv_len, _p(o), H,
+                                                  G, D, _p(workspace), workspace_bytes, _p(status), _stream(stream))
+
+
+def llama_op_token_logprobs(dtype, logits, row_stride, targets, T, V, logprobs, entropy=None, top_k=0, top_ids=None,
+                            top_logprobs=None, status=None, stream=None) -> int:
+    return load().llama_op_token_logprobs(dtype, _p(logits), row_stride, _p(targets), T, V, _p(logprobs), _p(entropy),
+                                          top_k, _p(top_ids), _p(top_logprobs), _p(status), _stream(stream))
 
 
 def check(status: int, what: str = "llama call") -> None:

@@ -1,0 +1,47 @@
+// Internal launch wrappers of the packed / paged operators (not part of the C ABI).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+
+#include "common.cuh"
+#include "paged.cuh"
+
+namespace llama {
+
+// RoPE on the q and k of packed rows and the write of k and v into their pages
+// (paged_write.cu); halves as for launch_rope_kv.
+template <typename T>
+cudaError_t launch_rope_kv_paged(const T *qkv, T *q_out, T *k, T *v, const PagedView &pv, const PackedView &b,
+                                 const float2 *table, int table_max_seq, int H, int G, int D, int halves, int *status,
+                                 cudaStream_t st);
+
+// CUDA-core attention over pages (paged_simt.cu): fp32, and the head widths that
+// have no tensor-core kernel.
+template <typename T>
+cudaError_t launch_packed_simt(const T *q, const T *k, const T *v, T *o, const PagedView &pv, const PackedView &b,
+                               int H, int G, int D, int *status, cudaStream_t st);
+// Split of one sequence's keys over CTAs: parts of `chunk` keys, `n` of them at
+// the longest length the call allows.
+struct DecodeSplit {
+  int chunk = 0, n = 1;
+};
+DecodeSplit paged_decode_simt_split(int n_seqs, int max_kv_len, int H, int G);
+template <typename T>
+cudaError_t launch_paged_decode_simt(const T *q, const T *k, const T *v, T *o, const PagedView &pv,
+                                     const int *kv_lens, int n_seqs, int max_kv_len, int H, int G, int D, float *part,
+                                     int *status, cudaStream_t st);
+// o[i][h] = the parts of part [n_seqs][H][split.n][D + 2] joined (paged_simt.cu).
+template <typename T>
+cudaError_t launch_paged_combine(const float *part, T *o, const PagedView &pv, const int *kv_lens, int n_seqs,
+                                 int max_kv_len, int H, int D, DecodeSplit split, cudaStream_t st);
+
+// Log-probabilities, entropy and top_k of logits rows (logprobs.cu); targets
+// and logprobs may both be null, entropy too.  A target outside [0, V) other than
+// -1 records the code bad_target.
+template <typename T>
+cudaError_t launch_token_logprobs(const T *logits, long long row_stride, const int *targets, int rows, int V,
+                                  float *logprobs, float *entropy, int top_k, int *top_ids, float *top_logprobs,
+                                  int *status, int bad_target, cudaStream_t st);
+
+}  // namespace llama

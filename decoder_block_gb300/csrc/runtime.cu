@@ -29,6 +29,7 @@
 
 #include "llama_block.h"
 #include "kernels.h"
+#include "paged_kernels.h"
 #include "tc_kernels.h"
 
 using namespace llama;
@@ -1023,6 +1024,30 @@ llama_status llama_stack_forward(llama_stack *stk, const int32_t *tokens, int32_
   s = stack_layers(stk, tokens, B, S, start_pos, kv, st, &hidden);
   if (s != LLAMA_OK) return s;
   return stack_head(stk, hidden, B * S, logits, st);
+}
+
+llama_status llama_stack_score(llama_stack *stk, const int32_t *tokens, int32_t B, int32_t S, int32_t start_pos,
+                               const llama_kv_cache *kv, const int32_t *targets, float *logits, float *logprobs,
+                               float *entropy, int32_t top_k, int32_t *top_ids, float *top_logprobs,
+                               llama_stream stream) {
+  if (stk == nullptr || top_k < 0 || (targets == nullptr) != (logprobs == nullptr)) return LLAMA_ERR_INVALID_ARG;
+  if (top_k > stk->vocab) return LLAMA_ERR_RANGE;
+  if (top_k > LLAMA_LOGPROBS_MAX_TOP) return LLAMA_ERR_UNSUPPORTED;
+  llama_status s = LLAMA_OK;
+  if (logprobs != nullptr) {
+    s = check_ptr(targets);
+    if (s == LLAMA_OK) s = check_ptr(logprobs);
+  }
+  if (s == LLAMA_OK && entropy != nullptr) s = check_ptr(entropy);
+  if (s == LLAMA_OK && top_k > 0) {
+    s = check_ptr(top_ids);
+    if (s == LLAMA_OK) s = check_ptr(top_logprobs);
+  }
+  if (s == LLAMA_OK) s = llama_stack_forward(stk, tokens, B, S, start_pos, kv, logits, stream);
+  if (s != LLAMA_OK) return s;
+  LAUNCH(launch_token_logprobs<float>(logits, stk->vocab, targets, B * S, stk->vocab, logprobs, entropy, top_k,
+                                      top_ids, top_logprobs, stk->status, DEV_BAD_TOKEN, (cudaStream_t)stream));
+  return LLAMA_OK;
 }
 
 llama_status llama_stack_generate(llama_stack *stk, const int32_t *prompt, int32_t B, int32_t S_prompt,

@@ -205,6 +205,20 @@ llama_status llama_stack_generate(llama_stack *stk, const int32_t *prompt, int32
                                   int32_t start_pos, int32_t n_new, const llama_kv_cache *kv,
                                   int32_t *out_tokens, float *logits, llama_stream stream);
 
+/* Scoring: llama_stack_forward (same arguments, same rules; logits holds the
+ * fp32 logits on return), then for every position the log-probability of its
+ * target, the entropy and the top_k likeliest tokens, exactly as
+ * llama_op_token_logprobs (llama_ops.h) computes them from logits with T = B*S
+ * and V = vocab.  To score a prompt, targets [B][S] holds the next token of
+ * every position and -1 where there is none; with S = 1 it serves a decode step.
+ * A target outside [-1, vocab) is reported as a bad token id by
+ * llama_stack_device_status. */
+#define LLAMA_LOGPROBS_MAX_TOP 32
+llama_status llama_stack_score(llama_stack *stk, const int32_t *tokens, int32_t B, int32_t S, int32_t start_pos,
+                               const llama_kv_cache *kv, const int32_t *targets, float *logits, float *logprobs,
+                               float *entropy, int32_t top_k, int32_t *top_ids, float *top_logprobs,
+                               llama_stream stream);
+
 void llama_stack_destroy(llama_stack *stk);
 
 /* Bytes of one layer's K plus V cache for max_batch x max_seq_len positions:
@@ -269,7 +283,7 @@ llama_status llama_stack_set_decode_mode(llama_stack *stk, int32_t mode);
  * handle lives on.  Returns LLAMA_OK when no kernel reported a problem since
  * the last read, LLAMA_ERR_DEVICE_TIMEOUT when a bounded wait ran out,
  * LLAMA_ERR_RANGE when a token id was outside [0, vocab) (its embedding row
- * was written as zeros), LLAMA_ERR_CUDA when the read itself failed. */
+ * was written as zeros; a target of llama_stack_score: its log-probability as NaN), LLAMA_ERR_CUDA when the read itself failed. */
 llama_status llama_block_device_status(llama_block *blk);
 llama_status llama_stack_device_status(llama_stack *stk);
 

@@ -4,8 +4,9 @@
  * compose the steps themselves.  Conventions as in llama_block.h: device
  * pointers, 16-byte alignment, row-major, asynchronous on `stream`, errors
  * returned (nothing enqueued on error).  dtype is LLAMA_F32 or LLAMA_BF16.
- * These entry points allocate nothing and report device-side wait expiry only
- * through their return of later calls' CUDA errors (no status word).
+ * These entry points allocate nothing and, but for those that take a status
+ * pointer, report device-side wait expiry only through their return of later
+ * calls' CUDA errors (no status word).
  */
 #ifndef LLAMA_OPS_H
 #define LLAMA_OPS_H
@@ -103,6 +104,140 @@ llama_status llama_op_rope_kv_write(int32_t dtype, const void *qkv, void *q_out,
 llama_status llama_op_attention_decode_noalloc(const void *q, const llama_kv_cache *kv, void *o, int32_t B,
                                                int32_t start_pos, int32_t H, int32_t G, int32_t D,
                                                llama_stream stream);
+
+/* ------------------------------------------------------------------------
+ * Batches of sequences of different lengths, over a paged key-value cache.
+ *
+ * The method's pages run every sequence of a batch at one start_pos over a
+ * contiguous cache ("Full Llama 3 transformer block", How it works); the entry
+ * points below compute the same RoPE, cache write and grouped-query attention
+ * when each sequence has its own length and its keys and values lie in pages.
+ * The order of a step is llama_op_rope_kv_write_paged, then
+ * llama_op_attention_packed (prompts, continued prompts, mixed batches) or
+ * llama_op_attention_paged_decode (one new token per sequence).
+ *
+ * Device status: lengths, offsets and page ids live on the device, where the
+ * host cannot check them before the launch.  Each of these entry points takes
+ * status, a device int32 that the caller has set to 0 (or NULL): the first
+ * problem that a kernel meets is stored there as a llama_status and the call
+ * goes on as described below; nothing is read or written out of range.
+ *
+ * Every pointer belongs to the device that is current (LLAMA_ERR_INVALID_ARG
+ * otherwise).  Calls allocate nothing, keep nothing between calls and can be
+ * captured into a CUDA graph; a replay reads the lengths, offsets and page ids
+ * as they are then, within the bounds given on the host at capture.  A
+ * workspace may hold anything before a call and is scratch after it: calls that
+ * are ordered (one stream, one graph after another) can share one, calls that
+ * may run at the same time need one each. */
+
+/* Pages of one layer's keys and values: k and v are each
+ * [n_pages][n_kv_heads][page_size][d_head] of the call's dtype, consecutive
+ * pages page_stride elements apart (0: dense; a larger stride lets the pages of
+ * k and v, or of several layers, interleave).  Position p of sequence i lies in
+ * row p % page_size of page page_table[i * table_stride + p / page_size].
+ * page_table is a device array; entries past the last page in use may hold
+ * anything.  Sequences may share pages that they only read (a common prefix).
+ * page_size: 16, 32, 64, 128 or 256 (LLAMA_ERR_UNSUPPORTED otherwise).
+ * page_stride: 0 or >= n_kv_heads * page_size * d_head, a multiple of 16 bytes.
+ * A page id outside [0, n_pages) reads as a page of zeros, is not written, and
+ * records LLAMA_ERR_RANGE. */
+typedef struct {
+    void *k;
+    void *v;
+    const int32_t *page_table;
+    int32_t n_pages;
+    int32_t page_size;
+    int32_t max_pages;    /* entries of a page_table row that may be used */
+    int32_t table_stride; /* entries from one row to the next, >= max_pages */
+    int64_t page_stride;  /* elements from one page to the next, 0: dense */
+} llama_paged_kv_cache;
+
+/* Most sequences of one call (LLAMA_ERR_UNSUPPORTED above). */
+#define LLAMA_PACKED_MAX_SEQS 4096
+
+/* n_seqs sequences packed one after another: the new tokens of sequence i are
+ * rows [q_offsets[i], q_offsets[i + 1]) of the token-major arrays of the call
+ * (q_offsets: device, n_seqs + 1 entries, non-decreasing, within [0,
+ * n_tokens]); kv_lens[i] (device, n_seqs entries) counts its positions with
+ * those tokens included, so that its new tokens are the last ones:  token t is
+ * at position kv_lens[i] - (q_offsets[i + 1] - t).  Sequences without new
+ * tokens are allowed.  Rows outside all sequences (padding behind the last one)
+ * are neither read nor written.
+ * max_kv_len: no kv_lens entry is larger (host value; it may be larger than any).
+ * A sequence with bad offsets is left out; a length that is negative, above
+ * max_kv_len or above max_pages * page_size counts as 0.  Both record
+ * LLAMA_ERR_RANGE. */
+typedef struct {
+    const int32_t *q_offsets;
+    const int32_t *kv_lens;
+    int32_t n_seqs;
+    int32_t n_tokens; /* rows of the token-major arrays */
+    int32_t max_kv_len;
+} llama_packed_batch;
+
+/* RoPE and the write of keys and values into their pages.  qkv [n_tokens]
+ * [(H + 2G) D], q_out [n_tokens][H][D], table, layout and the rotation as for
+ * llama_op_rope_kv_write; token t turns at its position, rotated k and raw v go
+ * to that position's row of its page, nothing else in the cache changes.  No two
+ * tokens of a call may share a position's row.  A token whose position is
+ * negative or >= table_max_seq gets a row of zeros in q_out, is not written to
+ * the cache, and records LLAMA_ERR_RANGE. */
+llama_status llama_op_rope_kv_write_paged(int32_t dtype, const void *qkv, void *q_out,
+                                          const llama_paged_kv_cache *kv, const llama_packed_batch *batch,
+                                          const float *table, int32_t table_max_seq, int32_t H, int32_t G,
+                                          int32_t D, int32_t layout, int32_t *status, llama_stream stream);
+
+/* Causal grouped-query attention of a packed batch: for token t of sequence i
+ * at position p,
+ *   o[t][h] = sum_{j <= p} softmax_j(q[t][h] . K_i[h / (H/G)][j] / sqrt(D)) V_i[h / (H/G)][j]
+ * over the sequence's pages (its own new keys included: write them first).
+ * q, o: [n_tokens][H][D], q already rotated.  A token that sees no key (p < 0:
+ * kv_lens[i] is less than the sequence's tokens) gets zeros.  Rows of the pages
+ * at or behind kv_lens[i] may hold anything, NaN included; the visible keys and
+ * values have to be finite.  D in {16, 32, 64, 128}.
+ * workspace: caller-owned device scratch of at least
+ * llama_op_attention_packed_workspace_bytes bytes (which reads only n_seqs,
+ * n_tokens and max_kv_len of batch; 0 for arguments that the call refuses); may
+ * be NULL when that is 0. */
+size_t llama_op_attention_packed_workspace_bytes(int32_t dtype, const llama_packed_batch *batch, int32_t H,
+                                                 int32_t G, int32_t D);
+llama_status llama_op_attention_packed(int32_t dtype, const void *q, const llama_paged_kv_cache *kv,
+                                       const llama_packed_batch *batch, void *o, int32_t H, int32_t G, int32_t D,
+                                       void *workspace, size_t workspace_bytes, int32_t *status,
+                                       llama_stream stream);
+
+/* The same for one new token per sequence: q, o: [n_seqs][H][D], row i at
+ * position kv_lens[i] - 1.  A sequence of length 0 gets zeros.  The cache's
+ * length is split over the GPU and the parts joined by their log-sum-exp;
+ * max_kv_len (an upper bound, as in llama_packed_batch) fixes the split, so that
+ * results depend on it in their last bits but not from run to run. */
+size_t llama_op_attention_paged_decode_workspace_bytes(int32_t dtype, int32_t n_seqs, int32_t max_kv_len,
+                                                       int32_t H, int32_t G, int32_t D);
+llama_status llama_op_attention_paged_decode(int32_t dtype, const void *q, const llama_paged_kv_cache *kv,
+                                             const int32_t *kv_lens, int32_t n_seqs, int32_t max_kv_len, void *o,
+                                             int32_t H, int32_t G, int32_t D, void *workspace,
+                                             size_t workspace_bytes, int32_t *status, llama_stream stream);
+
+/* Log-probabilities of given tokens, with the entropy of each distribution and
+ * its likeliest tokens.  logits: [T][V] of dtype, rows row_stride elements
+ * apart (>= V; columns at and behind V are not read; rows need no alignment).
+ * With p = softmax(logits[t]):
+ *   logprobs[t]        = ln p[targets[t]]          (fp32)
+ *   entropy[t]         = -sum_v p[v] ln p[v]       (fp32; NULL: not computed)
+ *   top_ids[t][j]      = id of the j-th largest logit, the lowest id among equals
+ *   top_logprobs[t][j] = ln p[top_ids[t][j]]       (fp32, [T][top_k])
+ * targets: int32 [T].  A target of -1 (a position without a next token) gives
+ * logprobs[t] = 0; any other target outside [0, V) gives NaN and records
+ * LLAMA_ERR_RANGE.  targets and logprobs may both be NULL.
+ * 0 <= top_k <= min(V, LLAMA_LOGPROBS_MAX_TOP); with top_k = 0 the two arrays
+ * are ignored.
+ * A logit of -inf has probability 0 (ln p = -inf) and adds nothing to the
+ * entropy; a row of nothing but -inf has ln p = -inf throughout and entropy 0.
+ * NaN or +inf anywhere in a row makes its logprobs, top_logprobs and entropy NaN;
+ * NaN is never among the top (ids that cannot be filled are -1). */
+llama_status llama_op_token_logprobs(int32_t dtype, const void *logits, int64_t row_stride, const int32_t *targets,
+                                     int32_t T, int32_t V, float *logprobs, float *entropy, int32_t top_k,
+                                     int32_t *top_ids, float *top_logprobs, int32_t *status, llama_stream stream);
 
 #ifdef __cplusplus
 }
