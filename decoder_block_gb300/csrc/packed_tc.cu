@@ -1,0 +1,925 @@
+// Causal grouped-query attention of a packed batch over cache pages, bf16,
+// d_head 64 or 128, on tcgen05 tensor cores ("The Evolving Transformer 04 ·
+// LLaMA", §05 GQA; "Full Llama 3 transformer block", How it works: keys
+// j <= position).  For token t at position p and its KV head's keys and values
+//   o = sum_{j<=p} 2^(x_j - m) v_j / sum_{j<=p} 2^(x_j - m),  x_j = q.k_j log2(e) / sqrt(D),
+// in one pass over the keys with the running maximum m and sum in fp32.
+//
+// A work item is (sequence, KV head, block of 2 * Mq query positions, range of
+// 128-key tiles).  Its 128-row query tile t holds the r heads of the group at Mq
+// = 128 / r positions, row i * r + hh: one TMA box, so that every K/V tile in
+// shared memory serves the whole group.  Keys and values arrive page by page:
+// one box per page (at most 128 rows) and 64 columns, in the 128-byte swizzle
+// the MMAs read, so a tile is the same whatever the page size.  Rows behind the
+// sequence's last key may hold anything: their scores are replaced, not added
+// to, and the V rows are cleared in shared memory before the product reads them
+// (0 * NaN is not 0).
+//   warp 0      takes items, loads Q, then K and V tiles into two-stage rings;
+//               each lane issues one page's box and holds the next tile's id
+//   warp 1      one thread issues S_t = Q_t K^T and O_t += P_t V (fp32 in tensor
+//               memory, P from tensor memory)
+//   warps 2-9   softmax of tile 0 / 1, one thread per row; the output
+// Work is dealt out in one of two ways:
+//   * direct: one item per CTA, found by the CTA itself from the offsets (few
+//     items, short keys: no kernel but this one runs);
+//   * planned: a one-CTA kernel lists the items longest first and zeroes a
+//     counter that persistent CTAs take them from.  When the longest items would
+//     outlast the rest (few query rows against many keys) it splits their keys
+//     into pieces; a piece leaves fp32 (O, m, l) per row in the workspace, and
+//     for every 32 rows the last piece's warp joins them in piece order, so the
+//     result does not depend on timing.
+// Every wait is bounded; a kernel that gives up records LLAMA_ERR_DEVICE_TIMEOUT
+// once its copies and MMAs in flight are done.
+#include <cudaTypedefs.h>
+#include <float.h>
+
+#include "paged_kernels.h"
+#include "ptx.cuh"
+
+namespace llama {
+namespace {
+
+constexpr int PT_THREADS = 320;
+constexpr int PT_KEYS = 128;    // keys of a tile
+constexpr int PT_STAGES = 2;
+constexpr float PT_RESCALE = 8.0f;  // log2 units: the running maximum is raised when it grows by > 2^8
+constexpr int PT_MIN_PIECE = 4;     // key tiles of a split item's piece, at least
+constexpr int PT_PLAN_THREADS = 1024;
+constexpr int PT_BUCKETS = 1024;    // item lengths the planner tells apart
+
+template <int D>
+struct PtLayout {
+  static constexpr int ATOM = 128 * 128;  // 128 rows x 64 columns
+  static constexpr int TILE = (D / 64) * ATOM;
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_K = 2 * TILE;
+  static constexpr int OFF_V = OFF_K + PT_STAGES * TILE;
+  static constexpr int OFF_ITEM = OFF_V + PT_STAGES * TILE;  // PtItem
+  static constexpr int OFF_BAR = OFF_ITEM + 64;
+  // q_full, q_empty, fin, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_done[2]
+  static constexpr int NBAR = 3 + 4 * PT_STAGES + 6;
+  static constexpr int BYTES_MIN = 1024 + OFF_BAR + NBAR * 8 + 16;
+  // one CTA per SM: two would need all of tensor memory each
+  static constexpr int BYTES = BYTES_MIN > 116 * 1024 ? BYTES_MIN : 116 * 1024;
+  static constexpr uint32_t TMEM_COLS = 512;  // S0, S1 (128 each), O0, O1 (D each)
+};
+
+// A work item as the producer hands it to the other roles.
+struct PtItem {
+  int seq, g, q0;     // sequence (-1: no more items), KV head, first query position of the block
+  int first, count, kv_len;
+  int j0, j1;         // key tiles
+  int slot, pieces, piece, entry;  // partial slot of piece 0 (-1: not split), number, index, split block
+};
+static_assert(sizeof(PtItem) <= 64, "PtItem fits its slot");
+
+// Planner's output at the start of the workspace.
+struct PtEntry {
+  int seq, blk, j0, j1;
+  int slot, pieces, piece, entry;
+};
+struct PtPlan {
+  int n_entries;  // items are entries x G
+  int next;       // item counter
+  int pad[2];
+};
+
+struct PtArgs {
+  bf16 *o;
+  PagedView pv;
+  PackedView b;
+  int H, G, r, Mq, box;  // box: rows of a page's TMA box
+  float scale_log2;
+  PtPlan *plan;          // null: direct
+  PtEntry *entries;
+  int *arrivals;         // [split block][G][2][4]
+  float *part;           // [slot][G][2][4][D + 2][32]
+  int *status;
+};
+
+__device__ __forceinline__ uint32_t pt_pack2(float a, float b) {
+  __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<uint32_t *>(&h);
+}
+
+// Key tiles that the rows [lo, hi) of a sequence's new tokens see.
+__device__ __forceinline__ int tiles_of(int shift, int lo, int hi) {
+  if (hi <= lo || shift + hi <= 0) return 0;
+  return (shift + hi - 1) / PT_KEYS + 1;
+}
+// The key tiles [j0, end) that query tile t of an item works on.
+__device__ __forceinline__ int item_end(const PtItem &it, int Mq, int t) {
+  const int lo = it.q0 + t * Mq, hi = min(it.count, lo + Mq);
+  return min(it.j1, tiles_of(it.kv_len - it.count, lo, hi));
+}
+
+// ------------------------------------------------------------------ plan ---
+// Inclusive sum over the CTA's threads.
+__device__ __forceinline__ int cta_scan(int v, int *warp_sums) {
+  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += x;
+  }
+  if (lane == 31) warp_sums[warp] = v;
+  __syncthreads();
+  if (warp == 0) {
+    int s = warp_sums[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += x;
+    }
+    warp_sums[lane] = s;
+  }
+  __syncthreads();
+  const int out = v + (warp > 0 ? warp_sums[warp - 1] : 0);
+  __syncthreads();
+  return out;
+}
+
+__global__ void __launch_bounds__(PT_PLAN_THREADS) packed_plan_kernel(PagedView pv, PackedView b, int G, int Mq,
+                                                                      int sms, int max_entries, int max_split,
+                                                                      PtPlan *plan, PtEntry *entries, int *arrivals,
+                                                                      int *status) {
+  __shared__ int first_blk[LLAMA_PACKED_MAX_SEQS + 1];  // blocks before sequence i
+  __shared__ int hist[PT_BUCKETS];
+  __shared__ int warp_sums[32];
+  __shared__ unsigned long long work_sum;
+  __shared__ int n_split, n_slots;
+  const int tid = threadIdx.x;
+  allow_dependents_launch();
+  grid_dependency_wait();
+  if (tid == 0) {
+    work_sum = 0;
+    n_split = n_slots = 0;
+  }
+  for (int i = tid; i < PT_BUCKETS; i += PT_PLAN_THREADS) hist[i] = 0;
+  for (int i = tid; i < max_split * G * 8; i += PT_PLAN_THREADS) arrivals[i] = 0;
+  for (int i = tid; i < b.n_seqs; i += PT_PLAN_THREADS) check_seq(b, pv, i, status);
+  // blocks of every sequence, as sums: 1024 sequences a round
+  int base = 0;
+  for (int i0 = 0; i0 < b.n_seqs; i0 += PT_PLAN_THREADS) {
+    const int i = i0 + tid;
+    const int n = i < b.n_seqs ? (seq_span(b, pv, i).count + 2 * Mq - 1) / (2 * Mq) : 0;
+    const int end = base + cta_scan(n, warp_sums);
+    if (i < b.n_seqs) first_blk[i + 1] = end;
+    if (tid == PT_PLAN_THREADS - 1) warp_sums[0] = end;
+    __syncthreads();
+    base = warp_sums[0];
+    __syncthreads();
+  }
+  if (tid == 0) first_blk[0] = 0;
+  __syncthreads();
+  const int n_blk = base;
+  // sequence of block u: the last i with first_blk[i] <= u
+  auto seq_of = [&](int u) {
+    int lo = 0, hi = b.n_seqs;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (first_blk[mid] <= u) lo = mid;
+      else hi = mid;
+    }
+    return lo;
+  };
+  auto tiles = [&](int u, int &seq, int &blk) {
+    seq = seq_of(u);
+    blk = u - first_blk[seq];
+    const SeqSpan s = seq_span(b, pv, seq);
+    return tiles_of(s.kv_len - s.count, blk * 2 * Mq, min(s.count, (blk + 1) * 2 * Mq));
+  };
+  unsigned long long mine = 0;
+  for (int u = tid; u < n_blk; u += PT_PLAN_THREADS) {
+    int seq, blk;
+    mine += (unsigned)tiles(u, seq, blk);
+  }
+  atomicAdd(&work_sum, mine);
+  __syncthreads();
+  // A CTA's even share of the key tiles; an item longer than that is what the
+  // others would wait for, so it is cut into pieces of at most that length.  The
+  // pieces of all split items then number less than 2 * sms / G (each has more
+  // than half a share), which sizes the workspace.
+  const unsigned long long share = (work_sum * G + sms - 1) / sms;
+  const int cap = (int)(share > PT_MIN_PIECE ? share : PT_MIN_PIECE);
+  // longest first: counting sort by piece length
+  auto pieces_of = [&](int n) { return n > cap ? (n + cap - 1) / cap : 1; };
+  auto bucket = [&](int len) { return PT_BUCKETS - 1 - min(len, PT_BUCKETS - 1); };
+  for (int u = tid; u < n_blk; u += PT_PLAN_THREADS) {
+    int seq, blk;
+    const int n = tiles(u, seq, blk), np = pieces_of(n);
+    atomicAdd(&hist[bucket((n + np - 1) / np)], np);
+  }
+  __syncthreads();
+  {
+    const int v = hist[tid];
+    const int end = cta_scan(v, warp_sums);
+    hist[tid] = end - v;
+    if (tid == PT_PLAN_THREADS - 1) {
+      plan->n_entries = min(end, max_entries);
+      plan->next = 0;
+    }
+  }
+  __syncthreads();
+  for (int u = tid; u < n_blk; u += PT_PLAN_THREADS) {
+    PtEntry e;
+    const int n = tiles(u, e.seq, e.blk);
+    e.pieces = pieces_of(n);
+    e.slot = e.entry = -1;
+    const int each = (n + e.pieces - 1) / e.pieces;
+    if (e.pieces > 1) {
+      e.entry = atomicAdd(&n_split, 1);
+      e.slot = atomicAdd(&n_slots, e.pieces);
+    }
+    const int at = atomicAdd(&hist[bucket(each)], e.pieces);
+    for (e.piece = 0; e.piece < e.pieces; ++e.piece) {
+      e.j0 = min(n, e.piece * each);
+      e.j1 = min(n, e.j0 + each);
+      if (at + e.piece < max_entries) entries[at + e.piece] = e;
+    }
+  }
+}
+
+// ------------------------------------------------------------- attention ---
+template <int D>
+__global__ void __launch_bounds__(PT_THREADS, 1)
+    packed_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                     const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PtArgs a) {
+  using L = PtLayout<D>;
+  constexpr int ATOMS = D / 64;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::OFF_BAR);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + L::NBAR);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  PtItem *item_slot = reinterpret_cast<PtItem *>(smem + L::OFF_ITEM);
+
+  const uint32_t s0 = ptx::smem_u32(smem);
+  const uint32_t bar0 = ptx::smem_u32(bars);
+  const uint32_t q_full = bar0, q_empty = bar0 + 8, fin = bar0 + 16;
+  auto k_full = [&](int s) { return bar0 + 8u * (3 + s); };
+  auto k_empty = [&](int s) { return bar0 + 8u * (3 + PT_STAGES + s); };
+  auto v_full = [&](int s) { return bar0 + 8u * (3 + 2 * PT_STAGES + s); };
+  auto v_empty = [&](int s) { return bar0 + 8u * (3 + 3 * PT_STAGES + s); };
+  auto s_full = [&](int t) { return bar0 + 8u * (3 + 4 * PT_STAGES + t); };
+  auto p_full = [&](int t) { return bar0 + 8u * (5 + 4 * PT_STAGES + t); };
+  auto o_done = [&](int t) { return bar0 + 8u * (7 + 4 * PT_STAGES + t); };
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
+    if (ptx::mbar_wait(bar, parity, abort_flag, nullptr, 0)) return true;
+    report_status(a.status, LLAMA_ERR_DEVICE_TIMEOUT);
+    return false;
+  };
+  auto wait_warp = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
+
+  if (threadIdx.x == 0) {
+    ptx::mbar_init(q_full, 1);
+    ptx::mbar_init(q_empty, 9);  // the MMAs reading Q are done; each softmax warp has read the item
+    ptx::mbar_init(fin, 1);
+    for (int s = 0; s < PT_STAGES; ++s) {
+      ptx::mbar_init(k_full(s), 1);
+      ptx::mbar_init(k_empty(s), 1);
+      ptx::mbar_init(v_full(s), 1);
+      ptx::mbar_init(v_empty(s), 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      ptx::mbar_init(s_full(t), 1);
+      ptx::mbar_init(p_full(t), 128);
+      ptx::mbar_init(o_done(t), 1);
+    }
+    *abort_flag = 0;
+    ptx::fence_mbar_init();
+  }
+  // Query rows behind r * Mq are never loaded: zero them.
+  if (warp >= 2 && a.r * a.Mq < 128) {
+    const int first = a.r * a.Mq;
+    for (int t = 0; t < 2; ++t)
+      for (int at = 0; at < ATOMS; ++at) {
+        uint4 *p = reinterpret_cast<uint4 *>(smem + L::OFF_Q + t * L::TILE + at * L::ATOM + first * 128);
+        for (int i = threadIdx.x - 64; i < (128 - first) * 8; i += PT_THREADS - 64) p[i] = make_uint4(0, 0, 0, 0);
+      }
+    ptx::fence_proxy_async_smem();
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(ptx::smem_u32(tmem_slot), L::TMEM_COLS);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  allow_dependents_launch();
+  grid_dependency_wait();
+
+  if (warp == 0) {
+    // ---------------------------------------------------------- producer ---
+    if (lane == 0) {
+      ptx::tma_prefetch_desc(&tmQ);
+      ptx::tma_prefetch_desc(&tmK);
+      ptx::tma_prefetch_desc(&tmV);
+    }
+    const int n_items = a.plan != nullptr ? *reinterpret_cast<volatile int *>(&a.plan->n_entries) * a.G : 0;
+    // The CTA's next item (all lanes); seq = -1 when there is none.
+    auto fetch = [&](int k) {
+      PtItem it;
+      it.seq = -1;
+      if (a.plan != nullptr) {
+        int u = 0;
+        if (lane == 0) u = atomicAdd(&a.plan->next, 1);
+        u = __shfl_sync(0xffffffffu, u, 0);
+        if (u >= n_items) return it;
+        const int4 *e = reinterpret_cast<const int4 *>(a.entries + u / a.G);
+        const int4 x = __ldcg(e), y = __ldcg(e + 1);
+        it.seq = x.x;
+        it.g = u % a.G;
+        it.q0 = x.y * 2 * a.Mq;
+        it.j0 = x.z;
+        it.j1 = x.w;
+        it.slot = y.x;
+        it.pieces = y.y;
+        it.piece = y.z;
+        it.entry = y.w;
+      } else {
+        if (k > 0) return it;
+        const int want = blockIdx.x / a.G;
+        int base = 0;
+        for (int i0 = 0; i0 < a.b.n_seqs; i0 += 32) {
+          const int i = i0 + lane;
+          const int n = i < a.b.n_seqs ? (seq_span(a.b, a.pv, i).count + 2 * a.Mq - 1) / (2 * a.Mq) : 0;
+          int end = n;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, end, o);
+            if (lane >= o) end += x;
+          }
+          const int mine = want - base - (end - n);
+          const unsigned m = __ballot_sync(0xffffffffu, mine >= 0 && mine < n);
+          if (m != 0) {
+            const int src = __ffs(m) - 1;
+            it.seq = i0 + src;
+            it.q0 = __shfl_sync(0xffffffffu, mine, src) * 2 * a.Mq;
+            break;
+          }
+          base += __shfl_sync(0xffffffffu, end, 31);
+          if (base > want) break;
+        }
+        if (it.seq < 0) return it;
+        it.g = blockIdx.x % a.G;
+        it.slot = it.entry = -1;
+        it.pieces = 1;
+        it.piece = 0;
+      }
+      const SeqSpan s = seq_span(a.b, a.pv, it.seq);
+      it.first = s.first;
+      it.count = s.count;
+      it.kv_len = s.kv_len;
+      if (a.plan == nullptr) {
+        it.j0 = 0;
+        it.j1 = tiles_of(s.kv_len - s.count, it.q0, min(s.count, it.q0 + 2 * a.Mq));
+      }
+      return it;
+    };
+    const int boxes_tile = PT_KEYS / a.box;                 // pages of a tile (1 when pages are larger)
+    const int my_box = lane / ATOMS, my_at = lane % ATOMS;  // the box this lane loads
+    const uint32_t dst = my_at * L::ATOM + my_box * a.box * 128;
+    const uint32_t box_bytes = a.box * 128u * ATOMS;
+    // Page of this lane's box of key tile j: its id, n_pages (a page of zeros) when
+    // the id is out of range, -1 when the tile has no such box.
+    auto page_of = [&](const PtItem &it, int j) {
+      const int key = j * PT_KEYS + my_box * a.box;
+      if (my_box >= boxes_tile || j >= it.j1 || key >= it.kv_len) return -1;
+      const int id = a.pv.page(it.seq, key >> a.pv.page_log2);
+      if (id < 0) report_status(a.status, LLAMA_ERR_RANGE);
+      return id < 0 ? a.pv.n_pages : id;
+    };
+    int items = 0, tiles = 0;  // Q loads and key tiles issued
+    bool v_short = false;      // the last key tile's V was not issued
+    bool ended = false;        // the end was handed over: the last Q has landed
+    bool ok = true;
+    PtItem it = fetch(0);
+    for (int k = 0; ok; ++k) {
+      int page = it.seq >= 0 ? page_of(it, it.j0) : -1;
+      if (k > 0 && !wait_warp(q_empty, (k - 1) & 1)) break;
+      if (lane == 0) *item_slot = it;  // published by the q_full arrival
+      __syncwarp();
+      if (it.seq < 0) {
+        if (lane == 0) ptx::mbar_arrive(q_full);
+        ended = true;
+        break;
+      }
+      const int n_t = it.q0 + a.Mq < it.count ? 2 : 1;  // query tiles that hold rows
+      if (lane == 0) {
+        ptx::mbar_arrive_expect_tx(q_full, n_t * ATOMS * a.r * a.Mq * 128u);
+        for (int t = 0; t < n_t; ++t)
+          for (int at = 0; at < ATOMS; ++at)
+            ptx::tma_load_3d(s0 + L::OFF_Q + t * L::TILE + at * L::ATOM, &tmQ, at * 64, it.g * a.r,
+                             it.first + it.q0 + t * a.Mq, q_full);
+      }
+      ++items;
+      PtItem next;
+      bool fetched = false;
+      for (int j = it.j0; j < it.j1; ++j) {
+        if (j == it.j0 + PT_STAGES) {  // the rings are full: time for the next item's look-ups
+          next = fetch(k + 1);
+          fetched = true;
+        }
+        const int st = tiles % PT_STAGES;
+        const uint32_t ph = (tiles / PT_STAGES) & 1;
+        const int boxes = min(boxes_tile, (it.kv_len - j * PT_KEYS + a.box - 1) / a.box);
+        const int row = (j * PT_KEYS) & ((1 << a.pv.page_log2) - 1) & ~(a.box - 1);
+        const int page_now = page;
+        if (j + 1 < it.j1) page = page_of(it, j + 1);
+        if (!wait_warp(k_empty(st), ph ^ 1)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) ptx::mbar_arrive_expect_tx(k_full(st), boxes * box_bytes);
+        __syncwarp();
+        if (page_now >= 0)
+          ptx::tma_load_4d(s0 + L::OFF_K + st * L::TILE + dst, &tmK, my_at * 64, row, it.g, page_now, k_full(st));
+        ++tiles;
+        v_short = true;
+        if (!wait_warp(v_empty(st), ph ^ 1)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) ptx::mbar_arrive_expect_tx(v_full(st), boxes * box_bytes);
+        __syncwarp();
+        if (page_now >= 0)
+          ptx::tma_load_4d(s0 + L::OFF_V + st * L::TILE + dst, &tmV, my_at * 64, row, it.g, page_now, v_full(st));
+        v_short = false;
+      }
+      if (!ok) break;
+      if (!fetched) next = fetch(k + 1);
+      it = next;
+    }
+    // every issued copy lands before the CTA exits
+    __syncwarp();
+    if (lane == 0) {
+      if (items > 0 && !ended) ptx::mbar_drain(q_full, (items - 1) & 1, nullptr, 0);
+      for (int j = max(0, tiles - PT_STAGES); j < tiles; ++j) {
+        ptx::mbar_drain(k_full(j % PT_STAGES), (j / PT_STAGES) & 1, nullptr, 0);
+        if (j + 1 < tiles || !v_short) ptx::mbar_drain(v_full(j % PT_STAGES), (j / PT_STAGES) & 1, nullptr, 0);
+      }
+    }
+  } else if (warp == 1) {
+    // --------------------------------------------------------------- MMA ---
+    if (lane == 0) {
+      constexpr uint32_t idesc_qk = ptx::idesc_bf16_f32(128, PT_KEYS, false);
+      constexpr uint32_t idesc_pv = ptx::idesc_bf16_f32(128, D, true);
+      auto issue_s = [&](int jj, int t) {
+        const uint32_t kb = s0 + L::OFF_K + (jj % PT_STAGES) * L::TILE;
+        const uint32_t qb = s0 + L::OFF_Q + t * L::TILE;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk / 4) * L::ATOM + (kk % 4) * 32;
+          ptx::mma_bf16_ss(tmem + t * 128, ptx::smem_desc_sw128(qb + off), ptx::smem_desc_sw128(kb + off), idesc_qk,
+                           kk > 0 ? 1u : 0u);
+        }
+        ptx::mma_commit(s_full(t));
+      };
+      auto issue_pv = [&](int jj, bool first, int t) {
+        const uint32_t vb = s0 + L::OFF_V + (jj % PT_STAGES) * L::TILE;
+#pragma unroll
+        for (int kk = 0; kk < PT_KEYS / 16; ++kk) {
+          const uint64_t bdesc = ptx::smem_desc_sw128_mn(vb + kk * 16 * 128, L::ATOM, 1024);
+          ptx::mma_bf16_ts(tmem + 256 + t * D, tmem + t * 128 + kk * 8, bdesc, idesc_pv, (!first || kk > 0) ? 1u : 0u);
+        }
+        ptx::mma_commit(o_done(t));
+      };
+      // S_0(j+1) goes out right after PV_0(j): the softmax of tile 0 for the next keys
+      // overlaps that of tile 1, and the next item's first S products the output of this one.
+      bool ok = true;
+      int jg = 0, n0 = 0, n1 = 0;  // key tiles over all items: of the ring, of query tiles 0 and 1
+      for (int k = 0; ok; ++k) {
+        if (!wait(q_full, k & 1)) break;
+        const PtItem it = *item_slot;
+        if (it.seq < 0) break;
+        const int e0 = item_end(it, a.Mq, 0), e1 = item_end(it, a.Mq, 1);
+        const int n = it.j1 - it.j0;
+        if (n <= 0) {  // no row of the block sees a key
+          ptx::mbar_arrive(q_empty);
+          continue;
+        }
+        auto issue_both = [&](int t, int j, int jj) {
+          if (j < (t == 0 ? e0 : e1)) issue_s(jj, t);
+        };
+        if (!wait(k_full(jg % PT_STAGES), (jg / PT_STAGES) & 1)) break;
+        ptx::tc_fence_after();
+        issue_both(0, it.j0, jg);
+        issue_both(1, it.j0, jg);
+        ptx::mma_commit(k_empty(jg % PT_STAGES));
+        if (n == 1) ptx::mma_commit(q_empty);
+        for (int i = 0; i < n; ++i) {
+          const int j = it.j0 + i, jj = jg + i, st = jj % PT_STAGES;
+          ok = false;
+          if (!wait(v_full(st), (jj / PT_STAGES) & 1)) break;
+          if (j < e0) {
+            if (!wait(p_full(0), n0 & 1)) break;
+            ++n0;
+            ptx::tc_fence_after();
+            issue_pv(jj, i == 0, 0);
+          }
+          const bool more = i + 1 < n;
+          if (more) {
+            if (!wait(k_full((jj + 1) % PT_STAGES), ((jj + 1) / PT_STAGES) & 1)) break;
+            ptx::tc_fence_after();
+            issue_both(0, j + 1, jj + 1);
+          }
+          if (j < e1) {
+            if (!wait(p_full(1), n1 & 1)) break;
+            ++n1;
+            ptx::tc_fence_after();
+            issue_pv(jj, i == 0, 1);
+          }
+          ptx::mma_commit(v_empty(st));
+          if (more) {
+            issue_both(1, j + 1, jj + 1);
+            ptx::mma_commit(k_empty((jj + 1) % PT_STAGES));
+            if (i + 2 == n) ptx::mma_commit(q_empty);
+          }
+          ok = true;
+        }
+        jg += n;
+      }
+      ptx::mma_commit(fin);
+      ptx::mbar_drain(fin, 0, nullptr, 0);
+    }
+  } else {
+    // ----------------------------------------------------------- softmax ---
+    const int t = (warp - 2) / 4;
+    const int qq = warp & 3;
+    const int row = qq * 32 + lane;
+    const int hh = row % a.r, i = row / a.r;
+    const uint32_t lane_base = tmem + ((uint32_t)(qq * 32) << 16);
+    const uint32_t s_col = lane_base + t * 128;
+    const uint32_t o_col = lane_base + 256 + t * D;
+    const uint64_t scale2 = ptx::f2pack(a.scale_log2, a.scale_log2);
+    if (a.plan == nullptr && blockIdx.x == 0)
+      for (int u = threadIdx.x - 64; u < a.b.n_seqs; u += PT_THREADS - 64) check_seq(a.b, a.pv, u, a.status);
+    bool ok = true;
+    int jg = 0, jt = 0;  // key tiles of earlier items: of the ring, of this query tile
+    for (int k = 0; ok; ++k) {
+      if (!wait_warp(q_full, k & 1)) break;
+      const PtItem it = *item_slot;
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(q_empty);
+      if (it.seq < 0) break;
+      const int shift = it.kv_len - it.count;
+      const int e0 = item_end(it, a.Mq, 0), e1 = item_end(it, a.Mq, 1);
+      const int my_end = t == 0 ? e0 : e1;
+      const int n_kv = max(0, my_end - it.j0);
+      const int rel = it.q0 + t * a.Mq + i;
+      const bool valid = i < a.Mq && rel < it.count;
+      const int pos = shift + min(rel, it.count - 1);
+      // finite: rows that see no key of a tile keep weights of 0 instead of NaN
+      float m_run = -FLT_MAX;
+      uint64_t l2 = ptx::f2pack(0.f, 0.f);  // running row sum, two partial halves
+      for (int jl = 0; jl < n_kv; ++jl) {
+        const int j = it.j0 + jl;
+        if (!wait_warp(s_full(t), (jt + jl) & 1)) {
+          ok = false;
+          break;
+        }
+        ptx::tc_fence_after();
+        const int key0 = j * PT_KEYS;
+        // The last tile of a sequence: clear the V rows behind its last key.  The first
+        // query tile that works on the tile does it, before its P is handed over.
+        if (key0 + PT_KEYS > it.kv_len && t == (j < e0 ? 0 : 1)) {
+          const int st = (jg + jl) % PT_STAGES;
+          if (!wait_warp(v_full(st), ((jg + jl) / PT_STAGES) & 1)) {
+            ok = false;
+            break;
+          }
+          if (key0 + row >= it.kv_len) {
+            uint4 *vr = reinterpret_cast<uint4 *>(smem + L::OFF_V + st * L::TILE + row * 128);
+#pragma unroll
+            for (int at = 0; at < ATOMS; ++at)
+#pragma unroll
+              for (int c = 0; c < 8; ++c) vr[at * (L::ATOM / 16) + c] = make_uint4(0, 0, 0, 0);
+          }
+          ptx::fence_proxy_async_smem();
+        }
+        // One pass over the tile, 32 columns at a time.  p = 2^(s*scale - m_run)
+        // uses the running maximum as it stands; a chunk whose own maximum exceeds
+        // it by more than 2^8 first raises it, scaling the row sum, the P chunks
+        // already written for this tile and, once the tile is done, O.  P (bf16)
+        // lands over S columns already read.
+        const bool masked = __any_sync(0xffffffffu, key0 + PT_KEYS - 1 > pos);
+        float alpha_tile = 1.f;
+        bool rescaled = false;  // warp-uniform
+#pragma unroll
+        for (int c = 0; c < PT_KEYS; c += 32) {
+          float sv[32];
+          float cm;
+          if (masked) {
+            ptx::tmem_ld32(s_col + c, sv);
+            cm = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              if (key0 + c + e > pos) sv[e] = -INFINITY;
+              cm = fmaxf(cm, sv[e]);
+            }
+          } else {
+            ptx::tmem_ld32_max(s_col + c, sv, cm);
+          }
+          const float cms = cm * a.scale_log2;
+          const bool need = cms > m_run + PT_RESCALE;
+          if (__any_sync(0xffffffffu, need)) {
+            float alpha = 1.f;
+            if (need) {
+              alpha = ptx::ex2_approx(m_run - cms);
+              m_run = cms;
+            }
+            l2 = ptx::fmul2(l2, ptx::f2pack(alpha, alpha));
+            alpha_tile *= alpha;
+            rescaled = true;
+            if (c > 0) {
+              ptx::tmem_st_wait();
+#pragma unroll 1
+              for (int pc = 0; pc < c / 2; pc += 16) {
+                float pv[16];
+                ptx::tmem_ld16(s_col + pc, pv);
+                uint32_t w[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                  const uint32_t u = __float_as_uint(pv[e]);
+                  w[e] = pt_pack2(__uint_as_float(u << 16) * alpha, __uint_as_float(u & 0xffff0000u) * alpha);
+                }
+                ptx::tmem_st16(s_col + pc, w);
+              }
+            }
+          }
+          const uint64_t negm2 = ptx::f2pack(-m_run, -m_run);
+          uint32_t pk[16];
+          uint64_t lc = ptx::f2pack(0.f, 0.f);  // a second, independent add chain
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            float x0, x1;
+            ptx::f2unpack(ptx::ffma2(ptx::f2pack(sv[e], sv[e + 1]), scale2, negm2), x0, x1);
+            const float p0 = ptx::ex2_approx(x0), p1 = ptx::ex2_approx(x1);
+            if ((e & 2) == 0)
+              l2 = ptx::fadd2(l2, ptx::f2pack(p0, p1));
+            else
+              lc = ptx::fadd2(lc, ptx::f2pack(p0, p1));
+            // bf16 P: the tensor cores' operand; the row sum keeps the unrounded values
+            pk[e / 2] = pt_pack2(p0, p1);
+          }
+          l2 = ptx::fadd2(l2, lc);
+          ptx::tmem_st16(s_col + c / 2, pk);
+        }
+        if (jl > 0 && rescaled) {
+          // O holds the earlier key tiles: after the last product into it, scale it
+          if (!wait_warp(o_done(t), (jt + jl - 1) & 1)) {
+            ok = false;
+            break;
+          }
+          ptx::tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < D; c += 16) {
+            float ov[16];
+            ptx::tmem_ld16(o_col + c, ov);
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) w[e] = __float_as_uint(ov[e] * alpha_tile);
+            ptx::tmem_st16(o_col + c, w);
+          }
+        }
+        ptx::tmem_st_wait();
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(p_full(t));
+      }
+      if (!ok) break;
+      if (n_kv > 0) {
+        if (!wait_warp(o_done(t), (jt + n_kv - 1) & 1)) break;
+        ptx::tc_fence_after();
+      }
+      float la, lb;
+      ptx::f2unpack(l2, la, lb);
+      float l = la + lb;
+      bf16 *dst = a.o + ((size_t)(it.first + rel) * a.H + it.g * a.r + hh) * D;
+      if (it.slot < 0) {
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll
+        for (int c = 0; c < D; c += 16) {
+          float ov[16];
+          if (n_kv > 0) {
+            ptx::tmem_ld16(o_col + c, ov);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) ov[e] = 0.f;
+          }
+          if (valid) {
+            uint32_t w[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = pt_pack2(ov[2 * e] * inv, ov[2 * e + 1] * inv);
+            *reinterpret_cast<uint4 *>(dst + c) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4 *>(dst + c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+          }
+        }
+      } else if (it.q0 + t * a.Mq < it.count) {
+        // a piece: the rows' partial (O, m, l), one column of 32 rows after another
+        constexpr int ROWS = (D + 2) * 32;
+        const size_t unit = ((size_t)it.g * 2 + t) * 4 + qq;  // 32 rows of the block
+        const size_t per_slot = (size_t)a.G * 8;
+        float *mine = a.part + ((size_t)(it.slot + it.piece) * per_slot + unit) * ROWS + lane;
+#pragma unroll
+        for (int c = 0; c < D; c += 16) {
+          float ov[16];
+          if (n_kv > 0) {
+            ptx::tmem_ld16(o_col + c, ov);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) ov[e] = 0.f;
+          }
+#pragma unroll
+          for (int e = 0; e < 16; ++e) __stcg(mine + (c + e) * 32, ov[e]);
+        }
+        __stcg(mine + D * 32, m_run);
+        __stcg(mine + (D + 1) * 32, l);
+        __threadfence();
+        __syncwarp();
+        int before = 0;
+        if (lane == 0) before = atomicAdd(a.arrivals + (size_t)it.entry * per_slot + unit, 1);
+        before = __shfl_sync(0xffffffffu, before, 0);
+        if (before == it.pieces - 1) {  // the last piece's warp joins them, in piece order
+          __threadfence();
+          const float *p0 = a.part + ((size_t)it.slot * per_slot + unit) * ROWS + lane;
+          const size_t step = per_slot * ROWS;
+          float m = -FLT_MAX;
+          for (int s = 0; s < it.pieces; ++s) m = fmaxf(m, __ldcg(p0 + s * step + D * 32));
+          l = 0.f;
+          for (int s = 0; s < it.pieces; ++s)
+            l = fmaf(ptx::ex2_approx(__ldcg(p0 + s * step + D * 32) - m), __ldcg(p0 + s * step + (D + 1) * 32), l);
+          const float inv = l > 0.f ? 1.f / l : 0.f;
+#pragma unroll 1
+          for (int c = 0; c < D; c += 16) {
+            float ov[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) ov[e] = 0.f;
+            for (int s = 0; s < it.pieces; ++s) {
+              const float f = ptx::ex2_approx(__ldcg(p0 + s * step + D * 32) - m) * inv;
+#pragma unroll
+              for (int e = 0; e < 16; ++e) ov[e] = fmaf(f, __ldcg(p0 + s * step + (c + e) * 32), ov[e]);
+            }
+            if (valid) {
+              uint32_t w[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) w[e] = pt_pack2(ov[2 * e], ov[2 * e + 1]);
+              *reinterpret_cast<uint4 *>(dst + c) = make_uint4(w[0], w[1], w[2], w[3]);
+              *reinterpret_cast<uint4 *>(dst + c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+            }
+          }
+        }
+      }
+      // the next item's first PV product overwrites O only after this warp's next P
+      ptx::tc_fence_before();
+      jg += max(0, it.j1 - it.j0);
+      jt += n_kv;
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, L::TMEM_COLS);
+  }
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  }();
+  return fn;
+}
+
+int sm_count() {
+  int dev = 0, sms = 0;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return sms > 0 ? sms : 1;
+}
+
+}  // namespace
+
+bool make_paged_map(CUtensorMap *map, const bf16 *pool, const PagedView &pv, int G, int D, int box) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
+  if (enc == nullptr) return false;
+  const cuuint64_t ps = (cuuint64_t)1 << pv.page_log2;
+  cuuint64_t dims[4] = {(cuuint64_t)D, ps, (cuuint64_t)G, (cuuint64_t)pv.n_pages};
+  cuuint64_t strides[3] = {(cuuint64_t)D * 2, ps * D * 2, (cuuint64_t)pv.page_stride * 2};
+  cuuint32_t bx[4] = {64, (cuuint32_t)box, 1, 1}, es[4] = {1, 1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<bf16 *>(pool), dims, strides, bx, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool make_heads_map(CUtensorMap *map, const bf16 *q, int rows, int H, int D, int box_heads, int box_rows) {
+  PFN_cuTensorMapEncodeTiled_v12000 enc = encode_fn();
+  if (enc == nullptr) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)H, (cuuint64_t)rows};
+  cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)H * D * 2};
+  cuuint32_t bx[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows}, es[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<bf16 *>(q), dims, strides, bx, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+namespace {
+
+// Sizes of one call: items, and the workspace they need (0 bytes: direct).
+struct PtSizes {
+  int Mq = 0;
+  long long max_blocks = 0;   // (sequence, block) pairs, at most
+  int max_split = 0, max_slots = 0;
+  long long max_entries = 0;
+  size_t off_entries = 0, off_arrivals = 0, off_part = 0, bytes = 0;
+};
+
+PtSizes packed_sizes(const PackedView &b, int H, int G, int D, int sms) {
+  PtSizes z;
+  z.Mq = 128 / (H / G);
+  z.max_blocks = (long long)b.n_tokens / (2 * z.Mq) + (b.n_seqs < b.n_tokens ? b.n_seqs : b.n_tokens);
+  // Direct: no more than one item per SM and at most 8 key tiles each, where a
+  // split would not pay for the planning kernel in front.
+  if (z.max_blocks * G <= sms && b.max_kv_len <= 8 * PT_KEYS) return z;
+  z.max_slots = (2 * sms + G - 1) / G + 1;
+  z.max_split = z.max_slots / 2 + 1;
+  z.max_entries = z.max_blocks + z.max_slots;
+  z.off_entries = sizeof(PtPlan);
+  z.off_arrivals = z.off_entries + (size_t)z.max_entries * sizeof(PtEntry);
+  z.off_part = z.off_arrivals + (size_t)z.max_split * G * 8 * sizeof(int);
+  z.off_part = (z.off_part + 127) / 128 * 128;
+  z.bytes = z.off_part + (size_t)z.max_slots * G * 8 * (D + 2) * 32 * sizeof(float);
+  return z;
+}
+
+template <int D>
+cudaError_t launch_tc(const bf16 *q, const bf16 *k, const bf16 *v, bf16 *o, const PagedView &pv, const PackedView &b,
+                      int H, int G, void *workspace, int *status, cudaStream_t st) {
+  using L = PtLayout<D>;
+  static PerContextOnce attr;
+  cudaError_t e = attr.run([] {
+    return cudaFuncSetAttribute(packed_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
+  });
+  if (e != cudaSuccess) return e;
+  const int sms = sm_count();
+  const PtSizes z = packed_sizes(b, H, G, D, sms);
+  PtArgs a;
+  a.o = o;
+  a.pv = pv;
+  a.b = b;
+  a.H = H;
+  a.G = G;
+  a.r = H / G;
+  a.Mq = z.Mq;
+  a.box = 1 << (pv.page_log2 < 7 ? pv.page_log2 : 7);
+  a.scale_log2 = 1.4426950408889634f / sqrtf((float)D);
+  a.plan = nullptr;
+  a.entries = nullptr;
+  a.arrivals = nullptr;
+  a.part = nullptr;
+  a.status = status;
+  CUtensorMap mq, mk, mv;
+  if (!make_heads_map(&mq, q, b.n_tokens, H, D, a.r, a.Mq) || !make_paged_map(&mk, k, pv, G, D, a.box) ||
+      !make_paged_map(&mv, v, pv, G, D, a.box))
+    return cudaErrorInvalidValue;
+  unsigned grid = (unsigned)(z.max_blocks * G);
+  if (z.bytes > 0) {
+    char *w = reinterpret_cast<char *>(workspace);
+    a.plan = reinterpret_cast<PtPlan *>(w);
+    a.entries = reinterpret_cast<PtEntry *>(w + z.off_entries);
+    a.arrivals = reinterpret_cast<int *>(w + z.off_arrivals);
+    a.part = reinterpret_cast<float *>(w + z.off_part);
+    count_launch();
+    e = launch_pdl(packed_plan_kernel, dim3(1), dim3(PT_PLAN_THREADS), 0, st, pv, b, G, a.Mq, sms, (int)z.max_entries,
+                   z.max_split, a.plan, a.entries, a.arrivals, status);
+    if (e != cudaSuccess) return e;
+    const long long items = z.max_entries * G;
+    grid = (unsigned)(items < sms ? items : sms);
+  }
+  count_launch();
+  return launch_pdl(packed_tc_kernel<D>, dim3(grid), dim3(PT_THREADS), L::BYTES, st, mq, mk, mv, a);
+}
+
+}  // namespace
+
+bool packed_tc_supported(int H, int G, int D) { return (D == 64 || D == 128) && H % G == 0 && H / G <= 128; }
+
+size_t packed_tc_workspace_bytes(const PackedView &b, int H, int G, int D) {
+  return packed_sizes(b, H, G, D, sm_count()).bytes;
+}
+
+cudaError_t launch_packed_tc(const bf16 *q, const bf16 *k, const bf16 *v, bf16 *o, const PagedView &pv,
+                             const PackedView &b, int H, int G, int D, void *workspace, int *status, cudaStream_t st) {
+  if (D == 128) return launch_tc<128>(q, k, v, o, pv, b, H, G, workspace, status, st);
+  return launch_tc<64>(q, k, v, o, pv, b, H, G, workspace, status, st);
+}
+
+}  // namespace llama

@@ -1,6 +1,7 @@
 // Internal launch wrappers of the packed / paged operators (not part of the C ABI).
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 
@@ -21,6 +22,20 @@ cudaError_t launch_rope_kv_paged(const T *qkv, T *q_out, T *k, T *v, const Paged
 template <typename T>
 cudaError_t launch_packed_simt(const T *q, const T *k, const T *v, T *o, const PagedView &pv, const PackedView &b,
                                int H, int G, int D, int *status, cudaStream_t st);
+
+// Tensor maps (packed_tc.cu), 64 columns wide in the 128-byte swizzle: `box` rows of
+// one page and KV head, coordinates (column, row in page, head, page); box_heads x
+// box_rows of packed query rows [rows][H][D], coordinates (column, head, row).
+bool make_paged_map(CUtensorMap *map, const bf16 *pool, const PagedView &pv, int G, int D, int box);
+bool make_heads_map(CUtensorMap *map, const bf16 *q, int rows, int H, int D, int box_heads, int box_rows);
+
+// Tensor-core attention of packed rows (packed_tc.cu): bf16, d_head 64 or 128, up
+// to 128 query heads per KV head.
+bool packed_tc_supported(int H, int G, int D);
+size_t packed_tc_workspace_bytes(const PackedView &b, int H, int G, int D);
+cudaError_t launch_packed_tc(const bf16 *q, const bf16 *k, const bf16 *v, bf16 *o, const PagedView &pv,
+                             const PackedView &b, int H, int G, int D, void *workspace, int *status, cudaStream_t st);
+
 // Split of one sequence's keys over CTAs: parts of `chunk` keys, `n` of them at
 // the longest length the call allows.
 struct DecodeSplit {

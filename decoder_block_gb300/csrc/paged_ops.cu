@@ -125,7 +125,8 @@ size_t llama_op_attention_packed_workspace_bytes(int32_t dtype, const llama_pack
                                                  int32_t G, int32_t D) {
   if (!dtype_ok(dtype) || batch == nullptr || check_heads(H, G, D) != LLAMA_OK || check_batch(batch) != LLAMA_OK)
     return 0;
-  return 0;
+  if (dtype != LLAMA_BF16 || !packed_tc_supported(H, G, D) || batch->n_seqs == 0 || batch->n_tokens == 0) return 0;
+  return packed_tc_workspace_bytes(view_of(batch), H, G, D);
 }
 
 llama_status llama_op_attention_packed(int32_t dtype, const void *q, const llama_paged_kv_cache *kv,
@@ -150,6 +151,9 @@ llama_status llama_op_attention_packed(int32_t dtype, const void *q, const llama
   }
   cudaStream_t st = (cudaStream_t)stream;
   const PackedView b = view_of(batch);
+  if (dtype == LLAMA_BF16 && packed_tc_supported(H, G, D))
+    return status_of(launch_packed_tc((const bf16 *)q, (const bf16 *)kv->k, (const bf16 *)kv->v, (bf16 *)o, pv, b, H,
+                                      G, D, workspace, status, st));
   if (dtype == LLAMA_BF16)
     return status_of(launch_packed_simt<bf16>((const bf16 *)q, (const bf16 *)kv->k, (const bf16 *)kv->v, (bf16 *)o, pv,
                                               b, H, G, D, status, st));
