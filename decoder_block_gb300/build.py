@@ -18,7 +18,7 @@ BUILD = os.path.join(PKG, "_build")
 LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libllama_block.so")
 SOURCES = ["runtime.cu", "ops.cu", "simt_kernels.cu", "gemm_tc.cu", "attention.cu", "decode_attn.cu", "decode_tc.cu", "noalloc.cu", "moe.cu", "decode_fused.cu",
-           "paged_ops.cu", "paged_write.cu", "paged_simt.cu", "packed_tc.cu", "logprobs.cu"]
+           "paged_ops.cu", "paged_write.cu", "paged_simt.cu", "packed_tc.cu", "paged_decode_tc.cu", "logprobs.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1,0 +1,858 @@
+// One new token per sequence over cache pages, bf16, d_head 64 or 128, on
+// tcgen05 tensor cores ("Full Llama 3 transformer block", How it works: cached
+// keys 0 .. kv_len - 1; "The Evolving Transformer 04 · LLaMA", §05 GQA).
+//
+// The cache is read once and that is what bounds the step; the tensor cores keep
+// the CUDA cores free enough for the loads to set the pace.  Keys are the
+// 128-row side of both products (the heads of a group, at most 16, the columns):
+//   S^T[128 keys x 16] = K_tile Q^T,      O^T[D x 16] += V_tile^T P^T,
+// with p = 2^(s log2(e)/sqrt(D) - m), one running maximum m and sum l per head in
+// fp32 over one pass.  Pages arrive as TMA boxes of their own, so a tile in shared
+// memory is the same whatever the page size; V rows behind the last key, which
+// may hold anything, are cleared in shared memory (0 * NaN is not 0).
+//   warp 0     takes items, loads Q, K and V; each lane issues one box of K or V
+//              and holds the next tile's page id
+//   warp 1     one thread issues the MMAs
+//   warps 2-5  softmax, one thread per key; the output, one thread per column
+// The keys of a sequence are split over CTAs and joined, o = sum 2^(m_c - M) o_c /
+// sum 2^(m_c - M) l_c, in one of two ways:
+//   * direct (few sequences, or short ones): a cluster of 1 to 8 CTAs shares a
+//     sequence and KV head and joins through distributed shared memory.  One
+//     launch, no workspace.
+//   * planned: a one-CTA kernel cuts all sequences into chunks of one size, chosen
+//     from their true lengths so that every SM gets several, and zeroes a counter
+//     that persistent CTAs take chunks from; fp32 partials go to the workspace and
+//     a third kernel joins them in chunk order.
+// Every wait is bounded; a kernel that gives up records LLAMA_ERR_DEVICE_TIMEOUT
+// once its copies and MMAs in flight are done.
+#include <float.h>
+
+#include "paged_kernels.h"
+#include "ptx.cuh"
+
+namespace llama {
+namespace {
+
+constexpr int PD_KEYS = 128;    // keys of a tile
+constexpr int PD_N = 16;        // head columns of a tile
+constexpr int PD_THREADS = 192;
+constexpr float PD_RESCALE = 8.0f;
+constexpr int PD_MAX_CLUSTER = 8;
+constexpr int PD_DIRECT_TILES = 8;  // key tiles of a CTA in the direct form, at most
+constexpr int PD_ROUNDS = 12;       // chunks per SM that the planner aims at
+constexpr int PD_PLAN_THREADS = 1024;
+
+template <int D>
+struct PdLayout {
+  static constexpr int STAGES = D == 128 ? 3 : 6;
+  static constexpr int ATOMS = D / 64;
+  static constexpr int ATOM = PD_KEYS * 128;  // 128 rows x 64 columns
+  static constexpr int TILE = ATOMS * ATOM;
+  static constexpr int Q_BYTES = ATOMS * PD_N * 128;
+  static constexpr int P_BYTES = 2 * PD_N * 128;  // 16 rows x 128 keys
+  static constexpr int OFF_K = 0;
+  static constexpr int OFF_V = OFF_K + STAGES * TILE;
+  // With D = 64 the V^T operand is given 128 rows: rows 64-127 read the 16 KB
+  // behind a stage's V (the next stage, or what follows the last one), and their
+  // results are never looked at.
+  static constexpr int OFF_Q = OFF_V + STAGES * TILE;
+  static constexpr int OFF_P = OFF_Q + 2 * Q_BYTES;
+  static constexpr int OFF_RED = OFF_P + 2 * P_BYTES;           // [4][4 warps][PD_N] floats
+  static constexpr int OFF_ITEM = OFF_RED + 4 * 4 * PD_N * 4;   // 2 items
+  static constexpr int OFF_BAR = OFF_ITEM + 2 * 32;
+  static constexpr int NBAR = 2 * STAGES + 18;
+  static constexpr int END = OFF_BAR + NBAR * 8 + 16;
+  static constexpr int BYTES = 1024 + (END > OFF_Q + ATOM ? END : OFF_Q + ATOM);
+  static constexpr uint32_t TMEM_COLS = 64;  // S^T x2, O^T x2, 16 columns each
+};
+
+// A work item: key tiles [j0, j1) of one sequence for one block of heads.
+struct PdItem {
+  int seq;  // -1: no more items
+  int g, h0, nh;
+  int j0, j1, len;
+  int slot;  // partial slot (planned); -1: this item is the whole sequence
+};
+static_assert(sizeof(PdItem) == 32, "PdItem fills its slot");
+
+struct PdPlan {
+  int n_entries, next, n_split, pad;
+};
+struct PdEntry {
+  int seq, j0, j1, slot;
+};
+struct PdSplit {
+  int seq, slot, n, pad;
+};
+
+struct PdArgs {
+  bf16 *o;
+  PagedView pv;
+  const int *kv_lens;
+  int n_seqs, max_kv_len;
+  int H, G, r, subs, box;  // subs: blocks of up to 16 heads per KV head
+  float scale_log2;
+  int cluster;     // direct: CTAs of a sequence and head block
+  PdPlan *plan;    // null: direct
+  PdEntry *entries;
+  float *part;     // [slot][H][D + 2]
+  int *status;
+};
+
+// ------------------------------------------------------------------ plan ---
+__device__ __forceinline__ int cta_scan(int v, int *warp_sums) {
+  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += x;
+  }
+  if (lane == 31) warp_sums[warp] = v;
+  __syncthreads();
+  if (warp == 0) {
+    int s = warp_sums[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += x;
+    }
+    warp_sums[lane] = s;
+  }
+  __syncthreads();
+  const int out = v + (warp > 0 ? warp_sums[warp - 1] : 0);
+  __syncthreads();
+  return out;
+}
+
+__global__ void __launch_bounds__(PD_PLAN_THREADS) decode_plan_kernel(PagedView pv, const int *kv_lens, int n_seqs,
+                                                                      int max_kv_len, int units, int sms,
+                                                                      int max_entries, PdPlan *plan, PdEntry *entries,
+                                                                      PdSplit *splits, int *status) {
+  __shared__ int first[LLAMA_PACKED_MAX_SEQS + 1];  // chunks before sequence i
+  __shared__ int warp_sums[32];
+  __shared__ unsigned long long total;
+  __shared__ int n_split, n_slots;
+  constexpr int PER = LLAMA_PACKED_MAX_SEQS / PD_PLAN_THREADS;
+  const int tid = threadIdx.x;
+  allow_dependents_launch();
+  grid_dependency_wait();
+  if (tid == 0) {
+    total = 0;
+    n_split = n_slots = 0;
+  }
+  __syncthreads();
+  int tiles[PER];
+  unsigned long long mine = 0;
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    const int i = k * PD_PLAN_THREADS + tid;
+    tiles[k] = 0;
+    if (i < n_seqs) {
+      const int raw = __ldg(kv_lens + i), len = checked_len(raw, max_kv_len, pv);
+      if (len != raw) report_status(status, LLAMA_ERR_RANGE);
+      tiles[k] = (len + PD_KEYS - 1) / PD_KEYS;
+      mine += (unsigned)tiles[k];
+    }
+  }
+  atomicAdd(&total, mine);
+  __syncthreads();
+  // Chunks of equal size, PD_ROUNDS per SM: a CTA that streams faster takes more of
+  // them, and the last ones to finish are short.  Chunks of split sequences then
+  // number less than 2 * PD_ROUNDS * sms / units, which sizes the workspace.
+  const unsigned long long share = (total * units + (unsigned)(PD_ROUNDS * sms) - 1) / (unsigned)(PD_ROUNDS * sms);
+  const int chunk = (int)(share > 1 ? share : 1);
+  int base = 0;
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    const int i = k * PD_PLAN_THREADS + tid;
+    if (k * PD_PLAN_THREADS >= n_seqs) break;
+    const int n = i < n_seqs ? max(1, (tiles[k] + chunk - 1) / chunk) : 0;
+    const int end = base + cta_scan(n, warp_sums);
+    if (i < n_seqs) first[i + 1] = end;
+    if (tid == PD_PLAN_THREADS - 1) warp_sums[0] = end;
+    __syncthreads();
+    base = warp_sums[0];
+    __syncthreads();
+  }
+  if (tid == 0) first[0] = 0;
+  __syncthreads();
+  const int n_entries = min(base, max_entries);
+  for (int i = tid; i < n_seqs; i += PD_PLAN_THREADS) {
+    const int n = first[i + 1] - first[i];
+    if (n > 1) {
+      const int at = atomicAdd(&n_split, 1), slot = atomicAdd(&n_slots, n);
+      splits[at] = PdSplit{i, slot, n, 0};
+      if (first[i] < max_entries) entries[first[i]].slot = slot;
+    } else if (first[i] < max_entries) {
+      entries[first[i]].slot = -1;
+    }
+  }
+  __syncthreads();
+  for (int e = tid; e < n_entries; e += PD_PLAN_THREADS) {
+    int lo = 0, hi = n_seqs;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if (first[mid] <= e) lo = mid;
+      else hi = mid;
+    }
+    const int c = e - first[lo];
+    const int nt = (checked_len(__ldg(kv_lens + lo), max_kv_len, pv) + PD_KEYS - 1) / PD_KEYS;
+    PdEntry x;
+    x.seq = lo;
+    x.j0 = c * chunk;
+    x.j1 = min(nt, x.j0 + chunk);
+    // the sequence's first entry holds its slots' start; other threads read it here
+    const int s0 = *reinterpret_cast<volatile int *>(&entries[first[lo]].slot);
+    x.slot = s0 < 0 ? -1 : s0 + c;
+    entries[e].seq = x.seq;
+    entries[e].j0 = x.j0;
+    entries[e].j1 = x.j1;
+    if (c > 0) entries[e].slot = x.slot;
+  }
+  if (tid == 0) {
+    plan->n_entries = n_entries;
+    plan->next = 0;
+    plan->n_split = n_split;
+  }
+}
+
+// ------------------------------------------------------------- attention ---
+// RN: head columns the softmax works on, the smallest of 2, 4, 8, 16 that holds
+// the block's heads; P^T rows RN .. 15 stay zero.
+template <int D, int RN>
+__global__ void __launch_bounds__(PD_THREADS, 1)
+    paged_decode_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                           const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PdArgs a) {
+  using L = PdLayout<D>;
+  constexpr int STAGES = L::STAGES, ATOMS = L::ATOMS;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::OFF_BAR);
+  uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + L::NBAR);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+  float *red = reinterpret_cast<float *>(smem + L::OFF_RED);
+  PdItem *item_slot = reinterpret_cast<PdItem *>(smem + L::OFF_ITEM);
+
+  const uint32_t s0 = ptx::smem_u32(smem);
+  const uint32_t b0 = ptx::smem_u32(bars);
+  auto kv_full = [&](int s) { return b0 + 8u * s; };
+  auto kv_empty = [&](int s) { return b0 + 8u * (STAGES + s); };
+  auto q_full = [&](int i) { return b0 + 8u * (2 * STAGES + i); };
+  auto q_empty = [&](int i) { return b0 + 8u * (2 * STAGES + 2 + i); };
+  auto s_full = [&](int i) { return b0 + 8u * (2 * STAGES + 4 + i); };
+  auto p_full = [&](int i) { return b0 + 8u * (2 * STAGES + 6 + i); };
+  auto p_free = [&](int i) { return b0 + 8u * (2 * STAGES + 8 + i); };
+  auto o_full = [&](int i) { return b0 + 8u * (2 * STAGES + 10 + i); };
+  auto o_free = [&](int i) { return b0 + 8u * (2 * STAGES + 12 + i); };
+  const uint32_t fin = b0 + 8u * (2 * STAGES + 14);
+  auto red_full = [&](int i) { return b0 + 8u * (2 * STAGES + 15 + i); };
+  const uint32_t lred_full = b0 + 8u * (2 * STAGES + 17);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
+    if (ptx::mbar_wait(bar, parity, abort_flag, nullptr, 0)) return true;
+    report_status(a.status, LLAMA_ERR_DEVICE_TIMEOUT);
+    return false;
+  };
+  auto wait_warp = [&](uint32_t bar, uint32_t parity) { return __all_sync(0xffffffffu, wait(bar, parity)) != 0; };
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      ptx::mbar_init(kv_full(s), 1);
+      ptx::mbar_init(kv_empty(s), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(q_full(i), 1);
+      ptx::mbar_init(q_empty(i), 5);  // the MMAs reading Q are done; each softmax warp has read the item
+      ptx::mbar_init(s_full(i), 1);
+      ptx::mbar_init(p_full(i), 128);
+      ptx::mbar_init(p_free(i), 1);
+      ptx::mbar_init(o_full(i), 1);
+      ptx::mbar_init(o_free(i), 128);
+      ptx::mbar_init(red_full(i), 4);
+    }
+    ptx::mbar_init(fin, 1);
+    ptx::mbar_init(lred_full, 4);
+    *abort_flag = 0;
+    ptx::fence_mbar_init();
+  }
+  if (RN < PD_N && warp >= 2) {  // P^T rows the softmax never writes
+    uint4 *pz = reinterpret_cast<uint4 *>(smem + L::OFF_P);
+    for (int i = threadIdx.x - 64; i < 2 * L::P_BYTES / 16; i += 128) pz[i] = make_uint4(0, 0, 0, 0);
+    ptx::fence_proxy_async_smem();
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(ptx::smem_u32(tmem_slot), L::TMEM_COLS);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  allow_dependents_launch();
+  grid_dependency_wait();
+  const int rank = a.cluster > 1 ? (int)(blockIdx.x % a.cluster) : 0;
+  const int units = a.G * a.subs;
+
+  if (warp == 0) {
+    // ---------------------------------------------------------- producer ---
+    if (lane == 0) {
+      ptx::tma_prefetch_desc(&tmQ);
+      ptx::tma_prefetch_desc(&tmK);
+      ptx::tma_prefetch_desc(&tmV);
+    }
+    const int n_items = a.plan != nullptr ? *reinterpret_cast<volatile int *>(&a.plan->n_entries) * units
+                                          : a.n_seqs * units;
+    auto fetch = [&](int k) {  // the CTA's k-th item (all lanes)
+      PdItem it;
+      it.seq = -1;
+      int u = 0;
+      if (a.plan != nullptr) {
+        if (lane == 0) u = atomicAdd(&a.plan->next, 1);
+        u = __shfl_sync(0xffffffffu, u, 0);
+      } else {
+        u = blockIdx.x / a.cluster + k * (gridDim.x / a.cluster);
+      }
+      if (u >= n_items) return it;
+      const int unit = u % units;
+      it.g = unit / a.subs;
+      it.h0 = it.g * a.r + (unit % a.subs) * PD_N;
+      it.nh = min(PD_N, (it.g + 1) * a.r - it.h0);
+      it.slot = -1;
+      int seq = u / units;
+      if (a.plan != nullptr) {
+        const int4 e = __ldcg(reinterpret_cast<const int4 *>(a.entries + seq));
+        seq = e.x;
+        it.j0 = e.y;
+        it.j1 = e.z;
+        it.slot = e.w;
+      }
+      const int raw = __ldg(a.kv_lens + seq);
+      it.seq = seq;
+      it.len = checked_len(raw, a.max_kv_len, a.pv);
+      if (a.plan == nullptr) {
+        if (it.len != raw && lane == 0) report_status(a.status, LLAMA_ERR_RANGE);
+        const int nt = (it.len + PD_KEYS - 1) / PD_KEYS, each = (nt + a.cluster - 1) / a.cluster;
+        it.j0 = min(nt, rank * each);
+        it.j1 = min(nt, it.j0 + each);
+      }
+      return it;
+    };
+    const int boxes_tile = PD_KEYS / a.box;  // pages of a tile (1 when pages are larger)
+    const bool is_v = lane >= 16;            // lanes 0-15 load K, 16-31 V
+    const int my_box = (lane & 15) / ATOMS, my_at = (lane & 15) % ATOMS;
+    const uint32_t dst = (is_v ? L::OFF_V : L::OFF_K) + my_at * L::ATOM + my_box * a.box * 128;
+    const CUtensorMap *map = is_v ? &tmV : &tmK;
+    const uint64_t once = ptx::policy_evict_first();  // each cached key is read once per call
+    // Page of this lane's box of key tile j: its id, n_pages (a page of zeros) when
+    // the id is out of range, -1 when the tile has no such box.
+    auto page_of = [&](const PdItem &it, int j) {
+      const int key = j * PD_KEYS + my_box * a.box;
+      if (my_box >= boxes_tile || j >= it.j1 || key >= it.len) return -1;
+      const int id = a.pv.page(it.seq, key >> a.pv.page_log2);
+      if (id < 0) report_status(a.status, LLAMA_ERR_RANGE);
+      return id < 0 ? a.pv.n_pages : id;
+    };
+    int tile = 0, items = 0;
+    bool ended = false, ok = true;
+    PdItem it = fetch(0);
+    for (int nq = 0; ok; ++nq) {
+      const int qi = nq & 1;
+      int page = it.seq >= 0 ? page_of(it, it.j0) : -1;
+      if (!wait_warp(q_empty(qi), ((nq >> 1) & 1) ^ 1)) break;
+      if (lane == 0) item_slot[qi] = it;  // published by the q_full arrival
+      __syncwarp();
+      if (it.seq < 0) {
+        if (lane == 0) ptx::mbar_arrive(q_full(qi));
+        ended = true;
+        break;
+      }
+      if (lane == 0) {
+        ptx::mbar_arrive_expect_tx(q_full(qi), L::Q_BYTES);
+        for (int at = 0; at < ATOMS; ++at)
+          ptx::tma_load_3d(s0 + L::OFF_Q + qi * L::Q_BYTES + at * (PD_N * 128), &tmQ, at * 64, it.h0, it.seq,
+                           q_full(qi));
+      }
+      ++items;
+      PdItem next;
+      bool fetched = false;
+      for (int j = it.j0; j < it.j1; ++j, ++tile) {
+        const int st = tile % STAGES;
+        const int boxes = min(boxes_tile, (it.len - j * PD_KEYS + a.box - 1) / a.box);
+        const int row = (j * PD_KEYS) & ((1 << a.pv.page_log2) - 1) & ~(a.box - 1);
+        const int page_now = page;
+        if (j + 1 < it.j1) {
+          page = page_of(it, j + 1);
+        } else {
+          next = fetch(nq + 1);
+          fetched = true;
+        }
+        if (!wait_warp(kv_empty(st), ((tile / STAGES) & 1) ^ 1)) {
+          ok = false;
+          break;
+        }
+        if (lane == 0) ptx::mbar_arrive_expect_tx(kv_full(st), 2u * boxes * ATOMS * a.box * 128u);
+        __syncwarp();
+        if (page_now >= 0)
+          ptx::tma_load_4d_hint(s0 + dst + st * L::TILE, map, my_at * 64, row, it.g, page_now, kv_full(st), once);
+      }
+      if (!ok) break;
+      if (!fetched) next = fetch(nq + 1);
+      it = next;
+    }
+    // every issued copy lands before the CTA exits
+    __syncwarp();
+    if (lane == 0) {
+      for (int t = max(0, tile - STAGES); t < tile; ++t)
+        ptx::mbar_drain(kv_full(t % STAGES), (t / STAGES) & 1, nullptr, 0);
+      // the last Q load's phase is the newest of its barrier unless the end was handed
+      // over there; the MMA thread waited for the one before it
+      for (int q = max(0, items - 2); q < items; ++q)
+        if (!(ended && (items & 1) == (q & 1))) ptx::mbar_drain(q_full(q & 1), (q >> 1) & 1, nullptr, 0);
+    }
+  } else if (warp == 1) {
+    // --------------------------------------------------------------- MMA ---
+    if (lane == 0) {
+      constexpr uint32_t idesc_s = ptx::idesc_bf16_f32(PD_KEYS, PD_N, false);
+      // O^T = V^T P^T: A = V^T (MN-major), B = P^T (K-major)
+      constexpr uint32_t idesc_o = ptx::idesc_bf16_f32(128, PD_N, false) | (1u << 15);
+      int tile = 0;
+      bool ok = true;
+      for (int nq = 0; ok; ++nq) {
+        const int qi = nq & 1, ob = nq & 1;
+        if (!wait(q_full(qi), (nq >> 1) & 1)) break;
+        const PdItem it = item_slot[qi];
+        if (it.seq < 0) break;
+        const int nt = it.j1 - it.j0;
+        if (!wait(o_free(ob), ((nq >> 1) & 1) ^ 1)) break;
+        const uint32_t qbase = s0 + L::OFF_Q + qi * L::Q_BYTES;
+        auto issue_s = [&](int t) -> bool {
+          const int st = t % STAGES;
+          if (!wait(kv_full(st), (t / STAGES) & 1)) return false;
+          ptx::tc_fence_after();
+          const uint32_t kb = s0 + L::OFF_K + st * L::TILE;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t ka = (kk / 4) * L::ATOM + (kk % 4) * 32;
+            const uint32_t qa = (kk / 4) * (PD_N * 128) + (kk % 4) * 32;
+            ptx::mma_bf16_ss(tmem + (t & 1) * PD_N, ptx::smem_desc_sw128(kb + ka), ptx::smem_desc_sw128(qbase + qa),
+                             idesc_s, kk > 0 ? 1u : 0u);
+          }
+          ptx::mma_commit(s_full(t & 1));
+          return true;
+        };
+        if (nt > 0) ok = issue_s(tile);
+        for (int j = 0; j < nt && ok; ++j, ++tile) {
+          // one tile ahead: the softmax of this tile overlaps the next S^T
+          if (j + 1 < nt && !issue_s(tile + 1)) {
+            ok = false;
+            break;
+          }
+          const int st = tile % STAGES, sb = tile & 1;
+          if (!wait(p_full(sb), (tile >> 1) & 1)) {
+            ok = false;
+            break;
+          }
+          ptx::tc_fence_after();
+          const uint32_t vb = s0 + L::OFF_V + st * L::TILE;
+          const uint32_t pb = s0 + L::OFF_P + sb * L::P_BYTES;
+#pragma unroll
+          for (int kk = 0; kk < PD_KEYS / 16; ++kk) {
+            const uint64_t adesc = ptx::smem_desc_sw128_mn(vb + kk * 16 * 128, L::ATOM, 1024);
+            const uint32_t pa = (kk / 4) * (PD_N * 128) + (kk % 4) * 32;
+            ptx::mma_bf16_ss(tmem + 32 + ob * PD_N, adesc, ptx::smem_desc_sw128(pb + pa), idesc_o,
+                             (j > 0 || kk > 0) ? 1u : 0u);
+          }
+          ptx::mma_commit(p_free(sb));
+          ptx::mma_commit(kv_empty(st));
+        }
+        if (!ok) break;
+        ptx::mma_commit(q_empty(qi));
+        ptx::mma_commit(o_full(ob));
+      }
+      ptx::mma_commit(fin);
+      ptx::mbar_drain(fin, 0, nullptr, 0);
+    }
+  } else {
+    // --------------------------------------------------- softmax, output ---
+    const int w4 = warp - 2;
+    const int qq = warp & 3;         // TMEM lane quarter
+    const int row = qq * 32 + lane;  // key of a tile (S^T), column of the head (O^T)
+    const uint32_t lane_base = tmem + ((uint32_t)(qq * 32) << 16);
+    // One value per head of each warp to all four: lane h of a warp stores its head's
+    // and one arrival per warp completes the phase.
+    auto exchange = [&](float *slots, const float(&v)[RN], uint32_t bar, uint32_t parity) -> bool {
+      if (lane < RN) {
+        float x = v[0];
+#pragma unroll
+        for (int h = 1; h < RN; ++h)
+          if (lane == h) x = v[h];
+        slots[w4 * PD_N + lane] = x;
+      }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(bar);
+      return wait_warp(bar, parity);
+    };
+    int tile = 0;
+    bool ok = true;
+    for (int nq = 0; ok; ++nq) {
+      const int qi = nq & 1, ob = nq & 1;
+      if (!wait_warp(q_full(qi), (nq >> 1) & 1)) break;
+      const PdItem it = item_slot[qi];
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(q_empty(qi));
+      if (it.seq < 0) break;
+      const int nt = it.j1 - it.j0;
+      float m_run[RN], l_run[RN];
+#pragma unroll
+      for (int h = 0; h < RN; ++h) {
+        m_run[h] = -INFINITY;
+        l_run[h] = 0.f;
+      }
+      for (int j = 0; j < nt; ++j, ++tile) {
+        const int sb = tile & 1;
+        if (!wait_warp(s_full(sb), (tile >> 1) & 1)) {
+          ok = false;
+          break;
+        }
+        ptx::tc_fence_after();
+        float s[PD_N];
+        ptx::tmem_ld16(lane_base + sb * PD_N, s);
+        const int key0 = (it.j0 + j) * PD_KEYS;
+        const bool valid = key0 + row < it.len;
+        if (key0 + PD_KEYS > it.len) {  // the sequence's last tile: clear V behind its last key
+          const int st = tile % STAGES;
+          if (!wait_warp(kv_full(st), (tile / STAGES) & 1)) {
+            ok = false;
+            break;
+          }
+          if (!valid) {
+            uint4 *vr = reinterpret_cast<uint4 *>(smem + L::OFF_V + st * L::TILE + row * 128);
+#pragma unroll
+            for (int at = 0; at < ATOMS; ++at)
+#pragma unroll
+              for (int c = 0; c < 8; ++c) vr[at * (L::ATOM / 16) + c] = make_uint4(0, 0, 0, 0);
+          }
+        }
+        // per-head maximum over the tile: warp shuffles, then across the 4 warps
+        float mx[RN];
+#pragma unroll
+        for (int h = 0; h < RN; ++h) mx[h] = warp_max((valid && h < it.nh) ? s[h] : -INFINITY);
+        float *rs = red + (tile & 1) * (4 * PD_N);
+        if (!exchange(rs, mx, red_full(tile & 1), (tile >> 1) & 1)) {
+          ok = false;
+          break;
+        }
+        bool need_any = false;
+        float alpha[RN];
+#pragma unroll
+        for (int h = 0; h < RN; ++h) {
+          const float mt =
+              fmaxf(fmaxf(rs[h], rs[PD_N + h]), fmaxf(rs[2 * PD_N + h], rs[3 * PD_N + h])) * a.scale_log2;
+          alpha[h] = 1.f;
+          if (h < it.nh && mt > m_run[h] + PD_RESCALE) {
+            alpha[h] = ptx::ex2_approx(m_run[h] - mt);
+            m_run[h] = mt;
+            need_any = true;
+          }
+        }
+        // P^T into shared memory: row h (query head), column = key, 128-byte swizzle
+        if (!wait_warp(p_free(sb), ((tile >> 1) & 1) ^ 1)) {
+          ok = false;
+          break;
+        }
+        uint8_t *pbuf = smem + L::OFF_P + sb * L::P_BYTES + (row / 64) * (PD_N * 128);
+        const int c = row % 64;
+#pragma unroll
+        for (int h = 0; h < RN; ++h) {
+          const float p = (valid && h < it.nh) ? ptx::ex2_approx(fmaf(s[h], a.scale_log2, -m_run[h])) : 0.f;
+          l_run[h] = l_run[h] * alpha[h] + p;
+          // bf16 P: the tensor cores' operand; the sum keeps the unrounded values
+          *reinterpret_cast<bf16 *>(pbuf + h * 128 + ((c >> 3) ^ (h & 7)) * 16 + (c & 7) * 2) = __float2bfloat16_rn(p);
+        }
+        if (need_any && j > 0) {  // rescale O^T (thread = column) before this tile's product
+          if (!wait_warp(p_free(sb ^ 1), ((tile - 1) >> 1) & 1)) {
+            ok = false;
+            break;
+          }
+          ptx::tc_fence_after();
+          float ov[PD_N];
+          ptx::tmem_ld16(lane_base + 32 + ob * PD_N, ov);
+          uint32_t wv[PD_N];
+#pragma unroll
+          for (int h = 0; h < PD_N; ++h) wv[h] = __float_as_uint(h < RN ? ov[h] * alpha[h < RN ? h : 0] : ov[h]);
+          ptx::tmem_st16(lane_base + 32 + ob * PD_N, wv);
+          ptx::tmem_st_wait();
+        }
+        ptx::fence_proxy_async_smem();
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(p_full(sb));
+      }
+      if (!ok) break;
+      // item end: sum l over the 128 keys, read O^T
+      if (!wait_warp(o_full(ob), (nq >> 1) & 1)) break;
+      ptx::tc_fence_after();
+      float ov[PD_N];
+      if (nt > 0) {
+        ptx::tmem_ld16(lane_base + 32 + ob * PD_N, ov);
+      } else {
+#pragma unroll
+        for (int h = 0; h < PD_N; ++h) ov[h] = 0.f;
+      }
+      ptx::tc_fence_before();
+      ptx::mbar_arrive(o_free(ob));
+#pragma unroll
+      for (int h = 0; h < RN; ++h) l_run[h] = warp_sum(l_run[h]);
+      float *ls = red + (2 + ob) * (4 * PD_N);
+      if (!exchange(ls, l_run, lred_full, nq & 1)) break;
+#pragma unroll
+      for (int h = 0; h < RN; ++h) {
+        if (h >= it.nh || row >= D) continue;
+        const float l = ls[h] + ls[PD_N + h] + ls[2 * PD_N + h] + ls[3 * PD_N + h];
+        if (a.cluster > 1) {  // for the join below: [PD_N][D + 2] over the first K stage, idle by now
+          float *pp = reinterpret_cast<float *>(smem + L::OFF_K) + h * (D + 2);
+          pp[row] = ov[h];
+          if (row == 0) {
+            pp[D] = m_run[h];
+            pp[D + 1] = l;
+          }
+        } else if (it.slot < 0) {
+          a.o[((size_t)it.seq * a.H + it.h0 + h) * D + row] = __float2bfloat16_rn(l > 0.f ? ov[h] / l : 0.f);
+        } else {
+          float *pp = a.part + ((size_t)it.slot * a.H + it.h0 + h) * (D + 2);
+          pp[row] = ov[h];
+          if (row == 0) {
+            pp[D] = m_run[h];
+            pp[D + 1] = l;
+          }
+        }
+      }
+    }
+  }
+  __syncwarp();
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (a.cluster > 1) {
+    // one item per cluster: its CTAs' parts meet here, head h finished by CTA h % cluster
+    ptx::cluster_sync();
+    const int u = blockIdx.x / a.cluster, unit = u % units, seq = u / units;
+    const int g = unit / a.subs, h0 = g * a.r + (unit % a.subs) * PD_N;
+    const int nh = min(PD_N, (g + 1) * a.r - h0);
+    if (*abort_flag == 0 && threadIdx.x < D) {
+      const uint32_t part = s0 + L::OFF_K;
+      for (int h = rank; h < nh; h += a.cluster) {
+        float mc[PD_MAX_CLUSTER], lc[PD_MAX_CLUSTER], oc[PD_MAX_CLUSTER];
+        float m = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < PD_MAX_CLUSTER; ++c) {
+          mc[c] = -INFINITY;
+          lc[c] = oc[c] = 0.f;
+          if (c < a.cluster) {
+            const uint32_t p = ptx::mapa_shared(part, c) + (uint32_t)(h * (D + 2)) * 4;
+            mc[c] = ptx::ld_cluster_f32(p + D * 4);
+            lc[c] = ptx::ld_cluster_f32(p + (D + 1) * 4);
+            oc[c] = ptx::ld_cluster_f32(p + threadIdx.x * 4);
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < PD_MAX_CLUSTER; ++c) m = fmaxf(m, mc[c]);
+        float l = 0.f, o = 0.f;
+#pragma unroll
+        for (int c = 0; c < PD_MAX_CLUSTER; ++c) {
+          const float f = mc[c] == -INFINITY ? 0.f : ptx::ex2_approx(mc[c] - m);
+          l = fmaf(f, lc[c], l);
+          o = fmaf(f, oc[c], o);
+        }
+        a.o[((size_t)seq * a.H + h0 + h) * D + threadIdx.x] = __float2bfloat16_rn(l > 0.f ? o / l : 0.f);
+      }
+    }
+    ptx::cluster_sync();  // no CTA leaves while others read its shared memory
+  }
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, L::TMEM_COLS);
+  }
+}
+
+// Joins the chunks of one split sequence's head: a CTA of 256 threads, D / 4 per
+// chunk, 8 or 16 chunks at a time.
+template <int D>
+__global__ void __launch_bounds__(256) decode_join_kernel(const PdPlan *plan, const PdSplit *splits,
+                                                          const float *__restrict__ part, bf16 *__restrict__ o,
+                                                          int H) {
+  constexpr int LANES = D / 4, GROUPS = 256 / LANES;
+  __shared__ float sm[8], so[GROUPS][D], sl[GROUPS];
+  grid_dependency_wait();
+  const int k = blockIdx.x / H, h = blockIdx.x % H;
+  if (k >= plan->n_split) return;
+  const PdSplit s = splits[k];
+  const float *p = part + ((size_t)s.slot * H + h) * (D + 2);
+  const size_t step = (size_t)H * (D + 2);
+  float m = -INFINITY;
+  for (int c = threadIdx.x; c < s.n; c += 256) m = fmaxf(m, p[c * step + D]);
+  m = warp_max(m);
+  if ((threadIdx.x & 31) == 0) sm[threadIdx.x / 32] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 8; ++w) m = fmaxf(m, sm[w]);
+  const int grp = threadIdx.x / LANES, d = threadIdx.x % LANES * 4;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = 0.f;
+#pragma unroll 4
+  for (int c = grp; c < s.n; c += GROUPS) {
+    const float *pc = p + c * step;
+    const float f = ptx::ex2_approx(pc[D] - m);
+    const float2 x = *reinterpret_cast<const float2 *>(pc + d), y = *reinterpret_cast<const float2 *>(pc + d + 2);
+    l = fmaf(f, pc[D + 1], l);
+    acc.x = fmaf(f, x.x, acc.x);
+    acc.y = fmaf(f, x.y, acc.y);
+    acc.z = fmaf(f, y.x, acc.z);
+    acc.w = fmaf(f, y.y, acc.w);
+  }
+  *reinterpret_cast<float4 *>(&so[grp][d]) = acc;
+  if (d == 0) sl[grp] = l;
+  __syncthreads();
+  if (threadIdx.x < D) {
+    float x = 0.f, z = 0.f;
+#pragma unroll
+    for (int g = 0; g < GROUPS; ++g) {
+      x += so[g][threadIdx.x];
+      z += sl[g];
+    }
+    o[((size_t)s.seq * H + h) * D + threadIdx.x] = __float2bfloat16_rn(x / z);
+  }
+}
+
+int sm_count() {
+  int dev = 0, sms = 0;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return sms > 0 ? sms : 1;
+}
+
+struct PdSizes {
+  int units = 0, cluster = 0;  // cluster: CTAs of a direct item (0: planned)
+  long long max_entries = 0;
+  int max_split = 0;
+  size_t off_entries = 0, off_splits = 0, off_part = 0, bytes = 0;
+};
+
+PdSizes decode_sizes(int n_seqs, int max_kv_len, int H, int G, int D, int sms) {
+  PdSizes z;
+  z.units = G * ((H / G + PD_N - 1) / PD_N);
+  const long long items = (long long)n_seqs * z.units;
+  const int tiles = (max_kv_len + PD_KEYS - 1) / PD_KEYS;
+  int cluster = 1;
+  while (cluster < PD_MAX_CLUSTER && items * cluster * 2 <= sms && tiles > cluster) cluster *= 2;
+  if ((tiles + cluster - 1) / cluster <= PD_DIRECT_TILES) {
+    z.cluster = cluster;
+    return z;
+  }
+  const int most = 2 * ((PD_ROUNDS * sms + z.units - 1) / z.units) + 2;  // chunks of split sequences
+  z.max_entries = (long long)n_seqs + most;
+  z.max_split = n_seqs < most / 2 ? n_seqs : most / 2;
+  z.off_entries = sizeof(PdPlan);
+  z.off_splits = z.off_entries + (size_t)z.max_entries * sizeof(PdEntry);
+  z.off_part = z.off_splits + (size_t)z.max_split * sizeof(PdSplit);
+  z.off_part = (z.off_part + 127) / 128 * 128;
+  z.bytes = z.off_part + (size_t)most * H * (D + 2) * sizeof(float);
+  return z;
+}
+
+template <int D, int RN>
+cudaError_t launch_tc(const bf16 *q, const bf16 *k, const bf16 *v, bf16 *o, const PagedView &pv, const int *kv_lens,
+                      int n_seqs, int max_kv_len, int H, int G, void *workspace, int *status, cudaStream_t st) {
+  using L = PdLayout<D>;
+  static PerContextOnce attr;
+  cudaError_t e = attr.run([] {
+    return cudaFuncSetAttribute(paged_decode_tc_kernel<D, RN>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
+  });
+  if (e != cudaSuccess) return e;
+  const int sms = sm_count();
+  const PdSizes z = decode_sizes(n_seqs, max_kv_len, H, G, D, sms);
+  PdArgs a;
+  a.o = o;
+  a.pv = pv;
+  a.kv_lens = kv_lens;
+  a.n_seqs = n_seqs;
+  a.max_kv_len = max_kv_len;
+  a.H = H;
+  a.G = G;
+  a.r = H / G;
+  a.subs = z.units / G;
+  a.box = 1 << (pv.page_log2 < 7 ? pv.page_log2 : 7);
+  a.scale_log2 = 1.4426950408889634f / sqrtf((float)D);
+  a.cluster = 1;
+  a.plan = nullptr;
+  a.entries = nullptr;
+  a.part = nullptr;
+  a.status = status;
+  CUtensorMap mq, mk, mv;
+  if (!make_heads_map(&mq, q, n_seqs, H, D, PD_N, 1) || !make_paged_map(&mk, k, pv, G, D, a.box) ||
+      !make_paged_map(&mv, v, pv, G, D, a.box))
+    return cudaErrorInvalidValue;
+  const long long items = (long long)n_seqs * z.units;
+  if (z.cluster > 0) {
+    a.cluster = z.cluster;
+    cudaLaunchAttribute attrs[2];
+    attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attrs[0].val.programmaticStreamSerializationAllowed = 1;
+    attrs[1].id = cudaLaunchAttributeClusterDimension;
+    attrs[1].val.clusterDim.x = (unsigned)z.cluster;
+    attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    // clusters: one item each; single CTAs: one per SM, each looping over its items
+    cfg.gridDim = dim3((unsigned)(z.cluster > 1 ? items * z.cluster : (items < sms ? items : sms)));
+    cfg.blockDim = dim3(PD_THREADS);
+    cfg.dynamicSmemBytes = L::BYTES;
+    cfg.stream = st;
+    cfg.attrs = attrs;
+    cfg.numAttrs = z.cluster > 1 ? 2 : 1;
+    count_launch();
+    return cudaLaunchKernelEx(&cfg, paged_decode_tc_kernel<D, RN>, mq, mk, mv, a);
+  }
+  char *w = reinterpret_cast<char *>(workspace);
+  a.plan = reinterpret_cast<PdPlan *>(w);
+  a.entries = reinterpret_cast<PdEntry *>(w + z.off_entries);
+  PdSplit *splits = reinterpret_cast<PdSplit *>(w + z.off_splits);
+  a.part = reinterpret_cast<float *>(w + z.off_part);
+  count_launch();
+  e = launch_pdl(decode_plan_kernel, dim3(1), dim3(PD_PLAN_THREADS), 0, st, pv, kv_lens, n_seqs, max_kv_len, z.units,
+                 sms, (int)z.max_entries, a.plan, a.entries, splits, status);
+  if (e != cudaSuccess) return e;
+  count_launch();
+  const long long most = z.max_entries * z.units;
+  e = launch_pdl(paged_decode_tc_kernel<D, RN>, dim3((unsigned)(most < sms ? most : sms)), dim3(PD_THREADS), L::BYTES,
+                 st, mq, mk, mv, a);
+  if (e != cudaSuccess) return e;
+  count_launch();
+  return launch_pdl(decode_join_kernel<D>, dim3((unsigned)(z.max_split * H)), dim3(256), 0, st,
+                    (const PdPlan *)a.plan, (const PdSplit *)splits, (const float *)a.part, o, H);
+}
+
+template <int D>
+cudaError_t launch_by_heads(const bf16 *q, const bf16 *k, const bf16 *v, bf16 *o, const PagedView &pv,
+                            const int *kv_lens, int n_seqs, int max_kv_len, int H, int G, void *workspace, int *status,
+                            cudaStream_t st) {
+  const int r = H / G;
+  auto f = r <= 2 ? launch_tc<D, 2> : r <= 4 ? launch_tc<D, 4> : r <= 8 ? launch_tc<D, 8> : launch_tc<D, 16>;
+  return f(q, k, v, o, pv, kv_lens, n_seqs, max_kv_len, H, G, workspace, status, st);
+}
+
+}  // namespace
+
+bool paged_decode_tc_supported(int H, int G, int D) { return (D == 64 || D == 128) && H % G == 0; }
+
+size_t paged_decode_tc_workspace_bytes(int n_seqs, int max_kv_len, int H, int G, int D) {
+  return decode_sizes(n_seqs, max_kv_len, H, G, D, sm_count()).bytes;
+}
+
+cudaError_t launch_paged_decode_tc(const bf16 *q, const bf16 *k, const bf16 *v, bf16 *o, const PagedView &pv,
+                                   const int *kv_lens, int n_seqs, int max_kv_len, int H, int G, int D,
+                                   void *workspace, int *status, cudaStream_t st) {
+  if (D == 128)
+    return launch_by_heads<128>(q, k, v, o, pv, kv_lens, n_seqs, max_kv_len, H, G, workspace, status, st);
+  return launch_by_heads<64>(q, k, v, o, pv, kv_lens, n_seqs, max_kv_len, H, G, workspace, status, st);
+}
+
+}  // namespace llama

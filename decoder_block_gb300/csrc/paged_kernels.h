@@ -36,6 +36,13 @@ size_t packed_tc_workspace_bytes(const PackedView &b, int H, int G, int D);
 cudaError_t launch_packed_tc(const bf16 *q, const bf16 *k, const bf16 *v, bf16 *o, const PagedView &pv,
                              const PackedView &b, int H, int G, int D, void *workspace, int *status, cudaStream_t st);
 
+// Tensor-core decode attention (paged_decode_tc.cu): bf16, d_head 64 or 128.
+bool paged_decode_tc_supported(int H, int G, int D);
+size_t paged_decode_tc_workspace_bytes(int n_seqs, int max_kv_len, int H, int G, int D);
+cudaError_t launch_paged_decode_tc(const bf16 *q, const bf16 *k, const bf16 *v, bf16 *o, const PagedView &pv,
+                                   const int *kv_lens, int n_seqs, int max_kv_len, int H, int G, int D,
+                                   void *workspace, int *status, cudaStream_t st);
+
 // Split of one sequence's keys over CTAs: parts of `chunk` keys, `n` of them at
 // the longest length the call allows.
 struct DecodeSplit {

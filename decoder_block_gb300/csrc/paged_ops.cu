@@ -166,6 +166,8 @@ size_t llama_op_attention_paged_decode_workspace_bytes(int32_t dtype, int32_t n_
   if (!dtype_ok(dtype) || n_seqs <= 0 || n_seqs > LLAMA_PACKED_MAX_SEQS || max_kv_len < 0 ||
       check_heads(H, G, D) != LLAMA_OK)
     return 0;
+  if (dtype == LLAMA_BF16 && paged_decode_tc_supported(H, G, D))
+    return paged_decode_tc_workspace_bytes(n_seqs, max_kv_len, H, G, D);
   const DecodeSplit split = paged_decode_simt_split(n_seqs, max_kv_len, H, G);
   return split.n > 1 ? (size_t)n_seqs * H * split.n * (D + 2) * sizeof(float) : 0;
 }
@@ -191,6 +193,9 @@ llama_status llama_op_attention_paged_decode(int32_t dtype, const void *q, const
     if (s != LLAMA_OK) return s;
   }
   cudaStream_t st = (cudaStream_t)stream;
+  if (dtype == LLAMA_BF16 && paged_decode_tc_supported(H, G, D))
+    return status_of(launch_paged_decode_tc((const bf16 *)q, (const bf16 *)kv->k, (const bf16 *)kv->v, (bf16 *)o, pv,
+                                            kv_lens, n_seqs, max_kv_len, H, G, D, workspace, status, st));
   float *part = (float *)workspace;
   if (dtype == LLAMA_BF16)
     return status_of(launch_paged_decode_simt<bf16>((const bf16 *)q, (const bf16 *)kv->k, (const bf16 *)kv->v,

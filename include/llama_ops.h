@@ -208,9 +208,10 @@ llama_status llama_op_attention_packed(int32_t dtype, const void *q, const llama
 
 /* The same for one new token per sequence: q, o: [n_seqs][H][D], row i at
  * position kv_lens[i] - 1.  A sequence of length 0 gets zeros.  The cache's
- * length is split over the GPU and the parts joined by their log-sum-exp;
- * max_kv_len (an upper bound, as in llama_packed_batch) fixes the split, so that
- * results depend on it in their last bits but not from run to run. */
+ * length is split over the GPU and the parts joined by their log-sum-exp.  The
+ * split follows from the sizes, max_kv_len (an upper bound, as in
+ * llama_packed_batch) and the lengths of all sequences of the call, so the last
+ * bits of a result depend on them, but not from run to run. */
 size_t llama_op_attention_paged_decode_workspace_bytes(int32_t dtype, int32_t n_seqs, int32_t max_kv_len,
                                                        int32_t H, int32_t G, int32_t D);
 llama_status llama_op_attention_paged_decode(int32_t dtype, const void *q, const llama_paged_kv_cache *kv,
