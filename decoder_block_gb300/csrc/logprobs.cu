@@ -1,111 +1,535 @@
 // Log-probabilities of given tokens, entropy and the likeliest tokens of logits
 // rows ("The Evolving Transformer 04 · LLaMA", §07 Assemble: the logits of a
 // position are the unnormalised log-probabilities of its next token).
-//   m = max_v x_v, Z = sum_v e^(x_v - m):  ln p(v) = x_v - m - ln Z,
-//   entropy = ln Z - sum_v e^(x_v - m) (x_v - m) / Z.
+//   m = max_v x_v, Z = sum_v e^(x_v - m), U = sum_v e^(x_v - m) (x_v - m):
+//   ln p(v) = (x_v - m) - ln Z,   entropy = ln Z - U / Z,
+// and the top_k largest x in the order (x descending, id ascending).
+//
+// Every logit is read once, and that is what bounds it.  Each thread keeps a running
+// (m, Z, U) -- a larger m' turns Z into f Z and U into f (U + Z (m - m')) with f =
+// e^(m - m') -- and, for the top, only which three of its batches of 16 or 32 logits
+// had the largest maxima and the fourth largest maximum: 14 instructions a batch.
+// Then the k-th largest of 64 such maxima is a bound that at least k logits reach, so
+// nothing below it is among the top; the few batches whose maximum reaches it are
+// read again, and each of the k to about 2 k logits found takes the place given by
+// how many of the others are ahead of it.  A row whose top is not found that way (a
+// thread with four such batches, or a great many equal logits) is read a second time,
+// its warps sorting candidates into lists of 32.  (Sorting candidates as they come
+// took 202 us where this takes 171: votes and shuffles in every batch.)
+// A row belongs to one warp, to a CTA, or to a cluster of CTAs whose parts meet
+// through distributed shared memory (few rows: the row is what there is to split).
+#include <float.h>
 #include <limits.h>
 #include <math.h>
 
 #include "paged_kernels.h"
+#include "ptx.cuh"
 
 namespace llama {
 namespace {
 
-constexpr int LP_THREADS = 512;
+constexpr int LP_THREADS = 256;
+constexpr int LP_WARPS = LP_THREADS / 32;
+// CTAs of an SM and 16-byte vectors of a lane's batch: 64 KB of an SM's loads in flight.
+// 2048 x 128256, top 20, fp32 / bf16: 171 / 113 us (1.05 GB at 0.91 of the measured
+// copy rate); with 3 CTAs 181 / 122 us, with 5 (spills) 252 / 454 us.
+constexpr int LP_CTAS = 4;
+constexpr int LP_VECS = 4;
+constexpr int LP_STEP = 32 * LP_VECS;  // vectors of a warp's batch
+constexpr int LP_MAX_CLUSTER = 8;
+constexpr float LP_LOG2E = 1.4426950408889634f;
 
-template <typename F>
-__device__ __forceinline__ float block_reduce(float v, float *buf, F &&op) {
-  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
-  if (lane == 0) buf[warp] = v;
-  __syncthreads();
-  v = buf[0];
-  for (int w = 1; w < LP_THREADS / 32; ++w) v = op(v, buf[w]);
-  __syncthreads();
-  return v;
+struct LpArgs {
+  const void *logits;
+  long long stride;
+  const int *targets;
+  int rows, V;
+  float *logprobs, *entropy;
+  int top_k;
+  int *top_ids;
+  float *top_logprobs;
+  int *status;
+  int bad_target;
+  int cluster;
+};
+
+__device__ __forceinline__ float max_nan(float a, float b) {  // NaN when either is
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(LP_THREADS) token_logprobs_kernel(const T *__restrict__ logits, long long stride,
-                                                                    const int *__restrict__ targets, int V,
-                                                                    float *__restrict__ logprobs,
-                                                                    float *__restrict__ entropy, int top_k,
-                                                                    int *__restrict__ top_ids,
-                                                                    float *__restrict__ top_logprobs, int *status, int bad_target) {
-  __shared__ float buf[LP_THREADS / 32];
-  __shared__ int ibuf[LP_THREADS / 32];
-  const int row = blockIdx.x, warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-  const T *x = logits + (size_t)row * stride;
-  float m = -INFINITY;
-  for (int v = threadIdx.x; v < V; v += LP_THREADS) m = fmaxf(m, to_f32<T>(x[v]));
-  m = block_reduce(m, buf, [](float a, float b) { return fmaxf(a, b); });
-  float z = 0.f, u = 0.f;
-  if (m > -INFINITY)
-    for (int v = threadIdx.x; v < V; v += LP_THREADS) {
-      const float d = to_f32<T>(x[v]) - m, e = expf(d);
-      z += e;
-      u += d == -INFINITY ? 0.f : e * d;
-    }
-  else  // no logit above -inf; NaN still has to show
-    for (int v = threadIdx.x; v < V; v += LP_THREADS)
-      if (isnan(to_f32<T>(x[v]))) z = NAN;
-  auto add = [](float a, float b) { return a + b; };
-  z = block_reduce(z, buf, add);
-  u = block_reduce(u, buf, add);
-  const float log_z = logf(z);  // -inf for a row of nothing but -inf
-  auto logprob = [&](float v) { return (m == -INFINITY && z == 0.f) ? -INFINITY : (v - m) - log_z; };
-  if (threadIdx.x == 0) {
-    if (logprobs != nullptr) {
-      const int y = targets[row];
-      if (y >= 0 && y < V) {
-        logprobs[row] = logprob(to_f32<T>(x[y]));
-      } else {
-        logprobs[row] = y == -1 ? 0.f : NAN;
-        if (y != -1) report_status(status, bad_target);
-      }
-    }
-    if (entropy != nullptr) entropy[row] = (m == -INFINITY && z == 0.f) ? 0.f : log_z - u / z;
-  }
-  // top_k times the best logit behind the last one taken
-  float last = INFINITY;
-  int last_id = -1;
-  for (int j = 0; j < top_k; ++j) {
-    float best = -INFINITY;
-    int id = INT_MAX;
-    for (int v = threadIdx.x; v < V; v += LP_THREADS) {
-      const float a = to_f32<T>(x[v]);
-      if (!(a < last || (a == last && v > last_id))) continue;
-      if (a > best || (a == best && v < id)) {
-        best = a;
-        id = v;
-      }
-    }
-    auto merge = [&](float ob, int oi) {
-      if (ob > best || (ob == best && oi < id)) {
-        best = ob;
-        id = oi;
-      }
-    };
+// Order of the top: larger logit first, lower id among equals.
+__device__ __forceinline__ bool ahead(float a, int ia, float b, int ib) { return a > b || (a == b && ia < ib); }
+
+// ------------------------------------------------------------ statistics ---
+struct Stats {
+  float m, z, u;
+};
+__device__ __forceinline__ Stats merge(const Stats &a, const Stats &b) {
+  Stats r;
+  r.m = fmaxf(a.m, b.m);
+  // m is finite or +inf; the side that has the maximum (also +inf) stays as it is
+  const float da = a.m == r.m ? 0.f : fmaxf(a.m - r.m, -200.f), db = b.m == r.m ? 0.f : fmaxf(b.m - r.m, -200.f);
+  const float fa = ptx::ex2_approx(da * LP_LOG2E), fb = ptx::ex2_approx(db * LP_LOG2E);
+  r.z = a.z * fa + b.z * fb;
+  r.u = fa * fmaf(a.z, da, a.u) + fb * fmaf(b.z, db, b.u);
+  return r;
+}
+// A row's statistics from one part in each of the first n lanes (a power of two).
+__device__ __forceinline__ Stats lanes_merge(Stats s, int n) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-      merge(__shfl_xor_sync(0xffffffffu, best, o), __shfl_xor_sync(0xffffffffu, id, o));
-    if (lane == 0) {
-      buf[warp] = best;
-      ibuf[warp] = id;
-    }
-    __syncthreads();
-    best = buf[0];
-    id = ibuf[0];
-    for (int w = 1; w < LP_THREADS / 32; ++w) merge(buf[w], ibuf[w]);
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      top_ids[(size_t)row * top_k + j] = id == INT_MAX ? -1 : id;
-      top_logprobs[(size_t)row * top_k + j] = id == INT_MAX ? NAN : logprob(best);
-    }
-    last = id == INT_MAX ? -INFINITY : best;
-    last_id = id;
+  for (int o = 16; o > 0; o >>= 1) {
+    if (o >= n) continue;
+    Stats t;
+    t.m = __shfl_xor_sync(0xffffffffu, s.m, o);
+    t.z = __shfl_xor_sync(0xffffffffu, s.z, o);
+    t.u = __shfl_xor_sync(0xffffffffu, s.u, o);
+    s = merge(s, t);
   }
+  s.m = __shfl_sync(0xffffffffu, s.m, 0);
+  s.z = __shfl_sync(0xffffffffu, s.z, 0);
+  s.u = __shfl_sync(0xffffffffu, s.u, 0);
+  return s;
+}
+
+// A batch: LP_VECS vectors per lane at v0 + 32 j + lane (index in the row's aligned
+// part), -inf behind v_end.
+template <typename T>
+__device__ __forceinline__ void load_batch(Vec16<T> (&x)[LP_VECS], const Vec16<T> *vec, int v0, int v_end) {
+#pragma unroll
+  for (int j = 0; j < LP_VECS; ++j) {
+    const int at = v0 + 32 * j + (int)(threadIdx.x & 31);
+    if (at < v_end) {
+      x[j].raw = __ldcs(reinterpret_cast<const uint4 *>(vec + at));
+    } else {
+#pragma unroll
+      for (int e = 0; e < Vec16<T>::N; ++e) x[j].set(e, -INFINITY);
+    }
+  }
+}
+
+// What a thread keeps of the part of a row that it reads.
+template <typename T>
+struct RowScan {
+  static constexpr int V = Vec16<T>::N;
+  float m = -FLT_MAX;  // finite, so that -inf alone gives weights of 0; a logit of -FLT_MAX itself counts
+  uint64_t z[2], u[2];  // four independent sums each
+  // m is the largest maximum of a batch, b2 to b4 the next ones; of batches i1 to i3
+  float b2 = -INFINITY, b3 = -INFINITY, b4 = -INFINITY;
+  int i1 = -1, i2 = -1, i3 = -1;
+
+  __device__ __forceinline__ RowScan() { z[0] = z[1] = u[0] = u[1] = ptx::f2pack(0.f, 0.f); }
+  __device__ __forceinline__ void raise(float nm) {
+    const float d = fmaxf(m - nm, -200.f);  // the old sums are worth nothing beyond e^-200
+    const float f = ptx::ex2_approx(d * LP_LOG2E);
+    const uint64_t f2 = ptx::f2pack(f, f), d2 = ptx::f2pack(d, d);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      u[i] = ptx::fmul2(ptx::ffma2(z[i], d2, u[i]), f2);
+      z[i] = ptx::fmul2(z[i], f2);
+    }
+    m = nm;
+  }
+  __device__ __forceinline__ void add(float a, float b, int i) {
+    float d0, d1;
+    ptx::f2unpack(ptx::fadd2(ptx::f2pack(a, b), ptx::f2pack(-m, -m)), d0, d1);
+    d0 = max_nan(d0, -200.f);  // -inf: weight 0 and 0 in U instead of 0 * inf
+    d1 = max_nan(d1, -200.f);
+    const uint64_t d2 = ptx::f2pack(d0, d1);
+    float y0, y1;
+    ptx::f2unpack(ptx::fmul2(d2, ptx::f2pack(LP_LOG2E, LP_LOG2E)), y0, y1);
+    const uint64_t e2 = ptx::f2pack(ptx::ex2_approx(y0), ptx::ex2_approx(y1));
+    z[i & 1] = ptx::fadd2(z[i & 1], e2);
+    u[i & 1] = ptx::ffma2(e2, d2, u[i & 1]);
+  }
+  __device__ __forceinline__ Stats stats() const {
+    float a, b, c, d;
+    Stats s;
+    s.m = m;
+    ptx::f2unpack(z[0], a, b);
+    ptx::f2unpack(z[1], c, d);
+    s.z = (a + b) + (c + d);
+    ptx::f2unpack(u[0], a, b);
+    ptx::f2unpack(u[1], c, d);
+    s.u = (a + b) + (c + d);
+    return s;
+  }
+  __device__ __forceinline__ void batch(const Vec16<T> (&x)[LP_VECS], int round) {
+    float bm = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < LP_VECS; ++j)
+#pragma unroll
+      for (int e = 0; e < V; ++e) bm = fmaxf(bm, x[j].get(e));
+    b4 = fmaxf(b4, fminf(bm, b3));
+    i3 = bm > b2 ? i2 : bm > b3 ? round : i3;
+    b3 = fmaxf(b3, fminf(bm, b2));
+    i2 = bm > m ? i1 : bm > b2 ? round : i2;
+    b2 = fmaxf(b2, fminf(bm, m));
+    i1 = bm > m ? round : i1;
+    if (bm > m) raise(bm);
+#pragma unroll
+    for (int j = 0; j < LP_VECS; ++j)
+#pragma unroll
+      for (int e = 0; e < V; e += 2) add(x[j].get(e), x[j].get(e + 1), j + e / 2);
+  }
+};
+
+// ------------------------------------------------------------------- top ---
+struct __align__(8) Cand {
+  float v;
+  int id;
+};
+
+// A float as an integer of the same order, its six low bits replaced by `slot`.
+__device__ __forceinline__ int slot_key(float x, int slot) {
+  const int b = __float_as_int(x);
+  return ((b < 0 ? b ^ 0x7fffffff : b) & ~63) | slot;
+}
+__device__ __forceinline__ float key_value(int key) {  // at most the value the key was made of
+  key &= ~63;
+  const float x = __int_as_float(key < 0 ? key ^ 0x7fffffff : key);
+  return x == x ? x : -INFINITY;
+}
+// Calls f(i, key) with the i-th largest of the lanes' two keys each for i < n, in every lane.
+template <typename F>
+__device__ __forceinline__ void top_keys(int a, int b, int n, F &&f) {
+  for (int i = 0; i < n; ++i) {
+    const int best = __reduce_max_sync(0xffffffffu, max(a, b));
+    if (a == best) a = INT_MIN;
+    if (b == best) b = INT_MIN;
+    f(i, best);
+  }
+}
+
+// The logits of one thread's batch, its vectors `first` + 32 j, that reach `bound`,
+// appended to all[].
+template <typename T>
+__device__ __forceinline__ void pick(const Vec16<T> *vec, int first, int v_end, int id0, float bound, Cand *all, int *n,
+                                     int cap) {
+  constexpr int V = Vec16<T>::N;
+  Vec16<T> x[LP_VECS];
+#pragma unroll
+  for (int j = 0; j < LP_VECS; ++j)
+    if (first + 32 * j < v_end) x[j] = load16<T>(reinterpret_cast<const T *>(vec + first + 32 * j));
+#pragma unroll
+  for (int j = 0; j < LP_VECS; ++j) {
+    if (first + 32 * j >= v_end) continue;
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const float v = x[j].get(e);
+      if (v >= bound) {
+        const int at = atomicAdd(n, 1);
+        if (at < cap) all[at] = Cand{v, id0 + (first + 32 * j) * V + e};
+      }
+    }
+  }
+}
+
+// A warp's sorted list: lane j holds the j-th entry.
+struct TopList {
+  float v;
+  int id;
+  // Keeps, of this lane's entry and that of the lane s away, the one ahead or behind.
+  __device__ __forceinline__ void exchange(int s, bool keep_ahead) {
+    const float xv = __shfl_xor_sync(0xffffffffu, v, s);
+    const int xi = __shfl_xor_sync(0xffffffffu, id, s);
+    if (keep_ahead == ahead(xv, xi, v, id)) {
+      v = xv;
+      id = xi;
+    }
+  }
+  __device__ __forceinline__ void sort() {  // bitonic, the one that is ahead in the lower lane
+    const int lane = threadIdx.x & 31;
+    for (int size = 2; size <= 32; size *= 2)
+      for (int s = size / 2; s > 0; s /= 2) exchange(s, ((lane & s) == 0) == ((lane & size) == 0));
+  }
+  // The 32 first of this list and another sorted one: the larger of entry j here and
+  // entry 31 - j there are those 32, in a bitonic order that five steps sort.
+  __device__ __forceinline__ void merge(float ov, int oi) {
+    const int lane = threadIdx.x & 31;
+    ov = __shfl_xor_sync(0xffffffffu, ov, 31);
+    oi = __shfl_xor_sync(0xffffffffu, oi, 31);
+    if (ahead(ov, oi, v, id)) {
+      v = ov;
+      id = oi;
+    }
+    for (int s = 16; s > 0; s >>= 1) exchange(s, (lane & s) == 0);
+  }
+};
+
+constexpr int LP_WAIT = 32 + 512;  // candidates of a warp: fewer than 32 wait, 16 per lane join them
+
+// The second pass over a warp's part of a row: everything that reaches `bound` and is
+// ahead of the k-th entry of the warp's list waits in `wait` and is sorted into the
+// list 32 at a time.  Leaves list and rest together in `wait`; returns their number,
+// less than 64.
+template <typename T>
+__device__ __noinline__ int second_pass(const Vec16<T> *vec, int v0, int step, int n_vec, int id0, int k, float bound,
+                                        Cand *wait) {
+  constexpr int V = Vec16<T>::N;
+  const int lane = threadIdx.x & 31;
+  TopList top{-INFINITY, INT_MAX};
+  float kth = -INFINITY;
+  int kth_id = INT_MAX, waiting = 0;
+  for (; v0 < n_vec; v0 += step) {
+#pragma unroll 1
+    for (int j = 0; j < LP_VECS; ++j) {
+      const int at = v0 + 32 * j + lane;
+      Vec16<T> x;
+      float vm = -INFINITY;
+      if (at < n_vec) {
+        x = load16<T>(reinterpret_cast<const T *>(vec + at));
+#pragma unroll
+        for (int e = 0; e < V; ++e) vm = fmaxf(vm, x.get(e));
+      }
+      if (!__any_sync(0xffffffffu, at < n_vec && vm >= bound && vm >= kth)) continue;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float v = at < n_vec ? x.get(e) : 0.f;
+        const int id = id0 + at * V + e;
+        const bool c = at < n_vec && v >= bound && ahead(v, id, kth, kth_id);
+        const unsigned mask = __ballot_sync(0xffffffffu, c);
+        if (c) wait[waiting + __popc(mask & ((1u << lane) - 1u))] = Cand{v, id};
+        waiting += __popc(mask);
+      }
+      if (waiting < 32) continue;
+      __syncwarp();
+      while (waiting >= 32) {
+        waiting -= 32;
+        TopList c{wait[waiting + lane].v, wait[waiting + lane].id};
+        c.sort();
+        top.merge(c.v, c.id);
+      }
+      __syncwarp();
+      kth = __shfl_sync(0xffffffffu, top.v, k - 1);
+      kth_id = __shfl_sync(0xffffffffu, top.id, k - 1);
+    }
+  }
+  const bool c = top.id != INT_MAX;
+  const unsigned mask = __ballot_sync(0xffffffffu, c);
+  if (c) wait[waiting + __popc(mask & ((1u << lane) - 1u))] = Cand{top.v, top.id};
+  __syncwarp();
+  return waiting + __popc(mask);
+}
+
+// Entry of this candidate in the order of all n of `all`: how many are ahead of it.
+__device__ __forceinline__ int rank_of(const Cand &c, const Cand *all, int n) {
+  int rank = 0;
+#pragma unroll 8
+  for (int i = 0; i < n; ++i) {
+    const Cand o = all[i];
+    rank += ahead(o.v, o.id, c.v, c.id) ? 1 : 0;
+  }
+  return rank;
+}
+
+// --------------------------------------------------------------- results ---
+// The given token of a row, looked up while the row is read.
+template <typename T>
+struct Target {
+  int id = -1;
+  float logit = 0.f;
+  __device__ __forceinline__ Target(const LpArgs &a, int row, const T *x, bool needed) {
+    if (!needed || a.logprobs == nullptr) return;
+    id = a.targets[row];
+    if (id >= 0 && id < a.V) logit = to_f32<T>(x[id]);
+  }
+};
+
+// A row's results from its statistics and its n candidates, by one warp (THREADS =
+// 32) or by a whole CTA.
+template <typename T, int THREADS>
+__device__ __forceinline__ void finish_row(const LpArgs &a, int row, const Target<T> &y, const Stats &s,
+                                           const Cand *all, int n) {
+  const int tid = THREADS == 32 ? threadIdx.x & 31 : threadIdx.x;
+  const bool empty = s.m == -FLT_MAX && s.z == 0.f;  // nothing but -inf
+  const float log_z = logf(s.z);
+  auto logprob = [&](float v) { return empty ? -INFINITY : (v - s.m) - log_z; };
+  if (tid == 0) {
+    if (a.logprobs != nullptr) {
+      float lp = y.id == -1 ? 0.f : NAN;
+      if (y.id >= 0 && y.id < a.V) lp = logprob(y.logit);
+      else if (y.id != -1) report_status(a.status, a.bad_target);
+      a.logprobs[row] = lp;
+    }
+    if (a.entropy != nullptr) a.entropy[row] = empty ? 0.f : log_z - s.u / s.z;
+  }
+  if (a.top_k == 0) return;
+  int *ids = a.top_ids + (size_t)row * a.top_k;
+  float *lps = a.top_logprobs + (size_t)row * a.top_k;
+  for (int i = tid; i < n; i += THREADS) {
+    const Cand c = all[i];
+    const int at = rank_of(c, all, n);
+    if (at < a.top_k) {
+      ids[at] = c.id;
+      lps[at] = logprob(c.v);
+    }
+  }
+  for (int at = n + tid; at < a.top_k; at += THREADS) {  // fewer logits than top_k that are not NaN
+    ids[at] = -1;
+    lps[at] = NAN;
+  }
+}
+
+// WPR: warps of a row in this CTA (1: eight rows per CTA; 8: one row, or a
+// cluster's part of one).
+template <typename T, int WPR>
+__global__ void __launch_bounds__(LP_THREADS, LP_CTAS) token_logprobs_kernel(const __grid_constant__ LpArgs a) {
+  constexpr int V = Vec16<T>::N, GROUPS = LP_WARPS / WPR;  // rows of this CTA
+  constexpr int CAP = WPR * 64, ENDS = 2 * (V - 1);        // candidates kept; logits outside whole vectors
+  __shared__ Cand s_wait[LP_WARPS][LP_WAIT];
+  __shared__ Cand s_all[GROUPS][CAP + ENDS];
+  __shared__ Cand s_first[32];  // a CTA's top, for the cluster's first CTA
+  __shared__ Stats s_stats[LP_WARPS];
+  __shared__ int s_max[GROUPS][64];
+  __shared__ int s_batch[GROUPS][CAP];  // batches to read again
+  __shared__ int s_n[GROUPS], s_batches[GROUPS];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, k = a.top_k, group = WPR == 1 ? warp : 0;
+  const int parts = WPR == 1 ? 1 : WPR * a.cluster;  // warps that share a row
+  const int rank = WPR == 1 ? 0 : (int)(blockIdx.x % a.cluster);
+  const int row = WPR == 1 ? (int)blockIdx.x * LP_WARPS + warp : (int)(blockIdx.x / a.cluster);
+  const int part = WPR == 1 ? 0 : rank * WPR + warp;
+  if (WPR == 1 && row >= a.rows) return;
+  auto sync = [] {
+    if (WPR == 1) __syncwarp();
+    else __syncthreads();
+  };
+  const T *x = reinterpret_cast<const T *>(a.logits) + (long long)row * a.stride;
+  const Target<T> y(a, row, x, part == 0);
+  // logits before the first 16-byte boundary, then whole vectors, then the rest
+  const int head = min(a.V, (int)((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / (int)sizeof(T));
+  const int n_vec = (a.V - head) / V;
+  const Vec16<T> *vec = reinterpret_cast<const Vec16<T> *>(x + head);
+  if (WPR == 1 || warp == 0) {
+    s_max[group][lane] = s_max[group][lane + 32] = slot_key(-INFINITY, 0);
+    if (lane == 0) s_n[group] = s_batches[group] = 0;
+  }
+  if (k > 0) sync();
+  RowScan<T> r;
+  int round = 0;
+  for (int v0 = part * LP_STEP; v0 < n_vec; v0 += parts * LP_STEP, ++round) {
+    Vec16<T> b[LP_VECS];
+    load_batch<T>(b, vec, v0, n_vec);
+    r.batch(b, round);
+  }
+  // in front of the first 16-byte boundary and behind the last one
+  const bool has_ends = part == parts - 1;
+  const int n_ends = has_ends ? a.V - n_vec * V : 0;  // at most ENDS
+  const int end_id = lane < head ? lane : lane + n_vec * V;
+  const float end = lane < n_ends ? to_f32<T>(x[end_id]) : -INFINITY;
+  if (has_ends) {
+    if (end > r.m) r.raise(end);
+    r.add(end, -INFINITY, 0);
+  }
+  Stats s = lanes_merge(r.stats(), 32);
+  if (WPR > 1 && lane == 0) s_stats[warp] = s;
+  int n = 0;
+  Cand *all = s_all[group];
+  if (k > 0) {
+    // 64 of the threads' two largest maxima: the largest of every warp that read a batch
+    const int active = WPR == 1 ? 1 : max(1, min(WPR, (n_vec - rank * WPR * LP_STEP + LP_STEP - 1) / LP_STEP));
+    const int share = (64 + active - 1) / active;
+    const int k1 = slot_key(r.m == -FLT_MAX ? -INFINITY : r.m, lane), k2 = slot_key(r.b2, 32 + lane);
+    if (share == 64) {
+      if (warp < active || WPR == 1) {
+        s_max[group][lane] = k1;
+        s_max[group][lane + 32] = k2;
+      }
+    } else if (warp < active) {
+      top_keys(k1, k2, share, [&](int i, int best) {
+        if (lane == 0 && warp * share + i < 64) s_max[0][warp * share + i] = best;
+      });
+    }
+    sync();
+    float bound = -INFINITY;
+    top_keys((s_max[group][lane] & ~63) | lane, (s_max[group][lane + 32] & ~63) | (32 + lane), k,
+             [&](int i, int best) { bound = key_value(best); });
+    // No bound, or a thread with a fourth batch that reaches it: read the row again.
+    const bool again = bound == -INFINITY || r.b4 >= bound;
+    bool redo = WPR == 1 ? __any_sync(0xffffffffu, again) != 0 : __syncthreads_or(again) != 0;
+    if (!redo) {
+      const int step = parts * LP_STEP, first = part * LP_STEP + lane;
+      auto need = [&](float max, int i) {
+        if (!(max >= bound) || i < 0) return;
+        const int at = atomicAdd(&s_batches[group], 1);
+        if (at < CAP) s_batch[group][at] = first + i * step;
+      };
+      need(r.m, r.i1);
+      need(r.b2, r.i2);
+      need(r.b3, r.i3);
+      sync();
+      const int n_batch = min(s_batches[group], CAP);
+      for (int i = WPR == 1 ? lane : threadIdx.x; i < n_batch; i += 32 * WPR)
+        pick<T>(vec, s_batch[group][i], n_vec, head, bound, all, &s_n[group], CAP);
+      sync();
+      n = s_n[group];
+      redo = n > CAP || s_batches[group] > CAP;
+      sync();
+    }
+    if (redo) {
+      if (WPR == 1 ? lane == 0 : threadIdx.x == 0) s_n[group] = 0;
+      sync();
+      const int mine =
+          second_pass<T>(vec, part * LP_STEP, parts * LP_STEP, n_vec, head, k, bound, s_wait[warp]);
+      int at = 0;
+      if (lane == 0) at = atomicAdd(&s_n[group], mine);
+      at = __shfl_sync(0xffffffffu, at, 0);
+      for (int i = lane; i < mine; i += 32) all[at + i] = s_wait[warp][i];
+      sync();
+      n = s_n[group];
+    }
+    if (has_ends && lane < n_ends && end >= bound) all[atomicAdd(&s_n[group], 1)] = Cand{end, end_id};  // never a NaN
+    sync();
+    n = s_n[group];
+  } else if (WPR > 1) {
+    __syncthreads();
+  }
+  if (WPR == 1) {
+    finish_row<T, 32>(a, row, y, s, all, n);
+    return;
+  }
+  s = lanes_merge(s_stats[lane & (LP_WARPS - 1)], LP_WARPS);
+  if (a.cluster == 1) {
+    finish_row<T, LP_THREADS>(a, row, y, s, all, n);
+    return;
+  }
+  // The CTAs' tops and statistics meet in the cluster's first CTA.
+  if (k > 0) {
+    if (threadIdx.x < 32) s_first[threadIdx.x] = Cand{-INFINITY, INT_MAX};
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += LP_THREADS) {
+      const Cand c = all[i];
+      const int at = rank_of(c, all, n);
+      if (at < k) s_first[at] = c;
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) s_stats[0] = s;
+  if (threadIdx.x == 0) s_n[0] = 0;
+  __syncthreads();
+  ptx::cluster_sync();
+  if (rank == 0) {
+    if (k > 0 && warp < a.cluster) {
+      const uint32_t from = ptx::mapa_shared(ptx::smem_u32(&s_first[lane]), warp);
+      Cand c;
+      c.v = ptx::ld_cluster_f32(from);
+      c.id = __float_as_int(ptx::ld_cluster_f32(from + 4));
+      const unsigned mask = __ballot_sync(0xffffffffu, c.id != INT_MAX);
+      int at = 0;
+      if (lane == 0) at = atomicAdd(&s_n[0], __popc(mask));
+      at = __shfl_sync(0xffffffffu, at, 0);
+      if (c.id != INT_MAX) all[at + __popc(mask & ((1u << lane) - 1u))] = c;
+    }
+    const uint32_t st = ptx::mapa_shared(ptx::smem_u32(&s_stats[0]), lane & (a.cluster - 1));
+    s.m = ptx::ld_cluster_f32(st);
+    s.z = ptx::ld_cluster_f32(st + 4);
+    s.u = ptx::ld_cluster_f32(st + 8);
+    s = lanes_merge(s, a.cluster);
+    __syncthreads();
+  }
+  ptx::cluster_sync();  // no CTA leaves while its parts are read
+  if (rank == 0) finish_row<T, LP_THREADS>(a, row, y, s, all, k > 0 ? s_n[0] : 0);
 }
 
 }  // namespace
@@ -115,10 +539,47 @@ cudaError_t launch_token_logprobs(const T *logits, long long row_stride, const i
                                   float *logprobs, float *entropy, int top_k, int *top_ids, float *top_logprobs,
                                   int *status, int bad_target, cudaStream_t st) {
   if (rows <= 0) return cudaSuccess;
+  int dev = 0, sms = 0;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  LpArgs a;
+  a.logits = logits;
+  a.stride = row_stride;
+  a.targets = targets;
+  a.rows = rows;
+  a.V = V;
+  a.logprobs = logprobs;
+  a.entropy = entropy;
+  a.top_k = top_k;
+  a.top_ids = top_ids;
+  a.top_logprobs = top_logprobs;
+  a.status = status;
+  a.bad_target = bad_target;
+  a.cluster = 1;
+  constexpr int CTA_LOGITS = LP_THREADS * LP_VECS * Vec16<T>::N;  // one batch of a CTA
   count_launch();
-  token_logprobs_kernel<T><<<(unsigned)rows, LP_THREADS, 0, st>>>(logits, row_stride, targets, V, logprobs, entropy,
-                                                                  top_k, top_ids, top_logprobs, status, bad_target);
-  return cudaGetLastError();
+  // Rows of a few batches, and enough of them: a warp each.
+  if (V <= 2 * CTA_LOGITS && (long long)rows >= 4LL * sms) {
+    token_logprobs_kernel<T, 1><<<(unsigned)((rows + LP_WARPS - 1) / LP_WARPS), LP_THREADS, 0, st>>>(a);
+    return cudaGetLastError();
+  }
+  // Too few rows to fill the SMs (four CTAs each): split each over a cluster, down to
+  // one batch per CTA.
+  while (a.cluster < LP_MAX_CLUSTER && (long long)rows * a.cluster * 2 <= 4LL * sms &&
+         V / (a.cluster * 2) >= CTA_LOGITS)
+    a.cluster *= 2;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = (unsigned)a.cluster;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  if ((long long)rows * a.cluster > 0x7fffffffLL) return cudaErrorInvalidValue;
+  cfg.gridDim = dim3((unsigned)(rows * a.cluster));
+  cfg.blockDim = dim3(LP_THREADS);
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = a.cluster > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<T, LP_WARPS>, a);
 }
 
 template cudaError_t launch_token_logprobs<float>(const float *, long long, const int *, int, int, float *, float *,
