@@ -1,7 +1,7 @@
-// Causal grouped-query attention of a packed batch over cache pages, bf16,
-// d_head 64 or 128, on tcgen05 tensor cores ("The Evolving Transformer 04 ·
-// LLaMA", §05 GQA; "Full Llama 3 transformer block", How it works: keys
-// j <= position).  For token t at position p and its KV head's keys and values
+// Causal grouped-query attention of a packed batch over cache pages, bf16, on
+// tcgen05 tensor cores ("The Evolving Transformer 04 · LLaMA", §05 GQA; "Full Llama 3
+// transformer block", How it works: keys j <= position).  d_head 64 or 128; 16 and 32
+// run as 64, their tiles filled up with zeros by the copies.  For token t at position p and its KV head's keys and values
 //   o = sum_{j<=p} 2^(x_j - m) v_j / sum_{j<=p} 2^(x_j - m),  x_j = q.k_j log2(e) / sqrt(D),
 // in one pass over the keys with the running maximum m and sum in fp32.
 //
@@ -88,7 +88,7 @@ struct PtArgs {
   bf16 *o;
   PagedView pv;
   PackedView b;
-  int H, G, r, Mq, box;  // box: rows of a page's TMA box
+  int H, G, D, r, Mq, box;  // D: the heads' width (the kernel's or less); box: rows of a page's TMA box
   float scale_log2;
   PtPlan *plan;          // null: direct
   PtEntry *entries;
@@ -698,7 +698,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
       float la, lb;
       ptx::f2unpack(l2, la, lb);
       float l = la + lb;
-      bf16 *dst = a.o + ((size_t)(it.first + rel) * a.H + it.g * a.r + hh) * D;
+      bf16 *dst = a.o + ((size_t)(it.first + rel) * a.H + it.g * a.r + hh) * a.D;
       if (it.slot < 0) {
         const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll
@@ -710,7 +710,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
 #pragma unroll
             for (int e = 0; e < 16; ++e) ov[e] = 0.f;
           }
-          if (valid) {
+          if (valid && c < a.D) {
             uint32_t w[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) w[e] = pt_pack2(ov[2 * e] * inv, ov[2 * e + 1] * inv);
@@ -763,7 +763,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
 #pragma unroll
               for (int e = 0; e < 16; ++e) ov[e] = fmaf(f, __ldcg(p0 + s * step + (c + e) * 32), ov[e]);
             }
-            if (valid) {
+            if (valid && c < a.D) {
               uint32_t w[8];
 #pragma unroll
               for (int e = 0; e < 8; ++e) w[e] = pt_pack2(ov[2 * e], ov[2 * e + 1]);
@@ -862,7 +862,7 @@ PtSizes packed_sizes(const PackedView &b, int H, int G, int D, int sms) {
 
 template <int D>
 cudaError_t launch_tc(const bf16 *q, const bf16 *k, const bf16 *v, bf16 *o, const PagedView &pv, const PackedView &b,
-                      int H, int G, void *workspace, int *status, cudaStream_t st) {
+                      int H, int G, int width, void *workspace, int *status, cudaStream_t st) {
   using L = PtLayout<D>;
   static PerContextOnce attr;
   cudaError_t e = attr.run([] {
@@ -877,18 +877,19 @@ cudaError_t launch_tc(const bf16 *q, const bf16 *k, const bf16 *v, bf16 *o, cons
   a.b = b;
   a.H = H;
   a.G = G;
+  a.D = width;
   a.r = H / G;
   a.Mq = z.Mq;
   a.box = 1 << (pv.page_log2 < 7 ? pv.page_log2 : 7);
-  a.scale_log2 = 1.4426950408889634f / sqrtf((float)D);
+  a.scale_log2 = 1.4426950408889634f / sqrtf((float)width);
   a.plan = nullptr;
   a.entries = nullptr;
   a.arrivals = nullptr;
   a.part = nullptr;
   a.status = status;
   CUtensorMap mq, mk, mv;
-  if (!make_heads_map(&mq, q, b.n_tokens, H, D, a.r, a.Mq) || !make_paged_map(&mk, k, pv, G, D, a.box) ||
-      !make_paged_map(&mv, v, pv, G, D, a.box))
+  if (!make_heads_map(&mq, q, b.n_tokens, H, width, a.r, a.Mq) || !make_paged_map(&mk, k, pv, G, width, a.box) ||
+      !make_paged_map(&mv, v, pv, G, width, a.box))
     return cudaErrorInvalidValue;
   unsigned grid = (unsigned)(z.max_blocks * G);
   if (z.bytes > 0) {
@@ -910,16 +911,16 @@ cudaError_t launch_tc(const bf16 *q, const bf16 *k, const bf16 *v, bf16 *o, cons
 
 }  // namespace
 
-bool packed_tc_supported(int H, int G, int D) { return (D == 64 || D == 128) && H % G == 0 && H / G <= 128; }
+bool packed_tc_supported(int H, int G, int D) { return (D == 16 || D == 32 || D == 64 || D == 128) && H % G == 0 && H / G <= 128; }
 
 size_t packed_tc_workspace_bytes(const PackedView &b, int H, int G, int D) {
-  return packed_sizes(b, H, G, D, sm_count()).bytes;
+  return packed_sizes(b, H, G, D < 64 ? 64 : D, sm_count()).bytes;
 }
 
 cudaError_t launch_packed_tc(const bf16 *q, const bf16 *k, const bf16 *v, bf16 *o, const PagedView &pv,
                              const PackedView &b, int H, int G, int D, void *workspace, int *status, cudaStream_t st) {
-  if (D == 128) return launch_tc<128>(q, k, v, o, pv, b, H, G, workspace, status, st);
-  return launch_tc<64>(q, k, v, o, pv, b, H, G, workspace, status, st);
+  if (D == 128) return launch_tc<128>(q, k, v, o, pv, b, H, G, D, workspace, status, st);
+  return launch_tc<64>(q, k, v, o, pv, b, H, G, D, workspace, status, st);
 }
 
 }  // namespace llama

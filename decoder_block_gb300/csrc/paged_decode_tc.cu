@@ -1,6 +1,7 @@
-// One new token per sequence over cache pages, bf16, d_head 64 or 128, on
-// tcgen05 tensor cores ("Full Llama 3 transformer block", How it works: cached
-// keys 0 .. kv_len - 1; "The Evolving Transformer 04 · LLaMA", §05 GQA).
+// One new token per sequence over cache pages, bf16, on tcgen05 tensor cores ("Full
+// Llama 3 transformer block", How it works: cached keys 0 .. kv_len - 1; "The Evolving
+// Transformer 04 · LLaMA", §05 GQA).  d_head 64 or 128; 16 and 32 run as 64, their
+// tiles filled up with zeros by the copies.
 //
 // The cache is read once and that is what bounds the step; the tensor cores keep
 // the CUDA cores free enough for the loads to set the pace.  Keys are the
@@ -90,7 +91,7 @@ struct PdArgs {
   PagedView pv;
   const int *kv_lens;
   int n_seqs, max_kv_len;
-  int H, G, r, subs, box;  // subs: blocks of up to 16 heads per KV head
+  int H, G, D, r, subs, box;  // D: the heads' width (the kernel's or less); subs: blocks of up to 16 heads per KV head
   float scale_log2;
   int cluster;     // direct: CTAs of a sequence and head block
   PdPlan *plan;    // null: direct
@@ -617,7 +618,8 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
             pp[D + 1] = l;
           }
         } else if (it.slot < 0) {
-          a.o[((size_t)it.seq * a.H + it.h0 + h) * D + row] = __float2bfloat16_rn(l > 0.f ? ov[h] / l : 0.f);
+          if (row < a.D)
+            a.o[((size_t)it.seq * a.H + it.h0 + h) * a.D + row] = __float2bfloat16_rn(l > 0.f ? ov[h] / l : 0.f);
         } else {
           float *pp = a.part + ((size_t)it.slot * a.H + it.h0 + h) * (D + 2);
           pp[row] = ov[h];
@@ -638,7 +640,7 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
     const int u = blockIdx.x / a.cluster, unit = u % units, seq = u / units;
     const int g = unit / a.subs, h0 = g * a.r + (unit % a.subs) * PD_N;
     const int nh = min(PD_N, (g + 1) * a.r - h0);
-    if (*abort_flag == 0 && threadIdx.x < D) {
+    if (*abort_flag == 0 && threadIdx.x < a.D) {
       const uint32_t part = s0 + L::OFF_K;
       for (int h = rank; h < nh; h += a.cluster) {
         float mc[PD_MAX_CLUSTER], lc[PD_MAX_CLUSTER], oc[PD_MAX_CLUSTER];
@@ -663,7 +665,7 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
           l = fmaf(f, lc[c], l);
           o = fmaf(f, oc[c], o);
         }
-        a.o[((size_t)seq * a.H + h0 + h) * D + threadIdx.x] = __float2bfloat16_rn(l > 0.f ? o / l : 0.f);
+        a.o[((size_t)seq * a.H + h0 + h) * a.D + threadIdx.x] = __float2bfloat16_rn(l > 0.f ? o / l : 0.f);
       }
     }
     ptx::cluster_sync();  // no CTA leaves while others read its shared memory
@@ -679,7 +681,7 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
 template <int D>
 __global__ void __launch_bounds__(256) decode_join_kernel(const PdPlan *plan, const PdSplit *splits,
                                                           const float *__restrict__ part, bf16 *__restrict__ o,
-                                                          int H) {
+                                                          int H, int width) {
   constexpr int LANES = D / 4, GROUPS = 256 / LANES;
   __shared__ float sm[8], so[GROUPS][D], sl[GROUPS];
   grid_dependency_wait();
@@ -712,14 +714,14 @@ __global__ void __launch_bounds__(256) decode_join_kernel(const PdPlan *plan, co
   *reinterpret_cast<float4 *>(&so[grp][d]) = acc;
   if (d == 0) sl[grp] = l;
   __syncthreads();
-  if (threadIdx.x < D) {
+  if (threadIdx.x < width) {
     float x = 0.f, z = 0.f;
 #pragma unroll
     for (int g = 0; g < GROUPS; ++g) {
       x += so[g][threadIdx.x];
       z += sl[g];
     }
-    o[((size_t)s.seq * H + h) * D + threadIdx.x] = __float2bfloat16_rn(x / z);
+    o[((size_t)s.seq * H + h) * width + threadIdx.x] = __float2bfloat16_rn(x / z);
   }
 }
 
@@ -761,7 +763,8 @@ PdSizes decode_sizes(int n_seqs, int max_kv_len, int H, int G, int D, int sms) {
 
 template <int D, int RN>
 cudaError_t launch_tc(const bf16 *q, const bf16 *k, const bf16 *v, bf16 *o, const PagedView &pv, const int *kv_lens,
-                      int n_seqs, int max_kv_len, int H, int G, void *workspace, int *status, cudaStream_t st) {
+                      int n_seqs, int max_kv_len, int H, int G, int width, void *workspace, int *status,
+                      cudaStream_t st) {
   using L = PdLayout<D>;
   static PerContextOnce attr;
   cudaError_t e = attr.run([] {
@@ -778,18 +781,19 @@ cudaError_t launch_tc(const bf16 *q, const bf16 *k, const bf16 *v, bf16 *o, cons
   a.max_kv_len = max_kv_len;
   a.H = H;
   a.G = G;
+  a.D = width;
   a.r = H / G;
   a.subs = z.units / G;
   a.box = 1 << (pv.page_log2 < 7 ? pv.page_log2 : 7);
-  a.scale_log2 = 1.4426950408889634f / sqrtf((float)D);
+  a.scale_log2 = 1.4426950408889634f / sqrtf((float)width);
   a.cluster = 1;
   a.plan = nullptr;
   a.entries = nullptr;
   a.part = nullptr;
   a.status = status;
   CUtensorMap mq, mk, mv;
-  if (!make_heads_map(&mq, q, n_seqs, H, D, PD_N, 1) || !make_paged_map(&mk, k, pv, G, D, a.box) ||
-      !make_paged_map(&mv, v, pv, G, D, a.box))
+  if (!make_heads_map(&mq, q, n_seqs, H, width, PD_N, 1) || !make_paged_map(&mk, k, pv, G, width, a.box) ||
+      !make_paged_map(&mv, v, pv, G, width, a.box))
     return cudaErrorInvalidValue;
   const long long items = (long long)n_seqs * z.units;
   if (z.cluster > 0) {
@@ -827,32 +831,32 @@ cudaError_t launch_tc(const bf16 *q, const bf16 *k, const bf16 *v, bf16 *o, cons
   if (e != cudaSuccess) return e;
   count_launch();
   return launch_pdl(decode_join_kernel<D>, dim3((unsigned)(z.max_split * H)), dim3(256), 0, st,
-                    (const PdPlan *)a.plan, (const PdSplit *)splits, (const float *)a.part, o, H);
+                    (const PdPlan *)a.plan, (const PdSplit *)splits, (const float *)a.part, o, H, width);
 }
 
 template <int D>
 cudaError_t launch_by_heads(const bf16 *q, const bf16 *k, const bf16 *v, bf16 *o, const PagedView &pv,
-                            const int *kv_lens, int n_seqs, int max_kv_len, int H, int G, void *workspace, int *status,
-                            cudaStream_t st) {
+                            const int *kv_lens, int n_seqs, int max_kv_len, int H, int G, int width, void *workspace,
+                            int *status, cudaStream_t st) {
   const int r = H / G;
   auto f = r <= 2 ? launch_tc<D, 2> : r <= 4 ? launch_tc<D, 4> : r <= 8 ? launch_tc<D, 8> : launch_tc<D, 16>;
-  return f(q, k, v, o, pv, kv_lens, n_seqs, max_kv_len, H, G, workspace, status, st);
+  return f(q, k, v, o, pv, kv_lens, n_seqs, max_kv_len, H, G, width, workspace, status, st);
 }
 
 }  // namespace
 
-bool paged_decode_tc_supported(int H, int G, int D) { return (D == 64 || D == 128) && H % G == 0; }
+bool paged_decode_tc_supported(int H, int G, int D) { return (D == 16 || D == 32 || D == 64 || D == 128) && H % G == 0; }
 
 size_t paged_decode_tc_workspace_bytes(int n_seqs, int max_kv_len, int H, int G, int D) {
-  return decode_sizes(n_seqs, max_kv_len, H, G, D, sm_count()).bytes;
+  return decode_sizes(n_seqs, max_kv_len, H, G, D < 64 ? 64 : D, sm_count()).bytes;
 }
 
 cudaError_t launch_paged_decode_tc(const bf16 *q, const bf16 *k, const bf16 *v, bf16 *o, const PagedView &pv,
                                    const int *kv_lens, int n_seqs, int max_kv_len, int H, int G, int D,
                                    void *workspace, int *status, cudaStream_t st) {
   if (D == 128)
-    return launch_by_heads<128>(q, k, v, o, pv, kv_lens, n_seqs, max_kv_len, H, G, workspace, status, st);
-  return launch_by_heads<64>(q, k, v, o, pv, kv_lens, n_seqs, max_kv_len, H, G, workspace, status, st);
+    return launch_by_heads<128>(q, k, v, o, pv, kv_lens, n_seqs, max_kv_len, H, G, D, workspace, status, st);
+  return launch_by_heads<64>(q, k, v, o, pv, kv_lens, n_seqs, max_kv_len, H, G, D, workspace, status, st);
 }
 
 }  // namespace llama

@@ -29,14 +29,14 @@ cudaError_t launch_packed_simt(const T *q, const T *k, const T *v, T *o, const P
 bool make_paged_map(CUtensorMap *map, const bf16 *pool, const PagedView &pv, int G, int D, int box);
 bool make_heads_map(CUtensorMap *map, const bf16 *q, int rows, int H, int D, int box_heads, int box_rows);
 
-// Tensor-core attention of packed rows (packed_tc.cu): bf16, d_head 64 or 128, up
-// to 128 query heads per KV head.
+// Tensor-core attention of packed rows (packed_tc.cu): bf16, up to 128 query heads
+// per KV head.
 bool packed_tc_supported(int H, int G, int D);
 size_t packed_tc_workspace_bytes(const PackedView &b, int H, int G, int D);
 cudaError_t launch_packed_tc(const bf16 *q, const bf16 *k, const bf16 *v, bf16 *o, const PagedView &pv,
                              const PackedView &b, int H, int G, int D, void *workspace, int *status, cudaStream_t st);
 
-// Tensor-core decode attention (paged_decode_tc.cu): bf16, d_head 64 or 128.
+// Tensor-core decode attention (paged_decode_tc.cu): bf16.
 bool paged_decode_tc_supported(int H, int G, int D);
 size_t paged_decode_tc_workspace_bytes(int n_seqs, int max_kv_len, int H, int G, int D);
 cudaError_t launch_paged_decode_tc(const bf16 *q, const bf16 *k, const bf16 *v, bf16 *o, const PagedView &pv,
