@@ -358,6 +358,7 @@ def llama_op_attention_decode_noalloc(q, kv: llama_kv_cache, o, B, start_pos, H,
 
 
 LLAMA_PACKED_MAX_SEQS = 4096
+LLAMA_PACKED_MAX_KV = 8388480
 
 
 def make_paged_kv_cache(k, v, page_table) -> llama_paged_kv_cache:

@@ -6,14 +6,14 @@
 // in one pass over the keys with the running maximum m and sum in fp32.
 //
 // A work item is (sequence, KV head, block of 2 * Mq query positions, range of
-// 128-key tiles).  Its 128-row query tile t holds the r heads of the group at Mq
-// = 128 / r positions, row i * r + hh: one TMA box, so that every K/V tile in
-// shared memory serves the whole group.  Keys and values arrive page by page:
-// one box per page (at most 128 rows) and 64 columns, in the 128-byte swizzle
-// the MMAs read, so a tile is the same whatever the page size.  Rows behind the
-// sequence's last key may hold anything: their scores are replaced, not added
-// to, and the V rows are cleared in shared memory before the product reads them
-// (0 * NaN is not 0).
+// 128-key tiles).  Its 128-row query tile t holds the rb heads of the group (all r, or
+// 128 of more) at Mq = 128 / rb positions, row i * rb + hh: one TMA box, so that every
+// K/V tile in shared memory serves the whole group.  Keys and values arrive page by
+// page: one box per page (at most 128 rows) and 64 columns, in the 128-byte swizzle
+// the MMAs read, so a tile is the same whatever the page size (at S = 8192 pages of 16
+// and of 256 take the same time).  Rows behind the sequence's last key may hold
+// anything: their scores are replaced, not added to, and the V rows are cleared in
+// shared memory before the product reads them (0 * NaN is not 0).
 //   warp 0      takes items, loads Q, then K and V tiles into two-stage rings;
 //               each lane issues one page's box and holds the next tile's id
 //   warp 1      one thread issues S_t = Q_t K^T and O_t += P_t V (fp32 in tensor
@@ -25,9 +25,8 @@
 //   * planned: a one-CTA kernel lists the items longest first and zeroes a
 //     counter that persistent CTAs take them from.  When the longest items would
 //     outlast the rest (few query rows against many keys) it splits their keys
-//     into pieces; a piece leaves fp32 (O, m, l) per row in the workspace, and
-//     for every 32 rows the last piece's warp joins them in piece order, so the
-//     result does not depend on timing.
+//     into pieces; a piece leaves fp32 (O, m, l) per row in the workspace, and a
+//     third kernel joins them in piece order, so results do not depend on timing.
 // Every wait is bounded; a kernel that gives up records LLAMA_ERR_DEVICE_TIMEOUT
 // once its copies and MMAs in flight are done.
 #include <cudaTypedefs.h>
@@ -44,6 +43,7 @@ constexpr int PT_KEYS = 128;    // keys of a tile
 constexpr int PT_STAGES = 2;
 constexpr float PT_RESCALE = 8.0f;  // log2 units: the running maximum is raised when it grows by > 2^8
 constexpr int PT_MIN_PIECE = 4;     // key tiles of a split item's piece, at least
+constexpr int PT_SPLIT_COST = 4;    // what a split costs, in key tiles of time
 constexpr int PT_PLAN_THREADS = 1024;
 constexpr int PT_BUCKETS = 1024;    // item lengths the planner tells apart
 
@@ -66,34 +66,42 @@ struct PtLayout {
 
 // A work item as the producer hands it to the other roles.
 struct PtItem {
-  int seq, g, q0;     // sequence (-1: no more items), KV head, first query position of the block
+  int seq, q0;        // sequence (-1: no more items), first query position of the block
+  int g, h0, nh;      // KV head, first query head and number of them
+  int unit;           // KV head and block of query heads
   int first, count, kv_len;
   int j0, j1;         // key tiles
-  int slot, pieces, piece, entry;  // partial slot of piece 0 (-1: not split), number, index, split block
+  int slot;           // a piece of a split item: where its partial goes (-1: not split)
 };
 static_assert(sizeof(PtItem) <= 64, "PtItem fits its slot");
 
-// Planner's output at the start of the workspace.
-struct PtEntry {
-  int seq, blk, j0, j1;
-  int slot, pieces, piece, entry;
-};
+// Planner's output, in the workspace.
 struct PtPlan {
-  int n_entries;  // items are entries x G
+  int n_entries;  // items are entries x units
   int next;       // item counter
-  int pad[2];
+  int n_split, pad;
+};
+struct PtEntry {
+  int seq, blk;
+  int range;  // first key tile | last + 1 << 16
+  int slot;
+};
+static_assert(LLAMA_PACKED_MAX_KV / PT_KEYS <= 65535, "key tiles fit 16 bits");
+struct PtSplit {  // a split block: its pieces' partials are slots slot .. slot + n - 1
+  int seq, blk, slot, n;
 };
 
 struct PtArgs {
   bf16 *o;
   PagedView pv;
   PackedView b;
-  int H, G, D, r, Mq, box;  // D: the heads' width (the kernel's or less); box: rows of a page's TMA box
+  int H, G, D, r;        // D: the heads' width (the kernel's or less); r: heads of a group
+  int rb, subs;          // heads of a work item (at most 128), items of a group
+  int Mq, box;           // query positions of a tile; rows of a page's TMA box
   float scale_log2;
   PtPlan *plan;          // null: direct
   PtEntry *entries;
-  int *arrivals;         // [split block][G][2][4]
-  float *part;           // [slot][G][2][4][D + 2][32]
+  float *part;           // [slot][unit][2 tiles][4 warps][D + 2][32 rows]
   int *status;
 };
 
@@ -114,55 +122,39 @@ __device__ __forceinline__ int item_end(const PtItem &it, int Mq, int t) {
 }
 
 // ------------------------------------------------------------------ plan ---
-// Inclusive sum over the CTA's threads.
-__device__ __forceinline__ int cta_scan(int v, int *warp_sums) {
-  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += x;
-  }
-  if (lane == 31) warp_sums[warp] = v;
-  __syncthreads();
-  if (warp == 0) {
-    int s = warp_sums[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += x;
-    }
-    warp_sums[lane] = s;
-  }
-  __syncthreads();
-  const int out = v + (warp > 0 ? warp_sums[warp - 1] : 0);
-  __syncthreads();
-  return out;
-}
+// A block's sequence and key tiles are looked up twice (to count, to place); a thread
+// keeps those of its first blocks, so a batch of up to 4096 blocks is looked up once.
+constexpr int PT_KEEP = 4;
 
-__global__ void __launch_bounds__(PT_PLAN_THREADS) packed_plan_kernel(PagedView pv, PackedView b, int G, int Mq,
-                                                                      int sms, int max_entries, int max_split,
-                                                                      PtPlan *plan, PtEntry *entries, int *arrivals,
-                                                                      int *status) {
+__global__ void __launch_bounds__(PT_PLAN_THREADS) packed_plan_kernel(PagedView pv, PackedView b, int units, int Mq,
+                                                                      int sms, int max_entries, PtPlan *plan,
+                                                                      PtEntry *entries, PtSplit *splits, int *status) {
   __shared__ int first_blk[LLAMA_PACKED_MAX_SEQS + 1];  // blocks before sequence i
+  __shared__ int2 seqs[PT_PLAN_THREADS];                // count and kv_len of the first sequences
   __shared__ int hist[PT_BUCKETS];
   __shared__ int warp_sums[32];
   __shared__ unsigned long long work_sum;
   __shared__ int n_split, n_slots;
   const int tid = threadIdx.x;
   allow_dependents_launch();
-  grid_dependency_wait();
+  hist[tid] = 0;
   if (tid == 0) {
     work_sum = 0;
     n_split = n_slots = 0;
+    first_blk[0] = 0;
   }
-  for (int i = tid; i < PT_BUCKETS; i += PT_PLAN_THREADS) hist[i] = 0;
-  for (int i = tid; i < max_split * G * 8; i += PT_PLAN_THREADS) arrivals[i] = 0;
-  for (int i = tid; i < b.n_seqs; i += PT_PLAN_THREADS) check_seq(b, pv, i, status);
+  grid_dependency_wait();
   // blocks of every sequence, as sums: 1024 sequences a round
   int base = 0;
   for (int i0 = 0; i0 < b.n_seqs; i0 += PT_PLAN_THREADS) {
     const int i = i0 + tid;
-    const int n = i < b.n_seqs ? (seq_span(b, pv, i).count + 2 * Mq - 1) / (2 * Mq) : 0;
+    int n = 0;
+    if (i < b.n_seqs) {
+      check_seq(b, pv, i, status);
+      const SeqSpan s = seq_span(b, pv, i);
+      n = (s.count + 2 * Mq - 1) / (2 * Mq);
+      if (i0 == 0) seqs[tid] = make_int2(s.count, s.kv_len);
+    }
     const int end = base + cta_scan(n, warp_sums);
     if (i < b.n_seqs) first_blk[i + 1] = end;
     if (tid == PT_PLAN_THREADS - 1) warp_sums[0] = end;
@@ -170,74 +162,96 @@ __global__ void __launch_bounds__(PT_PLAN_THREADS) packed_plan_kernel(PagedView 
     base = warp_sums[0];
     __syncthreads();
   }
-  if (tid == 0) first_blk[0] = 0;
-  __syncthreads();
   const int n_blk = base;
-  // sequence of block u: the last i with first_blk[i] <= u
-  auto seq_of = [&](int u) {
+  // sequence (the last i with first_blk[i] <= u), block and key tiles of block u
+  auto look_up = [&](int u, int &seq, int &blk) {
     int lo = 0, hi = b.n_seqs;
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
       if (first_blk[mid] <= u) lo = mid;
       else hi = mid;
     }
-    return lo;
+    seq = lo;
+    blk = u - first_blk[lo];
+    int2 s;
+    if (lo < PT_PLAN_THREADS) {
+      s = seqs[lo];
+    } else {
+      const SeqSpan x = seq_span(b, pv, lo);
+      s = make_int2(x.count, x.kv_len);
+    }
+    return tiles_of(s.y - s.x, blk * 2 * Mq, min(s.x, (blk + 1) * 2 * Mq));
   };
-  auto tiles = [&](int u, int &seq, int &blk) {
-    seq = seq_of(u);
-    blk = u - first_blk[seq];
-    const SeqSpan s = seq_span(b, pv, seq);
-    return tiles_of(s.kv_len - s.count, blk * 2 * Mq, min(s.count, (blk + 1) * 2 * Mq));
-  };
+  int seq[PT_KEEP], blk[PT_KEEP], len[PT_KEEP];
   unsigned long long mine = 0;
-  for (int u = tid; u < n_blk; u += PT_PLAN_THREADS) {
-    int seq, blk;
-    mine += (unsigned)tiles(u, seq, blk);
+#pragma unroll
+  for (int k = 0; k < PT_KEEP; ++k) {
+    const int u = k * PT_PLAN_THREADS + tid;
+    len[k] = u < n_blk ? look_up(u, seq[k], blk[k]) : 0;
+    mine += (unsigned)len[k];
   }
-  atomicAdd(&work_sum, mine);
-  __syncthreads();
-  // A CTA's even share of the key tiles; an item longer than that is what the
-  // others would wait for, so it is cut into pieces of at most that length.  The
-  // pieces of all split items then number less than 2 * sms / G (each has more
-  // than half a share), which sizes the workspace.
-  const unsigned long long share = (work_sum * G + sms - 1) / sms;
-  const int cap = (int)(share > PT_MIN_PIECE ? share : PT_MIN_PIECE);
-  // longest first: counting sort by piece length
-  auto pieces_of = [&](int n) { return n > cap ? (n + cap - 1) / cap : 1; };
-  auto bucket = [&](int len) { return PT_BUCKETS - 1 - min(len, PT_BUCKETS - 1); };
-  for (int u = tid; u < n_blk; u += PT_PLAN_THREADS) {
-    int seq, blk;
-    const int n = tiles(u, seq, blk), np = pieces_of(n);
-    atomicAdd(&hist[bucket((n + np - 1) / np)], np);
+  for (int u = PT_KEEP * PT_PLAN_THREADS + tid; u < n_blk; u += PT_PLAN_THREADS) {
+    int s, x;
+    mine += (unsigned)look_up(u, s, x);
   }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  if ((tid & 31) == 0 && mine != 0) atomicAdd(&work_sum, mine);
   __syncthreads();
-  {
-    const int v = hist[tid];
-    const int end = cta_scan(v, warp_sums);
-    hist[tid] = end - v;
-    if (tid == PT_PLAN_THREADS - 1) {
-      plan->n_entries = min(end, max_entries);
-      plan->next = 0;
+  // An SM's even share of the key tiles.  An item that is longer by more than a split
+  // costs is what the others would wait for: it is cut into pieces of at most a share.
+  // Such pieces number less than 2 * sms / units, which sizes the workspace.
+  const unsigned long long even = (work_sum * units + sms - 1) / sms;
+  const int share = (int)(even > PT_MIN_PIECE ? even : PT_MIN_PIECE);
+  auto pieces_of = [&](int n) { return n > share + PT_SPLIT_COST ? (n + share - 1) / share : 1; };
+  // longest piece first: counting sort
+  auto bucket = [&](int n, int pieces) { return PT_BUCKETS - 1 - min((n + pieces - 1) / pieces, PT_BUCKETS - 1); };
+#pragma unroll
+  for (int k = 0; k < PT_KEEP; ++k)
+    if (k * PT_PLAN_THREADS + tid < n_blk) {
+      const int p = pieces_of(len[k]);
+      atomicAdd(&hist[bucket(len[k], p)], p);
     }
+  for (int u = PT_KEEP * PT_PLAN_THREADS + tid; u < n_blk; u += PT_PLAN_THREADS) {
+    int s, x;
+    const int n = look_up(u, s, x), p = pieces_of(n);
+    atomicAdd(&hist[bucket(n, p)], p);
   }
   __syncthreads();
-  for (int u = tid; u < n_blk; u += PT_PLAN_THREADS) {
+  const int v = hist[tid], end = cta_scan(v, warp_sums);
+  hist[tid] = end - v;
+  __syncthreads();
+  auto place = [&](int s, int x, int n) {
     PtEntry e;
-    const int n = tiles(u, e.seq, e.blk);
-    e.pieces = pieces_of(n);
-    e.slot = e.entry = -1;
-    const int each = (n + e.pieces - 1) / e.pieces;
-    if (e.pieces > 1) {
-      e.entry = atomicAdd(&n_split, 1);
-      e.slot = atomicAdd(&n_slots, e.pieces);
+    e.seq = s;
+    e.blk = x;
+    const int p = pieces_of(n), each = (n + p - 1) / p;
+    int slot = -1;
+    if (p > 1) {
+      slot = atomicAdd(&n_slots, p);
+      splits[atomicAdd(&n_split, 1)] = PtSplit{s, x, slot, p};
     }
-    const int at = atomicAdd(&hist[bucket(each)], e.pieces);
-    for (e.piece = 0; e.piece < e.pieces; ++e.piece) {
-      e.j0 = min(n, e.piece * each);
-      e.j1 = min(n, e.j0 + each);
-      if (at + e.piece < max_entries) entries[at + e.piece] = e;
+    const int at = atomicAdd(&hist[bucket(n, p)], p);
+    for (int i = 0; i < p; ++i) {
+      e.range = min(n, i * each) | min(n, (i + 1) * each) << 16;
+      e.slot = slot < 0 ? -1 : slot + i;
+      if (at + i < max_entries) entries[at + i] = e;
     }
+  };
+#pragma unroll
+  for (int k = 0; k < PT_KEEP; ++k)
+    if (k * PT_PLAN_THREADS + tid < n_blk) place(seq[k], blk[k], len[k]);
+  for (int u = PT_KEEP * PT_PLAN_THREADS + tid; u < n_blk; u += PT_PLAN_THREADS) {
+    int s, x;
+    const int n = look_up(u, s, x);
+    place(s, x, n);
   }
+  if (tid == PT_PLAN_THREADS - 1) {
+    plan->n_entries = min(end, max_entries);
+    plan->next = 0;
+  }
+  __syncthreads();
+  if (tid == 0) plan->n_split = n_split;
 }
 
 // ------------------------------------------------------------- attention ---
@@ -291,9 +305,9 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
     *abort_flag = 0;
     ptx::fence_mbar_init();
   }
-  // Query rows behind r * Mq are never loaded: zero them.
-  if (warp >= 2 && a.r * a.Mq < 128) {
-    const int first = a.r * a.Mq;
+  // Query rows behind rb * Mq are never loaded: zero them.
+  if (warp >= 2 && a.rb * a.Mq < 128) {
+    const int first = a.rb * a.Mq;
     for (int t = 0; t < 2; ++t)
       for (int at = 0; at < ATOMS; ++at) {
         uint4 *p = reinterpret_cast<uint4 *>(smem + L::OFF_Q + t * L::TILE + at * L::ATOM + first * 128);
@@ -319,7 +333,8 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
       ptx::tma_prefetch_desc(&tmK);
       ptx::tma_prefetch_desc(&tmV);
     }
-    const int n_items = a.plan != nullptr ? *reinterpret_cast<volatile int *>(&a.plan->n_entries) * a.G : 0;
+    const int units = a.G * a.subs;
+    const int n_items = a.plan != nullptr ? *reinterpret_cast<volatile int *>(&a.plan->n_entries) * units : 0;
     // The CTA's next item (all lanes); seq = -1 when there is none.
     auto fetch = [&](int k) {
       PtItem it;
@@ -329,20 +344,16 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
         if (lane == 0) u = atomicAdd(&a.plan->next, 1);
         u = __shfl_sync(0xffffffffu, u, 0);
         if (u >= n_items) return it;
-        const int4 *e = reinterpret_cast<const int4 *>(a.entries + u / a.G);
-        const int4 x = __ldcg(e), y = __ldcg(e + 1);
-        it.seq = x.x;
-        it.g = u % a.G;
-        it.q0 = x.y * 2 * a.Mq;
-        it.j0 = x.z;
-        it.j1 = x.w;
-        it.slot = y.x;
-        it.pieces = y.y;
-        it.piece = y.z;
-        it.entry = y.w;
+        const int4 e = __ldcg(reinterpret_cast<const int4 *>(a.entries + u / units));
+        it.seq = e.x;
+        it.unit = u % units;
+        it.q0 = e.y * 2 * a.Mq;
+        it.j0 = e.z & 0xffff;
+        it.j1 = (unsigned)e.z >> 16;
+        it.slot = e.w;
       } else {
         if (k > 0) return it;
-        const int want = blockIdx.x / a.G;
+        const int want = blockIdx.x / units;
         int base = 0;
         for (int i0 = 0; i0 < a.b.n_seqs; i0 += 32) {
           const int i = i0 + lane;
@@ -365,11 +376,12 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
           if (base > want) break;
         }
         if (it.seq < 0) return it;
-        it.g = blockIdx.x % a.G;
-        it.slot = it.entry = -1;
-        it.pieces = 1;
-        it.piece = 0;
+        it.unit = blockIdx.x % units;
+        it.slot = -1;
       }
+      it.g = it.unit / a.subs;
+      it.h0 = it.g * a.r + it.unit % a.subs * a.rb;
+      it.nh = min(a.rb, (it.g + 1) * a.r - it.h0);
       const SeqSpan s = seq_span(a.b, a.pv, it.seq);
       it.first = s.first;
       it.count = s.count;
@@ -410,10 +422,10 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
       }
       const int n_t = it.q0 + a.Mq < it.count ? 2 : 1;  // query tiles that hold rows
       if (lane == 0) {
-        ptx::mbar_arrive_expect_tx(q_full, n_t * ATOMS * a.r * a.Mq * 128u);
+        ptx::mbar_arrive_expect_tx(q_full, n_t * ATOMS * a.rb * a.Mq * 128u);
         for (int t = 0; t < n_t; ++t)
           for (int at = 0; at < ATOMS; ++at)
-            ptx::tma_load_3d(s0 + L::OFF_Q + t * L::TILE + at * L::ATOM, &tmQ, at * 64, it.g * a.r,
+            ptx::tma_load_3d(s0 + L::OFF_Q + t * L::TILE + at * L::ATOM, &tmQ, at * 64, it.h0,
                              it.first + it.q0 + t * a.Mq, q_full);
       }
       ++items;
@@ -551,7 +563,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
     const int t = (warp - 2) / 4;
     const int qq = warp & 3;
     const int row = qq * 32 + lane;
-    const int hh = row % a.r, i = row / a.r;
+    const int hh = row % a.rb, i = row / a.rb;
     const uint32_t lane_base = tmem + ((uint32_t)(qq * 32) << 16);
     const uint32_t s_col = lane_base + t * 128;
     const uint32_t o_col = lane_base + 256 + t * D;
@@ -571,7 +583,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
       const int my_end = t == 0 ? e0 : e1;
       const int n_kv = max(0, my_end - it.j0);
       const int rel = it.q0 + t * a.Mq + i;
-      const bool valid = i < a.Mq && rel < it.count;
+      const bool valid = i < a.Mq && rel < it.count && hh < it.nh;
       const int pos = shift + min(rel, it.count - 1);
       // finite: rows that see no key of a tile keep weights of 0 instead of NaN
       float m_run = -FLT_MAX;
@@ -698,7 +710,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
       float la, lb;
       ptx::f2unpack(l2, la, lb);
       float l = la + lb;
-      bf16 *dst = a.o + ((size_t)(it.first + rel) * a.H + it.g * a.r + hh) * a.D;
+      bf16 *dst = a.o + ((size_t)(it.first + rel) * a.H + it.h0 + hh) * a.D;
       if (it.slot < 0) {
         const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll
@@ -720,10 +732,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
         }
       } else if (it.q0 + t * a.Mq < it.count) {
         // a piece: the rows' partial (O, m, l), one column of 32 rows after another
-        constexpr int ROWS = (D + 2) * 32;
-        const size_t unit = ((size_t)it.g * 2 + t) * 4 + qq;  // 32 rows of the block
-        const size_t per_slot = (size_t)a.G * 8;
-        float *mine = a.part + ((size_t)(it.slot + it.piece) * per_slot + unit) * ROWS + lane;
+        float *mine = a.part + ((((size_t)it.slot * (a.G * a.subs) + it.unit) * 2 + t) * 4 + qq) * ((D + 2) * 32) + lane;
 #pragma unroll
         for (int c = 0; c < D; c += 16) {
           float ov[16];
@@ -734,44 +743,10 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
             for (int e = 0; e < 16; ++e) ov[e] = 0.f;
           }
 #pragma unroll
-          for (int e = 0; e < 16; ++e) __stcg(mine + (c + e) * 32, ov[e]);
+          for (int e = 0; e < 16; ++e) mine[(c + e) * 32] = ov[e];
         }
-        __stcg(mine + D * 32, m_run);
-        __stcg(mine + (D + 1) * 32, l);
-        __threadfence();
-        __syncwarp();
-        int before = 0;
-        if (lane == 0) before = atomicAdd(a.arrivals + (size_t)it.entry * per_slot + unit, 1);
-        before = __shfl_sync(0xffffffffu, before, 0);
-        if (before == it.pieces - 1) {  // the last piece's warp joins them, in piece order
-          __threadfence();
-          const float *p0 = a.part + ((size_t)it.slot * per_slot + unit) * ROWS + lane;
-          const size_t step = per_slot * ROWS;
-          float m = -FLT_MAX;
-          for (int s = 0; s < it.pieces; ++s) m = fmaxf(m, __ldcg(p0 + s * step + D * 32));
-          l = 0.f;
-          for (int s = 0; s < it.pieces; ++s)
-            l = fmaf(ptx::ex2_approx(__ldcg(p0 + s * step + D * 32) - m), __ldcg(p0 + s * step + (D + 1) * 32), l);
-          const float inv = l > 0.f ? 1.f / l : 0.f;
-#pragma unroll 1
-          for (int c = 0; c < D; c += 16) {
-            float ov[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) ov[e] = 0.f;
-            for (int s = 0; s < it.pieces; ++s) {
-              const float f = ptx::ex2_approx(__ldcg(p0 + s * step + D * 32) - m) * inv;
-#pragma unroll
-              for (int e = 0; e < 16; ++e) ov[e] = fmaf(f, __ldcg(p0 + s * step + (c + e) * 32), ov[e]);
-            }
-            if (valid && c < a.D) {
-              uint32_t w[8];
-#pragma unroll
-              for (int e = 0; e < 8; ++e) w[e] = pt_pack2(ov[2 * e], ov[2 * e + 1]);
-              *reinterpret_cast<uint4 *>(dst + c) = make_uint4(w[0], w[1], w[2], w[3]);
-              *reinterpret_cast<uint4 *>(dst + c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
-            }
-          }
-        }
+        mine[D * 32] = m_run;
+        mine[(D + 1) * 32] = l;
       }
       // the next item's first PV product overwrites O only after this warp's next P
       ptx::tc_fence_before();
@@ -785,6 +760,47 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, L::TMEM_COLS);
   }
+}
+
+// Joins the pieces of split items, o = sum 2^(m_p - M) O_p / sum 2^(m_p - M) l_p in
+// piece order.  A CTA takes 32 rows of one block and unit; a warp 16 columns of them.
+template <int D>
+__global__ void __launch_bounds__(D * 2) packed_join_kernel(const __grid_constant__ PtArgs a, const PtSplit *splits) {
+  grid_dependency_wait();
+  const int units = a.G * a.subs;
+  const int qq = blockIdx.x % 4, t = blockIdx.x / 4 % 2, unit = blockIdx.x / 8 % units, k = blockIdx.x / 8 / units;
+  if (k >= *reinterpret_cast<volatile int *>(&a.plan->n_split)) return;
+  const PtSplit s = splits[k];
+  const int lane = threadIdx.x & 31, c0 = threadIdx.x / 32 * 16;
+  const int row = qq * 32 + lane, hh = row % a.rb, i = row / a.rb;
+  const SeqSpan q = seq_span(a.b, a.pv, s.seq);
+  const int rel = s.blk * 2 * a.Mq + t * a.Mq + i;
+  const int g = unit / a.subs, h = g * a.r + unit % a.subs * a.rb + hh;
+  if (s.blk * 2 * a.Mq + t * a.Mq >= q.count) return;  // no rows, nothing was written
+  const float *p = a.part + ((((size_t)s.slot * units + unit) * 2 + t) * 4 + qq) * ((D + 2) * 32) + lane;
+  const size_t step = (size_t)units * 8 * (D + 2) * 32;
+  float m = -FLT_MAX;
+#pragma unroll 8
+  for (int x = 0; x < s.n; ++x) m = fmaxf(m, p[x * step + D * 32]);
+  float l = 0.f, o[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) o[e] = 0.f;
+#pragma unroll 2
+  for (int x = 0; x < s.n; ++x) {
+    const float *px = p + x * step;
+    const float f = ptx::ex2_approx(px[D * 32] - m);
+    l = fmaf(f, px[(D + 1) * 32], l);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) o[e] = fmaf(f, px[(c0 + e) * 32], o[e]);
+  }
+  if (i >= a.Mq || rel >= q.count || h >= (g + 1) * a.r || c0 >= a.D) return;
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  uint32_t w[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) w[e] = pt_pack2(o[2 * e] * inv, o[2 * e + 1] * inv);
+  uint4 *dst = reinterpret_cast<uint4 *>(a.o + ((size_t)(q.first + rel) * a.H + h) * a.D + c0);
+  dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+  dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -835,28 +851,32 @@ namespace {
 
 // Sizes of one call: items, and the workspace they need (0 bytes: direct).
 struct PtSizes {
-  int Mq = 0;
-  long long max_blocks = 0;   // (sequence, block) pairs, at most
+  int rb = 0, subs = 0, units = 0, Mq = 0;
+  long long max_blocks = 0;  // (sequence, block) pairs, at most
   int max_split = 0, max_slots = 0;
   long long max_entries = 0;
-  size_t off_entries = 0, off_arrivals = 0, off_part = 0, bytes = 0;
+  size_t off_entries = 0, off_splits = 0, off_part = 0, bytes = 0;
 };
 
 PtSizes packed_sizes(const PackedView &b, int H, int G, int D, int sms) {
   PtSizes z;
-  z.Mq = 128 / (H / G);
+  const int r = H / G;
+  z.rb = r < 128 ? r : 128;
+  z.subs = (r + z.rb - 1) / z.rb;
+  z.units = G * z.subs;
+  z.Mq = 128 / z.rb;
   z.max_blocks = (long long)b.n_tokens / (2 * z.Mq) + (b.n_seqs < b.n_tokens ? b.n_seqs : b.n_tokens);
   // Direct: no more than one item per SM and at most 8 key tiles each, where a
   // split would not pay for the planning kernel in front.
-  if (z.max_blocks * G <= sms && b.max_kv_len <= 8 * PT_KEYS) return z;
-  z.max_slots = (2 * sms + G - 1) / G + 1;
-  z.max_split = z.max_slots / 2 + 1;
+  if (z.max_blocks * z.units <= sms && b.max_kv_len <= 8 * PT_KEYS) return z;
+  z.max_slots = 2 * ((sms + z.units - 1) / z.units) + 2;
+  z.max_split = z.max_slots / 2;
   z.max_entries = z.max_blocks + z.max_slots;
   z.off_entries = sizeof(PtPlan);
-  z.off_arrivals = z.off_entries + (size_t)z.max_entries * sizeof(PtEntry);
-  z.off_part = z.off_arrivals + (size_t)z.max_split * G * 8 * sizeof(int);
+  z.off_splits = z.off_entries + (size_t)z.max_entries * sizeof(PtEntry);
+  z.off_part = z.off_splits + (size_t)z.max_split * sizeof(PtSplit);
   z.off_part = (z.off_part + 127) / 128 * 128;
-  z.bytes = z.off_part + (size_t)z.max_slots * G * 8 * (D + 2) * 32 * sizeof(float);
+  z.bytes = z.off_part + (size_t)z.max_slots * z.units * 8 * (D + 2) * 32 * sizeof(float);
   return z;
 }
 
@@ -879,39 +899,44 @@ cudaError_t launch_tc(const bf16 *q, const bf16 *k, const bf16 *v, bf16 *o, cons
   a.G = G;
   a.D = width;
   a.r = H / G;
+  a.rb = z.rb;
+  a.subs = z.subs;
   a.Mq = z.Mq;
   a.box = 1 << (pv.page_log2 < 7 ? pv.page_log2 : 7);
   a.scale_log2 = 1.4426950408889634f / sqrtf((float)width);
   a.plan = nullptr;
   a.entries = nullptr;
-  a.arrivals = nullptr;
   a.part = nullptr;
   a.status = status;
   CUtensorMap mq, mk, mv;
-  if (!make_heads_map(&mq, q, b.n_tokens, H, width, a.r, a.Mq) || !make_paged_map(&mk, k, pv, G, width, a.box) ||
+  if (!make_heads_map(&mq, q, b.n_tokens, H, width, a.rb, a.Mq) || !make_paged_map(&mk, k, pv, G, width, a.box) ||
       !make_paged_map(&mv, v, pv, G, width, a.box))
     return cudaErrorInvalidValue;
-  unsigned grid = (unsigned)(z.max_blocks * G);
-  if (z.bytes > 0) {
-    char *w = reinterpret_cast<char *>(workspace);
-    a.plan = reinterpret_cast<PtPlan *>(w);
-    a.entries = reinterpret_cast<PtEntry *>(w + z.off_entries);
-    a.arrivals = reinterpret_cast<int *>(w + z.off_arrivals);
-    a.part = reinterpret_cast<float *>(w + z.off_part);
+  if (z.bytes == 0) {
     count_launch();
-    e = launch_pdl(packed_plan_kernel, dim3(1), dim3(PT_PLAN_THREADS), 0, st, pv, b, G, a.Mq, sms, (int)z.max_entries,
-                   z.max_split, a.plan, a.entries, a.arrivals, status);
-    if (e != cudaSuccess) return e;
-    const long long items = z.max_entries * G;
-    grid = (unsigned)(items < sms ? items : sms);
+    return launch_pdl(packed_tc_kernel<D>, dim3((unsigned)(z.max_blocks * z.units)), dim3(PT_THREADS), L::BYTES, st, mq,
+                      mk, mv, a);
   }
+  char *w = reinterpret_cast<char *>(workspace);
+  a.plan = reinterpret_cast<PtPlan *>(w);
+  a.entries = reinterpret_cast<PtEntry *>(w + z.off_entries);
+  PtSplit *splits = reinterpret_cast<PtSplit *>(w + z.off_splits);
+  a.part = reinterpret_cast<float *>(w + z.off_part);
   count_launch();
-  return launch_pdl(packed_tc_kernel<D>, dim3(grid), dim3(PT_THREADS), L::BYTES, st, mq, mk, mv, a);
+  e = launch_pdl(packed_plan_kernel, dim3(1), dim3(PT_PLAN_THREADS), 0, st, pv, b, z.units, a.Mq, sms,
+                 (int)z.max_entries, a.plan, a.entries, splits, status);
+  if (e != cudaSuccess) return e;
+  const long long items = z.max_entries * z.units;
+  count_launch();
+  e = launch_pdl(packed_tc_kernel<D>, dim3((unsigned)(items < sms ? items : sms)), dim3(PT_THREADS), L::BYTES, st, mq,
+                 mk, mv, a);
+  if (e != cudaSuccess) return e;
+  count_launch();
+  return launch_pdl(packed_join_kernel<D>, dim3((unsigned)(z.max_split * z.units * 8)), dim3(D * 2), 0, st, a,
+                    (const PtSplit *)splits);
 }
 
 }  // namespace
-
-bool packed_tc_supported(int H, int G, int D) { return (D == 16 || D == 32 || D == 64 || D == 128) && H % G == 0 && H / G <= 128; }
 
 size_t packed_tc_workspace_bytes(const PackedView &b, int H, int G, int D) {
   return packed_sizes(b, H, G, D < 64 ? 64 : D, sm_count()).bytes;

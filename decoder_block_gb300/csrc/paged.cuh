@@ -73,4 +73,29 @@ __device__ __forceinline__ int find_seq(const PackedView &b, int t) {
   return (a >= 0 && a <= t && t < e && e <= b.n_tokens) ? lo : -1;
 }
 
+// Inclusive sum over the threads of a CTA of 1024; warp_sums: 32 shared ints.
+__device__ __forceinline__ int cta_scan(int v, int *warp_sums) {
+  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += x;
+  }
+  if (lane == 31) warp_sums[warp] = v;
+  __syncthreads();
+  if (warp == 0) {
+    int s = warp_sums[lane];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, s, o);
+      if (lane >= o) s += x;
+    }
+    warp_sums[lane] = s;
+  }
+  __syncthreads();
+  const int out = v + (warp > 0 ? warp_sums[warp - 1] : 0);
+  __syncthreads();
+  return out;
+}
+
 }  // namespace llama

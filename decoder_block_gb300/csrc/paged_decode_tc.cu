@@ -101,47 +101,27 @@ struct PdArgs {
 };
 
 // ------------------------------------------------------------------ plan ---
-__device__ __forceinline__ int cta_scan(int v, int *warp_sums) {
-  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += x;
-  }
-  if (lane == 31) warp_sums[warp] = v;
-  __syncthreads();
-  if (warp == 0) {
-    int s = warp_sums[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += x;
-    }
-    warp_sums[lane] = s;
-  }
-  __syncthreads();
-  const int out = v + (warp > 0 ? warp_sums[warp - 1] : 0);
-  __syncthreads();
-  return out;
-}
-
 __global__ void __launch_bounds__(PD_PLAN_THREADS) decode_plan_kernel(PagedView pv, const int *kv_lens, int n_seqs,
                                                                       int max_kv_len, int units, int sms,
                                                                       int max_entries, PdPlan *plan, PdEntry *entries,
                                                                       PdSplit *splits, int *status) {
   __shared__ int first[LLAMA_PACKED_MAX_SEQS + 1];  // chunks before sequence i
+  __shared__ int s_slot[LLAMA_PACKED_MAX_SEQS];     // first slot (-1: one chunk)
+  __shared__ unsigned short s_tiles[LLAMA_PACKED_MAX_SEQS];
+  static_assert(LLAMA_PACKED_MAX_KV / PD_KEYS <= 65535, "key tiles fit 16 bits");
   __shared__ int warp_sums[32];
   __shared__ unsigned long long total;
   __shared__ int n_split, n_slots;
   constexpr int PER = LLAMA_PACKED_MAX_SEQS / PD_PLAN_THREADS;
   const int tid = threadIdx.x;
   allow_dependents_launch();
-  grid_dependency_wait();
   if (tid == 0) {
     total = 0;
     n_split = n_slots = 0;
+    first[0] = 0;
   }
   __syncthreads();
+  grid_dependency_wait();
   int tiles[PER];
   unsigned long long mine = 0;
 #pragma unroll
@@ -155,7 +135,9 @@ __global__ void __launch_bounds__(PD_PLAN_THREADS) decode_plan_kernel(PagedView 
       mine += (unsigned)tiles[k];
     }
   }
-  atomicAdd(&total, mine);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  if ((tid & 31) == 0 && mine != 0) atomicAdd(&total, mine);
   __syncthreads();
   // Chunks of equal size, PD_ROUNDS per SM: a CTA that streams faster takes more of
   // them, and the last ones to finish are short.  Chunks of split sequences then
@@ -165,50 +147,35 @@ __global__ void __launch_bounds__(PD_PLAN_THREADS) decode_plan_kernel(PagedView 
   int base = 0;
 #pragma unroll
   for (int k = 0; k < PER; ++k) {
-    const int i = k * PD_PLAN_THREADS + tid;
     if (k * PD_PLAN_THREADS >= n_seqs) break;
+    const int i = k * PD_PLAN_THREADS + tid;
     const int n = i < n_seqs ? max(1, (tiles[k] + chunk - 1) / chunk) : 0;
     const int end = base + cta_scan(n, warp_sums);
-    if (i < n_seqs) first[i + 1] = end;
+    if (i < n_seqs) {
+      first[i + 1] = end;
+      int slot = -1;
+      if (n > 1) {
+        slot = atomicAdd(&n_slots, n);
+        splits[atomicAdd(&n_split, 1)] = PdSplit{i, slot, n, 0};
+      }
+      s_slot[i] = slot;
+      s_tiles[i] = (unsigned short)tiles[k];
+    }
     if (tid == PD_PLAN_THREADS - 1) warp_sums[0] = end;
     __syncthreads();
     base = warp_sums[0];
     __syncthreads();
   }
-  if (tid == 0) first[0] = 0;
-  __syncthreads();
   const int n_entries = min(base, max_entries);
-  for (int i = tid; i < n_seqs; i += PD_PLAN_THREADS) {
-    const int n = first[i + 1] - first[i];
-    if (n > 1) {
-      const int at = atomicAdd(&n_split, 1), slot = atomicAdd(&n_slots, n);
-      splits[at] = PdSplit{i, slot, n, 0};
-      if (first[i] < max_entries) entries[first[i]].slot = slot;
-    } else if (first[i] < max_entries) {
-      entries[first[i]].slot = -1;
-    }
-  }
-  __syncthreads();
   for (int e = tid; e < n_entries; e += PD_PLAN_THREADS) {
-    int lo = 0, hi = n_seqs;
+    int lo = 0, hi = n_seqs;  // the last sequence with first[i] <= e
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
       if (first[mid] <= e) lo = mid;
       else hi = mid;
     }
-    const int c = e - first[lo];
-    const int nt = (checked_len(__ldg(kv_lens + lo), max_kv_len, pv) + PD_KEYS - 1) / PD_KEYS;
-    PdEntry x;
-    x.seq = lo;
-    x.j0 = c * chunk;
-    x.j1 = min(nt, x.j0 + chunk);
-    // the sequence's first entry holds its slots' start; other threads read it here
-    const int s0 = *reinterpret_cast<volatile int *>(&entries[first[lo]].slot);
-    x.slot = s0 < 0 ? -1 : s0 + c;
-    entries[e].seq = x.seq;
-    entries[e].j0 = x.j0;
-    entries[e].j1 = x.j1;
-    if (c > 0) entries[e].slot = x.slot;
+    const int c = e - first[lo], j0 = c * chunk, slot = s_slot[lo];
+    entries[e] = PdEntry{lo, j0, min((int)s_tiles[lo], j0 + chunk), slot < 0 ? -1 : slot + c};
   }
   if (tid == 0) {
     plan->n_entries = n_entries;
@@ -676,16 +643,17 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
   }
 }
 
-// Joins the chunks of one split sequence's head: a CTA of 256 threads, D / 4 per
-// chunk, 8 or 16 chunks at a time.
-template <int D>
+// Joins the chunks of one split sequence's head, o = sum 2^(m_c - M) o_c / sum
+// 2^(m_c - M) l_c.  COLS columns per CTA of 256 threads, COLS / 4 threads per chunk:
+// 32 columns when few rows would leave most SMs idle, else all.
+template <int D, int COLS>
 __global__ void __launch_bounds__(256) decode_join_kernel(const PdPlan *plan, const PdSplit *splits,
                                                           const float *__restrict__ part, bf16 *__restrict__ o,
                                                           int H, int width) {
-  constexpr int LANES = D / 4, GROUPS = 256 / LANES;
-  __shared__ float sm[8], so[GROUPS][D], sl[GROUPS];
+  constexpr int LANES = COLS / 4, GROUPS = 256 / LANES, PER = D / COLS;
+  __shared__ float sm[8], so[GROUPS][COLS], sl[GROUPS];
   grid_dependency_wait();
-  const int k = blockIdx.x / H, h = blockIdx.x % H;
+  const int c0 = (int)(blockIdx.x % PER) * COLS, h = blockIdx.x / PER % H, k = blockIdx.x / PER / H;
   if (k >= plan->n_split) return;
   const PdSplit s = splits[k];
   const float *p = part + ((size_t)s.slot * H + h) * (D + 2);
@@ -704,7 +672,8 @@ __global__ void __launch_bounds__(256) decode_join_kernel(const PdPlan *plan, co
   for (int c = grp; c < s.n; c += GROUPS) {
     const float *pc = p + c * step;
     const float f = ptx::ex2_approx(pc[D] - m);
-    const float2 x = *reinterpret_cast<const float2 *>(pc + d), y = *reinterpret_cast<const float2 *>(pc + d + 2);
+    const float2 x = *reinterpret_cast<const float2 *>(pc + c0 + d);
+    const float2 y = *reinterpret_cast<const float2 *>(pc + c0 + d + 2);
     l = fmaf(f, pc[D + 1], l);
     acc.x = fmaf(f, x.x, acc.x);
     acc.y = fmaf(f, x.y, acc.y);
@@ -714,14 +683,15 @@ __global__ void __launch_bounds__(256) decode_join_kernel(const PdPlan *plan, co
   *reinterpret_cast<float4 *>(&so[grp][d]) = acc;
   if (d == 0) sl[grp] = l;
   __syncthreads();
-  if (threadIdx.x < width) {
+  const int col = c0 + threadIdx.x;
+  if (threadIdx.x < COLS && col < width) {
     float x = 0.f, z = 0.f;
 #pragma unroll
     for (int g = 0; g < GROUPS; ++g) {
       x += so[g][threadIdx.x];
       z += sl[g];
     }
-    o[((size_t)s.seq * H + h) * width + threadIdx.x] = __float2bfloat16_rn(x / z);
+    o[((size_t)s.seq * H + h) * width + col] = __float2bfloat16_rn(x / z);
   }
 }
 
@@ -830,7 +800,9 @@ cudaError_t launch_tc(const bf16 *q, const bf16 *k, const bf16 *v, bf16 *o, cons
                  st, mq, mk, mv, a);
   if (e != cudaSuccess) return e;
   count_launch();
-  return launch_pdl(decode_join_kernel<D>, dim3((unsigned)(z.max_split * H)), dim3(256), 0, st,
+  const bool narrow = (long long)z.max_split * H < 2LL * sms;
+  return launch_pdl(narrow ? decode_join_kernel<D, 32> : decode_join_kernel<D, D>,
+                    dim3((unsigned)(z.max_split * H * (narrow ? D / 32 : 1))), dim3(256), 0, st,
                     (const PdPlan *)a.plan, (const PdSplit *)splits, (const float *)a.part, o, H, width);
 }
 
@@ -844,8 +816,6 @@ cudaError_t launch_by_heads(const bf16 *q, const bf16 *k, const bf16 *v, bf16 *o
 }
 
 }  // namespace
-
-bool paged_decode_tc_supported(int H, int G, int D) { return (D == 16 || D == 32 || D == 64 || D == 128) && H % G == 0; }
 
 size_t paged_decode_tc_workspace_bytes(int n_seqs, int max_kv_len, int H, int G, int D) {
   return decode_sizes(n_seqs, max_kv_len, H, G, D < 64 ? 64 : D, sm_count()).bytes;

@@ -17,46 +17,30 @@ cudaError_t launch_rope_kv_paged(const T *qkv, T *q_out, T *k, T *v, const Paged
                                  const float2 *table, int table_max_seq, int H, int G, int D, int halves, int *status,
                                  cudaStream_t st);
 
-// CUDA-core attention over pages (paged_simt.cu): fp32, and the head widths that
-// have no tensor-core kernel.
-template <typename T>
-cudaError_t launch_packed_simt(const T *q, const T *k, const T *v, T *o, const PagedView &pv, const PackedView &b,
-                               int H, int G, int D, int *status, cudaStream_t st);
-
 // Tensor maps (packed_tc.cu), 64 columns wide in the 128-byte swizzle: `box` rows of
 // one page and KV head, coordinates (column, row in page, head, page); box_heads x
 // box_rows of packed query rows [rows][H][D], coordinates (column, head, row).
 bool make_paged_map(CUtensorMap *map, const bf16 *pool, const PagedView &pv, int G, int D, int box);
 bool make_heads_map(CUtensorMap *map, const bf16 *q, int rows, int H, int D, int box_heads, int box_rows);
 
-// Tensor-core attention of packed rows (packed_tc.cu): bf16, up to 128 query heads
-// per KV head.
-bool packed_tc_supported(int H, int G, int D);
+// Tensor-core attention of packed rows (packed_tc.cu).
 size_t packed_tc_workspace_bytes(const PackedView &b, int H, int G, int D);
 cudaError_t launch_packed_tc(const bf16 *q, const bf16 *k, const bf16 *v, bf16 *o, const PagedView &pv,
                              const PackedView &b, int H, int G, int D, void *workspace, int *status, cudaStream_t st);
 
-// Tensor-core decode attention (paged_decode_tc.cu): bf16.
-bool paged_decode_tc_supported(int H, int G, int D);
+// Tensor-core decode attention (paged_decode_tc.cu).
 size_t paged_decode_tc_workspace_bytes(int n_seqs, int max_kv_len, int H, int G, int D);
 cudaError_t launch_paged_decode_tc(const bf16 *q, const bf16 *k, const bf16 *v, bf16 *o, const PagedView &pv,
                                    const int *kv_lens, int n_seqs, int max_kv_len, int H, int G, int D,
                                    void *workspace, int *status, cudaStream_t st);
 
-// Split of one sequence's keys over CTAs: parts of `chunk` keys, `n` of them at
-// the longest length the call allows.
-struct DecodeSplit {
-  int chunk = 0, n = 1;
-};
-DecodeSplit paged_decode_simt_split(int n_seqs, int max_kv_len, int H, int G);
-template <typename T>
-cudaError_t launch_paged_decode_simt(const T *q, const T *k, const T *v, T *o, const PagedView &pv,
+// fp32 attention over pages on CUDA cores (paged_simt.cu).
+cudaError_t launch_packed_simt(const float *q, const float *k, const float *v, float *o, const PagedView &pv,
+                               const PackedView &b, int H, int G, int D, int *status, cudaStream_t st);
+size_t paged_decode_simt_workspace_bytes(int n_seqs, int max_kv_len, int H, int G, int D);
+cudaError_t launch_paged_decode_simt(const float *q, const float *k, const float *v, float *o, const PagedView &pv,
                                      const int *kv_lens, int n_seqs, int max_kv_len, int H, int G, int D, float *part,
                                      int *status, cudaStream_t st);
-// o[i][h] = the parts of part [n_seqs][H][split.n][D + 2] joined (paged_simt.cu).
-template <typename T>
-cudaError_t launch_paged_combine(const float *part, T *o, const PagedView &pv, const int *kv_lens, int n_seqs,
-                                 int max_kv_len, int H, int D, DecodeSplit split, cudaStream_t st);
 
 // Log-probabilities, entropy and top_k of logits rows (logprobs.cu); targets
 // and logprobs may both be null, entropy too.  A target outside [0, V) other than

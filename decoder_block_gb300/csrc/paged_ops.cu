@@ -77,7 +77,7 @@ llama_status view_of(const llama_paged_kv_cache *kv, int32_t dtype, int32_t G, i
 
 llama_status check_batch(const llama_packed_batch *b) {
   if (b->n_seqs < 0 || b->n_tokens < 0 || b->max_kv_len < 0) return LLAMA_ERR_INVALID_ARG;
-  if (b->n_seqs > LLAMA_PACKED_MAX_SEQS) return LLAMA_ERR_UNSUPPORTED;
+  if (b->n_seqs > LLAMA_PACKED_MAX_SEQS || b->max_kv_len > LLAMA_PACKED_MAX_KV) return LLAMA_ERR_UNSUPPORTED;
   return LLAMA_OK;
 }
 
@@ -125,7 +125,7 @@ size_t llama_op_attention_packed_workspace_bytes(int32_t dtype, const llama_pack
                                                  int32_t G, int32_t D) {
   if (!dtype_ok(dtype) || batch == nullptr || check_heads(H, G, D) != LLAMA_OK || check_batch(batch) != LLAMA_OK)
     return 0;
-  if (dtype != LLAMA_BF16 || !packed_tc_supported(H, G, D) || batch->n_seqs == 0 || batch->n_tokens == 0) return 0;
+  if (dtype != LLAMA_BF16 || batch->n_seqs == 0 || batch->n_tokens == 0) return 0;
   return packed_tc_workspace_bytes(view_of(batch), H, G, D);
 }
 
@@ -151,25 +151,21 @@ llama_status llama_op_attention_packed(int32_t dtype, const void *q, const llama
   }
   cudaStream_t st = (cudaStream_t)stream;
   const PackedView b = view_of(batch);
-  if (dtype == LLAMA_BF16 && packed_tc_supported(H, G, D))
+  if (dtype == LLAMA_BF16)
     return status_of(launch_packed_tc((const bf16 *)q, (const bf16 *)kv->k, (const bf16 *)kv->v, (bf16 *)o, pv, b, H,
                                       G, D, workspace, status, st));
-  if (dtype == LLAMA_BF16)
-    return status_of(launch_packed_simt<bf16>((const bf16 *)q, (const bf16 *)kv->k, (const bf16 *)kv->v, (bf16 *)o, pv,
-                                              b, H, G, D, status, st));
-  return status_of(launch_packed_simt<float>((const float *)q, (const float *)kv->k, (const float *)kv->v, (float *)o,
-                                             pv, b, H, G, D, status, st));
+  return status_of(launch_packed_simt((const float *)q, (const float *)kv->k, (const float *)kv->v, (float *)o, pv, b, H,
+                                      G, D, status, st));
 }
 
 size_t llama_op_attention_paged_decode_workspace_bytes(int32_t dtype, int32_t n_seqs, int32_t max_kv_len,
                                                        int32_t H, int32_t G, int32_t D) {
   if (!dtype_ok(dtype) || n_seqs <= 0 || n_seqs > LLAMA_PACKED_MAX_SEQS || max_kv_len < 0 ||
-      check_heads(H, G, D) != LLAMA_OK)
+      max_kv_len > LLAMA_PACKED_MAX_KV || check_heads(H, G, D) != LLAMA_OK)
     return 0;
-  if (dtype == LLAMA_BF16 && paged_decode_tc_supported(H, G, D))
+  if (dtype == LLAMA_BF16)
     return paged_decode_tc_workspace_bytes(n_seqs, max_kv_len, H, G, D);
-  const DecodeSplit split = paged_decode_simt_split(n_seqs, max_kv_len, H, G);
-  return split.n > 1 ? (size_t)n_seqs * H * split.n * (D + 2) * sizeof(float) : 0;
+  return paged_decode_simt_workspace_bytes(n_seqs, max_kv_len, H, G, D);
 }
 
 llama_status llama_op_attention_paged_decode(int32_t dtype, const void *q, const llama_paged_kv_cache *kv,
@@ -178,7 +174,7 @@ llama_status llama_op_attention_paged_decode(int32_t dtype, const void *q, const
                                              size_t workspace_bytes, int32_t *status, llama_stream stream) {
   if (!dtype_ok(dtype) || kv == nullptr || n_seqs < 0 || max_kv_len < 0) return LLAMA_ERR_INVALID_ARG;
   llama_status s = check_heads(H, G, D);
-  if (s == LLAMA_OK && n_seqs > LLAMA_PACKED_MAX_SEQS) s = LLAMA_ERR_UNSUPPORTED;
+  if (s == LLAMA_OK && (n_seqs > LLAMA_PACKED_MAX_SEQS || max_kv_len > LLAMA_PACKED_MAX_KV)) s = LLAMA_ERR_UNSUPPORTED;
   PagedView pv;
   if (s == LLAMA_OK) s = view_of(kv, dtype, G, D, &pv);
   if (s != LLAMA_OK) return s;
@@ -193,17 +189,11 @@ llama_status llama_op_attention_paged_decode(int32_t dtype, const void *q, const
     if (s != LLAMA_OK) return s;
   }
   cudaStream_t st = (cudaStream_t)stream;
-  if (dtype == LLAMA_BF16 && paged_decode_tc_supported(H, G, D))
+  if (dtype == LLAMA_BF16)
     return status_of(launch_paged_decode_tc((const bf16 *)q, (const bf16 *)kv->k, (const bf16 *)kv->v, (bf16 *)o, pv,
                                             kv_lens, n_seqs, max_kv_len, H, G, D, workspace, status, st));
-  float *part = (float *)workspace;
-  if (dtype == LLAMA_BF16)
-    return status_of(launch_paged_decode_simt<bf16>((const bf16 *)q, (const bf16 *)kv->k, (const bf16 *)kv->v,
-                                                    (bf16 *)o, pv, kv_lens, n_seqs, max_kv_len, H, G, D, part, status,
-                                                    st));
-  return status_of(launch_paged_decode_simt<float>((const float *)q, (const float *)kv->k, (const float *)kv->v,
-                                                   (float *)o, pv, kv_lens, n_seqs, max_kv_len, H, G, D, part, status,
-                                                   st));
+  return status_of(launch_paged_decode_simt((const float *)q, (const float *)kv->k, (const float *)kv->v, (float *)o, pv,
+                                            kv_lens, n_seqs, max_kv_len, H, G, D, (float *)workspace, status, st));
 }
 
 llama_status llama_op_token_logprobs(int32_t dtype, const void *logits, int64_t row_stride, const int32_t *targets,

@@ -1,8 +1,7 @@
-// Attention over cache pages on CUDA cores, fp32 throughout: fp32 caches, and
-// the head widths 16 and 32 that have no tensor-core kernel ("The Evolving
-// Transformer 04 · LLaMA", §05 GQA; "Full Llama 3 transformer block", How it
-// works: keys j <= position).  One pass over the keys with the running maximum
-// and sum of the softmax.
+// fp32 attention over cache pages on CUDA cores ("The Evolving Transformer 04 ·
+// LLaMA", §05 GQA; "Full Llama 3 transformer block", How it works: keys
+// j <= position).  One pass over the keys with the running maximum and sum of the
+// softmax; fp32 products and sums throughout.
 #include <float.h>
 #include <math.h>
 
@@ -29,13 +28,13 @@ struct PsLayout {
 };
 
 // Stages rows of 16-byte vectors as fp32; `row_ptr(i)` null gives zeros.
-template <typename T, int D, typename F>
+template <int D, typename F>
 __device__ __forceinline__ void stage_rows(float *dst, int rows, F &&row_ptr) {
-  constexpr int V = Vec16<T>::N, RV = D / V;
+  constexpr int V = Vec16<float>::N, RV = D / V;
   for (int u = threadIdx.x; u < rows * RV; u += blockDim.x) {
     const int i = u / RV, c = (u % RV) * V;
-    const T *p = row_ptr(i);
-    Vec16<T> x;
+    const float *p = row_ptr(i);
+    Vec16<float> x;
     x.raw = make_uint4(0, 0, 0, 0);
     if (p != nullptr) x = load16(p + c);
     float *d = dst + i * (D + 4) + c;
@@ -45,9 +44,9 @@ __device__ __forceinline__ void stage_rows(float *dst, int rows, F &&row_ptr) {
   }
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(PS_THREADS) packed_simt_kernel(const T *__restrict__ q, const T *__restrict__ kc,
-                                                                 const T *__restrict__ vc, T *__restrict__ o,
+template <int D>
+__global__ void __launch_bounds__(PS_THREADS) packed_simt_kernel(const float *__restrict__ q, const float *__restrict__ kc,
+                                                                 const float *__restrict__ vc, float *__restrict__ o,
                                                                  PagedView pv, PackedView b, int H, int G, float scale,
                                                                  int *status) {
   using L = PsLayout<D>;
@@ -89,7 +88,7 @@ __global__ void __launch_bounds__(PS_THREADS) packed_simt_kernel(const T *__rest
   const int rows = min(PS_ROWS, s.count * r - row0);
   const int shift = s.kv_len - s.count;  // position of the sequence's first new token
 
-  stage_rows<T, D>(sq, PS_ROWS, [&](int i) -> const T * {
+  stage_rows<D>(sq, PS_ROWS, [&](int i) -> const float * {
     if (i >= rows) return nullptr;
     const int R = row0 + i;
     return q + ((size_t)(s.first + R / r) * H + g * r + R % r) * D;
@@ -108,7 +107,7 @@ __global__ void __launch_bounds__(PS_THREADS) packed_simt_kernel(const T *__rest
   const int n_keys = min(s.kv_len, shift + (row0 + rows - 1) / r + 1);
   for (int k0 = 0; k0 < n_keys; k0 += PS_KEYS) {
     __syncthreads();
-    auto row_of = [&](const T *pool, int j) -> const T * {
+    auto row_of = [&](const float *pool, int j) -> const float * {
       const int p = k0 + j;
       if (p >= s.kv_len) return nullptr;
       const int page = pv.page(seq, p >> pv.page_log2);
@@ -116,8 +115,8 @@ __global__ void __launch_bounds__(PS_THREADS) packed_simt_kernel(const T *__rest
       return pool + page * pv.page_stride +
              (((long long)g << pv.page_log2) + (p & ((1 << pv.page_log2) - 1))) * D;
     };
-    stage_rows<T, D>(sk, PS_KEYS, [&](int j) { return row_of(kc, j); });
-    stage_rows<T, D>(sv, PS_KEYS, [&](int j) { return row_of(vc, j); });
+    stage_rows<D>(sk, PS_KEYS, [&](int j) { return row_of(kc, j); });
+    stage_rows<D>(sv, PS_KEYS, [&](int j) { return row_of(vc, j); });
     if (threadIdx.x < PS_KEYS) {
       const int p = k0 + (int)threadIdx.x;
       if (p < s.kv_len && pv.page(seq, p >> pv.page_log2) < 0) report_status(status, LLAMA_ERR_RANGE);
@@ -191,18 +190,18 @@ __global__ void __launch_bounds__(PS_THREADS) packed_simt_kernel(const T *__rest
     const int R = row0 + ty * 4 + i;
     if (ty * 4 + i >= rows) continue;
     const float inv = ls > 0.f ? 1.f / ls : 0.f;
-    T *dst = o + ((size_t)(s.first + R / r) * H + g * r + R % r) * D;
+    float *dst = o + ((size_t)(s.first + R / r) * H + g * r + R % r) * D;
 #pragma unroll
-    for (int c = 0; c < D / 16; ++c) dst[tx + 16 * c] = from_f32<T>(acc[i][c] * inv);
+    for (int c = 0; c < D / 16; ++c) dst[tx + 16 * c] = (acc[i][c] * inv);
   }
 }
 
-template <typename T, int D>
-cudaError_t packed_simt(const T *q, const T *k, const T *v, T *o, const PagedView &pv, const PackedView &b, int H,
+template <int D>
+cudaError_t packed_simt(const float *q, const float *k, const float *v, float *o, const PagedView &pv, const PackedView &b, int H,
                         int G, int *status, cudaStream_t st) {
   static PerContextOnce attr;
   const cudaError_t e = attr.run([] {
-    return cudaFuncSetAttribute(packed_simt_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(packed_simt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 PsLayout<D>::BYTES);
   });
   if (e != cudaSuccess) return e;
@@ -210,7 +209,7 @@ cudaError_t packed_simt(const T *q, const T *k, const T *v, T *o, const PagedVie
   const long long tiles = (long long)b.n_tokens * (H / G) / PS_ROWS + b.n_seqs;
   if (tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
   count_launch();
-  packed_simt_kernel<T, D><<<dim3((unsigned)tiles, (unsigned)G), PS_THREADS, PsLayout<D>::BYTES, st>>>(
+  packed_simt_kernel<D><<<dim3((unsigned)tiles, (unsigned)G), PS_THREADS, PsLayout<D>::BYTES, st>>>(
       q, k, v, o, pv, b, H, G, 1.0f / sqrtf((float)D), status);
   return cudaGetLastError();
 }
@@ -220,10 +219,29 @@ cudaError_t packed_simt(const T *q, const T *k, const T *v, T *o, const PagedVie
 // heads); 64 keys at a time staged as fp32.
 constexpr int PD_KEYS = 64, PD_THREADS = 256, PD_HEADS = 8;
 
-template <typename T, int D>
-__global__ void __launch_bounds__(PD_THREADS) paged_decode_simt_kernel(const T *__restrict__ q,
-                                                                       const T *__restrict__ kc,
-                                                                       const T *__restrict__ vc, T *__restrict__ o,
+// Split of one sequence's keys over CTAs: parts of `chunk` keys, `n` of them at the
+// longest length the call allows.
+struct DecodeSplit {
+  int chunk = 0, n = 1;
+};
+DecodeSplit decode_split(int n_seqs, int max_kv_len, int H, int G) {
+  // About four CTAs per SM when the batch alone does not give them, parts of at
+  // least 128 keys (two tiles) so that the join stays small beside them.
+  const long long ctas = (long long)n_seqs * G * ((H / G + PD_HEADS - 1) / PD_HEADS);
+  const long long want = (4 * 152 + ctas - 1) / ctas, most = (max_kv_len + 127) / 128;
+  const int n = (int)(want < most ? want : most > 1 ? most : 1);
+  DecodeSplit s;
+  s.chunk = ((max_kv_len + n - 1) / n + PD_KEYS - 1) / PD_KEYS * PD_KEYS;
+  if (s.chunk < PD_KEYS) s.chunk = PD_KEYS;
+  s.n = (max_kv_len + s.chunk - 1) / s.chunk;
+  if (s.n < 1) s.n = 1;
+  return s;
+}
+
+template <int D>
+__global__ void __launch_bounds__(PD_THREADS) paged_decode_simt_kernel(const float *__restrict__ q,
+                                                                       const float *__restrict__ kc,
+                                                                       const float *__restrict__ vc, float *__restrict__ o,
                                                                        float *__restrict__ part, PagedView pv,
                                                                        const int *__restrict__ kv_lens, int max_kv_len,
                                                                        int H, int G, DecodeSplit split, float scale,
@@ -244,7 +262,7 @@ __global__ void __launch_bounds__(PD_THREADS) paged_decode_simt_kernel(const T *
   if (k0 >= len && !(blockIdx.x == 0 && split.n == 1)) return;
   const size_t bh = (size_t)seq * H + g * r + h0;
 
-  for (int u = threadIdx.x; u < nh * D; u += PD_THREADS) sq[u] = to_f32<T>(q[bh * D + u]) * scale;
+  for (int u = threadIdx.x; u < nh * D; u += PD_THREADS) sq[u] = (q[bh * D + u]) * scale;
   if (threadIdx.x < PD_HEADS) {
     sm[threadIdx.x] = -INFINITY;
     sl[threadIdx.x] = 0.f;
@@ -255,7 +273,7 @@ __global__ void __launch_bounds__(PD_THREADS) paged_decode_simt_kernel(const T *
   for (int h = 0; h < PD_HEADS; ++h) acc[h] = 0.f;
   for (int t0 = k0; t0 < k1; t0 += PD_KEYS) {
     const int n = min(PD_KEYS, k1 - t0);
-    auto row_of = [&](const T *pool, int j) -> const T * {
+    auto row_of = [&](const float *pool, int j) -> const float * {
       if (j >= n) return nullptr;
       const int p = t0 + j;
       const int page = pv.page(seq, p >> pv.page_log2);
@@ -263,7 +281,7 @@ __global__ void __launch_bounds__(PD_THREADS) paged_decode_simt_kernel(const T *
       return pool + page * pv.page_stride + (((long long)g << pv.page_log2) + (p & ((1 << pv.page_log2) - 1))) * D;
     };
     __syncthreads();
-    stage_rows<T, D>(sk, PD_KEYS, [&](int j) { return row_of(kc, j); });
+    stage_rows<D>(sk, PD_KEYS, [&](int j) { return row_of(kc, j); });
     if (threadIdx.x < n && pv.page(seq, (t0 + (int)threadIdx.x) >> pv.page_log2) < 0)
       report_status(status, LLAMA_ERR_RANGE);
     __syncthreads();
@@ -298,7 +316,7 @@ __global__ void __launch_bounds__(PD_THREADS) paged_decode_simt_kernel(const T *
         sm[h] = mn;
       }
     }
-    stage_rows<T, D>(sk, PD_KEYS, [&](int j) { return row_of(vc, j); });
+    stage_rows<D>(sk, PD_KEYS, [&](int j) { return row_of(vc, j); });
     __syncthreads();
 #pragma unroll
     for (int hh = 0; hh < PD_HEADS; ++hh)
@@ -321,7 +339,7 @@ __global__ void __launch_bounds__(PD_THREADS) paged_decode_simt_kernel(const T *
 #pragma unroll
     for (int s = 0; s < SLICES; ++s) x += red[(s * PD_HEADS + hh) * D + e];
     if (split.n == 1) {
-      o[bh * D + u] = from_f32<T>(sl[hh] > 0.f ? x / sl[hh] : 0.f);
+      o[bh * D + u] = (sl[hh] > 0.f ? x / sl[hh] : 0.f);
     } else {
       float *pp = part + ((bh + hh) * split.n + blockIdx.x) * (D + 2);
       pp[e] = x;
@@ -334,8 +352,7 @@ __global__ void __launch_bounds__(PD_THREADS) paged_decode_simt_kernel(const T *
 }
 
 // One warp-wide column of threads per output: o = sum_c 2^(m_c - M) o_c / sum_c 2^(m_c - M) l_c.
-template <typename T>
-__global__ void __launch_bounds__(128) paged_combine_kernel(const float *__restrict__ part, T *__restrict__ o,
+__global__ void __launch_bounds__(128) paged_combine_kernel(const float *__restrict__ part, float *__restrict__ o,
                                                             PagedView pv, const int *__restrict__ kv_lens,
                                                             int max_kv_len, int H, int D, DecodeSplit split) {
   const int bh = blockIdx.x, d = threadIdx.x;
@@ -343,93 +360,63 @@ __global__ void __launch_bounds__(128) paged_combine_kernel(const float *__restr
   const int n = (len + split.chunk - 1) / split.chunk;
   const float *p = part + (size_t)bh * split.n * (D + 2);
   float m = -INFINITY;
+#pragma unroll 8
   for (int s = 0; s < n; ++s) m = fmaxf(m, p[s * (D + 2) + D]);
   float ov = 0.f, lv = 0.f;
+#pragma unroll 8
   for (int s = 0; s < n; ++s) {
     const float f = ptx::ex2_approx(p[s * (D + 2) + D] - m);
     ov = fmaf(f, p[s * (D + 2) + d], ov);
     lv = fmaf(f, p[s * (D + 2) + D + 1], lv);
   }
-  o[(size_t)bh * D + d] = from_f32<T>(n > 0 ? ov / lv : 0.f);
+  o[(size_t)bh * D + d] = (n > 0 ? ov / lv : 0.f);
 }
 
-template <typename T, int D>
-cudaError_t decode_simt(const T *q, const T *k, const T *v, T *o, const PagedView &pv, const int *kv_lens, int n_seqs,
+template <int D>
+cudaError_t decode_simt(const float *q, const float *k, const float *v, float *o, const PagedView &pv, const int *kv_lens, int n_seqs,
                         int max_kv_len, int H, int G, float *part, int *status, cudaStream_t st) {
-  const DecodeSplit split = paged_decode_simt_split(n_seqs, max_kv_len, H, G);
+  const DecodeSplit split = decode_split(n_seqs, max_kv_len, H, G);
   const int blocks = (H / G + PD_HEADS - 1) / PD_HEADS;
-  if (n_seqs > 65535 || G * blocks > 65535) return cudaErrorInvalidValue;
+  if ((long long)G * blocks > 65535 || (long long)n_seqs * H > 0x7fffffffLL) return cudaErrorInvalidValue;
   count_launch();
-  paged_decode_simt_kernel<T, D><<<dim3((unsigned)split.n, (unsigned)n_seqs, (unsigned)(G * blocks)), PD_THREADS, 0,
+  paged_decode_simt_kernel<D><<<dim3((unsigned)split.n, (unsigned)n_seqs, (unsigned)(G * blocks)), PD_THREADS, 0,
                                    st>>>(q, k, v, o, part, pv, kv_lens, max_kv_len, H, G, split,
                                          1.0f / sqrtf((float)D), status);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || split.n == 1) return e;
-  return launch_paged_combine<T>(part, o, pv, kv_lens, n_seqs, max_kv_len, H, D, split, st);
+  count_launch();
+  paged_combine_kernel<<<(unsigned)(n_seqs * H), (unsigned)D, 0, st>>>(part, o, pv, kv_lens, max_kv_len, H, D, split);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
-template <typename T>
-cudaError_t launch_packed_simt(const T *q, const T *k, const T *v, T *o, const PagedView &pv, const PackedView &b,
+cudaError_t launch_packed_simt(const float *q, const float *k, const float *v, float *o, const PagedView &pv, const PackedView &b,
                                int H, int G, int D, int *status, cudaStream_t st) {
   switch (D) {
-    case 16: return packed_simt<T, 16>(q, k, v, o, pv, b, H, G, status, st);
-    case 32: return packed_simt<T, 32>(q, k, v, o, pv, b, H, G, status, st);
-    case 64: return packed_simt<T, 64>(q, k, v, o, pv, b, H, G, status, st);
-    case 128: return packed_simt<T, 128>(q, k, v, o, pv, b, H, G, status, st);
+    case 16: return packed_simt<16>(q, k, v, o, pv, b, H, G, status, st);
+    case 32: return packed_simt<32>(q, k, v, o, pv, b, H, G, status, st);
+    case 64: return packed_simt<64>(q, k, v, o, pv, b, H, G, status, st);
+    case 128: return packed_simt<128>(q, k, v, o, pv, b, H, G, status, st);
   }
   return cudaErrorInvalidValue;
 }
 
-DecodeSplit paged_decode_simt_split(int n_seqs, int max_kv_len, int H, int G) {
-  // About four CTAs per SM when the batch alone does not give them, parts of at
-  // least 256 keys (four tiles) so that the join stays small beside them.
-  const long long ctas = (long long)n_seqs * G * ((H / G + PD_HEADS - 1) / PD_HEADS);
-  const long long want = (4 * 152 + ctas - 1) / ctas;
-  const long long most = (max_kv_len + 255) / 256;
-  const int n = (int)(want < most ? (want > 1 ? want : 1) : (most > 1 ? most : 1));
-  DecodeSplit s;
-  s.chunk = ((max_kv_len + n - 1) / n + PD_KEYS - 1) / PD_KEYS * PD_KEYS;
-  if (s.chunk < PD_KEYS) s.chunk = PD_KEYS;
-  s.n = (max_kv_len + s.chunk - 1) / s.chunk;
-  if (s.n < 1) s.n = 1;
-  return s;
+size_t paged_decode_simt_workspace_bytes(int n_seqs, int max_kv_len, int H, int G, int D) {
+  const DecodeSplit split = decode_split(n_seqs, max_kv_len, H, G);
+  return split.n > 1 ? (size_t)n_seqs * H * split.n * (D + 2) * sizeof(float) : 0;
 }
 
-template <typename T>
-cudaError_t launch_paged_decode_simt(const T *q, const T *k, const T *v, T *o, const PagedView &pv,
+cudaError_t launch_paged_decode_simt(const float *q, const float *k, const float *v, float *o, const PagedView &pv,
                                      const int *kv_lens, int n_seqs, int max_kv_len, int H, int G, int D, float *part,
                                      int *status, cudaStream_t st) {
   switch (D) {
-    case 16: return decode_simt<T, 16>(q, k, v, o, pv, kv_lens, n_seqs, max_kv_len, H, G, part, status, st);
-    case 32: return decode_simt<T, 32>(q, k, v, o, pv, kv_lens, n_seqs, max_kv_len, H, G, part, status, st);
-    case 64: return decode_simt<T, 64>(q, k, v, o, pv, kv_lens, n_seqs, max_kv_len, H, G, part, status, st);
-    case 128: return decode_simt<T, 128>(q, k, v, o, pv, kv_lens, n_seqs, max_kv_len, H, G, part, status, st);
+    case 16: return decode_simt<16>(q, k, v, o, pv, kv_lens, n_seqs, max_kv_len, H, G, part, status, st);
+    case 32: return decode_simt<32>(q, k, v, o, pv, kv_lens, n_seqs, max_kv_len, H, G, part, status, st);
+    case 64: return decode_simt<64>(q, k, v, o, pv, kv_lens, n_seqs, max_kv_len, H, G, part, status, st);
+    case 128: return decode_simt<128>(q, k, v, o, pv, kv_lens, n_seqs, max_kv_len, H, G, part, status, st);
   }
   return cudaErrorInvalidValue;
 }
-
-template <typename T>
-cudaError_t launch_paged_combine(const float *part, T *o, const PagedView &pv, const int *kv_lens, int n_seqs,
-                                 int max_kv_len, int H, int D, DecodeSplit split, cudaStream_t st) {
-  if ((long long)n_seqs * H > 0x7fffffffLL) return cudaErrorInvalidValue;
-  count_launch();
-  paged_combine_kernel<T><<<(unsigned)(n_seqs * H), (unsigned)D, 0, st>>>(part, o, pv, kv_lens, max_kv_len, H, D,
-                                                                          split);
-  return cudaGetLastError();
-}
-
-#define PAGED_SIMT_INSTANCES(T)                                                                                       \
-  template cudaError_t launch_packed_simt<T>(const T *, const T *, const T *, T *, const PagedView &,                 \
-                                             const PackedView &, int, int, int, int *, cudaStream_t);                 \
-  template cudaError_t launch_paged_decode_simt<T>(const T *, const T *, const T *, T *, const PagedView &,           \
-                                                   const int *, int, int, int, int, int, float *, int *,              \
-                                                   cudaStream_t);                                                     \
-  template cudaError_t launch_paged_combine<T>(const float *, T *, const PagedView &, const int *, int, int, int, int, \
-                                               DecodeSplit, cudaStream_t);
-PAGED_SIMT_INSTANCES(float)
-PAGED_SIMT_INSTANCES(bf16)
-#undef PAGED_SIMT_INSTANCES
 
 }  // namespace llama

@@ -152,8 +152,10 @@ typedef struct {
     int64_t page_stride;  /* elements from one page to the next, 0: dense */
 } llama_paged_kv_cache;
 
-/* Most sequences of one call (LLAMA_ERR_UNSUPPORTED above). */
+/* Most sequences of one call, and the largest max_kv_len (LLAMA_ERR_UNSUPPORTED
+ * above). */
 #define LLAMA_PACKED_MAX_SEQS 4096
+#define LLAMA_PACKED_MAX_KV 8388480
 
 /* n_seqs sequences packed one after another: the new tokens of sequence i are
  * rows [q_offsets[i], q_offsets[i + 1]) of the token-major arrays of the call

@@ -34,10 +34,11 @@ LENS = [
     ("empty_sequences", [0, 33, 0, 0, 7, 0], [40, 33, 0, 128, 300, 0]),
     ("rows_that_see_nothing", [20, 9, 140], [12, 0, 135]),
     ("longer", [700, 3, 391], [700, 1500, 1024]),
+    ("few_rows_many_keys", [2, 70], [9000, 3333]),
 ]
 HEADS = [
     ("bf16", 32, 8, 128), ("bf16", 9, 3, 64), ("bf16", 4, 4, 128), ("bf16", 10, 2, 64), ("bf16", 16, 1, 128),
-    ("bf16", 40, 1, 64), ("bf16", 7, 1, 128), ("bf16", 4, 2, 32), ("bf16", 6, 2, 16), ("f32", 4, 2, 16),
+    ("bf16", 40, 1, 64), ("bf16", 7, 1, 128), ("bf16", 150, 1, 64), ("bf16", 4, 2, 32), ("bf16", 6, 2, 16), ("f32", 4, 2, 16),
     ("f32", 6, 2, 32), ("f32", 9, 3, 64), ("f32", 8, 2, 128),
 ]
 
@@ -46,7 +47,7 @@ HEADS = [
 @pytest.mark.parametrize("dtype,H,G,D", HEADS)
 def test_packed_attention(lb, name, q_lens, kv_lens, dtype, H, G, D):
     page = {"one_token": 16, "one_tile": 128, "tile_plus_one": 64, "odd_lengths": 16, "prefixes": 32,
-            "empty_sequences": 256, "rows_that_see_nothing": 64, "longer": 32}[name]
+            "empty_sequences": 256, "rows_that_see_nothing": 64, "longer": 32, "few_rows_many_keys": 128}[name]
     p = Problem(f"pk/{name}/{dtype}{H}{G}{D}", dtype, H, G, D, page, q_lens, kv_lens, pad=3)
     d = run_packed(lb, p)
     got, status = _finish(d)
