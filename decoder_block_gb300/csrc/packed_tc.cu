@@ -432,7 +432,9 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
       PtItem next;
       bool fetched = false;
       for (int j = it.j0; j < it.j1; ++j) {
-        if (j == it.j0 + PT_STAGES) {  // the rings are full: time for the next item's look-ups
+        // The next item's look-ups, hidden behind the last tiles of this one; any earlier and
+        // items are dealt out before it shows which CTAs run late (S = 2048: 58 us for 39).
+        if (j + 1 == it.j1) {
           next = fetch(k + 1);
           fetched = true;
         }
@@ -514,44 +516,49 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
           ptx::mbar_arrive(q_empty);
           continue;
         }
-        auto issue_both = [&](int t, int j, int jj) {
-          if (j < (t == 0 ? e0 : e1)) issue_s(jj, t);
-        };
         if (!wait(k_full(jg % PT_STAGES), (jg / PT_STAGES) & 1)) break;
         ptx::tc_fence_after();
-        issue_both(0, it.j0, jg);
-        issue_both(1, it.j0, jg);
+        if (it.j0 < e0) issue_s(jg, 0);
+        if (it.j0 < e1) issue_s(jg, 1);
         ptx::mma_commit(k_empty(jg % PT_STAGES));
         if (n == 1) ptx::mma_commit(q_empty);
-        for (int i = 0; i < n; ++i) {
-          const int j = it.j0 + i, jj = jg + i, st = jj % PT_STAGES;
-          ok = false;
-          if (!wait(v_full(st), (jj / PT_STAGES) & 1)) break;
-          if (j < e0) {
-            if (!wait(p_full(0), n0 & 1)) break;
+        // One key tile: t0, t1 say which query tiles work on it, s0, s1 on the next one.
+        auto step = [&](int i, bool t0, bool t1, bool more, bool s0, bool s1) -> bool {
+          const int jj = jg + i, st = jj % PT_STAGES;
+          if (!wait(v_full(st), (jj / PT_STAGES) & 1)) return false;
+          if (t0) {
+            if (!wait(p_full(0), n0 & 1)) return false;
             ++n0;
             ptx::tc_fence_after();
             issue_pv(jj, i == 0, 0);
           }
-          const bool more = i + 1 < n;
           if (more) {
-            if (!wait(k_full((jj + 1) % PT_STAGES), ((jj + 1) / PT_STAGES) & 1)) break;
+            if (!wait(k_full((jj + 1) % PT_STAGES), ((jj + 1) / PT_STAGES) & 1)) return false;
             ptx::tc_fence_after();
-            issue_both(0, j + 1, jj + 1);
+            if (s0) issue_s(jj + 1, 0);
           }
-          if (j < e1) {
-            if (!wait(p_full(1), n1 & 1)) break;
+          if (t1) {
+            if (!wait(p_full(1), n1 & 1)) return false;
             ++n1;
             ptx::tc_fence_after();
             issue_pv(jj, i == 0, 1);
           }
           ptx::mma_commit(v_empty(st));
           if (more) {
-            issue_both(1, j + 1, jj + 1);
+            if (s1) issue_s(jj + 1, 1);
             ptx::mma_commit(k_empty((jj + 1) % PT_STAGES));
             if (i + 2 == n) ptx::mma_commit(q_empty);
           }
-          ok = true;
+          return true;
+        };
+        // This thread paces the kernel, so the tiles that both query tiles see, and whose
+        // successors they see too, go without the questions of the last ones.
+        const int plain = min(min(e0, e1) - 1 - it.j0, n - 1);
+        int i = 0;
+        for (; ok && i < plain; ++i) ok = step(i, true, true, true, true, true);
+        for (; ok && i < n; ++i) {
+          const int j = it.j0 + i;
+          ok = step(i, j < e0, j < e1, i + 1 < n, j + 1 < e0, j + 1 < e1);
         }
         jg += n;
       }
