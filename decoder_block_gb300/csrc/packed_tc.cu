@@ -110,6 +110,40 @@ __device__ __forceinline__ uint32_t pt_pack2(float a, float b) {
   return *reinterpret_cast<uint32_t *>(&h);
 }
 
+// The MMA thread paces the kernel, so it forms its operands with few instructions: the
+// upper word of every shared-memory descriptor here is the same (128-byte swizzle, 8-row
+// groups 1024 bytes apart), and offsets are added to the lower one.
+constexpr uint32_t PT_DESC_HI = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lbo) { return (addr >> 4) | ((lbo >> 4) << 16); }
+// ACC 1: add to D; 0: overwrite it; -1: as `acc` says.
+template <int ACC>
+__device__ __forceinline__ void pt_mma_ss(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\t"
+      "mov.b64 x, {%1, %3};\n\tmov.b64 y, {%2, %3};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(PT_DESC_HI), "r"(idesc), "n"(ACC)
+      : "memory");
+}
+template <int ACC>
+__device__ __forceinline__ void pt_mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, uint32_t acc) {
+  if constexpr (ACC < 0)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tmov.b64 y, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t}" ::"r"(d),
+        "r"(a_tmem), "r"(b_lo), "r"(PT_DESC_HI), "r"(idesc), "r"(acc)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tmov.b64 y, {%2, %3};\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t}" ::"r"(d),
+        "r"(a_tmem), "r"(b_lo), "r"(PT_DESC_HI), "r"(idesc), "n"(ACC)
+        : "memory");
+}
+
 // Key tiles that the rows [lo, hi) of a sequence's new tokens see.
 __device__ __forceinline__ int tiles_of(int shift, int lo, int hi) {
   if (hi <= lo || shift + hi <= 0) return 0;
@@ -482,24 +516,26 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
     if (lane == 0) {
       constexpr uint32_t idesc_qk = ptx::idesc_bf16_f32(128, PT_KEYS, false);
       constexpr uint32_t idesc_pv = ptx::idesc_bf16_f32(128, D, true);
+      const uint32_t q_lo = desc_lo(s0 + L::OFF_Q, 16), k_lo = desc_lo(s0 + L::OFF_K, 16);
+      const uint32_t v_lo = desc_lo(s0 + L::OFF_V, L::ATOM);  // V: MN-major, 64-column blocks an atom apart
       auto issue_s = [&](int jj, int t) {
-        const uint32_t kb = s0 + L::OFF_K + (jj % PT_STAGES) * L::TILE;
-        const uint32_t qb = s0 + L::OFF_Q + t * L::TILE;
+        const uint32_t kb = k_lo + (jj % PT_STAGES) * (L::TILE >> 4), qb = q_lo + t * (L::TILE >> 4);
+        const uint32_t d = tmem + t * 128;
+        pt_mma_ss<0>(d, qb, kb, idesc_qk);
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk / 4) * L::ATOM + (kk % 4) * 32;
-          ptx::mma_bf16_ss(tmem + t * 128, ptx::smem_desc_sw128(qb + off), ptx::smem_desc_sw128(kb + off), idesc_qk,
-                           kk > 0 ? 1u : 0u);
+        for (int kk = 1; kk < D / 16; ++kk) {
+          const uint32_t off = ((kk / 4) * L::ATOM + (kk % 4) * 32) >> 4;
+          pt_mma_ss<1>(d, qb + off, kb + off, idesc_qk);
         }
         ptx::mma_commit(s_full(t));
       };
       auto issue_pv = [&](int jj, bool first, int t) {
-        const uint32_t vb = s0 + L::OFF_V + (jj % PT_STAGES) * L::TILE;
+        const uint32_t vb = v_lo + (jj % PT_STAGES) * (L::TILE >> 4);
+        const uint32_t d = tmem + 256 + t * D, p = tmem + t * 128;
+        pt_mma_ts<-1>(d, p, vb, idesc_pv, first ? 0u : 1u);
 #pragma unroll
-        for (int kk = 0; kk < PT_KEYS / 16; ++kk) {
-          const uint64_t bdesc = ptx::smem_desc_sw128_mn(vb + kk * 16 * 128, L::ATOM, 1024);
-          ptx::mma_bf16_ts(tmem + 256 + t * D, tmem + t * 128 + kk * 8, bdesc, idesc_pv, (!first || kk > 0) ? 1u : 0u);
-        }
+        for (int kk = 1; kk < PT_KEYS / 16; ++kk)  // 16 keys: two 8-row groups
+          pt_mma_ts<1>(d, p + kk * 8, vb + kk * (16 * 128 >> 4), idesc_pv, 1u);
         ptx::mma_commit(o_done(t));
       };
       // S_0(j+1) goes out right after PV_0(j): the softmax of tile 0 for the next keys
