@@ -56,8 +56,8 @@ struct PtLayout {
   static constexpr int OFF_V = OFF_K + PT_STAGES * TILE;
   static constexpr int OFF_ITEM = OFF_V + PT_STAGES * TILE;  // PtItem
   static constexpr int OFF_BAR = OFF_ITEM + 64;
-  // q_full, q_empty, fin, k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_done[2]
-  static constexpr int NBAR = 3 + 4 * PT_STAGES + 6;
+  // q_full, q_empty, fin, kv_full[2], kv_empty[2], s_full[2], p_full[2], o_done[2]
+  static constexpr int NBAR = 3 + 2 * PT_STAGES + 6;
   static constexpr int BYTES_MIN = 1024 + OFF_BAR + NBAR * 8 + 16;
   // one CTA per SM: two would need all of tensor memory each
   static constexpr int BYTES = BYTES_MIN > 116 * 1024 ? BYTES_MIN : 116 * 1024;
@@ -305,13 +305,13 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
   const uint32_t s0 = ptx::smem_u32(smem);
   const uint32_t bar0 = ptx::smem_u32(bars);
   const uint32_t q_full = bar0, q_empty = bar0 + 8, fin = bar0 + 16;
-  auto k_full = [&](int s) { return bar0 + 8u * (3 + s); };
-  auto k_empty = [&](int s) { return bar0 + 8u * (3 + PT_STAGES + s); };
-  auto v_full = [&](int s) { return bar0 + 8u * (3 + 2 * PT_STAGES + s); };
-  auto v_empty = [&](int s) { return bar0 + 8u * (3 + 3 * PT_STAGES + s); };
-  auto s_full = [&](int t) { return bar0 + 8u * (3 + 4 * PT_STAGES + t); };
-  auto p_full = [&](int t) { return bar0 + 8u * (5 + 4 * PT_STAGES + t); };
-  auto o_done = [&](int t) { return bar0 + 8u * (7 + 4 * PT_STAGES + t); };
+  // Stage jj % 2 of the rings: V of tile jj and K of the item's next tile, which one
+  // step of the MMA thread needs together (an item's first K comes with its Q).
+  auto kv_full = [&](int s) { return bar0 + 8u * (3 + s); };
+  auto kv_empty = [&](int s) { return bar0 + 8u * (3 + PT_STAGES + s); };
+  auto s_full = [&](int t) { return bar0 + 8u * (3 + 2 * PT_STAGES + t); };
+  auto p_full = [&](int t) { return bar0 + 8u * (5 + 2 * PT_STAGES + t); };
+  auto o_done = [&](int t) { return bar0 + 8u * (7 + 2 * PT_STAGES + t); };
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
@@ -326,10 +326,8 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
     ptx::mbar_init(q_empty, 9);  // the MMAs reading Q are done; each softmax warp has read the item
     ptx::mbar_init(fin, 1);
     for (int s = 0; s < PT_STAGES; ++s) {
-      ptx::mbar_init(k_full(s), 1);
-      ptx::mbar_init(k_empty(s), 1);
-      ptx::mbar_init(v_full(s), 1);
-      ptx::mbar_init(v_empty(s), 1);
+      ptx::mbar_init(kv_full(s), 1);
+      ptx::mbar_init(kv_empty(s), 1);
     }
     for (int t = 0; t < 2; ++t) {
       ptx::mbar_init(s_full(t), 1);
@@ -426,26 +424,36 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
       }
       return it;
     };
-    const int boxes_tile = PT_KEYS / a.box;                 // pages of a tile (1 when pages are larger)
-    const int my_box = lane / ATOMS, my_at = lane % ATOMS;  // the box this lane loads
-    const uint32_t dst = my_at * L::ATOM + my_box * a.box * 128;
+    const int boxes_tile = PT_KEYS / a.box;  // pages of a tile (1 when pages are larger)
+    const bool is_k = lane >= 16;            // lanes 0-15 load V, 16-31 the next tile's K
+    const int my_box = (lane & 15) / ATOMS, my_at = (lane & 15) % ATOMS;
+    const uint32_t dst = s0 + (is_k ? L::OFF_K : L::OFF_V) + my_at * L::ATOM + my_box * a.box * 128;
+    const CUtensorMap *map = is_k ? &tmK : &tmV;
+    auto boxes = [&](const PtItem &it, int j) {  // of tile j
+      return j < it.j1 ? min(boxes_tile, (it.kv_len - j * PT_KEYS + a.box - 1) / a.box) : 0;
+    };
     const uint32_t box_bytes = a.box * 128u * ATOMS;
     // Page of this lane's box of key tile j: its id, n_pages (a page of zeros) when
     // the id is out of range, -1 when the tile has no such box.
     auto page_of = [&](const PtItem &it, int j) {
-      const int key = j * PT_KEYS + my_box * a.box;
-      if (my_box >= boxes_tile || j >= it.j1 || key >= it.kv_len) return -1;
-      const int id = a.pv.page(it.seq, key >> a.pv.page_log2);
+      if (my_box >= boxes(it, j)) return -1;
+      const int id = a.pv.page(it.seq, (j * PT_KEYS + my_box * a.box) >> a.pv.page_log2);
       if (id < 0) report_status(a.status, LLAMA_ERR_RANGE);
       return id < 0 ? a.pv.n_pages : id;
     };
-    int items = 0, tiles = 0;  // Q loads and key tiles issued
-    bool v_short = false;      // the last key tile's V was not issued
+    auto load = [&](const PtItem &it, int page, int j, int jj, uint32_t bar) {  // this lane's box of tile j
+      if (page < 0) return;
+      const int r = (j * PT_KEYS) & ((1 << a.pv.page_log2) - 1) & ~(a.box - 1);
+      ptx::tma_load_4d(dst + (jj % PT_STAGES) * L::TILE, map, my_at * 64, r, it.g, page, bar);
+    };
+    int items = 0, tiles = 0;  // Q loads and stages issued
     bool ended = false;        // the end was handed over: the last Q has landed
     bool ok = true;
     PtItem it = fetch(0);
     for (int k = 0; ok; ++k) {
-      int page = it.seq >= 0 ? page_of(it, it.j0) : -1;
+      // V lanes hold the page of their box of tile j, K lanes that of tile j + 1
+      int page = it.seq >= 0 ? page_of(it, it.j0 + (is_k ? 1 : 0)) : -1;
+      const int first_page = it.seq >= 0 && is_k ? page_of(it, it.j0) : -1;
       if (k > 0 && !wait_warp(q_empty, (k - 1) & 1)) break;
       if (lane == 0) *item_slot = it;  // published by the q_full arrival
       __syncwarp();
@@ -456,12 +464,14 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
       }
       const int n_t = it.q0 + a.Mq < it.count ? 2 : 1;  // query tiles that hold rows
       if (lane == 0) {
-        ptx::mbar_arrive_expect_tx(q_full, n_t * ATOMS * a.rb * a.Mq * 128u);
+        ptx::mbar_arrive_expect_tx(q_full, n_t * ATOMS * a.rb * a.Mq * 128u + boxes(it, it.j0) * box_bytes);
         for (int t = 0; t < n_t; ++t)
           for (int at = 0; at < ATOMS; ++at)
             ptx::tma_load_3d(s0 + L::OFF_Q + t * L::TILE + at * L::ATOM, &tmQ, at * 64, it.h0,
                              it.first + it.q0 + t * a.Mq, q_full);
       }
+      __syncwarp();
+      load(it, first_page, it.j0, tiles, q_full);
       ++items;
       PtItem next;
       bool fetched = false;
@@ -473,30 +483,18 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
           fetched = true;
         }
         const int st = tiles % PT_STAGES;
-        const uint32_t ph = (tiles / PT_STAGES) & 1;
-        const int boxes = min(boxes_tile, (it.kv_len - j * PT_KEYS + a.box - 1) / a.box);
-        const int row = (j * PT_KEYS) & ((1 << a.pv.page_log2) - 1) & ~(a.box - 1);
         const int page_now = page;
-        if (j + 1 < it.j1) page = page_of(it, j + 1);
-        if (!wait_warp(k_empty(st), ph ^ 1)) {
+        page = page_of(it, j + 1 + (is_k ? 1 : 0));
+        // Stage 1 is released once more than it was filled: its first K overwrites no earlier
+        // stage's but the first item's first tile.
+        if (!wait_warp(kv_empty(st), ((tiles / PT_STAGES) & 1) ^ (st == 0 ? 1 : 0))) {
           ok = false;
           break;
         }
-        if (lane == 0) ptx::mbar_arrive_expect_tx(k_full(st), boxes * box_bytes);
+        if (lane == 0) ptx::mbar_arrive_expect_tx(kv_full(st), (boxes(it, j) + boxes(it, j + 1)) * box_bytes);
         __syncwarp();
-        if (page_now >= 0)
-          ptx::tma_load_4d(s0 + L::OFF_K + st * L::TILE + dst, &tmK, my_at * 64, row, it.g, page_now, k_full(st));
+        load(it, page_now, j + (is_k ? 1 : 0), tiles + (is_k ? 1 : 0), kv_full(st));
         ++tiles;
-        v_short = true;
-        if (!wait_warp(v_empty(st), ph ^ 1)) {
-          ok = false;
-          break;
-        }
-        if (lane == 0) ptx::mbar_arrive_expect_tx(v_full(st), boxes * box_bytes);
-        __syncwarp();
-        if (page_now >= 0)
-          ptx::tma_load_4d(s0 + L::OFF_V + st * L::TILE + dst, &tmV, my_at * 64, row, it.g, page_now, v_full(st));
-        v_short = false;
       }
       if (!ok) break;
       if (!fetched) next = fetch(k + 1);
@@ -506,10 +504,8 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
     __syncwarp();
     if (lane == 0) {
       if (items > 0 && !ended) ptx::mbar_drain(q_full, (items - 1) & 1, nullptr, 0);
-      for (int j = max(0, tiles - PT_STAGES); j < tiles; ++j) {
-        ptx::mbar_drain(k_full(j % PT_STAGES), (j / PT_STAGES) & 1, nullptr, 0);
-        if (j + 1 < tiles || !v_short) ptx::mbar_drain(v_full(j % PT_STAGES), (j / PT_STAGES) & 1, nullptr, 0);
-      }
+      for (int j = max(0, tiles - PT_STAGES); j < tiles; ++j)
+        ptx::mbar_drain(kv_full(j % PT_STAGES), (j / PT_STAGES) & 1, nullptr, 0);
     }
   } else if (warp == 1) {
     // --------------------------------------------------------------- MMA ---
@@ -542,6 +538,8 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
       // overlaps that of tile 1, and the next item's first S products the output of this one.
       bool ok = true;
       int jg = 0, n0 = 0, n1 = 0;  // key tiles over all items: of the ring, of query tiles 0 and 1
+      int owed = 1;                // stage whose release is still to come (1: see the producer)
+      static_assert(PT_STAGES == 2, "K of tile jj + 1 lies in the other stage");
       for (int k = 0; ok; ++k) {
         if (!wait(q_full, k & 1)) break;
         const PtItem it = *item_slot;
@@ -552,26 +550,25 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
           ptx::mbar_arrive(q_empty);
           continue;
         }
-        if (!wait(k_full(jg % PT_STAGES), (jg / PT_STAGES) & 1)) break;
         ptx::tc_fence_after();
         if (it.j0 < e0) issue_s(jg, 0);
         if (it.j0 < e1) issue_s(jg, 1);
-        ptx::mma_commit(k_empty(jg % PT_STAGES));
+        if (owed >= 0) ptx::mma_commit(kv_empty(owed));
+        owed = -1;
         if (n == 1) ptx::mma_commit(q_empty);
         // One key tile: t0, t1 say which query tiles work on it, s0, s1 on the next one.
-        auto step = [&](int i, bool t0, bool t1, bool more, bool s0, bool s1) -> bool {
+        auto step = [&](int i, bool t0, bool t1, bool s0, bool s1) -> bool {
           const int jj = jg + i, st = jj % PT_STAGES;
-          if (!wait(v_full(st), (jj / PT_STAGES) & 1)) return false;
+          if (!wait(kv_full(st), (jj / PT_STAGES) & 1)) return false;
           if (t0) {
             if (!wait(p_full(0), n0 & 1)) return false;
             ++n0;
             ptx::tc_fence_after();
             issue_pv(jj, i == 0, 0);
           }
-          if (more) {
-            if (!wait(k_full((jj + 1) % PT_STAGES), ((jj + 1) / PT_STAGES) & 1)) return false;
+          if (s0) {
             ptx::tc_fence_after();
-            if (s0) issue_s(jj + 1, 0);
+            issue_s(jj + 1, 0);
           }
           if (t1) {
             if (!wait(p_full(1), n1 & 1)) return false;
@@ -579,22 +576,22 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
             ptx::tc_fence_after();
             issue_pv(jj, i == 0, 1);
           }
-          ptx::mma_commit(v_empty(st));
-          if (more) {
-            if (s1) issue_s(jj + 1, 1);
-            ptx::mma_commit(k_empty((jj + 1) % PT_STAGES));
-            if (i + 2 == n) ptx::mma_commit(q_empty);
-          }
+          if (s1) issue_s(jj + 1, 1);
+          // The stage may be filled again when the next tile's K has been used too; behind an
+          // item's last tile that is the next item's first.
+          if (i + 1 < n) ptx::mma_commit(kv_empty(st));
+          else owed = st;
+          if (i + 2 == n) ptx::mma_commit(q_empty);
           return true;
         };
         // This thread paces the kernel, so the tiles that both query tiles see, and whose
         // successors they see too, go without the questions of the last ones.
         const int plain = min(min(e0, e1) - 1 - it.j0, n - 1);
         int i = 0;
-        for (; ok && i < plain; ++i) ok = step(i, true, true, true, true, true);
+        for (; ok && i < plain; ++i) ok = step(i, true, true, true, true);
         for (; ok && i < n; ++i) {
           const int j = it.j0 + i;
-          ok = step(i, j < e0, j < e1, i + 1 < n, j + 1 < e0, j + 1 < e1);
+          ok = step(i, j < e0, j < e1, j + 1 < e0, j + 1 < e1);
         }
         jg += n;
       }
@@ -643,7 +640,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
         // query tile that works on the tile does it, before its P is handed over.
         if (key0 + PT_KEYS > it.kv_len && t == (j < e0 ? 0 : 1)) {
           const int st = (jg + jl) % PT_STAGES;
-          if (!wait_warp(v_full(st), ((jg + jl) / PT_STAGES) & 1)) {
+          if (!wait_warp(kv_full(st), ((jg + jl) / PT_STAGES) & 1)) {
             ok = false;
             break;
           }
