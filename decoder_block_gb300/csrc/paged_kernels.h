@@ -35,8 +35,9 @@ cudaError_t launch_paged_decode_tc(const bf16 *q, const bf16 *k, const bf16 *v, 
                                    void *workspace, int *status, cudaStream_t st);
 
 // fp32 attention over pages on CUDA cores (paged_simt.cu).
+size_t packed_simt_workspace_bytes(const PackedView &b, int H, int G, int D);
 cudaError_t launch_packed_simt(const float *q, const float *k, const float *v, float *o, const PagedView &pv,
-                               const PackedView &b, int H, int G, int D, int *status, cudaStream_t st);
+                               const PackedView &b, int H, int G, int D, float *part, int *status, cudaStream_t st);
 size_t paged_decode_simt_workspace_bytes(int n_seqs, int max_kv_len, int H, int G, int D);
 cudaError_t launch_paged_decode_simt(const float *q, const float *k, const float *v, float *o, const PagedView &pv,
                                      const int *kv_lens, int n_seqs, int max_kv_len, int H, int G, int D, float *part,

@@ -125,8 +125,9 @@ size_t llama_op_attention_packed_workspace_bytes(int32_t dtype, const llama_pack
                                                  int32_t G, int32_t D) {
   if (!dtype_ok(dtype) || batch == nullptr || check_heads(H, G, D) != LLAMA_OK || check_batch(batch) != LLAMA_OK)
     return 0;
-  if (dtype != LLAMA_BF16 || batch->n_seqs == 0 || batch->n_tokens == 0) return 0;
-  return packed_tc_workspace_bytes(view_of(batch), H, G, D);
+  if (batch->n_seqs == 0 || batch->n_tokens == 0) return 0;
+  const PackedView b = view_of(batch);
+  return dtype == LLAMA_BF16 ? packed_tc_workspace_bytes(b, H, G, D) : packed_simt_workspace_bytes(b, H, G, D);
 }
 
 llama_status llama_op_attention_packed(int32_t dtype, const void *q, const llama_paged_kv_cache *kv,
@@ -155,7 +156,7 @@ llama_status llama_op_attention_packed(int32_t dtype, const void *q, const llama
     return status_of(launch_packed_tc((const bf16 *)q, (const bf16 *)kv->k, (const bf16 *)kv->v, (bf16 *)o, pv, b, H,
                                       G, D, workspace, status, st));
   return status_of(launch_packed_simt((const float *)q, (const float *)kv->k, (const float *)kv->v, (float *)o, pv, b, H,
-                                      G, D, status, st));
+                                      G, D, (float *)workspace, status, st));
 }
 
 size_t llama_op_attention_paged_decode_workspace_bytes(int32_t dtype, int32_t n_seqs, int32_t max_kv_len,

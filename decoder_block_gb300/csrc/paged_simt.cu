@@ -1,70 +1,121 @@
 // fp32 attention over cache pages on CUDA cores ("The Evolving Transformer 04 ·
 // LLaMA", §05 GQA; "Full Llama 3 transformer block", How it works: keys
 // j <= position).  One pass over the keys with the running maximum and sum of the
-// softmax; fp32 products and sums throughout.
+// softmax; fp32 products and sums throughout (the tensor cores round fp32 operands).
+// Keys are split over CTAs when the rows alone are too few to fill the SMs, and the
+// parts joined in order: o = sum e^(m_c - M) o_c / sum e^(m_c - M) l_c.
 #include <float.h>
 #include <math.h>
 
 #include "paged_kernels.h"
-#include "ptx.cuh"
 
 namespace llama {
 namespace {
 
+constexpr int KEYS = 64;        // keys of a tile
+constexpr int THREADS = 256;
+constexpr int SM_CTAS = 4 * 152;  // CTAs that the splits aim at: four per SM
+
+// Split of the keys over CTAs: parts of `chunk` keys, `n` of them at the longest
+// length that the call allows.
+struct Split {
+  int chunk = KEYS, n = 1;
+};
+Split split_of(long long ctas, int max_kv_len, int least) {
+  const long long want = (SM_CTAS + ctas - 1) / ctas, most = (max_kv_len + least - 1) / least;
+  const int n = (int)(want < most ? want : most > 1 ? most : 1);
+  Split s;
+  s.chunk = ((max_kv_len + n - 1) / n + KEYS - 1) / KEYS * KEYS;
+  if (s.chunk < KEYS) s.chunk = KEYS;
+  s.n = (max_kv_len + s.chunk - 1) / s.chunk;
+  if (s.n < 1) s.n = 1;
+  return s;
+}
+
+// A thread's vectors of a tile of KEYS rows of D floats: vector u = i * THREADS + tid
+// is column u % (D / 4) of row u / (D / 4).
+template <int D>
+struct TileRegs {
+  static constexpr int RV = D / 4, PER = KEYS * RV / THREADS;
+  float4 x[PER];
+  // row_ptr(i): row i in memory, null for zeros
+  template <typename F>
+  __device__ __forceinline__ void load(F &&row_ptr) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int u = i * THREADS + threadIdx.x;
+      const float *p = row_ptr(u / RV);
+      x[i] = p != nullptr ? *reinterpret_cast<const float4 *>(p + u % RV * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  }
+  __device__ __forceinline__ void store(float *dst) const {  // rows 16 bytes apart in banks
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      const int u = i * THREADS + threadIdx.x;
+      *reinterpret_cast<float4 *>(dst + u / RV * (D + 4) + u % RV * 4) = x[i];
+    }
+  }
+};
+
+// Row of position p of a sequence in a pool, null when its page id is out of range.
+__device__ __forceinline__ const float *page_row(const float *pool, const PagedView &pv, int seq, int g, int D, int p) {
+  const int page = pv.page(seq, p >> pv.page_log2);
+  if (page < 0) return nullptr;
+  return pool + page * pv.page_stride + (((long long)g << pv.page_log2) + (p & ((1 << pv.page_log2) - 1))) * D;
+}
+
 // ---------------------------------------------------------------- packed ---
 // CTA = (sequence, KV head g, 64 rows of the flattened (position, head of the
-// group) index R = position * r + hh): the r heads of a group share every K/V
-// tile, and no row is padding but in a sequence's last tile.  256 threads, 4 x 4
-// scores and 4 x (D / 16) outputs per thread.
-constexpr int PS_ROWS = 64, PS_KEYS = 64, PS_THREADS = 256;
+// group) index R = position * r + hh, part of the keys): the r heads of a group share
+// every K/V tile, and no row is padding but in a sequence's last tile.  4 x 4 scores
+// and 4 x (D / 16) outputs per thread.
+constexpr int ROWS = 64;
 
 template <int D>
 struct PsLayout {
-  static constexpr int LDQ = D + 4, LDP = PS_KEYS + 4;  // rows 16 bytes apart in banks
-  static constexpr int OFF_K = PS_ROWS * LDQ;
-  static constexpr int OFF_V = OFF_K + PS_KEYS * LDQ;
-  static constexpr int OFF_P = OFF_V + PS_KEYS * LDQ;
-  static constexpr int BYTES = (OFF_P + PS_ROWS * LDP) * 4;
+  static constexpr int LDQ = D + 4, LDP = KEYS + 4;
+  static constexpr int OFF_K = ROWS * LDQ;
+  static constexpr int OFF_V = OFF_K + KEYS * LDQ;
+  static constexpr int OFF_P = OFF_V + KEYS * LDQ;
+  static constexpr int BYTES = (OFF_P + ROWS * LDP) * 4;
 };
 
-// Stages rows of 16-byte vectors as fp32; `row_ptr(i)` null gives zeros.
-template <int D, typename F>
-__device__ __forceinline__ void stage_rows(float *dst, int rows, F &&row_ptr) {
-  constexpr int V = Vec16<float>::N, RV = D / V;
-  for (int u = threadIdx.x; u < rows * RV; u += blockDim.x) {
-    const int i = u / RV, c = (u % RV) * V;
-    const float *p = row_ptr(i);
-    Vec16<float> x;
-    x.raw = make_uint4(0, 0, 0, 0);
-    if (p != nullptr) x = load16(p + c);
-    float *d = dst + i * (D + 4) + c;
-#pragma unroll
-    for (int k = 0; k < V; k += 4)
-      *reinterpret_cast<float4 *>(d + k) = make_float4(x.get(k), x.get(k + 1), x.get(k + 2), x.get(k + 3));
-  }
+// Keys that the tile of rows R in [row0, row0 + rows) of a sequence sees.
+__device__ __forceinline__ int tile_keys(const SeqSpan &s, int r, int row0) {
+  const int rows = min(ROWS, s.count * r - row0);
+  return max(0, s.kv_len - s.count + (row0 + rows - 1) / r + 1);
 }
 
+struct PsArgs {
+  const float *q, *k, *v;
+  float *o, *part;  // part [split.n][n_tokens][H][D + 2]
+  PagedView pv;
+  PackedView b;
+  int H, G;
+  Split split;
+  float scale;
+  int *status;
+};
+
 template <int D>
-__global__ void __launch_bounds__(PS_THREADS) packed_simt_kernel(const float *__restrict__ q, const float *__restrict__ kc,
-                                                                 const float *__restrict__ vc, float *__restrict__ o,
-                                                                 PagedView pv, PackedView b, int H, int G, float scale,
-                                                                 int *status) {
+__global__ void __launch_bounds__(THREADS) packed_simt_kernel(const __grid_constant__ PsArgs a) {
   using L = PsLayout<D>;
   extern __shared__ __align__(16) float smem_f[];
   float *sq = smem_f, *sk = smem_f + L::OFF_K, *sv = smem_f + L::OFF_V, *sp = smem_f + L::OFF_P;
-  const int r = H / G, g = blockIdx.y;
+  const int r = a.H / a.G, g = blockIdx.y;
   const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
-  if (blockIdx.x == 0 && g == 0)
-    for (int i = threadIdx.x; i < b.n_seqs; i += blockDim.x) check_seq(b, pv, i, status);
+  if (blockIdx.x == 0 && g == 0 && blockIdx.z == 0)
+    for (int i = threadIdx.x; i < a.b.n_seqs; i += THREADS) check_seq(a.b, a.pv, i, a.status);
   // block -> (sequence, tile): the grid holds at least one block for every tile
   __shared__ int found[2];
   if (threadIdx.x == 0) found[0] = -1;
   __syncthreads();
   if (threadIdx.x < 32) {
     int base = 0;
-    for (int i0 = 0; i0 < b.n_seqs; i0 += 32) {
+    for (int i0 = 0; i0 < a.b.n_seqs; i0 += 32) {
       const int i = i0 + threadIdx.x;
-      const int n = i < b.n_seqs ? (int)(((long long)seq_span(b, pv, i).count * r + PS_ROWS - 1) / PS_ROWS) : 0;
+      const int n =
+          i < a.b.n_seqs ? (int)(((long long)seq_span(a.b, a.pv, i).count * r + ROWS - 1) / ROWS) : 0;
       int end = n;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
@@ -81,18 +132,23 @@ __global__ void __launch_bounds__(PS_THREADS) packed_simt_kernel(const float *__
     }
   }
   __syncthreads();
-  const int seq = found[0], tile = found[1];
+  const int seq = found[0], row0 = found[1] * ROWS;
   if (seq < 0) return;
-  const SeqSpan s = seq_span(b, pv, seq);
-  const int row0 = tile * PS_ROWS;
-  const int rows = min(PS_ROWS, s.count * r - row0);
+  const SeqSpan s = seq_span(a.b, a.pv, seq);
+  const int rows = min(ROWS, s.count * r - row0);
   const int shift = s.kv_len - s.count;  // position of the sequence's first new token
+  const int n_keys = tile_keys(s, r, row0);
+  const int k_begin = blockIdx.z * a.split.chunk, k_end = min(n_keys, k_begin + a.split.chunk);
+  if (blockIdx.z > 0 && k_begin >= n_keys) return;
+  const bool whole = n_keys <= a.split.chunk;  // one part: no join
 
-  stage_rows<D>(sq, PS_ROWS, [&](int i) -> const float * {
-    if (i >= rows) return nullptr;
-    const int R = row0 + i;
-    return q + ((size_t)(s.first + R / r) * H + g * r + R % r) * D;
-  });
+  for (int u = threadIdx.x; u < ROWS * (D / 4); u += THREADS) {
+    const int i = u / (D / 4), c = u % (D / 4) * 4, R = row0 + i;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (i < rows)
+      x = *reinterpret_cast<const float4 *>(a.q + ((size_t)(s.first + R / r) * a.H + g * r + R % r) * D + c);
+    *reinterpret_cast<float4 *>(sq + i * L::LDQ + c) = x;
+  }
   int pos[4];
   float m[4], l[4], acc[4][D / 16];
 #pragma unroll
@@ -104,22 +160,18 @@ __global__ void __launch_bounds__(PS_THREADS) packed_simt_kernel(const float *__
 #pragma unroll
     for (int c = 0; c < D / 16; ++c) acc[i][c] = 0.f;
   }
-  const int n_keys = min(s.kv_len, shift + (row0 + rows - 1) / r + 1);
-  for (int k0 = 0; k0 < n_keys; k0 += PS_KEYS) {
-    __syncthreads();
-    auto row_of = [&](const float *pool, int j) -> const float * {
-      const int p = k0 + j;
-      if (p >= s.kv_len) return nullptr;
-      const int page = pv.page(seq, p >> pv.page_log2);
-      if (page < 0) return nullptr;
-      return pool + page * pv.page_stride +
-             (((long long)g << pv.page_log2) + (p & ((1 << pv.page_log2) - 1))) * D;
-    };
-    stage_rows<D>(sk, PS_KEYS, [&](int j) { return row_of(kc, j); });
-    stage_rows<D>(sv, PS_KEYS, [&](int j) { return row_of(vc, j); });
-    if (threadIdx.x < PS_KEYS) {
-      const int p = k0 + (int)threadIdx.x;
-      if (p < s.kv_len && pv.page(seq, p >> pv.page_log2) < 0) report_status(status, LLAMA_ERR_RANGE);
+  for (int k0 = k_begin; k0 < k_end; k0 += KEYS) {
+    {
+      TileRegs<D> kr, vr;
+      kr.load([&](int j) { return k0 + j < s.kv_len ? page_row(a.k, a.pv, seq, g, D, k0 + j) : nullptr; });
+      vr.load([&](int j) { return k0 + j < s.kv_len ? page_row(a.v, a.pv, seq, g, D, k0 + j) : nullptr; });
+      if (threadIdx.x < KEYS) {
+        const int p = k0 + (int)threadIdx.x;
+        if (p < s.kv_len && a.pv.page(seq, p >> a.pv.page_log2) < 0) report_status(a.status, LLAMA_ERR_RANGE);
+      }
+      __syncthreads();
+      kr.store(sk);
+      vr.store(sv);
     }
     __syncthreads();
     // scores of rows ty*4 + i against keys tx + 16 j
@@ -130,23 +182,23 @@ __global__ void __launch_bounds__(PS_THREADS) packed_simt_kernel(const float *__
       for (int j = 0; j < 4; ++j) sc[i][j] = 0.f;
 #pragma unroll 4
     for (int d = 0; d < D; d += 4) {
-      float4 a[4], c[4];
+      float4 x[4], c[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4 *>(sq + (ty * 4 + i) * L::LDQ + d);
+      for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4 *>(sq + (ty * 4 + i) * L::LDQ + d);
 #pragma unroll
       for (int j = 0; j < 4; ++j) c[j] = *reinterpret_cast<const float4 *>(sk + (tx + 16 * j) * L::LDQ + d);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-          sc[i][j] = fmaf(a[i].x, c[j].x, fmaf(a[i].y, c[j].y, fmaf(a[i].z, c[j].z, fmaf(a[i].w, c[j].w, sc[i][j]))));
+          sc[i][j] = fmaf(x[i].x, c[j].x, fmaf(x[i].y, c[j].y, fmaf(x[i].z, c[j].z, fmaf(x[i].w, c[j].w, sc[i][j]))));
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float mt = -INFINITY;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        sc[i][j] = k0 + tx + 16 * j <= pos[i] ? sc[i][j] * scale : -INFINITY;
+        sc[i][j] = k0 + tx + 16 * j <= pos[i] ? sc[i][j] * a.scale : -INFINITY;
         mt = fmaxf(mt, sc[i][j]);
       }
 #pragma unroll
@@ -168,7 +220,7 @@ __global__ void __launch_bounds__(PS_THREADS) packed_simt_kernel(const float *__
     __syncwarp();  // a row's 16 threads are half a warp: only they read its weights
     // outputs of rows ty*4 + i, columns tx + 16 c
 #pragma unroll 4
-    for (int j = 0; j < PS_KEYS; j += 4) {
+    for (int j = 0; j < KEYS; j += 4) {
       float4 w[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float4 *>(sp + (ty * 4 + i) * L::LDP + j);
@@ -189,125 +241,181 @@ __global__ void __launch_bounds__(PS_THREADS) packed_simt_kernel(const float *__
     for (int off = 8; off > 0; off >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, off);
     const int R = row0 + ty * 4 + i;
     if (ty * 4 + i >= rows) continue;
-    const float inv = ls > 0.f ? 1.f / ls : 0.f;
-    float *dst = o + ((size_t)(s.first + R / r) * H + g * r + R % r) * D;
+    const size_t row = (size_t)(s.first + R / r) * a.H + g * r + R % r;
+    if (whole) {
+      const float inv = ls > 0.f ? 1.f / ls : 0.f;
 #pragma unroll
-    for (int c = 0; c < D / 16; ++c) dst[tx + 16 * c] = (acc[i][c] * inv);
+      for (int c = 0; c < D / 16; ++c) a.o[row * D + tx + 16 * c] = acc[i][c] * inv;
+    } else {
+      float *pp = a.part + ((size_t)blockIdx.z * a.b.n_tokens * a.H + row) * (D + 2);
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) pp[tx + 16 * c] = acc[i][c];
+      if (tx == 0) {
+        pp[D] = m[i];
+        pp[D + 1] = ls;
+      }
+    }
   }
 }
 
+// Joins n parts, `step` floats apart, of one row of D floats (then m and l): one warp.
 template <int D>
-cudaError_t packed_simt(const float *q, const float *k, const float *v, float *o, const PagedView &pv, const PackedView &b, int H,
-                        int G, int *status, cudaStream_t st) {
+__device__ __forceinline__ void join_row(const float *p, size_t step, int n, float *o) {
+  constexpr int PER = D > 32 ? D / 32 : 1;
+  const int lane = threadIdx.x & 31;
+  float m = -INFINITY, l = 0.f, acc[PER];
+#pragma unroll
+  for (int e = 0; e < PER; ++e) acc[e] = 0.f;
+  for (int c = lane; c < n; c += 32) m = fmaxf(m, p[c * step + D]);
+  m = warp_max(m);
+#pragma unroll 4
+  for (int c = 0; c < n; ++c) {
+    const float f = expf(p[c * step + D] - m);
+    l = fmaf(f, p[c * step + D + 1], l);
+#pragma unroll
+    for (int e = 0; e < PER; ++e)
+      if (lane + 32 * e < D) acc[e] = fmaf(f, p[c * step + lane + 32 * e], acc[e]);
+  }
+#pragma unroll
+  for (int e = 0; e < PER; ++e)
+    if (lane + 32 * e < D) o[lane + 32 * e] = l > 0.f ? acc[e] / l : 0.f;
+}
+
+template <int D>
+__global__ void __launch_bounds__(THREADS) packed_join_simt_kernel(const __grid_constant__ PsArgs a) {
+  const long long row = (long long)blockIdx.x * (THREADS / 32) + threadIdx.x / 32;  // token, head
+  if (row >= (long long)a.b.n_tokens * a.H) return;
+  const int t = (int)(row / a.H), r = a.H / a.G, hh = (int)(row % a.H) % r;
+  const int seq = find_seq(a.b, t);
+  if (seq < 0) return;
+  const SeqSpan s = seq_span(a.b, a.pv, seq);
+  const int n_keys = tile_keys(s, r, ((t - s.first) * r + hh) / ROWS * ROWS);
+  if (n_keys <= a.split.chunk) return;
+  join_row<D>(a.part + row * (D + 2), (size_t)a.b.n_tokens * a.H * (D + 2), (n_keys + a.split.chunk - 1) / a.split.chunk,
+              a.o + row * D);
+}
+
+// every sequence ends in at most one tile that is not full
+long long packed_tiles(const PackedView &b, int H, int G) { return (long long)b.n_tokens * (H / G) / ROWS + b.n_seqs; }
+Split packed_split(const PackedView &b, int H, int G) {
+  return split_of(packed_tiles(b, H, G) * G, b.max_kv_len, 4 * KEYS);
+}
+
+template <int D>
+cudaError_t packed_simt(PsArgs a, cudaStream_t st) {
   static PerContextOnce attr;
   const cudaError_t e = attr.run([] {
     return cudaFuncSetAttribute(packed_simt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 PsLayout<D>::BYTES);
   });
   if (e != cudaSuccess) return e;
-  // every sequence ends in at most one tile that is not full
-  const long long tiles = (long long)b.n_tokens * (H / G) / PS_ROWS + b.n_seqs;
-  if (tiles > 0x7fffffffLL) return cudaErrorInvalidValue;
+  a.scale = 1.0f / sqrtf((float)D);
+  const long long tiles = packed_tiles(a.b, a.H, a.G);
+  if (tiles > 0x7fffffffLL || a.G > 65535) return cudaErrorInvalidValue;
   count_launch();
-  packed_simt_kernel<D><<<dim3((unsigned)tiles, (unsigned)G), PS_THREADS, PsLayout<D>::BYTES, st>>>(
-      q, k, v, o, pv, b, H, G, 1.0f / sqrtf((float)D), status);
+  packed_simt_kernel<D><<<dim3((unsigned)tiles, (unsigned)a.G, (unsigned)a.split.n), THREADS, PsLayout<D>::BYTES, st>>>(a);
+  cudaError_t r = cudaGetLastError();
+  if (r != cudaSuccess || a.split.n == 1) return r;
+  count_launch();
+  const long long rows = (long long)a.b.n_tokens * a.H;
+  packed_join_simt_kernel<D><<<(unsigned)((rows + THREADS / 32 - 1) / (THREADS / 32)), THREADS, 0, st>>>(a);
   return cudaGetLastError();
 }
 
 // ---------------------------------------------------------------- decode ---
 // CTA = (part of the keys, sequence, KV head and block of up to 8 of its query
-// heads); 64 keys at a time staged as fp32.
-constexpr int PD_KEYS = 64, PD_THREADS = 256, PD_HEADS = 8;
-
-// Split of one sequence's keys over CTAs: parts of `chunk` keys, `n` of them at the
-// longest length the call allows.
-struct DecodeSplit {
-  int chunk = 0, n = 1;
-};
-DecodeSplit decode_split(int n_seqs, int max_kv_len, int H, int G) {
-  // About four CTAs per SM when the batch alone does not give them, parts of at
-  // least 128 keys (two tiles) so that the join stays small beside them.
-  const long long ctas = (long long)n_seqs * G * ((H / G + PD_HEADS - 1) / PD_HEADS);
-  const long long want = (4 * 152 + ctas - 1) / ctas, most = (max_kv_len + 127) / 128;
-  const int n = (int)(want < most ? want : most > 1 ? most : 1);
-  DecodeSplit s;
-  s.chunk = ((max_kv_len + n - 1) / n + PD_KEYS - 1) / PD_KEYS * PD_KEYS;
-  if (s.chunk < PD_KEYS) s.chunk = PD_KEYS;
-  s.n = (max_kv_len + s.chunk - 1) / s.chunk;
-  if (s.n < 1) s.n = 1;
-  return s;
-}
+// heads); the next tile's K and V are on their way while this one is worked on.
+constexpr int HEADS = 8;
 
 template <int D>
-__global__ void __launch_bounds__(PD_THREADS) paged_decode_simt_kernel(const float *__restrict__ q,
-                                                                       const float *__restrict__ kc,
-                                                                       const float *__restrict__ vc, float *__restrict__ o,
-                                                                       float *__restrict__ part, PagedView pv,
-                                                                       const int *__restrict__ kv_lens, int max_kv_len,
-                                                                       int H, int G, DecodeSplit split, float scale,
-                                                                       int *status) {
-  constexpr int LDQ = D + 4, SLICES = PD_THREADS / D;
-  constexpr int RED = SLICES * PD_HEADS * D, TILE = PD_KEYS * LDQ;
-  __shared__ __align__(16) float sk[TILE > RED ? TILE : RED];  // K, then V, of one tile; at the end the slices
-  __shared__ __align__(16) float sq[PD_HEADS * D];
-  __shared__ float sp[PD_HEADS][PD_KEYS + 1];
-  __shared__ float sm[PD_HEADS], sl[PD_HEADS], sc[PD_HEADS];
-  const int r = H / G, blocks = (r + PD_HEADS - 1) / PD_HEADS;
-  const int g = blockIdx.z / blocks, h0 = (blockIdx.z % blocks) * PD_HEADS;
-  const int nh = min(PD_HEADS, r - h0), seq = blockIdx.y;
-  const int raw_len = __ldg(kv_lens + seq);
-  const int len = checked_len(raw_len, max_kv_len, pv);
-  if (len != raw_len && blockIdx.x == 0 && blockIdx.z == 0 && threadIdx.x == 0) report_status(status, LLAMA_ERR_RANGE);
-  const int k0 = blockIdx.x * split.chunk, k1 = min(len, k0 + split.chunk);
-  if (k0 >= len && !(blockIdx.x == 0 && split.n == 1)) return;
-  const size_t bh = (size_t)seq * H + g * r + h0;
+struct DsLayout {
+  static constexpr int LD = D + 4, SLICES = THREADS / D;
+  static constexpr int RED = SLICES * HEADS * D;  // the slices' sums, over K and V at the end
+  static constexpr int OFF_V = KEYS * LD;
+  static constexpr int KV = 2 * KEYS * LD > RED ? 2 * KEYS * LD : RED;
+  static constexpr int OFF_Q = KV;
+  static constexpr int OFF_S = OFF_Q + HEADS * D;       // scores [HEADS][KEYS + 1]
+  static constexpr int OFF_W = OFF_S + HEADS * (KEYS + 1) / 4 * 4 + 4;  // weights [KEYS][HEADS]
+  static constexpr int BYTES = (OFF_W + KEYS * HEADS) * 4;
+};
 
-  for (int u = threadIdx.x; u < nh * D; u += PD_THREADS) sq[u] = (q[bh * D + u]) * scale;
-  if (threadIdx.x < PD_HEADS) {
+struct DsArgs {
+  const float *q, *k, *v;
+  float *o, *part;  // part [n_seqs][H][split.n][D + 2]
+  PagedView pv;
+  const int *kv_lens;
+  int n_seqs, max_kv_len, H, G;
+  Split split;
+  float scale;
+  int *status;
+};
+
+template <int D>
+__global__ void __launch_bounds__(THREADS) paged_decode_simt_kernel(const __grid_constant__ DsArgs a) {
+  using L = DsLayout<D>;
+  extern __shared__ __align__(16) float smem_f[];
+  float *sk = smem_f, *sv = smem_f + L::OFF_V, *sq = smem_f + L::OFF_Q, *ss = smem_f + L::OFF_S,
+        *sw = smem_f + L::OFF_W;
+  __shared__ float sm[HEADS], sl[HEADS], sc[HEADS];
+  const int r = a.H / a.G, blocks = (r + HEADS - 1) / HEADS;
+  const int g = blockIdx.z / blocks, h0 = (blockIdx.z % blocks) * HEADS;
+  const int nh = min(HEADS, r - h0), seq = blockIdx.y;
+  const int raw_len = __ldg(a.kv_lens + seq);
+  const int len = checked_len(raw_len, a.max_kv_len, a.pv);
+  if (len != raw_len && blockIdx.x == 0 && blockIdx.z == 0 && threadIdx.x == 0)
+    report_status(a.status, LLAMA_ERR_RANGE);
+  const int k0 = blockIdx.x * a.split.chunk, k1 = min(len, k0 + a.split.chunk);
+  if (k0 >= len && blockIdx.x > 0) return;
+  const size_t bh = (size_t)seq * a.H + g * r + h0;
+
+  TileRegs<D> kr, vr;
+  auto load = [&](int t0) {
+    kr.load([&](int j) { return t0 + j < k1 ? page_row(a.k, a.pv, seq, g, D, t0 + j) : nullptr; });
+    vr.load([&](int j) { return t0 + j < k1 ? page_row(a.v, a.pv, seq, g, D, t0 + j) : nullptr; });
+    const int p = t0 + (int)threadIdx.x;
+    if (threadIdx.x < KEYS && p < k1 && a.pv.page(seq, p >> a.pv.page_log2) < 0)
+      report_status(a.status, LLAMA_ERR_RANGE);
+  };
+  load(k0);
+  for (int u = threadIdx.x; u < HEADS * D; u += THREADS) sq[u] = u < nh * D ? a.q[bh * D + u] * a.scale : 0.f;
+  if (threadIdx.x < HEADS) {
     sm[threadIdx.x] = -INFINITY;
     sl[threadIdx.x] = 0.f;
   }
   const int d = threadIdx.x % D, slice = threadIdx.x / D;
-  float acc[PD_HEADS];
+  const int h = threadIdx.x / 32, lane = threadIdx.x & 31;
+  float acc[HEADS];
 #pragma unroll
-  for (int h = 0; h < PD_HEADS; ++h) acc[h] = 0.f;
-  for (int t0 = k0; t0 < k1; t0 += PD_KEYS) {
-    const int n = min(PD_KEYS, k1 - t0);
-    auto row_of = [&](const float *pool, int j) -> const float * {
-      if (j >= n) return nullptr;
-      const int p = t0 + j;
-      const int page = pv.page(seq, p >> pv.page_log2);
-      if (page < 0) return nullptr;
-      return pool + page * pv.page_stride + (((long long)g << pv.page_log2) + (p & ((1 << pv.page_log2) - 1))) * D;
-    };
+  for (int i = 0; i < HEADS; ++i) acc[i] = 0.f;
+  for (int t0 = k0; t0 < k1; t0 += KEYS) {
+    const int n = min(KEYS, k1 - t0);
     __syncthreads();
-    stage_rows<D>(sk, PD_KEYS, [&](int j) { return row_of(kc, j); });
-    if (threadIdx.x < n && pv.page(seq, (t0 + (int)threadIdx.x) >> pv.page_log2) < 0)
-      report_status(status, LLAMA_ERR_RANGE);
+    kr.store(sk);
+    vr.store(sv);
     __syncthreads();
-    {
-      const int key = threadIdx.x % PD_KEYS;
-      for (int h = threadIdx.x / PD_KEYS; h < nh; h += PD_THREADS / PD_KEYS) {
-        float x = 0.f;
+    if (t0 + KEYS < k1) load(t0 + KEYS);
+    {  // scores of key tid % 64 for heads tid / 64 and tid / 64 + 4
+      const int key = threadIdx.x % KEYS, ha = threadIdx.x / KEYS, hb = ha + HEADS / 2;
+      float x = 0.f, y = 0.f;
 #pragma unroll
-        for (int e = 0; e < D; e += 4) {
-          const float4 a = *reinterpret_cast<const float4 *>(sq + h * D + e);
-          const float4 c = *reinterpret_cast<const float4 *>(sk + key * LDQ + e);
-          x = fmaf(a.x, c.x, fmaf(a.y, c.y, fmaf(a.z, c.z, fmaf(a.w, c.w, x))));
-        }
-        sp[h][key] = key < n ? x : -INFINITY;
+      for (int e = 0; e < D; e += 4) {
+        const float4 c = *reinterpret_cast<const float4 *>(sk + key * L::LD + e);
+        const float4 p = *reinterpret_cast<const float4 *>(sq + ha * D + e);
+        const float4 q = *reinterpret_cast<const float4 *>(sq + hb * D + e);
+        x = fmaf(p.x, c.x, fmaf(p.y, c.y, fmaf(p.z, c.z, fmaf(p.w, c.w, x))));
+        y = fmaf(q.x, c.x, fmaf(q.y, c.y, fmaf(q.z, c.z, fmaf(q.w, c.w, y))));
       }
+      ss[ha * (KEYS + 1) + key] = key < n ? x : -INFINITY;
+      ss[hb * (KEYS + 1) + key] = key < n ? y : -INFINITY;
     }
     __syncthreads();
-    // warp h: the running maximum and sum of head h; every tile holds a key, so the maximum is one
-    const int h = threadIdx.x / 32, lane = threadIdx.x & 31;
-    if (h < nh) {
-      const float a = sp[h][lane], c = sp[h][lane + 32];
-      const float mn = fmaxf(sm[h], warp_max(fmaxf(a, c)));
-      const float pa = expf(a - mn), pc = expf(c - mn);
-      const float ls = warp_sum(pa + pc);
-      sp[h][lane] = pa;
-      sp[h][lane + 32] = pc;
+    {  // warp h: the running maximum and sum of head h; every tile holds a key, so the maximum is one
+      const float x = ss[h * (KEYS + 1) + lane], y = ss[h * (KEYS + 1) + lane + 32];
+      const float mn = fmaxf(sm[h], warp_max(fmaxf(x, y)));
+      const float px = expf(x - mn), py = expf(y - mn);
+      const float ls = warp_sum(px + py);
+      sw[lane * HEADS + h] = px;
+      sw[(lane + 32) * HEADS + h] = py;
       __syncwarp();
       if (lane == 0) {
         const float corr = expf(sm[h] - mn);
@@ -316,105 +424,137 @@ __global__ void __launch_bounds__(PD_THREADS) paged_decode_simt_kernel(const flo
         sm[h] = mn;
       }
     }
-    stage_rows<D>(sk, PD_KEYS, [&](int j) { return row_of(vc, j); });
     __syncthreads();
 #pragma unroll
-    for (int hh = 0; hh < PD_HEADS; ++hh)
-      if (hh < nh) {
-        float a = acc[hh] * sc[hh];
-        for (int j = slice; j < n; j += SLICES) a = fmaf(sp[hh][j], sk[j * LDQ + d], a);
-        acc[hh] = a;
-      }
+    for (int i = 0; i < HEADS; ++i) acc[i] *= sc[i];
+    for (int j = slice; j < n; j += L::SLICES) {
+      const float v = sv[j * L::LD + d];
+      const float4 w0 = *reinterpret_cast<const float4 *>(sw + j * HEADS);
+      const float4 w1 = *reinterpret_cast<const float4 *>(sw + j * HEADS + 4);
+      acc[0] = fmaf(w0.x, v, acc[0]);
+      acc[1] = fmaf(w0.y, v, acc[1]);
+      acc[2] = fmaf(w0.z, v, acc[2]);
+      acc[3] = fmaf(w0.w, v, acc[3]);
+      acc[4] = fmaf(w1.x, v, acc[4]);
+      acc[5] = fmaf(w1.y, v, acc[5]);
+      acc[6] = fmaf(w1.z, v, acc[6]);
+      acc[7] = fmaf(w1.w, v, acc[7]);
+    }
   }
-  // join the slices of the keys
   __syncthreads();
-  float *red = sk;  // [SLICES][PD_HEADS][D]
+  float *red = smem_f;  // [SLICES][HEADS][D]
 #pragma unroll
-  for (int hh = 0; hh < PD_HEADS; ++hh)
-    if (hh < nh) red[(slice * PD_HEADS + hh) * D + d] = acc[hh];
+  for (int i = 0; i < HEADS; ++i) red[(slice * HEADS + i) * D + d] = acc[i];
   __syncthreads();
-  for (int u = threadIdx.x; u < nh * D; u += PD_THREADS) {
-    const int hh = u / D, e = u % D;
+  for (int u = threadIdx.x; u < nh * D; u += THREADS) {
+    const int i = u / D, e = u % D;
     float x = 0.f;
 #pragma unroll
-    for (int s = 0; s < SLICES; ++s) x += red[(s * PD_HEADS + hh) * D + e];
-    if (split.n == 1) {
-      o[bh * D + u] = (sl[hh] > 0.f ? x / sl[hh] : 0.f);
+    for (int s = 0; s < L::SLICES; ++s) x += red[(s * HEADS + i) * D + e];
+    if (len <= a.split.chunk) {
+      a.o[bh * D + u] = sl[i] > 0.f ? x / sl[i] : 0.f;
     } else {
-      float *pp = part + ((bh + hh) * split.n + blockIdx.x) * (D + 2);
+      float *pp = a.part + ((bh + i) * a.split.n + blockIdx.x) * (D + 2);
       pp[e] = x;
       if (e == 0) {
-        pp[D] = sm[hh] * 1.4426950408889634f;  // the join works in powers of two
-        pp[D + 1] = sl[hh];
+        pp[D] = sm[i];
+        pp[D + 1] = sl[i];
       }
     }
   }
 }
 
-// One warp-wide column of threads per output: o = sum_c 2^(m_c - M) o_c / sum_c 2^(m_c - M) l_c.
-__global__ void __launch_bounds__(128) paged_combine_kernel(const float *__restrict__ part, float *__restrict__ o,
-                                                            PagedView pv, const int *__restrict__ kv_lens,
-                                                            int max_kv_len, int H, int D, DecodeSplit split) {
-  const int bh = blockIdx.x, d = threadIdx.x;
-  const int len = checked_len(__ldg(kv_lens + bh / H), max_kv_len, pv);
-  const int n = (len + split.chunk - 1) / split.chunk;
-  const float *p = part + (size_t)bh * split.n * (D + 2);
-  float m = -INFINITY;
-#pragma unroll 8
-  for (int s = 0; s < n; ++s) m = fmaxf(m, p[s * (D + 2) + D]);
-  float ov = 0.f, lv = 0.f;
-#pragma unroll 8
-  for (int s = 0; s < n; ++s) {
-    const float f = ptx::ex2_approx(p[s * (D + 2) + D] - m);
-    ov = fmaf(f, p[s * (D + 2) + d], ov);
-    lv = fmaf(f, p[s * (D + 2) + D + 1], lv);
-  }
-  o[(size_t)bh * D + d] = (n > 0 ? ov / lv : 0.f);
+template <int D>
+__global__ void __launch_bounds__(THREADS) decode_join_simt_kernel(const __grid_constant__ DsArgs a) {
+  const long long row = (long long)blockIdx.x * (THREADS / 32) + threadIdx.x / 32;  // sequence, head
+  if (row >= (long long)a.n_seqs * a.H) return;
+  const int len = checked_len(__ldg(a.kv_lens + row / a.H), a.max_kv_len, a.pv);
+  if (len <= a.split.chunk) return;
+  join_row<D>(a.part + row * a.split.n * (D + 2), D + 2, (len + a.split.chunk - 1) / a.split.chunk, a.o + row * D);
+}
+
+Split decode_split(int n_seqs, int max_kv_len, int H, int G) {
+  return split_of((long long)n_seqs * G * ((H / G + HEADS - 1) / HEADS), max_kv_len, 2 * KEYS);
 }
 
 template <int D>
-cudaError_t decode_simt(const float *q, const float *k, const float *v, float *o, const PagedView &pv, const int *kv_lens, int n_seqs,
-                        int max_kv_len, int H, int G, float *part, int *status, cudaStream_t st) {
-  const DecodeSplit split = decode_split(n_seqs, max_kv_len, H, G);
-  const int blocks = (H / G + PD_HEADS - 1) / PD_HEADS;
-  if ((long long)G * blocks > 65535 || (long long)n_seqs * H > 0x7fffffffLL) return cudaErrorInvalidValue;
+cudaError_t decode_simt(DsArgs a, cudaStream_t st) {
+  static PerContextOnce attr;
+  const cudaError_t e = attr.run([] {
+    return cudaFuncSetAttribute(paged_decode_simt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                DsLayout<D>::BYTES);
+  });
+  if (e != cudaSuccess) return e;
+  a.scale = 1.0f / sqrtf((float)D);
+  const long long units = (long long)a.G * ((a.H / a.G + HEADS - 1) / HEADS), rows = (long long)a.n_seqs * a.H;
+  if (units > 65535 || rows > 0x7fffffffLL) return cudaErrorInvalidValue;
   count_launch();
-  paged_decode_simt_kernel<D><<<dim3((unsigned)split.n, (unsigned)n_seqs, (unsigned)(G * blocks)), PD_THREADS, 0,
-                                   st>>>(q, k, v, o, part, pv, kv_lens, max_kv_len, H, G, split,
-                                         1.0f / sqrtf((float)D), status);
-  const cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || split.n == 1) return e;
+  paged_decode_simt_kernel<D>
+      <<<dim3((unsigned)a.split.n, (unsigned)a.n_seqs, (unsigned)units), THREADS, DsLayout<D>::BYTES, st>>>(a);
+  const cudaError_t r = cudaGetLastError();
+  if (r != cudaSuccess || a.split.n == 1) return r;
   count_launch();
-  paged_combine_kernel<<<(unsigned)(n_seqs * H), (unsigned)D, 0, st>>>(part, o, pv, kv_lens, max_kv_len, H, D, split);
+  decode_join_simt_kernel<D><<<(unsigned)((rows + THREADS / 32 - 1) / (THREADS / 32)), THREADS, 0, st>>>(a);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-cudaError_t launch_packed_simt(const float *q, const float *k, const float *v, float *o, const PagedView &pv, const PackedView &b,
-                               int H, int G, int D, int *status, cudaStream_t st) {
+size_t packed_simt_workspace_bytes(const PackedView &b, int H, int G, int D) {
+  const Split s = packed_split(b, H, G);
+  return s.n > 1 ? (size_t)s.n * b.n_tokens * H * (D + 2) * sizeof(float) : 0;
+}
+
+cudaError_t launch_packed_simt(const float *q, const float *k, const float *v, float *o, const PagedView &pv,
+                               const PackedView &b, int H, int G, int D, float *part, int *status, cudaStream_t st) {
+  PsArgs a;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.o = o;
+  a.part = part;
+  a.pv = pv;
+  a.b = b;
+  a.H = H;
+  a.G = G;
+  a.split = packed_split(b, H, G);
+  a.status = status;
   switch (D) {
-    case 16: return packed_simt<16>(q, k, v, o, pv, b, H, G, status, st);
-    case 32: return packed_simt<32>(q, k, v, o, pv, b, H, G, status, st);
-    case 64: return packed_simt<64>(q, k, v, o, pv, b, H, G, status, st);
-    case 128: return packed_simt<128>(q, k, v, o, pv, b, H, G, status, st);
+    case 16: return packed_simt<16>(a, st);
+    case 32: return packed_simt<32>(a, st);
+    case 64: return packed_simt<64>(a, st);
+    case 128: return packed_simt<128>(a, st);
   }
   return cudaErrorInvalidValue;
 }
 
 size_t paged_decode_simt_workspace_bytes(int n_seqs, int max_kv_len, int H, int G, int D) {
-  const DecodeSplit split = decode_split(n_seqs, max_kv_len, H, G);
-  return split.n > 1 ? (size_t)n_seqs * H * split.n * (D + 2) * sizeof(float) : 0;
+  const Split s = decode_split(n_seqs, max_kv_len, H, G);
+  return s.n > 1 ? (size_t)n_seqs * H * s.n * (D + 2) * sizeof(float) : 0;
 }
 
 cudaError_t launch_paged_decode_simt(const float *q, const float *k, const float *v, float *o, const PagedView &pv,
                                      const int *kv_lens, int n_seqs, int max_kv_len, int H, int G, int D, float *part,
                                      int *status, cudaStream_t st) {
+  DsArgs a;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.o = o;
+  a.part = part;
+  a.pv = pv;
+  a.kv_lens = kv_lens;
+  a.n_seqs = n_seqs;
+  a.max_kv_len = max_kv_len;
+  a.H = H;
+  a.G = G;
+  a.split = decode_split(n_seqs, max_kv_len, H, G);
+  a.status = status;
   switch (D) {
-    case 16: return decode_simt<16>(q, k, v, o, pv, kv_lens, n_seqs, max_kv_len, H, G, part, status, st);
-    case 32: return decode_simt<32>(q, k, v, o, pv, kv_lens, n_seqs, max_kv_len, H, G, part, status, st);
-    case 64: return decode_simt<64>(q, k, v, o, pv, kv_lens, n_seqs, max_kv_len, H, G, part, status, st);
-    case 128: return decode_simt<128>(q, k, v, o, pv, kv_lens, n_seqs, max_kv_len, H, G, part, status, st);
+    case 16: return decode_simt<16>(a, st);
+    case 32: return decode_simt<32>(a, st);
+    case 64: return decode_simt<64>(a, st);
+    case 128: return decode_simt<128>(a, st);
   }
   return cudaErrorInvalidValue;
 }
