@@ -14,7 +14,9 @@ namespace {
 
 constexpr int KEYS = 64;        // keys of a tile
 constexpr int THREADS = 256;
-constexpr int SM_CTAS = 4 * 152;  // CTAs that the splits aim at: four per SM
+// CTAs that the splits aim at: 16 per SM.  max_kv_len stands for every sequence, so in a
+// ragged batch most of them find no keys (16 against 4 per SM: 147 us for 266).
+constexpr int SM_CTAS = 16 * 152;
 
 // Split of the keys over CTAs: parts of `chunk` keys, `n` of them at the longest
 // length that the call allows.
@@ -258,28 +260,28 @@ __global__ void __launch_bounds__(THREADS) packed_simt_kernel(const __grid_const
   }
 }
 
-// Joins n parts, `step` floats apart, of one row of D floats (then m and l): one warp.
+// Joins the parts c0, c0 + by, ... below n, `step` floats apart, of one row of D floats
+// (then m and l): one warp, to its (m, l) and unscaled sums.
 template <int D>
-__device__ __forceinline__ void join_row(const float *p, size_t step, int n, float *o) {
-  constexpr int PER = D > 32 ? D / 32 : 1;
-  const int lane = threadIdx.x & 31;
+struct RowParts {
+  static constexpr int PER = D > 32 ? D / 32 : 1;
   float m = -INFINITY, l = 0.f, acc[PER];
+  __device__ __forceinline__ RowParts(const float *p, size_t step, int n, int c0, int by) {
+    const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int e = 0; e < PER; ++e) acc[e] = 0.f;
-  for (int c = lane; c < n; c += 32) m = fmaxf(m, p[c * step + D]);
-  m = warp_max(m);
+    for (int e = 0; e < PER; ++e) acc[e] = 0.f;
+    for (int c = c0 + by * lane; c < n; c += by * 32) m = fmaxf(m, p[c * step + D]);
+    m = warp_max(m);
 #pragma unroll 4
-  for (int c = 0; c < n; ++c) {
-    const float f = expf(p[c * step + D] - m);
-    l = fmaf(f, p[c * step + D + 1], l);
+    for (int c = c0; c < n; c += by) {
+      const float f = expf(p[c * step + D] - m);
+      l = fmaf(f, p[c * step + D + 1], l);
 #pragma unroll
-    for (int e = 0; e < PER; ++e)
-      if (lane + 32 * e < D) acc[e] = fmaf(f, p[c * step + lane + 32 * e], acc[e]);
+      for (int e = 0; e < PER; ++e)
+        if (lane + 32 * e < D) acc[e] = fmaf(f, p[c * step + lane + 32 * e], acc[e]);
+    }
   }
-#pragma unroll
-  for (int e = 0; e < PER; ++e)
-    if (lane + 32 * e < D) o[lane + 32 * e] = l > 0.f ? acc[e] / l : 0.f;
-}
+};
 
 template <int D>
 __global__ void __launch_bounds__(THREADS) packed_join_simt_kernel(const __grid_constant__ PsArgs a) {
@@ -291,14 +293,18 @@ __global__ void __launch_bounds__(THREADS) packed_join_simt_kernel(const __grid_
   const SeqSpan s = seq_span(a.b, a.pv, seq);
   const int n_keys = tile_keys(s, r, ((t - s.first) * r + hh) / ROWS * ROWS);
   if (n_keys <= a.split.chunk) return;
-  join_row<D>(a.part + row * (D + 2), (size_t)a.b.n_tokens * a.H * (D + 2), (n_keys + a.split.chunk - 1) / a.split.chunk,
-              a.o + row * D);
+  const RowParts<D> x(a.part + row * (D + 2), (size_t)a.b.n_tokens * a.H * (D + 2),
+                      (n_keys + a.split.chunk - 1) / a.split.chunk, 0, 1);
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int e = 0; e < RowParts<D>::PER; ++e)
+    if (lane + 32 * e < D) a.o[row * D + lane + 32 * e] = x.l > 0.f ? x.acc[e] / x.l : 0.f;
 }
 
 // every sequence ends in at most one tile that is not full
 long long packed_tiles(const PackedView &b, int H, int G) { return (long long)b.n_tokens * (H / G) / ROWS + b.n_seqs; }
 Split packed_split(const PackedView &b, int H, int G) {
-  return split_of(packed_tiles(b, H, G) * G, b.max_kv_len, 4 * KEYS);
+  return split_of(packed_tiles(b, H, G) * G, b.max_kv_len, 2 * KEYS);
 }
 
 template <int D>
@@ -464,17 +470,39 @@ __global__ void __launch_bounds__(THREADS) paged_decode_simt_kernel(const __grid
   }
 }
 
+// A CTA per row: the parts are many and the rows few, so its warps share them.
 template <int D>
 __global__ void __launch_bounds__(THREADS) decode_join_simt_kernel(const __grid_constant__ DsArgs a) {
-  const long long row = (long long)blockIdx.x * (THREADS / 32) + threadIdx.x / 32;  // sequence, head
-  if (row >= (long long)a.n_seqs * a.H) return;
+  constexpr int WARPS = THREADS / 32;
+  __shared__ float sm[WARPS], sl[WARPS], so[WARPS][D];
+  const int row = blockIdx.x, warp = threadIdx.x / 32, lane = threadIdx.x & 31;  // sequence, head
   const int len = checked_len(__ldg(a.kv_lens + row / a.H), a.max_kv_len, a.pv);
   if (len <= a.split.chunk) return;
-  join_row<D>(a.part + row * a.split.n * (D + 2), D + 2, (len + a.split.chunk - 1) / a.split.chunk, a.o + row * D);
+  const RowParts<D> x(a.part + (size_t)row * a.split.n * (D + 2), D + 2, (len + a.split.chunk - 1) / a.split.chunk,
+                      warp, WARPS);
+  if (lane == 0) {
+    sm[warp] = x.m;
+    sl[warp] = x.l;
+  }
+#pragma unroll
+  for (int e = 0; e < RowParts<D>::PER; ++e)
+    if (lane + 32 * e < D) so[warp][lane + 32 * e] = x.acc[e];
+  __syncthreads();
+  if (threadIdx.x >= D) return;
+  float m = -INFINITY, l = 0.f, o = 0.f;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) m = fmaxf(m, sm[w]);
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) {
+    const float f = expf(sm[w] - m);  // a warp without parts: e^-inf
+    l = fmaf(f, sl[w], l);
+    o = fmaf(f, so[w][threadIdx.x], o);
+  }
+  a.o[(size_t)row * D + threadIdx.x] = o / l;
 }
 
 Split decode_split(int n_seqs, int max_kv_len, int H, int G) {
-  return split_of((long long)n_seqs * G * ((H / G + HEADS - 1) / HEADS), max_kv_len, 2 * KEYS);
+  return split_of((long long)n_seqs * G * ((H / G + HEADS - 1) / HEADS), max_kv_len, KEYS);
 }
 
 template <int D>
@@ -494,7 +522,7 @@ cudaError_t decode_simt(DsArgs a, cudaStream_t st) {
   const cudaError_t r = cudaGetLastError();
   if (r != cudaSuccess || a.split.n == 1) return r;
   count_launch();
-  decode_join_simt_kernel<D><<<(unsigned)((rows + THREADS / 32 - 1) / (THREADS / 32)), THREADS, 0, st>>>(a);
+  decode_join_simt_kernel<D><<<(unsigned)rows, THREADS, 0, st>>>(a);
   return cudaGetLastError();
 }
 
