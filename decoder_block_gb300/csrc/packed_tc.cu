@@ -11,11 +11,14 @@
 // K/V tile in shared memory serves the whole group.  Keys and values arrive page by
 // page: one box per page (at most 128 rows) and 64 columns, in the 128-byte swizzle
 // the MMAs read, so a tile is the same whatever the page size (at S = 8192 pages of 16
-// and of 256 take the same time).  Rows behind the sequence's last key may hold
+// and of 256 differ by 5 %).  Rows behind the sequence's last key may hold
 // anything: their scores are replaced, not added to, and the V rows are cleared in
 // shared memory before the product reads them (0 * NaN is not 0).
-//   warp 0      takes items, loads Q, then K and V tiles into two-stage rings;
-//               each lane issues one page's box and holds the next tile's id
+//   warp 0      takes items, loads Q, then V and the next K tiles into two-stage rings;
+//               each lane issues one page's box and holds the next tile's id.  Lanes
+//               issue one after another (about 65 ns each), so the 32 boxes that pages
+//               of 16 rows make of a stage are issued by four more warps (S = 8192:
+//               388 us for 456); larger pages do better without them (366 us for 373)
 //   warp 1      one thread issues S_t = Q_t K^T and O_t += P_t V (fp32 in tensor
 //               memory, P from tensor memory)
 //   warps 2-9   softmax of tile 0 / 1, one thread per row; the output
@@ -57,7 +60,8 @@ struct PtLayout {
   static constexpr int OFF_ITEM = OFF_V + PT_STAGES * TILE;  // PtItem
   static constexpr int OFF_BAR = OFF_ITEM + 64;
   // q_full, q_empty, fin, kv_full[2], kv_empty[2], s_full[2], p_full[2], o_done[2]
-  static constexpr int NBAR = 3 + 2 * PT_STAGES + 6;
+  // i_full, near_end (16-row pages)
+  static constexpr int NBAR = 3 + 2 * PT_STAGES + 6 + 2;
   static constexpr int BYTES_MIN = 1024 + OFF_BAR + NBAR * 8 + 16;
   // one CTA per SM: two would need all of tensor memory each
   static constexpr int BYTES = BYTES_MIN > 116 * 1024 ? BYTES_MIN : 116 * 1024;
@@ -288,9 +292,73 @@ __global__ void __launch_bounds__(PT_PLAN_THREADS) packed_plan_kernel(PagedView 
   if (tid == 0) plan->n_split = n_split;
 }
 
+// ----------------------------------------------------------------- loads ---
+// One warp's part of filling stage jj % 2 with V of key tile j and K of tile j + 1 (when
+// the item has it).  A tile comes in boxes of a page's rows (at most 128) and 64 columns;
+// the WARPS warps' lanes share the stage's 16 boxes of V and 16 of K at most.
+template <int D, int WARPS>
+struct StageLoads {
+  using L = PtLayout<D>;
+  static constexpr int ATOMS = D / 64, MINE = 32 / WARPS;
+  const PtArgs &a;
+  const CUtensorMap *map;
+  uint32_t dst;
+  int box, at, ahead;  // this lane's box and 64-column atom; 1: of K, one tile ahead
+  int page = -1;       // of this lane's box in the coming stage
+
+  __device__ __forceinline__ StageLoads(const PtArgs &args, const CUtensorMap *tmK, const CUtensorMap *tmV,
+                                        uint32_t smem, int warp)
+      : a(args) {
+    const int lane = threadIdx.x & 31, slot = warp * MINE + lane;
+    ahead = slot >= 16 ? 1 : 0;
+    map = ahead ? tmK : tmV;
+    box = lane < MINE ? (slot & 15) / ATOMS : PT_KEYS;  // past the tile: no box
+    at = (slot & 15) % ATOMS;
+    dst = smem + (ahead ? L::OFF_K : L::OFF_V) + at * L::ATOM + box * a.box * 128;
+  }
+  __device__ __forceinline__ int boxes_of(const PtItem &it, int j) const {
+    return j < it.j1 ? min(PT_KEYS / a.box, (it.kv_len - j * PT_KEYS + a.box - 1) / a.box) : 0;
+  }
+  __device__ __forceinline__ uint32_t bytes(const PtItem &it, int j) const {
+    return boxes_of(it, j) * a.box * 128u * ATOMS;
+  }
+  // First row of a tile's boxes in their pages.
+  __device__ __forceinline__ int row_of(int j) const {
+    return (j * PT_KEYS) & ((1 << a.pv.page_log2) - 1) & ~(a.box - 1);
+  }
+  // Page of a box of tile j: its id, n_pages (a page of zeros) when the id is out of
+  // range, -1 when the tile has no such box.
+  __device__ __forceinline__ int page_of(const PtItem &it, int j, int b) const {
+    if (b >= boxes_of(it, j)) return -1;
+    const int id = a.pv.page(it.seq, (j * PT_KEYS + b * a.box) >> a.pv.page_log2);
+    if (id < 0) report_status(a.status, LLAMA_ERR_RANGE);
+    return id < 0 ? a.pv.n_pages : id;
+  }
+  __device__ __forceinline__ void begin(const PtItem &it) { page = page_of(it, it.j0 + ahead, box); }
+  // The page for tile j's stage; looks the next stage's up.
+  __device__ __forceinline__ int advance(const PtItem &it, int j) {
+    const int now = page;
+    page = page_of(it, j + 1 + ahead, box);
+    return now;
+  }
+  // Parity of kv_empty to wait for before stage jj is filled.  Stage 1 is released once
+  // more than it was filled: its first K overwrites no earlier stage's but the first
+  // item's first tile.
+  __device__ __forceinline__ uint32_t parity(int jj) const {
+    return ((jj / PT_STAGES) & 1) ^ (jj % PT_STAGES == 0 ? 1 : 0);
+  }
+  __device__ __forceinline__ void issue(const PtItem &it, int j, int jj, int pg, uint32_t bar, bool expect) const {
+    if (expect && (threadIdx.x & 31) == 0) ptx::mbar_arrive_expect_tx(bar, bytes(it, j) + bytes(it, j + 1));
+    __syncwarp();
+    if (pg >= 0)
+      ptx::tma_load_4d(dst + ((jj + ahead) % PT_STAGES) * L::TILE, map, at * 64, row_of(j + ahead), it.g, pg, bar);
+  }
+};
+
 // ------------------------------------------------------------- attention ---
-template <int D>
-__global__ void __launch_bounds__(PT_THREADS, 1)
+// ISSUERS: warps from PT_THREADS on that load the stages (0: warp 0 does).
+template <int D, int ISSUERS>
+__global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
     packed_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PtArgs a) {
   using L = PtLayout<D>;
@@ -313,6 +381,9 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
   auto p_full = [&](int t) { return bar0 + 8u * (5 + 2 * PT_STAGES + t); };
   auto o_done = [&](int t) { return bar0 + 8u * (7 + 2 * PT_STAGES + t); };
 
+  // with issuers: an item has been handed over; their loads have come to its last tile
+  const uint32_t i_full = bar0 + 8u * (9 + 2 * PT_STAGES), near_end = i_full + 8;
+
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
     if (ptx::mbar_wait(bar, parity, abort_flag, nullptr, 0)) return true;
@@ -323,7 +394,10 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
 
   if (threadIdx.x == 0) {
     ptx::mbar_init(q_full, 1);
-    ptx::mbar_init(q_empty, 9);  // the MMAs reading Q are done; each softmax warp has read the item
+    // the MMAs reading Q are done; each softmax and issuing warp has read the item
+    ptx::mbar_init(q_empty, 9 + ISSUERS);
+    ptx::mbar_init(i_full, 1);
+    ptx::mbar_init(near_end, 1);
     ptx::mbar_init(fin, 1);
     for (int s = 0; s < PT_STAGES; ++s) {
       ptx::mbar_init(kv_full(s), 1);
@@ -338,7 +412,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
     ptx::fence_mbar_init();
   }
   // Query rows behind rb * Mq are never loaded: zero them.
-  if (warp >= 2 && a.rb * a.Mq < 128) {
+  if (warp >= 2 && warp < 10 && a.rb * a.Mq < 128) {
     const int first = a.rb * a.Mq;
     for (int t = 0; t < 2; ++t)
       for (int at = 0; at < ATOMS; ++at) {
@@ -424,38 +498,20 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
       }
       return it;
     };
-    const int boxes_tile = PT_KEYS / a.box;  // pages of a tile (1 when pages are larger)
-    const bool is_k = lane >= 16;            // lanes 0-15 load V, 16-31 the next tile's K
-    const int my_box = (lane & 15) / ATOMS, my_at = (lane & 15) % ATOMS;
-    const uint32_t dst = s0 + (is_k ? L::OFF_K : L::OFF_V) + my_at * L::ATOM + my_box * a.box * 128;
-    const CUtensorMap *map = is_k ? &tmK : &tmV;
-    auto boxes = [&](const PtItem &it, int j) {  // of tile j
-      return j < it.j1 ? min(boxes_tile, (it.kv_len - j * PT_KEYS + a.box - 1) / a.box) : 0;
-    };
-    const uint32_t box_bytes = a.box * 128u * ATOMS;
-    // Page of this lane's box of key tile j: its id, n_pages (a page of zeros) when
-    // the id is out of range, -1 when the tile has no such box.
-    auto page_of = [&](const PtItem &it, int j) {
-      if (my_box >= boxes(it, j)) return -1;
-      const int id = a.pv.page(it.seq, (j * PT_KEYS + my_box * a.box) >> a.pv.page_log2);
-      if (id < 0) report_status(a.status, LLAMA_ERR_RANGE);
-      return id < 0 ? a.pv.n_pages : id;
-    };
-    auto load = [&](const PtItem &it, int page, int j, int jj, uint32_t bar) {  // this lane's box of tile j
-      if (page < 0) return;
-      const int r = (j * PT_KEYS) & ((1 << a.pv.page_log2) - 1) & ~(a.box - 1);
-      ptx::tma_load_4d(dst + (jj % PT_STAGES) * L::TILE, map, my_at * 64, r, it.g, page, bar);
-    };
-    int items = 0, tiles = 0;  // Q loads and stages issued
+    StageLoads<D, 1> loads(a, &tmK, &tmV, s0, 0);
+    const int my_box = lane / ATOMS, my_at = lane % ATOMS;  // this lane's box of an item's first K
+    int items = 0, tiles = 0;  // Q loads issued; key tiles of earlier items and of this one
     bool ended = false;        // the end was handed over: the last Q has landed
     bool ok = true;
     PtItem it = fetch(0);
     for (int k = 0; ok; ++k) {
-      // V lanes hold the page of their box of tile j, K lanes that of tile j + 1
-      int page = it.seq >= 0 ? page_of(it, it.j0 + (is_k ? 1 : 0)) : -1;
-      const int first_page = it.seq >= 0 && is_k ? page_of(it, it.j0) : -1;
+      const int first_page = it.seq >= 0 ? loads.page_of(it, it.j0, my_box) : -1;
+      if (ISSUERS == 0 && it.seq >= 0) loads.begin(it);
       if (k > 0 && !wait_warp(q_empty, (k - 1) & 1)) break;
-      if (lane == 0) *item_slot = it;  // published by the q_full arrival
+      if (lane == 0) {
+        *item_slot = it;  // published by the arrivals
+        if (ISSUERS > 0) ptx::mbar_arrive(i_full);
+      }
       __syncwarp();
       if (it.seq < 0) {
         if (lane == 0) ptx::mbar_arrive(q_full);
@@ -464,37 +520,38 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
       }
       const int n_t = it.q0 + a.Mq < it.count ? 2 : 1;  // query tiles that hold rows
       if (lane == 0) {
-        ptx::mbar_arrive_expect_tx(q_full, n_t * ATOMS * a.rb * a.Mq * 128u + boxes(it, it.j0) * box_bytes);
+        ptx::mbar_arrive_expect_tx(q_full, n_t * ATOMS * a.rb * a.Mq * 128u + loads.bytes(it, it.j0));
         for (int t = 0; t < n_t; ++t)
           for (int at = 0; at < ATOMS; ++at)
             ptx::tma_load_3d(s0 + L::OFF_Q + t * L::TILE + at * L::ATOM, &tmQ, at * 64, it.h0,
                              it.first + it.q0 + t * a.Mq, q_full);
       }
       __syncwarp();
-      load(it, first_page, it.j0, tiles, q_full);
+      if (first_page >= 0)
+        ptx::tma_load_4d(s0 + L::OFF_K + (tiles % PT_STAGES) * L::TILE + my_at * L::ATOM + my_box * a.box * 128, &tmK,
+                         my_at * 64, loads.row_of(it.j0), it.g, first_page, q_full);
       ++items;
+      // The next item's look-ups are hidden behind the last tiles of this one; any earlier and
+      // items are dealt out before it shows which CTAs run late (S = 2048: 58 us for 39).
+      if (ISSUERS > 0) {
+        if (!wait_warp(near_end, k & 1)) break;
+        tiles += max(0, it.j1 - it.j0);
+        it = fetch(k + 1);
+        continue;
+      }
       PtItem next;
       bool fetched = false;
-      for (int j = it.j0; j < it.j1; ++j) {
-        // The next item's look-ups, hidden behind the last tiles of this one; any earlier and
-        // items are dealt out before it shows which CTAs run late (S = 2048: 58 us for 39).
+      for (int j = it.j0; j < it.j1; ++j, ++tiles) {
         if (j + 1 == it.j1) {
           next = fetch(k + 1);
           fetched = true;
         }
-        const int st = tiles % PT_STAGES;
-        const int page_now = page;
-        page = page_of(it, j + 1 + (is_k ? 1 : 0));
-        // Stage 1 is released once more than it was filled: its first K overwrites no earlier
-        // stage's but the first item's first tile.
-        if (!wait_warp(kv_empty(st), ((tiles / PT_STAGES) & 1) ^ (st == 0 ? 1 : 0))) {
+        const int page = loads.advance(it, j);
+        if (!wait_warp(kv_empty(tiles % PT_STAGES), loads.parity(tiles))) {
           ok = false;
           break;
         }
-        if (lane == 0) ptx::mbar_arrive_expect_tx(kv_full(st), (boxes(it, j) + boxes(it, j + 1)) * box_bytes);
-        __syncwarp();
-        load(it, page_now, j + (is_k ? 1 : 0), tiles + (is_k ? 1 : 0), kv_full(st));
-        ++tiles;
+        loads.issue(it, j, tiles, page, kv_full(tiles % PT_STAGES), true);
       }
       if (!ok) break;
       if (!fetched) next = fetch(k + 1);
@@ -504,8 +561,9 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
     __syncwarp();
     if (lane == 0) {
       if (items > 0 && !ended) ptx::mbar_drain(q_full, (items - 1) & 1, nullptr, 0);
-      for (int j = max(0, tiles - PT_STAGES); j < tiles; ++j)
-        ptx::mbar_drain(kv_full(j % PT_STAGES), (j / PT_STAGES) & 1, nullptr, 0);
+      if (ISSUERS == 0)
+        for (int j = max(0, tiles - PT_STAGES); j < tiles; ++j)
+          ptx::mbar_drain(kv_full(j % PT_STAGES), (j / PT_STAGES) & 1, nullptr, 0);
     }
   } else if (warp == 1) {
     // --------------------------------------------------------------- MMA ---
@@ -538,7 +596,7 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
       // overlaps that of tile 1, and the next item's first S products the output of this one.
       bool ok = true;
       int jg = 0, n0 = 0, n1 = 0;  // key tiles over all items: of the ring, of query tiles 0 and 1
-      int owed = 1;                // stage whose release is still to come (1: see the producer)
+      int owed = 1;                // stage whose release is still to come (1: see StageLoads)
       static_assert(PT_STAGES == 2, "K of tile jj + 1 lies in the other stage");
       for (int k = 0; ok; ++k) {
         if (!wait(q_full, k & 1)) break;
@@ -598,6 +656,33 @@ __global__ void __launch_bounds__(PT_THREADS, 1)
       ptx::mma_commit(fin);
       ptx::mbar_drain(fin, 0, nullptr, 0);
     }
+  } else if (ISSUERS > 0 && warp >= 10) {
+    // ------------------------------------------------------------ issuers ---
+    StageLoads<D, ISSUERS == 0 ? 1 : ISSUERS> loads(a, &tmK, &tmV, s0, warp - 10);
+    int tiles = 0;
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      if (!wait_warp(i_full, k & 1)) break;
+      const PtItem it = *item_slot;
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(q_empty);
+      if (it.seq < 0) break;
+      if (it.j0 >= it.j1 && warp == 10 && lane == 0) ptx::mbar_arrive(near_end);
+      loads.begin(it);
+      for (int j = it.j0; j < it.j1; ++j, ++tiles) {
+        const int page = loads.advance(it, j);
+        if (!wait_warp(kv_empty(tiles % PT_STAGES), loads.parity(tiles))) {
+          ok = false;
+          break;
+        }
+        if (j + 1 == it.j1 && warp == 10 && lane == 0) ptx::mbar_arrive(near_end);
+        loads.issue(it, j, tiles, page, kv_full(tiles % PT_STAGES), warp == 10);
+      }
+    }
+    __syncwarp();
+    if (warp == 10 && lane == 0)
+      for (int j = max(0, tiles - PT_STAGES); j < tiles; ++j)
+        ptx::mbar_drain(kv_full(j % PT_STAGES), (j / PT_STAGES) & 1, nullptr, 0);
   } else {
     // ----------------------------------------------------------- softmax ---
     const int t = (warp - 2) / 4;
@@ -926,7 +1011,10 @@ cudaError_t launch_tc(const bf16 *q, const bf16 *k, const bf16 *v, bf16 *o, cons
   using L = PtLayout<D>;
   static PerContextOnce attr;
   cudaError_t e = attr.run([] {
-    return cudaFuncSetAttribute(packed_tc_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
+    const cudaError_t e =
+        cudaFuncSetAttribute(packed_tc_kernel<D, 0>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(packed_tc_kernel<D, 4>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
   });
   if (e != cudaSuccess) return e;
   const int sms = sm_count();
@@ -952,9 +1040,11 @@ cudaError_t launch_tc(const bf16 *q, const bf16 *k, const bf16 *v, bf16 *o, cons
   if (!make_heads_map(&mq, q, b.n_tokens, H, width, a.rb, a.Mq) || !make_paged_map(&mk, k, pv, G, width, a.box) ||
       !make_paged_map(&mv, v, pv, G, width, a.box))
     return cudaErrorInvalidValue;
+  auto kernel = a.box == 16 ? packed_tc_kernel<D, 4> : packed_tc_kernel<D, 0>;
+  const dim3 threads(PT_THREADS + (a.box == 16 ? 128 : 0));
   if (z.bytes == 0) {
     count_launch();
-    return launch_pdl(packed_tc_kernel<D>, dim3((unsigned)(z.max_blocks * z.units)), dim3(PT_THREADS), L::BYTES, st, mq,
+    return launch_pdl(kernel, dim3((unsigned)(z.max_blocks * z.units)), threads, L::BYTES, st, mq,
                       mk, mv, a);
   }
   char *w = reinterpret_cast<char *>(workspace);
@@ -968,7 +1058,7 @@ cudaError_t launch_tc(const bf16 *q, const bf16 *k, const bf16 *v, bf16 *o, cons
   if (e != cudaSuccess) return e;
   const long long items = z.max_entries * z.units;
   count_launch();
-  e = launch_pdl(packed_tc_kernel<D>, dim3((unsigned)(items < sms ? items : sms)), dim3(PT_THREADS), L::BYTES, st, mq,
+  e = launch_pdl(kernel, dim3((unsigned)(items < sms ? items : sms)), threads, L::BYTES, st, mq,
                  mk, mv, a);
   if (e != cudaSuccess) return e;
   count_launch();
