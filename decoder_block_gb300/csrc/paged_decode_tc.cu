@@ -11,10 +11,13 @@
 // fp32 over one pass.  Pages arrive as TMA boxes of their own, so a tile in shared
 // memory is the same whatever the page size; V rows behind the last key, which
 // may hold anything, are cleared in shared memory (0 * NaN is not 0).
-//   warp 0     takes items, loads Q, K and V; each lane issues one box of K or V
-//              and holds the next tile's page id
+//   warp 0     takes items and loads Q
 //   warp 1     one thread issues the MMAs
 //   warps 2-5  softmax, one thread per key; the output, one thread per column
+//   warps 6-9  load K and V: each lane issues one box and holds the next tile's page id.
+//              Lanes of a warp issue one after another, about 65 ns each, and pages of 16
+//              rows make 32 boxes of a tile (64 sequences over such pages: 127 us from
+//              one warp, 96 from four; pages of 64: 96 and 94)
 // The keys of a sequence are split over CTAs and joined, o = sum 2^(m_c - M) o_c /
 // sum 2^(m_c - M) l_c, in one of two ways:
 //   * direct (few sequences, or short ones): a cluster of 1 to 8 CTAs shares a
@@ -36,7 +39,8 @@ namespace {
 
 constexpr int PD_KEYS = 128;    // keys of a tile
 constexpr int PD_N = 16;        // head columns of a tile
-constexpr int PD_THREADS = 192;
+constexpr int PD_LOADERS = 4;   // warps that load K and V
+constexpr int PD_THREADS = 192 + PD_LOADERS * 32;
 constexpr float PD_RESCALE = 8.0f;
 constexpr int PD_MAX_CLUSTER = 8;
 constexpr int PD_DIRECT_TILES = 8;  // key tiles of a CTA in the direct form, at most
@@ -61,7 +65,7 @@ struct PdLayout {
   static constexpr int OFF_RED = OFF_P + 2 * P_BYTES;           // [4][4 warps][PD_N] floats
   static constexpr int OFF_ITEM = OFF_RED + 4 * 4 * PD_N * 4;   // 2 items
   static constexpr int OFF_BAR = OFF_ITEM + 2 * 32;
-  static constexpr int NBAR = 2 * STAGES + 18;
+  static constexpr int NBAR = 2 * STAGES + 18 + 3;
   static constexpr int END = OFF_BAR + NBAR * 8 + 16;
   static constexpr int BYTES = 1024 + (END > OFF_Q + ATOM ? END : OFF_Q + ATOM);
   static constexpr uint32_t TMEM_COLS = 64;  // S^T x2, O^T x2, 16 columns each
@@ -184,6 +188,59 @@ __global__ void __launch_bounds__(PD_PLAN_THREADS) decode_plan_kernel(PagedView 
   }
 }
 
+// ----------------------------------------------------------------- loads ---
+// One warp's part of filling a stage with K and V of a key tile, in boxes of a page's
+// rows (at most 128) and 64 columns; the loading warps' lanes share the 16 boxes of K and
+// 16 of V at most.
+template <int D>
+struct TileLoads {
+  using L = PdLayout<D>;
+  static constexpr int ATOMS = L::ATOMS, MINE = 32 / PD_LOADERS;
+  const PdArgs &a;
+  const CUtensorMap *map;
+  uint32_t dst;
+  uint64_t once = ptx::policy_evict_first();  // each cached key is read once per call
+  int box, at;    // this lane's box and 64-column atom
+  int page = -1;  // of this lane's box in the coming tile
+
+  __device__ __forceinline__ TileLoads(const PdArgs &args, const CUtensorMap *tmK, const CUtensorMap *tmV,
+                                       uint32_t smem, int warp)
+      : a(args) {
+    const int lane = threadIdx.x & 31, slot = warp * MINE + lane;
+    map = slot < 16 ? tmK : tmV;
+    box = lane < MINE ? (slot & 15) / ATOMS : PD_KEYS;  // past the tile: no box
+    at = (slot & 15) % ATOMS;
+    dst = smem + (slot < 16 ? L::OFF_K : L::OFF_V) + at * L::ATOM + box * a.box * 128;
+  }
+  __device__ __forceinline__ int boxes_of(const PdItem &it, int j) const {
+    return j < it.j1 ? min(PD_KEYS / a.box, (it.len - j * PD_KEYS + a.box - 1) / a.box) : 0;
+  }
+  // Page of this lane's box of key tile j: its id, n_pages (a page of zeros) when the id is
+  // out of range, -1 when the tile has no such box.
+  __device__ __forceinline__ void look_up(const PdItem &it, int j) {
+    page = -1;
+    if (box >= boxes_of(it, j)) return;
+    page = a.pv.page(it.seq, (j * PD_KEYS + box * a.box) >> a.pv.page_log2);
+    if (page < 0) {
+      report_status(a.status, LLAMA_ERR_RANGE);
+      page = a.pv.n_pages;
+    }
+  }
+  // The page for tile j; looks the next tile's up.
+  __device__ __forceinline__ int advance(const PdItem &it, int j) {
+    const int now = page;
+    look_up(it, j + 1);
+    return now;
+  }
+  __device__ __forceinline__ void issue(const PdItem &it, int j, int stage, int pg, uint32_t bar, bool expect) const {
+    if (expect && (threadIdx.x & 31) == 0)
+      ptx::mbar_arrive_expect_tx(bar, 2u * boxes_of(it, j) * ATOMS * a.box * 128u);
+    __syncwarp();
+    const int row = (j * PD_KEYS) & ((1 << a.pv.page_log2) - 1) & ~(a.box - 1);
+    if (pg >= 0) ptx::tma_load_4d_hint(dst + stage * L::TILE, map, at * 64, row, it.g, pg, bar, once);
+  }
+};
+
 // ------------------------------------------------------------- attention ---
 // RN: head columns the softmax works on, the smallest of 2, 4, 8, 16 that holds
 // the block's heads; P^T rows RN .. 15 stay zero.
@@ -215,6 +272,9 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
   const uint32_t fin = b0 + 8u * (2 * STAGES + 14);
   auto red_full = [&](int i) { return b0 + 8u * (2 * STAGES + 15 + i); };
   const uint32_t lred_full = b0 + 8u * (2 * STAGES + 17);
+  // an item has been handed over; the loads have come to its last tile
+  auto i_full = [&](int i) { return b0 + 8u * (2 * STAGES + 18 + i); };
+  const uint32_t near_end = b0 + 8u * (2 * STAGES + 20);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
@@ -231,7 +291,9 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
     }
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(q_full(i), 1);
-      ptx::mbar_init(q_empty(i), 5);  // the MMAs reading Q are done; each softmax warp has read the item
+      // the MMAs reading Q are done; each softmax and loading warp has read the item
+      ptx::mbar_init(q_empty(i), 5 + PD_LOADERS);
+      ptx::mbar_init(i_full(i), 1);
       ptx::mbar_init(s_full(i), 1);
       ptx::mbar_init(p_full(i), 128);
       ptx::mbar_init(p_free(i), 1);
@@ -241,10 +303,11 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
     }
     ptx::mbar_init(fin, 1);
     ptx::mbar_init(lred_full, 4);
+    ptx::mbar_init(near_end, 1);
     *abort_flag = 0;
     ptx::fence_mbar_init();
   }
-  if (RN < PD_N && warp >= 2) {  // P^T rows the softmax never writes
+  if (RN < PD_N && warp >= 2 && warp < 6) {  // P^T rows the softmax never writes
     uint4 *pz = reinterpret_cast<uint4 *>(smem + L::OFF_P);
     for (int i = threadIdx.x - 64; i < 2 * L::P_BYTES / 16; i += 128) pz[i] = make_uint4(0, 0, 0, 0);
     ptx::fence_proxy_async_smem();
@@ -306,78 +369,38 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
       }
       return it;
     };
-    const int boxes_tile = PD_KEYS / a.box;  // pages of a tile (1 when pages are larger)
-    const bool is_v = lane >= 16;            // lanes 0-15 load K, 16-31 V
-    const int my_box = (lane & 15) / ATOMS, my_at = (lane & 15) % ATOMS;
-    const uint32_t dst = (is_v ? L::OFF_V : L::OFF_K) + my_at * L::ATOM + my_box * a.box * 128;
-    const CUtensorMap *map = is_v ? &tmV : &tmK;
-    const uint64_t once = ptx::policy_evict_first();  // each cached key is read once per call
-    // Page of this lane's box of key tile j: its id, n_pages (a page of zeros) when
-    // the id is out of range, -1 when the tile has no such box.
-    auto page_of = [&](const PdItem &it, int j) {
-      const int key = j * PD_KEYS + my_box * a.box;
-      if (my_box >= boxes_tile || j >= it.j1 || key >= it.len) return -1;
-      const int id = a.pv.page(it.seq, key >> a.pv.page_log2);
-      if (id < 0) report_status(a.status, LLAMA_ERR_RANGE);
-      return id < 0 ? a.pv.n_pages : id;
-    };
-    int tile = 0, items = 0;
-    bool ended = false, ok = true;
+    int items = 0;
+    bool ended = false;
     PdItem it = fetch(0);
-    for (int nq = 0; ok; ++nq) {
+    for (int nq = 0;; ++nq) {
       const int qi = nq & 1;
-      int page = it.seq >= 0 ? page_of(it, it.j0) : -1;
       if (!wait_warp(q_empty(qi), ((nq >> 1) & 1) ^ 1)) break;
-      if (lane == 0) item_slot[qi] = it;  // published by the q_full arrival
-      __syncwarp();
-      if (it.seq < 0) {
-        if (lane == 0) ptx::mbar_arrive(q_full(qi));
-        ended = true;
-        break;
-      }
       if (lane == 0) {
-        ptx::mbar_arrive_expect_tx(q_full(qi), L::Q_BYTES);
-        for (int at = 0; at < ATOMS; ++at)
-          ptx::tma_load_3d(s0 + L::OFF_Q + qi * L::Q_BYTES + at * (PD_N * 128), &tmQ, at * 64, it.h0, it.seq,
-                           q_full(qi));
-      }
-      ++items;
-      PdItem next;
-      bool fetched = false;
-      for (int j = it.j0; j < it.j1; ++j, ++tile) {
-        const int st = tile % STAGES;
-        const int boxes = min(boxes_tile, (it.len - j * PD_KEYS + a.box - 1) / a.box);
-        const int row = (j * PD_KEYS) & ((1 << a.pv.page_log2) - 1) & ~(a.box - 1);
-        const int page_now = page;
-        if (j + 1 < it.j1) {
-          page = page_of(it, j + 1);
+        item_slot[qi] = it;  // published by the arrivals
+        ptx::mbar_arrive(i_full(qi));
+        if (it.seq < 0) {
+          ptx::mbar_arrive(q_full(qi));
         } else {
-          next = fetch(nq + 1);
-          fetched = true;
+          ptx::mbar_arrive_expect_tx(q_full(qi), L::Q_BYTES);
+          for (int at = 0; at < ATOMS; ++at)
+            ptx::tma_load_3d(s0 + L::OFF_Q + qi * L::Q_BYTES + at * (PD_N * 128), &tmQ, at * 64, it.h0, it.seq,
+                             q_full(qi));
         }
-        if (!wait_warp(kv_empty(st), ((tile / STAGES) & 1) ^ 1)) {
-          ok = false;
-          break;
-        }
-        if (lane == 0) ptx::mbar_arrive_expect_tx(kv_full(st), 2u * boxes * ATOMS * a.box * 128u);
-        __syncwarp();
-        if (page_now >= 0)
-          ptx::tma_load_4d_hint(s0 + dst + st * L::TILE, map, my_at * 64, row, it.g, page_now, kv_full(st), once);
       }
-      if (!ok) break;
-      if (!fetched) next = fetch(nq + 1);
-      it = next;
+      __syncwarp();
+      ended = it.seq < 0;
+      if (ended) break;
+      ++items;
+      // the next item's look-ups hide behind the last tile of this one
+      if (!wait_warp(near_end, nq & 1)) break;
+      it = fetch(nq + 1);
     }
-    // every issued copy lands before the CTA exits
-    __syncwarp();
-    if (lane == 0) {
-      for (int t = max(0, tile - STAGES); t < tile; ++t)
-        ptx::mbar_drain(kv_full(t % STAGES), (t / STAGES) & 1, nullptr, 0);
-      // the last Q load's phase is the newest of its barrier unless the end was handed
-      // over there; the MMA thread waited for the one before it
+    // Every issued copy lands before the CTA exits.  The last Q load's phase is the newest
+    // of its barrier unless the end was handed over there; the MMA thread waited for the
+    // one before it.
+    if (lane == 0)
       for (int q = max(0, items - 2); q < items; ++q)
         if (!(ended && (items & 1) == (q & 1))) ptx::mbar_drain(q_full(q & 1), (q >> 1) & 1, nullptr, 0);
-    }
   } else if (warp == 1) {
     // --------------------------------------------------------------- MMA ---
     if (lane == 0) {
@@ -441,6 +464,35 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
       ptx::mma_commit(fin);
       ptx::mbar_drain(fin, 0, nullptr, 0);
     }
+  } else if (warp >= 6) {
+    // ------------------------------------------------------------- K and V ---
+    TileLoads<D> loads(a, &tmK, &tmV, s0, warp - 6);
+    int tile = 0;
+    bool ok = true;
+    for (int nq = 0; ok; ++nq) {
+      const int qi = nq & 1;
+      if (!wait_warp(i_full(qi), (nq >> 1) & 1)) break;
+      const PdItem it = item_slot[qi];
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(q_empty(qi));
+      if (it.seq < 0) break;
+      if (it.j0 >= it.j1 && warp == 6 && lane == 0) ptx::mbar_arrive(near_end);
+      loads.look_up(it, it.j0);
+      for (int j = it.j0; j < it.j1; ++j, ++tile) {
+        const int st = tile % STAGES;
+        const int page = loads.advance(it, j);
+        if (j + 1 == it.j1 && warp == 6 && lane == 0) ptx::mbar_arrive(near_end);
+        if (!wait_warp(kv_empty(st), ((tile / STAGES) & 1) ^ 1)) {
+          ok = false;
+          break;
+        }
+        loads.issue(it, j, st, page, kv_full(st), warp == 6);
+      }
+    }
+    __syncwarp();
+    if (warp == 6 && lane == 0)  // every issued copy lands before the CTA exits
+      for (int t = max(0, tile - STAGES); t < tile; ++t)
+        ptx::mbar_drain(kv_full(t % STAGES), (t / STAGES) & 1, nullptr, 0);
   } else {
     // --------------------------------------------------- softmax, output ---
     const int w4 = warp - 2;
