@@ -583,14 +583,14 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
         }
         ptx::mma_commit(s_full(t));
       };
-      auto issue_pv = [&](int jj, bool first, int t) {
+      auto issue_pv = [&](int jj, bool first, bool last, int t) {
         const uint32_t vb = v_lo + (jj % PT_STAGES) * (L::TILE >> 4);
         const uint32_t d = tmem + 256 + t * D, p = tmem + t * 128;
         pt_mma_ts<-1>(d, p, vb, idesc_pv, first ? 0u : 1u);
 #pragma unroll
         for (int kk = 1; kk < PT_KEYS / 16; ++kk)  // 16 keys: two 8-row groups
           pt_mma_ts<1>(d, p + kk * 8, vb + kk * (16 * 128 >> 4), idesc_pv, 1u);
-        ptx::mma_commit(o_done(t));
+        if (last) ptx::mma_commit(o_done(t));
       };
       // S_0(j+1) goes out right after PV_0(j): the softmax of tile 0 for the next keys
       // overlaps that of tile 1, and the next item's first S products the output of this one.
@@ -622,7 +622,7 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
             if (!wait(p_full(0), n0 & 1)) return false;
             ++n0;
             ptx::tc_fence_after();
-            issue_pv(jj, i == 0, 0);
+            issue_pv(jj, i == 0, !s0, 0);
           }
           if (s0) {
             ptx::tc_fence_after();
@@ -632,7 +632,7 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
             if (!wait(p_full(1), n1 & 1)) return false;
             ++n1;
             ptx::tc_fence_after();
-            issue_pv(jj, i == 0, 1);
+            issue_pv(jj, i == 0, !s1, 1);
           }
           if (s1) issue_s(jj + 1, 1);
           // The stage may be filled again when the next tile's K has been used too; behind an
@@ -697,6 +697,7 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
       for (int u = threadIdx.x - 64; u < a.b.n_seqs; u += PT_THREADS - 64) check_seq(a.b, a.pv, u, a.status);
     bool ok = true;
     int jg = 0, jt = 0;  // key tiles of earlier items: of the ring, of this query tile
+    int outputs = 0;     // items that this query tile worked on
     for (int k = 0; ok; ++k) {
       if (!wait_warp(q_full, k & 1)) break;
       const PtItem it = *item_slot;
@@ -807,12 +808,8 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
           ptx::tmem_st16(s_col + c / 2, pk);
         }
         if (jl > 0 && rescaled) {
-          // O holds the earlier key tiles: after the last product into it, scale it
-          if (!wait_warp(o_done(t), (jt + jl - 1) & 1)) {
-            ok = false;
-            break;
-          }
-          ptx::tc_fence_after();
+          // O holds the earlier key tiles: scale it.  (The last product into it is done: it was
+          // issued before this tile's S, whose commit covers it.)
 #pragma unroll
           for (int c = 0; c < D; c += 16) {
             float ov[16];
@@ -829,7 +826,8 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
       }
       if (!ok) break;
       if (n_kv > 0) {
-        if (!wait_warp(o_done(t), (jt + n_kv - 1) & 1)) break;
+        if (!wait_warp(o_done(t), outputs & 1)) break;
+        ++outputs;
         ptx::tc_fence_after();
       }
       float la, lb;
