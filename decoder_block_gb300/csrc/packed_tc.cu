@@ -82,13 +82,14 @@ static_assert(sizeof(PtItem) <= 64, "PtItem fits its slot");
 // Planner's output, in the workspace.
 struct PtPlan {
   int n_entries;  // items are entries x units
-  int next;       // item counter
+  int next;       // item counter, past the CTAs' first items
   int n_split, pad;
 };
-struct PtEntry {
+struct __align__(16) PtEntry {
   int seq, blk;
   int range;  // first key tile | last + 1 << 16
   int slot;
+  int first, count, kv_len, pad;  // the sequence's rows and length
 };
 static_assert(LLAMA_PACKED_MAX_KV / PT_KEYS <= 65535, "key tiles fit 16 bits");
 struct PtSplit {  // a split block: its pieces' partials are slots slot .. slot + n - 1
@@ -168,7 +169,7 @@ __global__ void __launch_bounds__(PT_PLAN_THREADS) packed_plan_kernel(PagedView 
                                                                       int sms, int max_entries, PtPlan *plan,
                                                                       PtEntry *entries, PtSplit *splits, int *status) {
   __shared__ int first_blk[LLAMA_PACKED_MAX_SEQS + 1];  // blocks before sequence i
-  __shared__ int2 seqs[PT_PLAN_THREADS];                // count and kv_len of the first sequences
+  __shared__ SeqSpan seqs[PT_PLAN_THREADS];             // the first sequences
   __shared__ int hist[PT_BUCKETS];
   __shared__ int warp_sums[32];
   __shared__ unsigned long long work_sum;
@@ -191,7 +192,7 @@ __global__ void __launch_bounds__(PT_PLAN_THREADS) packed_plan_kernel(PagedView 
       check_seq(b, pv, i, status);
       const SeqSpan s = seq_span(b, pv, i);
       n = (s.count + 2 * Mq - 1) / (2 * Mq);
-      if (i0 == 0) seqs[tid] = make_int2(s.count, s.kv_len);
+      if (i0 == 0) seqs[tid] = s;
     }
     const int end = base + cta_scan(n, warp_sums);
     if (i < b.n_seqs) first_blk[i + 1] = end;
@@ -201,6 +202,7 @@ __global__ void __launch_bounds__(PT_PLAN_THREADS) packed_plan_kernel(PagedView 
     __syncthreads();
   }
   const int n_blk = base;
+  auto span_of = [&](int i) { return i < PT_PLAN_THREADS ? seqs[i] : seq_span(b, pv, i); };
   // sequence (the last i with first_blk[i] <= u), block and key tiles of block u
   auto look_up = [&](int u, int &seq, int &blk) {
     int lo = 0, hi = b.n_seqs;
@@ -211,14 +213,8 @@ __global__ void __launch_bounds__(PT_PLAN_THREADS) packed_plan_kernel(PagedView 
     }
     seq = lo;
     blk = u - first_blk[lo];
-    int2 s;
-    if (lo < PT_PLAN_THREADS) {
-      s = seqs[lo];
-    } else {
-      const SeqSpan x = seq_span(b, pv, lo);
-      s = make_int2(x.count, x.kv_len);
-    }
-    return tiles_of(s.y - s.x, blk * 2 * Mq, min(s.x, (blk + 1) * 2 * Mq));
+    const SeqSpan s = span_of(lo);
+    return tiles_of(s.kv_len - s.count, blk * 2 * Mq, min(s.count, (blk + 1) * 2 * Mq));
   };
   int seq[PT_KEEP], blk[PT_KEEP], len[PT_KEEP];
   unsigned long long mine = 0;
@@ -263,6 +259,11 @@ __global__ void __launch_bounds__(PT_PLAN_THREADS) packed_plan_kernel(PagedView 
     PtEntry e;
     e.seq = s;
     e.blk = x;
+    const SeqSpan span = span_of(s);
+    e.first = span.first;
+    e.count = span.count;
+    e.kv_len = span.kv_len;
+    e.pad = 0;
     const int p = pieces_of(n), each = (n + p - 1) / p;
     int slot = -1;
     if (p > 1) {
@@ -446,17 +447,24 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
       PtItem it;
       it.seq = -1;
       if (a.plan != nullptr) {
-        int u = 0;
-        if (lane == 0) u = atomicAdd(&a.plan->next, 1);
-        u = __shfl_sync(0xffffffffu, u, 0);
+        int u = blockIdx.x;
+        if (k > 0) {
+          if (lane == 0) u = gridDim.x + atomicAdd(&a.plan->next, 1);
+          u = __shfl_sync(0xffffffffu, u, 0);
+          if (u >= n_items) return it;
+        }
+        const int4 *e = reinterpret_cast<const int4 *>(a.entries + u / units);
+        const int4 x = __ldcg(e), y = __ldcg(e + 1);  // the first: there is room, if not an entry
         if (u >= n_items) return it;
-        const int4 e = __ldcg(reinterpret_cast<const int4 *>(a.entries + u / units));
-        it.seq = e.x;
+        it.seq = x.x;
         it.unit = u % units;
-        it.q0 = e.y * 2 * a.Mq;
-        it.j0 = e.z & 0xffff;
-        it.j1 = (unsigned)e.z >> 16;
-        it.slot = e.w;
+        it.q0 = x.y * 2 * a.Mq;
+        it.j0 = x.z & 0xffff;
+        it.j1 = (unsigned)x.z >> 16;
+        it.slot = x.w;
+        it.first = y.x;
+        it.count = y.y;
+        it.kv_len = y.z;
       } else {
         if (k > 0) return it;
         const int want = blockIdx.x / units;
@@ -488,11 +496,11 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
       it.g = it.unit / a.subs;
       it.h0 = it.g * a.r + it.unit % a.subs * a.rb;
       it.nh = min(a.rb, (it.g + 1) * a.r - it.h0);
-      const SeqSpan s = seq_span(a.b, a.pv, it.seq);
-      it.first = s.first;
-      it.count = s.count;
-      it.kv_len = s.kv_len;
       if (a.plan == nullptr) {
+        const SeqSpan s = seq_span(a.b, a.pv, it.seq);
+        it.first = s.first;
+        it.count = s.count;
+        it.kv_len = s.kv_len;
         it.j0 = 0;
         it.j1 = tiles_of(s.kv_len - s.count, it.q0, min(s.count, it.q0 + 2 * a.Mq));
       }
@@ -1058,7 +1066,9 @@ cudaError_t launch_tc(const bf16 *q, const bf16 *k, const bf16 *v, bf16 *o, cons
   count_launch();
   e = launch_pdl(kernel, dim3((unsigned)(items < sms ? items : sms)), threads, L::BYTES, st, mq,
                  mk, mv, a);
-  if (e != cudaSuccess) return e;
+  // no piece of a split is shorter than PT_MIN_PIECE tiles, nor an item split that is not
+  // PT_SPLIT_COST longer
+  if (e != cudaSuccess || b.max_kv_len <= (PT_MIN_PIECE + PT_SPLIT_COST) * PT_KEYS) return e;
   count_launch();
   return launch_pdl(packed_join_kernel<D>, dim3((unsigned)(z.max_split * z.units * 8)), dim3(D * 2), 0, st, a,
                     (const PtSplit *)splits);

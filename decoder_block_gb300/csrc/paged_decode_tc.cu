@@ -83,8 +83,9 @@ static_assert(sizeof(PdItem) == 32, "PdItem fills its slot");
 struct PdPlan {
   int n_entries, next, n_split, pad;
 };
-struct PdEntry {
+struct __align__(16) PdEntry {
   int seq, j0, j1, slot;
+  int len, pad[3];
 };
 struct PdSplit {
   int seq, slot, n, pad;
@@ -179,7 +180,8 @@ __global__ void __launch_bounds__(PD_PLAN_THREADS) decode_plan_kernel(PagedView 
       else hi = mid;
     }
     const int c = e - first[lo], j0 = c * chunk, slot = s_slot[lo];
-    entries[e] = PdEntry{lo, j0, min((int)s_tiles[lo], j0 + chunk), slot < 0 ? -1 : slot + c};
+    const int len = checked_len(__ldg(kv_lens + lo), max_kv_len, pv);
+    entries[e] = PdEntry{lo, j0, min((int)s_tiles[lo], j0 + chunk), slot < 0 ? -1 : slot + c, len, {0, 0, 0}};
   }
   if (tid == 0) {
     plan->n_entries = n_entries;
@@ -337,36 +339,40 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
     auto fetch = [&](int k) {  // the CTA's k-th item (all lanes)
       PdItem it;
       it.seq = -1;
-      int u = 0;
-      if (a.plan != nullptr) {
-        if (lane == 0) u = atomicAdd(&a.plan->next, 1);
-        u = __shfl_sync(0xffffffffu, u, 0);
-      } else {
+      int u = blockIdx.x;
+      if (a.plan == nullptr) {
         u = blockIdx.x / a.cluster + k * (gridDim.x / a.cluster);
+      } else if (k > 0) {
+        if (lane == 0) u = gridDim.x + atomicAdd(&a.plan->next, 1);
+        u = __shfl_sync(0xffffffffu, u, 0);
+      }
+      int4 x = make_int4(0, 0, 0, -1);
+      int len = 0;
+      if (a.plan != nullptr && (k == 0 || u < n_items)) {  // the first: there is room, if not an entry
+        const PdEntry *e = a.entries + u / units;
+        x = __ldcg(reinterpret_cast<const int4 *>(e));
+        len = __ldcg(&e->len);
       }
       if (u >= n_items) return it;
       const int unit = u % units;
       it.g = unit / a.subs;
       it.h0 = it.g * a.r + (unit % a.subs) * PD_N;
       it.nh = min(PD_N, (it.g + 1) * a.r - it.h0);
-      it.slot = -1;
-      int seq = u / units;
+      it.slot = x.w;
       if (a.plan != nullptr) {
-        const int4 e = __ldcg(reinterpret_cast<const int4 *>(a.entries + seq));
-        seq = e.x;
-        it.j0 = e.y;
-        it.j1 = e.z;
-        it.slot = e.w;
+        it.seq = x.x;
+        it.j0 = x.y;
+        it.j1 = x.z;
+        it.len = len;
+        return it;
       }
-      const int raw = __ldg(a.kv_lens + seq);
-      it.seq = seq;
+      it.seq = u / units;
+      const int raw = __ldg(a.kv_lens + it.seq);
       it.len = checked_len(raw, a.max_kv_len, a.pv);
-      if (a.plan == nullptr) {
-        if (it.len != raw && lane == 0) report_status(a.status, LLAMA_ERR_RANGE);
-        const int nt = (it.len + PD_KEYS - 1) / PD_KEYS, each = (nt + a.cluster - 1) / a.cluster;
-        it.j0 = min(nt, rank * each);
-        it.j1 = min(nt, it.j0 + each);
-      }
+      if (it.len != raw && lane == 0) report_status(a.status, LLAMA_ERR_RANGE);
+      const int nt = (it.len + PD_KEYS - 1) / PD_KEYS, each = (nt + a.cluster - 1) / a.cluster;
+      it.j0 = min(nt, rank * each);
+      it.j1 = min(nt, it.j0 + each);
       return it;
     };
     int items = 0;
