@@ -390,6 +390,7 @@ __global__ void __launch_bounds__(LP_THREADS, LP_CTAS) token_logprobs_kernel(con
   const int rank = WPR == 1 ? 0 : (int)(blockIdx.x % a.cluster);
   const int row = WPR == 1 ? (int)blockIdx.x * LP_WARPS + warp : (int)(blockIdx.x / a.cluster);
   const int part = WPR == 1 ? 0 : rank * WPR + warp;
+  grid_dependency_wait();
   if (WPR == 1 && row >= a.rows) return;
   auto sync = [] {
     if (WPR == 1) __syncwarp();
@@ -560,25 +561,27 @@ cudaError_t launch_token_logprobs(const T *logits, long long row_stride, const i
   count_launch();
   // Rows of a few batches, and enough of them: a warp each.
   if (V <= 2 * CTA_LOGITS && (long long)rows >= 4LL * sms) {
-    token_logprobs_kernel<T, 1><<<(unsigned)((rows + LP_WARPS - 1) / LP_WARPS), LP_THREADS, 0, st>>>(a);
-    return cudaGetLastError();
+    return launch_pdl(token_logprobs_kernel<T, 1>, dim3((unsigned)((rows + LP_WARPS - 1) / LP_WARPS)),
+                      dim3(LP_THREADS), 0, st, a);
   }
   // Too few rows to fill the SMs (four CTAs each): split each over a cluster, down to
   // one batch per CTA.
   while (a.cluster < LP_MAX_CLUSTER && (long long)rows * a.cluster * 2 <= 4LL * sms &&
          V / (a.cluster * 2) >= CTA_LOGITS)
     a.cluster *= 2;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = (unsigned)a.cluster;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchAttribute attrs[2];
+  attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attrs[0].val.programmaticStreamSerializationAllowed = 1;
+  attrs[1].id = cudaLaunchAttributeClusterDimension;
+  attrs[1].val.clusterDim.x = (unsigned)a.cluster;
+  attrs[1].val.clusterDim.y = attrs[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   if ((long long)rows * a.cluster > 0x7fffffffLL) return cudaErrorInvalidValue;
   cfg.gridDim = dim3((unsigned)(rows * a.cluster));
   cfg.blockDim = dim3(LP_THREADS);
   cfg.stream = st;
-  cfg.attrs = &attr;
-  cfg.numAttrs = a.cluster > 1 ? 1 : 0;
+  cfg.attrs = attrs;
+  cfg.numAttrs = a.cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<T, LP_WARPS>, a);
 }
 

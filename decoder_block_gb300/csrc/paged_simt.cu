@@ -106,6 +106,8 @@ __global__ void __launch_bounds__(THREADS) packed_simt_kernel(const __grid_const
   float *sq = smem_f, *sk = smem_f + L::OFF_K, *sv = smem_f + L::OFF_V, *sp = smem_f + L::OFF_P;
   const int r = a.H / a.G, g = blockIdx.y;
   const int tx = threadIdx.x % 16, ty = threadIdx.x / 16;
+  allow_dependents_launch();
+  grid_dependency_wait();
   if (blockIdx.x == 0 && g == 0 && blockIdx.z == 0)
     for (int i = threadIdx.x; i < a.b.n_seqs; i += THREADS) check_seq(a.b, a.pv, i, a.status);
   // block -> (sequence, tile): the grid holds at least one block for every tile
@@ -286,6 +288,7 @@ struct RowParts {
 template <int D>
 __global__ void __launch_bounds__(THREADS) packed_join_simt_kernel(const __grid_constant__ PsArgs a) {
   const long long row = (long long)blockIdx.x * (THREADS / 32) + threadIdx.x / 32;  // token, head
+  grid_dependency_wait();
   if (row >= (long long)a.b.n_tokens * a.H) return;
   const int t = (int)(row / a.H), r = a.H / a.G, hh = (int)(row % a.H) % r;
   const int seq = find_seq(a.b, t);
@@ -319,13 +322,13 @@ cudaError_t packed_simt(PsArgs a, cudaStream_t st) {
   const long long tiles = packed_tiles(a.b, a.H, a.G);
   if (tiles > 0x7fffffffLL || a.G > 65535) return cudaErrorInvalidValue;
   count_launch();
-  packed_simt_kernel<D><<<dim3((unsigned)tiles, (unsigned)a.G, (unsigned)a.split.n), THREADS, PsLayout<D>::BYTES, st>>>(a);
-  cudaError_t r = cudaGetLastError();
+  const cudaError_t r = launch_pdl(packed_simt_kernel<D>, dim3((unsigned)tiles, (unsigned)a.G, (unsigned)a.split.n),
+                                   dim3(THREADS), PsLayout<D>::BYTES, st, a);
   if (r != cudaSuccess || a.split.n == 1) return r;
   count_launch();
   const long long rows = (long long)a.b.n_tokens * a.H;
-  packed_join_simt_kernel<D><<<(unsigned)((rows + THREADS / 32 - 1) / (THREADS / 32)), THREADS, 0, st>>>(a);
-  return cudaGetLastError();
+  return launch_pdl(packed_join_simt_kernel<D>, dim3((unsigned)((rows + THREADS / 32 - 1) / (THREADS / 32))),
+                    dim3(THREADS), 0, st, a);
 }
 
 // ---------------------------------------------------------------- decode ---
@@ -366,6 +369,8 @@ __global__ void __launch_bounds__(THREADS) paged_decode_simt_kernel(const __grid
   const int r = a.H / a.G, blocks = (r + HEADS - 1) / HEADS;
   const int g = blockIdx.z / blocks, h0 = (blockIdx.z % blocks) * HEADS;
   const int nh = min(HEADS, r - h0), seq = blockIdx.y;
+  allow_dependents_launch();
+  grid_dependency_wait();
   const int raw_len = __ldg(a.kv_lens + seq);
   const int len = checked_len(raw_len, a.max_kv_len, a.pv);
   if (len != raw_len && blockIdx.x == 0 && blockIdx.z == 0 && threadIdx.x == 0)
@@ -476,6 +481,7 @@ __global__ void __launch_bounds__(THREADS) decode_join_simt_kernel(const __grid_
   constexpr int WARPS = THREADS / 32;
   __shared__ float sm[WARPS], sl[WARPS], so[WARPS][D];
   const int row = blockIdx.x, warp = threadIdx.x / 32, lane = threadIdx.x & 31;  // sequence, head
+  grid_dependency_wait();
   const int len = checked_len(__ldg(a.kv_lens + row / a.H), a.max_kv_len, a.pv);
   if (len <= a.split.chunk) return;
   const RowParts<D> x(a.part + (size_t)row * a.split.n * (D + 2), D + 2, (len + a.split.chunk - 1) / a.split.chunk,
@@ -517,13 +523,12 @@ cudaError_t decode_simt(DsArgs a, cudaStream_t st) {
   const long long units = (long long)a.G * ((a.H / a.G + HEADS - 1) / HEADS), rows = (long long)a.n_seqs * a.H;
   if (units > 65535 || rows > 0x7fffffffLL) return cudaErrorInvalidValue;
   count_launch();
-  paged_decode_simt_kernel<D>
-      <<<dim3((unsigned)a.split.n, (unsigned)a.n_seqs, (unsigned)units), THREADS, DsLayout<D>::BYTES, st>>>(a);
-  const cudaError_t r = cudaGetLastError();
+  const cudaError_t r = launch_pdl(paged_decode_simt_kernel<D>,
+                                   dim3((unsigned)a.split.n, (unsigned)a.n_seqs, (unsigned)units), dim3(THREADS),
+                                   DsLayout<D>::BYTES, st, a);
   if (r != cudaSuccess || a.split.n == 1) return r;
   count_launch();
-  decode_join_simt_kernel<D><<<(unsigned)rows, THREADS, 0, st>>>(a);
-  return cudaGetLastError();
+  return launch_pdl(decode_join_simt_kernel<D>, dim3((unsigned)rows), dim3(THREADS), 0, st, a);
 }
 
 }  // namespace

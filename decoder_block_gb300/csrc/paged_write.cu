@@ -40,6 +40,8 @@ __global__ void __launch_bounds__(PW_THREADS, PW_CTAS) rope_kv_paged_kernel(cons
   const int t0 = (int)blockIdx.x * a.rows;
   const int heads = a.H + 2 * a.G, units = heads << a.unit_log2;
   const int slot_mask = (1 << a.pv.page_log2) - 1;
+  allow_dependents_launch();
+  grid_dependency_wait();
   if (blockIdx.x == 0)
     for (int i = threadIdx.x; i < a.b.n_seqs; i += PW_THREADS) check_seq(a.b, a.pv, i, a.status);
   if (warp < a.rows) {
@@ -168,8 +170,8 @@ cudaError_t launch_rope_kv_paged(const T *qkv, T *q_out, T *k, T *v, const Paged
   a.rows = 1;
   while (a.rows < PW_ROWS && b.n_tokens / (2 * a.rows) >= 4 * sms) a.rows *= 2;
   count_launch();
-  rope_kv_paged_kernel<T><<<(unsigned)((b.n_tokens + a.rows - 1) / a.rows), PW_THREADS, 0, st>>>(qkv, q_out, k, v, a);
-  return cudaGetLastError();
+  return launch_pdl(rope_kv_paged_kernel<T>, dim3((unsigned)((b.n_tokens + a.rows - 1) / a.rows)), dim3(PW_THREADS), 0,
+                    st, qkv, q_out, k, v, a);
 }
 
 template cudaError_t launch_rope_kv_paged<float>(const float *, float *, float *, float *, const PagedView &,
