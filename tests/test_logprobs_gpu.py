@@ -136,6 +136,25 @@ def test_token_logprobs_targets_and_optional_outputs(lb):
     assert lp is None and ent is None and np.array_equal(ids, _reference(x.astype(np.float64), 4)[2]) and status == 0
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_token_logprobs_rows_more_than_four_gigabytes_apart(lb, dtype):
+    t = torch()
+    V, k, stride = 3001, 7, (1 << 30) + 5  # rows 2^30 elements apart, none of them aligned alike
+    x = store(synth.normal(0, "lpfar", (4, V), std=2.5), dtype)
+    pool = t.empty(3 * stride + V, dtype=t.float32 if dtype == "f32" else t.bfloat16, device="cuda")
+    t.as_strided(pool, (4, V), (stride, 1)).copy_(to_dev(x))
+    y = to_dev(np.array([0, 5, V - 1, 1000], np.int32))
+    out = [t.empty(4, device="cuda"), t.empty(4, device="cuda"), t.empty((4, k), dtype=t.int32, device="cuda"),
+           t.empty((4, k), device="cuda")]
+    lb.check(lb.llama_op_token_logprobs(lb.LLAMA_F32 if dtype == "f32" else lb.LLAMA_BF16, pool, stride, y, 4, V, out[0],
+                                        out[1], k, out[2], out[3], None, t.cuda.current_stream()))
+    t.cuda.synchronize()
+    lp, ent, ids, _, _ = _reference(synth.as_f64(x), k)
+    assert np.allclose(to_f64(out[0]), lp[np.arange(4), [0, 5, V - 1, 1000]], atol=1e-5)
+    assert np.allclose(to_f64(out[1]), ent, atol=1e-5)
+    assert np.array_equal(out[2].cpu().numpy(), ids)
+
+
 def test_token_logprobs_repeat_and_capture(lb):
     t = torch()
     T, V, k = 37, 30011, 8

@@ -430,3 +430,145 @@ def test_two_streams_with_their_own_workspaces(lb):
     t.cuda.synchronize()
     a.check(to_f64(da.o), "stream 1")
     b.check(to_f64(db.o), "stream 2")
+
+
+# ------------------------------------------------- far offsets, long keys ---
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_pages_more_than_four_gigabytes_apart(lb, dtype):
+    """Page offsets past 2^32 bytes and 2^31 elements (a pool whose pages lie far apart)."""
+    t = torch()
+    H, G, D, page = 4, 2, 64, 16
+    p = Problem(f"far/{dtype}", dtype, H, G, D, page, [20, 1], [20, 40], spare=0, rubbish=False)
+    d = p.device(lb)
+    stride = (3 << 29) // (1 if dtype == "bf16" else 2)  # elements; 5 pages
+    pools = []
+    for src in (d.k, d.v):
+        pool = t.empty((p.n_pages - 1) * stride + G * page * D, dtype=src.dtype, device="cuda")
+        view = t.as_strided(pool, (p.n_pages, G, page, D), (stride, page * D, D, 1))
+        view.copy_(src)
+        pools.append(view)
+    assert (p.n_pages - 1) * stride * pools[0].element_size() > 1 << 32
+    d.kv = lb.make_paged_kv_cache(pools[0], pools[1], d.table)
+    run_packed(lb, p, d)
+    got, status = _finish(d)
+    p.check(got, "packed")
+    # decode: one row per sequence, the first rows of q
+    q = Problem(f"far/{dtype}", dtype, H, G, D, page, [1, 1], [20, 40], spare=0, rubbish=False)
+    q.table, q.k, q.v, q.n_pages = p.table, p.k, p.v, p.n_pages
+    q.q = p.q[:2]
+    d.o.fill_(7.0)
+    lens = to_dev(np.array([20, 40], np.int32))
+    need = lb.llama_op_attention_paged_decode_workspace_bytes(d.code, 2, 40, H, G, D)
+    ws = t.empty(max(16, need), dtype=t.uint8, device="cuda")
+    lb.check(lb.llama_op_attention_paged_decode(d.code, d.q, d.kv, lens, 2, 40, d.o, H, G, D, ws, ws.numel(), d.status))
+    t.cuda.synchronize()
+    q.check(to_f64(d.o)[:2], "decode")
+    # write: the same pages as in a dense pool
+    qkv = to_dev(store(synth.normal(0, "far/qkv", (p.T, (H + 2 * G) * D)), dtype))
+    table = t.empty((64, D // 2, 2), dtype=t.float32, device="cuda")
+    lb.check(lb.llama_op_rope_table(table, 64, D, 1e4))
+    dense = [d.k.clone(), d.v.clone()]
+    for k, v in (pools, dense):
+        lb.check(lb.llama_op_rope_kv_write_paged(d.code, qkv, d.o, lb.make_paged_kv_cache(k, v, d.table), d.batch,
+                                                 table, 64, H, G, D, 0, d.status))
+    t.cuda.synchronize()
+    assert not t.equal(dense[0], d.k)
+    assert t.equal(pools[0], dense[0]) and t.equal(pools[1], dense[1])
+    assert int(d.status[0]) == 0 and status == 0
+
+
+def test_packed_attention_very_long_keys(lb):
+    p = Problem("pk/150k", "bf16", 4, 1, 64, 256, [3, 40, 1], [150001, 200, 140000], rubbish=False)
+    got, status = _finish(run_packed(lb, p))
+    p.check(got, "150001 keys")
+    assert status == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_paged_decode_very_long_keys(lb, dtype):
+    p = Problem(f"dec/150k{dtype}", dtype, 4, 1, 64, 128, [1, 1], [150001, 77], rubbish=False)
+    got, status = _finish(run_decode(lb, p))
+    p.check(got, "150001 keys")
+    assert status == 0
+
+
+def test_packed_attention_more_blocks_than_the_planner_keeps(lb):
+    """128 heads per KV head make a block of every two positions: 6000 blocks.  An item does not
+    depend on its company, so the batch has to equal its two halves bit for bit."""
+    t = torch()
+    n, H, D, page = 2000, 128, 64, 16
+    p = Problem("pk/blocks", "bf16", H, 1, D, page, [5] * n, [9] * n, rubbish=False)
+    d = p.device(lb)
+    d.batch = lb.make_packed_batch(d.offsets, d.kv_lens, p.T, 2000)  # a bound that rules out no split
+    run_packed(lb, p, d, max_kv=2000)
+    t.cuda.synchronize()
+    whole = d.o.clone()
+    assert int(d.status[0]) == 0
+    d.o.zero_()
+    for a, b in ((0, n // 2), (n // 2, n)):
+        rows = slice(int(p.offsets[a]), int(p.offsets[b]))
+        q, o = d.q[rows].contiguous(), t.zeros_like(d.o[rows])
+        off, lens = (d.offsets[a:b + 1] - d.offsets[a]).contiguous(), d.kv_lens[a:b].clone()
+        batch = lb.make_packed_batch(off, lens, q.shape[0], 2000)
+        kv = lb.make_paged_kv_cache(d.k, d.v, d.table[a:b].clone())
+        ws = t.empty(lb.llama_op_attention_packed_workspace_bytes(d.code, batch, H, 1, D), dtype=t.uint8,
+                     device="cuda")
+        lb.check(lb.llama_op_attention_packed(d.code, q, kv, batch, o, H, 1, D, ws, ws.numel(), d.status))
+        d.o[rows] = o
+    t.cuda.synchronize()
+    assert t.equal(whole, d.o)
+    assert bool(t.isfinite(whole.float()).all())
+
+
+def test_two_graphs_share_a_workspace(lb):
+    t = torch()
+    a = Problem("share/a", "bf16", 32, 8, 128, 64, [1] * 7, [3000, 10, 2000, 600, 4000, 1, 2500])
+    b = Problem("share/b", "bf16", 8, 2, 128, 32, [300, 2, 1], [1300, 5000, 700])
+    c = Problem("share/c", "f32", 8, 2, 64, 32, [30, 2, 1], [1300, 900, 700])
+    da, db, dc = a.device(lb), b.device(lb), c.device(lb)
+    need = [lb.llama_op_attention_paged_decode_workspace_bytes(da.code, 7, a.max_kv, 32, 8, 128),
+            lb.llama_op_attention_packed_workspace_bytes(db.code, db.batch, 8, 2, 128),
+            lb.llama_op_attention_packed_workspace_bytes(dc.code, dc.batch, 8, 2, 64)]
+    assert min(need) > 0
+    ws = t.empty(max(need), dtype=t.uint8, device="cuda")
+    graphs = []
+    for run, p, d in ((run_decode, a, da), (run_packed, b, db), (run_packed, c, dc)):
+        run(lb, p, d, workspace=ws)
+        t.cuda.synchronize()
+        g = t.cuda.CUDAGraph()
+        with t.cuda.graph(g):
+            run(lb, p, d, workspace=ws)
+        graphs.append(g)
+    for d in (da, db, dc):
+        d.o.fill_(7.0)
+    for _ in range(5):
+        for g in graphs:
+            g.replay()
+    t.cuda.synchronize()
+    for p, d in ((a, da), (b, db), (c, dc)):
+        p.check(to_f64(d.o), "shared workspace")
+        assert int(d.status[0]) == 0
+
+
+def test_workspace_too_small_is_refused(lb):
+    t = torch()
+    p = Problem("ws", "bf16", 32, 8, 128, 64, [40, 1], [3000, 2000])
+    d = p.device(lb)
+    need = lb.llama_op_attention_packed_workspace_bytes(d.code, d.batch, 32, 8, 128)
+    ws = t.empty(need, dtype=t.uint8, device="cuda")
+    assert lb.llama_op_attention_packed(d.code, d.q, d.kv, d.batch, d.o, 32, 8, 128, ws, need - 1, d.status) \
+        == lb.LLAMA_ERR_RANGE
+    assert lb.llama_op_attention_packed(d.code, d.q, d.kv, d.batch, d.o, 32, 8, 128, None, need, d.status) \
+        == lb.LLAMA_ERR_INVALID_ARG
+    # 40 sequences of up to 3000 keys: too many for clusters, so planned
+    need = lb.llama_op_attention_paged_decode_workspace_bytes(d.code, 40, 3000, 32, 8, 128)
+    assert need > 0
+    lens = t.ones(40, dtype=t.int32, device="cuda")
+    q = t.zeros((40, 32, 128), dtype=t.bfloat16, device="cuda")
+    tab = t.zeros((40, 47), dtype=t.int32, device="cuda")
+    kv = lb.make_paged_kv_cache(d.k, d.v, tab)
+    assert lb.llama_op_attention_paged_decode(d.code, q, kv, lens, 40, 3000, q, 32, 8, 128, ws, need - 1) \
+        == lb.LLAMA_ERR_RANGE
+    t.cuda.synchronize()
+    assert bool((d.o == 7.0).all())
