@@ -755,7 +755,9 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
         const bool masked = __any_sync(0xffffffffu, key0 + PT_KEYS - 1 > pos);
         float alpha_tile = 1.f;
         bool rescaled = false;  // warp-uniform
-#pragma unroll
+        // (rolled up beside the issuers: 379 us for 383 over 16-row pages, ragged 151 for 157;
+        // without them 375 for 364)
+#pragma unroll(ISSUERS > 0 ? 1 : 4)
         for (int c = 0; c < PT_KEYS; c += 32) {
           float sv[32];
           float cm;
