@@ -272,21 +272,24 @@ __device__ __noinline__ int second_pass(const Vec16<T> *vec, int v0, int step, i
   TopList top{-INFINITY, INT_MAX};
   float kth = -INFINITY;
   int kth_id = INT_MAX, waiting = 0;
+  Vec16<T> x[LP_VECS], next[LP_VECS];
+  load_batch<T>(next, vec, v0, n_vec);
   for (; v0 < n_vec; v0 += step) {
-#pragma unroll 1
+    float bm = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < LP_VECS; ++j) {
+      x[j] = next[j];
+#pragma unroll
+      for (int e = 0; e < V; ++e) bm = fmaxf(bm, x[j].get(e));
+    }
+    load_batch<T>(next, vec, v0 + step, n_vec);  // a batch ahead: nothing where the row ends
+    if (!__any_sync(0xffffffffu, bm >= bound && bm >= kth)) continue;
+#pragma unroll
     for (int j = 0; j < LP_VECS; ++j) {
       const int at = v0 + 32 * j + lane;
-      Vec16<T> x;
-      float vm = -INFINITY;
-      if (at < n_vec) {
-        x = load16<T>(reinterpret_cast<const T *>(vec + at));
-#pragma unroll
-        for (int e = 0; e < V; ++e) vm = fmaxf(vm, x.get(e));
-      }
-      if (!__any_sync(0xffffffffu, at < n_vec && vm >= bound && vm >= kth)) continue;
 #pragma unroll
       for (int e = 0; e < V; ++e) {
-        const float v = at < n_vec ? x.get(e) : 0.f;
+        const float v = x[j].get(e);
         const int id = id0 + at * V + e;
         const bool c = at < n_vec && v >= bound && ahead(v, id, kth, kth_id);
         const unsigned mask = __ballot_sync(0xffffffffu, c);
