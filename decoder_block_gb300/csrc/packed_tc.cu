@@ -92,8 +92,9 @@ struct __align__(16) PtEntry {
   int first, count, kv_len, pad;  // the sequence's rows and length
 };
 static_assert(LLAMA_PACKED_MAX_KV / PT_KEYS <= 65535, "key tiles fit 16 bits");
-struct PtSplit {  // a split block: its pieces' partials are slots slot .. slot + n - 1
-  int seq, blk, slot, n;
+struct __align__(16) PtSplit {  // a split block: its pieces' partials are slots slot .. slot + n - 1
+  int q0, slot, n;
+  int first, count, pad[3];  // the sequence's rows
 };
 
 struct PtArgs {
@@ -268,7 +269,7 @@ __global__ void __launch_bounds__(PT_PLAN_THREADS) packed_plan_kernel(PagedView 
     int slot = -1;
     if (p > 1) {
       slot = atomicAdd(&n_slots, p);
-      splits[atomicAdd(&n_split, 1)] = PtSplit{s, x, slot, p};
+      splits[atomicAdd(&n_split, 1)] = PtSplit{x * 2 * Mq, slot, p, span.first, span.count, {0, 0, 0}};
     }
     const int at = atomicAdd(&hist[bucket(n, p)], p);
     for (int i = 0; i < p; ++i) {
@@ -863,8 +864,8 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
             *reinterpret_cast<uint4 *>(dst + c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
           }
         }
-      } else if (it.q0 + t * a.Mq < it.count) {
-        // a piece: the rows' partial (O, m, l), one column of 32 rows after another
+      } else if (__any_sync(0xffffffffu, valid)) {
+        // a piece: the partial (O, m, l) of these 32 rows, one column after another
         float *mine = a.part + ((((size_t)it.slot * (a.G * a.subs) + it.unit) * 2 + t) * 4 + qq) * ((D + 2) * 32) + lane;
 #pragma unroll
         for (int c = 0; c < D; c += 16) {
@@ -896,44 +897,47 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
 }
 
 // Joins the pieces of split items, o = sum 2^(m_p - M) O_p / sum 2^(m_p - M) l_p in
-// piece order.  A CTA takes 32 rows of one block and unit; a warp 16 columns of them.
+// piece order.  A CTA takes 32 rows of one block and unit, a warp JOIN_COLS columns of
+// them; four pieces are on their way at a time.
+constexpr int JOIN_COLS = 8;
+
 template <int D>
-__global__ void __launch_bounds__(D * 2) packed_join_kernel(const __grid_constant__ PtArgs a, const PtSplit *splits) {
+__global__ void __launch_bounds__(D / JOIN_COLS * 32) packed_join_kernel(const __grid_constant__ PtArgs a,
+                                                                         const PtSplit *splits) {
   grid_dependency_wait();
   const int units = a.G * a.subs;
   const int qq = blockIdx.x % 4, t = blockIdx.x / 4 % 2, unit = blockIdx.x / 8 % units, k = blockIdx.x / 8 / units;
+  const PtSplit s = splits[k];  // there is room, if not an entry
   if (k >= *reinterpret_cast<volatile int *>(&a.plan->n_split)) return;
-  const PtSplit s = splits[k];
-  const int lane = threadIdx.x & 31, c0 = threadIdx.x / 32 * 16;
+  const int lane = threadIdx.x & 31, c0 = threadIdx.x / 32 * JOIN_COLS;
   const int row = qq * 32 + lane, hh = row % a.rb, i = row / a.rb;
-  const SeqSpan q = seq_span(a.b, a.pv, s.seq);
-  const int rel = s.blk * 2 * a.Mq + t * a.Mq + i;
+  const int rel = s.q0 + t * a.Mq + i;
   const int g = unit / a.subs, h = g * a.r + unit % a.subs * a.rb + hh;
-  if (s.blk * 2 * a.Mq + t * a.Mq >= q.count) return;  // no rows, nothing was written
+  const bool valid = i < a.Mq && rel < s.count && h < (g + 1) * a.r;
+  if (!__any_sync(0xffffffffu, valid)) return;  // nothing was written
   const float *p = a.part + ((((size_t)s.slot * units + unit) * 2 + t) * 4 + qq) * ((D + 2) * 32) + lane;
   const size_t step = (size_t)units * 8 * (D + 2) * 32;
   float m = -FLT_MAX;
 #pragma unroll 8
   for (int x = 0; x < s.n; ++x) m = fmaxf(m, p[x * step + D * 32]);
-  float l = 0.f, o[16];
+  float l = 0.f, o[JOIN_COLS];
 #pragma unroll
-  for (int e = 0; e < 16; ++e) o[e] = 0.f;
-#pragma unroll 2
+  for (int e = 0; e < JOIN_COLS; ++e) o[e] = 0.f;
+#pragma unroll 4
   for (int x = 0; x < s.n; ++x) {
     const float *px = p + x * step;
     const float f = ptx::ex2_approx(px[D * 32] - m);
     l = fmaf(f, px[(D + 1) * 32], l);
 #pragma unroll
-    for (int e = 0; e < 16; ++e) o[e] = fmaf(f, px[(c0 + e) * 32], o[e]);
+    for (int e = 0; e < JOIN_COLS; ++e) o[e] = fmaf(f, px[(c0 + e) * 32], o[e]);
   }
-  if (i >= a.Mq || rel >= q.count || h >= (g + 1) * a.r || c0 >= a.D) return;
+  if (!valid || c0 >= a.D) return;
   const float inv = l > 0.f ? 1.f / l : 0.f;
-  uint32_t w[8];
+  uint32_t w[JOIN_COLS / 2];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) w[e] = pt_pack2(o[2 * e] * inv, o[2 * e + 1] * inv);
-  uint4 *dst = reinterpret_cast<uint4 *>(a.o + ((size_t)(q.first + rel) * a.H + h) * a.D + c0);
-  dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
-  dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  for (int e = 0; e < JOIN_COLS / 2; ++e) w[e] = pt_pack2(o[2 * e] * inv, o[2 * e + 1] * inv);
+  *reinterpret_cast<uint4 *>(a.o + ((size_t)(s.first + rel) * a.H + h) * a.D + c0) =
+      make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -1072,7 +1076,7 @@ cudaError_t launch_tc(const bf16 *q, const bf16 *k, const bf16 *v, bf16 *o, cons
   // PT_SPLIT_COST longer
   if (e != cudaSuccess || b.max_kv_len <= (PT_MIN_PIECE + PT_SPLIT_COST) * PT_KEYS) return e;
   count_launch();
-  return launch_pdl(packed_join_kernel<D>, dim3((unsigned)(z.max_split * z.units * 8)), dim3(D * 2), 0, st, a,
+  return launch_pdl(packed_join_kernel<D>, dim3((unsigned)(z.max_split * z.units * 8)), dim3(D / JOIN_COLS * 32), 0, st, a,
                     (const PtSplit *)splits);
 }
 
