@@ -18,7 +18,7 @@
 //               each lane issues one page's box and holds the next tile's id.  Lanes
 //               issue one after another (about 65 ns each), so the 32 boxes that pages
 //               of 16 rows make of a stage are issued by four more warps (S = 8192:
-//               388 us for 456); larger pages do better without them (366 us for 373)
+//               379 us for 456); larger pages do better without them (364 us for 373)
 //   warp 1      one thread issues S_t = Q_t K^T and O_t += P_t V (fp32 in tensor
 //               memory, P from tensor memory)
 //   warps 2-9   softmax of tile 0 / 1, one thread per row; the output
@@ -59,13 +59,19 @@ struct PtLayout {
   static constexpr int OFF_V = OFF_K + PT_STAGES * TILE;
   static constexpr int OFF_ITEM = OFF_V + PT_STAGES * TILE;  // PtItem
   static constexpr int OFF_BAR = OFF_ITEM + 64;
-  // q_full, q_empty, fin, kv_full[2], kv_empty[2], s_full[2], p_full[2], o_done[2]
+  // q_full, q_empty, fin, kv_full[2], kv_empty[2], s_full[3], p_full[3], o_done[2],
   // i_full, near_end (16-row pages)
-  static constexpr int NBAR = 3 + 2 * PT_STAGES + 6 + 2;
+  static constexpr int NBAR = 3 + 2 * PT_STAGES + 8 + 2;
+  // S buffers of 128 columns in tensor memory, then O of both query tiles.  With D = 64
+  // there is room for a third: a query tile's next S is ready when its softmax is done
+  // with this one (S = 8192, 32 heads: 306 us for 324).  With D = 128 the next S goes where
+  // this one's P was.
+  static constexpr int S_BUFS = D == 64 ? 3 : 2;
   static constexpr int BYTES_MIN = 1024 + OFF_BAR + NBAR * 8 + 16;
   // one CTA per SM: two would need all of tensor memory each
   static constexpr int BYTES = BYTES_MIN > 116 * 1024 ? BYTES_MIN : 116 * 1024;
-  static constexpr uint32_t TMEM_COLS = 512;  // S0, S1 (128 each), O0, O1 (D each)
+  static constexpr uint32_t TMEM_COLS = 512;
+  static constexpr uint32_t O_COL = S_BUFS * 128;
 };
 
 // A work item as the producer hands it to the other roles.
@@ -379,12 +385,12 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
   // step of the MMA thread needs together (an item's first K comes with its Q).
   auto kv_full = [&](int s) { return bar0 + 8u * (3 + s); };
   auto kv_empty = [&](int s) { return bar0 + 8u * (3 + PT_STAGES + s); };
-  auto s_full = [&](int t) { return bar0 + 8u * (3 + 2 * PT_STAGES + t); };
-  auto p_full = [&](int t) { return bar0 + 8u * (5 + 2 * PT_STAGES + t); };
-  auto o_done = [&](int t) { return bar0 + 8u * (7 + 2 * PT_STAGES + t); };
+  auto s_full = [&](int buf) { return bar0 + 8u * (3 + 2 * PT_STAGES + buf); };
+  auto p_full = [&](int buf) { return bar0 + 8u * (6 + 2 * PT_STAGES + buf); };
+  auto o_done = [&](int t) { return bar0 + 8u * (9 + 2 * PT_STAGES + t); };
 
   // with issuers: an item has been handed over; their loads have come to its last tile
-  const uint32_t i_full = bar0 + 8u * (9 + 2 * PT_STAGES), near_end = i_full + 8;
+  const uint32_t i_full = bar0 + 8u * (11 + 2 * PT_STAGES), near_end = i_full + 8;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
@@ -405,11 +411,12 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
       ptx::mbar_init(kv_full(s), 1);
       ptx::mbar_init(kv_empty(s), 1);
     }
-    for (int t = 0; t < 2; ++t) {
-      ptx::mbar_init(s_full(t), 1);
-      ptx::mbar_init(p_full(t), 128);
-      ptx::mbar_init(o_done(t), 1);
+    for (int i = 0; i < 3; ++i) {
+      ptx::mbar_init(s_full(i), 1);
+      ptx::mbar_init(p_full(i), 128);
     }
+    ptx::mbar_init(o_done(0), 1);
+    ptx::mbar_init(o_done(1), 1);
     *abort_flag = 0;
     ptx::fence_mbar_init();
   }
@@ -581,20 +588,20 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
       constexpr uint32_t idesc_pv = ptx::idesc_bf16_f32(128, D, true);
       const uint32_t q_lo = desc_lo(s0 + L::OFF_Q, 16), k_lo = desc_lo(s0 + L::OFF_K, 16);
       const uint32_t v_lo = desc_lo(s0 + L::OFF_V, L::ATOM);  // V: MN-major, 64-column blocks an atom apart
-      auto issue_s = [&](int jj, int t) {
+      auto issue_s = [&](int jj, int t, int buf) {
         const uint32_t kb = k_lo + (jj % PT_STAGES) * (L::TILE >> 4), qb = q_lo + t * (L::TILE >> 4);
-        const uint32_t d = tmem + t * 128;
+        const uint32_t d = tmem + buf * 128;
         pt_mma_ss<0>(d, qb, kb, idesc_qk);
 #pragma unroll
         for (int kk = 1; kk < D / 16; ++kk) {
           const uint32_t off = ((kk / 4) * L::ATOM + (kk % 4) * 32) >> 4;
           pt_mma_ss<1>(d, qb + off, kb + off, idesc_qk);
         }
-        ptx::mma_commit(s_full(t));
+        ptx::mma_commit(s_full(buf));
       };
-      auto issue_pv = [&](int jj, bool first, bool last, int t) {
+      auto issue_pv = [&](int jj, bool first, bool last, int t, int buf) {
         const uint32_t vb = v_lo + (jj % PT_STAGES) * (L::TILE >> 4);
-        const uint32_t d = tmem + 256 + t * D, p = tmem + t * 128;
+        const uint32_t d = tmem + L::O_COL + t * D, p = tmem + buf * 128;
         pt_mma_ts<-1>(d, p, vb, idesc_pv, first ? 0u : 1u);
 #pragma unroll
         for (int kk = 1; kk < PT_KEYS / 16; ++kk)  // 16 keys: two 8-row groups
@@ -605,6 +612,24 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
       // overlaps that of tile 1, and the next item's first S products the output of this one.
       bool ok = true;
       int jg = 0, n0 = 0, n1 = 0;  // key tiles over all items: of the ring, of query tiles 0 and 1
+      // With three buffers the S products take them in turn (key tile by key tile, query tile
+      // 0 first), and so do the P products; with two, query tile t keeps buffer t.
+      int s_buf = 0, p_buf = 0, p_phase = 0;
+      auto next_s = [&](int jj, int t) {
+        issue_s(jj, t, L::S_BUFS == 3 ? s_buf : t);
+        s_buf = s_buf == 2 ? 0 : s_buf + 1;
+      };
+      auto next_pv = [&](int jj, bool first, bool last, int t) -> bool {
+        const int buf = L::S_BUFS == 3 ? p_buf : t;
+        if (!wait(p_full(buf), L::S_BUFS == 3 ? p_phase : (t == 0 ? n0 : n1) & 1)) return false;
+        if (t == 0) ++n0;
+        else ++n1;
+        if (p_buf == 2) p_phase ^= 1;
+        p_buf = p_buf == 2 ? 0 : p_buf + 1;
+        ptx::tc_fence_after();
+        issue_pv(jj, first, last, t, buf);
+        return true;
+      };
       int owed = 1;                // stage whose release is still to come (1: see StageLoads)
       static_assert(PT_STAGES == 2, "K of tile jj + 1 lies in the other stage");
       for (int k = 0; ok; ++k) {
@@ -618,8 +643,8 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
           continue;
         }
         ptx::tc_fence_after();
-        if (it.j0 < e0) issue_s(jg, 0);
-        if (it.j0 < e1) issue_s(jg, 1);
+        if (it.j0 < e0) next_s(jg, 0);
+        if (it.j0 < e1) next_s(jg, 1);
         if (owed >= 0) ptx::mma_commit(kv_empty(owed));
         owed = -1;
         if (n == 1) ptx::mma_commit(q_empty);
@@ -627,23 +652,21 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
         auto step = [&](int i, bool t0, bool t1, bool s0, bool s1) -> bool {
           const int jj = jg + i, st = jj % PT_STAGES;
           if (!wait(kv_full(st), (jj / PT_STAGES) & 1)) return false;
-          if (t0) {
-            if (!wait(p_full(0), n0 & 1)) return false;
-            ++n0;
+          if constexpr (L::S_BUFS == 3) {
             ptx::tc_fence_after();
-            issue_pv(jj, i == 0, !s0, 0);
+            if (s0) next_s(jj + 1, 0);
+            if (t0 && !next_pv(jj, i == 0, true, 0)) return false;
+            if (s1) next_s(jj + 1, 1);
+            if (t1 && !next_pv(jj, i == 0, true, 1)) return false;
+          } else {
+            if (t0 && !next_pv(jj, i == 0, !s0, 0)) return false;
+            if (s0) {
+              ptx::tc_fence_after();
+              next_s(jj + 1, 0);
+            }
+            if (t1 && !next_pv(jj, i == 0, !s1, 1)) return false;
+            if (s1) next_s(jj + 1, 1);
           }
-          if (s0) {
-            ptx::tc_fence_after();
-            issue_s(jj + 1, 0);
-          }
-          if (t1) {
-            if (!wait(p_full(1), n1 & 1)) return false;
-            ++n1;
-            ptx::tc_fence_after();
-            issue_pv(jj, i == 0, !s1, 1);
-          }
-          if (s1) issue_s(jj + 1, 1);
           // The stage may be filled again when the next tile's K has been used too; behind an
           // item's last tile that is the next item's first.
           if (i + 1 < n) ptx::mma_commit(kv_empty(st));
@@ -699,14 +722,14 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
     const int row = qq * 32 + lane;
     const int hh = row % a.rb, i = row / a.rb;
     const uint32_t lane_base = tmem + ((uint32_t)(qq * 32) << 16);
-    const uint32_t s_col = lane_base + t * 128;
-    const uint32_t o_col = lane_base + 256 + t * D;
+    const uint32_t o_col = lane_base + L::O_COL + t * D;
     const uint64_t scale2 = ptx::f2pack(a.scale_log2, a.scale_log2);
     if (a.plan == nullptr && blockIdx.x == 0)
       for (int u = threadIdx.x - 64; u < a.b.n_seqs; u += PT_THREADS - 64) check_seq(a.b, a.pv, u, a.status);
     bool ok = true;
     int jg = 0, jt = 0;  // key tiles of earlier items: of the ring, of this query tile
-    int outputs = 0;     // items that this query tile worked on
+    int done = 0;        // o_done phases: of every tile (three S buffers), of every item (two)
+    int mg = 0;          // S products of earlier items
     for (int k = 0; ok; ++k) {
       if (!wait_warp(q_full, k & 1)) break;
       const PtItem it = *item_slot;
@@ -723,9 +746,14 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
       // finite: rows that see no key of a tile keep weights of 0 instead of NaN
       float m_run = -FLT_MAX;
       uint64_t l2 = ptx::f2pack(0.f, 0.f);  // running row sum, two partial halves
+      const int a0 = max(0, e0 - it.j0), a1 = max(0, e1 - it.j0);
       for (int jl = 0; jl < n_kv; ++jl) {
         const int j = it.j0 + jl;
-        if (!wait_warp(s_full(t), (jt + jl) & 1)) {
+        // this tile's place among all S products
+        const int m = mg + min(jl, a0) + min(jl, a1) + (t == 1 && jl < a0 ? 1 : 0);
+        const int buf = L::S_BUFS == 3 ? m % 3 : t;
+        const uint32_t s_col = lane_base + buf * 128;
+        if (!wait_warp(s_full(buf), (L::S_BUFS == 3 ? m / 3 : jt + jl) & 1)) {
           ok = false;
           break;
         }
@@ -818,9 +846,17 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
           l2 = ptx::fadd2(l2, lc);
           ptx::tmem_st16(s_col + c / 2, pk);
         }
-        if (jl > 0 && rescaled) {
-          // O holds the earlier key tiles: scale it.  (The last product into it is done: it was
-          // issued before this tile's S, whose commit covers it.)
+        // The last product into O has to be done before O is scaled.  With two buffers it is: it
+        // was issued before this tile's S, whose commit covers it.  With three it may still run;
+        // its phase is waited for at every tile, so that none is passed over.
+        if (L::S_BUFS == 3 && jl > 0) {
+          if (!wait_warp(o_done(t), (done + jl - 1) & 1)) {
+            ok = false;
+            break;
+          }
+          ptx::tc_fence_after();
+        }
+        if (jl > 0 && rescaled) {  // O holds the earlier key tiles
 #pragma unroll
           for (int c = 0; c < D; c += 16) {
             float ov[16];
@@ -833,12 +869,12 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
         }
         ptx::tmem_st_wait();
         ptx::tc_fence_before();
-        ptx::mbar_arrive(p_full(t));
+        ptx::mbar_arrive(p_full(buf));
       }
       if (!ok) break;
       if (n_kv > 0) {
-        if (!wait_warp(o_done(t), outputs & 1)) break;
-        ++outputs;
+        done += L::S_BUFS == 3 ? n_kv : 1;
+        if (!wait_warp(o_done(t), (done - 1) & 1)) break;
         ptx::tc_fence_after();
       }
       float la, lb;
@@ -886,6 +922,7 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
       ptx::tc_fence_before();
       jg += max(0, it.j1 - it.j0);
       jt += n_kv;
+      mg += a0 + a1;
     }
   }
   ptx::tc_fence_before();
