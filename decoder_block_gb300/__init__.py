@@ -359,17 +359,37 @@ def llama_op_attention_decode_noalloc(q, kv: llama_kv_cache, o, B, start_pos, H,
 
 LLAMA_PACKED_MAX_SEQS = 4096
 LLAMA_PACKED_MAX_KV = 8388480
+LLAMA_PACKED_MAX_HEADS = 65535
+LLAMA_PACKED_MAX_ROWS = 1 << 30
+
+
+def _need_int32(what, *tensors):
+    for x in tensors:
+        if x.element_size() != 4 or x.is_floating_point() or x.stride(-1) != 1 and x.shape[-1] > 1:
+            raise ValueError(f"{what}: page ids, offsets and lengths are dense int32")
 
 
 def make_paged_kv_cache(k, v, page_table) -> llama_paged_kv_cache:
     """Struct of a page pool: k, v tensors [n_pages][n_kv_heads][page_size][d_head] (dense within a page, the same
     stride from page to page), page_table int32 [n_seqs][max_pages] (dense rows)."""
+    for x in (k, v):
+        want = 1
+        for size, stride in zip(reversed(x.shape[1:]), reversed(x.stride()[1:])):
+            if size > 1 and stride != want:
+                raise ValueError("make_paged_kv_cache: a page's elements have to be dense")
+            want *= size
+    if k.shape != v.shape or k.dtype != v.dtype or (k.shape[0] > 1 and k.stride(0) != v.stride(0)):
+        raise ValueError("make_paged_kv_cache: k and v need one shape, dtype and page stride")
+    _need_int32("make_paged_kv_cache", page_table)
     return llama_paged_kv_cache(_p(k), _p(v), _p(page_table), k.shape[0], k.shape[2], page_table.shape[1],
                                 page_table.stride(0), k.stride(0))
 
 
 def make_packed_batch(q_offsets, kv_lens, n_tokens, max_kv_len) -> llama_packed_batch:
     """Struct of a packed batch: q_offsets int32 [n_seqs + 1], kv_lens int32 [n_seqs] (device)."""
+    _need_int32("make_packed_batch", q_offsets, kv_lens)
+    if q_offsets.shape[0] != kv_lens.shape[0] + 1:
+        raise ValueError("make_packed_batch: q_offsets has one entry more than kv_lens")
     return llama_packed_batch(_p(q_offsets), _p(kv_lens), kv_lens.shape[0], n_tokens, max_kv_len)
 
 

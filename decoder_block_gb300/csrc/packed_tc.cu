@@ -173,8 +173,9 @@ __device__ __forceinline__ int item_end(const PtItem &it, int Mq, int t) {
 constexpr int PT_KEEP = 4;
 
 __global__ void __launch_bounds__(PT_PLAN_THREADS) packed_plan_kernel(PagedView pv, PackedView b, int units, int Mq,
-                                                                      int sms, int max_entries, PtPlan *plan,
-                                                                      PtEntry *entries, PtSplit *splits, int *status) {
+                                                                      int sms, int max_blocks, int max_entries,
+                                                                      PtPlan *plan, PtEntry *entries, PtSplit *splits,
+                                                                      int *status) {
   __shared__ int first_blk[LLAMA_PACKED_MAX_SEQS + 1];  // blocks before sequence i
   __shared__ SeqSpan seqs[PT_PLAN_THREADS];             // the first sequences
   __shared__ int hist[PT_BUCKETS];
@@ -201,14 +202,15 @@ __global__ void __launch_bounds__(PT_PLAN_THREADS) packed_plan_kernel(PagedView 
       n = (s.count + 2 * Mq - 1) / (2 * Mq);
       if (i0 == 0) seqs[tid] = s;
     }
-    const int end = base + cta_scan(n, warp_sums);
+    const int end = add_counts(base, cta_scan(n, warp_sums));
     if (i < b.n_seqs) first_blk[i + 1] = end;
     if (tid == PT_PLAN_THREADS - 1) warp_sums[0] = end;
     __syncthreads();
     base = warp_sums[0];
     __syncthreads();
   }
-  const int n_blk = base;
+  // (more blocks than well-formed offsets can make: see add_counts)
+  const int n_blk = min(base, max_blocks);
   auto span_of = [&](int i) { return i < PT_PLAN_THREADS ? seqs[i] : seq_span(b, pv, i); };
   // sequence (the last i with first_blk[i] <= u), block and key tiles of block u
   auto look_up = [&](int u, int &seq, int &blk) {
@@ -243,7 +245,7 @@ __global__ void __launch_bounds__(PT_PLAN_THREADS) packed_plan_kernel(PagedView 
   // costs is what the others would wait for: it is cut into pieces of at most a share.
   // Such pieces number less than 2 * sms / units, which sizes the workspace.
   const unsigned long long even = (work_sum * units + sms - 1) / sms;
-  const int share = (int)(even > PT_MIN_PIECE ? even : PT_MIN_PIECE);
+  const int share = even > 65535 ? 65535 : even > PT_MIN_PIECE ? (int)even : PT_MIN_PIECE;  // no item is longer
   auto pieces_of = [&](int n) { return n > share + PT_SPLIT_COST ? (n + share - 1) / share : 1; };
   // longest piece first: counting sort
   auto bucket = [&](int n, int pieces) { return PT_BUCKETS - 1 - min((n + pieces - 1) / pieces, PT_BUCKETS - 1); };
@@ -1103,7 +1105,7 @@ cudaError_t launch_tc(const bf16 *q, const bf16 *k, const bf16 *v, bf16 *o, cons
   a.part = reinterpret_cast<float *>(w + z.off_part);
   count_launch();
   e = launch_pdl(packed_plan_kernel, dim3(1), dim3(PT_PLAN_THREADS), 0, st, pv, b, z.units, a.Mq, sms,
-                 (int)z.max_entries, a.plan, a.entries, splits, status);
+                 (int)z.max_blocks, (int)z.max_entries, a.plan, a.entries, splits, status);
   if (e != cudaSuccess) return e;
   const long long items = z.max_entries * z.units;
   count_launch();

@@ -73,13 +73,17 @@ __device__ __forceinline__ int find_seq(const PackedView &b, int t) {
   return (a >= 0 && a <= t && t < e && e <= b.n_tokens) ? lo : -1;
 }
 
-// Inclusive sum over the threads of a CTA of 1024; warp_sums: 32 shared ints.
+// Sum of two counts, at most INT_MAX: offsets that descend make sequences overlap, and
+// their blocks may number more than an int holds.
+__device__ __forceinline__ int add_counts(int a, int b) { return (int)min((unsigned)a + (unsigned)b, 0x7fffffffu); }
+
+// Inclusive sum of counts over the threads of a CTA of 1024; warp_sums: 32 shared ints.
 __device__ __forceinline__ int cta_scan(int v, int *warp_sums) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int x = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += x;
+    if (lane >= o) v = add_counts(v, x);
   }
   if (lane == 31) warp_sums[warp] = v;
   __syncthreads();
@@ -88,12 +92,12 @@ __device__ __forceinline__ int cta_scan(int v, int *warp_sums) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int x = __shfl_up_sync(0xffffffffu, s, o);
-      if (lane >= o) s += x;
+      if (lane >= o) s = add_counts(s, x);
     }
     warp_sums[lane] = s;
   }
   __syncthreads();
-  const int out = v + (warp > 0 ? warp_sums[warp - 1] : 0);
+  const int out = add_counts(v, warp > 0 ? warp_sums[warp - 1] : 0);
   __syncthreads();
   return out;
 }

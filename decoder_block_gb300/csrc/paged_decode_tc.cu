@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(PD_PLAN_THREADS) decode_plan_kernel(PagedView 
   // them, and the last ones to finish are short.  Chunks of split sequences then
   // number less than 2 * PD_ROUNDS * sms / units, which sizes the workspace.
   const unsigned long long share = (total * units + (unsigned)(PD_ROUNDS * sms) - 1) / (unsigned)(PD_ROUNDS * sms);
-  const int chunk = (int)(share > 1 ? share : 1);
+  const int chunk = share > 65535 ? 65535 : share > 1 ? (int)share : 1;  // no sequence is longer
   int base = 0;
 #pragma unroll
   for (int k = 0; k < PER; ++k) {

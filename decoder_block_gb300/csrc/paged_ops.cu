@@ -50,7 +50,7 @@ int esize(int32_t dtype) { return dtype == LLAMA_BF16 ? 2 : 4; }
 llama_status check_heads(int32_t H, int32_t G, int32_t D) {
   if (H <= 0 || G <= 0 || D <= 0) return LLAMA_ERR_INVALID_ARG;
   if (H % G != 0) return LLAMA_ERR_SHAPE;
-  if (D != 16 && D != 32 && D != 64 && D != 128) return LLAMA_ERR_UNSUPPORTED;
+  if ((D != 16 && D != 32 && D != 64 && D != 128) || H > LLAMA_PACKED_MAX_HEADS) return LLAMA_ERR_UNSUPPORTED;
   return LLAMA_OK;
 }
 
@@ -75,9 +75,11 @@ llama_status view_of(const llama_paged_kv_cache *kv, int32_t dtype, int32_t G, i
   return LLAMA_OK;
 }
 
-llama_status check_batch(const llama_packed_batch *b) {
+llama_status check_batch(const llama_packed_batch *b, int32_t H) {
   if (b->n_seqs < 0 || b->n_tokens < 0 || b->max_kv_len < 0) return LLAMA_ERR_INVALID_ARG;
-  if (b->n_seqs > LLAMA_PACKED_MAX_SEQS || b->max_kv_len > LLAMA_PACKED_MAX_KV) return LLAMA_ERR_UNSUPPORTED;
+  if (b->n_seqs > LLAMA_PACKED_MAX_SEQS || b->max_kv_len > LLAMA_PACKED_MAX_KV ||
+      (long long)b->n_tokens * H > LLAMA_PACKED_MAX_ROWS)
+    return LLAMA_ERR_UNSUPPORTED;
   return LLAMA_OK;
 }
 
@@ -103,7 +105,7 @@ llama_status llama_op_rope_kv_write_paged(int32_t dtype, const void *qkv, void *
   if (layout != LLAMA_ROPE_INTERLEAVED && layout != LLAMA_ROPE_HALVES) return LLAMA_ERR_INVALID_ARG;
   if (kv == nullptr || batch == nullptr || table_max_seq <= 0) return LLAMA_ERR_INVALID_ARG;
   llama_status s = check_heads(H, G, D);
-  if (s == LLAMA_OK) s = check_batch(batch);
+  if (s == LLAMA_OK) s = check_batch(batch, H);
   PagedView pv;
   if (s == LLAMA_OK) s = view_of(kv, dtype, G, D, &pv);
   if (s != LLAMA_OK) return s;
@@ -123,7 +125,7 @@ llama_status llama_op_rope_kv_write_paged(int32_t dtype, const void *qkv, void *
 
 size_t llama_op_attention_packed_workspace_bytes(int32_t dtype, const llama_packed_batch *batch, int32_t H,
                                                  int32_t G, int32_t D) {
-  if (!dtype_ok(dtype) || batch == nullptr || check_heads(H, G, D) != LLAMA_OK || check_batch(batch) != LLAMA_OK)
+  if (!dtype_ok(dtype) || batch == nullptr || check_heads(H, G, D) != LLAMA_OK || check_batch(batch, H) != LLAMA_OK)
     return 0;
   if (batch->n_seqs == 0 || batch->n_tokens == 0) return 0;
   const PackedView b = view_of(batch);
@@ -136,7 +138,7 @@ llama_status llama_op_attention_packed(int32_t dtype, const void *q, const llama
                                        llama_stream stream) {
   if (!dtype_ok(dtype) || kv == nullptr || batch == nullptr) return LLAMA_ERR_INVALID_ARG;
   llama_status s = check_heads(H, G, D);
-  if (s == LLAMA_OK) s = check_batch(batch);
+  if (s == LLAMA_OK) s = check_batch(batch, H);
   PagedView pv;
   if (s == LLAMA_OK) s = view_of(kv, dtype, G, D, &pv);
   if (s != LLAMA_OK) return s;

@@ -283,7 +283,8 @@ llama_status llama_stack_set_decode_mode(llama_stack *stk, int32_t mode);
  * handle lives on.  Returns LLAMA_OK when no kernel reported a problem since
  * the last read, LLAMA_ERR_DEVICE_TIMEOUT when a bounded wait ran out,
  * LLAMA_ERR_RANGE when a token id was outside [0, vocab) (its embedding row
- * was written as zeros; a target of llama_stack_score: its log-probability as NaN), LLAMA_ERR_CUDA when the read itself failed. */
+ * was written as zeros; a target of llama_stack_score: its log-probability as
+ * NaN), LLAMA_ERR_CUDA when the read itself failed. */
 llama_status llama_block_device_status(llama_block *blk);
 llama_status llama_stack_device_status(llama_stack *stk);
 

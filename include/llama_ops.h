@@ -152,10 +152,12 @@ typedef struct {
     int64_t page_stride;  /* elements from one page to the next, 0: dense */
 } llama_paged_kv_cache;
 
-/* Most sequences of one call, and the largest max_kv_len (LLAMA_ERR_UNSUPPORTED
- * above). */
+/* Most sequences of one call, the largest max_kv_len, most query heads, and most
+ * (token, query head) pairs, n_tokens * H (LLAMA_ERR_UNSUPPORTED above). */
 #define LLAMA_PACKED_MAX_SEQS 4096
 #define LLAMA_PACKED_MAX_KV 8388480
+#define LLAMA_PACKED_MAX_HEADS 65535
+#define LLAMA_PACKED_MAX_ROWS 1073741824
 
 /* n_seqs sequences packed one after another: the new tokens of sequence i are
  * rows [q_offsets[i], q_offsets[i + 1]) of the token-major arrays of the call
@@ -166,9 +168,10 @@ typedef struct {
  * tokens are allowed.  Rows outside all sequences (padding behind the last one)
  * are neither read nor written.
  * max_kv_len: no kv_lens entry is larger (host value; it may be larger than any).
- * A sequence with bad offsets is left out; a length that is negative, above
- * max_kv_len or above max_pages * page_size counts as 0.  Both record
- * LLAMA_ERR_RANGE. */
+ * A sequence with bad offsets is left out (offsets that descend make others
+ * overlap: the rows of o and q_out may then hold anything); a length that is
+ * negative, above max_kv_len or above max_pages * page_size counts as 0.  Both
+ * record LLAMA_ERR_RANGE. */
 typedef struct {
     const int32_t *q_offsets;
     const int32_t *kv_lens;
@@ -195,8 +198,8 @@ llama_status llama_op_rope_kv_write_paged(int32_t dtype, const void *qkv, void *
  * over the sequence's pages (its own new keys included: write them first).
  * q, o: [n_tokens][H][D], q already rotated.  A token that sees no key (p < 0:
  * kv_lens[i] is less than the sequence's tokens) gets zeros.  Rows of the pages
- * at or behind kv_lens[i] may hold anything, NaN included; the visible keys and
- * values have to be finite.  D in {16, 32, 64, 128}.
+ * at or behind kv_lens[i] may hold anything, NaN included; the keys and values
+ * before it have to be finite.  D in {16, 32, 64, 128}.
  * workspace: caller-owned device scratch of at least
  * llama_op_attention_packed_workspace_bytes bytes (which reads only n_seqs,
  * n_tokens and max_kv_len of batch; 0 for arguments that the call refuses); may

@@ -58,6 +58,7 @@ def test_cache_refusals(lb, kv, expected):
 @pytest.mark.parametrize("batch,expected", [
     (dict(n_seqs=-1), "LLAMA_ERR_INVALID_ARG"), (dict(max_kv_len=-1), "LLAMA_ERR_INVALID_ARG"),
     (dict(n_seqs=4097), "LLAMA_ERR_UNSUPPORTED"), (dict(n_seqs=0), "LLAMA_OK"),
+    (dict(max_kv_len=8388481), "LLAMA_ERR_UNSUPPORTED"), (dict(max_kv_len=8388480), "LLAMA_ERR_INVALID_ARG"),
 ])
 def test_batch_refusals(lb, batch, expected):
     assert _all(lb, _kv(lb), _batch(lb, **batch)) == [getattr(lb, expected)] * 3
@@ -66,10 +67,41 @@ def test_batch_refusals(lb, batch, expected):
 @pytest.mark.parametrize("heads,expected", [
     (dict(H=0), "LLAMA_ERR_INVALID_ARG"), (dict(G=0), "LLAMA_ERR_INVALID_ARG"), (dict(D=0), "LLAMA_ERR_INVALID_ARG"),
     (dict(H=5), "LLAMA_ERR_SHAPE"), (dict(D=96), "LLAMA_ERR_UNSUPPORTED"), (dict(D=256), "LLAMA_ERR_UNSUPPORTED"),
-    (dict(dtype=2), "LLAMA_ERR_INVALID_ARG"),
+    (dict(dtype=2), "LLAMA_ERR_INVALID_ARG"), (dict(H=65536, G=1, D=16), "LLAMA_ERR_UNSUPPORTED"),
+    (dict(H=65535, G=1, D=16), "LLAMA_ERR_INVALID_ARG"),  # host memory
 ])
 def test_head_refusals(lb, heads, expected):
     assert _all(lb, _kv(lb), _batch(lb), **heads) == [getattr(lb, expected)] * 3
+
+
+def test_more_rows_than_the_kernels_count(lb):
+    kv, bf = _kv(lb), lb.LLAMA_BF16
+    for n, expected in ((lb.LLAMA_PACKED_MAX_ROWS // 4, lb.LLAMA_ERR_INVALID_ARG),  # host memory
+                        (lb.LLAMA_PACKED_MAX_ROWS // 4 + 1, lb.LLAMA_ERR_UNSUPPORTED)):
+        b = _batch(lb, n_tokens=n)
+        assert lb.llama_op_attention_packed(bf, ADDR, kv, b, ADDR, 4, 2, 64) == expected
+        assert lb.llama_op_rope_kv_write_paged(bf, ADDR, ADDR, kv, b, ADDR, 64, 4, 2, 64) == expected
+        assert (lb.llama_op_attention_packed_workspace_bytes(bf, b, 4, 2, 64) > 0) == (
+            expected == lb.LLAMA_ERR_INVALID_ARG)
+
+
+def test_struct_builders_refuse_what_the_structs_cannot_say(lb):
+    torch = pytest.importorskip("torch")
+    pool = torch.zeros(4, 2, 2, 16, 32)
+    table, lens = torch.zeros(3, 5, dtype=torch.int32), torch.zeros(3, dtype=torch.int32)
+    kv = lb.make_paged_kv_cache(pool[:, 0], pool[:, 1], table[:, :4])
+    assert (kv.n_pages, kv.page_size, kv.max_pages, kv.table_stride, kv.page_stride) == (4, 16, 4, 5, 2 * 2 * 16 * 32)
+    for k, v, t in [(pool[:, 0], pool[:, 1].contiguous(), table), (pool[:, 0], pool[:, 1], table.long()),
+                    (pool[:, 0].transpose(1, 2), pool[:, 1].transpose(1, 2), table),
+                    (pool[:, 0], pool[:, 1].bfloat16(), table), (pool[:, 0], pool[:2, 1], table),
+                    (pool[:, 0], pool[:, 1], table[:, ::2])]:
+        with pytest.raises(ValueError):
+            lb.make_paged_kv_cache(k, v, t)
+    offsets = torch.zeros(4, dtype=torch.int32)
+    assert lb.make_packed_batch(offsets, lens, 9, 7).n_seqs == 3
+    for o, n in [(offsets.long(), lens), (offsets, lens.long()), (offsets[:3], lens), (offsets.float(), lens)]:
+        with pytest.raises(ValueError):
+            lb.make_packed_batch(o, n, 9, 7)
 
 
 def test_no_tokens_is_no_work(lb):

@@ -226,6 +226,37 @@ def test_bad_offsets_leave_the_sequence_out(lb):
     assert np.all(np.abs(got[:24] - ref[:24]) <= bound[:24])
 
 
+@pytest.mark.parametrize("dtype,H,G,D", [("bf16", 40, 1, 64), ("bf16", 4, 2, 128), ("f32", 4, 2, 32)])
+def test_offsets_that_descend_stay_in_bounds(lb, dtype, H, G, D):
+    """Every other sequence claims all rows: more blocks than the plan has room for, and nothing behind it written."""
+    p = Problem("bad/desc", dtype, H, G, D, 16, [60] * 40, [1500] * 40)
+    d = p.device(lb)
+    n = len(p.kv_lens)
+    d.offsets.copy_(to_dev(np.asarray([0 if i % 2 == 0 else p.T for i in range(n + 1)], dtype=np.int32)))
+    need = lb.llama_op_attention_packed_workspace_bytes(d.code, d.batch, H, G, D)
+    ws = torch().full((need + 4096,), 0xA5, dtype=torch().uint8, device="cuda")
+    lb.check(lb.llama_op_attention_packed(d.code, d.q, d.kv, d.batch, d.o, H, G, D, ws, need, d.status))
+    got, status = _finish(d)
+    assert status == lb.LLAMA_ERR_RANGE
+    assert bool((ws[need:] == 0xA5).all())
+    d.offsets.copy_(to_dev(p.offsets))  # and the next call is right
+    d.status.zero_()
+    run_packed(lb, p, d)
+    got, status = _finish(d)
+    assert status == 0
+    p.check(got, "after the bad call")
+
+
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("f32", 32)])
+def test_bound_of_no_keys(lb, dtype, D):
+    p = Problem("bound0", dtype, 4, 2, D, 16, [3, 0, 2], [0, 0, 0])
+    for run in (run_packed, run_decode):
+        d = run(lb, p)
+        got, status = _finish(d)
+        assert status == 0
+        assert np.all((got if run is run_packed else got[:3]) == 0.0)
+
+
 # ----------------------------------------------------- RoPE + page write ---
 
 @pytest.mark.parametrize("layout", ["interleaved", "halves"])
