@@ -15,7 +15,7 @@ namespace llama {
 namespace {
 
 constexpr int PW_THREADS = 256;
-constexpr int PW_CTAS = 3;   // CTAs of an SM (a fourth: 41 us for the 38.5 below)
+constexpr int PW_CTAS = 3;   // CTAs of an SM (a fourth: 41 us for the 38.5 above)
 constexpr int PW_ROWS = 4;   // rows of a CTA, at most
 constexpr int PW_UNITS = 2;  // units of a thread in flight
 
