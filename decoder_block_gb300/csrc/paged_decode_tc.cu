@@ -563,7 +563,7 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
         // per-head maximum over the tile: warp shuffles, then across the 4 warps
         float mx[RN];
 #pragma unroll
-        for (int h = 0; h < RN; ++h) mx[h] = warp_max((valid && h < it.nh) ? s[h] : -INFINITY);
+        for (int h = 0; h < RN; ++h) mx[h] = ptx::warp_max_redux((valid && h < it.nh) ? s[h] : -INFINITY);
         float *rs = red + (tile & 1) * (4 * PD_N);
         if (!exchange(rs, mx, red_full(tile & 1), (tile >> 1) & 1)) {
           ok = false;

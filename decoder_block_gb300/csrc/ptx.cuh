@@ -133,6 +133,13 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
   }
 }
 
+// Largest value of the warp, in every lane; NaN only when all are.
+__device__ __forceinline__ float warp_max_redux(float x) {
+  float m;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x));
+  return m;
+}
+
 // Bounded wait (kWaitBudgetCycles) with acquire at cluster scope, for phases
 // completed by arrivals (release.cluster) of another CTA of the cluster;
 // false when it gave up.
