@@ -31,6 +31,8 @@
 // once its copies and MMAs in flight are done.
 #include <float.h>
 
+#include <mutex>
+
 #include "paged_kernels.h"
 #include "ptx.cuh"
 
@@ -43,8 +45,16 @@ constexpr int PD_LOADERS = 4;   // warps that load K and V
 constexpr int PD_THREADS = 192 + PD_LOADERS * 32;
 constexpr float PD_RESCALE = 8.0f;
 constexpr int PD_MAX_CLUSTER = 8;
-constexpr int PD_DIRECT_TILES = 8;  // key tiles of a CTA in the direct form, at most
+// Key tiles of a CTA in the direct form, at most, when clusters share items and when CTAs
+// take whole ones.  The planned form costs about 6 us more to start and join, and then
+// spreads ragged lengths evenly (direct for planned: 4 sequences of 7500 keys on 8 KV heads
+// 25 us for 30, of up to 7500 19 for 20; 32 of 2000 keys, 16 tiles, 46 for 50, of up to
+// 2000 39 for 34).
+constexpr int PD_CLUSTER_TILES = 15, PD_WHOLE_TILES = 12;
 constexpr int PD_ROUNDS = 12;       // chunks per SM that the planner aims at
+// Key tiles of a split sequence's chunk, at least: a chunk costs about as much as a tile
+// besides (4 sequences of 6000 keys on 8 KV heads, planned: 1: 31 us, 4: 23, 5: 21, 6: 22).
+constexpr int PD_MIN_CHUNK = 5;
 constexpr int PD_PLAN_THREADS = 1024;
 
 template <int D>
@@ -148,7 +158,7 @@ __global__ void __launch_bounds__(PD_PLAN_THREADS) decode_plan_kernel(PagedView 
   // them, and the last ones to finish are short.  Chunks of split sequences then
   // number less than 2 * PD_ROUNDS * sms / units, which sizes the workspace.
   const unsigned long long share = (total * units + (unsigned)(PD_ROUNDS * sms) - 1) / (unsigned)(PD_ROUNDS * sms);
-  const int chunk = share > 65535 ? 65535 : share > 1 ? (int)share : 1;  // no sequence is longer
+  const int chunk = share > 65535 ? 65535 : share > PD_MIN_CHUNK ? (int)share : PD_MIN_CHUNK;  // no sequence is longer
   int base = 0;
 #pragma unroll
   for (int k = 0; k < PER; ++k) {
@@ -760,6 +770,38 @@ int sm_count() {
   return sms > 0 ? sms : 1;
 }
 
+// Clusters of 1, 2, 4 or 8 CTAs, one CTA per SM, that run at once on the current device: a
+// cluster needs its SMs in one processing cluster, so 152 SMs hold 15 of eight and 36 of
+// four (16 sequences of 1024 keys as clusters of eight take two
+// turns: 18 us for 10.8).
+int clusters_at_once(int cluster, int sms) {
+  static std::mutex mutex;
+  static int known[64][PD_MAX_CLUSTER + 1];  // 0: not asked yet
+  int dev = 0;
+  if (cluster == 1 || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return sms / cluster;
+  std::lock_guard<std::mutex> lock(mutex);
+  int &n = known[dev][cluster];
+  if (n > 0) return n;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = (unsigned)cluster;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)cluster);
+  cfg.blockDim = dim3(PD_THREADS);
+  cfg.dynamicSmemBytes = PdLayout<128>::BYTES;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int found = 0;
+  if (cudaFuncSetAttribute(paged_decode_tc_kernel<128, 4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           PdLayout<128>::BYTES) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&found, paged_decode_tc_kernel<128, 4>, &cfg) != cudaSuccess || found <= 0) {
+    cudaGetLastError();
+    return sms / cluster;
+  }
+  return n = found;
+}
+
 struct PdSizes {
   int units = 0, cluster = 0;  // cluster: CTAs of a direct item (0: planned)
   long long max_entries = 0;
@@ -773,8 +815,8 @@ PdSizes decode_sizes(int n_seqs, int max_kv_len, int H, int G, int D, int sms) {
   const long long items = (long long)n_seqs * z.units;
   const int tiles = (max_kv_len + PD_KEYS - 1) / PD_KEYS;
   int cluster = 1;
-  while (cluster < PD_MAX_CLUSTER && items * cluster * 2 <= sms && tiles > cluster) cluster *= 2;
-  if ((tiles + cluster - 1) / cluster <= PD_DIRECT_TILES) {
+  while (cluster < PD_MAX_CLUSTER && items <= clusters_at_once(cluster * 2, sms) && tiles > cluster) cluster *= 2;
+  if ((tiles + cluster - 1) / cluster <= (cluster > 1 ? PD_CLUSTER_TILES : PD_WHOLE_TILES)) {
     z.cluster = cluster;
     return z;
   }

@@ -126,6 +126,26 @@ def test_paged_decode(lb, name, kv_lens, dtype, H, G, D):
     assert status == 0
 
 
+@pytest.mark.parametrize("name,kv_lens", DECODE_LENS, ids=[c[0] for c in DECODE_LENS])
+@pytest.mark.parametrize("dtype,H,G,D", HEADS)
+def test_paged_decode_under_a_loose_bound(lb, name, kv_lens, dtype, H, G, D):
+    """A server that captures one graph for all lengths gives its longest: the split is then found on the device."""
+    p = Problem(f"decl/{name}/{dtype}{H}{G}{D}", dtype, H, G, D, 64, [1] * len(kv_lens), kv_lens)
+    got, status = _finish(run_decode(lb, p, max_kv=1 << 20))
+    p.check(got, name)
+    assert status == 0
+
+
+@pytest.mark.parametrize("n,most", [(16, 1024), (15, 2100), (40, 2050), (80, 1500), (170, 1537)])
+def test_paged_decode_more_clusters_than_run_at_once(lb, n, most):
+    kv = np.random.default_rng(n).integers(1, most + 1, n)
+    kv[0] = most
+    p = Problem(f"dec/room{n}", "bf16", 3, 1, 64, 64, [1] * n, kv.tolist())
+    got, status = _finish(run_decode(lb, p))
+    p.check(got, f"{n} sequences of up to {most}")
+    assert status == 0
+
+
 @pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
 @pytest.mark.parametrize("dtype,D", [("bf16", 128), ("bf16", 64), ("f32", 64)])
 def test_paged_decode_every_page_size(lb, page, dtype, D):
