@@ -23,10 +23,11 @@
 //   * direct (few sequences, or short ones): a cluster of 1 to 8 CTAs shares a
 //     sequence and KV head and joins through distributed shared memory.  One
 //     launch, no workspace.
-//   * planned: a one-CTA kernel cuts all sequences into chunks of one size, chosen
-//     from their true lengths so that every SM gets several, and zeroes a counter
-//     that persistent CTAs take chunks from; fp32 partials go to the workspace and
-//     a third kernel joins them in chunk order.
+//   * planned: all sequences are cut into chunks of about one size, chosen from their true
+//     lengths so that every SM gets several.  Up to 32 sequences: every CTA finds the chunks
+//     for itself and takes each gridDim-th.  More: a one-CTA kernel lists them and zeroes a
+//     counter that persistent CTAs take them from.  fp32 partials go to the workspace and a
+//     last kernel joins them in chunk order.
 // Every wait is bounded; a kernel that gives up records LLAMA_ERR_DEVICE_TIMEOUT
 // once its copies and MMAs in flight are done.
 #include <float.h>
@@ -55,6 +56,11 @@ constexpr int PD_ROUNDS = 12;       // chunks per SM that the planner aims at
 // Key tiles of a split sequence's chunk, at least: a chunk costs about as much as a tile
 // besides (4 sequences of 6000 keys on 8 KV heads, planned: 1: 31 us, 4: 23, 5: 21, 6: 22).
 constexpr int PD_MIN_CHUNK = 5;
+// Sequences that every CTA cuts into chunks for itself, at most (one per lane): no kernel in
+// front, but chunks are dealt out in turn instead of taken (one sequence of 20000 keys on 8
+// KV heads 17.8 us for 19.5; with 64 sequences of up to 4096 the turns cost as much as the
+// kernel).
+constexpr int PD_SHARED_SEQS = 32;
 constexpr int PD_PLAN_THREADS = 1024;
 
 template <int D>
@@ -109,13 +115,46 @@ struct PdArgs {
   int H, G, D, r, subs, box;  // D: the heads' width (the kernel's or less); subs: blocks of up to 16 heads per KV head
   float scale_log2;
   int cluster;     // direct: CTAs of a sequence and head block
-  PdPlan *plan;    // null: direct
+  int shared_sms;  // at most 32 sequences, cut by every CTA for itself: SMs that share them (0: not so)
+  PdPlan *plan;    // null: direct, or shared_sms
   PdEntry *entries;
   float *part;     // [slot][H][D + 2]
   int *status;
 };
 
 // ------------------------------------------------------------------ plan ---
+// Key tiles of a chunk, at most: PD_ROUNDS chunks per SM, so that the last ones to finish
+// are short.  A sequence's chunks differ by no more than its last one is shorter.  Chunks of split sequences then number less than 2 * PD_ROUNDS * sms /
+// units, which sizes the workspace.
+__device__ __forceinline__ int chunk_of(unsigned long long tiles, int units, int sms) {
+  const unsigned long long share = (tiles * units + (unsigned)(PD_ROUNDS * sms) - 1) / (unsigned)(PD_ROUNDS * sms);
+  return share > 65535 ? 65535 : share > PD_MIN_CHUNK ? (int)share : PD_MIN_CHUNK;  // no sequence is longer
+}
+
+// The chunks of up to 32 sequences, found by a warp for itself: lane i has sequence i's
+// length, key tiles, chunks and the number of its first one.
+struct WarpPlan {
+  int len = 0, tiles = 0, n = 0, first = 0, total = 0;
+  __device__ __forceinline__ void find(const PagedView &pv, const int *kv_lens, int n_seqs, int max_kv_len, int units,
+                                      int sms, int *status) {
+    const int lane = threadIdx.x & 31;
+    const int raw = lane < n_seqs ? __ldg(kv_lens + lane) : 0;
+    len = checked_len(raw, max_kv_len, pv);
+    if (len != raw) report_status(status, LLAMA_ERR_RANGE);
+    tiles = (len + PD_KEYS - 1) / PD_KEYS;
+    const int chunk = chunk_of(__reduce_add_sync(0xffffffffu, (unsigned)tiles), units, sms);
+    n = lane < n_seqs ? max(1, (tiles + chunk - 1) / chunk) : 0;
+    int end = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, end, o);
+      if (lane >= o) end += x;
+    }
+    first = end - n;
+    total = __shfl_sync(0xffffffffu, end, 31);
+  }
+};
+
 __global__ void __launch_bounds__(PD_PLAN_THREADS) decode_plan_kernel(PagedView pv, const int *kv_lens, int n_seqs,
                                                                       int max_kv_len, int units, int sms,
                                                                       int max_entries, PdPlan *plan, PdEntry *entries,
@@ -154,11 +193,8 @@ __global__ void __launch_bounds__(PD_PLAN_THREADS) decode_plan_kernel(PagedView 
   for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
   if ((tid & 31) == 0 && mine != 0) atomicAdd(&total, mine);
   __syncthreads();
-  // Chunks of equal size, PD_ROUNDS per SM: a CTA that streams faster takes more of
-  // them, and the last ones to finish are short.  Chunks of split sequences then
-  // number less than 2 * PD_ROUNDS * sms / units, which sizes the workspace.
-  const unsigned long long share = (total * units + (unsigned)(PD_ROUNDS * sms) - 1) / (unsigned)(PD_ROUNDS * sms);
-  const int chunk = share > 65535 ? 65535 : share > PD_MIN_CHUNK ? (int)share : PD_MIN_CHUNK;  // no sequence is longer
+  // (a CTA that streams faster takes more of the chunks)
+  const int chunk = chunk_of(total, units, sms);
   int base = 0;
 #pragma unroll
   for (int k = 0; k < PER; ++k) {
@@ -189,9 +225,10 @@ __global__ void __launch_bounds__(PD_PLAN_THREADS) decode_plan_kernel(PagedView 
       if (first[mid] <= e) lo = mid;
       else hi = mid;
     }
-    const int c = e - first[lo], j0 = c * chunk, slot = s_slot[lo];
+    const int n = first[lo + 1] - first[lo], each = (s_tiles[lo] + n - 1) / n;
+    const int c = e - first[lo], j0 = c * each, slot = s_slot[lo];
     const int len = checked_len(__ldg(kv_lens + lo), max_kv_len, pv);
-    entries[e] = PdEntry{lo, j0, min((int)s_tiles[lo], j0 + chunk), slot < 0 ? -1 : slot + c, len, {0, 0, 0}};
+    entries[e] = PdEntry{lo, j0, min((int)s_tiles[lo], j0 + each), slot < 0 ? -1 : slot + c, len, {0, 0, 0}};
   }
   if (tid == 0) {
     plan->n_entries = n_entries;
@@ -346,10 +383,32 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
     }
     const int n_items = a.plan != nullptr ? *reinterpret_cast<volatile int *>(&a.plan->n_entries) * units
                                           : a.n_seqs * units;
+    const bool shared = a.shared_sms > 0;
+    WarpPlan mine;
+    if (shared)
+      mine.find(a.pv, a.kv_lens, a.n_seqs, a.max_kv_len, units, a.shared_sms, blockIdx.x == 0 ? a.status : nullptr);
     auto fetch = [&](int k) {  // the CTA's k-th item (all lanes)
       PdItem it;
       it.seq = -1;
       int u = blockIdx.x;
+      if (shared) {
+        u += k * gridDim.x;
+        if (u >= mine.total * units) return it;
+        const int e = u / units, unit = u % units;
+        const int src = 31 - __clz(__ballot_sync(0xffffffffu, mine.n > 0 && mine.first <= e));
+        const int n = __shfl_sync(0xffffffffu, mine.n, src), c = e - __shfl_sync(0xffffffffu, mine.first, src);
+        const int tiles = __shfl_sync(0xffffffffu, mine.tiles, src);
+        it.seq = src;
+        it.g = unit / a.subs;
+        it.h0 = it.g * a.r + (unit % a.subs) * PD_N;
+        it.nh = min(PD_N, (it.g + 1) * a.r - it.h0);
+        const int each = (tiles + n - 1) / n;
+        it.j0 = c * each;
+        it.j1 = min(tiles, it.j0 + each);
+        it.len = __shfl_sync(0xffffffffu, mine.len, src);
+        it.slot = n > 1 ? e : -1;
+        return it;
+      }
       if (a.plan == nullptr) {
         u = blockIdx.x / a.cluster + k * (gridDim.x / a.cluster);
       } else if (k > 0) {
@@ -717,13 +776,23 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
 template <int D, int COLS>
 __global__ void __launch_bounds__(256) decode_join_kernel(const PdPlan *plan, const PdSplit *splits,
                                                           const float *__restrict__ part, bf16 *__restrict__ o,
-                                                          int H, int width) {
+                                                          int H, int width, const __grid_constant__ PdArgs a) {
   constexpr int LANES = COLS / 4, GROUPS = 256 / LANES, PER = D / COLS;
   __shared__ float sm[8], so[GROUPS][COLS], sl[GROUPS];
   grid_dependency_wait();
   const int c0 = (int)(blockIdx.x % PER) * COLS, h = blockIdx.x / PER % H, k = blockIdx.x / PER / H;
-  if (k >= plan->n_split) return;
-  const PdSplit s = splits[k];
+  PdSplit s;
+  if (plan != nullptr) {
+    if (k >= plan->n_split) return;
+    s = splits[k];
+  } else {  // the same chunks as the CTAs found
+    WarpPlan x;
+    x.find(a.pv, a.kv_lens, a.n_seqs, a.max_kv_len, a.G * a.subs, a.shared_sms, nullptr);
+    s.seq = k;
+    s.slot = __shfl_sync(0xffffffffu, x.first, k);
+    s.n = __shfl_sync(0xffffffffu, x.n, k);
+    if (s.n == 1) return;
+  }
   const float *p = part + ((size_t)s.slot * H + h) * (D + 2);
   const size_t step = (size_t)H * (D + 2);
   float m = -INFINITY;
@@ -804,6 +873,7 @@ int clusters_at_once(int cluster, int sms) {
 
 struct PdSizes {
   int units = 0, cluster = 0;  // cluster: CTAs of a direct item (0: planned)
+  bool shared = false;         // planned by every CTA for itself
   long long max_entries = 0;
   int max_split = 0;
   size_t off_entries = 0, off_splits = 0, off_part = 0, bytes = 0;
@@ -821,6 +891,13 @@ PdSizes decode_sizes(int n_seqs, int max_kv_len, int H, int G, int D, int sms) {
     return z;
   }
   const int most = 2 * ((PD_ROUNDS * sms + z.units - 1) / z.units) + 2;  // chunks of split sequences
+  if (n_seqs <= PD_SHARED_SEQS) {
+    z.shared = true;
+    z.max_entries = (long long)n_seqs + most;
+    z.max_split = n_seqs;
+    z.bytes = (size_t)z.max_entries * H * (D + 2) * sizeof(float);
+    return z;
+  }
   z.max_entries = (long long)n_seqs + most;
   z.max_split = n_seqs < most / 2 ? n_seqs : most / 2;
   z.off_entries = sizeof(PdPlan);
@@ -857,6 +934,7 @@ cudaError_t launch_tc(const bf16 *q, const bf16 *k, const bf16 *v, bf16 *o, cons
   a.box = 1 << (pv.page_log2 < 7 ? pv.page_log2 : 7);
   a.scale_log2 = 1.4426950408889634f / sqrtf((float)width);
   a.cluster = 1;
+  a.shared_sms = z.shared ? sms : 0;
   a.plan = nullptr;
   a.entries = nullptr;
   a.part = nullptr;
@@ -886,14 +964,18 @@ cudaError_t launch_tc(const bf16 *q, const bf16 *k, const bf16 *v, bf16 *o, cons
     return cudaLaunchKernelEx(&cfg, paged_decode_tc_kernel<D, RN>, mq, mk, mv, a);
   }
   char *w = reinterpret_cast<char *>(workspace);
-  a.plan = reinterpret_cast<PdPlan *>(w);
-  a.entries = reinterpret_cast<PdEntry *>(w + z.off_entries);
-  PdSplit *splits = reinterpret_cast<PdSplit *>(w + z.off_splits);
-  a.part = reinterpret_cast<float *>(w + z.off_part);
-  count_launch();
-  e = launch_pdl(decode_plan_kernel, dim3(1), dim3(PD_PLAN_THREADS), 0, st, pv, kv_lens, n_seqs, max_kv_len, z.units,
-                 sms, (int)z.max_entries, a.plan, a.entries, splits, status);
-  if (e != cudaSuccess) return e;
+  PdSplit *splits = nullptr;
+  a.part = reinterpret_cast<float *>(w);
+  if (!z.shared) {
+    a.plan = reinterpret_cast<PdPlan *>(w);
+    a.entries = reinterpret_cast<PdEntry *>(w + z.off_entries);
+    splits = reinterpret_cast<PdSplit *>(w + z.off_splits);
+    a.part = reinterpret_cast<float *>(w + z.off_part);
+    count_launch();
+    e = launch_pdl(decode_plan_kernel, dim3(1), dim3(PD_PLAN_THREADS), 0, st, pv, kv_lens, n_seqs, max_kv_len,
+                   z.units, sms, (int)z.max_entries, a.plan, a.entries, splits, status);
+    if (e != cudaSuccess) return e;
+  }
   count_launch();
   const long long most = z.max_entries * z.units;
   e = launch_pdl(paged_decode_tc_kernel<D, RN>, dim3((unsigned)(most < sms ? most : sms)), dim3(PD_THREADS), L::BYTES,
@@ -903,7 +985,7 @@ cudaError_t launch_tc(const bf16 *q, const bf16 *k, const bf16 *v, bf16 *o, cons
   const bool narrow = (long long)z.max_split * H < 2LL * sms;
   return launch_pdl(narrow ? decode_join_kernel<D, 32> : decode_join_kernel<D, D>,
                     dim3((unsigned)(z.max_split * H * (narrow ? D / 32 : 1))), dim3(256), 0, st,
-                    (const PdPlan *)a.plan, (const PdSplit *)splits, (const float *)a.part, o, H, width);
+                    (const PdPlan *)a.plan, (const PdSplit *)splits, (const float *)a.part, o, H, width, a);
 }
 
 template <int D>

@@ -136,6 +136,17 @@ def test_paged_decode_under_a_loose_bound(lb, name, kv_lens, dtype, H, G, D):
     assert status == 0
 
 
+@pytest.mark.parametrize("dtype,H,G,D", [("bf16", 8, 2, 128), ("bf16", 3, 1, 64), ("bf16", 20, 1, 32)])
+@pytest.mark.parametrize("n", [31, 32, 33, 64, 1500])
+def test_paged_decode_many_sequences_under_a_loose_bound(lb, n, dtype, H, G, D):
+    kv = np.random.default_rng(n + D).integers(0, 60, n)
+    kv[:3], kv[n - 1] = [2100, 0, 1290], 900
+    p = Problem(f"decl/many{n}{D}", dtype, H, G, D, 16, [1] * n, kv.tolist())
+    got, status = _finish(run_decode(lb, p, max_kv=1 << 17))
+    p.check(got, f"{n} sequences")
+    assert status == 0
+
+
 @pytest.mark.parametrize("n,most", [(16, 1024), (15, 2100), (40, 2050), (80, 1500), (170, 1537)])
 def test_paged_decode_more_clusters_than_run_at_once(lb, n, most):
     kv = np.random.default_rng(n).integers(1, most + 1, n)
