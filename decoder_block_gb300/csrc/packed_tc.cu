@@ -1047,9 +1047,12 @@ PtSizes packed_sizes(const PackedView &b, int H, int G, int D, int sms) {
   z.units = G * z.subs;
   z.Mq = 128 / z.rb;
   z.max_blocks = (long long)b.n_tokens / (2 * z.Mq) + (b.n_seqs < b.n_tokens ? b.n_seqs : b.n_tokens);
-  // Direct: no more than one item per SM and at most 8 key tiles each, where a
-  // split would not pay for the planning kernel in front.
-  if (z.max_blocks * z.units <= sms && b.max_kv_len <= 8 * PT_KEYS) return z;
+  // Direct: no more than one item per SM, and so few key tiles that the planned form, which
+  // costs about 8 us more to start and join, cannot win them back by splitting items for
+  // the idle SMs (planned / direct: 8B-shaped, 512 tokens behind 600 29 / 21 us, 1100
+  // behind 900 39 / 33, but three tokens, the longest behind 1900, 20 / 28).
+  const long long items = z.max_blocks * z.units, tiles = (b.max_kv_len + PT_KEYS - 1) / PT_KEYS;
+  if (items <= sms && tiles <= 16 && tiles * (sms - items) <= 8LL * sms) return z;
   z.max_slots = 2 * ((sms + z.units - 1) / z.units) + 2;
   z.max_split = z.max_slots / 2;
   z.max_entries = z.max_blocks + z.max_slots;

@@ -55,6 +55,16 @@ def test_packed_attention(lb, name, q_lens, kv_lens, dtype, H, G, D):
     assert status == 0
 
 
+@pytest.mark.parametrize("name,q_lens,kv_lens", LENS, ids=[c[0] for c in LENS])
+@pytest.mark.parametrize("dtype,H,G,D", HEADS)
+def test_packed_attention_under_a_loose_bound(lb, name, q_lens, kv_lens, dtype, H, G, D):
+    """A server that captures one graph for all lengths gives its longest: the work is then dealt out on the device."""
+    p = Problem(f"pkl/{name}/{dtype}{H}{G}{D}", dtype, H, G, D, 32, q_lens, kv_lens, pad=2)
+    got, status = _finish(run_packed(lb, p, max_kv=1 << 18))
+    p.check(got, name)
+    assert status == 0
+
+
 @pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
 @pytest.mark.parametrize("dtype,D", [("bf16", 128), ("bf16", 64), ("f32", 64)])
 def test_packed_attention_every_page_size(lb, page, dtype, D):
