@@ -32,8 +32,6 @@
 // once its copies and MMAs in flight are done.
 #include <float.h>
 
-#include <mutex>
-
 #include "paged_kernels.h"
 #include "ptx.cuh"
 
@@ -839,36 +837,11 @@ int sm_count() {
   return sms > 0 ? sms : 1;
 }
 
-// Clusters of 1, 2, 4 or 8 CTAs, one CTA per SM, that run at once on the current device: a
-// cluster needs its SMs in one processing cluster, so 152 SMs hold 15 of eight and 36 of
-// four (16 sequences of 1024 keys as clusters of eight take two
-// turns: 18 us for 10.8).
+// Clusters of a size that run at once: 152 SMs hold 15 of eight CTAs and 36 of four (16
+// sequences of 1024 keys as clusters of eight take two turns: 18 us for 10.8).
 int clusters_at_once(int cluster, int sms) {
-  static std::mutex mutex;
-  static int known[64][PD_MAX_CLUSTER + 1];  // 0: not asked yet
-  int dev = 0;
-  if (cluster == 1 || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return sms / cluster;
-  std::lock_guard<std::mutex> lock(mutex);
-  int &n = known[dev][cluster];
-  if (n > 0) return n;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = (unsigned)cluster;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)cluster);
-  cfg.blockDim = dim3(PD_THREADS);
-  cfg.dynamicSmemBytes = PdLayout<128>::BYTES;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  int found = 0;
-  if (cudaFuncSetAttribute(paged_decode_tc_kernel<128, 4>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           PdLayout<128>::BYTES) != cudaSuccess ||
-      cudaOccupancyMaxActiveClusters(&found, paged_decode_tc_kernel<128, 4>, &cfg) != cudaSuccess || found <= 0) {
-    cudaGetLastError();
-    return sms / cluster;
-  }
-  return n = found;
+  static ClusterRoom room;
+  return room.at_once(paged_decode_tc_kernel<128, 4>, cluster, PD_THREADS, PdLayout<128>::BYTES, sms);
 }
 
 struct PdSizes {

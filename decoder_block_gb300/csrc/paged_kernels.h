@@ -5,10 +5,51 @@
 #include <cuda_runtime.h>
 #include <stddef.h>
 
+#include <mutex>
+
 #include "common.cuh"
 #include "paged.cuh"
 
 namespace llama {
+
+// How many clusters of a kernel run at once on the current device, asked once per device
+// and size.  A cluster's SMs are neighbours (one processing cluster of the GPU), so there
+// are fewer than the number of SMs says: those left over in each hold smaller ones only.
+class ClusterRoom {
+ public:
+  // slots: CTAs that run at once without clusters, for when the device cannot be asked
+  template <typename K>
+  int at_once(K kernel, int cluster, int threads, int smem, int slots) {
+    int dev = 0;
+    if (cluster <= 1 || cluster > MOST || cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= DEVICES)
+      return slots / cluster;
+    std::lock_guard<std::mutex> lock(mutex_);
+    int &n = known_[dev][cluster];
+    if (n > 0) return n;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = (unsigned)cluster;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)cluster);
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int found = 0;
+    if ((smem > 0 && cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess) ||
+        cudaOccupancyMaxActiveClusters(&found, kernel, &cfg) != cudaSuccess || found <= 0) {
+      cudaGetLastError();
+      return slots / cluster;
+    }
+    return n = found;
+  }
+
+ private:
+  static constexpr int DEVICES = 64, MOST = 8;
+  std::mutex mutex_;
+  int known_[DEVICES][MOST + 1] = {};
+};
 
 // RoPE on the q and k of packed rows and the write of k and v into their pages
 // (paged_write.cu); halves as for launch_rope_kv.
