@@ -567,13 +567,18 @@ cudaError_t launch_token_logprobs(const T *logits, long long row_stride, const i
     return launch_pdl(token_logprobs_kernel<T, 1>, dim3((unsigned)((rows + LP_WARPS - 1) / LP_WARPS)),
                       dim3(LP_THREADS), 0, st, a);
   }
-  // Too few rows to fill the SMs (four CTAs each): split each over a cluster, down to
-  // one batch per CTA.
-  // (76 rows of 128255 bf16: 15.7 us as clusters of eight, two of which wait, 12.5 of four)
+  // Too few rows to fill the SMs: split each over a cluster, down to one batch per CTA, while
+  // three CTAs per SM do not have work (four when parts are long; 64 rows of 128255 bf16: 10.1
+  // us as 4 x 64 CTAs, 12.0 as 8 x 64; 304 rows of 128256 fp32: 33.7 us whole, 28.0 in two
+  // parts) and all clusters run at once (76 rows of 128255 bf16: 15.7 us as clusters of
+  // eight, two of which wait, 12.3 of four).
   static ClusterRoom room;
-  while (a.cluster < LP_MAX_CLUSTER && V / (a.cluster * 2) >= CTA_LOGITS &&
-         rows <= room.at_once(token_logprobs_kernel<T, LP_WARPS>, a.cluster * 2, LP_THREADS, 0, 4 * sms))
-    a.cluster *= 2;
+  for (int c = 2; c <= LP_MAX_CLUSTER && V / c >= CTA_LOGITS; c *= 2) {
+    if ((long long)rows * c > (V / c >= 8 * CTA_LOGITS ? 4LL : 3LL) * sms ||
+        rows > room.at_once(token_logprobs_kernel<T, LP_WARPS>, c, LP_THREADS, 0, 4 * sms))
+      break;
+    a.cluster = c;
+  }
   cudaLaunchAttribute attrs[2];
   attrs[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attrs[0].val.programmaticStreamSerializationAllowed = 1;
