@@ -109,6 +109,27 @@ __device__ __forceinline__ void load_batch(Vec16<T> (&x)[LP_VECS], const Vec16<T
   }
 }
 
+// Largest logit of a lane's batch, NaN left out (-inf or NaN when there is nothing else).
+// bf16 in pairs as they are: half the instructions.
+__device__ __forceinline__ float batch_max(const Vec16<float> (&x)[LP_VECS]) {
+  float bm = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < LP_VECS; ++j)
+#pragma unroll
+    for (int e = 0; e < Vec16<float>::N; ++e) bm = fmaxf(bm, x[j].get(e));
+  return bm;
+}
+__device__ __forceinline__ float batch_max(const Vec16<bf16> (&x)[LP_VECS]) {
+  uint32_t m = 0xff80ff80u;  // -inf, -inf
+#pragma unroll
+  for (int j = 0; j < LP_VECS; ++j) {
+    const uint32_t w[4] = {x[j].raw.x, x[j].raw.y, x[j].raw.z, x[j].raw.w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) asm("max.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w[e]));
+  }
+  return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+}
+
 // What a thread keeps of the part of a row that it reads.
 template <typename T>
 struct RowScan {
@@ -156,11 +177,7 @@ struct RowScan {
     return s;
   }
   __device__ __forceinline__ void batch(const Vec16<T> (&x)[LP_VECS], int round) {
-    float bm = -INFINITY;
-#pragma unroll
-    for (int j = 0; j < LP_VECS; ++j)
-#pragma unroll
-      for (int e = 0; e < V; ++e) bm = fmaxf(bm, x[j].get(e));
+    const float bm = batch_max(x);
     b4 = fmaxf(b4, fminf(bm, b3));
     i3 = bm > b2 ? i2 : bm > b3 ? round : i3;
     b3 = fmaxf(b3, fminf(bm, b2));
