@@ -579,8 +579,13 @@ cudaError_t launch_token_logprobs(const T *logits, long long row_stride, const i
   a.cluster = 1;
   constexpr int CTA_LOGITS = LP_THREADS * LP_VECS * Vec16<T>::N;  // one batch of a CTA
   count_launch();
-  // Rows of a few batches, and enough of them: a warp each.
-  if (V <= 2 * CTA_LOGITS && (long long)rows >= 4LL * sms) {
+  // A warp per row has no barriers and no idle warps, but it needs four times as many rows as
+  // CTAs run at once, or as many times more as a row has batches of a CTA; and with a larger
+  // top one of its lanes more often has four batches that reach the bound, and the row is
+  // read again (warp / CTA per row: 8000 rows of 32000 bf16, top 1 96 / 135 us, top 20 207 /
+  // 162; 3000 rows of 8000 fp32, top 20 34 / 41 us, 1300 rows 27 / 20).
+  if (V <= 8 * CTA_LOGITS && (long long)rows * CTA_LOGITS >=
+                                 (long long)sms * (V > CTA_LOGITS ? V : CTA_LOGITS) * (top_k > 4 ? top_k : 4)) {
     return launch_pdl(token_logprobs_kernel<T, 1>, dim3((unsigned)((rows + LP_WARPS - 1) / LP_WARPS)),
                       dim3(LP_THREADS), 0, st, a);
   }

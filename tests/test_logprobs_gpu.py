@@ -111,6 +111,19 @@ def test_token_logprobs_orders_and_masks(lb, dtype, kind):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,V,k", [(4900, 261, 32), (1300, 3001, 8), (640, 4100, 1), (2500, 8197, 4), (40, 9000, 20),
+                                   (76, 33000, 3), (152, 8300, 2)])
+@pytest.mark.parametrize("kind", ["rising", "few_values", "masked", "noise"])
+def test_token_logprobs_many_rows(lb, dtype, T, V, k, kind):
+    i = np.arange(V, dtype=np.float32)[None].repeat(T, 0)
+    noise = synth.normal(0, f"lpm/{T}{V}", (T, V))
+    x = {"rising": i / 70.0, "few_values": np.floor(noise * 1.5), "masked": np.where(i % 7 == 5, noise, -np.inf),
+         "noise": noise * 2.5}[kind].astype(np.float32)
+    y = synth.uniform_int(0, f"lpm/y{T}{V}", (T,), V)
+    _check(lb, store(x, dtype), V, V, y, k)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("V", [40, 9000])
 def test_token_logprobs_without_a_distribution(lb, dtype, V):
     x = synth.normal(0, f"lpn{V}", (4, V))

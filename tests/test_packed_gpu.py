@@ -227,6 +227,24 @@ def test_bad_lengths_count_as_zero(lb):
     p.check(got, "packed, bad lengths")
 
 
+@pytest.mark.parametrize("n", [4, 40])
+def test_bad_lengths_count_as_zero_under_a_loose_bound(lb, n):
+    p = Problem(f"bad/lenl{n}", "bf16", 4, 2, 64, 16, [1] * n, [40, 33, 700, 25] * (n // 4))
+    d = p.device(lb)
+    bound = 1 << 17
+    d.kv_lens[1] = -(1 << 31)
+    d.kv_lens[n - 1] = bound + 1
+    d.kv_lens[n - 4] = p.table.shape[1] * 16 + 1  # more than the pages of a row hold
+    p.kv_lens[1] = p.kv_lens[n - 1] = p.kv_lens[n - 4] = 0
+    for run in (run_decode, run_packed):
+        d.o.fill_(7.0)
+        d.status.zero_()
+        run(lb, p, d, max_kv=bound)
+        got, status = _finish(d)
+        assert status == lb.LLAMA_ERR_RANGE
+        p.check(got, run.__name__)
+
+
 @pytest.mark.parametrize("dtype,D", [("bf16", 128), ("bf16", 64), ("f32", 32)])
 @pytest.mark.parametrize("bad_id", [-1, 1 << 20, -(1 << 31)])
 def test_bad_page_ids_read_as_zeros(lb, dtype, D, bad_id):
