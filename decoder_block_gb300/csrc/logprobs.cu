@@ -452,7 +452,10 @@ __global__ void __launch_bounds__(LP_THREADS, LP_CTAS) token_logprobs_kernel(con
     // 64 of the threads' two largest maxima: the largest of every warp that read a batch
     const int active = WPR == 1 ? 1 : max(1, min(WPR, (n_vec - rank * WPR * LP_STEP + LP_STEP - 1) / LP_STEP));
     const int share = (64 + active - 1) / active;
-    const int k1 = slot_key(r.m == -FLT_MAX ? -INFINITY : r.m, lane), k2 = slot_key(r.b2, 32 + lane);
+    // (a first batch above -FLT_MAX leaves the start value of m as b2, behind which no batch
+    // stands and which no logit need reach: i2 < 0)
+    const int k1 = slot_key(r.m == -FLT_MAX ? -INFINITY : r.m, lane);
+    const int k2 = slot_key(r.i2 < 0 ? -INFINITY : r.b2, 32 + lane);
     if (share == 64) {
       if (warp < active || WPR == 1) {
         s_max[group][lane] = k1;
