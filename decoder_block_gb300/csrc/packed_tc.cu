@@ -100,7 +100,7 @@ struct __align__(16) PtEntry {
 static_assert(LLAMA_PACKED_MAX_KV / PT_KEYS <= 65535, "key tiles fit 16 bits");
 struct __align__(16) PtSplit {  // a split block: its pieces' partials are slots slot .. slot + n - 1
   int q0, slot, n;
-  int first, count, pad[3];  // the sequence's rows
+  int first, count, kv_len, pad[2];  // the sequence's rows and length
 };
 
 struct PtArgs {
@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(PT_PLAN_THREADS) packed_plan_kernel(PagedView 
     int slot = -1;
     if (p > 1) {
       slot = atomicAdd(&n_slots, p);
-      splits[atomicAdd(&n_split, 1)] = PtSplit{x * 2 * Mq, slot, p, span.first, span.count, {0, 0, 0}};
+      splits[atomicAdd(&n_split, 1)] = PtSplit{x * 2 * Mq, slot, p, span.first, span.count, span.kv_len, {0, 0}};
     }
     const int at = atomicAdd(&hist[bucket(n, p)], p);
     for (int i = 0; i < p; ++i) {
@@ -884,7 +884,8 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
       float l = la + lb;
       bf16 *dst = a.o + ((size_t)(it.first + rel) * a.H + it.h0 + hh) * a.D;
       if (it.slot < 0) {
-        const float inv = l > 0.f ? 1.f / l : 0.f;
+        // a row that sees no key is zeros; one whose scores are all NaN or -inf is NaN (0 / 0)
+        const float inv = pos < 0 ? 0.f : 1.f / l;
 #pragma unroll
         for (int c = 0; c < D; c += 16) {
           float ov[16];
@@ -975,7 +976,7 @@ __global__ void __launch_bounds__(D / JOIN_COLS * 32) packed_join_kernel(const _
       for (int e = 0; e < JOIN_COLS; ++e) o[e] = fmaf(f, px[(c0 + e) * 32], o[e]);
     }
     if (!valid || c0 >= a.D) continue;
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = s.kv_len - s.count + rel < 0 ? 0.f : 1.f / l;
     uint32_t v[JOIN_COLS / 2];
 #pragma unroll
     for (int e = 0; e < JOIN_COLS / 2; ++e) v[e] = pt_pack2(o[2 * e] * inv, o[2 * e + 1] * inv);

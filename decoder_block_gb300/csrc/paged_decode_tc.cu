@@ -10,7 +10,9 @@
 // with p = 2^(s log2(e)/sqrt(D) - m), one running maximum m and sum l per head in
 // fp32 over one pass.  Pages arrive as TMA boxes of their own, so a tile in shared
 // memory is the same whatever the page size; V rows behind the last key, which
-// may hold anything, are cleared in shared memory (0 * NaN is not 0).
+// may hold anything, are cleared in shared memory (0 * NaN is not 0).  l is 0 for a
+// sequence without keys alone, whose row is zeros; a query that holds NaN or an infinity
+// makes it NaN (m stays -inf where every score is NaN or -inf).
 //   warp 0     takes items and loads Q
 //   warp 1     one thread issues the MMAs
 //   warps 2-5  softmax, one thread per key; the output, one thread per column
@@ -711,7 +713,7 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
           }
         } else if (it.slot < 0) {
           if (row < a.D)
-            a.o[((size_t)it.seq * a.H + it.h0 + h) * a.D + row] = __float2bfloat16_rn(l > 0.f ? ov[h] / l : 0.f);
+            a.o[((size_t)it.seq * a.H + it.h0 + h) * a.D + row] = __float2bfloat16_rn(l == 0.f ? 0.f : ov[h] / l);
         } else {
           float *pp = a.part + ((size_t)it.slot * a.H + it.h0 + h) * (D + 2);
           pp[row] = ov[h];
@@ -757,7 +759,7 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
           l = fmaf(f, lc[c], l);
           o = fmaf(f, oc[c], o);
         }
-        a.o[((size_t)seq * a.H + h0 + h) * a.D + threadIdx.x] = __float2bfloat16_rn(l > 0.f ? o / l : 0.f);
+        a.o[((size_t)seq * a.H + h0 + h) * a.D + threadIdx.x] = __float2bfloat16_rn(l == 0.f ? 0.f : o / l);
       }
     }
     ptx::cluster_sync();  // no CTA leaves while others read its shared memory

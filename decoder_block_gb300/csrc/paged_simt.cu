@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(THREADS) packed_simt_kernel(const __grid_const
     if (ty * 4 + i >= rows) continue;
     const size_t row = (size_t)(s.first + R / r) * a.H + g * r + R % r;
     if (whole) {
-      const float inv = ls > 0.f ? 1.f / ls : 0.f;
+      const float inv = pos[i] < 0 ? 0.f : 1.f / ls;  // no key: zeros; scores of NaN or -inf alone: NaN
 #pragma unroll
       for (int c = 0; c < D / 16; ++c) a.o[row * D + tx + 16 * c] = acc[i][c] * inv;
     } else {
@@ -299,9 +299,10 @@ __global__ void __launch_bounds__(THREADS) packed_join_simt_kernel(const __grid_
   const RowParts<D> x(a.part + row * (D + 2), (size_t)a.b.n_tokens * a.H * (D + 2),
                       (n_keys + a.split.chunk - 1) / a.split.chunk, 0, 1);
   const int lane = threadIdx.x & 31;
+  const bool sees = s.kv_len - (s.first + s.count - t) >= 0;
 #pragma unroll
   for (int e = 0; e < RowParts<D>::PER; ++e)
-    if (lane + 32 * e < D) a.o[row * D + lane + 32 * e] = x.l > 0.f ? x.acc[e] / x.l : 0.f;
+    if (lane + 32 * e < D) a.o[row * D + lane + 32 * e] = sees ? x.acc[e] / x.l : 0.f;
 }
 
 // every sequence ends in at most one tile that is not full
@@ -463,7 +464,7 @@ __global__ void __launch_bounds__(THREADS) paged_decode_simt_kernel(const __grid
 #pragma unroll
     for (int s = 0; s < L::SLICES; ++s) x += red[(s * HEADS + i) * D + e];
     if (len <= a.split.chunk) {
-      a.o[bh * D + u] = sl[i] > 0.f ? x / sl[i] : 0.f;
+      a.o[bh * D + u] = len > 0 ? x / sl[i] : 0.f;
     } else {
       float *pp = a.part + ((bh + i) * a.split.n + blockIdx.x) * (D + 2);
       pp[e] = x;

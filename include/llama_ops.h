@@ -199,7 +199,9 @@ llama_status llama_op_rope_kv_write_paged(int32_t dtype, const void *qkv, void *
  * q, o: [n_tokens][H][D], q already rotated.  A token that sees no key (p < 0:
  * kv_lens[i] is less than the sequence's tokens) gets zeros.  Rows of the pages
  * at or behind kv_lens[i] may hold anything, NaN included; the keys and values
- * before it have to be finite.  D in {16, 32, 64, 128}.
+ * before it have to be finite.  A query row that holds NaN or an infinity gives
+ * NaN for its head where it sees a key; other rows and heads are as without it.
+ * D in {16, 32, 64, 128}.
  * workspace: caller-owned device scratch of at least
  * llama_op_attention_packed_workspace_bytes bytes (which reads only n_seqs,
  * n_tokens and max_kv_len of batch; 0 for arguments that the call refuses); may
