@@ -122,6 +122,27 @@ __device__ __forceinline__ void allow_dependents_launch() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// Loads of what an earlier kernel of the stream may have written.  A programmatic
+// dependent may start before that kernel ends, so the data is not read-only while it
+// runs: no non-coherent load (__ldg, const __restrict__).  volatile keeps the load
+// behind grid_dependency_wait(); other memory operations may pass it.
+__device__ __forceinline__ int ld_after_wait(const int *p) {
+  int v;
+  asm volatile("ld.global.s32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ int4 ld_after_wait(const int4 *p) {
+  int4 v;
+  asm volatile("ld.global.v4.s32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+// The same of data that is read once (evicted first).
+__device__ __forceinline__ uint4 ld_once_after_wait(const void *p) {
+  uint4 v;
+  asm volatile("ld.global.cs.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
+
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st,
                               Args &&...args) {

@@ -102,7 +102,7 @@ __device__ __forceinline__ void load_batch(Vec16<T> (&x)[LP_VECS], const Vec16<T
   for (int j = 0; j < LP_VECS; ++j) {
     const int at = v0 + 32 * j + (int)(threadIdx.x & 31);
     if (at < v_end) {
-      x[j].raw = __ldcs(reinterpret_cast<const uint4 *>(vec + at));
+      x[j].raw = ld_once_after_wait(vec + at);
     } else {
 #pragma unroll
       for (int e = 0; e < Vec16<T>::N; ++e) x[j].set(e, -INFINITY);
@@ -353,7 +353,7 @@ struct Target {
   float logit = 0.f;
   __device__ __forceinline__ Target(const LpArgs &a, int row, const T *x, bool needed) {
     if (!needed || a.logprobs == nullptr) return;
-    id = a.targets[row];
+    id = ld_after_wait(a.targets + row);
     if (id >= 0 && id < a.V) logit = to_f32<T>(x[id]);
   }
 };

@@ -464,7 +464,7 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
           if (u >= n_items) return it;
         }
         const int4 *e = reinterpret_cast<const int4 *>(a.entries + u / units);
-        const int4 x = __ldcg(e), y = __ldcg(e + 1);  // the first: there is room, if not an entry
+        const int4 x = ld_after_wait(e), y = ld_after_wait(e + 1);  // the first: there is room, if not an entry
         if (u >= n_items) return it;
         it.seq = x.x;
         it.unit = u % units;

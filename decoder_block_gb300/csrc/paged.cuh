@@ -15,7 +15,7 @@ struct PagedView {
 
   // Page of index `idx` of sequence i, -1 when its id is out of range.
   __device__ __forceinline__ int page(int i, int idx) const {
-    const int id = __ldg(table + (size_t)i * table_stride + idx);
+    const int id = ld_after_wait(table + (size_t)i * table_stride + idx);
     return (unsigned)id < (unsigned)n_pages ? id : -1;
   }
   __device__ __forceinline__ long long capacity() const { return (long long)max_pages << page_log2; }
@@ -37,17 +37,17 @@ struct SeqSpan {
   int first, count, kv_len;
 };
 __device__ __forceinline__ SeqSpan seq_span(const PackedView &b, const PagedView &pv, int i) {
-  const int a = __ldg(b.q_offsets + i), e = __ldg(b.q_offsets + i + 1);
+  const int a = ld_after_wait(b.q_offsets + i), e = ld_after_wait(b.q_offsets + i + 1);
   SeqSpan s;
   s.first = a;
   s.count = (a >= 0 && e >= a && e <= b.n_tokens) ? e - a : 0;
-  s.kv_len = checked_len(__ldg(b.kv_lens + i), b.max_kv_len, pv);
+  s.kv_len = checked_len(ld_after_wait(b.kv_lens + i), b.max_kv_len, pv);
   return s;
 }
 
 // Records LLAMA_ERR_RANGE when sequence i's offsets or length are out of range.
 __device__ __forceinline__ void check_seq(const PackedView &b, const PagedView &pv, int i, int *status) {
-  const int a = __ldg(b.q_offsets + i), e = __ldg(b.q_offsets + i + 1), len = __ldg(b.kv_lens + i);
+  const int a = ld_after_wait(b.q_offsets + i), e = ld_after_wait(b.q_offsets + i + 1), len = ld_after_wait(b.kv_lens + i);
   if (a < 0 || e < a || e > b.n_tokens || len < 0 || len > b.max_kv_len || len > pv.capacity())
     report_status(status, LLAMA_ERR_RANGE);
 }
@@ -62,14 +62,14 @@ __device__ __forceinline__ int find_seq(const PackedView &b, int t) {
   while (n > 1) {
     const int step = (n + 31) / 32;
     const int probe = lo + lane * step;
-    const bool le = lane * step < n && __ldg(b.q_offsets + probe) <= t;
+    const bool le = lane * step < n && ld_after_wait(b.q_offsets + probe) <= t;
     const unsigned m = __ballot_sync(0xffffffffu, le);
     if (m == 0) return -1;
     const int k = 31 - __clz(m);
     n = min(step, n - k * step);
     lo += k * step;
   }
-  const int a = __ldg(b.q_offsets + lo), e = __ldg(b.q_offsets + lo + 1);
+  const int a = ld_after_wait(b.q_offsets + lo), e = ld_after_wait(b.q_offsets + lo + 1);
   return (a >= 0 && a <= t && t < e && e <= b.n_tokens) ? lo : -1;
 }
 

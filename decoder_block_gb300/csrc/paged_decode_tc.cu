@@ -138,7 +138,7 @@ struct WarpPlan {
   __device__ __forceinline__ void find(const PagedView &pv, const int *kv_lens, int n_seqs, int max_kv_len, int units,
                                       int sms, int *status) {
     const int lane = threadIdx.x & 31;
-    const int raw = lane < n_seqs ? __ldg(kv_lens + lane) : 0;
+    const int raw = lane < n_seqs ? ld_after_wait(kv_lens + lane) : 0;
     len = checked_len(raw, max_kv_len, pv);
     if (len != raw) report_status(status, LLAMA_ERR_RANGE);
     tiles = (len + PD_KEYS - 1) / PD_KEYS;
@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(PD_PLAN_THREADS) decode_plan_kernel(PagedView 
     const int i = k * PD_PLAN_THREADS + tid;
     tiles[k] = 0;
     if (i < n_seqs) {
-      const int raw = __ldg(kv_lens + i), len = checked_len(raw, max_kv_len, pv);
+      const int raw = ld_after_wait(kv_lens + i), len = checked_len(raw, max_kv_len, pv);
       if (len != raw) report_status(status, LLAMA_ERR_RANGE);
       tiles[k] = (len + PD_KEYS - 1) / PD_KEYS;
       mine += (unsigned)tiles[k];
@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(PD_PLAN_THREADS) decode_plan_kernel(PagedView 
     }
     const int n = first[lo + 1] - first[lo], each = (s_tiles[lo] + n - 1) / n;
     const int c = e - first[lo], j0 = c * each, slot = s_slot[lo];
-    const int len = checked_len(__ldg(kv_lens + lo), max_kv_len, pv);
+    const int len = checked_len(ld_after_wait(kv_lens + lo), max_kv_len, pv);
     entries[e] = PdEntry{lo, j0, min((int)s_tiles[lo], j0 + each), slot < 0 ? -1 : slot + c, len, {0, 0, 0}};
   }
   if (tid == 0) {
@@ -419,8 +419,8 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
       int len = 0;
       if (a.plan != nullptr && (k == 0 || u < n_items)) {  // the first: there is room, if not an entry
         const PdEntry *e = a.entries + u / units;
-        x = __ldcg(reinterpret_cast<const int4 *>(e));
-        len = __ldcg(&e->len);
+        x = ld_after_wait(reinterpret_cast<const int4 *>(e));
+        len = ld_after_wait(&e->len);
       }
       if (u >= n_items) return it;
       const int unit = u % units;
@@ -436,7 +436,7 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
         return it;
       }
       it.seq = u / units;
-      const int raw = __ldg(a.kv_lens + it.seq);
+      const int raw = ld_after_wait(a.kv_lens + it.seq);
       it.len = checked_len(raw, a.max_kv_len, a.pv);
       if (it.len != raw && lane == 0) report_status(a.status, LLAMA_ERR_RANGE);
       const int nt = (it.len + PD_KEYS - 1) / PD_KEYS, each = (nt + a.cluster - 1) / a.cluster;
@@ -775,8 +775,8 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
 // 32 columns when few rows would leave most SMs idle, else all.
 template <int D, int COLS>
 __global__ void __launch_bounds__(256) decode_join_kernel(const PdPlan *plan, const PdSplit *splits,
-                                                          const float *__restrict__ part, bf16 *__restrict__ o,
-                                                          int H, int width, const __grid_constant__ PdArgs a) {
+                                                          const float *part, bf16 *o, int H, int width,
+                                                          const __grid_constant__ PdArgs a) {
   constexpr int LANES = COLS / 4, GROUPS = 256 / LANES, PER = D / COLS;
   __shared__ float sm[8], so[GROUPS][COLS], sl[GROUPS];
   grid_dependency_wait();

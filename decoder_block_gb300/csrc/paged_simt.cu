@@ -372,7 +372,7 @@ __global__ void __launch_bounds__(THREADS) paged_decode_simt_kernel(const __grid
   const int nh = min(HEADS, r - h0), seq = blockIdx.y;
   allow_dependents_launch();
   grid_dependency_wait();
-  const int raw_len = __ldg(a.kv_lens + seq);
+  const int raw_len = ld_after_wait(a.kv_lens + seq);
   const int len = checked_len(raw_len, a.max_kv_len, a.pv);
   if (len != raw_len && blockIdx.x == 0 && blockIdx.z == 0 && threadIdx.x == 0)
     report_status(a.status, LLAMA_ERR_RANGE);
@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(THREADS) decode_join_simt_kernel(const __grid_
   __shared__ float sm[WARPS], sl[WARPS], so[WARPS][D];
   const int row = blockIdx.x, warp = threadIdx.x / 32, lane = threadIdx.x & 31;  // sequence, head
   grid_dependency_wait();
-  const int len = checked_len(__ldg(a.kv_lens + row / a.H), a.max_kv_len, a.pv);
+  const int len = checked_len(ld_after_wait(a.kv_lens + row / a.H), a.max_kv_len, a.pv);
   if (len <= a.split.chunk) return;
   const RowParts<D> x(a.part + (size_t)row * a.split.n * (D + 2), D + 2, (len + a.split.chunk - 1) / a.split.chunk,
                       warp, WARPS);

@@ -32,9 +32,8 @@ struct PwArgs {
 };
 
 template <typename T>
-__global__ void __launch_bounds__(PW_THREADS, PW_CTAS) rope_kv_paged_kernel(const T *__restrict__ qkv, T *__restrict__ q_out,
-                                                                   T *__restrict__ kc, T *__restrict__ vc,
-                                                                   const __grid_constant__ PwArgs a) {
+__global__ void __launch_bounds__(PW_THREADS, PW_CTAS)
+    rope_kv_paged_kernel(const T *qkv, T *q_out, T *kc, T *vc, const __grid_constant__ PwArgs a) {
   constexpr int V = Vec16<T>::N;
   __shared__ int s_pos[PW_ROWS], s_page[PW_ROWS];  // position: -1 out of range, -2 no such row
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
@@ -83,10 +82,10 @@ __global__ void __launch_bounds__(PW_THREADS, PW_CTAS) rope_kv_paged_kernel(cons
       if (r_[k] >= 0) {
         const int head = u >> a.unit_log2, e = (u & ((1 << a.unit_log2) - 1)) * V;
         const T *src = qkv + ((size_t)(t0 + row) * heads + head) * a.D + e;
-        x[k].raw = __ldcs(reinterpret_cast<const uint4 *>(src));
-        y[k].raw = __ldcs(reinterpret_cast<const uint4 *>(src + a.D / 2));
+        x[k].raw = ld_once_after_wait(src);
+        y[k].raw = ld_once_after_wait(src + a.D / 2);
         // the unit's V pairs: (e + j, e + j + D/2); or (e + 2j, e + 2j + 1), then those D/2 further
-        if (head < a.H + a.G && s_pos[row] >= 0) {
+        if (head < a.H + a.G && s_pos[row] >= 0) {  // (the table is made once: a constant here)
           const float4 *c = reinterpret_cast<const float4 *>(a.table + (size_t)s_pos[row] * (a.D / 2) +
                                                              (a.halves ? e : e / 2));
           const float4 *c2 = a.halves ? c + V / 4 : c + a.D / 8;
