@@ -141,6 +141,7 @@ def load() -> ctypes.CDLL:
         "llama_op_attention_paged_decode": (st, [c_int32, c_void_p, POINTER(llama_paged_kv_cache), c_void_p, c_int32,
                                                  c_int32, c_void_p, c_int32, c_int32, c_int32, c_void_p, c_size_t,
                                                  c_void_p, c_void_p]),
+        "llama_op_set_wait_budget": (st, [c_int64]),
         "llama_op_token_logprobs": (st, [c_int32, c_void_p, c_int64, c_void_p, c_int32, c_int32, c_void_p, c_void_p,
                                          c_int32, c_void_p, c_void_p, c_void_p, c_void_p]),
         "llama_op_rope_kv_write": (st, [c_int32, c_void_p, c_void_p, POINTER(llama_kv_cache), c_void_p, c_int32,
@@ -417,6 +418,10 @@ def llama_op_attention_paged_decode(dtype, q, kv: llama_paged_kv_cache, kv_lens,
                                     workspace=None, workspace_bytes=0, status=None, stream=None) -> int:
     return load().llama_op_attention_paged_decode(dtype, _p(q), byref(kv), _p(kv_lens), n_seqs, max_kv_len, _p(o), H,
                                                   G, D, _p(workspace), workspace_bytes, _p(status), _stream(stream))
+
+
+def llama_op_set_wait_budget(cycles: int) -> int:
+    return load().llama_op_set_wait_budget(cycles)
 
 
 def llama_op_token_logprobs(dtype, logits, row_stride, targets, T, V, logprobs, entropy=None, top_k=0, top_ids=None,

@@ -30,8 +30,9 @@
 //     outlast the rest (few query rows against many keys) it splits their keys
 //     into pieces; a piece leaves fp32 (O, m, l) per row in the workspace, and a
 //     third kernel joins them in piece order, so results do not depend on timing.
-// Every wait is bounded; a kernel that gives up records LLAMA_ERR_DEVICE_TIMEOUT
-// once its copies and MMAs in flight are done.
+// Every wait is bounded (llama_op_set_wait_budget).  A CTA that gives up records
+// LLAMA_ERR_DEVICE_TIMEOUT and leaves once its copies, MMAs and tensor memory stores in
+// flight are done; the four loading warps each arm the bytes they are about to ask for.
 #include <cudaTypedefs.h>
 #include <float.h>
 
@@ -115,6 +116,7 @@ struct PtArgs {
   PtEntry *entries;
   float *part;           // [slot][unit][2 tiles][4 warps][D + 2][32 rows]
   int *status;
+  long long wait_cycles;  // a wait's budget
 };
 
 __device__ __forceinline__ uint32_t pt_pack2(float a, float b) {
@@ -357,8 +359,10 @@ struct StageLoads {
   __device__ __forceinline__ uint32_t parity(int jj) const {
     return ((jj / PT_STAGES) & 1) ^ (jj % PT_STAGES == 0 ? 1 : 0);
   }
-  __device__ __forceinline__ void issue(const PtItem &it, int j, int jj, int pg, uint32_t bar, bool expect) const {
-    if (expect && (threadIdx.x & 31) == 0) ptx::mbar_arrive_expect_tx(bar, bytes(it, j) + bytes(it, j + 1));
+  // Every loading warp arrives at the stage's barrier, with the bytes of its own boxes.
+  __device__ __forceinline__ void issue(const PtItem &it, int j, int jj, int pg, uint32_t bar) const {
+    const unsigned boxes = __ballot_sync(0xffffffffu, pg >= 0);
+    if ((threadIdx.x & 31) == 0) ptx::mbar_arrive_expect_tx(bar, __popc(boxes) * a.box * 128u);
     __syncwarp();
     if (pg >= 0)
       ptx::tma_load_4d(dst + ((jj + ahead) % PT_STAGES) * L::TILE, map, at * 64, row_of(j + ahead), it.g, pg, bar);
@@ -380,6 +384,8 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
   PtItem *item_slot = reinterpret_cast<PtItem *>(smem + L::OFF_ITEM);
 
+  __shared__ int s_loaded[4];
+
   const uint32_t s0 = ptx::smem_u32(smem);
   const uint32_t bar0 = ptx::smem_u32(bars);
   const uint32_t q_full = bar0, q_empty = bar0 + 8, fin = bar0 + 16;
@@ -396,7 +402,7 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
-    if (ptx::mbar_wait(bar, parity, abort_flag, nullptr, 0)) return true;
+    if (ptx::mbar_wait_within(bar, parity, abort_flag, a.wait_cycles)) return true;
     report_status(a.status, LLAMA_ERR_DEVICE_TIMEOUT);
     return false;
   };
@@ -410,7 +416,7 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
     ptx::mbar_init(near_end, 1);
     ptx::mbar_init(fin, 1);
     for (int s = 0; s < PT_STAGES; ++s) {
-      ptx::mbar_init(kv_full(s), 1);
+      ptx::mbar_init(kv_full(s), ISSUERS > 0 ? ISSUERS : 1);
       ptx::mbar_init(kv_empty(s), 1);
     }
     for (int i = 0; i < 3; ++i) {
@@ -569,7 +575,7 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
           ok = false;
           break;
         }
-        loads.issue(it, j, tiles, page, kv_full(tiles % PT_STAGES), true);
+        loads.issue(it, j, tiles, page, kv_full(tiles % PT_STAGES));
       }
       if (!ok) break;
       if (!fetched) next = fetch(k + 1);
@@ -710,13 +716,11 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
           break;
         }
         if (j + 1 == it.j1 && warp == 10 && lane == 0) ptx::mbar_arrive(near_end);
-        loads.issue(it, j, tiles, page, kv_full(tiles % PT_STAGES), warp == 10);
+        loads.issue(it, j, tiles, page, kv_full(tiles % PT_STAGES));
       }
     }
     __syncwarp();
-    if (warp == 10 && lane == 0)
-      for (int j = max(0, tiles - PT_STAGES); j < tiles; ++j)
-        ptx::mbar_drain(kv_full(j % PT_STAGES), (j / PT_STAGES) & 1, nullptr, 0);
+    ptx::settle_loads<ISSUERS == 0 ? 1 : ISSUERS, PT_STAGES>(tiles, warp - 10, s_loaded, kv_full);
   } else {
     // ----------------------------------------------------------- softmax ---
     const int t = (warp - 2) / 4;
@@ -853,6 +857,7 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
         // its phase is waited for at every tile, so that none is passed over.
         if (L::S_BUFS == 3 && jl > 0) {
           if (!wait_warp(o_done(t), (done + jl - 1) & 1)) {
+            ptx::tmem_st_wait();  // of this tile's P: nothing of this CTA may be in flight when it leaves
             ok = false;
             break;
           }
@@ -1096,6 +1101,7 @@ cudaError_t launch_tc(const bf16 *q, const bf16 *k, const bf16 *v, bf16 *o, cons
   a.entries = nullptr;
   a.part = nullptr;
   a.status = status;
+  a.wait_cycles = op_wait_cycles();
   CUtensorMap mq, mk, mv;
   if (!make_heads_map(&mq, q, b.n_tokens, H, width, a.rb, a.Mq) || !make_paged_map(&mk, k, pv, G, width, a.box) ||
       !make_paged_map(&mv, v, pv, G, width, a.box))

@@ -30,8 +30,10 @@
 //     for itself and takes each gridDim-th.  More: a one-CTA kernel lists them and zeroes a
 //     counter that persistent CTAs take them from.  fp32 partials go to the workspace and a
 //     last kernel joins them in chunk order.
-// Every wait is bounded; a kernel that gives up records LLAMA_ERR_DEVICE_TIMEOUT
-// once its copies and MMAs in flight are done.
+// Every wait is bounded (llama_op_set_wait_budget).  A CTA that gives up records
+// LLAMA_ERR_DEVICE_TIMEOUT and leaves once its copies and MMAs in flight are done: each
+// loading warp arms the bytes that it is about to ask for itself, and at the end the
+// warps arrive at the stages that only some of them came to (see settle_loads).
 #include <float.h>
 
 #include "paged_kernels.h"
@@ -120,6 +122,7 @@ struct PdArgs {
   PdEntry *entries;
   float *part;     // [slot][H][D + 2]
   int *status;
+  long long wait_cycles;  // a wait's budget
 };
 
 // ------------------------------------------------------------------ plan ---
@@ -281,9 +284,10 @@ struct TileLoads {
     look_up(it, j + 1);
     return now;
   }
-  __device__ __forceinline__ void issue(const PdItem &it, int j, int stage, int pg, uint32_t bar, bool expect) const {
-    if (expect && (threadIdx.x & 31) == 0)
-      ptx::mbar_arrive_expect_tx(bar, 2u * boxes_of(it, j) * ATOMS * a.box * 128u);
+  // Every loading warp arrives at the stage's barrier, with the bytes of its own boxes.
+  __device__ __forceinline__ void issue(const PdItem &it, int j, int stage, int pg, uint32_t bar) const {
+    const unsigned boxes = __ballot_sync(0xffffffffu, pg >= 0);
+    if ((threadIdx.x & 31) == 0) ptx::mbar_arrive_expect_tx(bar, __popc(boxes) * a.box * 128u);
     __syncwarp();
     const int row = (j * PD_KEYS) & ((1 << a.pv.page_log2) - 1) & ~(a.box - 1);
     if (pg >= 0) ptx::tma_load_4d_hint(dst + stage * L::TILE, map, at * 64, row, it.g, pg, bar, once);
@@ -307,6 +311,8 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
   float *red = reinterpret_cast<float *>(smem + L::OFF_RED);
   PdItem *item_slot = reinterpret_cast<PdItem *>(smem + L::OFF_ITEM);
 
+  __shared__ int s_loaded[PD_LOADERS];
+
   const uint32_t s0 = ptx::smem_u32(smem);
   const uint32_t b0 = ptx::smem_u32(bars);
   auto kv_full = [&](int s) { return b0 + 8u * s; };
@@ -327,7 +333,7 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
-    if (ptx::mbar_wait(bar, parity, abort_flag, nullptr, 0)) return true;
+    if (ptx::mbar_wait_within(bar, parity, abort_flag, a.wait_cycles)) return true;
     report_status(a.status, LLAMA_ERR_DEVICE_TIMEOUT);
     return false;
   };
@@ -335,7 +341,7 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      ptx::mbar_init(kv_full(s), 1);
+      ptx::mbar_init(kv_full(s), PD_LOADERS);
       ptx::mbar_init(kv_empty(s), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -561,13 +567,11 @@ __global__ void __launch_bounds__(PD_THREADS, 1)
           ok = false;
           break;
         }
-        loads.issue(it, j, st, page, kv_full(st), warp == 6);
+        loads.issue(it, j, st, page, kv_full(st));
       }
     }
     __syncwarp();
-    if (warp == 6 && lane == 0)  // every issued copy lands before the CTA exits
-      for (int t = max(0, tile - STAGES); t < tile; ++t)
-        ptx::mbar_drain(kv_full(t % STAGES), (t / STAGES) & 1, nullptr, 0);
+    ptx::settle_loads<PD_LOADERS, STAGES>(tile, warp - 6, s_loaded, kv_full);
   } else {
     // --------------------------------------------------- softmax, output ---
     const int w4 = warp - 2;
@@ -914,6 +918,7 @@ cudaError_t launch_tc(const bf16 *q, const bf16 *k, const bf16 *v, bf16 *o, cons
   a.entries = nullptr;
   a.part = nullptr;
   a.status = status;
+  a.wait_cycles = op_wait_cycles();
   CUtensorMap mq, mk, mv;
   if (!make_heads_map(&mq, q, n_seqs, H, width, PD_N, 1) || !make_paged_map(&mk, k, pv, G, width, a.box) ||
       !make_paged_map(&mv, v, pv, G, width, a.box))

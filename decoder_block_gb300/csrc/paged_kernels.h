@@ -51,6 +51,10 @@ class ClusterRoom {
   int known_[DEVICES][MOST + 1] = {};
 };
 
+// Budget of a wait in the packed and paged-decode attention kernels, in SM clock cycles
+// (llama_op_set_wait_budget).
+long long op_wait_cycles();
+
 // RoPE on the q and k of packed rows and the write of k and v into their pages
 // (paged_write.cu); halves as for launch_rope_kv.
 template <typename T>

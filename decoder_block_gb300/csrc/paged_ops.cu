@@ -1,5 +1,6 @@
 // C entry points of the packed / paged operators and of the token
 // log-probabilities (llama_ops.h): validation, then the launch.
+#include <atomic>
 #include <initializer_list>
 
 #include "kernels.h"
@@ -8,6 +9,8 @@
 using namespace llama;
 
 namespace {
+
+std::atomic<long long> wait_cycles{0};  // 0: the default
 
 // Device memory of the current device, 16-byte aligned.
 llama_status check(const void *p) {
@@ -95,7 +98,18 @@ PackedView view_of(const llama_packed_batch *b) {
 
 }  // namespace
 
+long long llama::op_wait_cycles() {
+  const long long c = wait_cycles.load(std::memory_order_relaxed);
+  return c > 0 ? c : kWaitBudgetCycles;
+}
+
 extern "C" {
+
+llama_status llama_op_set_wait_budget(int64_t cycles) {
+  if (cycles < 0) return LLAMA_ERR_INVALID_ARG;
+  wait_cycles.store(cycles, std::memory_order_relaxed);
+  return LLAMA_OK;
+}
 
 llama_status llama_op_rope_kv_write_paged(int32_t dtype, const void *qkv, void *q_out,
                                           const llama_paged_kv_cache *kv, const llama_packed_batch *batch,

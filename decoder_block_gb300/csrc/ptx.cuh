@@ -133,6 +133,26 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, volatil
   }
 }
 
+// The same with the budget given in SM clock cycles, for kernels without a handle; the
+// caller records what happened.
+__device__ __forceinline__ bool mbar_wait_within(uint32_t bar, uint32_t parity, volatile int *abort, long long budget) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (true) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort) return false;
+    if (clock64() - t0 > budget) {
+      *abort = 1;
+      return false;
+    }
+  }
+}
+
+// Barrier `id` (1 to 15) of `threads` threads of the CTA, whole warps.
+__device__ __forceinline__ void named_barrier(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
 // Largest value of the warp, in every lane; NaN only when all are.
 __device__ __forceinline__ float warp_max_redux(float x) {
   float m;
@@ -175,6 +195,26 @@ __device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity, int *s
       report_status(status, code);
       return;
     }
+  }
+}
+
+// The end of WARPS warps that fill the stages of a ring together, each arriving at a
+// stage's barrier with the bytes of its own copies behind a wait that may give up: every
+// issued copy lands before the CTA exits.  `count` is how many stages this warp arrived
+// at; a warp that gave up earlier than others arrives, without bytes, where they did.
+// Those are the last STAGES stages at most and their barriers are in the phase of that
+// stage, as a warp comes to a stage only once its previous filling was used, for which
+// all warps had arrived.  counts: WARPS shared ints; uses named barrier 1.
+template <int WARPS, int STAGES, typename F>
+__device__ __forceinline__ void settle_loads(int count, int warp, int *counts, F &&full) {
+  if ((threadIdx.x & 31) == 0) counts[warp] = count;
+  named_barrier(1, WARPS * 32);
+  int most = 0;
+  for (int w = 0; w < WARPS; ++w) most = max(most, counts[w]);
+  if ((threadIdx.x & 31) == 0) {
+    for (int t = count; t < most; ++t) mbar_arrive(full(t % STAGES));
+    if (warp == 0)
+      for (int t = max(0, most - STAGES); t < most; ++t) mbar_drain(full(t % STAGES), (t / STAGES) & 1, nullptr, 0);
   }
 }
 

@@ -226,6 +226,18 @@ llama_status llama_op_attention_paged_decode(int32_t dtype, const void *q, const
                                              int32_t H, int32_t G, int32_t D, void *workspace,
                                              size_t workspace_bytes, int32_t *status, llama_stream stream);
 
+/* Bound, in SM clock cycles, on every wait of the bf16 kernels of
+ * llama_op_attention_packed and llama_op_attention_paged_decode that gives up,
+ * for later calls (and captures) of the process; 0 restores the default, about
+ * 4e9 cycles (2 s at 2 GHz), which no legitimate wait reaches.  As
+ * llama_block_set_wait_budget: a wait that runs out records
+ * LLAMA_ERR_DEVICE_TIMEOUT in the call's status, the kernel returns once its
+ * copies and MMAs in flight have completed (those waits keep the default) with
+ * its tensor memory freed, o is undefined and the next call starts afresh.  A
+ * diagnosis knob; the library itself never sets it.  LLAMA_ERR_INVALID_ARG for
+ * a negative budget. */
+llama_status llama_op_set_wait_budget(int64_t cycles);
+
 /* Log-probabilities of given tokens, with the entropy of each distribution and
  * its likeliest tokens.  logits: [T][V] of dtype, rows row_stride elements
  * apart (>= V; columns at and behind V are not read; rows need no alignment).
