@@ -46,7 +46,7 @@ constexpr int PT_THREADS = 320;
 constexpr int PT_KEYS = 128;    // keys of a tile
 constexpr int PT_STAGES = 2;
 constexpr float PT_RESCALE = 8.0f;  // log2 units: the running maximum is raised when it grows by > 2^8
-constexpr int PT_MIN_PIECE = 4;     // key tiles of a split item's piece, at least
+constexpr int PT_MIN_PIECE = 4;     // key tiles that a split item's pieces may have, at least (9 make 3 + 3 + 3)
 constexpr int PT_SPLIT_COST = 4;    // what a split costs, in key tiles of time
 constexpr int PT_PLAN_THREADS = 1024;
 constexpr int PT_BUCKETS = 1024;    // item lengths the planner tells apart
@@ -244,8 +244,10 @@ __global__ void __launch_bounds__(PT_PLAN_THREADS) packed_plan_kernel(PagedView 
   if ((tid & 31) == 0 && mine != 0) atomicAdd(&work_sum, mine);
   __syncthreads();
   // An SM's even share of the key tiles.  An item that is longer by more than a split
-  // costs is what the others would wait for: it is cut into pieces of at most a share.
-  // Such pieces number less than 2 * sms / units, which sizes the workspace.
+  // costs is what the others would wait for: it is cut into pieces of at most a share.  An
+  // item of n > share tiles makes fewer than n / share + 1 < 2 n / share pieces and the n of
+  // all blocks add up to share * sms / units at most, so pieces number less than 2 * sms /
+  // units, which sizes the workspace (packed_sizes).
   const unsigned long long even = (work_sum * units + sms - 1) / sms;
   const int share = even > 65535 ? 65535 : even > PT_MIN_PIECE ? (int)even : PT_MIN_PIECE;  // no item is longer
   auto pieces_of = [&](int n) { return n > share + PT_SPLIT_COST ? (n + share - 1) / share : 1; };
@@ -1059,7 +1061,9 @@ PtSizes packed_sizes(const PackedView &b, int H, int G, int D, int sms) {
   // behind 900 39 / 33, but three tokens, the longest behind 1900, 20 / 28).
   const long long items = z.max_blocks * z.units, tiles = (b.max_kv_len + PT_KEYS - 1) / PT_KEYS;
   if (items <= sms && tiles <= 16 && tiles * (sms - items) <= 8LL * sms) return z;
-  z.max_slots = 2 * ((sms + z.units - 1) / z.units) + 2;
+  // Split items: none where no sequence is long enough (no share is below PT_MIN_PIECE) or
+  // every SM has an item anyway; see the planner.
+  z.max_slots = b.max_kv_len > (PT_MIN_PIECE + PT_SPLIT_COST) * PT_KEYS && z.units < sms ? 2 * sms / z.units : 0;
   z.max_split = z.max_slots / 2;
   z.max_entries = z.max_blocks + z.max_slots;
   z.off_entries = sizeof(PtPlan);
@@ -1126,9 +1130,7 @@ cudaError_t launch_tc(const bf16 *q, const bf16 *k, const bf16 *v, bf16 *o, cons
   count_launch();
   e = launch_pdl(kernel, dim3((unsigned)(items < sms ? items : sms)), threads, L::BYTES, st, mq,
                  mk, mv, a);
-  // no piece of a split is shorter than PT_MIN_PIECE tiles, nor an item split that is not
-  // PT_SPLIT_COST longer
-  if (e != cudaSuccess || b.max_kv_len <= (PT_MIN_PIECE + PT_SPLIT_COST) * PT_KEYS) return e;
+  if (e != cudaSuccess || z.max_split == 0) return e;
   count_launch();
   const long long joins = (long long)z.max_split * z.units * 8, ctas = (long long)JOIN_CTAS * sms;
   return launch_pdl(packed_join_kernel<D>, dim3((unsigned)(joins < ctas ? joins : ctas)), dim3(D / JOIN_COLS * 32), 0,

@@ -18,3 +18,20 @@ def test_wait_budget_setter(lb):
     assert lb.llama_op_set_wait_budget(-1) == lb.LLAMA_ERR_INVALID_ARG
     assert lb.llama_op_set_wait_budget(1000) == lb.LLAMA_OK
     assert lb.llama_op_set_wait_budget(0) == lb.LLAMA_OK
+
+
+def _batch(lb, n_seqs, n_tokens, max_kv):
+    return lb.llama_packed_batch(q_offsets=None, kv_lens=None, n_seqs=n_seqs, n_tokens=n_tokens, max_kv_len=max_kv)
+
+
+@pytest.mark.parametrize("G,n_tokens,n_seqs,max_kv", [
+    (8, 8192, 4, 1024),      # no sequence is long enough for an item to be split
+    (8, 100000, 300, 1000),
+    (512, 4096, 2, 8192),    # more KV heads than there are SMs: nor does any item outlast the rest
+    (2048, 300, 1, 1 << 20),
+])
+def test_packed_workspace_holds_no_parts_that_cannot_be(lb, G, n_tokens, n_seqs, max_kv):
+    for r, D in ((1, 128), (4, 64)):
+        blocks = n_tokens // (2 * (128 // r)) + n_seqs
+        n = lb.llama_op_attention_packed_workspace_bytes(lb.LLAMA_BF16, _batch(lb, n_seqs, n_tokens, max_kv), G * r, G, D)
+        assert 32 * blocks < n < 32 * blocks + (64 << 10), (r, D)
