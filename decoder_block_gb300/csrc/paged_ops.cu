@@ -12,10 +12,11 @@ namespace {
 
 std::atomic<long long> wait_cycles{0};  // 0: the default
 
-// Device memory of the current device, 16-byte aligned.
-llama_status check(const void *p) {
+// Device memory of the current device, aligned to `align` bytes: 16 where vectors or TMA
+// boxes are read or written, the size of an element where those come one at a time.
+llama_status check(const void *p, unsigned align) {
   if (p == nullptr) return LLAMA_ERR_INVALID_ARG;
-  if ((reinterpret_cast<uintptr_t>(p) & 15u) != 0) return LLAMA_ERR_ALIGN;
+  if (reinterpret_cast<uintptr_t>(p) % align != 0) return LLAMA_ERR_ALIGN;
   cudaPointerAttributes a;
   if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
     cudaGetLastError();
@@ -30,15 +31,15 @@ llama_status check(const void *p) {
   return a.type == cudaMemoryTypeDevice && a.device == dev ? LLAMA_OK : LLAMA_ERR_INVALID_ARG;
 }
 
-llama_status check_all(std::initializer_list<const void *> ptrs) {
+llama_status check_all(std::initializer_list<const void *> ptrs, unsigned align) {
   for (const void *p : ptrs) {
-    const llama_status s = check(p);
+    const llama_status s = check(p, align);
     if (s != LLAMA_OK) return s;
   }
   return LLAMA_OK;
 }
 
-llama_status check_status(const int32_t *status) { return status == nullptr ? LLAMA_OK : check(status); }
+llama_status check_status(const int32_t *status) { return status == nullptr ? LLAMA_OK : check(status, 4); }
 
 llama_status status_of(cudaError_t e) {
   if (e == cudaSuccess) return LLAMA_OK;
@@ -124,7 +125,8 @@ llama_status llama_op_rope_kv_write_paged(int32_t dtype, const void *qkv, void *
   if (s == LLAMA_OK) s = view_of(kv, dtype, G, D, &pv);
   if (s != LLAMA_OK) return s;
   if (batch->n_seqs == 0 || batch->n_tokens == 0) return LLAMA_OK;
-  s = check_all({qkv, q_out, kv->k, kv->v, kv->page_table, batch->q_offsets, batch->kv_lens, table});
+  s = check_all({qkv, q_out, kv->k, kv->v, table}, 16);
+  if (s == LLAMA_OK) s = check_all({kv->page_table, batch->q_offsets, batch->kv_lens}, 4);
   if (s == LLAMA_OK) s = check_status(status);
   if (s != LLAMA_OK) return s;
   cudaStream_t st = (cudaStream_t)stream;
@@ -157,13 +159,14 @@ llama_status llama_op_attention_packed(int32_t dtype, const void *q, const llama
   if (s == LLAMA_OK) s = view_of(kv, dtype, G, D, &pv);
   if (s != LLAMA_OK) return s;
   if (batch->n_seqs == 0 || batch->n_tokens == 0) return LLAMA_OK;
-  s = check_all({q, o, kv->k, kv->v, kv->page_table, batch->q_offsets, batch->kv_lens});
+  s = check_all({q, o, kv->k, kv->v}, 16);
+  if (s == LLAMA_OK) s = check_all({kv->page_table, batch->q_offsets, batch->kv_lens}, 4);
   if (s == LLAMA_OK) s = check_status(status);
   if (s != LLAMA_OK) return s;
   const size_t need = llama_op_attention_packed_workspace_bytes(dtype, batch, H, G, D);
   if (need > 0) {
     if (workspace_bytes < need) return LLAMA_ERR_RANGE;
-    s = check(workspace);
+    s = check(workspace, 16);
     if (s != LLAMA_OK) return s;
   }
   cudaStream_t st = (cudaStream_t)stream;
@@ -196,13 +199,14 @@ llama_status llama_op_attention_paged_decode(int32_t dtype, const void *q, const
   if (s == LLAMA_OK) s = view_of(kv, dtype, G, D, &pv);
   if (s != LLAMA_OK) return s;
   if (n_seqs == 0) return LLAMA_OK;
-  s = check_all({q, o, kv->k, kv->v, kv->page_table, kv_lens});
+  s = check_all({q, o, kv->k, kv->v}, 16);
+  if (s == LLAMA_OK) s = check_all({kv->page_table, kv_lens}, 4);
   if (s == LLAMA_OK) s = check_status(status);
   if (s != LLAMA_OK) return s;
   const size_t need = llama_op_attention_paged_decode_workspace_bytes(dtype, n_seqs, max_kv_len, H, G, D);
   if (need > 0) {
     if (workspace_bytes < need) return LLAMA_ERR_RANGE;
-    s = check(workspace);
+    s = check(workspace, 16);
     if (s != LLAMA_OK) return s;
   }
   cudaStream_t st = (cudaStream_t)stream;
@@ -221,10 +225,10 @@ llama_status llama_op_token_logprobs(int32_t dtype, const void *logits, int64_t 
   if (top_k > V) return LLAMA_ERR_RANGE;
   if (top_k > LLAMA_LOGPROBS_MAX_TOP) return LLAMA_ERR_UNSUPPORTED;
   if (T == 0) return LLAMA_OK;
-  llama_status s = check(logits);
-  if (s == LLAMA_OK && logprobs != nullptr) s = check_all({targets, logprobs});
-  if (s == LLAMA_OK && entropy != nullptr) s = check(entropy);
-  if (s == LLAMA_OK && top_k > 0) s = check_all({top_ids, top_logprobs});
+  llama_status s = check(logits, (unsigned)esize(dtype));
+  if (s == LLAMA_OK && logprobs != nullptr) s = check_all({targets, logprobs}, 4);
+  if (s == LLAMA_OK && entropy != nullptr) s = check(entropy, 4);
+  if (s == LLAMA_OK && top_k > 0) s = check_all({top_ids, top_logprobs}, 4);
   if (s == LLAMA_OK) s = check_status(status);
   if (s != LLAMA_OK) return s;
   cudaStream_t st = (cudaStream_t)stream;

@@ -192,6 +192,12 @@ llama_status check_ptr(const void *p) {
   if (!is_device_ptr(p)) return LLAMA_ERR_INVALID_ARG;
   return LLAMA_OK;
 }
+// Of arrays whose 4-byte elements are read or written one at a time.
+llama_status check_elements(const void *p) {
+  if (p == nullptr) return LLAMA_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(p) % 4 != 0) return LLAMA_ERR_ALIGN;
+  return is_device_ptr(p) ? LLAMA_OK : LLAMA_ERR_INVALID_ARG;
+}
 
 llama_status validate_config(const llama_config *c, Dims *dm) {
   if (c == nullptr) return LLAMA_ERR_INVALID_ARG;
@@ -1035,13 +1041,13 @@ llama_status llama_stack_score(llama_stack *stk, const int32_t *tokens, int32_t 
   if (top_k > LLAMA_LOGPROBS_MAX_TOP) return LLAMA_ERR_UNSUPPORTED;
   llama_status s = LLAMA_OK;
   if (logprobs != nullptr) {
-    s = check_ptr(targets);
-    if (s == LLAMA_OK) s = check_ptr(logprobs);
+    s = check_elements(targets);
+    if (s == LLAMA_OK) s = check_elements(logprobs);
   }
-  if (s == LLAMA_OK && entropy != nullptr) s = check_ptr(entropy);
+  if (s == LLAMA_OK && entropy != nullptr) s = check_elements(entropy);
   if (s == LLAMA_OK && top_k > 0) {
-    s = check_ptr(top_ids);
-    if (s == LLAMA_OK) s = check_ptr(top_logprobs);
+    s = check_elements(top_ids);
+    if (s == LLAMA_OK) s = check_elements(top_logprobs);
   }
   if (s == LLAMA_OK) s = llama_stack_forward(stk, tokens, B, S, start_pos, kv, logits, stream);
   if (s != LLAMA_OK) return s;

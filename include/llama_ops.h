@@ -123,7 +123,8 @@ llama_status llama_op_attention_decode_noalloc(const void *q, const llama_kv_cac
  * goes on as described below; nothing is read or written out of range.
  *
  * Every pointer belongs to the device that is current (LLAMA_ERR_INVALID_ARG
- * otherwise).  Calls allocate nothing, keep nothing between calls and can be
+ * otherwise).  q_offsets, kv_lens, page_table and status need the alignment of
+ * their elements only, the rest 16 bytes (LLAMA_ERR_ALIGN).  Calls allocate nothing, keep nothing between calls and can be
  * captured into a CUDA graph; a replay reads the lengths, offsets and page ids
  * as they are then, within the bounds given on the host at capture.  A
  * workspace may hold anything before a call and is scratch after it: calls that
@@ -240,7 +241,8 @@ llama_status llama_op_set_wait_budget(int64_t cycles);
 
 /* Log-probabilities of given tokens, with the entropy of each distribution and
  * its likeliest tokens.  logits: [T][V] of dtype, rows row_stride elements
- * apart (>= V; columns at and behind V are not read; rows need no alignment).
+ * apart (>= V; columns at and behind V are not read).  Every array of this call
+ * needs the alignment of its elements only.
  * With p = softmax(logits[t]):
  *   logprobs[t]        = ln p[targets[t]]          (fp32)
  *   entropy[t]         = -sum_v p[v] ln p[v]       (fp32; NULL: not computed)

@@ -1,4 +1,5 @@
 """Host-side checks of the packed / paged operators beside those of test_packed_cpu.py."""
+import ctypes
 import os
 
 import pytest
@@ -35,3 +36,12 @@ def test_packed_workspace_holds_no_parts_that_cannot_be(lb, G, n_tokens, n_seqs,
         blocks = n_tokens // (2 * (128 // r)) + n_seqs
         n = lb.llama_op_attention_packed_workspace_bytes(lb.LLAMA_BF16, _batch(lb, n_seqs, n_tokens, max_kv), G * r, G, D)
         assert 32 * blocks < n < 32 * blocks + (64 << 10), (r, D)
+
+
+def test_elements_have_to_be_aligned(lb):
+    host = (ctypes.c_char * 4096)()
+    at = (ctypes.addressof(host) + 15) & ~15
+    for dtype, off, expected in ((lb.LLAMA_F32, 2, lb.LLAMA_ERR_ALIGN), (lb.LLAMA_BF16, 1, lb.LLAMA_ERR_ALIGN),
+                                 (lb.LLAMA_F32, 4, lb.LLAMA_ERR_INVALID_ARG),   # host memory, met next
+                                 (lb.LLAMA_BF16, 2, lb.LLAMA_ERR_INVALID_ARG)):
+        assert lb.llama_op_token_logprobs(dtype, at + off, 10, at, 2, 10, at) == expected
