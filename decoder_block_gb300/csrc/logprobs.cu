@@ -564,9 +564,7 @@ cudaError_t launch_token_logprobs(const T *logits, long long row_stride, const i
                                   float *logprobs, float *entropy, int top_k, int *top_ids, float *top_logprobs,
                                   int *status, int bad_target, cudaStream_t st) {
   if (rows <= 0) return cudaSuccess;
-  int dev = 0, sms = 0;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const int sms = sm_count();
   LpArgs a;
   a.logits = logits;
   a.stride = row_stride;

@@ -836,13 +836,6 @@ __global__ void __launch_bounds__(256) decode_join_kernel(const PdPlan *plan, co
   }
 }
 
-int sm_count() {
-  int dev = 0, sms = 0;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  return sms > 0 ? sms : 1;
-}
-
 // Clusters of a size that run at once: 152 SMs hold 15 of eight CTAs and 36 of four (16
 // sequences of 1024 keys as clusters of eight take two turns: 18 us for 10.8).
 int clusters_at_once(int cluster, int sms) {

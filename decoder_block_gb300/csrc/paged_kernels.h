@@ -51,6 +51,14 @@ class ClusterRoom {
   int known_[DEVICES][MOST + 1] = {};
 };
 
+// SMs of the current device, by which work is split and workspaces sized; 1 without a GPU.
+inline int sm_count() {
+  int dev = 0, sms = 0;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return sms > 0 ? sms : 1;
+}
+
 // Budget of a wait in the packed and paged-decode attention kernels, in SM clock cycles
 // (llama_op_set_wait_budget).
 long long op_wait_cycles();

@@ -14,9 +14,9 @@ namespace {
 
 constexpr int KEYS = 64;        // keys of a tile
 constexpr int THREADS = 256;
-// CTAs that the splits aim at: 16 per SM.  max_kv_len stands for every sequence, so in a
+// CTAs per SM that the splits aim at.  max_kv_len stands for every sequence, so in a
 // ragged batch most of them find no keys (16 against 4 per SM: 147 us for 266).
-constexpr int SM_CTAS = 16 * 152;
+constexpr int SM_CTAS = 16;
 
 // Split of the keys over CTAs: parts of `chunk` keys, `n` of them at the longest
 // length that the call allows.
@@ -24,7 +24,8 @@ struct Split {
   int chunk = KEYS, n = 1;
 };
 Split split_of(long long ctas, int max_kv_len, int least) {
-  const long long want = (SM_CTAS + ctas - 1) / ctas, most = (max_kv_len + least - 1) / least;
+  const long long aim = (long long)SM_CTAS * sm_count();
+  const long long want = (aim + ctas - 1) / ctas, most = (max_kv_len + least - 1) / least;
   const int n = (int)(want < most ? want : most > 1 ? most : 1);
   Split s;
   s.chunk = ((max_kv_len + n - 1) / n + KEYS - 1) / KEYS * KEYS;

@@ -164,9 +164,7 @@ cudaError_t launch_rope_kv_paged(const T *qkv, T *q_out, T *k, T *v, const Paged
   for (a.unit_log2 = 0; (2 * V) << a.unit_log2 < D; ++a.unit_log2) {
   }
   // few rows: one per CTA, many: enough per CTA that a thread has several units to move
-  int dev = 0, sms = 0;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const int sms = sm_count();
   a.rows = 1;
   while (a.rows < PW_ROWS && b.n_tokens / (2 * a.rows) >= 4 * sms) a.rows *= 2;
   count_launch();

@@ -45,3 +45,15 @@ def test_elements_have_to_be_aligned(lb):
                                  (lb.LLAMA_F32, 4, lb.LLAMA_ERR_INVALID_ARG),   # host memory, met next
                                  (lb.LLAMA_BF16, 2, lb.LLAMA_ERR_INVALID_ARG)):
         assert lb.llama_op_token_logprobs(dtype, at + off, 10, at, 2, 10, at) == expected
+
+
+def test_fp32_parts_follow_the_sms_of_the_device(lb):
+    torch = pytest.importorskip("torch")
+    sms = torch.cuda.get_device_properties(0).multi_processor_count if torch.cuda.is_available() else 1
+    kv, H, G, D = 1 << 20, 8, 4, 64
+    for n_seqs in (1, 3, 40, 1000):
+        want = -(-16 * sms // (n_seqs * G))  # parts that make 16 CTAs per SM
+        chunk = -(-(-(-kv // want)) // 64) * 64
+        parts = -(-kv // chunk)
+        assert lb.llama_op_attention_paged_decode_workspace_bytes(lb.LLAMA_F32, n_seqs, kv, H, G, D) == (
+            n_seqs * H * parts * (D + 2) * 4 if parts > 1 else 0)
