@@ -276,7 +276,9 @@ struct TopList {
   }
 };
 
-constexpr int LP_WAIT = 32 + 512;  // candidates of a warp: fewer than 32 wait, 16 per lane join them
+// Candidates of a warp: fewer than 32 wait, a vector's logits of each lane join them.
+template <typename T>
+constexpr int LP_WAIT = 32 + 32 * Vec16<T>::N;
 
 // The second pass over a warp's part of a row: everything that reaches `bound` and is
 // ahead of the k-th entry of the warp's list waits in `wait` and is sorted into the
@@ -399,7 +401,7 @@ template <typename T, int WPR>
 __global__ void __launch_bounds__(LP_THREADS, LP_CTAS) token_logprobs_kernel(const __grid_constant__ LpArgs a) {
   constexpr int V = Vec16<T>::N, GROUPS = LP_WARPS / WPR;  // rows of this CTA
   constexpr int CAP = WPR * 64, ENDS = 2 * (V - 1);        // candidates kept; logits outside whole vectors
-  __shared__ Cand s_wait[LP_WARPS][LP_WAIT];
+  __shared__ Cand s_wait[LP_WARPS][LP_WAIT<T>];
   __shared__ Cand s_all[GROUPS][CAP + ENDS];
   __shared__ Cand s_first[32];  // a CTA's top, for the cluster's first CTA
   __shared__ Stats s_stats[LP_WARPS];
