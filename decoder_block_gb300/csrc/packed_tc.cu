@@ -787,9 +787,8 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
         // One pass over the tile, 32 columns at a time.  p = 2^(s*scale - m_run)
         // uses the running maximum as it stands; a chunk whose own maximum exceeds
         // it by more than 2^8 first raises it, scaling the row sum, the P chunks
-        // already written for this tile and, once the tile is done, O.  It is raised to
-        // a whole number: the factor is a power of two and changes no bit of P that was
-        // rounded already.  P (bf16) lands over S columns already read.
+        // already written for this tile and, once the tile is done, O.  P (bf16)
+        // lands over S columns already read.
         const bool masked = __any_sync(0xffffffffu, key0 + PT_KEYS - 1 > pos);
         float alpha_tile = 1.f;
         bool rescaled = false;  // warp-uniform
@@ -815,10 +814,8 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
           if (__any_sync(0xffffffffu, need)) {
             float alpha = 1.f;
             if (need) {
-              const float up = ceilf(cms);
-              // 2^(m_run - up), 0 below the normal numbers
-              alpha = __int_as_float((127 + (int)fmaxf(m_run - up, -127.f)) << 23);
-              m_run = up;
+              alpha = ptx::ex2_approx(m_run - cms);
+              m_run = cms;
             }
             l2 = ptx::fmul2(l2, ptx::f2pack(alpha, alpha));
             alpha_tile *= alpha;
