@@ -31,9 +31,11 @@ namespace {
 constexpr int LP_THREADS = 256;
 constexpr int LP_WARPS = LP_THREADS / 32;
 // CTAs of an SM and 16-byte vectors of a lane's batch: 64 KB of an SM's loads in flight.
-// 2048 x 128256, top 20, fp32: 171 us (1.05 GB at 0.91 of the measured copy rate); with 3
-// CTAs 181, with 5 (spills) 252 us.  bf16, top 5: 104 us, 0.75 (the same number of logits in half
-// the bytes).
+// 2048 x 128256, top 20, fp32: 171 to 175 us (1.05 GB at 0.89 to 0.91 of the measured copy
+// rate); with 3 CTAs 181, with 5 252 us (64 registers spill 24 to 48 bytes of a thread, 48
+// registers 52 to 136).  bf16, top 5: 104 us, 0.75 (the same number of logits in half the bytes).
+// A row with fewer logits above -inf than top_k has no bound and is read twice: 419 us for 196
+// in a loop with a cold L2.
 constexpr int LP_CTAS = 4;
 constexpr int LP_VECS = 4;
 constexpr int LP_STEP = 32 * LP_VECS;  // vectors of a warp's batch

@@ -788,7 +788,11 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
         // uses the running maximum as it stands; a chunk whose own maximum exceeds
         // it by more than 2^8 first raises it, scaling the row sum, the P chunks
         // already written for this tile and, once the tile is done, O.  P (bf16)
-        // lands over S columns already read.
+        // lands over S columns already read.  Those chunks' P are rounded a second time
+        // by it; each is then below 2^-8 of the largest, 96 of them 0.27 of the row's sum at
+        // most.  (Raised by whole powers of two, which change no bit of P, the largest
+        // weight is no longer 1 and rounds too: 0.0019-0.0023 for 0.0011-0.0021 relative
+        // to 64-bit results on 18 batches.)
         const bool masked = __any_sync(0xffffffffu, key0 + PT_KEYS - 1 > pos);
         float alpha_tile = 1.f;
         bool rescaled = false;  // warp-uniform

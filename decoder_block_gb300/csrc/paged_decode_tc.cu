@@ -55,8 +55,8 @@ constexpr int PD_MAX_CLUSTER = 8;
 // 2000 39 for 34).
 constexpr int PD_CLUSTER_TILES = 15, PD_WHOLE_TILES = 12;
 constexpr int PD_ROUNDS = 12;       // chunks per SM that the planner aims at
-// Key tiles of a split sequence's chunk, at least: a chunk costs about as much as a tile
-// besides (4 sequences of 6000 keys on 8 KV heads, planned: 1: 31 us, 4: 23, 5: 21, 6: 22).
+// Key tiles that a split sequence's chunks may have, at least (6 make 3 + 3): a chunk costs
+// about as much as a tile besides (4 sequences of 6000 keys on 8 KV heads, planned: 1: 31 us, 4: 23, 5: 21, 6: 22).
 constexpr int PD_MIN_CHUNK = 5;
 // Sequences that every CTA cuts into chunks for itself, at most (one per lane): no kernel in
 // front, but chunks are dealt out in turn instead of taken (one sequence of 20000 keys on 8
@@ -127,8 +127,9 @@ struct PdArgs {
 
 // ------------------------------------------------------------------ plan ---
 // Key tiles of a chunk, at most: PD_ROUNDS chunks per SM, so that the last ones to finish
-// are short.  A sequence's chunks differ by no more than its last one is shorter.  Chunks of split sequences then number less than 2 * PD_ROUNDS * sms /
-// units, which sizes the workspace.
+// are short.  A sequence's chunks differ by no more than its last one is shorter.  Chunks
+// of split sequences then number less than 2 * PD_ROUNDS * sms / units, which sizes the
+// workspace.
 __device__ __forceinline__ int chunk_of(unsigned long long tiles, int units, int sms) {
   const unsigned long long share = (tiles * units + (unsigned)(PD_ROUNDS * sms) - 1) / (unsigned)(PD_ROUNDS * sms);
   return share > 65535 ? 65535 : share > PD_MIN_CHUNK ? (int)share : PD_MIN_CHUNK;  // no sequence is longer

@@ -167,7 +167,7 @@ typedef struct {
  * those tokens included, so that its new tokens are the last ones:  token t is
  * at position kv_lens[i] - (q_offsets[i + 1] - t).  Sequences without new
  * tokens are allowed.  Rows outside all sequences (padding behind the last one)
- * are neither read nor written.
+ * are not written, and what they hold has no effect.
  * max_kv_len: no kv_lens entry is larger (host value; it may be larger than any).
  * A sequence with bad offsets is left out (offsets that descend make others
  * overlap: the rows of o and q_out may then hold anything); a length that is
@@ -202,7 +202,10 @@ llama_status llama_op_rope_kv_write_paged(int32_t dtype, const void *qkv, void *
  * at or behind kv_lens[i] may hold anything, NaN included; the keys and values
  * before it have to be finite.  A query row that holds NaN or an infinity gives
  * NaN for its head where it sees a key; other rows and heads are as without it.
- * D in {16, 32, 64, 128}.
+ * D in {16, 32, 64, 128}.  Scores, statistics and sums are fp32; with LLAMA_BF16
+ * each softmax weight is rounded to bf16 for its product with V, here and in the
+ * decode call (here a second time where a later key of the same 128 outweighs it
+ * and all keys before by more than 2^8).
  * workspace: caller-owned device scratch of at least
  * llama_op_attention_packed_workspace_bytes bytes (which reads only n_seqs,
  * n_tokens and max_kv_len of batch; 0 for arguments that the call refuses); may
