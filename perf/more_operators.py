@@ -270,12 +270,15 @@ def _verify_state(gen, case):
     seq = torch.searchsorted(off[1:], row, right=True)
     has_draft = row + 1 < off[seq + 1]
     drow = row[has_draft]
-    draft = target[drow] + _normal(gen, (n_drafts, stride), dtype, std=0.7)
+    dseq = seq[drow]
+    step = drow - off[dseq]
+    draft = _normal(gen, (n, most, stride), dtype, std=0.7)  # a step of the draft model for all of its sequences each
+    draft[dseq, step] += target[drow]
     temps = [float(t) for t in case["temperatures"].split(",")]
     temps = torch.tensor([temps[i % len(temps)] for i in range(n)], device=_DEV)
     tokens = torch.randint(0, V, (rows,), device=_DEV, generator=gen, dtype=torch.int32)
     if n_drafts:
-        z = draft[:, :V].float() / temps[seq[drow]].clamp_min(0.05)[:, None]
+        z = draft[dseq, step, :V].float() / temps[dseq].clamp_min(0.05)[:, None]
         noise = torch.empty((n_drafts, V), device=_DEV).exponential_(generator=gen)
         picked = (z - torch.log(noise)).argmax(-1)
         if not case["draft_model"]:  # looked up: the likeliest token most of the time
@@ -283,9 +286,9 @@ def _verify_state(gen, case):
                                  target[drow, :V].float().argmax(-1), picked)
         tokens[drow + 1] = picked.to(torch.int32)
     target[:, V:] = float("nan")  # the padding of a row is never a logit
-    draft[:, V:] = float("nan")
+    draft[..., V:] = float("nan")
     # fp32 uniforms of 24 bits, and exponential variates above 0
-    uniforms = torch.rand(max(n_drafts, 1), device=_DEV, generator=gen)
+    uniforms = torch.rand((n, most), device=_DEV, generator=gen)
     noise = torch.empty((n, V), device=_DEV).exponential_(generator=gen).clamp_min(1e-30)
     return dict(target=target, draft=draft if case["draft_model"] else None, tokens=tokens, temps=temps,
                 uniforms=uniforms, noise=noise, offsets=off.to(torch.int32), most=most, n_drafts=n_drafts,
@@ -374,9 +377,9 @@ def _run_own(st):
                                                         c["D"], st["ws"], st["ws"].numel(), None, stream))
         return st["o"]
     if c["op"] == "verify":
-        lb.check(lb.llama_op_verify_drafts(st["code"], st["target"], c["stride"], st["draft"], c["stride"], c["V"],
-                                           st["batch"], st["out"], st["accepted"], st["logp"], st["ws"],
-                                           st["ws"].numel(), None, stream))
+        lb.check(lb.llama_op_verify_drafts(st["code"], st["target"], c["stride"], st["draft"], st["most"] * c["stride"],
+                                           c["stride"], c["V"], st["batch"], st["out"], st["accepted"], st["logp"],
+                                           st["ws"], st["ws"].numel(), None, stream))
         return st["out"], st["accepted"], st["logp"]
     if c["op"] == "write":
         layout = lb.LLAMA_ROPE_HALVES if c["layout"] == "halves" else lb.LLAMA_ROPE_INTERLEAVED
@@ -519,6 +522,7 @@ def _plain_verify(st):
     if n_drafts:
         drow = row[row + 1 < off[seq + 1]]
         dseq = seq[drow]
+        step = drow - off[dseq]
         drafted = st["tokens"][drow + 1].long()
 
         def log_p(x, m, z, at, t):
@@ -526,17 +530,17 @@ def _plain_verify(st):
 
         ratio = log_p(x[drow], m[drow], z[drow], drafted, temp[dseq])
         if st["draft"] is not None:
-            xd, md, ed, zd = softmax_parts(st["draft"], temp[dseq])
+            xd, md, ed, zd = softmax_parts(st["draft"][dseq, step], temp[dseq])
             ratio = ratio - log_p(xd, md, zd, drafted, temp[dseq])
-        ok = torch.where(greedy[dseq], best[drow].long() == drafted, st["uniforms"].double() < ratio.exp())
-        keep[dseq, drow - off[dseq]] = ok
+        ok = torch.where(greedy[dseq], best[drow].long() == drafted, st["uniforms"][dseq, step].double() < ratio.exp())
+        keep[dseq, step] = ok
     accepted = keep.long().cumprod(-1).sum(-1)
     last = off[:-1] + accepted                   # the row that the next token is drawn from
     p = e[last] / z[last, None].float()
     w = p
     if n_drafts:
         refused = last + 1 < off[1:]             # a draft was not kept: what it would have been drawn from goes
-        d = (last - torch.arange(n, device=_DEV)).clamp_max(n_drafts - 1)
+        d = (last - torch.arange(n, device=_DEV)).clamp_max(n_drafts - 1)  # its place among all drafts
         if st["draft"] is not None:
             q = ed[d] / zd[d, None].float()
         else:
@@ -570,7 +574,9 @@ def work(case):
         temps = [float(t) for t in case["temperatures"].split(",")]
         n, rows = len(drafts), sum(drafts) + len(drafts)
         drawn = sum(temps[i % len(temps)] > 0 for i in range(n))
-        read = rows + (sum(drafts) if case["draft_model"] else 0)
+        read = rows
+        if case["draft_model"]:
+            read += sum(d for i, d in enumerate(drafts) if temps[i % len(temps)] > 0)
         return dict(bytes=read * V * e + drawn * V * 4 + rows * 12 + n * (max(max(drafts), 1) + 1) * 8,
                     flops=4 * read * V + 4 * drawn * V)
     G, D = case["G"], case["D"]
@@ -628,14 +634,14 @@ def _exact_held(x):
 def _exact_verify(case, st):
     V, f64 = case["V"], torch.float64
     off, drafts = st["offsets"].tolist(), _ints(case["drafts"])
-    out, acc, logp = torch.full_like(st["out"], -1), torch.zeros_like(st["accepted"]), torch.zeros_like(st["logp"], dtype=f64)
+    out, acc = torch.full_like(st["out"], -1), torch.zeros_like(st["accepted"])
+    logp = torch.zeros_like(st["logp"], dtype=f64)
     tokens, uniforms, temps = st["tokens"].tolist(), st["uniforms"].tolist(), st["temps"].double().tolist()
     for i, n in enumerate(drafts):
         t = temps[i] or 1.0
         x = st["target"][off[i]:off[i + 1], :V].to(f64)
         lp = torch.log_softmax(x / t, -1)
-        d0 = off[i] - i
-        lq = torch.log_softmax(st["draft"][d0:d0 + n, :V].to(f64) / t, -1) if case["draft_model"] else None
+        lq = torch.log_softmax(st["draft"][i, :n, :V].to(f64) / t, -1) if case["draft_model"] else None
         top = torch.sort(x, dim=-1, descending=True, stable=True).indices[:, 0].tolist()
         j = 0
         while j < n:
@@ -644,7 +650,7 @@ def _exact_verify(case, st):
                 kept = top[j] == tok
             else:
                 q = float(lq[j, tok]) if lq is not None else 0.0
-                kept = uniforms[d0 + j] < math.exp(float(lp[j, tok]) - q)
+                kept = uniforms[i][j] < math.exp(float(lp[j, tok]) - q)
             if not kept:
                 break
             out[i, j] = tok
