@@ -75,6 +75,12 @@ class llama_packed_batch(ctypes.Structure):
                 ("max_kv_len", c_int32)]
 
 
+class llama_draft_batch(ctypes.Structure):
+    _fields_ = [("q_offsets", c_void_p), ("tokens", c_void_p), ("temperatures", c_void_p), ("uniforms", c_void_p),
+                ("noise", c_void_p), ("noise_stride", c_int64), ("n_seqs", c_int32), ("n_rows", c_int32),
+                ("max_drafts", c_int32)]
+
+
 _lib = None
 
 
@@ -141,6 +147,25 @@ def load() -> ctypes.CDLL:
         "llama_op_attention_paged_decode": (st, [c_int32, c_void_p, POINTER(llama_paged_kv_cache), c_void_p, c_int32,
                                                  c_int32, c_void_p, c_int32, c_int32, c_int32, c_void_p, c_size_t,
                                                  c_void_p, c_void_p]),
+        "llama_kv4_block_bytes": (c_size_t, [c_int32, c_int32]),
+        "llama_op_rope_kv4_write_paged": (st, [c_int32, c_void_p, c_void_p, POINTER(llama_paged_kv_cache),
+                                               POINTER(llama_packed_batch), c_void_p, c_int32, c_int32, c_int32, c_int32,
+                                               c_int32, c_void_p, c_void_p]),
+        "llama_op_kv4_read_paged": (st, [c_int32, POINTER(llama_paged_kv_cache), POINTER(llama_packed_batch), c_void_p,
+                                         c_void_p, c_int32, c_int32, c_void_p, c_void_p]),
+        "llama_op_attention_packed_kv4_workspace_bytes": (c_size_t, [c_int32, POINTER(llama_packed_batch), c_int32,
+                                                                     c_int32, c_int32]),
+        "llama_op_attention_packed_kv4": (st, [c_int32, c_void_p, POINTER(llama_paged_kv_cache),
+                                               POINTER(llama_packed_batch), c_void_p, c_int32, c_int32, c_int32,
+                                               c_void_p, c_size_t, c_void_p, c_void_p]),
+        "llama_op_attention_paged_decode_kv4_workspace_bytes": (c_size_t, [c_int32] * 6),
+        "llama_op_attention_paged_decode_kv4": (st, [c_int32, c_void_p, POINTER(llama_paged_kv_cache), c_void_p, c_int32,
+                                                     c_int32, c_void_p, c_int32, c_int32, c_int32, c_void_p, c_size_t,
+                                                     c_void_p, c_void_p]),
+        "llama_op_verify_drafts_workspace_bytes": (c_size_t, [POINTER(llama_draft_batch), c_int32]),
+        "llama_op_verify_drafts": (st, [c_int32, c_void_p, c_int64, c_void_p, c_int64, c_int64, c_int32,
+                                        POINTER(llama_draft_batch), c_void_p, c_void_p, c_void_p, c_void_p, c_size_t,
+                                        c_void_p, c_void_p]),
         "llama_op_set_wait_budget": (st, [c_int64]),
         "llama_op_token_logprobs": (st, [c_int32, c_void_p, c_int64, c_void_p, c_int32, c_int32, c_void_p, c_void_p,
                                          c_int32, c_void_p, c_void_p, c_void_p, c_void_p]),
@@ -420,6 +445,59 @@ def llama_op_attention_paged_decode(dtype, q, kv: llama_paged_kv_cache, kv_lens,
                                                   G, D, _p(workspace), workspace_bytes, _p(status), _stream(stream))
 
 
+def llama_kv4_block_bytes(page_size, d_head) -> int:
+    return load().llama_kv4_block_bytes(page_size, d_head)
+
+
+def make_paged_kv4_cache(k, v, page_table, page_size) -> llama_paged_kv_cache:
+    """Struct of a pool of pages held in 4 bits: k, v uint8 tensors [n_pages][n_kv_heads][block bytes] (see
+    llama_kv4_block_bytes; dense within a page, the same stride from page to page), page_table as for
+    make_paged_kv_cache."""
+    for x in (k, v):
+        if x.element_size() != 1 or x.dim() != 3 or x.stride(-1) != 1 or (x.shape[1] > 1 and x.stride(1) != x.shape[2]):
+            raise ValueError("make_paged_kv4_cache: pools are bytes [n_pages][n_kv_heads][block], dense within a page")
+    if k.shape != v.shape or (k.shape[0] > 1 and k.stride(0) != v.stride(0)):
+        raise ValueError("make_paged_kv4_cache: k and v need one shape and page stride")
+    if k.shape[2] not in [llama_kv4_block_bytes(page_size, d) for d in (16, 32, 64, 128)]:
+        raise ValueError("make_paged_kv4_cache: a block is llama_kv4_block_bytes(page_size, d_head) bytes")
+    _need_int32("make_paged_kv4_cache", page_table)
+    return llama_paged_kv_cache(_p(k), _p(v), _p(page_table), k.shape[0], page_size, page_table.shape[1],
+                                page_table.stride(0), k.stride(0))
+
+
+def llama_op_rope_kv4_write_paged(dtype, qkv, q_out, kv: llama_paged_kv_cache, batch: llama_packed_batch, table,
+                                  table_max_seq, H, G, D, layout=0, status=None, stream=None) -> int:
+    return load().llama_op_rope_kv4_write_paged(dtype, _p(qkv), _p(q_out), byref(kv), byref(batch), _p(table),
+                                                table_max_seq, H, G, D, layout, _p(status), _stream(stream))
+
+
+def llama_op_kv4_read_paged(dtype, kv: llama_paged_kv_cache, batch: llama_packed_batch, k_out, v_out, G, D, status=None,
+                            stream=None) -> int:
+    return load().llama_op_kv4_read_paged(dtype, byref(kv), byref(batch), _p(k_out), _p(v_out), G, D, _p(status),
+                                          _stream(stream))
+
+
+def llama_op_attention_packed_kv4_workspace_bytes(dtype, batch: llama_packed_batch, H, G, D) -> int:
+    return load().llama_op_attention_packed_kv4_workspace_bytes(dtype, byref(batch), H, G, D)
+
+
+def llama_op_attention_packed_kv4(dtype, q, kv: llama_paged_kv_cache, batch: llama_packed_batch, o, H, G, D,
+                                  workspace=None, workspace_bytes=0, status=None, stream=None) -> int:
+    return load().llama_op_attention_packed_kv4(dtype, _p(q), byref(kv), byref(batch), _p(o), H, G, D, _p(workspace),
+                                                workspace_bytes, _p(status), _stream(stream))
+
+
+def llama_op_attention_paged_decode_kv4_workspace_bytes(dtype, n_seqs, max_kv_len, H, G, D) -> int:
+    return load().llama_op_attention_paged_decode_kv4_workspace_bytes(dtype, n_seqs, max_kv_len, H, G, D)
+
+
+def llama_op_attention_paged_decode_kv4(dtype, q, kv: llama_paged_kv_cache, kv_lens, n_seqs, max_kv_len, o, H, G, D,
+                                        workspace=None, workspace_bytes=0, status=None, stream=None) -> int:
+    return load().llama_op_attention_paged_decode_kv4(dtype, _p(q), byref(kv), _p(kv_lens), n_seqs, max_kv_len, _p(o),
+                                                      H, G, D, _p(workspace), workspace_bytes, _p(status),
+                                                      _stream(stream))
+
+
 def llama_op_set_wait_budget(cycles: int) -> int:
     return load().llama_op_set_wait_budget(cycles)
 
@@ -428,6 +506,42 @@ def llama_op_token_logprobs(dtype, logits, row_stride, targets, T, V, logprobs, 
                             top_logprobs=None, status=None, stream=None) -> int:
     return load().llama_op_token_logprobs(dtype, _p(logits), row_stride, _p(targets), T, V, _p(logprobs), _p(entropy),
                                           top_k, _p(top_ids), _p(top_logprobs), _p(status), _stream(stream))
+
+
+LLAMA_MAX_DRAFTS = 64
+
+
+def make_draft_batch(q_offsets, tokens, n_rows, max_drafts, temperatures=None, uniforms=None,
+                     noise=None) -> llama_draft_batch:
+    """Struct of a batch of drafts: q_offsets int32 [n_seqs + 1], tokens int32 [n_rows], temperatures fp32 [n_seqs],
+    uniforms fp32 [n_seqs][max_drafts], noise fp32 [n_seqs][V] (dense rows); device tensors."""
+    _need_int32("make_draft_batch", q_offsets, tokens)
+    n = q_offsets.shape[0] - 1
+    if tokens.shape[0] < n_rows:
+        raise ValueError("make_draft_batch: tokens has an entry for every row")
+    for what, x in (("temperatures", temperatures), ("uniforms", uniforms), ("noise", noise)):
+        if x is None:
+            continue
+        if x.element_size() != 4 or not x.is_floating_point() or x.shape[0] != n or (x.shape[-1] > 1 and x.stride(-1) != 1):
+            raise ValueError(f"make_draft_batch: {what} is fp32, a dense row for every sequence")
+    if uniforms is not None and max_drafts > 0 and (uniforms.dim() != 2 or uniforms.shape[1] != max_drafts
+                                                    or (n > 1 and uniforms.stride(0) != max_drafts)):
+        raise ValueError("make_draft_batch: uniforms is [n_seqs][max_drafts]")
+    stride = 0 if noise is None else noise.stride(0) if n > 1 else noise.shape[1]
+    return llama_draft_batch(_p(q_offsets), _p(tokens), _p(temperatures), _p(uniforms), _p(noise), stride, n, n_rows,
+                             max_drafts)
+
+
+def llama_op_verify_drafts_workspace_bytes(batch: llama_draft_batch, V) -> int:
+    return load().llama_op_verify_drafts_workspace_bytes(byref(batch), V)
+
+
+def llama_op_verify_drafts(dtype, target_logits, target_stride, draft_logits, draft_seq_stride, draft_step_stride, V,
+                           batch: llama_draft_batch, out_tokens, n_accepted, logprobs=None, workspace=None,
+                           workspace_bytes=0, status=None, stream=None) -> int:
+    return load().llama_op_verify_drafts(dtype, _p(target_logits), target_stride, _p(draft_logits), draft_seq_stride,
+                                         draft_step_stride, V, byref(batch), _p(out_tokens), _p(n_accepted),
+                                         _p(logprobs), _p(workspace), workspace_bytes, _p(status), _stream(stream))
 
 
 def check(status: int, what: str = "llama call") -> None:

@@ -1,0 +1,113 @@
+// Rows of keys and values held in 4 bits, a scale for 16 of them (llama_ops.h describes
+// the blocks): sizes, reading and writing.
+//
+// The scale's byte is the top of an fp32 or bf16 number -- three bits of mantissa under
+// an exponent that starts at -20 -- so that it turns into one with an add and a shift,
+// reaches from 2^-20 to 3840 without a factor per tensor, and a code times it has seven
+// significant bits: bf16 holds every value exactly.  Equal steps lose less of such
+// blocks than fp4's do (normal values: an error of 0.093 of their RMS for 0.095 to 0.100).
+#pragma once
+
+#include <stdint.h>
+
+#include "common.cuh"
+#include "paged.cuh"
+
+namespace llama {
+
+constexpr int KV4_BLOCK = 16;                  // elements of a scale
+constexpr int KV4_SCALE_BASE = (127 - 20) << 3;  // a scale byte plus this: sign, exponent and three bits of an fp32
+constexpr float KV4_LEVELS = 7.0f;             // codes stored are 8 - 7 .. 8 + 7
+constexpr float KV4_MOST = 7.0f * 3840.0f;
+
+__host__ __device__ constexpr int kv4_code_bytes(int D) { return D / 2; }
+__host__ __device__ constexpr int kv4_scale_bytes(int D) { return D / KV4_BLOCK; }
+__host__ __device__ constexpr int kv4_block_bytes(int page_size, int D) {
+  return page_size * (kv4_code_bytes(D) + kv4_scale_bytes(D));
+}
+
+// Where a row of a page lies.
+struct Kv4Row {
+  const uint8_t *codes = nullptr;  // null: zeros
+  const uint8_t *scales = nullptr;
+  __device__ __forceinline__ bool operator!=(decltype(nullptr)) const { return codes != nullptr; }
+};
+__device__ __forceinline__ long long kv4_block_at(const PagedView &pv, int page, int g, int D) {
+  return page * pv.page_stride + (long long)g * kv4_block_bytes(1 << pv.page_log2, D);
+}
+__device__ __forceinline__ Kv4Row kv4_row(const uint8_t *pool, const PagedView &pv, int page, int g, int D, int slot) {
+  Kv4Row r;
+  const uint8_t *block = pool + kv4_block_at(pv, page, g, D);
+  r.codes = block + slot * kv4_code_bytes(D);
+  r.scales = block + (kv4_code_bytes(D) << pv.page_log2) + slot * kv4_scale_bytes(D);
+  return r;
+}
+
+__device__ __forceinline__ float kv4_scale(uint32_t byte) { return __uint_as_float((byte + KV4_SCALE_BASE) << 20); }
+// The scale twice, as bf16, from two bytes (low half: `a`).
+__device__ __forceinline__ uint32_t kv4_scale2(uint32_t a, uint32_t b) {
+  return ((a + KV4_SCALE_BASE) << 4) | ((b + KV4_SCALE_BASE) << 20);
+}
+
+__device__ __forceinline__ uint32_t bf16x2_fma(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t d;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+  return d;
+}
+__device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// A code n under bf16's mantissa reads as 16 + n (bits 3 to 6 of 16.0 = 0x4180); times s and
+// less 24 s, in one rounding that has nothing to round, it is (n - 8) s.  24 s has five
+// significant bits; with the code in the lowest bits, 128 + n, 136 s would have up to nine
+// and not be a bf16.
+constexpr uint32_t KV4_MASK = 0x00780078u, KV4_MAGIC = 0x41804180u;
+__device__ __forceinline__ uint32_t kv4_bias2(uint32_t scale2) { return bf16x2_mul(scale2, 0xc1c0c1c0u); }  // -24 s
+// Codes in bits 4 j .. and 4 j + 16 .. of a word (elements 2 j and 2 j + 1 of its eight).
+template <int J>
+__device__ __forceinline__ uint32_t kv4_pair(uint32_t w, uint32_t scale2, uint32_t bias2) {
+  const uint32_t at = J == 0 ? w << 3 : w >> (J == 0 ? 0 : 4 * J - 3);
+  return bf16x2_fma((at & KV4_MASK) | KV4_MAGIC, scale2, bias2);
+}
+// Eight elements as bf16.
+__device__ __forceinline__ uint4 kv4_eight(uint32_t w, uint32_t scale2, uint32_t bias2) {
+  return make_uint4(kv4_pair<0>(w, scale2, bias2), kv4_pair<1>(w, scale2, bias2), kv4_pair<2>(w, scale2, bias2),
+                    kv4_pair<3>(w, scale2, bias2));
+}
+// Four elements 4 (c % 2) .. of eight as fp32.
+__device__ __forceinline__ float4 kv4_four(uint32_t w, int half, float scale) {
+  w >>= 8 * half;
+  return make_float4((float)((int)(w & 15) - 8) * scale, (float)((int)(w >> 16 & 15) - 8) * scale,
+                     (float)((int)(w >> 4 & 15) - 8) * scale, (float)((int)(w >> 20 & 15) - 8) * scale);
+}
+
+// A block of 16 values: its scale byte and codes (two words).  `bad` is set for a NaN or a
+// magnitude beyond KV4_MOST.
+__device__ __forceinline__ uint32_t kv4_quantise(const float *x, uint32_t (&words)[2], bool &bad) {
+  float most = 0.f;
+  bool nan = false;
+#pragma unroll
+  for (int e = 0; e < KV4_BLOCK; ++e) {
+    most = fmaxf(most, fabsf(x[e]));  // (NaN is left out)
+    nan |= x[e] != x[e];
+  }
+  bad |= nan || most > KV4_MOST;
+  // the smallest three-bit mantissa at or above most / 7: round the fp32's bits up
+  const int up = (int)((__float_as_uint(__fdiv_rn(most, KV4_LEVELS)) + 0xfffffu) >> 20) - KV4_SCALE_BASE;
+  const uint32_t byte = (uint32_t)min(max(up, 0), 255);
+  const float s = kv4_scale(byte);
+  words[0] = words[1] = 0;
+#pragma unroll
+  for (int e = 0; e < KV4_BLOCK; ++e) {
+    // NaN becomes -7 by the clamp and 0 by the choice
+    const float n = fminf(fmaxf(rintf(__fdiv_rn(x[e], s)), -KV4_LEVELS), KV4_LEVELS);
+    const uint32_t code = (uint32_t)((x[e] != x[e] ? 0 : (int)n) + 8);
+    words[e / 8] |= code << (4 * (e % 8 / 2) + 16 * (e % 2));
+  }
+  return byte;
+}
+
+}  // namespace llama

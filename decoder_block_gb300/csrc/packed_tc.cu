@@ -30,12 +30,16 @@
 //     outlast the rest (few query rows against many keys) it splits their keys
 //     into pieces; a piece leaves fp32 (O, m, l) per row in the workspace, and a
 //     third kernel joins them in piece order, so results do not depend on timing.
+// Pages held in 4 bits: the four loading warps copy a tile's codes and scales into shared
+// memory a stage ahead, and write the bf16 that they stand for where the copies above
+// would have put them; nothing else differs.
 // Every wait is bounded (llama_op_set_wait_budget).  A CTA that gives up records
 // LLAMA_ERR_DEVICE_TIMEOUT and leaves once its copies, MMAs and tensor memory stores in
 // flight are done; the four loading warps each arm the bytes they are about to ask for.
 #include <cudaTypedefs.h>
 #include <float.h>
 
+#include "kv4.cuh"
 #include "paged_kernels.h"
 #include "ptx.cuh"
 
@@ -61,8 +65,8 @@ struct PtLayout {
   static constexpr int OFF_ITEM = OFF_V + PT_STAGES * TILE;  // PtItem
   static constexpr int OFF_BAR = OFF_ITEM + 64;
   // q_full, q_empty, fin, kv_full[2], kv_empty[2], s_full[3], p_full[3], o_done[2],
-  // i_full, near_end (16-row pages)
-  static constexpr int NBAR = 3 + 2 * PT_STAGES + 8 + 2;
+  // i_full, near_end (16-row pages and 4-bit ones), k_first (4-bit pages)
+  static constexpr int NBAR = 3 + 2 * PT_STAGES + 8 + 3;
   // S buffers of 128 columns in tensor memory, then O of both query tiles.  With D = 64
   // there is room for a third: a query tile's next S is ready when its softmax is done
   // with this one (S = 8192, 32 heads: 306 us for 324).  With D = 128 the next S goes where
@@ -73,6 +77,19 @@ struct PtLayout {
   static constexpr int BYTES = BYTES_MIN > 116 * 1024 ? BYTES_MIN : 116 * 1024;
   static constexpr uint32_t TMEM_COLS = 512;
   static constexpr uint32_t O_COL = S_BUFS * 128;
+};
+
+// Shared memory of a kernel; W: head width of 4-bit pages (0: bf16 pages).  Codes and scales
+// on their way come behind everything else: FILLS stages of [4 warps][V, K][32 rows].
+template <int D, int W>
+struct PtShared {
+  static constexpr int FILLS = D == 128 ? 1 : 3;
+  static constexpr int ROWS = 32 * kv4_code_bytes(W), SCALES = 32 * kv4_scale_bytes(W);  // of a warp, K or V
+  static constexpr int WARP = 2 * (ROWS + SCALES);
+  static constexpr int OFF_CODES = (PtLayout<D>::BYTES_MIN - 1024 + 15) / 16 * 16;
+  static constexpr int END = 1024 + OFF_CODES + FILLS * 4 * WARP;
+  static constexpr int BYTES = W == 0 ? PtLayout<D>::BYTES : END > PtLayout<D>::BYTES ? END : PtLayout<D>::BYTES;
+  static_assert(BYTES <= 227 * 1024, "fits an SM");
 };
 
 // A work item as the producer hands it to the other roles.
@@ -115,6 +132,7 @@ struct PtArgs {
   PtPlan *plan;          // null: direct
   PtEntry *entries;
   float *part;           // [slot][unit][2 tiles][4 warps][D + 2][32 rows]
+  const uint8_t *kc, *vc;  // pools of 4-bit blocks
   int *status;
   long long wait_cycles;  // a wait's budget
 };
@@ -371,9 +389,158 @@ struct StageLoads {
   }
 };
 
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy8(uint32_t dst, const void *src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared16(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ uint2 ld_shared8(uint32_t at) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_shared_u16(uint32_t at) {
+  uint16_t v;
+  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_shared_u8(uint32_t at) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(at));
+  return v;
+}
+__device__ __forceinline__ void st_shared16(uint32_t at, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// One warp's part of the stages over 4-bit pages: rows 32 warp .. + 31 of every tile, V and K
+// apart.  An item of n key tiles has fills 0 to n: fill f brings V of its tile f - 1 and K of
+// its tile f (the first and last lack one), as the stages do.
+//   request(f)  copies codes and scales to shared memory; a lane's 16 bytes of codes are
+//               its own again in unpack, the scales are shared by the warp
+//   unpack      writes their bf16 where a TMA box would have put them.  Lanes of the right
+//               half of a 128-wide row take their chunks in another order, so that the
+//               eight lanes of a store meet in no bank.
+// Rows behind the sequence's last key may hold any codes: those are finite numbers, and their
+// weights are 0.
+template <int D, int W>
+struct Unpacker {
+  using L = PtLayout<D>;
+  using S = PtShared<D, W>;
+  static constexpr int RB = kv4_code_bytes(W), SB = kv4_scale_bytes(W);
+  static constexpr int CHUNK = RB < 16 ? RB : 16;           // bytes of codes that a lane moves at a time
+  static constexpr int ROUNDS = RB * 32 / (CHUNK * 32);     // of 32 lanes, for 32 rows
+  static constexpr int PER_ROW = RB / CHUNK;                // lanes of a row
+  const PtArgs &a;
+  uint32_t smem;
+  int warp, lane;
+  int page = -2;  // lanes 0, 1: of the next fill's V rows 0-15, 16-31; lanes 2, 3: of K's (-1: bad id, -2: none)
+
+  __device__ __forceinline__ Unpacker(const PtArgs &args, uint32_t s0, int w)
+      : a(args), smem(s0), warp(w), lane(threadIdx.x & 31) {}
+  __device__ __forceinline__ uint32_t staged(int n, int which) const {
+    return smem + S::OFF_CODES + (uint32_t)((n % S::FILLS) * 4 + warp) * S::WARP + which * (S::ROWS + S::SCALES);
+  }
+  // Pages of fill f.
+  __device__ __forceinline__ void look_up(const PtItem &it, int f) {
+    const int j = it.j0 + f - 1 + lane / 2, p = j * PT_KEYS + warp * 32 + (lane & 1) * 16;
+    page = -2;
+    if (lane < 4 && j >= it.j0 && j < it.j1 && p < it.kv_len) {
+      page = a.pv.page(it.seq, p >> a.pv.page_log2);
+      if (page < 0) report_status(a.status, LLAMA_ERR_RANGE);
+    }
+  }
+  // Fill f, the n-th of the CTA.
+  __device__ __forceinline__ void request(const PtItem &it, int f, int n) {
+    const int pages[4] = {__shfl_sync(0xffffffffu, page, 0), __shfl_sync(0xffffffffu, page, 1),
+                          __shfl_sync(0xffffffffu, page, 2), __shfl_sync(0xffffffffu, page, 3)};
+    const int rows = 1 << a.pv.page_log2;
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+      const int p0 = (it.j0 + f - 1 + which) * PT_KEYS + warp * 32;
+      const uint8_t *pool = which ? a.kc : a.vc;
+      const uint32_t dst = staged(n, which);
+#pragma unroll
+      for (int i = 0; i < ROUNDS; ++i) {
+        const int row = (i * 32 + lane) / PER_ROW, at = (i * 32 + lane) % PER_ROW * CHUNK;
+        const int pg = row < 16 ? pages[2 * which] : pages[2 * which + 1];
+        const uint32_t to = dst + row * RB + at;
+        if (pg >= 0) {
+          const uint8_t *from = kv4_row(pool, a.pv, pg, it.g, W, (p0 + row) & (rows - 1)).codes + at;
+          if constexpr (CHUNK == 16) copy16(to, from);
+          else copy8(to, from);
+        } else if (pg == -1) {  // a page of zeros
+          asm volatile("st.shared.v2.u32 [%0], {%1, %1};" ::"r"(to), "r"(0x88888888u) : "memory");
+          if constexpr (CHUNK == 16)
+            asm volatile("st.shared.v2.u32 [%0], {%1, %1};" ::"r"(to + 8), "r"(0x88888888u) : "memory");
+        }
+      }
+      const int l = lane - 16 * which;  // V's scales: lanes 0 .., K's: lanes 16 ..
+      if (l >= 0 && l < 2 * SB) {
+        const int row = l * 16 / SB, pg = row < 16 ? pages[2 * which] : pages[2 * which + 1];
+        if (pg >= 0)
+          copy16(dst + S::ROWS + l * 16, kv4_row(pool, a.pv, pg, it.g, W, (p0 + row) & (rows - 1)).scales);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  struct Raw {
+    uint4 codes[ROUNDS];
+    uint32_t scales[ROUNDS];
+  };
+  __device__ __forceinline__ void take(int n, int which, Raw &r) const {
+    const uint32_t from = staged(n, which);
+#pragma unroll
+    for (int i = 0; i < ROUNDS; ++i) {
+      const int row = (i * 32 + lane) / PER_ROW, col = (i * 32 + lane) % PER_ROW;
+      if constexpr (CHUNK == 16) {
+        r.codes[i] = ld_shared16(from + row * RB + col * 16);
+        r.scales[i] = ld_shared_u16(from + S::ROWS + row * SB + col * 2);
+      } else {
+        const uint2 c = ld_shared8(from + row * RB);
+        r.codes[i] = make_uint4(c.x, c.y, 0, 0);
+        r.scales[i] = ld_shared_u8(from + S::ROWS + row * SB);
+      }
+    }
+  }
+  __device__ __forceinline__ void unpack(const Raw &r, uint32_t tile) const {
+#pragma unroll
+    for (int i = 0; i < ROUNDS; ++i) {
+      const int row = warp * 32 + (i * 32 + lane) / PER_ROW, col = (i * 32 + lane) % PER_ROW;
+      const bool turned = W == 128 && col >= 2;
+      uint32_t w[4] = {r.codes[i].x, r.codes[i].y, r.codes[i].z, r.codes[i].w};
+      uint32_t s0 = r.scales[i] & 255u, s1 = r.scales[i] >> 8;
+      if (W == 128) {
+        const uint32_t x = w[0], y = w[1], s = s0;
+        w[0] = turned ? w[2] : w[0];
+        w[1] = turned ? w[3] : w[1];
+        w[2] = turned ? x : w[2];
+        w[3] = turned ? y : w[3];
+        s0 = turned ? s1 : s0;
+        s1 = turned ? s : s1;
+      }
+      const uint32_t base = tile + (W == 128 ? col / 2 * L::ATOM : 0) + row * 128;
+      const int c0 = W == 128 ? col % 2 * 4 : col * 4;
+#pragma unroll
+      for (int e = 0; e < CHUNK / 4; ++e) {
+        const uint32_t s2 = kv4_scale2(e < 2 ? s0 : s1, e < 2 ? s0 : s1);
+        const int c = c0 + (turned ? e ^ 2 : e);
+        st_shared16(base + ((c ^ (row & 7)) << 4), kv4_eight(w[e], s2, kv4_bias2(s2)));
+      }
+    }
+  }
+};
+
 // ------------------------------------------------------------- attention ---
-// ISSUERS: warps from PT_THREADS on that load the stages (0: warp 0 does).
-template <int D, int ISSUERS>
+// ISSUERS: warps from PT_THREADS on that load the stages (0: warp 0 does).  W: head width of
+// 4-bit pages, which the issuers unpack (0: bf16 pages).
+template <int D, int ISSUERS, int W>
 __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
     packed_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PtArgs a) {
@@ -401,6 +568,8 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
 
   // with issuers: an item has been handed over; their loads have come to its last tile
   const uint32_t i_full = bar0 + 8u * (11 + 2 * PT_STAGES), near_end = i_full + 8;
+  const uint32_t k_first = i_full + 16;  // 4-bit pages: an item's first K is unpacked
+  static_assert(W == 0 || ISSUERS == 4, "four warps unpack");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
@@ -416,6 +585,7 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
     ptx::mbar_init(q_empty, 9 + ISSUERS);
     ptx::mbar_init(i_full, 1);
     ptx::mbar_init(near_end, 1);
+    ptx::mbar_init(k_first, ISSUERS > 0 ? ISSUERS : 1);
     ptx::mbar_init(fin, 1);
     for (int s = 0; s < PT_STAGES; ++s) {
       ptx::mbar_init(kv_full(s), ISSUERS > 0 ? ISSUERS : 1);
@@ -440,6 +610,11 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
       }
     ptx::fence_proxy_async_smem();
   }
+  if (W > 0 && W < 64 && warp >= 2 && warp < 10) {  // columns of K and V behind the heads' width
+    uint4 *p = reinterpret_cast<uint4 *>(smem + L::OFF_K);
+    for (int i = threadIdx.x - 64; i < 2 * PT_STAGES * L::TILE / 16; i += PT_THREADS - 64) p[i] = make_uint4(0, 0, 0, 0);
+    ptx::fence_proxy_async_smem();
+  }
   if (warp == 1) {
     ptx::tmem_alloc(ptx::smem_u32(tmem_slot), L::TMEM_COLS);
     ptx::tmem_relinquish();
@@ -455,8 +630,10 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
     // ---------------------------------------------------------- producer ---
     if (lane == 0) {
       ptx::tma_prefetch_desc(&tmQ);
-      ptx::tma_prefetch_desc(&tmK);
-      ptx::tma_prefetch_desc(&tmV);
+      if (W == 0) {
+        ptx::tma_prefetch_desc(&tmK);
+        ptx::tma_prefetch_desc(&tmV);
+      }
     }
     const int units = a.G * a.subs;
     const int n_items = a.plan != nullptr ? *reinterpret_cast<volatile int *>(&a.plan->n_entries) * units : 0;
@@ -531,7 +708,7 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
     bool ok = true;
     PtItem it = fetch(0);
     for (int k = 0; ok; ++k) {
-      const int first_page = it.seq >= 0 ? loads.page_of(it, it.j0, my_box) : -1;
+      const int first_page = W == 0 && it.seq >= 0 ? loads.page_of(it, it.j0, my_box) : -1;
       if (ISSUERS == 0 && it.seq >= 0) loads.begin(it);
       if (k > 0 && !wait_warp(q_empty, (k - 1) & 1)) break;
       if (lane == 0) {
@@ -546,7 +723,7 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
       }
       const int n_t = it.q0 + a.Mq < it.count ? 2 : 1;  // query tiles that hold rows
       if (lane == 0) {
-        ptx::mbar_arrive_expect_tx(q_full, n_t * ATOMS * a.rb * a.Mq * 128u + loads.bytes(it, it.j0));
+        ptx::mbar_arrive_expect_tx(q_full, n_t * ATOMS * a.rb * a.Mq * 128u + (W == 0 ? loads.bytes(it, it.j0) : 0u));
         for (int t = 0; t < n_t; ++t)
           for (int at = 0; at < ATOMS; ++at)
             ptx::tma_load_3d(s0 + L::OFF_Q + t * L::TILE + at * L::ATOM, &tmQ, at * 64, it.h0,
@@ -640,6 +817,7 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
         issue_pv(jj, first, last, t, buf);
         return true;
       };
+      int k_items = 0;             // items that have brought a first K
       int owed = 1;                // stage whose release is still to come (1: see StageLoads)
       static_assert(PT_STAGES == 2, "K of tile jj + 1 lies in the other stage");
       for (int k = 0; ok; ++k) {
@@ -652,6 +830,7 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
           ptx::mbar_arrive(q_empty);
           continue;
         }
+        if (W > 0 && !wait(k_first, k_items++ & 1)) break;
         ptx::tc_fence_after();
         if (it.j0 < e0) next_s(jg, 0);
         if (it.j0 < e1) next_s(jg, 1);
@@ -698,6 +877,57 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
       ptx::mma_commit(fin);
       ptx::mbar_drain(fin, 0, nullptr, 0);
     }
+  } else if (W > 0 && warp >= 10) {
+    // ---------------------------------------------------------- unpackers ---
+    using S = PtShared<D, W == 0 ? 64 : W>;
+    Unpacker<D, W == 0 ? 64 : W> u(a, s0, warp - 10);
+    typename decltype(u)::Raw raw[2];
+    int tiles = 0, fills = 0;  // key tiles of earlier items, fills taken so far
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      if (!wait_warp(i_full, k & 1)) break;
+      const PtItem it = *item_slot;
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(q_empty);
+      if (it.seq < 0) break;
+      const int n = it.j1 - it.j0;
+      if (n <= 0) {
+        if (warp == 10 && lane == 0) ptx::mbar_arrive(near_end);
+        continue;
+      }
+      // one group of copies per fill, of a fill that is not there an empty one
+      u.look_up(it, 0);
+      for (int f = 0; f < S::FILLS; ++f) {
+        u.request(it, f, fills + f);
+        u.look_up(it, f + 1);
+      }
+      for (int f = 0; f <= n; ++f, ++fills) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(S::FILLS - 1) : "memory");
+        __syncwarp();
+        if (f > 0) u.take(fills, 0, raw[0]);
+        if (f < n) u.take(fills, 1, raw[1]);
+        __syncwarp();
+        u.request(it, f + S::FILLS, fills + S::FILLS);
+        u.look_up(it, f + S::FILLS + 1);
+        const int jj = tiles + f - 1;  // the stage
+        if (f > 0) {
+          // as StageLoads::parity
+          if (!wait_warp(kv_empty(jj % PT_STAGES), ((jj / PT_STAGES) & 1) ^ (jj % PT_STAGES == 0 ? 1 : 0))) {
+            ok = false;
+            break;
+          }
+          if (f == n && warp == 10 && lane == 0) ptx::mbar_arrive(near_end);
+          u.unpack(raw[0], s0 + L::OFF_V + (jj % PT_STAGES) * L::TILE);
+        }
+        if (f < n) u.unpack(raw[1], s0 + L::OFF_K + ((jj + 1) % PT_STAGES) * L::TILE);
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(f == 0 ? k_first : kv_full(jj % PT_STAGES));
+      }
+      tiles += n;
+      fills += S::FILLS - 1;  // those behind the item's last were empty
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (ISSUERS > 0 && warp >= 10) {
     // ------------------------------------------------------------ issuers ---
     StageLoads<D, ISSUERS == 0 ? 1 : ISSUERS> loads(a, &tmK, &tmV, s0, warp - 10);
@@ -769,7 +999,7 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
         const int key0 = j * PT_KEYS;
         // The last tile of a sequence: clear the V rows behind its last key.  The first
         // query tile that works on the tile does it, before its P is handed over.
-        if (key0 + PT_KEYS > it.kv_len && t == (j < e0 ? 0 : 1)) {
+        if (W == 0 && key0 + PT_KEYS > it.kv_len && t == (j < e0 ? 0 : 1)) {
           const int st = (jg + jl) % PT_STAGES;
           if (!wait_warp(kv_full(st), ((jg + jl) / PT_STAGES) & 1)) {
             ok = false;
@@ -1071,16 +1301,19 @@ PtSizes packed_sizes(const PackedView &b, int H, int G, int D, int sms) {
   return z;
 }
 
-template <int D>
-cudaError_t launch_tc(const bf16 *q, const bf16 *k, const bf16 *v, bf16 *o, const PagedView &pv, const PackedView &b,
+// k, v: bf16 pages, or with W > 0 pages held in 4 bits, of heads of width W.
+template <int D, int W>
+cudaError_t launch_tc(const bf16 *q, const void *k, const void *v, bf16 *o, const PagedView &pv, const PackedView &b,
                       int H, int G, int width, void *workspace, int *status, cudaStream_t st) {
-  using L = PtLayout<D>;
+  constexpr int BYTES = PtShared<D, W>::BYTES;
   static PerContextOnce attr;
   cudaError_t e = attr.run([] {
-    const cudaError_t e =
-        cudaFuncSetAttribute(packed_tc_kernel<D, 0>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
-    if (e != cudaSuccess) return e;
-    return cudaFuncSetAttribute(packed_tc_kernel<D, 4>, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
+    if constexpr (W == 0) {
+      const cudaError_t e =
+          cudaFuncSetAttribute(packed_tc_kernel<D, 0, 0>, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES);
+      if (e != cudaSuccess) return e;
+    }
+    return cudaFuncSetAttribute(packed_tc_kernel<D, 4, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES);
   });
   if (e != cudaSuccess) return e;
   const int sms = sm_count();
@@ -1101,17 +1334,26 @@ cudaError_t launch_tc(const bf16 *q, const bf16 *k, const bf16 *v, bf16 *o, cons
   a.plan = nullptr;
   a.entries = nullptr;
   a.part = nullptr;
+  a.kc = W > 0 ? (const uint8_t *)k : nullptr;
+  a.vc = W > 0 ? (const uint8_t *)v : nullptr;
   a.status = status;
   a.wait_cycles = op_wait_cycles();
   CUtensorMap mq, mk, mv;
-  if (!make_heads_map(&mq, q, b.n_tokens, H, width, a.rb, a.Mq) || !make_paged_map(&mk, k, pv, G, width, a.box) ||
-      !make_paged_map(&mv, v, pv, G, width, a.box))
+  if (!make_heads_map(&mq, q, b.n_tokens, H, width, a.rb, a.Mq)) return cudaErrorInvalidValue;
+  if (W > 0) {
+    mk = mv = mq;  // not used
+  } else if (!make_paged_map(&mk, (const bf16 *)k, pv, G, width, a.box) ||
+             !make_paged_map(&mv, (const bf16 *)v, pv, G, width, a.box)) {
     return cudaErrorInvalidValue;
-  auto kernel = a.box == 16 ? packed_tc_kernel<D, 4> : packed_tc_kernel<D, 0>;
-  const dim3 threads(PT_THREADS + (a.box == 16 ? 128 : 0));
+  }
+  auto kernel = packed_tc_kernel<D, 4, W>;
+  if constexpr (W == 0) {
+    if (a.box != 16) kernel = packed_tc_kernel<D, 0, 0>;
+  }
+  const dim3 threads(PT_THREADS + (W > 0 || a.box == 16 ? 128 : 0));
   if (z.bytes == 0) {
     count_launch();
-    return launch_pdl(kernel, dim3((unsigned)(z.max_blocks * z.units)), threads, L::BYTES, st, mq,
+    return launch_pdl(kernel, dim3((unsigned)(z.max_blocks * z.units)), threads, BYTES, st, mq,
                       mk, mv, a);
   }
   char *w = reinterpret_cast<char *>(workspace);
@@ -1125,7 +1367,7 @@ cudaError_t launch_tc(const bf16 *q, const bf16 *k, const bf16 *v, bf16 *o, cons
   if (e != cudaSuccess) return e;
   const long long items = z.max_entries * z.units;
   count_launch();
-  e = launch_pdl(kernel, dim3((unsigned)(items < sms ? items : sms)), threads, L::BYTES, st, mq,
+  e = launch_pdl(kernel, dim3((unsigned)(items < sms ? items : sms)), threads, BYTES, st, mq,
                  mk, mv, a);
   if (e != cudaSuccess || z.max_split == 0) return e;
   count_launch();
@@ -1142,8 +1384,19 @@ size_t packed_tc_workspace_bytes(const PackedView &b, int H, int G, int D) {
 
 cudaError_t launch_packed_tc(const bf16 *q, const bf16 *k, const bf16 *v, bf16 *o, const PagedView &pv,
                              const PackedView &b, int H, int G, int D, void *workspace, int *status, cudaStream_t st) {
-  if (D == 128) return launch_tc<128>(q, k, v, o, pv, b, H, G, D, workspace, status, st);
-  return launch_tc<64>(q, k, v, o, pv, b, H, G, D, workspace, status, st);
+  if (D == 128) return launch_tc<128, 0>(q, k, v, o, pv, b, H, G, D, workspace, status, st);
+  return launch_tc<64, 0>(q, k, v, o, pv, b, H, G, D, workspace, status, st);
+}
+
+cudaError_t launch_packed_kv4(const bf16 *q, const uint8_t *k, const uint8_t *v, bf16 *o, const PagedView &pv,
+                              const PackedView &b, int H, int G, int D, void *workspace, int *status, cudaStream_t st) {
+  switch (D) {
+    case 16: return launch_tc<64, 16>(q, k, v, o, pv, b, H, G, D, workspace, status, st);
+    case 32: return launch_tc<64, 32>(q, k, v, o, pv, b, H, G, D, workspace, status, st);
+    case 64: return launch_tc<64, 64>(q, k, v, o, pv, b, H, G, D, workspace, status, st);
+    case 128: return launch_tc<128, 128>(q, k, v, o, pv, b, H, G, D, workspace, status, st);
+  }
+  return cudaErrorInvalidValue;
 }
 
 }  // namespace llama

@@ -70,6 +70,16 @@ cudaError_t launch_rope_kv_paged(const T *qkv, T *q_out, T *k, T *v, const Paged
                                  const float2 *table, int table_max_seq, int H, int G, int D, int halves, int *status,
                                  cudaStream_t st);
 
+// The same into pages held in 4 bits, and rows of k and v [n_tokens][G][D] back from them
+// (kv4_pages.cu); page_stride of pv is in bytes.
+template <typename T>
+cudaError_t launch_rope_kv4(const T *qkv, T *q_out, uint8_t *k, uint8_t *v, const PagedView &pv, const PackedView &b,
+                            const float2 *table, int table_max_seq, int H, int G, int D, int halves, int *status,
+                            cudaStream_t st);
+template <typename T>
+cudaError_t launch_kv4_read(const uint8_t *k, const uint8_t *v, T *k_out, T *v_out, const PagedView &pv,
+                            const PackedView &b, int G, int D, int *status, cudaStream_t st);
+
 // Tensor maps (packed_tc.cu), 64 columns wide in the 128-byte swizzle: `box` rows of
 // one page and KV head, coordinates (column, row in page, head, page); box_heads x
 // box_rows of packed query rows [rows][H][D], coordinates (column, head, row).
@@ -81,18 +91,31 @@ size_t packed_tc_workspace_bytes(const PackedView &b, int H, int G, int D);
 cudaError_t launch_packed_tc(const bf16 *q, const bf16 *k, const bf16 *v, bf16 *o, const PagedView &pv,
                              const PackedView &b, int H, int G, int D, void *workspace, int *status, cudaStream_t st);
 
+// The same over pages held in 4 bits (page_stride in bytes); the workspace is the same too.
+cudaError_t launch_packed_kv4(const bf16 *q, const uint8_t *k, const uint8_t *v, bf16 *o, const PagedView &pv,
+                              const PackedView &b, int H, int G, int D, void *workspace, int *status, cudaStream_t st);
+
 // Tensor-core decode attention (paged_decode_tc.cu).
 size_t paged_decode_tc_workspace_bytes(int n_seqs, int max_kv_len, int H, int G, int D);
 cudaError_t launch_paged_decode_tc(const bf16 *q, const bf16 *k, const bf16 *v, bf16 *o, const PagedView &pv,
                                    const int *kv_lens, int n_seqs, int max_kv_len, int H, int G, int D,
                                    void *workspace, int *status, cudaStream_t st);
 
-// fp32 attention over pages on CUDA cores (paged_simt.cu).
+// Decode attention over pages held in 4 bits, q and o bf16 (kv4_decode.cu).
+size_t kv4_decode_workspace_bytes(int n_seqs, int max_kv_len, int H, int G, int D);
+cudaError_t launch_kv4_decode(const bf16 *q, const uint8_t *k, const uint8_t *v, bf16 *o, const PagedView &pv,
+                              const int *kv_lens, int n_seqs, int max_kv_len, int H, int G, int D, void *workspace,
+                              int *status, cudaStream_t st);
+
+// fp32 attention over pages on CUDA cores (paged_simt.cu); P: float, or uint8_t for pages
+// held in 4 bits.
 size_t packed_simt_workspace_bytes(const PackedView &b, int H, int G, int D);
-cudaError_t launch_packed_simt(const float *q, const float *k, const float *v, float *o, const PagedView &pv,
+template <typename P>
+cudaError_t launch_packed_simt(const float *q, const P *k, const P *v, float *o, const PagedView &pv,
                                const PackedView &b, int H, int G, int D, float *part, int *status, cudaStream_t st);
 size_t paged_decode_simt_workspace_bytes(int n_seqs, int max_kv_len, int H, int G, int D);
-cudaError_t launch_paged_decode_simt(const float *q, const float *k, const float *v, float *o, const PagedView &pv,
+template <typename P>
+cudaError_t launch_paged_decode_simt(const float *q, const P *k, const P *v, float *o, const PagedView &pv,
                                      const int *kv_lens, int n_seqs, int max_kv_len, int H, int G, int D, float *part,
                                      int *status, cudaStream_t st);
 
@@ -103,5 +126,12 @@ template <typename T>
 cudaError_t launch_token_logprobs(const T *logits, long long row_stride, const int *targets, int rows, int V,
                                   float *logprobs, float *entropy, int top_k, int *top_ids, float *top_logprobs,
                                   int *status, int bad_target, cudaStream_t st);
+
+// Verification of drafted tokens (verify_drafts.cu).
+size_t verify_drafts_workspace_bytes(int n_rows, int V);
+template <typename T>
+cudaError_t launch_verify_drafts(const T *target, long long target_stride, const T *draft, long long seq_stride,
+                                 long long step_stride, int V, const llama_draft_batch &b, int *out_tokens,
+                                 int *n_accepted, float *logprobs, void *workspace, int *status, cudaStream_t st);
 
 }  // namespace llama

@@ -3,10 +3,12 @@
 // j <= position).  One pass over the keys with the running maximum and sum of the
 // softmax; fp32 products and sums throughout (the tensor cores round fp32 operands).
 // Keys are split over CTAs when the rows alone are too few to fill the SMs, and the
-// parts joined in order: o = sum e^(m_c - M) o_c / sum e^(m_c - M) l_c.
+// parts joined in order: o = sum e^(m_c - M) o_c / sum e^(m_c - M) l_c.  Pages of fp32 and
+// pages held in 4 bits differ in how a tile's vectors are loaded alone.
 #include <float.h>
 #include <math.h>
 
+#include "kv4.cuh"
 #include "paged_kernels.h"
 
 namespace llama {
@@ -35,20 +37,26 @@ Split split_of(long long ctas, int max_kv_len, int least) {
   return s;
 }
 
+// Vector c of a row.
+__device__ __forceinline__ float4 four(const float *row, int c) { return *reinterpret_cast<const float4 *>(row + c * 4); }
+__device__ __forceinline__ float4 four(const Kv4Row &row, int c) {
+  return kv4_four(reinterpret_cast<const uint32_t *>(row.codes)[c / 2], c & 1, kv4_scale(row.scales[c / 4]));
+}
+
 // A thread's vectors of a tile of KEYS rows of D floats: vector u = i * THREADS + tid
 // is column u % (D / 4) of row u / (D / 4).
 template <int D>
 struct TileRegs {
   static constexpr int RV = D / 4, PER = KEYS * RV / THREADS;
   float4 x[PER];
-  // row_ptr(i): row i in memory, null for zeros
+  // row_ptr(i): row i in memory (a float * or Kv4Row), null for zeros
   template <typename F>
   __device__ __forceinline__ void load(F &&row_ptr) {
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
       const int u = i * THREADS + threadIdx.x;
-      const float *p = row_ptr(u / RV);
-      x[i] = p != nullptr ? *reinterpret_cast<const float4 *>(p + u % RV * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+      const auto p = row_ptr(u / RV);
+      x[i] = p != nullptr ? four(p, u % RV) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
   }
   __device__ __forceinline__ void store(float *dst) const {  // rows 16 bytes apart in banks
@@ -65,6 +73,10 @@ __device__ __forceinline__ const float *page_row(const float *pool, const PagedV
   const int page = pv.page(seq, p >> pv.page_log2);
   if (page < 0) return nullptr;
   return pool + page * pv.page_stride + (((long long)g << pv.page_log2) + (p & ((1 << pv.page_log2) - 1))) * D;
+}
+__device__ __forceinline__ Kv4Row page_row(const uint8_t *pool, const PagedView &pv, int seq, int g, int D, int p) {
+  const int page = pv.page(seq, p >> pv.page_log2);
+  return page < 0 ? Kv4Row() : kv4_row(pool, pv, page, g, D, p & ((1 << pv.page_log2) - 1));
 }
 
 // ---------------------------------------------------------------- packed ---
@@ -89,8 +101,10 @@ __device__ __forceinline__ int tile_keys(const SeqSpan &s, int r, int row0) {
   return max(0, s.kv_len - s.count + (row0 + rows - 1) / r + 1);
 }
 
+template <typename P>  // of a pool's elements: float, or uint8_t for 4-bit blocks
 struct PsArgs {
-  const float *q, *k, *v;
+  const float *q;
+  const P *k, *v;
   float *o, *part;  // part [split.n][n_tokens][H][D + 2]
   PagedView pv;
   PackedView b;
@@ -100,9 +114,10 @@ struct PsArgs {
   int *status;
 };
 
-template <int D>
-__global__ void __launch_bounds__(THREADS) packed_simt_kernel(const __grid_constant__ PsArgs a) {
+template <int D, typename P>
+__global__ void __launch_bounds__(THREADS) packed_simt_kernel(const __grid_constant__ PsArgs<P> a) {
   using L = PsLayout<D>;
+  using Row = decltype(page_row((const P *)nullptr, PagedView(), 0, 0, 0, 0));
   extern __shared__ __align__(16) float smem_f[];
   float *sq = smem_f, *sk = smem_f + L::OFF_K, *sv = smem_f + L::OFF_V, *sp = smem_f + L::OFF_P;
   const int r = a.H / a.G, g = blockIdx.y;
@@ -168,8 +183,8 @@ __global__ void __launch_bounds__(THREADS) packed_simt_kernel(const __grid_const
   for (int k0 = k_begin; k0 < k_end; k0 += KEYS) {
     {
       TileRegs<D> kr, vr;
-      kr.load([&](int j) { return k0 + j < s.kv_len ? page_row(a.k, a.pv, seq, g, D, k0 + j) : nullptr; });
-      vr.load([&](int j) { return k0 + j < s.kv_len ? page_row(a.v, a.pv, seq, g, D, k0 + j) : nullptr; });
+      kr.load([&](int j) { return k0 + j < s.kv_len ? page_row(a.k, a.pv, seq, g, D, k0 + j) : Row(); });
+      vr.load([&](int j) { return k0 + j < s.kv_len ? page_row(a.v, a.pv, seq, g, D, k0 + j) : Row(); });
       if (threadIdx.x < KEYS) {
         const int p = k0 + (int)threadIdx.x;
         if (p < s.kv_len && a.pv.page(seq, p >> a.pv.page_log2) < 0) report_status(a.status, LLAMA_ERR_RANGE);
@@ -286,8 +301,8 @@ struct RowParts {
   }
 };
 
-template <int D>
-__global__ void __launch_bounds__(THREADS) packed_join_simt_kernel(const __grid_constant__ PsArgs a) {
+template <int D, typename P>
+__global__ void __launch_bounds__(THREADS) packed_join_simt_kernel(const __grid_constant__ PsArgs<P> a) {
   const long long row = (long long)blockIdx.x * (THREADS / 32) + threadIdx.x / 32;  // token, head
   grid_dependency_wait();
   if (row >= (long long)a.b.n_tokens * a.H) return;
@@ -312,11 +327,11 @@ Split packed_split(const PackedView &b, int H, int G) {
   return split_of(packed_tiles(b, H, G) * G, b.max_kv_len, 2 * KEYS);
 }
 
-template <int D>
-cudaError_t packed_simt(PsArgs a, cudaStream_t st) {
+template <int D, typename P>
+cudaError_t packed_simt(PsArgs<P> a, cudaStream_t st) {
   static PerContextOnce attr;
   const cudaError_t e = attr.run([] {
-    return cudaFuncSetAttribute(packed_simt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(packed_simt_kernel<D, P>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 PsLayout<D>::BYTES);
   });
   if (e != cudaSuccess) return e;
@@ -324,12 +339,12 @@ cudaError_t packed_simt(PsArgs a, cudaStream_t st) {
   const long long tiles = packed_tiles(a.b, a.H, a.G);
   if (tiles > 0x7fffffffLL || a.G > 65535) return cudaErrorInvalidValue;
   count_launch();
-  const cudaError_t r = launch_pdl(packed_simt_kernel<D>, dim3((unsigned)tiles, (unsigned)a.G, (unsigned)a.split.n),
+  const cudaError_t r = launch_pdl(packed_simt_kernel<D, P>, dim3((unsigned)tiles, (unsigned)a.G, (unsigned)a.split.n),
                                    dim3(THREADS), PsLayout<D>::BYTES, st, a);
   if (r != cudaSuccess || a.split.n == 1) return r;
   count_launch();
   const long long rows = (long long)a.b.n_tokens * a.H;
-  return launch_pdl(packed_join_simt_kernel<D>, dim3((unsigned)((rows + THREADS / 32 - 1) / (THREADS / 32))),
+  return launch_pdl(packed_join_simt_kernel<D, P>, dim3((unsigned)((rows + THREADS / 32 - 1) / (THREADS / 32))),
                     dim3(THREADS), 0, st, a);
 }
 
@@ -350,8 +365,10 @@ struct DsLayout {
   static constexpr int BYTES = (OFF_W + KEYS * HEADS) * 4;
 };
 
+template <typename P>  // of a pool's elements: float, or uint8_t for 4-bit blocks
 struct DsArgs {
-  const float *q, *k, *v;
+  const float *q;
+  const P *k, *v;
   float *o, *part;  // part [n_seqs][H][split.n][D + 2]
   PagedView pv;
   const int *kv_lens;
@@ -361,9 +378,10 @@ struct DsArgs {
   int *status;
 };
 
-template <int D>
-__global__ void __launch_bounds__(THREADS) paged_decode_simt_kernel(const __grid_constant__ DsArgs a) {
+template <int D, typename P>
+__global__ void __launch_bounds__(THREADS) paged_decode_simt_kernel(const __grid_constant__ DsArgs<P> a) {
   using L = DsLayout<D>;
+  using Row = decltype(page_row((const P *)nullptr, PagedView(), 0, 0, 0, 0));
   extern __shared__ __align__(16) float smem_f[];
   float *sk = smem_f, *sv = smem_f + L::OFF_V, *sq = smem_f + L::OFF_Q, *ss = smem_f + L::OFF_S,
         *sw = smem_f + L::OFF_W;
@@ -383,8 +401,8 @@ __global__ void __launch_bounds__(THREADS) paged_decode_simt_kernel(const __grid
 
   TileRegs<D> kr, vr;
   auto load = [&](int t0) {
-    kr.load([&](int j) { return t0 + j < k1 ? page_row(a.k, a.pv, seq, g, D, t0 + j) : nullptr; });
-    vr.load([&](int j) { return t0 + j < k1 ? page_row(a.v, a.pv, seq, g, D, t0 + j) : nullptr; });
+    kr.load([&](int j) { return t0 + j < k1 ? page_row(a.k, a.pv, seq, g, D, t0 + j) : Row(); });
+    vr.load([&](int j) { return t0 + j < k1 ? page_row(a.v, a.pv, seq, g, D, t0 + j) : Row(); });
     const int p = t0 + (int)threadIdx.x;
     if (threadIdx.x < KEYS && p < k1 && a.pv.page(seq, p >> a.pv.page_log2) < 0)
       report_status(a.status, LLAMA_ERR_RANGE);
@@ -478,8 +496,8 @@ __global__ void __launch_bounds__(THREADS) paged_decode_simt_kernel(const __grid
 }
 
 // A CTA per row: the parts are many and the rows few, so its warps share them.
-template <int D>
-__global__ void __launch_bounds__(THREADS) decode_join_simt_kernel(const __grid_constant__ DsArgs a) {
+template <int D, typename P>
+__global__ void __launch_bounds__(THREADS) decode_join_simt_kernel(const __grid_constant__ DsArgs<P> a) {
   constexpr int WARPS = THREADS / 32;
   __shared__ float sm[WARPS], sl[WARPS], so[WARPS][D];
   const int row = blockIdx.x, warp = threadIdx.x / 32, lane = threadIdx.x & 31;  // sequence, head
@@ -513,11 +531,11 @@ Split decode_split(int n_seqs, int max_kv_len, int H, int G) {
   return split_of((long long)n_seqs * G * ((H / G + HEADS - 1) / HEADS), max_kv_len, KEYS);
 }
 
-template <int D>
-cudaError_t decode_simt(DsArgs a, cudaStream_t st) {
+template <int D, typename P>
+cudaError_t decode_simt(DsArgs<P> a, cudaStream_t st) {
   static PerContextOnce attr;
   const cudaError_t e = attr.run([] {
-    return cudaFuncSetAttribute(paged_decode_simt_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(paged_decode_simt_kernel<D, P>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 DsLayout<D>::BYTES);
   });
   if (e != cudaSuccess) return e;
@@ -525,12 +543,12 @@ cudaError_t decode_simt(DsArgs a, cudaStream_t st) {
   const long long units = (long long)a.G * ((a.H / a.G + HEADS - 1) / HEADS), rows = (long long)a.n_seqs * a.H;
   if (units > 65535 || rows > 0x7fffffffLL) return cudaErrorInvalidValue;
   count_launch();
-  const cudaError_t r = launch_pdl(paged_decode_simt_kernel<D>,
+  const cudaError_t r = launch_pdl(paged_decode_simt_kernel<D, P>,
                                    dim3((unsigned)a.split.n, (unsigned)a.n_seqs, (unsigned)units), dim3(THREADS),
                                    DsLayout<D>::BYTES, st, a);
   if (r != cudaSuccess || a.split.n == 1) return r;
   count_launch();
-  return launch_pdl(decode_join_simt_kernel<D>, dim3((unsigned)rows), dim3(THREADS), 0, st, a);
+  return launch_pdl(decode_join_simt_kernel<D, P>, dim3((unsigned)rows), dim3(THREADS), 0, st, a);
 }
 
 }  // namespace
@@ -540,9 +558,10 @@ size_t packed_simt_workspace_bytes(const PackedView &b, int H, int G, int D) {
   return s.n > 1 ? (size_t)s.n * b.n_tokens * H * (D + 2) * sizeof(float) : 0;
 }
 
-cudaError_t launch_packed_simt(const float *q, const float *k, const float *v, float *o, const PagedView &pv,
+template <typename P>
+cudaError_t launch_packed_simt(const float *q, const P *k, const P *v, float *o, const PagedView &pv,
                                const PackedView &b, int H, int G, int D, float *part, int *status, cudaStream_t st) {
-  PsArgs a;
+  PsArgs<P> a;
   a.q = q;
   a.k = k;
   a.v = v;
@@ -568,10 +587,11 @@ size_t paged_decode_simt_workspace_bytes(int n_seqs, int max_kv_len, int H, int 
   return s.n > 1 ? (size_t)n_seqs * H * s.n * (D + 2) * sizeof(float) : 0;
 }
 
-cudaError_t launch_paged_decode_simt(const float *q, const float *k, const float *v, float *o, const PagedView &pv,
+template <typename P>
+cudaError_t launch_paged_decode_simt(const float *q, const P *k, const P *v, float *o, const PagedView &pv,
                                      const int *kv_lens, int n_seqs, int max_kv_len, int H, int G, int D, float *part,
                                      int *status, cudaStream_t st) {
-  DsArgs a;
+  DsArgs<P> a;
   a.q = q;
   a.k = k;
   a.v = v;
@@ -593,5 +613,17 @@ cudaError_t launch_paged_decode_simt(const float *q, const float *k, const float
   }
   return cudaErrorInvalidValue;
 }
+
+template cudaError_t launch_packed_simt<float>(const float *, const float *, const float *, float *, const PagedView &,
+                                               const PackedView &, int, int, int, float *, int *, cudaStream_t);
+template cudaError_t launch_packed_simt<uint8_t>(const float *, const uint8_t *, const uint8_t *, float *,
+                                                 const PagedView &, const PackedView &, int, int, int, float *, int *,
+                                                 cudaStream_t);
+template cudaError_t launch_paged_decode_simt<float>(const float *, const float *, const float *, float *,
+                                                     const PagedView &, const int *, int, int, int, int, int, float *,
+                                                     int *, cudaStream_t);
+template cudaError_t launch_paged_decode_simt<uint8_t>(const float *, const uint8_t *, const uint8_t *, float *,
+                                                       const PagedView &, const int *, int, int, int, int, int, float *,
+                                                       int *, cudaStream_t);
 
 }  // namespace llama

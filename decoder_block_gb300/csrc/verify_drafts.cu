@@ -1,0 +1,537 @@
+// Keeps or replaces drafted tokens by the target's probabilities ("The Evolving
+// Transformer 04 · LLaMA", §07 Assemble: the logits of a position are the unnormalised
+// log-probabilities of its next token).  With p and q the target's and the draft's
+// softmax, a draft x is kept with probability min(1, p[x] / q[x]) and otherwise replaced
+// by one drawn from max(p - q, 0): what comes out is distributed as p.  Drawing is a race
+// of exponential variates E: the id with the smallest E_v / w_v, the largest w_v / E_v,
+// is v with probability w_v / sum w.  No running sum is needed for it, so nothing depends
+// on the order in which a row's parts are added up, and its parts can be searched apart.
+//
+// Every logit has to be read once, and that bounds it.  Two kernels:
+//   rows   a CTA takes a part of a row, target's or draft's, and leaves its maximum m,
+//          sum of e^((x - m) / T) and, for greedy sequences, the id of m;
+//   draw   a cluster takes a sequence: every CTA of it adds up the parts of its rows,
+//          takes the decisions, and searches a part of the one row (with its draft's and
+//          the noise) that the next token is drawn from.  The CTAs meet through
+//          distributed shared memory.
+// Rows behind the first refused draft are summed in vain: knowing it first would take a
+// chain of kernels as long as the drafts, each too small to fill the GPU.
+#include <float.h>
+#include <limits.h>
+#include <math.h>
+
+#include "paged_kernels.h"
+#include "ptx.cuh"
+
+namespace llama {
+namespace {
+
+constexpr int VD_THREADS = 256;
+constexpr int VD_WARPS = VD_THREADS / 32;
+constexpr int VD_VECS = 4;          // 16-byte vectors of a thread in flight
+constexpr int VD_MAX_PARTS = 32;    // of a row: a lane each when they are added up
+constexpr int VD_MIN_PART = 4096;   // logits of a part, at least
+constexpr int VD_MAX_CLUSTER = 8;
+constexpr float VD_LOG2E = 1.4426950408889634f;
+
+struct VdPart {
+  float m, z;  // largest logit that is not NaN (-FLT_MAX at least); z: NaN where the row holds NaN or +inf
+  int id;      // of m (greedy alone)
+  int pad;
+};
+
+struct VdArgs {
+  const void *target, *draft;
+  long long target_stride, seq_stride, step_stride;
+  int V;
+  const int *q_offsets, *tokens;
+  const float *temperatures, *uniforms, *noise;
+  long long noise_stride;
+  int n_seqs, n_rows, max_drafts;
+  int parts;    // of a row
+  VdPart *part; // [n_rows][2: target, draft][parts]
+  int *out_tokens, *n_accepted;
+  float *logprobs;
+  int *status;
+  int cluster;
+};
+
+__device__ __forceinline__ float ld_float_after_wait(const float *p) {
+  return __int_as_float(ld_after_wait(reinterpret_cast<const int *>(p)));
+}
+template <typename T> __device__ __forceinline__ float ld_logit(const T *p);
+template <> __device__ __forceinline__ float ld_logit<float>(const float *p) { return ld_float_after_wait(p); }
+template <> __device__ __forceinline__ float ld_logit<bf16>(const bf16 *p) {
+  uint16_t v;
+  asm volatile("ld.global.u16 %0, [%1];" : "=h"(v) : "l"(p));
+  return __uint_as_float((uint32_t)v << 16);
+}
+
+// Temperature of sequence i; 0: greedy.  (Denormals divide to infinities.)
+__device__ __forceinline__ float temperature_of(const VdArgs &a, int i) {
+  if (a.noise == nullptr) return 0.f;
+  if (a.temperatures == nullptr) return 1.f;
+  const float t = ld_float_after_wait(a.temperatures + i);
+  return fabsf(t) < FLT_MIN ? 0.f : t;
+}
+__device__ __forceinline__ bool temperature_ok(float t) { return t >= 0.f && t <= FLT_MAX; }
+
+// Rows of sequence i: n < 0 when they are out of range.
+__device__ __forceinline__ void rows_of(const VdArgs &a, int i, int &first, int &n) {
+  first = ld_after_wait(a.q_offsets + i);
+  const int end = ld_after_wait(a.q_offsets + i + 1);
+  n = first >= 0 && end >= first && end <= a.n_rows && end - first <= a.max_drafts + 1 ? end - first : -1;
+}
+
+// (maximum, sum) of two parts; c: log2(e) / T.
+__device__ __forceinline__ void merge(float &m, float &z, float om, float oz, float c) {
+  const float up = fmaxf(m, om);
+  z = z * ptx::ex2_approx((m - up) * c) + oz * ptx::ex2_approx((om - up) * c);
+  m = up;
+}
+
+// ------------------------------------------------------------------ rows ---
+template <typename T, bool GREEDY>
+struct VdScan {
+  float m = -FLT_MAX, z = 0.f;  // finite: -inf alone leaves weights of 0
+  int at = -1;                  // greedy: first batch that has the maximum
+  // N logits, a batch or some that are in no whole vector.
+  template <int N>
+  __device__ __forceinline__ void add(const float (&x)[N], float c, int batch) {
+    float bm = x[0];
+#pragma unroll
+    for (int e = 1; e < N; ++e) bm = fmaxf(bm, x[e]);
+    if (GREEDY && bm >= m && (bm > m || at < 0)) at = batch;
+    if (bm > m) {
+      z *= ptx::ex2_approx((m - bm) * c);
+      m = bm;
+    }
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int e = 0; e < N; ++e) s[e & 3] += ptx::ex2_approx((x[e] - m) * c);
+    z += (s[0] + s[1]) + (s[2] + s[3]);
+  }
+};
+
+// Part `part` of a row: this thread's (m, z, id of m).
+template <typename T, bool GREEDY>
+__device__ __forceinline__ void scan_part(const T *x, int V, int part, int parts, float c, float &m, float &z, int &id) {
+  constexpr int N = Vec16<T>::N;
+  const int head0 = (int)((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / (int)sizeof(T);
+  const int head = head0 < V ? head0 : V;  // logits in front of the first whole vector
+  const int n_vec = (V - head) / N, rest = V - head - n_vec * N;
+  const T *body = x + head;
+  const int v0 = (int)((long long)n_vec * part / parts), v1 = (int)((long long)n_vec * (part + 1) / parts);
+  VdScan<T, GREEDY> s;
+  for (int v = v0; v < v1; v += VD_VECS * VD_THREADS) {
+    Vec16<T> w[VD_VECS];
+#pragma unroll
+    for (int k = 0; k < VD_VECS; ++k) {
+      const int at = v + k * VD_THREADS + (int)threadIdx.x;
+      if (at < v1) {
+        w[k].raw = ld_once_after_wait(body + (size_t)at * N);
+      } else {
+#pragma unroll
+        for (int e = 0; e < N; ++e) w[k].set(e, -INFINITY);
+      }
+    }
+    float f[VD_VECS * N];
+#pragma unroll
+    for (int k = 0; k < VD_VECS; ++k)
+#pragma unroll
+      for (int e = 0; e < N; ++e) f[k * N + e] = w[k].get(e);
+    s.add(f, c, v);
+  }
+  id = INT_MAX;
+  if (GREEDY && s.at >= 0) {  // the batch again, for the place of its maximum
+#pragma unroll 1
+    for (int k = VD_VECS - 1; k >= 0; --k) {
+      const int at = s.at + k * VD_THREADS + (int)threadIdx.x;
+      if (at >= v1) continue;
+      const Vec16<T> w = load16<T>(body + (size_t)at * N);
+#pragma unroll
+      for (int e = N - 1; e >= 0; --e)
+        if (w.get(e) == s.m) id = head + at * N + e;
+    }
+  }
+  m = s.m;
+  z = s.z;
+  // the ends: one logit of each of the first part's first threads
+  if (part == 0 && (int)threadIdx.x < head + rest) {
+    const int at = (int)threadIdx.x < head ? threadIdx.x : V - rest + (int)threadIdx.x - head;
+    const float f = ld_logit<T>(x + at);
+    if (GREEDY && (f > m || (f == m && at < id))) id = at;
+    if (f > m) {
+      z *= ptx::ex2_approx((m - f) * c);
+      m = f;
+    }
+    z += ptx::ex2_approx((f - m) * c);
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(VD_THREADS, 4) verify_rows_kernel(const __grid_constant__ VdArgs a) {
+  __shared__ float s_m[VD_WARPS], s_z[VD_WARPS];
+  __shared__ int s_id[VD_WARPS];
+  __shared__ int s_seq;
+  allow_dependents_launch();
+  grid_dependency_wait();
+  const int part = blockIdx.x % a.parts, side = blockIdx.x / a.parts % 2, row = blockIdx.x / a.parts / 2;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  PackedView b;
+  b.q_offsets = a.q_offsets;
+  b.n_seqs = a.n_seqs;
+  b.n_tokens = a.n_rows;
+  if (warp == 0) {
+    const int i = find_seq(b, row);
+    if (lane == 0) s_seq = i;
+  }
+  __syncthreads();
+  const int seq = s_seq;
+  if (seq < 0) return;
+  int first, n;
+  rows_of(a, seq, first, n);
+  const float t = temperature_of(a, seq);
+  if (n < 0 || !temperature_ok(t)) return;
+  const T *x;
+  if (side == 0) {
+    x = reinterpret_cast<const T *>(a.target) + (size_t)row * a.target_stride;
+  } else {
+    if (a.draft == nullptr || t == 0.f || row - first >= n - 1) return;
+    x = reinterpret_cast<const T *>(a.draft) + (size_t)seq * a.seq_stride + (size_t)(row - first) * a.step_stride;
+  }
+  const float c = t == 0.f ? VD_LOG2E : VD_LOG2E / t;
+  float m, z;
+  int id = INT_MAX;
+  if (t == 0.f) scan_part<T, true>(x, a.V, part, a.parts, c, m, z, id);
+  else scan_part<T, false>(x, a.V, part, a.parts, c, m, z, id);
+  auto join = [&](float om, float oz, int oid) {
+    if (om > m) id = oid;
+    else if (om == m) id = min(id, oid);
+    merge(m, z, om, oz, c);
+  };
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float om = __shfl_down_sync(0xffffffffu, m, o), oz = __shfl_down_sync(0xffffffffu, z, o);
+    const int oid = __shfl_down_sync(0xffffffffu, id, o);
+    join(om, oz, oid);
+  }
+  if (lane == 0) {
+    s_m[warp] = m;
+    s_z[warp] = z;
+    s_id[warp] = id;
+  }
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+#pragma unroll
+  for (int w = 1; w < VD_WARPS; ++w) join(s_m[w], s_z[w], s_id[w]);
+  a.part[((size_t)row * 2 + side) * a.parts + part] = VdPart{m, z, id, 0};
+}
+
+// ------------------------------------------------------------------ draw ---
+// A row's (m, z, id), from its parts, in every lane.
+__device__ __forceinline__ VdPart row_sum(const VdArgs &a, int row, int side, float c) {
+  const int lane = threadIdx.x & 31;
+  VdPart p{-FLT_MAX, 0.f, INT_MAX, 0};
+  if (lane < a.parts) {
+    const int4 v = ld_after_wait(reinterpret_cast<const int4 *>(a.part + ((size_t)row * 2 + side) * a.parts + lane));
+    p = VdPart{__int_as_float(v.x), __int_as_float(v.y), v.z, 0};
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float om = __shfl_xor_sync(0xffffffffu, p.m, o), oz = __shfl_xor_sync(0xffffffffu, p.z, o);
+    const int oid = __shfl_xor_sync(0xffffffffu, p.id, o);
+    if (om > p.m) p.id = oid;
+    else if (om == p.m) p.id = min(p.id, oid);
+    merge(p.m, p.z, om, oz, c);
+  }
+  // (the lanes add in different orders)
+  p.z = __shfl_sync(0xffffffffu, p.z, 0);
+  return p;
+}
+__device__ __forceinline__ bool row_ok(float z) { return z > 0.f && z <= FLT_MAX; }
+
+// The best so far of a race; all: of the one without the draft's share, which counts where
+// nothing is left of the other.
+struct VdBest {
+  float score, all;
+  int id, all_id;
+  __device__ __forceinline__ void join(float s, int i, float s_all, int i_all) {
+    if (s > score || (s == score && i < id)) {
+      score = s;
+      id = i;
+    }
+    if (s_all > all || (s_all == all && i_all < all_id)) {
+      all = s_all;
+      all_id = i_all;
+    }
+  }
+  __device__ __forceinline__ int drawn() const { return score > 0.f ? id : all > 0.f ? all_id : -1; }
+};
+
+template <typename T>
+__global__ void __launch_bounds__(VD_THREADS) verify_draw_kernel(const __grid_constant__ VdArgs a) {
+  constexpr int MOST = LLAMA_MAX_DRAFTS + 1;
+  __shared__ float s_m[2][MOST], s_z[2][MOST];
+  __shared__ int s_id[MOST];
+  __shared__ bool s_keep[MOST];
+  __shared__ double s_lp[MOST];  // ln p of each draft
+  __shared__ VdBest s_best[VD_WARPS];
+  __shared__ VdBest s_cta[VD_MAX_CLUSTER];  // of the cluster's first CTA: every CTA's
+  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  const int seq = blockIdx.x / a.cluster, rank = blockIdx.x % a.cluster;
+  if (a.cluster > 1) ptx::cluster_sync();  // every CTA runs: the first one's shared memory may be written
+  grid_dependency_wait();
+  int first, n;
+  rows_of(a, seq, first, n);
+  const float t = temperature_of(a, seq);
+  const bool fine = n >= 0 && temperature_ok(t);
+  if (!fine && rank == 0 && threadIdx.x == 0) report_status(a.status, LLAMA_ERR_RANGE);
+  const int width = a.max_drafts + 1;
+  int kept = 0, token = -1;
+  if (fine && n > 0) {  // the same in every CTA of the cluster
+    const bool greedy = t == 0.f;
+    const float c = greedy ? VD_LOG2E : VD_LOG2E / t;
+    const double per_t = greedy ? 1.0 : 1.0 / (double)t;
+    for (int k = warp; k < n; k += VD_WARPS) {
+      const VdPart p = row_sum(a, first + k, 0, c);
+      const bool has_draft = a.draft != nullptr && !greedy && k + 1 < n;
+      VdPart q{0.f, 0.f, 0, 0};
+      if (has_draft) q = row_sum(a, first + k, 1, c);
+      if (lane == 0) {
+        s_m[0][k] = p.m;
+        s_z[0][k] = p.z;
+        s_m[1][k] = q.m;
+        s_z[1][k] = has_draft && row_ok(q.z) ? q.z : 0.f;  // 0: the draft was certain
+        s_id[k] = p.id;
+        if (k + 1 < n) {
+          const int x = ld_after_wait(a.tokens + first + k + 1);
+          bool keep = false;
+          double lp = 0.0;
+          if (x < 0 || x >= a.V) {
+            if (rank == 0) report_status(a.status, LLAMA_ERR_RANGE);
+          } else if (row_ok(p.z)) {
+            const T *row = reinterpret_cast<const T *>(a.target) + (size_t)(first + k) * a.target_stride;
+            lp = ((double)ld_logit<T>(row + x) - (double)p.m) * per_t - log((double)p.z);
+            if (greedy) {
+              keep = x == p.id;
+            } else {
+              double lq = 0.0;
+              if (s_z[1][k] > 0.f) {
+                const T *drow = reinterpret_cast<const T *>(a.draft) + (size_t)seq * a.seq_stride + (size_t)k * a.step_stride;
+                lq = ((double)ld_logit<T>(drow + x) - (double)q.m) * per_t - log((double)q.z);
+              }
+              keep = (double)ld_float_after_wait(a.uniforms + (size_t)seq * a.max_drafts + k) < exp(lp - lq);
+            }
+          }
+          s_keep[k] = keep;
+          s_lp[k] = lp;
+        }
+      }
+    }
+    __syncthreads();
+    while (kept + 1 < n && s_keep[kept]) ++kept;
+    const bool refused = kept + 1 < n;
+    const float z = s_z[0][kept];
+    if (greedy) {
+      token = row_ok(z) ? s_id[kept] : -1;
+    } else if (row_ok(z)) {
+      const T *x = reinterpret_cast<const T *>(a.target) + (size_t)(first + kept) * a.target_stride;
+      const float *noise = a.noise + (size_t)seq * a.noise_stride;
+      const bool both = refused && s_z[1][kept] > 0.f;
+      const T *y = both ? reinterpret_cast<const T *>(a.draft) + (size_t)seq * a.seq_stride + (size_t)kept * a.step_stride
+                        : nullptr;
+      const int banned = refused && !both ? ld_after_wait(a.tokens + first + kept + 1) : -1;
+      const float m = s_m[0][kept], mq = s_m[1][kept], inv = 1.f / z, inv_q = both ? 1.f / s_z[1][kept] : 0.f;
+      VdBest best{0.f, 0.f, INT_MAX, INT_MAX};
+      auto race = [&](float fx, float fy, float e, int id) {
+        if (!(e > 0.f)) return;
+        const float p = ptx::ex2_approx((fx - m) * c) * inv;
+        float w = p;
+        if (both) w = fmaxf(p - ptx::ex2_approx((fy - mq) * c) * inv_q, 0.f);
+        if (id == banned) w = 0.f;
+        // (0 does not win: ids start behind every other)
+        const float s = w / e, s_all = p / e;
+        if (s > best.score) {
+          best.score = s;
+          best.id = id;
+        }
+        if (s_all > best.all) {
+          best.all = s_all;
+          best.all_id = id;
+        }
+      };
+      constexpr int N = Vec16<T>::N;
+      const bool whole = ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(noise) |
+                           reinterpret_cast<uintptr_t>(y)) & 15) == 0;
+      const int stride = a.cluster * VD_THREADS, me = rank * VD_THREADS + (int)threadIdx.x;
+      int done = 0;  // ids below are searched by whole vectors
+      if (whole) {
+        const int n_vec = a.V / N;
+        done = n_vec * N;
+        for (int v = me; v < n_vec; v += 2 * stride) {
+          Vec16<T> fx[2], fy[2];
+          float4 e[2][N / 4];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int at = v + k * stride;
+            if (at >= n_vec) continue;
+            fx[k] = load16<T>(x + (size_t)at * N);
+            if (both) fy[k] = load16<T>(y + (size_t)at * N);
+#pragma unroll
+            for (int i = 0; i < N / 4; ++i) {
+              const uint4 u = ld_once_after_wait(noise + (size_t)at * N + 4 * i);
+              e[k][i] = *reinterpret_cast<const float4 *>(&u);
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int at = v + k * stride;
+            if (at >= n_vec) continue;
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+              race(fx[k].get(i), both ? fy[k].get(i) : 0.f, reinterpret_cast<const float *>(e[k])[i], at * N + i);
+          }
+        }
+      }
+      for (int v = done + me; v < a.V; v += 4 * stride) {
+        float fx[4], fy[4], e[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int at = v + k * stride;
+          e[k] = 0.f;
+          if (at >= a.V) continue;
+          fx[k] = ld_logit<T>(x + at);
+          fy[k] = both ? ld_logit<T>(y + at) : 0.f;
+          e[k] = ld_float_after_wait(noise + at);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (e[k] > 0.f) race(fx[k], fy[k], e[k], v + k * stride);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        const float s = __shfl_xor_sync(0xffffffffu, best.score, o), sa = __shfl_xor_sync(0xffffffffu, best.all, o);
+        const int i = __shfl_xor_sync(0xffffffffu, best.id, o), ia = __shfl_xor_sync(0xffffffffu, best.all_id, o);
+        best.join(s, i, sa, ia);
+      }
+      if (lane == 0) s_best[warp] = best;
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        for (int w = 1; w < VD_WARPS; ++w) best.join(s_best[w].score, s_best[w].id, s_best[w].all, s_best[w].all_id);
+        // into the first CTA's array, through distributed shared memory
+        uint32_t dst = ptx::smem_u32(&s_cta[rank]);
+        if (a.cluster > 1) dst = ptx::mapa_shared(dst, 0);
+        if (a.cluster > 1) {
+          ptx::st_cluster_u32(dst, __float_as_uint(best.score));
+          ptx::st_cluster_u32(dst + 4, __float_as_uint(best.all));
+          ptx::st_cluster_u32(dst + 8, (uint32_t)best.id);
+          ptx::st_cluster_u32(dst + 12, (uint32_t)best.all_id);
+        } else {
+          s_cta[0] = best;
+        }
+      }
+    }
+  }
+  if (a.cluster > 1) ptx::cluster_sync();
+  if (rank != 0) return;
+  __syncthreads();
+  const bool drawing = fine && n > 0 && t != 0.f && row_ok(s_z[0][kept]);
+  if (drawing) {
+    VdBest best = s_cta[0];
+    for (int k = 1; k < a.cluster; ++k) best.join(s_cta[k].score, s_cta[k].id, s_cta[k].all, s_cta[k].all_id);
+    token = best.drawn();
+  }
+  for (int k = threadIdx.x; k < width; k += VD_THREADS) {
+    int x = -1;
+    float lp = 0.f;
+    if (k < kept) {
+      x = ld_after_wait(a.tokens + first + k + 1);
+      lp = (float)s_lp[k];
+    } else if (k == kept && token >= 0) {
+      x = token;
+      const T *row = reinterpret_cast<const T *>(a.target) + (size_t)(first + kept) * a.target_stride;
+      lp = (float)(((double)ld_logit<T>(row + x) - (double)s_m[0][kept]) * (t == 0.f ? 1.0 : 1.0 / (double)t) -
+                   log((double)s_z[0][kept]));
+    }
+    a.out_tokens[(size_t)seq * width + k] = x;
+    if (a.logprobs != nullptr) a.logprobs[(size_t)seq * width + k] = lp;
+  }
+  if (threadIdx.x == 0) a.n_accepted[seq] = kept;
+}
+
+// Parts of a row: enough CTAs to fill the GPU several times over, none with less than
+// VD_MIN_PART logits.
+int parts_of(int n_rows, int V) {
+  const long long aim = 16LL * sm_count(), want = (aim + 2LL * n_rows - 1) / (2LL * n_rows);
+  const int most = V / VD_MIN_PART < VD_MAX_PARTS ? V / VD_MIN_PART : VD_MAX_PARTS;
+  return want < most ? (int)want : most > 1 ? most : 1;
+}
+
+}  // namespace
+
+size_t verify_drafts_workspace_bytes(int n_rows, int V) {
+  return n_rows == 0 ? 0 : (size_t)n_rows * 2 * parts_of(n_rows, V) * sizeof(VdPart);
+}
+
+template <typename T>
+cudaError_t launch_verify_drafts(const T *target, long long target_stride, const T *draft, long long seq_stride,
+                                 long long step_stride, int V, const llama_draft_batch &b, int *out_tokens,
+                                 int *n_accepted, float *logprobs, void *workspace, int *status, cudaStream_t st) {
+  VdArgs a;
+  a.target = target;
+  a.draft = draft;
+  a.target_stride = target_stride;
+  a.seq_stride = seq_stride;
+  a.step_stride = step_stride;
+  a.V = V;
+  a.q_offsets = b.q_offsets;
+  a.tokens = b.tokens;
+  a.temperatures = b.temperatures;
+  a.uniforms = b.uniforms;
+  a.noise = b.noise;
+  a.noise_stride = b.noise_stride;
+  a.n_seqs = b.n_seqs;
+  a.n_rows = b.n_rows;
+  a.max_drafts = b.max_drafts;
+  a.part = reinterpret_cast<VdPart *>(workspace);
+  a.out_tokens = out_tokens;
+  a.n_accepted = n_accepted;
+  a.logprobs = logprobs;
+  a.status = status;
+  a.parts = 1;
+  if (b.n_rows > 0) {
+    a.parts = parts_of(b.n_rows, V);
+    count_launch();
+    const cudaError_t e = launch_pdl(verify_rows_kernel<T>, dim3((unsigned)(b.n_rows * 2LL * a.parts)),
+                                     dim3(VD_THREADS), 0, st, a);
+    if (e != cudaSuccess) return e;
+  }
+  // clusters as large as keep every SM at work, a CTA not below VD_MIN_PART ids
+  a.cluster = 1;
+  while (a.cluster < VD_MAX_CLUSTER && 2LL * a.cluster * b.n_seqs <= 4LL * sm_count() && V / (2 * a.cluster) >= VD_MIN_PART)
+    a.cluster *= 2;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)a.cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(b.n_seqs * a.cluster));
+  cfg.blockDim = dim3(VD_THREADS);
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.cluster > 1 ? 2 : 1;
+  count_launch();
+  return cudaLaunchKernelEx(&cfg, verify_draw_kernel<T>, a);
+}
+
+template cudaError_t launch_verify_drafts<float>(const float *, long long, const float *, long long, long long, int,
+                                                 const llama_draft_batch &, int *, int *, float *, void *, int *,
+                                                 cudaStream_t);
+template cudaError_t launch_verify_drafts<bf16>(const bf16 *, long long, const bf16 *, long long, long long, int,
+                                                const llama_draft_batch &, int *, int *, float *, void *, int *,
+                                                cudaStream_t);
+
+}  // namespace llama

@@ -230,8 +230,79 @@ llama_status llama_op_attention_paged_decode(int32_t dtype, const void *q, const
                                              int32_t H, int32_t G, int32_t D, void *workspace,
                                              size_t workspace_bytes, int32_t *status, llama_stream stream);
 
+/* ------------------------------------------------------------------------
+ * A paged key-value cache held in 4 bits.
+ *
+ * The method's pages have no counterpart: these entry points are the ones above
+ * over pages that hold each value in 4 bits and a scale for 16 of them, 9/32 of
+ * what bf16 takes (llama_op_rope_kv4_write_paged for llama_op_rope_kv_write_paged
+ * and so on; everything said there about batches, lengths, offsets, page ids,
+ * status, workspaces, streams and graphs holds here too).
+ *
+ * Pages: a llama_paged_kv_cache whose k and v are pools of bytes,
+ * [n_pages][n_kv_heads][llama_kv4_block_bytes(page_size, d_head)], with
+ * page_stride in bytes (0: dense; otherwise a multiple of 16, at least
+ * n_kv_heads blocks).  A block, the rows of one page and KV head, is
+ *     page_size rows of d_head / 2 bytes: the codes, and behind them
+ *     page_size rows of d_head / 16 bytes: the scales.
+ * Eight elements 8w .. 8w + 7 of a row are the four bytes of a little-endian
+ * word; element 8w + e is the four bits from bit 4 (e / 2) + 16 (e % 2) (the even
+ * elements in the low half, the odd ones in the high half).  A code n, 0 to 15,
+ * stands for (n - 8) s; s is the scale of its 16 elements, a byte b that stands
+ * for 2^(b / 8 - 20) (1 + (b % 8) / 8), b / 8 rounded down: 2^-20 to 3840.  Every
+ * such value is a bf16 (seven significant bits at most), and every byte is a
+ * valid code or scale.
+ * A page id outside [0, n_pages) reads as a page of zeros, is not written, and
+ * records LLAMA_ERR_RANGE. */
+
+/* Bytes of one page's rows of one KV head: page_size * (d_head / 2 + d_head / 16);
+ * 0 for a page size or head width that is not supported. */
+size_t llama_kv4_block_bytes(int32_t page_size, int32_t d_head);
+
+/* RoPE and the write of keys and values into 4-bit pages.  Arguments as for
+ * llama_op_rope_kv_write_paged; dtype is that of qkv and q_out.  k is rotated in
+ * fp32 (each product and their difference or sum rounded to fp32) and stored
+ * from there, v as it is.  Of each 16 elements x with the largest magnitude a:
+ *     s = the smallest scale that is at least a / 7 (2^-20 when a is 0)
+ *     n = 8 + x / s rounded to the nearest whole number, even ones at ties
+ * so that |x - (n - 8) s| <= s / 2 and n is 1 to 15.  A value beyond 7 * 3840 =
+ * 26880 in magnitude is stored as that, a NaN as 0; both record LLAMA_ERR_RANGE. */
+llama_status llama_op_rope_kv4_write_paged(int32_t dtype, const void *qkv, void *q_out,
+                                           const llama_paged_kv_cache *kv, const llama_packed_batch *batch,
+                                           const float *table, int32_t table_max_seq, int32_t H, int32_t G,
+                                           int32_t D, int32_t layout, int32_t *status, llama_stream stream);
+
+/* Keys and values back from 4-bit pages: rows [q_offsets[i], q_offsets[i + 1]) of
+ * k_out and v_out [n_tokens][G][D] get, in dtype (exactly), what the pages hold at
+ * the last positions of sequence i -- of its new tokens behind a write, of the
+ * whole sequence where it has as many rows as kv_lens[i].  A row before the
+ * sequence's start (it has more rows than kv_lens[i]) gets zeros.  Of the batch,
+ * n_tokens counts rows of k_out and v_out; either may be NULL. */
+llama_status llama_op_kv4_read_paged(int32_t dtype, const llama_paged_kv_cache *kv, const llama_packed_batch *batch,
+                                     void *k_out, void *v_out, int32_t G, int32_t D, int32_t *status,
+                                     llama_stream stream);
+
+/* llama_op_attention_packed over 4-bit pages; dtype is that of q and o.  With
+ * LLAMA_BF16 the products are those of a bf16 cache that holds the values the
+ * pages stand for. */
+size_t llama_op_attention_packed_kv4_workspace_bytes(int32_t dtype, const llama_packed_batch *batch, int32_t H,
+                                                     int32_t G, int32_t D);
+llama_status llama_op_attention_packed_kv4(int32_t dtype, const void *q, const llama_paged_kv_cache *kv,
+                                           const llama_packed_batch *batch, void *o, int32_t H, int32_t G, int32_t D,
+                                           void *workspace, size_t workspace_bytes, int32_t *status,
+                                           llama_stream stream);
+
+/* llama_op_attention_paged_decode over 4-bit pages; dtype is that of q and o. */
+size_t llama_op_attention_paged_decode_kv4_workspace_bytes(int32_t dtype, int32_t n_seqs, int32_t max_kv_len,
+                                                           int32_t H, int32_t G, int32_t D);
+llama_status llama_op_attention_paged_decode_kv4(int32_t dtype, const void *q, const llama_paged_kv_cache *kv,
+                                                 const int32_t *kv_lens, int32_t n_seqs, int32_t max_kv_len, void *o,
+                                                 int32_t H, int32_t G, int32_t D, void *workspace,
+                                                 size_t workspace_bytes, int32_t *status, llama_stream stream);
+
 /* Bound, in SM clock cycles, on every wait of the bf16 kernels of
- * llama_op_attention_packed and llama_op_attention_paged_decode that gives up,
+ * llama_op_attention_packed, llama_op_attention_packed_kv4 and
+ * llama_op_attention_paged_decode that gives up,
  * for later calls (and captures) of the process; 0 restores the default, about
  * 4e9 cycles (2 s at 2 GHz), which no legitimate wait reaches.  As
  * llama_block_set_wait_budget: a wait that runs out records
@@ -263,6 +334,76 @@ llama_status llama_op_set_wait_budget(int64_t cycles);
 llama_status llama_op_token_logprobs(int32_t dtype, const void *logits, int64_t row_stride, const int32_t *targets,
                                      int32_t T, int32_t V, float *logprobs, float *entropy, int32_t top_k,
                                      int32_t *top_ids, float *top_logprobs, int32_t *status, llama_stream stream);
+
+/* ------------------------------------------------------------------------
+ * Drafted tokens.
+ *
+ * A cheap model, or a look-up, drafts the next tokens of each sequence; one step
+ * of the full model then gives its logits at all of them (the rows of a
+ * llama_packed_batch: the last confirmed token and the drafts behind it), and
+ * llama_op_verify_drafts keeps or replaces them so that what comes out is
+ * distributed as if the full model had drawn every token itself.
+ *
+ * Sequence i owns rows [q_offsets[i], q_offsets[i + 1]): one more than it has
+ * drafts, at most max_drafts + 1, or none (an empty slot).  tokens [n_rows] holds
+ * the token at each row, so that row r's logits judge the draft tokens[r + 1]: draft
+ * j of sequence i (from 0) is tokens[q_offsets[i] + 1 + j].  Rows behind the last
+ * sequence are not read.
+ * temperatures: fp32 [n_seqs] (NULL: all 1); probabilities are those of the logits
+ * divided by it, and a sequence with temperature 0 (or a denormal) is decoded
+ * greedily.
+ * uniforms: fp32 [n_seqs][max_drafts], one in [0, 1) for every draft.
+ * noise: fp32 [n_seqs][V], rows noise_stride elements apart (>= V): independent
+ * exponential variates (-ln of a uniform); an id whose variate is not above 0 (or
+ * is NaN) is never drawn.  uniforms and noise may both be NULL: every sequence is
+ * then decoded greedily, whatever the temperatures. */
+#define LLAMA_MAX_DRAFTS 64
+typedef struct {
+    const int32_t *q_offsets;
+    const int32_t *tokens;
+    const float *temperatures;
+    const float *uniforms;
+    const float *noise;
+    int64_t noise_stride;
+    int32_t n_seqs;     /* at most LLAMA_PACKED_MAX_SEQS */
+    int32_t n_rows;
+    int32_t max_drafts; /* 0 to LLAMA_MAX_DRAFTS */
+} llama_draft_batch;
+
+/* Verifies drafts.  target_logits: [n_rows][V] of dtype, rows target_stride
+ * elements apart (>= V).  draft_logits: the logits that draft j of sequence i was
+ * drawn from, at the same temperature, begin draft_seq_stride * i +
+ * draft_step_stride * j elements behind it (neither stride negative), so that
+ * [n_seqs][max_drafts][V] and the [max_drafts][n_seqs][V] of a draft model's steps
+ * both serve; NULL: every draft was certain (a look-up, a greedy draft).  Columns
+ * at and behind V are not read; every array needs the alignment of its elements
+ * only.  With p and q the target's and the draft's probabilities at draft j's row:
+ *   the draft x is kept while u < p[x] / q[x] (q[x] = 1 for certain drafts);
+ *   in place of the first that is not kept, a token is drawn from
+ *   max(p - q, 0) (a certain draft: p without x), from p where that is 0 everywhere;
+ *   behind drafts that were all kept, a token is drawn from p at the last row;
+ *   drawn from w: the id of the largest w[v] / noise[i][v], the lowest among equals.
+ * Greedy: a draft is kept while it is the id of the largest logit (the lowest id
+ * among equals), and the token behind is that id.
+ *   out_tokens [n_seqs][max_drafts + 1]: the kept drafts, the token drawn, then -1
+ *   n_accepted [n_seqs]: drafts kept
+ *   logprobs   [n_seqs][max_drafts + 1]: ln p of each token of out_tokens, at the
+ *              sequence's temperature (greedy: 1), 0 beside a -1; may be NULL
+ * p and q are summed in fp32, in parts; the test u < p / q is taken in fp64 on the sums.
+ * A logit of -inf has probability 0.  A row that holds a NaN or +inf, or nothing but
+ * -inf, keeps no draft and draws no token (-1, logprob 0).  Nor does an empty slot,
+ * and neither does a sequence whose offsets or row count are out of range or whose
+ * temperature is negative or not finite, which record LLAMA_ERR_RANGE.  A draft
+ * outside [0, V) is not kept and records it too.  Rows of draft logits that hold a
+ * NaN or +inf, or nothing but -inf, count as certain drafts.
+ * workspace: at least llama_op_verify_drafts_workspace_bytes bytes (which reads
+ * n_rows of the batch alone), 16-byte aligned. */
+size_t llama_op_verify_drafts_workspace_bytes(const llama_draft_batch *batch, int32_t V);
+llama_status llama_op_verify_drafts(int32_t dtype, const void *target_logits, int64_t target_stride,
+                                    const void *draft_logits, int64_t draft_seq_stride,
+                                    int64_t draft_step_stride, int32_t V, const llama_draft_batch *batch,
+                                    int32_t *out_tokens, int32_t *n_accepted, float *logprobs, void *workspace,
+                                    size_t workspace_bytes, int32_t *status, llama_stream stream);
 
 #ifdef __cplusplus
 }
