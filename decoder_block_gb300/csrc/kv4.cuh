@@ -60,23 +60,64 @@ __device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
   return d;
 }
 
-// A code n under bf16's mantissa reads as 16 + n (bits 3 to 6 of 16.0 = 0x4180); times s and
-// less 24 s, in one rounding that has nothing to round, it is (n - 8) s.  24 s has five
-// significant bits; with the code in the lowest bits, 128 + n, 136 s would have up to nine
-// and not be a bf16.
-constexpr uint32_t KV4_MASK = 0x00780078u, KV4_MAGIC = 0x41804180u;
-__device__ __forceinline__ uint32_t kv4_bias2(uint32_t scale2) { return bf16x2_mul(scale2, 0xc1c0c1c0u); }  // -24 s
+// A code n in the mantissa of 16.0 or 128.0 reads as 16 + n (bits 3 to 6 of a bf16) or 128 + n
+// (bits 0 to 3); times s and less 24 s or 136 s, in one rounding that has nothing to round,
+// it is (n - 8) s.  (24 s and 136 s are bf16 too: s is 8 to 15 times a power of two, and
+// 17 * 15 = 255.)  The codes in the lowest bits need no shift.
+struct Kv4Scale {
+  uint32_t s, b24, b136;
+};
+// From a byte for each half.
+__device__ __forceinline__ Kv4Scale kv4_scales(uint32_t lo, uint32_t hi) {
+  Kv4Scale r;
+  r.s = kv4_scale2(lo, hi);
+  r.b24 = bf16x2_mul(r.s, 0xc1c0c1c0u);
+  r.b136 = bf16x2_mul(r.s, 0xc308c308u);
+  return r;
+}
+// A byte for both.
+__device__ __forceinline__ Kv4Scale kv4_scales(uint32_t byte) {
+  Kv4Scale r;
+  r.s = byte * 0x00100010u + KV4_SCALE_BASE * 0x00100010u;
+  r.b24 = bf16x2_mul(r.s, 0xc1c0c1c0u);
+  r.b136 = bf16x2_mul(r.s, 0xc308c308u);
+  return r;
+}
 // Codes in bits 4 j .. and 4 j + 16 .. of a word (elements 2 j and 2 j + 1 of its eight).
 template <int J>
-__device__ __forceinline__ uint32_t kv4_pair(uint32_t w, uint32_t scale2, uint32_t bias2) {
-  const uint32_t at = J == 0 ? w << 3 : w >> (J == 0 ? 0 : 4 * J - 3);
-  return bf16x2_fma((at & KV4_MASK) | KV4_MAGIC, scale2, bias2);
+__device__ __forceinline__ uint32_t kv4_pair(uint32_t w, const Kv4Scale &k) {
+  if constexpr (J == 0) return bf16x2_fma((w & 0x000f000fu) | 0x43004300u, k.s, k.b136);
+  return bf16x2_fma(((w >> (J == 0 ? 0 : 4 * J - 3)) & 0x00780078u) | 0x41804180u, k.s, k.b24);
 }
 // Eight elements as bf16.
-__device__ __forceinline__ uint4 kv4_eight(uint32_t w, uint32_t scale2, uint32_t bias2) {
-  return make_uint4(kv4_pair<0>(w, scale2, bias2), kv4_pair<1>(w, scale2, bias2), kv4_pair<2>(w, scale2, bias2),
-                    kv4_pair<3>(w, scale2, bias2));
+__device__ __forceinline__ uint4 kv4_eight(uint32_t w, const Kv4Scale &k) {
+  return make_uint4(kv4_pair<0>(w, k), kv4_pair<1>(w, k), kv4_pair<2>(w, k), kv4_pair<3>(w, k));
 }
+
+// Half of every value is an fp16 (a multiple of 2^-24, at most 15360), and so is all that
+// comes on the way there: 16 + n (bits 6 to 9 of 16.0) times s / 2, less 12 s.  Values that
+// are to be weighted are taken so, where the weights can be fp16 too.
+struct Kv4Half {
+  uint32_t s, b;
+};
+__device__ __forceinline__ Kv4Half kv4_halves(uint32_t lo, uint32_t hi) {
+  const float a = __uint_as_float((lo + KV4_SCALE_BASE - 8) << 20), b = __uint_as_float((hi + KV4_SCALE_BASE - 8) << 20);
+  Kv4Half r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r.s) : "f"(b), "f"(a));
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r.b) : "r"(r.s), "r"(0xce00ce00u));  // -24
+  return r;
+}
+template <int J>
+__device__ __forceinline__ uint32_t kv4_half_pair(uint32_t w, const Kv4Half &k) {
+  const uint32_t at = J == 0 ? w << 6 : J == 1 ? w << 2 : J == 2 ? w >> 2 : w >> 6;
+  uint32_t d;
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"((at & 0x03c003c0u) | 0x4c004c00u), "r"(k.s), "r"(k.b));
+  return d;
+}
+__device__ __forceinline__ uint4 kv4_half_eight(uint32_t w, const Kv4Half &k) {
+  return make_uint4(kv4_half_pair<0>(w, k), kv4_half_pair<1>(w, k), kv4_half_pair<2>(w, k), kv4_half_pair<3>(w, k));
+}
+
 // Four elements 4 (c % 2) .. of eight as fp32.
 __device__ __forceinline__ float4 kv4_four(uint32_t w, int half, float scale) {
   w >>= 8 * half;

@@ -24,6 +24,7 @@
 // what begins or ends inside the CTA's run goes to the workspace, where a second kernel
 // joins it, in order.  With short sequences (direct) a CTA takes one item instead, and there
 // is no second kernel.
+#include <cuda_fp16.h>
 #include <float.h>
 
 #include "kv4.cuh"
@@ -35,6 +36,11 @@ namespace {
 
 constexpr int KD_KEYS = 32;  // keys of a warp's tile
 constexpr float KD_RESCALE = 8.0f;  // log2 units: the running maximum is raised when it grows by > 2^8
+// Weights are fp16 for their product with V: 2^7 times what they are, so that the largest,
+// 2^15, has room above, and what is less than 2^-31 of the running maximum's, not 2^-24, is
+// lost (120000 keys of such weights: 2^-14 of the sum).
+constexpr float KD_WEIGHT = 7.0f;
+constexpr float KD_VALUE = 2.0f;  // V's operand is half of V
 // Key tiles of a CTA's item in the direct form, at most.
 constexpr int KD_DIRECT_TILES = 64;
 
@@ -83,6 +89,11 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void mma16816_half(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
@@ -90,6 +101,10 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 }
 __device__ __forceinline__ uint32_t kd_pack2(float a, float b) {
   __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<uint32_t *>(&h);
+}
+__device__ __forceinline__ uint32_t kd_pack_half2(float a, float b) {
+  __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<uint32_t *>(&h);
 }
 template <int BYTES>
@@ -117,29 +132,38 @@ __device__ __forceinline__ uint32_t ld_byte(uint32_t at) {
 
 // A place in the row of tiles.
 struct KdCursor {
-  int seq, unit, j, n;  // n: tiles of the sequence
-  __device__ __forceinline__ void seek(const int *first, int n_seqs, int units, long long at) {
-    int lo = 0, hi = n_seqs;  // the last sequence that begins at or before it
+  int seq, unit, g, j, n, len;  // n: tiles of the sequence, len: its keys
+  __device__ __forceinline__ void seek(const KdArgs &a, const int *first, long long at) {
+    int lo = 0, hi = a.n_seqs;  // the last sequence that begins at or before it
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
-      if ((long long)first[mid] * units <= at) lo = mid;
+      if ((long long)first[mid] * a.units <= at) lo = mid;
       else hi = mid;
     }
-    seq = lo;
     n = first[lo + 1] - first[lo];
-    const long long rest = at - (long long)first[lo] * units;
-    unit = n > 0 ? (int)(rest / n) : 0;
-    j = n > 0 ? (int)(rest % n) : 0;
+    const long long rest = at - (long long)first[lo] * a.units;
+    set(a, lo, (int)(rest / n), (int)(rest % n), n);
   }
-  __device__ __forceinline__ void next(const int *first, int n_seqs, int units) {
-    if (++j < n) return;
-    j = 0;
-    if (++unit < units) return;
-    unit = 0;
-    for (++seq; seq < n_seqs; ++seq) {
-      n = first[seq + 1] - first[seq];
-      if (n > 0) break;
+  __device__ __forceinline__ void set(const KdArgs &a, int s, int u, int at, int tiles) {
+    seq = s;
+    unit = u;
+    g = u / a.subs;
+    j = at;
+    n = tiles;
+    len = ld_after_wait(a.kv_lens + s);
+  }
+  __device__ __forceinline__ void next(const KdArgs &a, const int *first) {
+    if (++j < n || a.direct) return;
+    int s = seq, u = unit + 1;
+    if (u == a.units) {
+      u = 0;
+      for (++s; s < a.n_seqs; ++s) {
+        n = first[s + 1] - first[s];
+        if (n > 0) break;
+      }
+      if (s == a.n_seqs) return;  // the end of the row
     }
+    set(a, s, u, 0, n);
   }
 };
 
@@ -160,8 +184,26 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_decode_ker
   grid_dependency_wait();
 
   // ------------------------------------------------------------- lengths ---
-  // (4096 sequences: 8 or 16 each)
-  {
+  if (lane < 2) meta[warp * 2 + lane].seq = -1;
+  auto no_keys = [&](int i, int from, int step) {  // sequence i: zeros
+    uint4 *dst = reinterpret_cast<uint4 *>(a.o + (size_t)i * a.H * D);
+    for (int e = from; e < a.H * D / 8; e += step) dst[e] = make_uint4(0, 0, 0, 0);
+  };
+  KdCursor at = {0, 0, 0, 0, 0, 0};
+  long long begin = 0, each = 1;
+  int n_run;  // tiles of this CTA's run
+  if (a.direct) {
+    const int seq = blockIdx.x / a.units, unit = blockIdx.x % a.units;
+    const int raw = ld_after_wait(a.kv_lens + seq), len = checked_len(raw, a.max_kv_len, a.pv);
+    if (raw != len && unit == 0 && threadIdx.x == 0) report_status(a.status, LLAMA_ERR_RANGE);
+    n_run = (len + KD_KEYS - 1) / KD_KEYS;
+    if (n_run == 0) {
+      if (unit == 0) no_keys(seq, threadIdx.x, THREADS);
+      return;
+    }
+    at.set(a, seq, unit, 0, n_run);
+  } else {
+    // (4096 sequences: 8 or 16 each)
     const int per = (a.n_seqs + THREADS - 1) / THREADS;
     int mine = 0;
     for (int k = 0; k < per; ++k) {
@@ -172,10 +214,7 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_decode_ker
       const int n = (len + KD_KEYS - 1) / KD_KEYS;
       first[i] = n;
       mine += n;
-      if (n == 0 && i % (int)gridDim.x == (int)blockIdx.x) {  // no keys: zeros
-        uint4 *dst = reinterpret_cast<uint4 *>(a.o + (size_t)i * a.H * D);
-        for (int e = 0; e < a.H * D / 8; ++e) dst[e] = make_uint4(0, 0, 0, 0);
-      }
+      if (n == 0 && i % (int)gridDim.x == (int)blockIdx.x) no_keys(i, 0, 1);
     }
     int end = mine;
 #pragma unroll
@@ -195,80 +234,82 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_decode_ker
       before += n;
     }
     if (threadIdx.x == THREADS - 1) first[a.n_seqs] = before;
-    if (lane < 2) meta[warp * 2 + lane].seq = -1;
     __syncthreads();
-  }
-
-  // ----------------------------------------------------------------- runs ---
-  long long begin, end, each = 1;
-  if (a.direct) {
-    const int seq = blockIdx.x / a.units, unit = blockIdx.x % a.units, n = first[seq + 1] - first[seq];
-    begin = (long long)first[seq] * a.units + (long long)unit * n;
-    end = begin + n;
-  } else {
     const long long total = (long long)first[a.n_seqs] * a.units;
     each = (total + gridDim.x - 1) / gridDim.x;
     each = each > L::WARPS ? each : L::WARPS;
     begin = min(total, each * blockIdx.x);
-    end = min(total, begin + each);
+    n_run = (int)(min(total, begin + each) - begin);
   }
-  const int len_run = (int)(end - begin);
-  const int w0 = (int)((long long)len_run * warp / L::WARPS), w1 = (int)((long long)len_run * (warp + 1) / L::WARPS);
+  const int w0 = (int)((long long)n_run * warp / L::WARPS), w1 = (int)((long long)n_run * (warp + 1) / L::WARPS);
   const uint32_t ring = s0 + warp * L::RING;
 
   // -------------------------------------------------------------- copies ---
-  KdCursor ahead = {0, 0, 0, 0};  // the tile whose pages are known and that is copied next
-  int left = w1 - w0;
-  int page = -2;   // lanes 0, 1: pages of its rows 0-15, 16-31 (-1: bad id, -2: none)
+  // Lanes 0 to 7 look up where a tile's rows lie: bit 0 says which 16 rows, bit 1 K or V, bit
+  // 2 codes or scales.  A half behind the last key is given the first half's rows, which may
+  // be read; its scores are replaced.
+  KdCursor ahead = at;  // the tile whose pages are known and that is copied next
+  int left = w1 - w0, id = 0, slot = 0;
+  const int rows_mask = (1 << a.pv.page_log2) - 1;
+  const uint8_t *const pool = lane & 2 ? a.v : a.k;
+  const int row_bytes = lane & 4 ? L::SB : L::RB, to_scales = lane & 4 ? L::RB << a.pv.page_log2 : 0;
+  const int block = kv4_block_bytes(1 << a.pv.page_log2, D);
   auto look_up = [&] {
-    page = -2;
-    if (left > 0 && lane < 2) {
-      const int p = ahead.j * KD_KEYS + lane * 16;
-      if (p < ld_after_wait(a.kv_lens + ahead.seq)) {
-        page = a.pv.page(ahead.seq, p >> a.pv.page_log2);
-        if (page < 0) report_status(a.status, LLAMA_ERR_RANGE);
-      }
+    if (left > 0 && lane < 8) {
+      int p = ahead.j * KD_KEYS + (lane & 1) * 16;
+      p = p < ahead.len ? p : ahead.j * KD_KEYS;
+      slot = p & rows_mask;
+      id = ld_after_wait(a.pv.table + (size_t)ahead.seq * a.pv.table_stride + (p >> a.pv.page_log2));
     }
   };
   auto request = [&](int n) {
-    const int pages[2] = {__shfl_sync(0xffffffffu, page, 0), __shfl_sync(0xffffffffu, page, 1)};
     if (left > 0) {
-      const int g = ahead.unit / a.subs, p0 = ahead.j * KD_KEYS, mask = (1 << a.pv.page_log2) - 1;
       const uint32_t stage = ring + n % L::STAGES * L::STAGE;
       constexpr int CHUNK = L::RB < 16 ? L::RB : 16, PER_ROW = L::RB / CHUNK;
+      const bool bad = lane < 8 && (unsigned)id >= (unsigned)a.pv.n_pages;
+      const unsigned bads = __ballot_sync(0xffffffffu, bad);
+      const uint8_t *ptr = pool;
+      if (!bad) ptr += id * a.pv.page_stride + (ahead.g * block + to_scales + slot * row_bytes);
+      auto rows_at = [&](int from) {
+        return reinterpret_cast<const uint8_t *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(ptr), from));
+      };
+      auto copies = [&](bool all_good) {
 #pragma unroll
-      for (int which = 0; which < 2; ++which) {
-        const uint8_t *pool = which ? a.v : a.k;
-        const uint32_t dst = stage + which * L::HALF;
+        for (int which = 0; which < 2; ++which)
 #pragma unroll
-        for (int i = 0; i < PER_ROW; ++i) {
-          const int row = (i * 32 + lane) / PER_ROW, at = (i * 32 + lane) % PER_ROW * CHUNK;
-          const int pg = row < 16 ? pages[0] : pages[1];
-          const uint32_t to = dst + row * L::RB + at;
-          if (pg >= 0) {
-            copy_async<CHUNK>(to, kv4_row(pool, a.pv, pg, g, D, (p0 + row) & mask).codes + at);
-          } else if (pg == -1) {  // a page of zeros
-            asm volatile("st.shared.v2.u32 [%0], {%1, %1};" ::"r"(to), "r"(0x88888888u) : "memory");
-            if (CHUNK == 16)
-              asm volatile("st.shared.v2.u32 [%0], {%1, %1};" ::"r"(to + 8), "r"(0x88888888u) : "memory");
+          for (int i = 0; i < PER_ROW; ++i) {
+            const int byte = (i * 32 + lane) * CHUNK, half = D >= 64 ? i * 32 / PER_ROW / 16 : lane / 16;
+            const uint32_t to = stage + which * L::HALF + byte;
+            const uint8_t *from = rows_at(which * 2 + half) + (byte - half * 16 * L::RB);
+            if (all_good || !(bads >> (which * 2 + half) & 1)) {
+              copy_async<CHUNK>(to, from);
+            } else {  // a page of zeros
+              asm volatile("st.shared.v2.u32 [%0], {%1, %1};" ::"r"(to), "r"(0x88888888u) : "memory");
+              if (CHUNK == 16)
+                asm volatile("st.shared.v2.u32 [%0], {%1, %1};" ::"r"(to + 8), "r"(0x88888888u) : "memory");
+            }
           }
-        }
-        const int l = lane - 16 * which;  // K's scales: lanes 0 .., V's: lanes 16 ..
-        if (l >= 0 && l < 2 * L::SB) {
-          const int row = l * 16 / L::SB, pg = row < 16 ? pages[0] : pages[1];
-          if (pg >= 0)
-            copy_async<16>(dst + KD_KEYS * L::RB + l * 16, kv4_row(pool, a.pv, pg, g, D, (p0 + row) & mask).scales);
-        }
+        // scales: K's by lanes 0 .., V's by lanes 16 ..
+        const int which = lane / 16, l = lane % 16, half = l / L::SB & 1, src = 4 + which * 2 + half;
+        const uint8_t *from = rows_at(src) + l % L::SB * 16;
+        if (l < 2 * L::SB && (all_good || !(bads >> src & 1)))
+          copy_async<16>(stage + which * L::HALF + KD_KEYS * L::RB + l * 16, from);
+      };
+      if (bads == 0) {
+        copies(true);
+      } else {
+        if (lane == 0) report_status(a.status, LLAMA_ERR_RANGE);
+        copies(false);
       }
-      ahead.next(first, a.n_seqs, a.units);
+      ahead.next(a, first);
       --left;
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
 
   if (left > 0) {
-    KdCursor at;
-    at.seek(first, a.n_seqs, a.units, begin + w0);
+    if (a.direct) at.j = w0;
+    else at.seek(a, first, begin + w0);
     ahead = at;
     look_up();
 #pragma unroll 1
@@ -282,8 +323,8 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_decode_ker
       // ----------------------------------------------------------- a piece ---
       const int seq = at.seq, unit = at.unit, j0 = at.j, n_tiles = at.n;
       const int j1 = min(n_tiles, j0 + todo - done);
-      const int len = ld_after_wait(a.kv_lens + seq);
-      const int g = unit / a.subs, h_in = unit % a.subs * (8 * NB), nh = min(8 * NB, a.r - h_in);
+      const int len = at.len, g = at.g;
+      const int h_in = (unit - g * a.subs) * (8 * NB), nh = min(8 * NB, a.r - h_in);
       const size_t row0 = (size_t)seq * a.H + g * a.r + h_in;
       uint32_t qf[NB][STEPS][2];
 #pragma unroll
@@ -323,7 +364,8 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_decode_ker
           for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int e = 0; e < 4; ++e) sc[mb][b][e] = 0.f;
-          uint32_t w[2][KW], sa[2], sb[2];
+          uint32_t w[2][KW];
+          Kv4Scale sa[2], sb[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int row = mb * 16 + e * 8 + gi;
@@ -334,31 +376,23 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_decode_ker
             if constexpr (D == 128) {
               uint16_t x;
               asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(scales + ti * 2));
-              sa[e] = x & 255;
-              sb[e] = x >> 8;
+              sa[e] = kv4_scales((uint32_t)x & 255);
+              sb[e] = kv4_scales((uint32_t)x >> 8);
             } else {
-              sa[e] = ld_byte(scales + (D == 64 ? ti : D == 32 ? ti / 2 : 0));
+              sa[e] = kv4_scales(ld_byte(scales + (D == 64 ? ti : D == 32 ? ti / 2 : 0)));
               sb[e] = sa[e];
             }
-            sa[e] = kv4_scale2(sa[e], sa[e]);
-            sb[e] = D == 128 ? kv4_scale2(sb[e], sb[e]) : sa[e];
           }
-          const uint32_t ba[2] = {kv4_bias2(sa[0]), kv4_bias2(sa[1])};
-          const uint32_t bb[2] = {D == 128 ? kv4_bias2(sb[0]) : ba[0], D == 128 ? kv4_bias2(sb[1]) : ba[1]};
 #pragma unroll
           for (int s = 0; s < STEPS; ++s) {
             // elements 4 s .. 4 s + 3 of the thread's; 16 of them share a scale
             uint32_t f[4];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const uint32_t word = w[e][s / 2], s2 = s < 4 ? sa[e] : sb[e], b2 = s < 4 ? ba[e] : bb[e];
-              if (s % 2 == 0) {
-                f[e] = kv4_pair<0>(word, s2, b2);
-                f[2 + e] = kv4_pair<1>(word, s2, b2);
-              } else {
-                f[e] = kv4_pair<2>(word, s2, b2);
-                f[2 + e] = kv4_pair<3>(word, s2, b2);
-              }
+              const uint32_t word = w[e][s / 2];
+              const Kv4Scale &k = s < 4 ? sa[e] : sb[e];
+              f[e] = s % 2 == 0 ? kv4_pair<0>(word, k) : kv4_pair<2>(word, k);
+              f[2 + e] = s % 2 == 0 ? kv4_pair<1>(word, k) : kv4_pair<3>(word, k);
             }
 #pragma unroll
             for (int b = 0; b < NB; ++b) mma16816(sc[mb][b], f, qf[b][s][0], qf[b][s][1]);
@@ -400,22 +434,24 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_decode_ker
               }
             }
           }
+          const float less[2] = {KD_WEIGHT - m[b][0], KD_WEIGHT - m[b][1]};
 #pragma unroll
           for (int mb = 0; mb < 2; ++mb) {
             float p[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              p[e] = ptx::ex2_approx(fmaf(sc[mb][b][e], a.scale_log2, -m[b][e & 1]));
+              p[e] = ptx::ex2_approx(fmaf(sc[mb][b][e], a.scale_log2, less[e & 1]));
               l[b][e & 1] += p[e];
             }
-            pf[mb][b][0] = transpose8x8(kd_pack2(p[0], p[1]));
-            pf[mb][b][1] = transpose8x8(kd_pack2(p[2], p[3]));
+            pf[mb][b][0] = transpose8x8(kd_pack_half2(p[0], p[1]));
+            pf[mb][b][1] = transpose8x8(kd_pack_half2(p[2], p[3]));
           }
         }
         // outputs: columns gi (D / 8) .. of the values, keys 2 ti, 2 ti + 1, and 8 more
 #pragma unroll
         for (int mb = 0; mb < 2; ++mb) {
-          uint32_t even[2][VW], odd[2][VW], s2[2], b2[2];
+          uint32_t even[2][VW], odd[2][VW];
+          Kv4Half sv2[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int row = mb * 16 + e * 8 + 2 * ti;
@@ -424,8 +460,7 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_decode_ker
             ld_words<VW>(at, x);
             ld_words<VW>(at + L::RB, y);
             const uint32_t sat = sv + KD_KEYS * L::RB + row * L::SB + gi * L::SB / 8;
-            s2[e] = kv4_scale2(ld_byte(sat), ld_byte(sat + L::SB));
-            b2[e] = kv4_bias2(s2[e]);
+            sv2[e] = kv4_halves(ld_byte(sat), ld_byte(sat + L::SB));
 #pragma unroll
             for (int w = 0; w < VW; ++w) {
               if constexpr (D == 32) {
@@ -445,19 +480,18 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_decode_ker
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const uint32_t ev = even[e][i / 4], od = odd[e][i / 4];
-              switch (i % 4) {
-                case 0: f[2 * e] = kv4_pair<0>(ev, s2[e], b2[e]); f[2 * e + 1] = kv4_pair<0>(od, s2[e], b2[e]); break;
-                case 1: f[2 * e] = kv4_pair<1>(ev, s2[e], b2[e]); f[2 * e + 1] = kv4_pair<1>(od, s2[e], b2[e]); break;
-                case 2: f[2 * e] = kv4_pair<2>(ev, s2[e], b2[e]); f[2 * e + 1] = kv4_pair<2>(od, s2[e], b2[e]); break;
-                default: f[2 * e] = kv4_pair<3>(ev, s2[e], b2[e]); f[2 * e + 1] = kv4_pair<3>(od, s2[e], b2[e]); break;
-              }
+              const Kv4Half &k = sv2[e];
+              f[2 * e] = i % 4 == 0 ? kv4_half_pair<0>(ev, k) : i % 4 == 1 ? kv4_half_pair<1>(ev, k)
+                         : i % 4 == 2 ? kv4_half_pair<2>(ev, k) : kv4_half_pair<3>(ev, k);
+              f[2 * e + 1] = i % 4 == 0 ? kv4_half_pair<0>(od, k) : i % 4 == 1 ? kv4_half_pair<1>(od, k)
+                             : i % 4 == 2 ? kv4_half_pair<2>(od, k) : kv4_half_pair<3>(od, k);
             }
 #pragma unroll
-            for (int b = 0; b < NB; ++b) mma16816(acc[b][i], f, pf[mb][b][0], pf[mb][b][1]);
+            for (int b = 0; b < NB; ++b) mma16816_half(acc[b][i], f, pf[mb][b][0], pf[mb][b][1]);
           }
         }
         __syncwarp();  // the stage may be filled again
-        at.next(first, a.n_seqs, a.units);
+        at.next(a, first);
       }
 #pragma unroll
       for (int b = 0; b < NB; ++b)
@@ -473,7 +507,7 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_decode_ker
           for (int e = 0; e < 2; ++e) {
             const int h = b * 8 + ti * 2 + e;
             if (h >= nh) continue;
-            const float inv = 1.f / l[b][e];  // scores of NaN or -inf alone: NaN
+            const float inv = KD_VALUE / l[b][e];  // scores of NaN or -inf alone: NaN
             uint32_t *dst = reinterpret_cast<uint32_t *>(a.o + (row0 + h) * D + gi * (D / 8));
 #pragma unroll
             for (int i = 0; i < STEPS; ++i) dst[i] = kd_pack2(acc[b][i][e] * inv, acc[b][i][e + 2] * inv);
@@ -506,34 +540,34 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_decode_ker
   }
 
   // ---------------------------------------------------------------- joins ---
-  // Pieces in order: each warp's first, then its last.  A chain of one item's pieces is begun
-  // by the first of the CTA and by every warp's last.
+  // Pieces in order: each warp's first, then its last; a lane for each.  A chain of one item's
+  // pieces begins where the piece before belongs to another.
   __syncthreads();
+  static_assert(2 * L::WARPS <= 32, "a lane for every piece");
   auto piece = [&](int s) {
     return reinterpret_cast<const float *>(smem + (s & 1 ? s / 2 * L::RING : L::OFF_PART + s / 2 * L::PART));
   };
+  KdMeta mine = {-1, 0, 0, 0};
+  if (lane < 2 * L::WARPS) mine = meta[lane];
+  const unsigned there = __ballot_sync(0xffffffffu, mine.seq >= 0);
+  const unsigned below = there & ((1u << lane) - 1u);
+  const int prev = below != 0 ? 31 - __clz(below) : lane;
+  const int prev_seq = __shfl_sync(0xffffffffu, mine.seq, prev), prev_unit = __shfl_sync(0xffffffffu, mine.unit, prev);
+  const bool joined = prev != lane && prev_seq == mine.seq && prev_unit == mine.unit;
+  unsigned starts = __ballot_sync(0xffffffffu, mine.seq >= 0 && !joined);
   int4 span = make_int4(-1, 0, 0, 0);
-  for (int c = 0; c < 2 * L::WARPS; ++c) {
-    const KdMeta head = meta[c];
-    if (head.seq < 0) continue;
-    // (a first piece joins the chain before it, if one reaches it)
-    if ((c & 1) == 0) {
-      bool joined = false;
-      for (int s = c - 1; s >= 0 && !joined; --s)
-        if (meta[s].seq >= 0) {
-          joined = meta[s].seq == head.seq && meta[s].unit == head.unit;
-          break;
-        }
-      if (joined) continue;
-    }
-    int last = c;
-    for (int s = c + 1; s < 2 * L::WARPS; ++s) {
-      if (meta[s].seq < 0) continue;
-      if (meta[s].seq != head.seq || meta[s].unit != head.unit) break;
-      last = s;
-    }
-    const int n_tiles = first[head.seq + 1] - first[head.seq];
-    const bool whole = head.j0 == 0 && meta[last].j1 == n_tiles;
+  while (starts != 0) {
+    const int c = __ffs(starts) - 1;
+    starts &= starts - 1;
+    const unsigned chain = there & (starts != 0 ? (1u << (__ffs(starts) - 1)) - 1u : 0xffffffffu) & ~((1u << c) - 1u);
+    const int last = 31 - __clz(chain);
+    KdMeta head;
+    head.seq = __shfl_sync(0xffffffffu, mine.seq, c);
+    head.unit = __shfl_sync(0xffffffffu, mine.unit, c);
+    head.j0 = __shfl_sync(0xffffffffu, mine.j0, c);
+    const int end = __shfl_sync(0xffffffffu, mine.j1, last);
+    const int n_tiles = a.direct ? n_run : first[head.seq + 1] - first[head.seq];
+    const bool whole = head.j0 == 0 && end == n_tiles;
     if (!whole && head.j0 == 0) {
       const long long item_end = (long long)first[head.seq] * a.units + (long long)(head.unit + 1) * n_tiles;
       span = make_int4(head.seq, head.unit, (int)((item_end - 1) / each), 0);
@@ -543,11 +577,9 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_decode_ker
     for (int u = threadIdx.x; u < nh * (D / 2); u += THREADS) {
       const int h = u / (D / 2), d = u % (D / 2) * 2;
       float mm = -FLT_MAX, ll = 0.f, x = 0.f, y = 0.f;
-      for (int s = c; s <= last; ++s)
-        if (meta[s].seq >= 0) mm = fmaxf(mm, piece(s)[8 * NB * D + h]);
-      for (int s = c; s <= last; ++s) {
-        if (meta[s].seq < 0) continue;
-        const float *p = piece(s);
+      for (unsigned left = chain; left != 0; left &= left - 1) mm = fmaxf(mm, piece(__ffs(left) - 1)[8 * NB * D + h]);
+      for (unsigned left = chain; left != 0; left &= left - 1) {
+        const float *p = piece(__ffs(left) - 1);
         const float f = ptx::ex2_approx(p[8 * NB * D + h] - mm);
         const float2 v = *reinterpret_cast<const float2 *>(p + h * D + d);
         ll = fmaf(f, p[8 * NB * (D + 1) + h], ll);
@@ -555,7 +587,7 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_decode_ker
         y = fmaf(f, v.y, y);
       }
       if (whole) {
-        const float inv = 1.f / ll;
+        const float inv = KD_VALUE / ll;
         *reinterpret_cast<uint32_t *>(a.o + ((size_t)head.seq * a.H + g * a.r + h_in + h) * D + d) =
             kd_pack2(x * inv, y * inv);
       } else {
@@ -594,7 +626,7 @@ __global__ void __launch_bounds__(D / 2) kv4_decode_join_kernel(const __grid_con
     x = fmaf(f, v.x, x);
     y = fmaf(f, v.y, y);
   }
-  const float inv = 1.f / l;
+  const float inv = KD_VALUE / l;
   *reinterpret_cast<uint32_t *>(a.o + ((size_t)span.x * a.H + g * a.r + h_in + h) * D + d) = kd_pack2(x * inv, y * inv);
 }
 

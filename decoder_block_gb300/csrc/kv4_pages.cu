@@ -239,8 +239,7 @@ __global__ void __launch_bounds__(KW_THREADS) kv4_read_kernel(T *k_out, T *v_out
     for (int i = 0; i < KR_UNITS; ++i) {
       if (dst[i] == nullptr) continue;
       if constexpr (sizeof(T) == 2) {
-        const uint32_t s2 = kv4_scale2(byte[i], byte[i]);
-        *reinterpret_cast<uint4 *>(dst[i]) = kv4_eight(w[i], s2, kv4_bias2(s2));
+        *reinterpret_cast<uint4 *>(dst[i]) = kv4_eight(w[i], kv4_scales(byte[i]));
       } else {
         const float s = kv4_scale(byte[i]);
         reinterpret_cast<float4 *>(dst[i])[0] = kv4_four(w[i], 0, s);

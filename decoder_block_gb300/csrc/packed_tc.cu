@@ -31,12 +31,14 @@
 //     into pieces; a piece leaves fp32 (O, m, l) per row in the workspace, and a
 //     third kernel joins them in piece order, so results do not depend on timing.
 // Pages held in 4 bits: the four loading warps copy a tile's codes and scales into shared
-// memory a stage ahead, and write the bf16 that they stand for where the copies above
-// would have put them; nothing else differs.
+// memory a stage ahead, and write the 16-bit numbers that they stand for where the copies
+// above would have put them: keys as bf16, as the queries are, and values as fp16 (half
+// of each, kv4.cuh), as the weights then are: an eighth of bf16's rounding.
 // Every wait is bounded (llama_op_set_wait_budget).  A CTA that gives up records
 // LLAMA_ERR_DEVICE_TIMEOUT and leaves once its copies, MMAs and tensor memory stores in
 // flight are done; the four loading warps each arm the bytes they are about to ask for.
 #include <cudaTypedefs.h>
+#include <cuda_fp16.h>
 #include <float.h>
 
 #include "kv4.cuh"
@@ -50,6 +52,10 @@ constexpr int PT_THREADS = 320;
 constexpr int PT_KEYS = 128;    // keys of a tile
 constexpr int PT_STAGES = 2;
 constexpr float PT_RESCALE = 8.0f;  // log2 units: the running maximum is raised when it grows by > 2^8
+// Weights over 4-bit pages are fp16: 2^7 times what they are, so that the largest, 2^15, has
+// room above, and what is less than 2^-31 of the running maximum's, not 2^-24, is lost.
+constexpr float PT_WEIGHT = 7.0f;
+constexpr float PT_VALUE = 2.0f;    // V's operand is then half of V
 constexpr int PT_MIN_PIECE = 4;     // key tiles that a split item's pieces may have, at least (9 make 3 + 3 + 3)
 constexpr int PT_SPLIT_COST = 4;    // what a split costs, in key tiles of time
 constexpr int PT_PLAN_THREADS = 1024;
@@ -137,6 +143,10 @@ struct PtArgs {
   long long wait_cycles;  // a wait's budget
 };
 
+__device__ __forceinline__ uint32_t pt_pack_half2(float a, float b) {
+  __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<uint32_t *>(&h);
+}
 __device__ __forceinline__ uint32_t pt_pack2(float a, float b) {
   __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<uint32_t *>(&h);
@@ -509,6 +519,7 @@ struct Unpacker {
       }
     }
   }
+  template <bool HALF>  // V: half of the values, as fp16
   __device__ __forceinline__ void unpack(const Raw &r, uint32_t tile) const {
 #pragma unroll
     for (int i = 0; i < ROUNDS; ++i) {
@@ -529,9 +540,10 @@ struct Unpacker {
       const int c0 = W == 128 ? col % 2 * 4 : col * 4;
 #pragma unroll
       for (int e = 0; e < CHUNK / 4; ++e) {
-        const uint32_t s2 = kv4_scale2(e < 2 ? s0 : s1, e < 2 ? s0 : s1);
         const int c = c0 + (turned ? e ^ 2 : e);
-        st_shared16(base + ((c ^ (row & 7)) << 4), kv4_eight(w[e], s2, kv4_bias2(s2)));
+        const uint32_t s = e < 2 ? s0 : s1;
+        st_shared16(base + ((c ^ (row & 7)) << 4),
+                    HALF ? kv4_half_eight(w[e], kv4_halves(s, s)) : kv4_eight(w[e], kv4_scales(s)));
       }
     }
   }
@@ -772,7 +784,8 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
     // --------------------------------------------------------------- MMA ---
     if (lane == 0) {
       constexpr uint32_t idesc_qk = ptx::idesc_bf16_f32(128, PT_KEYS, false);
-      constexpr uint32_t idesc_pv = ptx::idesc_bf16_f32(128, D, true);
+      constexpr uint32_t idesc_pv =
+          W > 0 ? ptx::idesc_f16_f32(128, D, true) : ptx::idesc_bf16_f32(128, D, true);
       const uint32_t q_lo = desc_lo(s0 + L::OFF_Q, 16), k_lo = desc_lo(s0 + L::OFF_K, 16);
       const uint32_t v_lo = desc_lo(s0 + L::OFF_V, L::ATOM);  // V: MN-major, 64-column blocks an atom apart
       auto issue_s = [&](int jj, int t, int buf) {
@@ -917,9 +930,9 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
             break;
           }
           if (f == n && warp == 10 && lane == 0) ptx::mbar_arrive(near_end);
-          u.unpack(raw[0], s0 + L::OFF_V + (jj % PT_STAGES) * L::TILE);
+          u.template unpack<true>(raw[0], s0 + L::OFF_V + (jj % PT_STAGES) * L::TILE);
         }
-        if (f < n) u.unpack(raw[1], s0 + L::OFF_K + ((jj + 1) % PT_STAGES) * L::TILE);
+        if (f < n) u.template unpack<false>(raw[1], s0 + L::OFF_K + ((jj + 1) % PT_STAGES) * L::TILE);
         ptx::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(f == 0 ? k_first : kv_full(jj % PT_STAGES));
@@ -1064,13 +1077,19 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
                   const uint32_t u = __float_as_uint(pv[e]);
-                  w[e] = pt_pack2(__uint_as_float(u << 16) * alpha, __uint_as_float(u & 0xffff0000u) * alpha);
+                  if constexpr (W > 0) {
+                    const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&u));
+                    w[e] = pt_pack_half2(x.x * alpha, x.y * alpha);
+                  } else {
+                    w[e] = pt_pack2(__uint_as_float(u << 16) * alpha, __uint_as_float(u & 0xffff0000u) * alpha);
+                  }
                 }
                 ptx::tmem_st16(s_col + pc, w);
               }
             }
           }
-          const uint64_t negm2 = ptx::f2pack(-m_run, -m_run);
+          const float less = (W > 0 ? PT_WEIGHT : 0.f) - m_run;
+          const uint64_t negm2 = ptx::f2pack(less, less);
           uint32_t pk[16];
           uint64_t lc = ptx::f2pack(0.f, 0.f);  // a second, independent add chain
 #pragma unroll
@@ -1082,8 +1101,8 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
               l2 = ptx::fadd2(l2, ptx::f2pack(p0, p1));
             else
               lc = ptx::fadd2(lc, ptx::f2pack(p0, p1));
-            // bf16 P: the tensor cores' operand; the row sum keeps the unrounded values
-            pk[e / 2] = pt_pack2(p0, p1);
+            // 16-bit P: the tensor cores' operand; the row sum keeps the unrounded values
+            pk[e / 2] = W > 0 ? pt_pack_half2(p0, p1) : pt_pack2(p0, p1);
           }
           l2 = ptx::fadd2(l2, lc);
           ptx::tmem_st16(s_col + c / 2, pk);
@@ -1126,7 +1145,7 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
       bf16 *dst = a.o + ((size_t)(it.first + rel) * a.H + it.h0 + hh) * a.D;
       if (it.slot < 0) {
         // a row that sees no key is zeros; one whose scores are all NaN or -inf is NaN (0 / 0)
-        const float inv = pos < 0 ? 0.f : 1.f / l;
+        const float inv = pos < 0 ? 0.f : (W > 0 ? PT_VALUE : 1.f) / l;
 #pragma unroll
         for (int c = 0; c < D; c += 16) {
           float ov[16];
@@ -1157,7 +1176,7 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
             for (int e = 0; e < 16; ++e) ov[e] = 0.f;
           }
 #pragma unroll
-          for (int e = 0; e < 16; ++e) mine[(c + e) * 32] = ov[e];
+          for (int e = 0; e < 16; ++e) mine[(c + e) * 32] = W > 0 ? PT_VALUE * ov[e] : ov[e];
         }
         mine[D * 32] = m_run;
         mine[(D + 1) * 32] = l;

@@ -585,6 +585,10 @@ __host__ __device__ constexpr uint32_t idesc_bf16_f32(int M, int N, bool b_mn_ma
          | ((uint32_t)(N >> 3) << 17)    // N / 8
          | ((uint32_t)(M >> 4) << 24);   // M / 16
 }
+// The same with fp16 A and B (format 0).
+__host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn_major = false) {
+  return idesc_bf16_f32(M, N, b_mn_major) & ~((1u << 7) | (1u << 10));
+}
 
 }  // namespace ptx
 }  // namespace llama

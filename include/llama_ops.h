@@ -283,8 +283,9 @@ llama_status llama_op_kv4_read_paged(int32_t dtype, const llama_paged_kv_cache *
                                      llama_stream stream);
 
 /* llama_op_attention_packed over 4-bit pages; dtype is that of q and o.  With
- * LLAMA_BF16 the products are those of a bf16 cache that holds the values the
- * pages stand for. */
+ * LLAMA_BF16 scores are those of a bf16 cache that holds the values the pages
+ * stand for, and each softmax weight is rounded to fp16 for its product with V (a
+ * weight below 2^-31 of its row's largest so far to 0), here and in the decode call. */
 size_t llama_op_attention_packed_kv4_workspace_bytes(int32_t dtype, const llama_packed_batch *batch, int32_t H,
                                                      int32_t G, int32_t D);
 llama_status llama_op_attention_packed_kv4(int32_t dtype, const void *q, const llama_paged_kv_cache *kv,

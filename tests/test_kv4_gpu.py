@@ -349,20 +349,27 @@ def test_results_repeat_bit_for_bit(lb):
             assert t.equal(run(lb, p, max_kv=1 << 16).o, first)
 
 
-@pytest.mark.parametrize("D,page", [(128, 16), (64, 64)])
-def test_packed_is_the_bf16_cache_of_the_same_values(lb, D, page):
-    """Prompts, continued prompts: the same products as over bf16 pages that hold the values."""
-    t = torch()
-    p = Kv4Problem(f"same{D}", "bf16", 8, 2, D, page, [300, 5, 64], [300, 1200, 100])
-    d = run_packed(lb, p)
-    k, v = (to_dev(store(x[:, 0], "bf16")) for x in (p.k, p.v))
-    o = t.full_like(d.o, 7.0)
-    kv = lb.make_paged_kv_cache(k, v, d.table)
-    need = lb.llama_op_attention_packed_workspace_bytes(d.code, d.batch, 8, 2, D)
-    ws = t.zeros(max(need, 16), dtype=t.uint8, device="cuda")
-    lb.check(lb.llama_op_attention_packed(d.code, d.q, kv, d.batch, o, 8, 2, D, ws, ws.numel(), None, t.cuda.current_stream()))
-    t.cuda.synchronize()
-    assert t.equal(o, d.o)
+@pytest.mark.parametrize("run", [run_packed, run_decode])
+@pytest.mark.parametrize("D", [128, 64, 16])
+def test_weights_are_rounded_to_fp16(lb, run, D):
+    """Closer than weights of 8 bits allow: with rounding errors of at most 2^-11 of each weight (and what fp32 adds, as
+    in _packed) instead of 2^-8, next to the rounding of the output.  Values of one sign and near one another, so that
+    nothing hides behind large ones."""
+    p = Kv4Problem(f"fp16{D}", "bf16", 4, 2, D, 32, [1] * 3, [900, 2500, 60])
+    ref, bound = p.attention()
+    got = to_f64(run(lb, p, max_kv=1 << 16).o)
+    o = np.abs(ref)
+    rel = (bound - 2.0 ** -8 * 1.01 * o) / 1.01  # of sum w |v|: the statistics' share and 2^-8
+    weights = np.zeros_like(ref)
+    r = p.H // p.G
+    for i, L in enumerate(p.kv_lens):
+        k, v = p.rows(i, p.k), p.rows(i, p.v)
+        for h in range(p.H):
+            s = synth.as_f64(p.q)[i, h] @ k[h // r].T / np.sqrt(D)
+            w = np.exp(s - s.max())
+            weights[i, h] = (w / w.sum()) @ np.abs(v[h // r])
+    tight = rel - weights * (2.0 ** -8 - 2.0 ** -11 - 3000 * 2.0 ** -32)
+    assert np.all(tight > 0) and np.all(np.abs(got - ref) <= tight * 1.01 + 2.0 ** -8 * 1.01 * o)
 
 
 def test_far_pages(lb):
