@@ -60,6 +60,13 @@ __device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
   return d;
 }
 
+// (x & mask) | set in one instruction (the compiler makes two of it, for it has room for one
+// constant in each).
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t mask, uint32_t set) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(d) : "r"(x), "r"(mask), "r"(set));
+  return d;
+}
 // A code n in the mantissa of 16.0 or 128.0 reads as 16 + n (bits 3 to 6 of a bf16) or 128 + n
 // (bits 0 to 3); times s and less 24 s or 136 s, in one rounding that has nothing to round,
 // it is (n - 8) s.  (24 s and 136 s are bf16 too: s is 8 to 15 times a power of two, and
@@ -86,8 +93,8 @@ __device__ __forceinline__ Kv4Scale kv4_scales(uint32_t byte) {
 // Codes in bits 4 j .. and 4 j + 16 .. of a word (elements 2 j and 2 j + 1 of its eight).
 template <int J>
 __device__ __forceinline__ uint32_t kv4_pair(uint32_t w, const Kv4Scale &k) {
-  if constexpr (J == 0) return bf16x2_fma((w & 0x000f000fu) | 0x43004300u, k.s, k.b136);
-  return bf16x2_fma(((w >> (J == 0 ? 0 : 4 * J - 3)) & 0x00780078u) | 0x41804180u, k.s, k.b24);
+  if constexpr (J == 0) return bf16x2_fma(and_or(w, 0x000f000fu, 0x43004300u), k.s, k.b136);
+  return bf16x2_fma(and_or(w >> (J == 0 ? 0 : 4 * J - 3), 0x00780078u, 0x41804180u), k.s, k.b24);
 }
 // Eight elements as bf16.
 __device__ __forceinline__ uint4 kv4_eight(uint32_t w, const Kv4Scale &k) {
@@ -111,7 +118,7 @@ template <int J>
 __device__ __forceinline__ uint32_t kv4_half_pair(uint32_t w, const Kv4Half &k) {
   const uint32_t at = J == 0 ? w << 6 : J == 1 ? w << 2 : J == 2 ? w >> 2 : w >> 6;
   uint32_t d;
-  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"((at & 0x03c003c0u) | 0x4c004c00u), "r"(k.s), "r"(k.b));
+  asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(and_or(at, 0x03c003c0u, 0x4c004c00u)), "r"(k.s), "r"(k.b));
   return d;
 }
 __device__ __forceinline__ uint4 kv4_half_eight(uint32_t w, const Kv4Half &k) {
