@@ -5,7 +5,7 @@
 //   o = sum_{j<=p} 2^(x_j - m) v_j / sum_{j<=p} 2^(x_j - m),  x_j = q.k_j log2(e) / sqrt(D),
 // in one pass over the keys with the running maximum m and sum in fp32.
 //
-// A work item is (sequence, KV head, block of 2 * Mq query positions, range of
+// A work item is (sequence, KV head, block of query positions, range of
 // 128-key tiles).  Its 128-row query tile t holds the rb heads of the group (all r, or
 // 128 of more) at Mq = 128 / rb positions, row i * rb + hh: one TMA box, so that every
 // K/V tile in shared memory serves the whole group.  Keys and values arrive page by
@@ -48,7 +48,6 @@
 namespace llama {
 namespace {
 
-constexpr int PT_THREADS = 320;
 constexpr int PT_KEYS = 128;    // keys of a tile
 constexpr int PT_STAGES = 2;
 constexpr float PT_RESCALE = 8.0f;  // log2 units: the running maximum is raised when it grows by > 2^8
@@ -61,12 +60,13 @@ constexpr int PT_SPLIT_COST = 4;    // what a split costs, in key tiles of time
 constexpr int PT_PLAN_THREADS = 1024;
 constexpr int PT_BUCKETS = 1024;    // item lengths the planner tells apart
 
-template <int D>
+// QT: query tiles of an item.
+template <int D, int QT>
 struct PtLayout {
   static constexpr int ATOM = 128 * 128;  // 128 rows x 64 columns
   static constexpr int TILE = (D / 64) * ATOM;
   static constexpr int OFF_Q = 0;
-  static constexpr int OFF_K = 2 * TILE;
+  static constexpr int OFF_K = QT * TILE;
   static constexpr int OFF_V = OFF_K + PT_STAGES * TILE;
   static constexpr int OFF_ITEM = OFF_V + PT_STAGES * TILE;  // PtItem
   static constexpr int OFF_BAR = OFF_ITEM + 64;
@@ -85,16 +85,20 @@ struct PtLayout {
   static constexpr uint32_t O_COL = S_BUFS * 128;
 };
 
-// Shared memory of a kernel; W: head width of 4-bit pages (0: bf16 pages).  Codes and scales
-// on their way come behind everything else: FILLS stages of [4 warps][V, K][32 rows].
-template <int D, int W>
+// Shared memory of a kernel; W: head width of 4-bit pages (0: bf16 pages), which WARPS warps
+// unpack.  Codes and scales on their way come behind everything else: FILLS stages of
+// [WARPS][V, K][128 / WARPS rows].
+template <int D, int W, int QT>
 struct PtShared {
-  static constexpr int FILLS = D == 128 ? 1 : 3;
-  static constexpr int ROWS = 32 * kv4_code_bytes(W), SCALES = 32 * kv4_scale_bytes(W);  // of a warp, K or V
+  using L = PtLayout<D, QT>;
+  static constexpr int WARPS = QT == 1 ? 8 : 4;
+  static constexpr int FILLS = D == 128 && QT == 2 ? 1 : 3;
+  static constexpr int WARP_ROWS = PT_KEYS / WARPS;
+  static constexpr int ROWS = WARP_ROWS * kv4_code_bytes(W), SCALES = WARP_ROWS * kv4_scale_bytes(W);  // K or V
   static constexpr int WARP = 2 * (ROWS + SCALES);
-  static constexpr int OFF_CODES = (PtLayout<D>::BYTES_MIN - 1024 + 15) / 16 * 16;
-  static constexpr int END = 1024 + OFF_CODES + FILLS * 4 * WARP;
-  static constexpr int BYTES = W == 0 ? PtLayout<D>::BYTES : END > PtLayout<D>::BYTES ? END : PtLayout<D>::BYTES;
+  static constexpr int OFF_CODES = (L::BYTES_MIN - 1024 + 15) / 16 * 16;
+  static constexpr int END = 1024 + OFF_CODES + FILLS * WARPS * WARP;
+  static constexpr int BYTES = W == 0 ? L::BYTES : END > L::BYTES ? END : L::BYTES;
   static_assert(BYTES <= 227 * 1024, "fits an SM");
 };
 
@@ -133,11 +137,11 @@ struct PtArgs {
   PackedView b;
   int H, G, D, r;        // D: the heads' width (the kernel's or less); r: heads of a group
   int rb, subs;          // heads of a work item (at most 128), items of a group
-  int Mq, box;           // query positions of a tile; rows of a page's TMA box
+  int Mq, Bq, box;       // query positions of a tile and of an item; rows of a page's TMA box
   float scale_log2;
   PtPlan *plan;          // null: direct
   PtEntry *entries;
-  float *part;           // [slot][unit][2 tiles][4 warps][D + 2][32 rows]
+  float *part;           // [slot][unit][tiles][4 warps][D + 2][32 rows]
   const uint8_t *kc, *vc;  // pools of 4-bit blocks
   int *status;
   long long wait_cycles;  // a wait's budget
@@ -202,7 +206,7 @@ __device__ __forceinline__ int item_end(const PtItem &it, int Mq, int t) {
 // keeps those of its first blocks, so a batch of up to 4096 blocks is looked up once.
 constexpr int PT_KEEP = 4;
 
-__global__ void __launch_bounds__(PT_PLAN_THREADS) packed_plan_kernel(PagedView pv, PackedView b, int units, int Mq,
+__global__ void __launch_bounds__(PT_PLAN_THREADS) packed_plan_kernel(PagedView pv, PackedView b, int units, int Bq,
                                                                       int sms, int max_blocks, int max_entries,
                                                                       PtPlan *plan, PtEntry *entries, PtSplit *splits,
                                                                       int *status) {
@@ -229,7 +233,7 @@ __global__ void __launch_bounds__(PT_PLAN_THREADS) packed_plan_kernel(PagedView 
     if (i < b.n_seqs) {
       check_seq(b, pv, i, status);
       const SeqSpan s = seq_span(b, pv, i);
-      n = (s.count + 2 * Mq - 1) / (2 * Mq);
+      n = (s.count + Bq - 1) / Bq;
       if (i0 == 0) seqs[tid] = s;
     }
     const int end = add_counts(base, cta_scan(n, warp_sums));
@@ -253,7 +257,7 @@ __global__ void __launch_bounds__(PT_PLAN_THREADS) packed_plan_kernel(PagedView 
     seq = lo;
     blk = u - first_blk[lo];
     const SeqSpan s = span_of(lo);
-    return tiles_of(s.kv_len - s.count, blk * 2 * Mq, min(s.count, (blk + 1) * 2 * Mq));
+    return tiles_of(s.kv_len - s.count, blk * Bq, min(s.count, (blk + 1) * Bq));
   };
   int seq[PT_KEEP], blk[PT_KEEP], len[PT_KEEP];
   unsigned long long mine = 0;
@@ -309,7 +313,7 @@ __global__ void __launch_bounds__(PT_PLAN_THREADS) packed_plan_kernel(PagedView 
     int slot = -1;
     if (p > 1) {
       slot = atomicAdd(&n_slots, p);
-      splits[atomicAdd(&n_split, 1)] = PtSplit{x * 2 * Mq, slot, p, span.first, span.count, span.kv_len, {0, 0}};
+      splits[atomicAdd(&n_split, 1)] = PtSplit{x * Bq, slot, p, span.first, span.count, span.kv_len, {0, 0}};
     }
     const int at = atomicAdd(&hist[bucket(n, p)], p);
     for (int i = 0; i < p; ++i) {
@@ -340,7 +344,7 @@ __global__ void __launch_bounds__(PT_PLAN_THREADS) packed_plan_kernel(PagedView 
 // the WARPS warps' lanes share the stage's 16 boxes of V and 16 of K at most.
 template <int D, int WARPS>
 struct StageLoads {
-  using L = PtLayout<D>;
+  using L = PtLayout<D, 2>;
   static constexpr int ATOMS = D / 64, MINE = 32 / WARPS;
   const PtArgs &a;
   const CUtensorMap *map;
@@ -429,7 +433,7 @@ __device__ __forceinline__ void st_shared16(uint32_t at, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
 }
 
-// One warp's part of the stages over 4-bit pages: rows 32 warp .. + 31 of every tile, V and K
+// One warp's part of the stages over 4-bit pages: its 16 or 32 rows of every tile, V and K
 // apart.  An item of n key tiles has fills 0 to n: fill f brings V of its tile f - 1 and K of
 // its tile f (the first and last lack one), as the stages do.
 //   request(f)  copies codes and scales to shared memory; a lane's 16 bytes of codes are
@@ -439,14 +443,16 @@ __device__ __forceinline__ void st_shared16(uint32_t at, uint4 v) {
 //               eight lanes of a store meet in no bank.
 // Rows behind the sequence's last key may hold any codes: those are finite numbers, and their
 // weights are 0.
-template <int D, int W>
+template <int D, int W, int QT>
 struct Unpacker {
-  using L = PtLayout<D>;
-  using S = PtShared<D, W>;
-  static constexpr int RB = kv4_code_bytes(W), SB = kv4_scale_bytes(W);
+  using L = PtLayout<D, QT>;
+  using S = PtShared<D, W, QT>;
+  static constexpr int RB = kv4_code_bytes(W), SB = kv4_scale_bytes(W), WR = S::WARP_ROWS;
   static constexpr int CHUNK = RB < 16 ? RB : 16;           // bytes of codes that a lane moves at a time
-  static constexpr int ROUNDS = RB * 32 / (CHUNK * 32);     // of 32 lanes, for 32 rows
   static constexpr int PER_ROW = RB / CHUNK;                // lanes of a row
+  static constexpr int LANES = WR * PER_ROW < 32 ? WR * PER_ROW : 32;
+  static constexpr int ROUNDS = WR * PER_ROW / LANES;
+  static constexpr int HALVES = WR / 16;                    // of 16 rows, which no page splits
   const PtArgs &a;
   uint32_t smem;
   int warp, lane;
@@ -455,13 +461,13 @@ struct Unpacker {
   __device__ __forceinline__ Unpacker(const PtArgs &args, uint32_t s0, int w)
       : a(args), smem(s0), warp(w), lane(threadIdx.x & 31) {}
   __device__ __forceinline__ uint32_t staged(int n, int which) const {
-    return smem + S::OFF_CODES + (uint32_t)((n % S::FILLS) * 4 + warp) * S::WARP + which * (S::ROWS + S::SCALES);
+    return smem + S::OFF_CODES + (uint32_t)((n % S::FILLS) * S::WARPS + warp) * S::WARP + which * (S::ROWS + S::SCALES);
   }
   // Pages of fill f.
   __device__ __forceinline__ void look_up(const PtItem &it, int f) {
-    const int j = it.j0 + f - 1 + lane / 2, p = j * PT_KEYS + warp * 32 + (lane & 1) * 16;
+    const int j = it.j0 + f - 1 + lane / 2, p = j * PT_KEYS + warp * WR + (lane & 1) * 16;
     page = -2;
-    if (lane < 4 && j >= it.j0 && j < it.j1 && p < it.kv_len) {
+    if (lane < 4 && (lane & 1) < HALVES && j >= it.j0 && j < it.j1 && p < it.kv_len) {
       page = a.pv.page(it.seq, p >> a.pv.page_log2);
       if (page < 0) report_status(a.status, LLAMA_ERR_RANGE);
     }
@@ -473,13 +479,13 @@ struct Unpacker {
     const int rows = 1 << a.pv.page_log2;
 #pragma unroll
     for (int which = 0; which < 2; ++which) {
-      const int p0 = (it.j0 + f - 1 + which) * PT_KEYS + warp * 32;
+      const int p0 = (it.j0 + f - 1 + which) * PT_KEYS + warp * WR;
       const uint8_t *pool = which ? a.kc : a.vc;
       const uint32_t dst = staged(n, which);
 #pragma unroll
       for (int i = 0; i < ROUNDS; ++i) {
-        const int row = (i * 32 + lane) / PER_ROW, at = (i * 32 + lane) % PER_ROW * CHUNK;
-        const int pg = row < 16 ? pages[2 * which] : pages[2 * which + 1];
+        const int row = (i * LANES + lane) / PER_ROW, at = (i * LANES + lane) % PER_ROW * CHUNK;
+        const int pg = LANES < 32 && lane >= LANES ? -2 : row < 16 ? pages[2 * which] : pages[2 * which + 1];
         const uint32_t to = dst + row * RB + at;
         if (pg >= 0) {
           const uint8_t *from = kv4_row(pool, a.pv, pg, it.g, W, (p0 + row) & (rows - 1)).codes + at;
@@ -492,7 +498,7 @@ struct Unpacker {
         }
       }
       const int l = lane - 16 * which;  // V's scales: lanes 0 .., K's: lanes 16 ..
-      if (l >= 0 && l < 2 * SB) {
+      if (l >= 0 && l < S::SCALES / 16) {
         const int row = l * 16 / SB, pg = row < 16 ? pages[2 * which] : pages[2 * which + 1];
         if (pg >= 0)
           copy16(dst + S::ROWS + l * 16, kv4_row(pool, a.pv, pg, it.g, W, (p0 + row) & (rows - 1)).scales);
@@ -508,7 +514,7 @@ struct Unpacker {
     const uint32_t from = staged(n, which);
 #pragma unroll
     for (int i = 0; i < ROUNDS; ++i) {
-      const int row = (i * 32 + lane) / PER_ROW, col = (i * 32 + lane) % PER_ROW;
+      const int row = (i * LANES + lane % LANES) / PER_ROW, col = (i * LANES + lane % LANES) % PER_ROW;
       if constexpr (CHUNK == 16) {
         r.codes[i] = ld_shared16(from + row * RB + col * 16);
         r.scales[i] = ld_shared_u16(from + S::ROWS + row * SB + col * 2);
@@ -521,9 +527,10 @@ struct Unpacker {
   }
   template <bool HALF>  // V: half of the values, as fp16
   __device__ __forceinline__ void unpack(const Raw &r, uint32_t tile) const {
+    if (LANES < 32 && lane >= LANES) return;
 #pragma unroll
     for (int i = 0; i < ROUNDS; ++i) {
-      const int row = warp * 32 + (i * 32 + lane) / PER_ROW, col = (i * 32 + lane) % PER_ROW;
+      const int row = warp * WR + (i * LANES + lane) / PER_ROW, col = (i * LANES + lane) % PER_ROW;
       const bool turned = W == 128 && col >= 2;
       uint32_t w[4] = {r.codes[i].x, r.codes[i].y, r.codes[i].z, r.codes[i].w};
       uint32_t s0 = r.scales[i] & 255u, s1 = r.scales[i] >> 8;
@@ -538,26 +545,34 @@ struct Unpacker {
       }
       const uint32_t base = tile + (W == 128 ? col / 2 * L::ATOM : 0) + row * 128;
       const int c0 = W == 128 ? col % 2 * 4 : col * 4;
+      Kv4Scale ks[2];
+      Kv4Half hs[2];
+      if (HALF) {
+        hs[0] = kv4_halves(s0, s0);
+        hs[1] = kv4_halves(s1, s1);
+      } else {
+        ks[0] = kv4_scales(s0);
+        ks[1] = kv4_scales(s1);
+      }
 #pragma unroll
       for (int e = 0; e < CHUNK / 4; ++e) {
         const int c = c0 + (turned ? e ^ 2 : e);
-        const uint32_t s = e < 2 ? s0 : s1;
-        st_shared16(base + ((c ^ (row & 7)) << 4),
-                    HALF ? kv4_half_eight(w[e], kv4_halves(s, s)) : kv4_eight(w[e], kv4_scales(s)));
+        st_shared16(base + ((c ^ (row & 7)) << 4), HALF ? kv4_half_eight(w[e], hs[e / 2]) : kv4_eight(w[e], ks[e / 2]));
       }
     }
   }
 };
 
 // ------------------------------------------------------------- attention ---
-// ISSUERS: warps from PT_THREADS on that load the stages (0: warp 0 does).  W: head width of
-// 4-bit pages, which the issuers unpack (0: bf16 pages).
-template <int D, int ISSUERS, int W>
-__global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
+// ISSUERS: warps behind the softmax that load the stages (0: warp 0 does).  W: head width of
+// 4-bit pages, which the issuers unpack (0: bf16 pages).  QT: query tiles of an item.
+template <int D, int ISSUERS, int W, int QT>
+__global__ void __launch_bounds__(64 + QT * 128 + ISSUERS * 32, 1)
     packed_tc_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ PtArgs a) {
-  using L = PtLayout<D>;
+  using L = PtLayout<D, QT>;
   constexpr int ATOMS = D / 64;
+  constexpr int SOFT = 4 * QT, FIRST_ISSUER = 2 + SOFT;  // softmax warps from 2 on, issuers behind them
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::OFF_BAR);
@@ -581,7 +596,7 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
   // with issuers: an item has been handed over; their loads have come to its last tile
   const uint32_t i_full = bar0 + 8u * (11 + 2 * PT_STAGES), near_end = i_full + 8;
   const uint32_t k_first = i_full + 16;  // 4-bit pages: an item's first K is unpacked
-  static_assert(W == 0 || ISSUERS == 4, "four warps unpack");
+  static_assert(W == 0 ? QT == 2 : ISSUERS == PtShared<D, W, QT>::WARPS, "as laid out");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   auto wait = [&](uint32_t bar, uint32_t parity) -> bool {
@@ -594,7 +609,7 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
   if (threadIdx.x == 0) {
     ptx::mbar_init(q_full, 1);
     // the MMAs reading Q are done; each softmax and issuing warp has read the item
-    ptx::mbar_init(q_empty, 9 + ISSUERS);
+    ptx::mbar_init(q_empty, 1 + SOFT + ISSUERS);
     ptx::mbar_init(i_full, 1);
     ptx::mbar_init(near_end, 1);
     ptx::mbar_init(k_first, ISSUERS > 0 ? ISSUERS : 1);
@@ -613,18 +628,18 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
     ptx::fence_mbar_init();
   }
   // Query rows behind rb * Mq are never loaded: zero them.
-  if (warp >= 2 && warp < 10 && a.rb * a.Mq < 128) {
+  if (warp >= 2 && warp < FIRST_ISSUER && a.rb * a.Mq < 128) {
     const int first = a.rb * a.Mq;
-    for (int t = 0; t < 2; ++t)
+    for (int t = 0; t < QT; ++t)
       for (int at = 0; at < ATOMS; ++at) {
         uint4 *p = reinterpret_cast<uint4 *>(smem + L::OFF_Q + t * L::TILE + at * L::ATOM + first * 128);
-        for (int i = threadIdx.x - 64; i < (128 - first) * 8; i += PT_THREADS - 64) p[i] = make_uint4(0, 0, 0, 0);
+        for (int i = threadIdx.x - 64; i < (128 - first) * 8; i += SOFT * 32) p[i] = make_uint4(0, 0, 0, 0);
       }
     ptx::fence_proxy_async_smem();
   }
-  if (W > 0 && W < 64 && warp >= 2 && warp < 10) {  // columns of K and V behind the heads' width
+  if (W > 0 && W < 64 && warp >= 2 && warp < FIRST_ISSUER) {  // columns of K and V behind the heads' width
     uint4 *p = reinterpret_cast<uint4 *>(smem + L::OFF_K);
-    for (int i = threadIdx.x - 64; i < 2 * PT_STAGES * L::TILE / 16; i += PT_THREADS - 64) p[i] = make_uint4(0, 0, 0, 0);
+    for (int i = threadIdx.x - 64; i < 2 * PT_STAGES * L::TILE / 16; i += SOFT * 32) p[i] = make_uint4(0, 0, 0, 0);
     ptx::fence_proxy_async_smem();
   }
   if (warp == 1) {
@@ -665,7 +680,7 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
         if (u >= n_items) return it;
         it.seq = x.x;
         it.unit = u % units;
-        it.q0 = x.y * 2 * a.Mq;
+        it.q0 = x.y * a.Bq;
         it.j0 = x.z & 0xffff;
         it.j1 = (unsigned)x.z >> 16;
         it.slot = x.w;
@@ -678,7 +693,7 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
         int base = 0;
         for (int i0 = 0; i0 < a.b.n_seqs; i0 += 32) {
           const int i = i0 + lane;
-          const int n = i < a.b.n_seqs ? (seq_span(a.b, a.pv, i).count + 2 * a.Mq - 1) / (2 * a.Mq) : 0;
+          const int n = i < a.b.n_seqs ? (seq_span(a.b, a.pv, i).count + a.Bq - 1) / a.Bq : 0;
           int end = n;
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1) {
@@ -690,7 +705,7 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
           if (m != 0) {
             const int src = __ffs(m) - 1;
             it.seq = i0 + src;
-            it.q0 = __shfl_sync(0xffffffffu, mine, src) * 2 * a.Mq;
+            it.q0 = __shfl_sync(0xffffffffu, mine, src) * a.Bq;
             break;
           }
           base += __shfl_sync(0xffffffffu, end, 31);
@@ -709,7 +724,7 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
         it.count = s.count;
         it.kv_len = s.kv_len;
         it.j0 = 0;
-        it.j1 = tiles_of(s.kv_len - s.count, it.q0, min(s.count, it.q0 + 2 * a.Mq));
+        it.j1 = tiles_of(s.kv_len - s.count, it.q0, min(s.count, it.q0 + a.Bq));
       }
       return it;
     };
@@ -733,7 +748,7 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
         ended = true;
         break;
       }
-      const int n_t = it.q0 + a.Mq < it.count ? 2 : 1;  // query tiles that hold rows
+      const int n_t = QT == 2 && it.q0 + a.Mq < it.count ? 2 : 1;  // query tiles that hold rows
       if (lane == 0) {
         ptx::mbar_arrive_expect_tx(q_full, n_t * ATOMS * a.rb * a.Mq * 128u + (W == 0 ? loads.bytes(it, it.j0) : 0u));
         for (int t = 0; t < n_t; ++t)
@@ -837,7 +852,7 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
         if (!wait(q_full, k & 1)) break;
         const PtItem it = *item_slot;
         if (it.seq < 0) break;
-        const int e0 = item_end(it, a.Mq, 0), e1 = item_end(it, a.Mq, 1);
+        const int e0 = item_end(it, a.Mq, 0), e1 = QT == 2 ? item_end(it, a.Mq, 1) : 0;
         const int n = it.j1 - it.j0;
         if (n <= 0) {  // no row of the block sees a key
           ptx::mbar_arrive(q_empty);
@@ -878,7 +893,7 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
         };
         // This thread paces the kernel, so the tiles that both query tiles see, and whose
         // successors they see too, go without the questions of the last ones.
-        const int plain = min(min(e0, e1) - 1 - it.j0, n - 1);
+        const int plain = QT == 2 ? min(min(e0, e1) - 1 - it.j0, n - 1) : 0;
         int i = 0;
         for (; ok && i < plain; ++i) ok = step(i, true, true, true, true);
         for (; ok && i < n; ++i) {
@@ -890,10 +905,10 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
       ptx::mma_commit(fin);
       ptx::mbar_drain(fin, 0, nullptr, 0);
     }
-  } else if (W > 0 && warp >= 10) {
+  } else if (W > 0 && warp >= FIRST_ISSUER) {
     // ---------------------------------------------------------- unpackers ---
-    using S = PtShared<D, W == 0 ? 64 : W>;
-    Unpacker<D, W == 0 ? 64 : W> u(a, s0, warp - 10);
+    using S = PtShared<D, W == 0 ? 64 : W, QT>;
+    Unpacker<D, W == 0 ? 64 : W, QT> u(a, s0, warp - FIRST_ISSUER);
     typename decltype(u)::Raw raw[2];
     int tiles = 0, fills = 0;  // key tiles of earlier items, fills taken so far
     bool ok = true;
@@ -905,7 +920,7 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
       if (it.seq < 0) break;
       const int n = it.j1 - it.j0;
       if (n <= 0) {
-        if (warp == 10 && lane == 0) ptx::mbar_arrive(near_end);
+        if (warp == FIRST_ISSUER && lane == 0) ptx::mbar_arrive(near_end);
         continue;
       }
       // one group of copies per fill, of a fill that is not there an empty one
@@ -929,7 +944,7 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
             ok = false;
             break;
           }
-          if (f == n && warp == 10 && lane == 0) ptx::mbar_arrive(near_end);
+          if (f == n && warp == FIRST_ISSUER && lane == 0) ptx::mbar_arrive(near_end);
           u.template unpack<true>(raw[0], s0 + L::OFF_V + (jj % PT_STAGES) * L::TILE);
         }
         if (f < n) u.template unpack<false>(raw[1], s0 + L::OFF_K + ((jj + 1) % PT_STAGES) * L::TILE);
@@ -941,9 +956,9 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
       fills += S::FILLS - 1;  // those behind the item's last were empty
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
-  } else if (ISSUERS > 0 && warp >= 10) {
+  } else if (ISSUERS > 0 && warp >= FIRST_ISSUER) {
     // ------------------------------------------------------------ issuers ---
-    StageLoads<D, ISSUERS == 0 ? 1 : ISSUERS> loads(a, &tmK, &tmV, s0, warp - 10);
+    StageLoads<D, ISSUERS == 0 ? 1 : ISSUERS> loads(a, &tmK, &tmV, s0, warp - FIRST_ISSUER);
     int tiles = 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
@@ -952,7 +967,7 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(q_empty);
       if (it.seq < 0) break;
-      if (it.j0 >= it.j1 && warp == 10 && lane == 0) ptx::mbar_arrive(near_end);
+      if (it.j0 >= it.j1 && warp == FIRST_ISSUER && lane == 0) ptx::mbar_arrive(near_end);
       loads.begin(it);
       for (int j = it.j0; j < it.j1; ++j, ++tiles) {
         const int page = loads.advance(it, j);
@@ -960,12 +975,12 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
           ok = false;
           break;
         }
-        if (j + 1 == it.j1 && warp == 10 && lane == 0) ptx::mbar_arrive(near_end);
+        if (j + 1 == it.j1 && warp == FIRST_ISSUER && lane == 0) ptx::mbar_arrive(near_end);
         loads.issue(it, j, tiles, page, kv_full(tiles % PT_STAGES));
       }
     }
     __syncwarp();
-    ptx::settle_loads<ISSUERS == 0 ? 1 : ISSUERS, PT_STAGES>(tiles, warp - 10, s_loaded, kv_full);
+    ptx::settle_loads<ISSUERS == 0 ? 1 : ISSUERS, PT_STAGES>(tiles, warp - FIRST_ISSUER, s_loaded, kv_full);
   } else {
     // ----------------------------------------------------------- softmax ---
     const int t = (warp - 2) / 4;
@@ -976,7 +991,7 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
     const uint32_t o_col = lane_base + L::O_COL + t * D;
     const uint64_t scale2 = ptx::f2pack(a.scale_log2, a.scale_log2);
     if (a.plan == nullptr && blockIdx.x == 0)
-      for (int u = threadIdx.x - 64; u < a.b.n_seqs; u += PT_THREADS - 64) check_seq(a.b, a.pv, u, a.status);
+      for (int u = threadIdx.x - 64; u < a.b.n_seqs; u += SOFT * 32) check_seq(a.b, a.pv, u, a.status);
     bool ok = true;
     int jg = 0, jt = 0;  // key tiles of earlier items: of the ring, of this query tile
     int done = 0;        // o_done phases: of every tile (three S buffers), of every item (two)
@@ -988,7 +1003,7 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
       if (lane == 0) ptx::mbar_arrive(q_empty);
       if (it.seq < 0) break;
       const int shift = it.kv_len - it.count;
-      const int e0 = item_end(it, a.Mq, 0), e1 = item_end(it, a.Mq, 1);
+      const int e0 = item_end(it, a.Mq, 0), e1 = QT == 2 ? item_end(it, a.Mq, 1) : 0;
       const int my_end = t == 0 ? e0 : e1;
       const int n_kv = max(0, my_end - it.j0);
       const int rel = it.q0 + t * a.Mq + i;
@@ -1165,7 +1180,7 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
         }
       } else if (__any_sync(0xffffffffu, valid)) {
         // a piece: the partial (O, m, l) of these 32 rows, one column after another
-        float *mine = a.part + ((((size_t)it.slot * (a.G * a.subs) + it.unit) * 2 + t) * 4 + qq) * ((D + 2) * 32) + lane;
+        float *mine = a.part + ((((size_t)it.slot * (a.G * a.subs) + it.unit) * QT + t) * 4 + qq) * ((D + 2) * 32) + lane;
 #pragma unroll
         for (int c = 0; c < D; c += 16) {
           float ov[16];
@@ -1204,23 +1219,23 @@ __global__ void __launch_bounds__(PT_THREADS + ISSUERS * 32, 1)
 constexpr int JOIN_COLS = 8;
 constexpr int JOIN_CTAS = 4;
 
-template <int D>
+template <int D, int QT>
 __global__ void __launch_bounds__(D / JOIN_COLS * 32) packed_join_kernel(const __grid_constant__ PtArgs a,
                                                                          const PtSplit *splits) {
   grid_dependency_wait();
   const int units = a.G * a.subs;
   const int n_split = *reinterpret_cast<volatile int *>(&a.plan->n_split);
   const int lane = threadIdx.x & 31, c0 = threadIdx.x / 32 * JOIN_COLS;
-  for (int w = blockIdx.x; w < n_split * units * 8; w += gridDim.x) {
-    const int qq = w % 4, t = w / 4 % 2, unit = w / 8 % units;
-    const PtSplit s = splits[w / 8 / units];
+  for (int w = blockIdx.x; w < n_split * units * 4 * QT; w += gridDim.x) {
+    const int qq = w % 4, t = w / 4 % QT, unit = w / (4 * QT) % units;
+    const PtSplit s = splits[w / (4 * QT) / units];
     const int row = qq * 32 + lane, hh = row % a.rb, i = row / a.rb;
     const int rel = s.q0 + t * a.Mq + i;
     const int g = unit / a.subs, h = g * a.r + unit % a.subs * a.rb + hh;
     const bool valid = i < a.Mq && rel < s.count && h < (g + 1) * a.r;
     if (!__any_sync(0xffffffffu, valid)) continue;  // nothing was written
-    const float *p = a.part + ((((size_t)s.slot * units + unit) * 2 + t) * 4 + qq) * ((D + 2) * 32) + lane;
-    const size_t step = (size_t)units * 8 * (D + 2) * 32;
+    const float *p = a.part + ((((size_t)s.slot * units + unit) * QT + t) * 4 + qq) * ((D + 2) * 32) + lane;
+    const size_t step = (size_t)units * 4 * QT * (D + 2) * 32;
     float m = -FLT_MAX;
 #pragma unroll 8
     for (int x = 0; x < s.n; ++x) m = fmaxf(m, p[x * step + D * 32]);
@@ -1286,21 +1301,23 @@ namespace {
 
 // Sizes of one call: items, and the workspace they need (0 bytes: direct).
 struct PtSizes {
-  int rb = 0, subs = 0, units = 0, Mq = 0;
+  int rb = 0, subs = 0, units = 0, Mq = 0, Bq = 0;
   long long max_blocks = 0;  // (sequence, block) pairs, at most
   int max_split = 0, max_slots = 0;
   long long max_entries = 0;
   size_t off_entries = 0, off_splits = 0, off_part = 0, bytes = 0;
 };
 
-PtSizes packed_sizes(const PackedView &b, int H, int G, int D, int sms) {
+// tiles_of_item: query tiles of an item.
+PtSizes packed_sizes(const PackedView &b, int H, int G, int D, int sms, int tiles_of_item) {
   PtSizes z;
   const int r = H / G;
   z.rb = r < 128 ? r : 128;
   z.subs = (r + z.rb - 1) / z.rb;
   z.units = G * z.subs;
   z.Mq = 128 / z.rb;
-  z.max_blocks = (long long)b.n_tokens / (2 * z.Mq) + (b.n_seqs < b.n_tokens ? b.n_seqs : b.n_tokens);
+  z.Bq = tiles_of_item * z.Mq;
+  z.max_blocks = (long long)b.n_tokens / z.Bq + (b.n_seqs < b.n_tokens ? b.n_seqs : b.n_tokens);
   // Direct: no more than one item per SM, and so few key tiles that the planned form, which
   // costs about 8 us more to start and join, cannot win them back by splitting items for
   // the idle SMs (planned / direct: 8B-shaped, 512 tokens behind 600 29 / 21 us, 1100
@@ -1316,27 +1333,27 @@ PtSizes packed_sizes(const PackedView &b, int H, int G, int D, int sms) {
   z.off_splits = z.off_entries + (size_t)z.max_entries * sizeof(PtEntry);
   z.off_part = z.off_splits + (size_t)z.max_split * sizeof(PtSplit);
   z.off_part = (z.off_part + 127) / 128 * 128;
-  z.bytes = z.off_part + (size_t)z.max_slots * z.units * 8 * (D + 2) * 32 * sizeof(float);
+  z.bytes = z.off_part + (size_t)z.max_slots * z.units * 4 * tiles_of_item * (D + 2) * 32 * sizeof(float);
   return z;
 }
 
 // k, v: bf16 pages, or with W > 0 pages held in 4 bits, of heads of width W.
-template <int D, int W>
+template <int D, int W, int QT>
 cudaError_t launch_tc(const bf16 *q, const void *k, const void *v, bf16 *o, const PagedView &pv, const PackedView &b,
                       int H, int G, int width, void *workspace, int *status, cudaStream_t st) {
-  constexpr int BYTES = PtShared<D, W>::BYTES;
+  constexpr int BYTES = PtShared<D, W, QT>::BYTES, ISSUERS = W > 0 ? PtShared<D, W, QT>::WARPS : 4;
   static PerContextOnce attr;
   cudaError_t e = attr.run([] {
     if constexpr (W == 0) {
       const cudaError_t e =
-          cudaFuncSetAttribute(packed_tc_kernel<D, 0, 0>, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES);
+          cudaFuncSetAttribute(packed_tc_kernel<D, 0, 0, 2>, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES);
       if (e != cudaSuccess) return e;
     }
-    return cudaFuncSetAttribute(packed_tc_kernel<D, 4, W>, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES);
+    return cudaFuncSetAttribute(packed_tc_kernel<D, ISSUERS, W, QT>, cudaFuncAttributeMaxDynamicSharedMemorySize, BYTES);
   });
   if (e != cudaSuccess) return e;
   const int sms = sm_count();
-  const PtSizes z = packed_sizes(b, H, G, D, sms);
+  const PtSizes z = packed_sizes(b, H, G, D, sms, QT);
   PtArgs a;
   a.o = o;
   a.pv = pv;
@@ -1348,6 +1365,7 @@ cudaError_t launch_tc(const bf16 *q, const void *k, const void *v, bf16 *o, cons
   a.rb = z.rb;
   a.subs = z.subs;
   a.Mq = z.Mq;
+  a.Bq = z.Bq;
   a.box = 1 << (pv.page_log2 < 7 ? pv.page_log2 : 7);
   a.scale_log2 = 1.4426950408889634f / sqrtf((float)width);
   a.plan = nullptr;
@@ -1365,11 +1383,11 @@ cudaError_t launch_tc(const bf16 *q, const void *k, const void *v, bf16 *o, cons
              !make_paged_map(&mv, (const bf16 *)v, pv, G, width, a.box)) {
     return cudaErrorInvalidValue;
   }
-  auto kernel = packed_tc_kernel<D, 4, W>;
+  auto kernel = packed_tc_kernel<D, ISSUERS, W, QT>;
   if constexpr (W == 0) {
-    if (a.box != 16) kernel = packed_tc_kernel<D, 0, 0>;
+    if (a.box != 16) kernel = packed_tc_kernel<D, 0, 0, 2>;
   }
-  const dim3 threads(PT_THREADS + (W > 0 || a.box == 16 ? 128 : 0));
+  const dim3 threads(64 + QT * 128 + (W > 0 || a.box == 16 ? ISSUERS * 32 : 0));
   if (z.bytes == 0) {
     count_launch();
     return launch_pdl(kernel, dim3((unsigned)(z.max_blocks * z.units)), threads, BYTES, st, mq,
@@ -1381,7 +1399,7 @@ cudaError_t launch_tc(const bf16 *q, const void *k, const void *v, bf16 *o, cons
   PtSplit *splits = reinterpret_cast<PtSplit *>(w + z.off_splits);
   a.part = reinterpret_cast<float *>(w + z.off_part);
   count_launch();
-  e = launch_pdl(packed_plan_kernel, dim3(1), dim3(PT_PLAN_THREADS), 0, st, pv, b, z.units, a.Mq, sms,
+  e = launch_pdl(packed_plan_kernel, dim3(1), dim3(PT_PLAN_THREADS), 0, st, pv, b, z.units, a.Bq, sms,
                  (int)z.max_blocks, (int)z.max_entries, a.plan, a.entries, splits, status);
   if (e != cudaSuccess) return e;
   const long long items = z.max_entries * z.units;
@@ -1390,32 +1408,50 @@ cudaError_t launch_tc(const bf16 *q, const void *k, const void *v, bf16 *o, cons
                  mk, mv, a);
   if (e != cudaSuccess || z.max_split == 0) return e;
   count_launch();
-  const long long joins = (long long)z.max_split * z.units * 8, ctas = (long long)JOIN_CTAS * sms;
-  return launch_pdl(packed_join_kernel<D>, dim3((unsigned)(joins < ctas ? joins : ctas)), dim3(D / JOIN_COLS * 32), 0,
+  const long long joins = (long long)z.max_split * z.units * 4 * QT, ctas = (long long)JOIN_CTAS * sms;
+  return launch_pdl(packed_join_kernel<D, QT>, dim3((unsigned)(joins < ctas ? joins : ctas)), dim3(D / JOIN_COLS * 32), 0,
                     st, a, (const PtSplit *)splits);
 }
 
 }  // namespace
 
 size_t packed_tc_workspace_bytes(const PackedView &b, int H, int G, int D) {
-  return packed_sizes(b, H, G, D < 64 ? 64 : D, sm_count()).bytes;
+  return packed_sizes(b, H, G, D < 64 ? 64 : D, sm_count(), 2).bytes;
 }
 
 cudaError_t launch_packed_tc(const bf16 *q, const bf16 *k, const bf16 *v, bf16 *o, const PagedView &pv,
                              const PackedView &b, int H, int G, int D, void *workspace, int *status, cudaStream_t st) {
-  if (D == 128) return launch_tc<128, 0>(q, k, v, o, pv, b, H, G, D, workspace, status, st);
-  return launch_tc<64, 0>(q, k, v, o, pv, b, H, G, D, workspace, status, st);
+  if (D == 128) return launch_tc<128, 0, 2>(q, k, v, o, pv, b, H, G, D, workspace, status, st);
+  return launch_tc<64, 0, 2>(q, k, v, o, pv, b, H, G, D, workspace, status, st);
+}
+
+namespace {
+// Query tiles of an item over 4-bit pages: one where the sequences' rows are few on average
+// (drafts, single tokens): eight warps then unpack, with more tiles on their way.
+int kv4_tiles(const PackedView &b, int H, int G) {
+  return (long long)b.n_tokens * (H / G) <= 128LL * b.n_seqs ? 1 : 2;
+}
+template <int QT>
+cudaError_t launch_kv4(const bf16 *q, const uint8_t *k, const uint8_t *v, bf16 *o, const PagedView &pv,
+                       const PackedView &b, int H, int G, int D, void *workspace, int *status, cudaStream_t st) {
+  switch (D) {
+    case 16: return launch_tc<64, 16, QT>(q, k, v, o, pv, b, H, G, D, workspace, status, st);
+    case 32: return launch_tc<64, 32, QT>(q, k, v, o, pv, b, H, G, D, workspace, status, st);
+    case 64: return launch_tc<64, 64, QT>(q, k, v, o, pv, b, H, G, D, workspace, status, st);
+    case 128: return launch_tc<128, 128, QT>(q, k, v, o, pv, b, H, G, D, workspace, status, st);
+  }
+  return cudaErrorInvalidValue;
+}
+}  // namespace
+
+size_t packed_kv4_workspace_bytes(const PackedView &b, int H, int G, int D) {
+  return packed_sizes(b, H, G, D < 64 ? 64 : D, sm_count(), kv4_tiles(b, H, G)).bytes;
 }
 
 cudaError_t launch_packed_kv4(const bf16 *q, const uint8_t *k, const uint8_t *v, bf16 *o, const PagedView &pv,
                               const PackedView &b, int H, int G, int D, void *workspace, int *status, cudaStream_t st) {
-  switch (D) {
-    case 16: return launch_tc<64, 16>(q, k, v, o, pv, b, H, G, D, workspace, status, st);
-    case 32: return launch_tc<64, 32>(q, k, v, o, pv, b, H, G, D, workspace, status, st);
-    case 64: return launch_tc<64, 64>(q, k, v, o, pv, b, H, G, D, workspace, status, st);
-    case 128: return launch_tc<128, 128>(q, k, v, o, pv, b, H, G, D, workspace, status, st);
-  }
-  return cudaErrorInvalidValue;
+  return kv4_tiles(b, H, G) == 1 ? launch_kv4<1>(q, k, v, o, pv, b, H, G, D, workspace, status, st)
+                                 : launch_kv4<2>(q, k, v, o, pv, b, H, G, D, workspace, status, st);
 }
 
 }  // namespace llama

@@ -91,7 +91,8 @@ size_t packed_tc_workspace_bytes(const PackedView &b, int H, int G, int D);
 cudaError_t launch_packed_tc(const bf16 *q, const bf16 *k, const bf16 *v, bf16 *o, const PagedView &pv,
                              const PackedView &b, int H, int G, int D, void *workspace, int *status, cudaStream_t st);
 
-// The same over pages held in 4 bits (page_stride in bytes); the workspace is the same too.
+// The same over pages held in 4 bits (page_stride in bytes).
+size_t packed_kv4_workspace_bytes(const PackedView &b, int H, int G, int D);
 cudaError_t launch_packed_kv4(const bf16 *q, const uint8_t *k, const uint8_t *v, bf16 *o, const PagedView &pv,
                               const PackedView &b, int H, int G, int D, void *workspace, int *status, cudaStream_t st);
 

@@ -283,7 +283,11 @@ llama_status llama_op_attention_packed(int32_t dtype, const void *q, const llama
 
 size_t llama_op_attention_packed_kv4_workspace_bytes(int32_t dtype, const llama_packed_batch *batch, int32_t H,
                                                      int32_t G, int32_t D) {
-  return llama_op_attention_packed_workspace_bytes(dtype, batch, H, G, D);
+  const size_t need = llama_op_attention_packed_workspace_bytes(dtype, batch, H, G, D);
+  if (dtype != LLAMA_BF16 || batch == nullptr || check_heads(H, G, D) != LLAMA_OK ||
+      check_batch(batch, H) != LLAMA_OK || batch->n_seqs == 0 || batch->n_tokens == 0)
+    return need;
+  return packed_kv4_workspace_bytes(view_of(batch), H, G, D);
 }
 
 llama_status llama_op_attention_packed_kv4(int32_t dtype, const void *q, const llama_paged_kv_cache *kv,
