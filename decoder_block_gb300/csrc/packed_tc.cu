@@ -75,9 +75,9 @@ struct PtLayout {
   static constexpr int NBAR = 3 + 2 * PT_STAGES + 8 + 3;
   // S buffers of 128 columns in tensor memory, then O of both query tiles.  With D = 64
   // there is room for a third: a query tile's next S is ready when its softmax is done
-  // with this one (S = 8192, 32 heads: 306 us for 324).  With D = 128 the next S goes where
-  // this one's P was.
-  static constexpr int S_BUFS = D == 64 ? 3 : 2;
+  // with this one (S = 8192, 32 heads: 306 us for 324).  With D = 128 and two query tiles the
+  // next S goes where this one's P was.
+  static constexpr int S_BUFS = D == 64 || QT == 1 ? 3 : 2;
   static constexpr int BYTES_MIN = 1024 + OFF_BAR + NBAR * 8 + 16;
   // one CTA per SM: two would need all of tensor memory each
   static constexpr int BYTES = BYTES_MIN > 116 * 1024 ? BYTES_MIN : 116 * 1024;
