@@ -1,31 +1,35 @@
-// One new token per sequence over cache pages held in 4 bits, q and o bf16 ("Full Llama 3
-// transformer block", How it works: cached keys 0 .. kv_len - 1; "The Evolving Transformer
-// 04 · LLaMA", §05 GQA).
-//   o = sum_j 2^(x_j - m) v_j / sum_j 2^(x_j - m),  x_j = q.k_j log2(e) / sqrt(D),
+// Attention of few query rows a sequence over cache pages held in 4 bits, q and o bf16: one
+// new token of each sequence, or the last confirmed one and its drafts ("Full Llama 3
+// transformer block", How it works: keys j <= position; "The Evolving Transformer 04 ·
+// LLaMA", §05 GQA).  For token t at position p
+//   o = sum_{j<=p} 2^(x_j - m) v_j / sum_{j<=p} 2^(x_j - m),  x_j = q.k_j log2(e) / sqrt(D),
 // in one pass over the keys, the running maximum m and the sum in fp32.
 //
 // The cache is read once, and a byte of it is nearly two elements: what has to be kept small
-// is the work per element.  A warp takes 32 keys at a time for the 8 (or 16) heads of an
-// item, codes go from shared memory into registers and from there straight into the
-// operands of mma.sync, keys and columns of the values on its 16-row side:
-//   S^T[16 keys x 8 heads] = K Q^T,     O^T[16 columns x 8 heads] += V^T P^T.
+// is the work per element.  A warp takes 32 keys at a time for 8, 16 or 24 rows (head of the
+// group, token) of a sequence; codes go from shared memory into registers and from there
+// straight into the operands of mma.sync, keys and columns of the values on its 16-row side:
+//   S^T[16 keys x 8 rows] = K Q^T,     O^T[16 columns x 8 rows] += V^T P^T.
 // The order of d within K and Q, and of the columns in V and O, is free: it is the one that
-// leaves every thread whole words of codes.  Two codes become two bf16 with a shift, a
-// masked or and an fma (kv4.cuh); V's products run over keys, so the words of two keys are
-// interleaved first, half a word at a time.  P^T comes from S^T by movmatrix.  (tcgen05 takes
-// its operands from shared memory: the bf16 written there and read back are four times the
-// codes, more than the SM's shared memory moves in the time that the codes take to come.)
+// leaves every thread whole words of codes.  Two codes become two 16-bit numbers with a
+// shift, a masked or and an fma (kv4.cuh): K bf16 as Q is, V fp16, and P^T, which comes from
+// S^T by movmatrix, fp16 too.  V's products run over keys, so the words of two keys are
+// interleaved first, half a word at a time.  (tcgen05 takes its operands from shared memory:
+// the 16-bit numbers written there and read back are four times the codes, and its 128 rows
+// are mostly padding here: 64 sequences of 5 rows on 8 KV heads 104 us with it.)
 // Each warp copies its own tiles into its own shared memory, a few tiles ahead, and waits
 // for nothing but those copies.
 //
-// All tiles of the call in one row -- sequence by sequence, head block by head block -- are
-// dealt out to the CTAs, and a CTA's to its warps, in even runs.  A run that begins or ends
-// inside an item leaves its (O, m, l); the CTA joins those of its warps, in order, and
-// what begins or ends inside the CTA's run goes to the workspace, where a second kernel
-// joins it, in order.  With short sequences (direct) a CTA takes one item instead, and there
-// is no second kernel.
+// All tiles of the call in one row -- sequence by sequence, block of rows by block of rows --
+// are dealt out to the CTAs, and a CTA's to its warps, in even runs.  A run that begins or
+// ends inside an item leaves its (O, m, l); the CTA joins those of its warps, in order,
+// and what begins or ends inside the CTA's run goes to the workspace, where a second kernel
+// joins it, in order.  With short sequences (direct: one token each) a CTA takes one item
+// instead, and there is no second kernel.
 #include <cuda_fp16.h>
 #include <float.h>
+
+#include <type_traits>
 
 #include "kv4.cuh"
 #include "paged_kernels.h"
@@ -43,8 +47,9 @@ constexpr float KD_WEIGHT = 7.0f;
 constexpr float KD_VALUE = 2.0f;  // V's operand is half of V
 // Key tiles of a CTA's item in the direct form, at most.
 constexpr int KD_DIRECT_TILES = 64;
+constexpr int KD_MAX_NB = 3;
 
-// NB: blocks of 8 heads of an item.
+// NB: blocks of 8 rows of an item.
 template <int D, int NB>
 struct KdLayout {
   static constexpr int WARPS = NB == 1 ? 16 : 8;
@@ -57,20 +62,22 @@ struct KdLayout {
   static constexpr int OFF_PART = WARPS * RING;   // of each warp, its first
   static constexpr int OFF_META = OFF_PART + WARPS * PART;
   static constexpr int OFF_SUMS = OFF_META + WARPS * 2 * 16;
-  static constexpr int OFF_FIRST = OFF_SUMS + 128;  // tiles before sequence i
+  // tiles before sequence i: of one item with a row each, else of its items for one KV head
+  static constexpr int OFF_FIRST = OFF_SUMS + 128;
   static int bytes(int n_seqs) { return OFF_FIRST + (n_seqs + 1) * 4; }
 };
 static_assert(KdLayout<128, 1>::OFF_FIRST + (LLAMA_PACKED_MAX_SEQS + 1) * 4 <= 227 * 1024, "fits an SM");
-static_assert(KdLayout<128, 2>::OFF_FIRST + (LLAMA_PACKED_MAX_SEQS + 1) * 4 <= 227 * 1024, "fits an SM");
+static_assert(KdLayout<128, 3>::OFF_FIRST + (LLAMA_PACKED_MAX_SEQS + 1) * 4 <= 227 * 1024, "fits an SM");
 
 struct KdArgs {
   const bf16 *q;
   const uint8_t *k, *v;
   bf16 *o;
   PagedView pv;
-  const int *kv_lens;
-  int n_seqs, max_kv_len;
-  int H, G, r, subs, units;  // r: heads of a group; subs: head blocks of a group; units = G * subs
+  PackedView b;  // q_offsets null: one row of q and o per sequence
+  int H, G, r;   // r: heads of a group
+  int times;     // items of a sequence for each of the tiles that `first` counts
+  int most;      // tiles that `first` may count: offsets that descend make sequences overlap
   int direct;
   float scale_log2;
   float *part;  // [CTA][2][8 NB][D + 2]
@@ -114,7 +121,6 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void *src) {
   else
     asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
-// N words (or, N = 0, one that is not whole) from shared memory.
 template <int N>
 __device__ __forceinline__ void ld_words(uint32_t at, uint32_t (&w)[N]) {
   if constexpr (N == 4)
@@ -130,45 +136,56 @@ __device__ __forceinline__ uint32_t ld_byte(uint32_t at) {
   return v;
 }
 
-// A place in the row of tiles.
+// The rows and keys of a sequence as its items have them; no rows where they are out of range.
+__device__ __forceinline__ SeqSpan kd_span(const KdArgs &a, int i) {
+  if (a.b.q_offsets != nullptr) return seq_span(a.b, a.pv, i);
+  return SeqSpan{i, 1, checked_len(ld_after_wait(a.b.kv_lens + i), a.b.max_kv_len, a.pv)};
+}
+__device__ __forceinline__ int kd_tiles(int keys) { return (keys + KD_KEYS - 1) / KD_KEYS; }
+
+// A place in the row of tiles.  A unit is a KV head and a block of 8 NB rows.
+template <int NB>
 struct KdCursor {
-  int seq, unit, g, j, n, len;  // n: tiles of the sequence, len: its keys
+  int seq, unit, units, g, sub, j, n;  // units, n: of the sequence, n its key tiles
+  SeqSpan s;
+  __device__ __forceinline__ void set(const KdArgs &a, int i, int u, int at) {
+    seq = i;
+    s = kd_span(a, i);
+    n = kd_tiles(s.kv_len);
+    const int subs = (s.count * a.r + 8 * NB - 1) / (8 * NB);
+    units = a.G * subs;
+    unit = u;
+    g = u / subs;
+    sub = u - g * subs;
+    j = at;
+  }
   __device__ __forceinline__ void seek(const KdArgs &a, const int *first, long long at) {
-    int lo = 0, hi = a.n_seqs;  // the last sequence that begins at or before it
+    int lo = 0, hi = a.b.n_seqs;  // the last sequence that begins at or before it
     while (hi - lo > 1) {
       const int mid = (lo + hi) / 2;
-      if ((long long)first[mid] * a.units <= at) lo = mid;
+      if ((long long)first[mid] * a.times <= at) lo = mid;
       else hi = mid;
     }
-    n = first[lo + 1] - first[lo];
-    const long long rest = at - (long long)first[lo] * a.units;
-    set(a, lo, (int)(rest / n), (int)(rest % n), n);
+    set(a, lo, 0, 0);
+    const long long rest = at - (long long)first[lo] * a.times;
+    set(a, lo, (int)(rest / n), (int)(rest % n));
   }
-  __device__ __forceinline__ void set(const KdArgs &a, int s, int u, int at, int tiles) {
-    seq = s;
-    unit = u;
-    g = u / a.subs;
-    j = at;
-    n = tiles;
-    len = ld_after_wait(a.kv_lens + s);
-  }
-  __device__ __forceinline__ void next(const KdArgs &a, const int *first) {
-    if (++j < n || a.direct) return;
-    int s = seq, u = unit + 1;
-    if (u == a.units) {
+  __device__ __forceinline__ bool next(const KdArgs &a, const int *first) {  // true: it is another item's
+    if (++j < n || a.direct) return false;
+    int i = seq, u = unit + 1;
+    if (u == units) {
       u = 0;
-      for (++s; s < a.n_seqs; ++s) {
-        n = first[s + 1] - first[s];
-        if (n > 0) break;
+      for (++i; i < a.b.n_seqs && first[i + 1] == first[i]; ++i) {
       }
-      if (s == a.n_seqs) return;  // the end of the row
+      if (i == a.b.n_seqs) return false;  // the end of the row
     }
-    set(a, s, u, 0, n);
+    set(a, i, u, 0);
+    return true;
   }
 };
 
 template <int D, int NB>
-__global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_decode_kernel(const __grid_constant__ KdArgs a) {
+__global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_rows_kernel(const __grid_constant__ KdArgs a) {
   using L = KdLayout<D, NB>;
   constexpr int THREADS = L::WARPS * 32;
   constexpr int KW = D / 32 > 0 ? D / 32 : 1;  // words of a key's codes that a thread takes (of 8 elements)
@@ -180,165 +197,202 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_decode_ker
   int *first = reinterpret_cast<int *>(smem + L::OFF_FIRST);
   int *sums = reinterpret_cast<int *>(smem + L::OFF_SUMS);
   KdMeta *meta = reinterpret_cast<KdMeta *>(smem + L::OFF_META);
+  const uint32_t ring = s0 + warp * L::RING;
   allow_dependents_launch();
+  if (lane < 2) meta[warp * 2 + lane].seq = -1;
   grid_dependency_wait();
 
   // ------------------------------------------------------------- lengths ---
-  if (lane < 2) meta[warp * 2 + lane].seq = -1;
-  auto no_keys = [&](int i, int from, int step) {  // sequence i: zeros
-    uint4 *dst = reinterpret_cast<uint4 *>(a.o + (size_t)i * a.H * D);
-    for (int e = from; e < a.H * D / 8; e += step) dst[e] = make_uint4(0, 0, 0, 0);
-  };
-  KdCursor at = {0, 0, 0, 0, 0, 0};
+  KdCursor<NB> at;
   long long begin = 0, each = 1;
   int n_run;  // tiles of this CTA's run
   if (a.direct) {
-    const int seq = blockIdx.x / a.units, unit = blockIdx.x % a.units;
-    const int raw = ld_after_wait(a.kv_lens + seq), len = checked_len(raw, a.max_kv_len, a.pv);
-    if (raw != len && unit == 0 && threadIdx.x == 0) report_status(a.status, LLAMA_ERR_RANGE);
-    n_run = (len + KD_KEYS - 1) / KD_KEYS;
-    if (n_run == 0) {
-      if (unit == 0) no_keys(seq, threadIdx.x, THREADS);
+    const int units = a.G * ((a.r + 8 * NB - 1) / (8 * NB));
+    const int seq = blockIdx.x / units, unit = blockIdx.x % units;
+    at.set(a, seq, unit, 0);
+    n_run = at.n;
+    if (unit == 0 && threadIdx.x == 0 && ld_after_wait(a.b.kv_lens + seq) != at.s.kv_len)
+      report_status(a.status, LLAMA_ERR_RANGE);
+    if (n_run == 0) {  // no keys: zeros
+      uint4 *dst = reinterpret_cast<uint4 *>(a.o + (size_t)seq * a.H * D);
+      if (unit == 0)
+        for (int e = threadIdx.x; e < a.H * D / 8; e += THREADS) dst[e] = make_uint4(0, 0, 0, 0);
       return;
     }
-    at.set(a, seq, unit, 0, n_run);
   } else {
     // (4096 sequences: 8 or 16 each)
-    const int per = (a.n_seqs + THREADS - 1) / THREADS;
+    const int per = (a.b.n_seqs + THREADS - 1) / THREADS;
+    auto add = [&](int x, int y) { return (int)min((unsigned)x + (unsigned)y, (unsigned)a.most); };
     int mine = 0;
+    bool blind = false;  // rows before their sequence's first key
     for (int k = 0; k < per; ++k) {
       const int i = threadIdx.x * per + k;
-      if (i >= a.n_seqs) break;
-      const int raw = ld_after_wait(a.kv_lens + i), len = checked_len(raw, a.max_kv_len, a.pv);
-      if (raw != len && blockIdx.x == 0) report_status(a.status, LLAMA_ERR_RANGE);
-      const int n = (len + KD_KEYS - 1) / KD_KEYS;
+      if (i >= a.b.n_seqs) break;
+      const SeqSpan s = kd_span(a, i);
+      if (blockIdx.x == 0) {
+        if (a.b.q_offsets != nullptr) check_seq(a.b, a.pv, i, a.status);
+        else if (ld_after_wait(a.b.kv_lens + i) != s.kv_len) report_status(a.status, LLAMA_ERR_RANGE);
+      }
+      int n = kd_tiles(s.kv_len);
+      if (a.b.q_offsets != nullptr) n = min((long long)n * ((s.count * a.r + 8 * NB - 1) / (8 * NB)), (long long)a.most);
+      blind |= s.kv_len < s.count;
       first[i] = n;
-      mine += n;
-      if (n == 0 && i % (int)gridDim.x == (int)blockIdx.x) no_keys(i, 0, 1);
+      mine = add(mine, n);
     }
     int end = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int x = __shfl_up_sync(0xffffffffu, end, o);
-      if (lane >= o) end += x;
+      if (lane >= o) end = add(end, x);
     }
     if (lane == 31) sums[warp] = end;
     __syncthreads();
-    int before = end - mine;
-    for (int w = 0; w < warp; ++w) before += sums[w];
+    int before = __shfl_up_sync(0xffffffffu, end, 1);  // (not end - mine: the sums may be cut off)
+    if (lane == 0) before = 0;
+    for (int w = 0; w < warp; ++w) before = add(before, sums[w]);
     for (int k = 0; k < per; ++k) {
       const int i = threadIdx.x * per + k;
-      if (i >= a.n_seqs) break;
+      if (i >= a.b.n_seqs) break;
       const int n = first[i];
       first[i] = before;
-      before += n;
+      before = add(before, n);
     }
-    if (threadIdx.x == THREADS - 1) first[a.n_seqs] = before;
-    __syncthreads();
-    const long long total = (long long)first[a.n_seqs] * a.units;
+    if (threadIdx.x == THREADS - 1) first[a.b.n_seqs] = before;
+    if (__syncthreads_or(blind))  // those rows are zeros
+      for (int i = 0; i < a.b.n_seqs; ++i) {
+        const SeqSpan s = kd_span(a, i);
+        const long long n = (long long)max(0, s.count - s.kv_len) * (a.H * D / 8);
+        uint4 *dst = reinterpret_cast<uint4 *>(a.o + (size_t)s.first * a.H * D);
+        for (long long e = (long long)blockIdx.x * THREADS + threadIdx.x; e < n; e += (long long)gridDim.x * THREADS)
+          dst[e] = make_uint4(0, 0, 0, 0);
+      }
+    const long long total = (long long)first[a.b.n_seqs] * a.times;
     each = (total + gridDim.x - 1) / gridDim.x;
     each = each > L::WARPS ? each : L::WARPS;
     begin = min(total, each * blockIdx.x);
     n_run = (int)(min(total, begin + each) - begin);
   }
   const int w0 = (int)((long long)n_run * warp / L::WARPS), w1 = (int)((long long)n_run * (warp + 1) / L::WARPS);
-  const uint32_t ring = s0 + warp * L::RING;
+  const int todo = w1 - w0;
 
-  // -------------------------------------------------------------- copies ---
-  // Lanes 0 to 7 look up where a tile's rows lie: bit 0 says which 16 rows, bit 1 K or V, bit
-  // 2 codes or scales.  A half behind the last key is given the first half's rows, which may
-  // be read; its scores are replaced.
-  KdCursor ahead = at;  // the tile whose pages are known and that is copied next
-  int left = w1 - w0, id = 0, slot = 0;
-  const int rows_mask = (1 << a.pv.page_log2) - 1;
-  const uint8_t *const pool = lane & 2 ? a.v : a.k;
-  const int row_bytes = lane & 4 ? L::SB : L::RB, to_scales = lane & 4 ? L::RB << a.pv.page_log2 : 0;
-  const int block = kv4_block_bytes(1 << a.pv.page_log2, D);
-  auto look_up = [&] {
-    if (left > 0 && lane < 8) {
-      int p = ahead.j * KD_KEYS + (lane & 1) * 16;
-      p = p < ahead.len ? p : ahead.j * KD_KEYS;
-      slot = p & rows_mask;
-      id = ld_after_wait(a.pv.table + (size_t)ahead.seq * a.pv.table_stride + (p >> a.pv.page_log2));
-    }
-  };
-  auto request = [&](int n) {
-    if (left > 0) {
-      const uint32_t stage = ring + n % L::STAGES * L::STAGE;
-      constexpr int CHUNK = L::RB < 16 ? L::RB : 16, PER_ROW = L::RB / CHUNK;
-      const bool bad = lane < 8 && (unsigned)id >= (unsigned)a.pv.n_pages;
-      const unsigned bads = __ballot_sync(0xffffffffu, bad);
-      const uint8_t *ptr = pool;
-      if (!bad) ptr += id * a.pv.page_stride + (ahead.g * block + to_scales + slot * row_bytes);
-      auto rows_at = [&](int from) {
-        return reinterpret_cast<const uint8_t *>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(ptr), from));
-      };
-      auto copies = [&](bool all_good) {
-#pragma unroll
-        for (int which = 0; which < 2; ++which)
-#pragma unroll
-          for (int i = 0; i < PER_ROW; ++i) {
-            const int byte = (i * 32 + lane) * CHUNK, half = D >= 64 ? i * 32 / PER_ROW / 16 : lane / 16;
-            const uint32_t to = stage + which * L::HALF + byte;
-            const uint8_t *from = rows_at(which * 2 + half) + (byte - half * 16 * L::RB);
-            if (all_good || !(bads >> (which * 2 + half) & 1)) {
-              copy_async<CHUNK>(to, from);
-            } else {  // a page of zeros
-              asm volatile("st.shared.v2.u32 [%0], {%1, %1};" ::"r"(to), "r"(0x88888888u) : "memory");
-              if (CHUNK == 16)
-                asm volatile("st.shared.v2.u32 [%0], {%1, %1};" ::"r"(to + 8), "r"(0x88888888u) : "memory");
-            }
-          }
-        // scales: K's by lanes 0 .., V's by lanes 16 ..
-        const int which = lane / 16, l = lane % 16, half = l / L::SB & 1, src = 4 + which * 2 + half;
-        const uint8_t *from = rows_at(src) + l % L::SB * 16;
-        if (l < 2 * L::SB && (all_good || !(bads >> src & 1)))
-          copy_async<16>(stage + which * L::HALF + KD_KEYS * L::RB + l * 16, from);
-      };
-      if (bads == 0) {
-        copies(true);
-      } else {
-        if (lane == 0) report_status(a.status, LLAMA_ERR_RANGE);
-        copies(false);
-      }
-      ahead.next(a, first);
-      --left;
-    }
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  };
-
-  if (left > 0) {
+  if (todo > 0) {
     if (a.direct) at.j = w0;
     else at.seek(a, first, begin + w0);
-    ahead = at;
+    // ------------------------------------------------------------ copies ---
+    // A tile's rows are two runs of 16, which no page splits; a run behind the last key is given
+    // the first one's rows, which may be read, and its scores are replaced.  Every lane knows
+    // the page ids and adds to pointers of its own (by bulk copies, whose operands have to be
+    // made uniform, a tile took 893 instructions for the 838 of lanes asking one another).
+    KdCursor<NB> ahead = at;  // the tile whose pages are known and that is copied next
+    int left = todo, fill = 0, id0 = 0, id1 = 0;
+    const int rows_mask = (1 << a.pv.page_log2) - 1;
+    const bool narrow = a.pv.page_log2 == 4;
+    const uint32_t stride = (uint32_t)a.pv.page_stride;
+    constexpr int CHUNK = L::RB < 16 ? L::RB : 16;   // bytes of a lane's copy
+    constexpr int COPIES = D >= 64 ? L::RB / 32 : 1;  // of 32 lanes for a run; D < 64: for both runs
+    const int s_lane = lane % 16, s_half = s_lane / L::SB & 1;  // scales: K's by lanes 0 .., V's by lanes 16 ..
+    const uint8_t *from_k, *from_v, *from_s;
+    auto aim = [&] {  // this lane's bytes of page 0
+      const int block = kv4_block_bytes(1 << a.pv.page_log2, D) * ahead.g;
+      const int off = D >= 64 ? lane * 16 : lane % 16 * CHUNK;
+      from_k = a.k + block + off;
+      from_v = a.v + block + off;
+      from_s = (lane < 16 ? a.k : a.v) + block + (L::RB << a.pv.page_log2) + s_lane % L::SB * 16;
+    };
+    auto look_up = [&] {
+      if (left <= 0) return;
+      const int p = ahead.j * KD_KEYS;
+      const int *table = a.pv.table + (size_t)ahead.seq * a.pv.table_stride + (p >> a.pv.page_log2);
+      id0 = id1 = ld_after_wait(table);
+      if (narrow && p + 16 < ahead.s.kv_len) id1 = ld_after_wait(table + 1);
+    };
+    auto request = [&] {
+      if (left > 0) {
+        const uint32_t stage = ring + fill * L::STAGE;
+        const int slot0 = ahead.j * KD_KEYS & rows_mask, slot1 = narrow ? 0 : slot0 + 16;
+        const bool bad0 = (unsigned)id0 >= (unsigned)a.pv.n_pages, bad1 = (unsigned)id1 >= (unsigned)a.pv.n_pages;
+        auto copies = [&](auto checked) {
+          constexpr bool CHECKED = decltype(checked)::value;  // a page may be out of range: one of zeros
+          auto run = [&](const uint8_t *from, uint32_t to, int h) {
+            const uint8_t *p = from + (uint64_t)(uint32_t)(h ? id1 : id0) * stride + (h ? slot1 : slot0) * L::RB;
+#pragma unroll
+            for (int i = 0; i < COPIES; ++i) {
+              if (CHECKED && (h ? bad1 : bad0)) {
+                asm volatile("st.shared.v2.u32 [%0], {%1, %1};" ::"r"(to + i * 512), "r"(0x88888888u) : "memory");
+                if (CHUNK == 16)
+                  asm volatile("st.shared.v2.u32 [%0], {%1, %1};" ::"r"(to + i * 512 + 8), "r"(0x88888888u) : "memory");
+              } else {
+                copy_async<CHUNK>(to + i * 512, p + i * 512);
+              }
+            }
+          };
+#pragma unroll
+          for (int which = 0; which < 2; ++which) {
+            const uint32_t to = stage + which * L::HALF + lane * CHUNK;
+            if constexpr (D >= 64) {
+              run(which ? from_v : from_k, to, 0);
+              run(which ? from_v : from_k, to + 16 * L::RB, 1);
+            } else {
+              run(which ? from_v : from_k, to, lane / 16);
+            }
+          }
+          if (s_lane < 2 * L::SB && !(CHECKED && (s_half ? bad1 : bad0)))
+            copy_async<16>(stage + (lane < 16 ? 0 : L::HALF) + KD_KEYS * L::RB + s_lane * 16,
+                           from_s + (uint64_t)(uint32_t)(s_half ? id1 : id0) * stride + (s_half ? slot1 : slot0) * L::SB);
+        };
+        if (!bad0 && !bad1) {
+          copies(std::false_type());
+        } else {
+          if (lane == 0) report_status(a.status, LLAMA_ERR_RANGE);
+          copies(std::true_type());
+        }
+        if (ahead.next(a, first)) aim();
+        --left;
+        fill = fill + 1 == L::STAGES ? 0 : fill + 1;
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    aim();
     look_up();
 #pragma unroll 1
     for (int n = 0; n < L::STAGES - 1; ++n) {
-      request(n);
+      request();
       look_up();
     }
-    const int todo = w1 - w0;
-    int done = 0;
+    int done = 0, use = 0;
     while (done < todo) {
       // ----------------------------------------------------------- a piece ---
-      const int seq = at.seq, unit = at.unit, j0 = at.j, n_tiles = at.n;
+      const int seq = at.seq, unit = at.unit, j0 = at.j, n_tiles = at.n, g = at.g;
       const int j1 = min(n_tiles, j0 + todo - done);
-      const int len = at.len, g = at.g;
-      const int h_in = (unit - g * a.subs) * (8 * NB), nh = min(8 * NB, a.r - h_in);
-      const size_t row0 = (size_t)seq * a.H + g * a.r + h_in;
+      const int r0 = at.sub * (8 * NB), nr = min(8 * NB, at.s.count * a.r - r0);
+      const int before = at.s.kv_len - at.s.count + 1;  // keys that the sequence's first new token sees
+      // row R of the sequence in q and o
+      auto row_at = [&](int R) { return (size_t)(at.s.first + R / a.r) * a.H + g * a.r + R % a.r; };
       uint32_t qf[NB][STEPS][2];
+      int sees[NB][2];  // keys that this thread's columns of S^T see
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         const int h = b * 8 + gi;
-        const uint32_t *src = reinterpret_cast<const uint32_t *>(a.q + (row0 + h) * D + ti * (D / 4));
+        const int *src = reinterpret_cast<const int *>(a.q + row_at(r0 + min(h, nr - 1)) * D + ti * (D / 4));
 #pragma unroll
-        for (int s = 0; s < STEPS; ++s)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            qf[b][s][e] = 0;
-            if (h < nh) qf[b][s][e] = (uint32_t)ld_after_wait(reinterpret_cast<const int *>(src) + 2 * s + e);
+        for (int s = 0; s < STEPS; ++s) {
+          if constexpr (STEPS >= 2) {
+            if (s % 2 == 0) {
+              const int4 x = ld_after_wait(reinterpret_cast<const int4 *>(src + 2 * s));
+              qf[b][s][0] = (uint32_t)x.x;
+              qf[b][s][1] = (uint32_t)x.y;
+              qf[b][s + 1 < STEPS ? s + 1 : s][0] = (uint32_t)x.z;
+              qf[b][s + 1 < STEPS ? s + 1 : s][1] = (uint32_t)x.w;
+            }
+          } else {
+            qf[b][s][0] = (uint32_t)ld_after_wait(src);
+            qf[b][s][1] = (uint32_t)ld_after_wait(src + 1);
           }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) sees[b][e] = before + (r0 + min(b * 8 + ti * 2 + e, nr - 1)) / a.r;
       }
+      const int all_see = before + r0 / a.r;
       float acc[NB][STEPS][4], m[NB][2], l[NB][2];
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
@@ -351,11 +405,11 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_decode_ker
       }
 #pragma unroll 1
       for (int j = j0; j < j1; ++j, ++done) {
-        request(done + L::STAGES - 1);
+        request();
         look_up();
         asm volatile("cp.async.wait_group %0;" ::"n"(L::STAGES - 1) : "memory");
         __syncwarp();
-        const uint32_t sk = ring + done % L::STAGES * L::STAGE, sv = sk + L::HALF;
+        const uint32_t sk = ring + use * L::STAGE, sv = sk + L::HALF;
         // scores: keys gi and gi + 8 of both halves of the tile
         float sc[2][NB][4];
 #pragma unroll
@@ -398,7 +452,7 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_decode_ker
             for (int b = 0; b < NB; ++b) mma16816(sc[mb][b], f, qf[b][s][0], qf[b][s][1]);
           }
         }
-        if ((j + 1) * KD_KEYS > len) {
+        if ((j + 1) * KD_KEYS > all_see) {
           const int key = j * KD_KEYS + gi;
 #pragma unroll
           for (int mb = 0; mb < 2; ++mb)
@@ -406,9 +460,9 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_decode_ker
             for (int b = 0; b < NB; ++b)
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                if (key + mb * 16 + (e / 2) * 8 >= len) sc[mb][b][e] = -INFINITY;
+                if (key + mb * 16 + (e / 2) * 8 >= sees[b][e & 1]) sc[mb][b][e] = -INFINITY;
         }
-        // weights: heads 8 b + 2 ti and the next
+        // weights: rows 8 b + 2 ti and the next
         uint32_t pf[2][NB][2];
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
@@ -456,11 +510,11 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_decode_ker
           for (int e = 0; e < 2; ++e) {
             const int row = mb * 16 + e * 8 + 2 * ti;
             uint32_t x[VW], y[VW];
-            const uint32_t at = sv + row * L::RB + (D >= 64 ? gi * (D / 16) : D == 32 ? gi / 2 * 4 : gi / 4 * 4);
-            ld_words<VW>(at, x);
-            ld_words<VW>(at + L::RB, y);
-            const uint32_t sat = sv + KD_KEYS * L::RB + row * L::SB + gi * L::SB / 8;
-            sv2[e] = kv4_halves(ld_byte(sat), ld_byte(sat + L::SB));
+            const uint32_t from = sv + row * L::RB + (D >= 64 ? gi * (D / 16) : D == 32 ? gi / 2 * 4 : gi / 4 * 4);
+            ld_words<VW>(from, x);
+            ld_words<VW>(from + L::RB, y);
+            const uint32_t scales = sv + KD_KEYS * L::RB + row * L::SB + gi * L::SB / 8;
+            sv2[e] = kv4_halves(ld_byte(scales), ld_byte(scales + L::SB));
 #pragma unroll
             for (int w = 0; w < VW; ++w) {
               if constexpr (D == 32) {
@@ -491,7 +545,8 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_decode_ker
           }
         }
         __syncwarp();  // the stage may be filled again
-        at.next(a, first);
+        use = use + 1 == L::STAGES ? 0 : use + 1;
+        if (j + 1 < j1) ++at.j;  // (the piece is looked at below)
       }
 #pragma unroll
       for (int b = 0; b < NB; ++b)
@@ -506,9 +561,9 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_decode_ker
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int h = b * 8 + ti * 2 + e;
-            if (h >= nh) continue;
+            if (h >= nr || sees[b][e] <= 0) continue;
             const float inv = KD_VALUE / l[b][e];  // scores of NaN or -inf alone: NaN
-            uint32_t *dst = reinterpret_cast<uint32_t *>(a.o + (row0 + h) * D + gi * (D / 8));
+            uint32_t *dst = reinterpret_cast<uint32_t *>(a.o + row_at(r0 + h) * D + gi * (D / 8));
 #pragma unroll
             for (int i = 0; i < STEPS; ++i) dst[i] = kd_pack2(acc[b][i][e] * inv, acc[b][i][e + 2] * inv);
           }
@@ -535,6 +590,7 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_decode_ker
           }
         if (lane == 0) meta[warp * 2 + which] = KdMeta{seq, unit, j0, j1};
       }
+      at.next(a, first);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
   }
@@ -561,20 +617,17 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_decode_ker
     starts &= starts - 1;
     const unsigned chain = there & (starts != 0 ? (1u << (__ffs(starts) - 1)) - 1u : 0xffffffffu) & ~((1u << c) - 1u);
     const int last = 31 - __clz(chain);
-    KdMeta head;
-    head.seq = __shfl_sync(0xffffffffu, mine.seq, c);
-    head.unit = __shfl_sync(0xffffffffu, mine.unit, c);
-    head.j0 = __shfl_sync(0xffffffffu, mine.j0, c);
-    const int end = __shfl_sync(0xffffffffu, mine.j1, last);
-    const int n_tiles = a.direct ? n_run : first[head.seq + 1] - first[head.seq];
-    const bool whole = head.j0 == 0 && end == n_tiles;
-    if (!whole && head.j0 == 0) {
-      const long long item_end = (long long)first[head.seq] * a.units + (long long)(head.unit + 1) * n_tiles;
-      span = make_int4(head.seq, head.unit, (int)((item_end - 1) / each), 0);
+    const int head_j0 = __shfl_sync(0xffffffffu, mine.j0, c), end = __shfl_sync(0xffffffffu, mine.j1, last);
+    KdCursor<NB> it;
+    it.set(a, __shfl_sync(0xffffffffu, mine.seq, c), __shfl_sync(0xffffffffu, mine.unit, c), 0);
+    const bool whole = head_j0 == 0 && end == it.n;
+    if (!whole && head_j0 == 0) {
+      const long long item_end = (long long)first[it.seq] * a.times + (long long)(it.unit + 1) * it.n;
+      span = make_int4(it.seq, it.unit, (int)min((item_end - 1) / each, (long long)gridDim.x - 1), 0);
     }
-    const int g = head.unit / a.subs, h_in = head.unit % a.subs * (8 * NB), nh = min(8 * NB, a.r - h_in);
-    float *out = whole ? nullptr : a.part + ((size_t)blockIdx.x * 2 + (head.j0 == 0 ? 1 : 0)) * (8 * NB * (D + 2));
-    for (int u = threadIdx.x; u < nh * (D / 2); u += THREADS) {
+    const int r0 = it.sub * (8 * NB), nr = min(8 * NB, it.s.count * a.r - r0);
+    float *out = whole ? nullptr : a.part + ((size_t)blockIdx.x * 2 + (head_j0 == 0 ? 1 : 0)) * (8 * NB * (D + 2));
+    for (int u = threadIdx.x; u < nr * (D / 2); u += THREADS) {
       const int h = u / (D / 2), d = u % (D / 2) * 2;
       float mm = -FLT_MAX, ll = 0.f, x = 0.f, y = 0.f;
       for (unsigned left = chain; left != 0; left &= left - 1) mm = fmaxf(mm, piece(__ffs(left) - 1)[8 * NB * D + h]);
@@ -587,9 +640,11 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_decode_ker
         y = fmaf(f, v.y, y);
       }
       if (whole) {
+        const int R = r0 + h, i = R / a.r;
         const float inv = KD_VALUE / ll;
-        *reinterpret_cast<uint32_t *>(a.o + ((size_t)head.seq * a.H + g * a.r + h_in + h) * D + d) =
-            kd_pack2(x * inv, y * inv);
+        if (it.s.kv_len - it.s.count + i >= 0)
+          *reinterpret_cast<uint32_t *>(a.o + ((size_t)(it.s.first + i) * a.H + it.g * a.r + R % a.r) * D + d) =
+              kd_pack2(x * inv, y * inv);
       } else {
         *reinterpret_cast<float2 *>(out + h * D + d) = make_float2(x, y);
         if (d == 0) {
@@ -603,15 +658,17 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_decode_ker
 }
 
 // Joins the parts of the items that several CTAs had: a CTA of D / 2 threads for each CTA that
-// may have begun one, and head.
+// may have begun one, and row.
 template <int D, int NB>
-__global__ void __launch_bounds__(D / 2) kv4_decode_join_kernel(const __grid_constant__ KdArgs a) {
+__global__ void __launch_bounds__(D / 2) kv4_rows_join_kernel(const __grid_constant__ KdArgs a) {
   grid_dependency_wait();
   const int c0 = blockIdx.x, h = blockIdx.y;
   const int4 span = ld_after_wait(a.spans + c0);
   if (span.x < 0) return;
-  const int g = span.y / a.subs, h_in = span.y % a.subs * (8 * NB);
-  if (h >= a.r - h_in) return;
+  KdCursor<NB> it;
+  it.set(a, span.x, span.y, 0);
+  const int R = it.sub * (8 * NB) + h, i = R / a.r;
+  if (R >= it.s.count * a.r || it.s.kv_len - it.s.count + i < 0) return;
   auto part = [&](int c) { return a.part + ((size_t)c * 2 + (c == c0 ? 1 : 0)) * (8 * NB * (D + 2)); };
   const int d = threadIdx.x * 2;
   float m = -FLT_MAX, l = 0.f, x = 0.f, y = 0.f;
@@ -627,24 +684,22 @@ __global__ void __launch_bounds__(D / 2) kv4_decode_join_kernel(const __grid_con
     y = fmaf(f, v.y, y);
   }
   const float inv = KD_VALUE / l;
-  *reinterpret_cast<uint32_t *>(a.o + ((size_t)span.x * a.H + g * a.r + h_in + h) * D + d) = kd_pack2(x * inv, y * inv);
+  *reinterpret_cast<uint32_t *>(a.o + ((size_t)(it.s.first + i) * a.H + it.g * a.r + R % a.r) * D + d) =
+      kd_pack2(x * inv, y * inv);
 }
 
-// Form and grid of a call.
+// Form and grid of a call; rows: of a sequence and KV head, on average.
 struct KdPlan {
-  int nb = 1, subs = 1, units = 1;
-  bool direct = true;
-  int ctas = 1;
+  int nb = 1, ctas = 1;
+  bool direct = false;
   size_t off_part = 0, bytes = 0;
 };
-KdPlan plan_of(int n_seqs, int max_kv_len, int H, int G, int D) {
+KdPlan plan_of(const PackedView &b, long long rows, int H, int G, int D, bool decode) {
   KdPlan p;
-  const int r = H / G, sms = sm_count();
-  p.nb = r > 8 ? 2 : 1;
-  p.subs = (r + 8 * p.nb - 1) / (8 * p.nb);
-  p.units = G * p.subs;
-  const long long items = (long long)n_seqs * p.units;
-  p.direct = (max_kv_len + KD_KEYS - 1) / KD_KEYS <= KD_DIRECT_TILES && items <= 0x7fffffffLL;
+  const int sms = sm_count();
+  p.nb = rows <= 8 ? 1 : rows <= 16 || decode ? 2 : KD_MAX_NB;
+  const long long items = (long long)b.n_seqs * G * ((H / G + 8 * p.nb - 1) / (8 * p.nb));
+  p.direct = decode && (b.max_kv_len + KD_KEYS - 1) / KD_KEYS <= KD_DIRECT_TILES && items <= 0x7fffffffLL;
   p.ctas = p.direct ? (int)items : sms > 2 ? sms : 2;
   if (!p.direct) {
     p.off_part = ((size_t)p.ctas * 16 + 127) / 128 * 128;
@@ -658,49 +713,46 @@ cudaError_t launch(KdArgs a, const KdPlan &p, cudaStream_t st) {
   using L = KdLayout<D, NB>;
   static PerContextOnce attr;
   const cudaError_t e = attr.run([] {
-    return cudaFuncSetAttribute(kv4_decode_kernel<D, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(kv4_rows_kernel<D, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 L::bytes(LLAMA_PACKED_MAX_SEQS));
   });
   if (e != cudaSuccess) return e;
   count_launch();
   const cudaError_t r =
-      launch_pdl(kv4_decode_kernel<D, NB>, dim3((unsigned)p.ctas), dim3(L::WARPS * 32), L::bytes(a.n_seqs), st, a);
+      launch_pdl(kv4_rows_kernel<D, NB>, dim3((unsigned)p.ctas), dim3(L::WARPS * 32), L::bytes(a.b.n_seqs), st, a);
   if (r != cudaSuccess || p.direct) return r;
   count_launch();
-  return launch_pdl(kv4_decode_join_kernel<D, NB>, dim3((unsigned)(p.ctas - 1), 8 * NB), dim3(D / 2), 0, st, a);
+  return launch_pdl(kv4_rows_join_kernel<D, NB>, dim3((unsigned)(p.ctas - 1), 8 * NB), dim3(D / 2), 0, st, a);
 }
 
-}  // namespace
-
-size_t kv4_decode_workspace_bytes(int n_seqs, int max_kv_len, int H, int G, int D) {
-  return plan_of(n_seqs, max_kv_len, H, G, D).bytes;
+// Tiles of a KV head's items over all sequences, at most.
+long long most_tiles(const PackedView &b, int H, int G) {
+  return (long long)((b.max_kv_len + KD_KEYS - 1) / KD_KEYS) * ((long long)b.n_tokens * (H / G) / 8 + b.n_seqs);
 }
 
-cudaError_t launch_kv4_decode(const bf16 *q, const uint8_t *k, const uint8_t *v, bf16 *o, const PagedView &pv,
-                              const int *kv_lens, int n_seqs, int max_kv_len, int H, int G, int D, void *workspace,
-                              int *status, cudaStream_t st) {
-  const KdPlan p = plan_of(n_seqs, max_kv_len, H, G, D);
+cudaError_t launch_rows(const bf16 *q, const uint8_t *k, const uint8_t *v, bf16 *o, const PagedView &pv,
+                        const PackedView &b, int H, int G, int D, void *workspace, const KdPlan &p, int *status,
+                        cudaStream_t st) {
   KdArgs a;
   a.q = q;
   a.k = k;
   a.v = v;
   a.o = o;
   a.pv = pv;
-  a.kv_lens = kv_lens;
-  a.n_seqs = n_seqs;
-  a.max_kv_len = max_kv_len;
+  a.b = b;
   a.H = H;
   a.G = G;
   a.r = H / G;
-  a.subs = p.subs;
-  a.units = p.units;
   a.direct = p.direct;
+  a.times = b.q_offsets != nullptr ? G : G * ((a.r + 8 * p.nb - 1) / (8 * p.nb));
+  a.most = b.q_offsets != nullptr ? (int)most_tiles(b, H, G) : 0x7fffffff;
   a.scale_log2 = 1.4426950408889634f / sqrtf((float)D);
   a.part = p.direct ? nullptr : reinterpret_cast<float *>((char *)workspace + p.off_part);
   a.spans = p.direct ? nullptr : reinterpret_cast<int4 *>(workspace);
   a.status = status;
-#define KD_CASE(d) \
-  case d: return p.nb == 1 ? launch<d, 1>(a, p, st) : launch<d, 2>(a, p, st);
+#define KD_CASE(d)                                     \
+  case d:                                              \
+    return p.nb == 1 ? launch<d, 1>(a, p, st) : p.nb == 2 ? launch<d, 2>(a, p, st) : launch<d, KD_MAX_NB>(a, p, st);
   switch (D) {
     KD_CASE(16)
     KD_CASE(32)
@@ -709,6 +761,44 @@ cudaError_t launch_kv4_decode(const bf16 *q, const uint8_t *k, const uint8_t *v,
   }
 #undef KD_CASE
   return cudaErrorInvalidValue;
+}
+
+PackedView decode_view(const int *kv_lens, int n_seqs, int max_kv_len) {
+  PackedView b;
+  b.kv_lens = kv_lens;
+  b.n_seqs = n_seqs;
+  b.n_tokens = n_seqs;
+  b.max_kv_len = max_kv_len;
+  return b;
+}
+
+long long rows_of(const PackedView &b, int H, int G) {
+  return ((long long)b.n_tokens * (H / G) + b.n_seqs - 1) / b.n_seqs;
+}
+
+}  // namespace
+
+size_t kv4_decode_workspace_bytes(int n_seqs, int max_kv_len, int H, int G, int D) {
+  return plan_of(decode_view(nullptr, n_seqs, max_kv_len), H / G, H, G, D, true).bytes;
+}
+
+cudaError_t launch_kv4_decode(const bf16 *q, const uint8_t *k, const uint8_t *v, bf16 *o, const PagedView &pv,
+                              const int *kv_lens, int n_seqs, int max_kv_len, int H, int G, int D, void *workspace,
+                              int *status, cudaStream_t st) {
+  const PackedView b = decode_view(kv_lens, n_seqs, max_kv_len);
+  return launch_rows(q, k, v, o, pv, b, H, G, D, workspace, plan_of(b, H / G, H, G, D, true), status, st);
+}
+
+// Few rows: what tcgen05's 128-row tiles would mostly pad.  (The counts of tiles are ints.)
+bool kv4_rows_fit(const PackedView &b, int H, int G) {
+  return rows_of(b, H, G) <= KV4_FEW_ROWS && most_tiles(b, H, G) <= 0x7fffffffLL;
+}
+size_t kv4_rows_workspace_bytes(const PackedView &b, int H, int G, int D) {
+  return plan_of(b, rows_of(b, H, G), H, G, D, false).bytes;
+}
+cudaError_t launch_kv4_rows(const bf16 *q, const uint8_t *k, const uint8_t *v, bf16 *o, const PagedView &pv,
+                            const PackedView &b, int H, int G, int D, void *workspace, int *status, cudaStream_t st) {
+  return launch_rows(q, k, v, o, pv, b, H, G, D, workspace, plan_of(b, rows_of(b, H, G), H, G, D, false), status, st);
 }
 
 }  // namespace llama

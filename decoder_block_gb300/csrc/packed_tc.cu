@@ -1445,11 +1445,13 @@ cudaError_t launch_kv4(const bf16 *q, const uint8_t *k, const uint8_t *v, bf16 *
 }  // namespace
 
 size_t packed_kv4_workspace_bytes(const PackedView &b, int H, int G, int D) {
+  if (kv4_rows_fit(b, H, G)) return kv4_rows_workspace_bytes(b, H, G, D);
   return packed_sizes(b, H, G, D < 64 ? 64 : D, sm_count(), kv4_tiles(b, H, G)).bytes;
 }
 
 cudaError_t launch_packed_kv4(const bf16 *q, const uint8_t *k, const uint8_t *v, bf16 *o, const PagedView &pv,
                               const PackedView &b, int H, int G, int D, void *workspace, int *status, cudaStream_t st) {
+  if (kv4_rows_fit(b, H, G)) return launch_kv4_rows(q, k, v, o, pv, b, H, G, D, workspace, status, st);
   return kv4_tiles(b, H, G) == 1 ? launch_kv4<1>(q, k, v, o, pv, b, H, G, D, workspace, status, st)
                                  : launch_kv4<2>(q, k, v, o, pv, b, H, G, D, workspace, status, st);
 }

@@ -102,7 +102,14 @@ cudaError_t launch_paged_decode_tc(const bf16 *q, const bf16 *k, const bf16 *v, 
                                    const int *kv_lens, int n_seqs, int max_kv_len, int H, int G, int D,
                                    void *workspace, int *status, cudaStream_t st);
 
-// Decode attention over pages held in 4 bits, q and o bf16 (kv4_decode.cu).
+// Packed attention of few rows a sequence over pages held in 4 bits (kv4_rows.cu), where it fits.
+constexpr int KV4_FEW_ROWS = 24;  // rows (token, head) of a sequence and KV head, at most on average
+bool kv4_rows_fit(const PackedView &b, int H, int G);
+size_t kv4_rows_workspace_bytes(const PackedView &b, int H, int G, int D);
+cudaError_t launch_kv4_rows(const bf16 *q, const uint8_t *k, const uint8_t *v, bf16 *o, const PagedView &pv,
+                            const PackedView &b, int H, int G, int D, void *workspace, int *status, cudaStream_t st);
+
+// Decode attention over pages held in 4 bits, q and o bf16 (kv4_rows.cu).
 size_t kv4_decode_workspace_bytes(int n_seqs, int max_kv_len, int H, int G, int D);
 cudaError_t launch_kv4_decode(const bf16 *q, const uint8_t *k, const uint8_t *v, bf16 *o, const PagedView &pv,
                               const int *kv_lens, int n_seqs, int max_kv_len, int H, int G, int D, void *workspace,

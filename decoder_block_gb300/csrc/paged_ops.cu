@@ -75,7 +75,7 @@ llama_status view_of(const llama_paged_kv_cache *kv, int32_t dtype, int32_t G, i
   v.page_stride = kv->page_stride == 0 ? dense : kv->page_stride;
   if (v.page_stride < dense) return LLAMA_ERR_INVALID_ARG;
   if (v.page_stride * unit % 16 != 0) return LLAMA_ERR_ALIGN;
-  if (v.page_stride >= (1LL << 39) / unit) return LLAMA_ERR_UNSUPPORTED;
+  if (v.page_stride >= (dtype == KV4_PAGES ? 1LL << 32 : (1LL << 39) / unit)) return LLAMA_ERR_UNSUPPORTED;
   v.table = kv->page_table;
   v.n_pages = kv->n_pages;
   v.max_pages = kv->max_pages;

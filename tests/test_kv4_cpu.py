@@ -100,6 +100,7 @@ def test_refusals(lb, host):
     assert _calls(lb, bf, _cache(lb, host, page_stride=dense - 16), ok_b, host, 4, 2, 64) == [inv] * 4
     assert _calls(lb, bf, _cache(lb, host, page_stride=dense + 8), ok_b, host, 4, 2, 64) == [align] * 4
     assert _calls(lb, bf, _cache(lb, host, page_stride=1 << 39), ok_b, host, 4, 2, 64) == [uns] * 4
+    assert _calls(lb, bf, _cache(lb, host, page_stride=1 << 32), ok_b, host, 4, 2, 64) == [uns] * 4
     assert _calls(lb, bf, ok_kv, _batch(lb, host, n_seqs=-1), host, 4, 2, 64) == [inv] * 4
     assert _calls(lb, bf, ok_kv, _batch(lb, host, n_seqs=4097), host, 4, 2, 64) == [uns] * 4
     assert _calls(lb, bf, ok_kv, _batch(lb, host, max_kv=lb.LLAMA_PACKED_MAX_KV + 1), host, 4, 2, 64) == [uns] * 4
