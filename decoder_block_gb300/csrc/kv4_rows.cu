@@ -48,6 +48,7 @@ constexpr float KD_VALUE = 2.0f;  // V's operand is half of V
 // Key tiles of a CTA's item in the direct form, at most.
 constexpr int KD_DIRECT_TILES = 64;
 constexpr int KD_MAX_NB = 3;
+constexpr int KD_LEAST = 4;  // tiles of a CTA's run, at least: a warp on each scheduler
 
 // NB: blocks of 8 rows of an item.
 template <int D, int NB>
@@ -268,12 +269,12 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_rows_kerne
       }
     const long long total = (long long)first[a.b.n_seqs] * a.times;
     each = (total + gridDim.x - 1) / gridDim.x;
-    each = each > L::WARPS ? each : L::WARPS;
+    each = each > KD_LEAST ? each : KD_LEAST;
     begin = min(total, each * blockIdx.x);
     n_run = (int)(min(total, begin + each) - begin);
   }
-  const int w0 = (int)((long long)n_run * warp / L::WARPS), w1 = (int)((long long)n_run * (warp + 1) / L::WARPS);
-  const int todo = w1 - w0;
+  const int share = n_run / L::WARPS, more = n_run % L::WARPS;  // the first `more` warps take one more
+  const int w0 = warp * share + min(warp, more), todo = share + (warp < more ? 1 : 0);
 
   if (todo > 0) {
     if (a.direct) at.j = w0;
@@ -297,6 +298,14 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_rows_kerne
       const int off = D >= 64 ? lane * 16 : lane % 16 * CHUNK;
       from_k = a.k + block + off;
       from_v = a.v + block + off;
+      // the item's queries, a line each: they are loaded when its first tile is there
+      const int r0 = ahead.sub * (8 * NB), nr = min(8 * NB, ahead.s.count * a.r - r0);
+      constexpr int LINES = D >= 64 ? D / 64 : 1;
+      for (int i = lane; i < nr * LINES; i += 32) {
+        const int R = r0 + i / LINES;
+        const bf16 *row = a.q + ((size_t)(ahead.s.first + R / a.r) * a.H + ahead.g * a.r + R % a.r) * D;
+        asm volatile("prefetch.global.L1 [%0];" ::"l"(row + i % LINES * 64));
+      }
       from_s = (lane < 16 ? a.k : a.v) + block + (L::RB << a.pv.page_log2) + s_lane % L::SB * 16;
     };
     auto look_up = [&] {
@@ -610,51 +619,70 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_rows_kerne
   const int prev = below != 0 ? 31 - __clz(below) : lane;
   const int prev_seq = __shfl_sync(0xffffffffu, mine.seq, prev), prev_unit = __shfl_sync(0xffffffffu, mine.unit, prev);
   const bool joined = prev != lane && prev_seq == mine.seq && prev_unit == mine.unit;
-  unsigned starts = __ballot_sync(0xffffffffu, mine.seq >= 0 && !joined);
-  int4 span = make_int4(-1, 0, 0, 0);
-  while (starts != 0) {
-    const int c = __ffs(starts) - 1;
-    starts &= starts - 1;
-    const unsigned chain = there & (starts != 0 ? (1u << (__ffs(starts) - 1)) - 1u : 0xffffffffu) & ~((1u << c) - 1u);
-    const int last = 31 - __clz(chain);
-    const int head_j0 = __shfl_sync(0xffffffffu, mine.j0, c), end = __shfl_sync(0xffffffffu, mine.j1, last);
+  const unsigned starts = __ballot_sync(0xffffffffu, mine.seq >= 0 && !joined);
+  // A warp for each chain and row: a lane for each piece's m and l, then for each two columns.
+  const int rows = a.b.q_offsets != nullptr ? 8 * NB : min(8 * NB, a.r);
+  for (int u = warp; u < __popc(starts) * rows; u += L::WARPS) {
+    const int c = __fns(starts, 0, u / rows + 1), h = u % rows;
+    const unsigned later = starts & ~((2u << c) - 1u);
+    const unsigned chain = there & (later != 0 ? (1u << (__ffs(later) - 1)) - 1u : 0xffffffffu) & ~((1u << c) - 1u);
+    const int head_j0 = __shfl_sync(0xffffffffu, mine.j0, c), end = __shfl_sync(0xffffffffu, mine.j1, 31 - __clz(chain));
     KdCursor<NB> it;
     it.set(a, __shfl_sync(0xffffffffu, mine.seq, c), __shfl_sync(0xffffffffu, mine.unit, c), 0);
-    const bool whole = head_j0 == 0 && end == it.n;
-    if (!whole && head_j0 == 0) {
-      const long long item_end = (long long)first[it.seq] * a.times + (long long)(it.unit + 1) * it.n;
-      span = make_int4(it.seq, it.unit, (int)min((item_end - 1) / each, (long long)gridDim.x - 1), 0);
-    }
-    const int r0 = it.sub * (8 * NB), nr = min(8 * NB, it.s.count * a.r - r0);
-    float *out = whole ? nullptr : a.part + ((size_t)blockIdx.x * 2 + (head_j0 == 0 ? 1 : 0)) * (8 * NB * (D + 2));
-    for (int u = threadIdx.x; u < nr * (D / 2); u += THREADS) {
-      const int h = u / (D / 2), d = u % (D / 2) * 2;
-      float mm = -FLT_MAX, ll = 0.f, x = 0.f, y = 0.f;
-      for (unsigned left = chain; left != 0; left &= left - 1) mm = fmaxf(mm, piece(__ffs(left) - 1)[8 * NB * D + h]);
-      for (unsigned left = chain; left != 0; left &= left - 1) {
-        const float *p = piece(__ffs(left) - 1);
-        const float f = ptx::ex2_approx(p[8 * NB * D + h] - mm);
-        const float2 v = *reinterpret_cast<const float2 *>(p + h * D + d);
-        ll = fmaf(f, p[8 * NB * (D + 1) + h], ll);
-        x = fmaf(f, v.x, x);
-        y = fmaf(f, v.y, y);
-      }
-      if (whole) {
-        const int R = r0 + h, i = R / a.r;
-        const float inv = KD_VALUE / ll;
-        if (it.s.kv_len - it.s.count + i >= 0)
-          *reinterpret_cast<uint32_t *>(a.o + ((size_t)(it.s.first + i) * a.H + it.g * a.r + R % a.r) * D + d) =
-              kd_pack2(x * inv, y * inv);
-      } else {
-        *reinterpret_cast<float2 *>(out + h * D + d) = make_float2(x, y);
-        if (d == 0) {
-          out[8 * NB * D + h] = mm;
-          out[8 * NB * (D + 1) + h] = ll;
+    const int R = it.sub * (8 * NB) + h, i = R / a.r;
+    if (R >= it.s.count * a.r) continue;
+    const bool whole = head_j0 == 0 && end == it.n, in = chain >> lane & 1;
+    const float m = in ? piece(lane)[8 * NB * D + h] : -FLT_MAX, top = warp_max(m);
+    const float f = in ? ptx::ex2_approx(m - top) : 0.f;
+    const float l = warp_sum(in ? f * piece(lane)[8 * NB * (D + 1) + h] : 0.f);
+    float2 x[D > 64 ? D / 64 : 1];
+#pragma unroll
+    for (int e = 0; e < (D > 64 ? D / 64 : 1); ++e) x[e] = make_float2(0.f, 0.f);
+    for (unsigned left = chain; left != 0; left &= left - 1) {
+      const int s = __ffs(left) - 1;
+      const float g = __shfl_sync(0xffffffffu, f, s);
+      const float *p = piece(s) + h * D + 2 * lane;
+      if (2 * lane < D) {
+#pragma unroll
+        for (int e = 0; e < (D > 64 ? D / 64 : 1); ++e) {
+          const float2 v = *reinterpret_cast<const float2 *>(p + 64 * e);
+          x[e].x = fmaf(g, v.x, x[e].x);
+          x[e].y = fmaf(g, v.y, x[e].y);
         }
       }
     }
+    if (2 * lane >= D) continue;
+    if (!whole) {
+      float *out = a.part + ((size_t)blockIdx.x * 2 + (head_j0 == 0 ? 1 : 0)) * (8 * NB * (D + 2));
+#pragma unroll
+      for (int e = 0; e < (D > 64 ? D / 64 : 1); ++e)
+        *reinterpret_cast<float2 *>(out + h * D + 64 * e + 2 * lane) = x[e];
+      if (lane == 0) {
+        out[8 * NB * D + h] = top;
+        out[8 * NB * (D + 1) + h] = l;
+      }
+    } else if (it.s.kv_len - it.s.count + i >= 0) {
+      const float inv = KD_VALUE / l;
+      bf16 *dst = a.o + ((size_t)(it.s.first + i) * a.H + it.g * a.r + R % a.r) * D + 2 * lane;
+#pragma unroll
+      for (int e = 0; e < (D > 64 ? D / 64 : 1); ++e)
+        *reinterpret_cast<uint32_t *>(dst + 64 * e) = kd_pack2(x[e].x * inv, x[e].y * inv);
+    }
   }
-  if (a.spans != nullptr && threadIdx.x == 0) a.spans[blockIdx.x] = span;
+  if (a.spans != nullptr && warp == 0) {  // the item that this CTA begins and does not end is its last one
+    int4 span = make_int4(-1, 0, 0, 0);
+    if (starts != 0) {
+      const int c = 31 - __clz(starts);
+      KdCursor<NB> it;
+      it.set(a, __shfl_sync(0xffffffffu, mine.seq, c), __shfl_sync(0xffffffffu, mine.unit, c), 0);
+      const int j0 = __shfl_sync(0xffffffffu, mine.j0, c), end = __shfl_sync(0xffffffffu, mine.j1, 31 - __clz(there));
+      if (j0 == 0 && end < it.n) {
+        const long long item_end = (long long)first[it.seq] * a.times + (long long)(it.unit + 1) * it.n;
+        span = make_int4(it.seq, it.unit, (int)min((item_end - 1) / each, (long long)gridDim.x - 1), 0);
+      }
+    }
+    if (lane == 0) a.spans[blockIdx.x] = span;
+  }
 }
 
 // Joins the parts of the items that several CTAs had: a CTA of D / 2 threads for each CTA that
@@ -699,7 +727,7 @@ KdPlan plan_of(const PackedView &b, long long rows, int H, int G, int D, bool de
   const int sms = sm_count();
   p.nb = rows <= 8 ? 1 : rows <= 16 || decode ? 2 : KD_MAX_NB;
   const long long items = (long long)b.n_seqs * G * ((H / G + 8 * p.nb - 1) / (8 * p.nb));
-  p.direct = decode && (b.max_kv_len + KD_KEYS - 1) / KD_KEYS <= KD_DIRECT_TILES && items <= 0x7fffffffLL;
+  p.direct = decode && (b.max_kv_len + KD_KEYS - 1) / KD_KEYS <= KD_DIRECT_TILES && items <= sms;
   p.ctas = p.direct ? (int)items : sms > 2 ? sms : 2;
   if (!p.direct) {
     p.off_part = ((size_t)p.ctas * 16 + 127) / 128 * 128;
@@ -722,7 +750,7 @@ cudaError_t launch(KdArgs a, const KdPlan &p, cudaStream_t st) {
       launch_pdl(kv4_rows_kernel<D, NB>, dim3((unsigned)p.ctas), dim3(L::WARPS * 32), L::bytes(a.b.n_seqs), st, a);
   if (r != cudaSuccess || p.direct) return r;
   count_launch();
-  return launch_pdl(kv4_rows_join_kernel<D, NB>, dim3((unsigned)(p.ctas - 1), 8 * NB), dim3(D / 2), 0, st, a);
+  return launch_pdl(kv4_rows_join_kernel<D, NB>, dim3((unsigned)(p.ctas - 1), (unsigned)(a.b.q_offsets != nullptr || a.r > 8 * NB ? 8 * NB : a.r)), dim3(D / 2), 0, st, a);
 }
 
 // Tiles of a KV head's items over all sequences, at most.
