@@ -132,28 +132,50 @@ __device__ __forceinline__ float4 kv4_four(uint32_t w, int half, float scale) {
                      (float)((int)(w >> 4 & 15) - 8) * scale, (float)((int)(w >> 20 & 15) - 8) * scale);
 }
 
-// A block of 16 values: its scale byte and codes (two words).  `bad` is set for a NaN or a
-// magnitude beyond KV4_MOST.
-__device__ __forceinline__ uint32_t kv4_quantise(const float *x, uint32_t (&words)[2], bool &bad) {
+__device__ __forceinline__ float max_nan_abs(float a, float b) {  // NaN when either is
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(fabsf(b)));
+  return d;
+}
+// A block of 16 values: its scale byte and codes (two words).  `bad` is set for a NaN, which is
+// stored as 0, or a magnitude beyond KV4_MOST, stored as that.
+//
+// A code is x / s rounded, ties to even.  With y = 1 / s rounded, q = x y is off by 2^-23; the
+// remainder x - s q is exact in one fma (s has four bits), and q + (x - s q) y then differs
+// from x / s by 2^-46 before it is rounded.  That is as good as the quotient itself: x / s is
+// halfway between two whole numbers, which are fp32 numbers, or away from there by more
+// than its rounding (by 2^-23 / 1.875 of itself at least, as x and s times a half are fp32).
+// The sum with 1.5 * 2^23 + 8 rounds it and has the code in its lowest bits; multiplied by
+// powers of two the codes add up in their places, and what the sums' upper bits add is known.
+__device__ __forceinline__ uint32_t kv4_quantise(float (&x)[KV4_BLOCK], uint32_t (&words)[2], bool &bad) {
   float most = 0.f;
-  bool nan = false;
 #pragma unroll
-  for (int e = 0; e < KV4_BLOCK; ++e) {
-    most = fmaxf(most, fabsf(x[e]));  // (NaN is left out)
-    nan |= x[e] != x[e];
+  for (int e = 0; e < KV4_BLOCK; ++e) most = max_nan_abs(most, x[e]);
+  if (!(most <= KV4_MOST)) {
+    bad = true;
+    most = 0.f;
+#pragma unroll
+    for (int e = 0; e < KV4_BLOCK; ++e) {
+      x[e] = x[e] != x[e] ? 0.f : fminf(fmaxf(x[e], -KV4_MOST), KV4_MOST);
+      most = fmaxf(most, fabsf(x[e]));
+    }
   }
-  bad |= nan || most > KV4_MOST;
   // the smallest three-bit mantissa at or above most / 7: round the fp32's bits up
   const int up = (int)((__float_as_uint(__fdiv_rn(most, KV4_LEVELS)) + 0xfffffu) >> 20) - KV4_SCALE_BASE;
   const uint32_t byte = (uint32_t)min(max(up, 0), 255);
-  const float s = kv4_scale(byte);
-  words[0] = words[1] = 0;
+  const float s = kv4_scale(byte), y = __frcp_rn(s);
+  constexpr float SUM = 12582912.f + 8.f;      // 1.5 * 2^23 + 8
+  constexpr uint32_t UPPER = 0x4b400000u;      // its bits without the 8
 #pragma unroll
-  for (int e = 0; e < KV4_BLOCK; ++e) {
-    // NaN becomes -7 by the clamp and 0 by the choice
-    const float n = fminf(fmaxf(rintf(__fdiv_rn(x[e], s)), -KV4_LEVELS), KV4_LEVELS);
-    const uint32_t code = (uint32_t)((x[e] != x[e] ? 0 : (int)n) + 8);
-    words[e / 8] |= code << (4 * (e % 8 / 2) + 16 * (e % 2));
+  for (int h = 0; h < 2; ++h) {
+    uint32_t w = 0u - UPPER * 0x11111111u;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float v = x[8 * h + e], q = v * y;
+      const float n = fmaf(fmaf(-s, q, v), y, q) + SUM;
+      w += __float_as_uint(n) << (4 * (e / 2) + 16 * (e % 2));
+    }
+    words[h] = w;
   }
   return byte;
 }

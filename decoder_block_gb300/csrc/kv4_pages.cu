@@ -3,7 +3,8 @@
 // transformer block", How it works: rotate, then write at the position).
 //
 // Both are data movement.  A CTA takes a few consecutive rows; one warp per row finds
-// its sequence, position and page.
+// its sequence, position and page.  A thread keeps its place in a row (which head, which
+// elements) and goes through the rows, so that the place is worked out once.
 //   write  query heads move in units of two 16-byte vectors D / 2 apart, the two that
 //          turn together in the halves layout.  Of keys and values a thread takes 32
 //          elements, 16 and 16 more D / 2 further: whole blocks, so that a scale is
@@ -17,9 +18,15 @@ namespace {
 
 constexpr int KW_THREADS = 256;
 constexpr int KW_CTAS = 3;   // CTAs of an SM
-constexpr int KW_ROWS = 4;   // rows of a CTA, at most
-constexpr int KW_UNITS = 2;  // units of a thread in flight
+constexpr int KW_ROWS = 16;  // rows of a CTA, at most
+constexpr int KW_UNITS = 2;  // rows of a thread in flight
 constexpr int KR_UNITS = 4;
+#ifndef KW_MOST
+#define KW_MOST 4
+#endif
+#ifndef KR_MOST
+#define KR_MOST 8
+#endif
 
 struct KwArgs {
   PagedView pv;
@@ -28,31 +35,34 @@ struct KwArgs {
   int table_max_seq;
   int H, G, D, rows;  // rows of a CTA
   int halves;
+  int q_lanes, kv_lanes;  // threads side by side in a row (powers of two)
   int *status;
 };
 
 // Position and page of the CTA's rows, one warp each: position -1 out of range, -2 no such row.
+// Also where the page begins in a pool, in bytes.
 __device__ __forceinline__ void find_rows(const PagedView &pv, const PackedView &b, int t0, int rows, int max_pos,
-                                          bool early_is_bad, int *s_pos, int *s_page, int *status) {
-  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-  if (warp >= rows) return;
-  const int t = t0 + warp;
-  const int i = t < b.n_tokens ? find_seq(b, t) : -1;
-  int pos = -2, page = -1;
-  if (i >= 0) {
-    const SeqSpan s = seq_span(b, pv, i);
-    pos = s.kv_len - (s.first + s.count - t);
-    if (pos < 0 || pos >= max_pos) {
-      if ((pos >= 0 || early_is_bad) && lane == 0) report_status(status, LLAMA_ERR_RANGE);
-      pos = -1;
-    } else {
-      page = pv.page(i, pos >> pv.page_log2);
-      if (page < 0 && lane == 0) report_status(status, LLAMA_ERR_RANGE);
+                                          bool early_is_bad, int *s_pos, long long *s_page, int *status) {
+  const int lane = threadIdx.x & 31;
+  for (int row = threadIdx.x / 32; row < rows; row += KW_THREADS / 32) {
+    const int t = t0 + row;
+    const int i = t < b.n_tokens ? find_seq(b, t) : -1;
+    int pos = -2, page = -1;
+    if (i >= 0) {
+      const SeqSpan s = seq_span(b, pv, i);
+      pos = s.kv_len - (s.first + s.count - t);
+      if (pos < 0 || pos >= max_pos) {
+        if ((pos >= 0 || early_is_bad) && lane == 0) report_status(status, LLAMA_ERR_RANGE);
+        pos = -1;
+      } else {
+        page = pv.page(i, pos >> pv.page_log2);
+        if (page < 0 && lane == 0) report_status(status, LLAMA_ERR_RANGE);
+      }
     }
-  }
-  if (lane == 0) {
-    s_pos[warp] = pos;
-    s_page[warp] = page;
+    if (lane == 0) {
+      s_pos[row] = pos;
+      s_page[row] = page < 0 ? -1 : page * pv.page_stride;
+    }
   }
 }
 
@@ -68,7 +78,8 @@ template <typename T, int N>
 __global__ void __launch_bounds__(KW_THREADS, KW_CTAS)
     rope_kv4_kernel(const T *qkv, T *q_out, uint8_t *kc, uint8_t *vc, const __grid_constant__ KwArgs a) {
   constexpr int V = Vec16<T>::N;
-  __shared__ int s_pos[KW_ROWS], s_page[KW_ROWS];
+  __shared__ int s_pos[KW_ROWS];
+  __shared__ long long s_page[KW_ROWS];
   const int t0 = (int)blockIdx.x * a.rows;
   const int heads = a.H + 2 * a.G, per_head = a.D / (2 * V);
   allow_dependents_launch();
@@ -82,14 +93,17 @@ __global__ void __launch_bounds__(KW_THREADS, KW_CTAS)
   auto angles = [&](int pos, int at) { return a.table + (size_t)pos * (a.D / 2) + at; };
 
   // Keys and values first: theirs is the longer way.
-  const int kv_units = 2 * a.G * (a.D / N);
-  for (int u0 = threadIdx.x; u0 < a.rows * kv_units; u0 += KW_THREADS) {
-    const int row = u0 / kv_units, u = u0 % kv_units;
-    const int pos = s_pos[row], page = s_page[row];
+  const int kv_units = 2 * a.G * (a.D / N), kv_rows = KW_THREADS / a.kv_lanes;
+  for (int u = threadIdx.x & (a.kv_lanes - 1); u < kv_units; u += a.kv_lanes) {
+   const int head = u / (a.D / N), e = u % (a.D / N) * (N / 2);  // elements e .., and those D / 2 further
+   const bool key = head < a.G;
+   uint8_t *const block = (key ? kc : vc) + (long long)(key ? head : head - a.G) * kv4_block_bytes(1 << a.pv.page_log2, a.D);
+   const T *const first = qkv + ((size_t)t0 * heads + a.H + head) * a.D;
+   for (int row = threadIdx.x / a.kv_lanes; row < a.rows; row += kv_rows) {
+    const int pos = s_pos[row];
+    const long long page = s_page[row];
     if (pos < 0 || page < 0) continue;
-    const int head = u / (a.D / N), e = u % (a.D / N) * (N / 2);  // elements e .., and those D / 2 further
-    const bool key = head < a.G;
-    const T *src = qkv + ((size_t)(t0 + row) * heads + a.H + head) * a.D;
+    const T *src = first + (size_t)row * (heads * a.D);
     float x[N];
 #pragma unroll
     for (int j = 0; j < N; j += V) {
@@ -115,38 +129,40 @@ __global__ void __launch_bounds__(KW_THREADS, KW_CTAS)
         turn(x[j + 2], x[j + 3], make_float2(f.z, f.w), x[j + 2], x[j + 3]);
       }
     }
-    const int g = key ? head : head - a.G, slot = pos & ((1 << a.pv.page_log2) - 1);
-    const Kv4Row r = kv4_row(key ? kc : vc, a.pv, page, g, a.D, slot);
+    const int slot = pos & ((1 << a.pv.page_log2) - 1);
+    uint8_t *codes = block + page + slot * kv4_code_bytes(a.D);
+    uint8_t *scales = block + page + (kv4_code_bytes(a.D) << a.pv.page_log2) + slot * kv4_scale_bytes(a.D);
     bool bad = false;
     // blocks of 16: at e and, with N = 32, at e + D / 2
 #pragma unroll
     for (int j = 0; j < N / KV4_BLOCK; ++j) {
       const int at = N == 32 ? e + j * (a.D / 2) : 0;
       uint32_t w[2];
-      const uint32_t byte = kv4_quantise(x + j * KV4_BLOCK, w, bad);
-      *reinterpret_cast<uint2 *>(const_cast<uint8_t *>(r.codes) + at / 2) = make_uint2(w[0], w[1]);
-      const_cast<uint8_t *>(r.scales)[at / KV4_BLOCK] = (uint8_t)byte;
+      const uint32_t byte = kv4_quantise(reinterpret_cast<float(&)[KV4_BLOCK]>(x[j * KV4_BLOCK]), w, bad);
+      *reinterpret_cast<uint2 *>(codes + at / 2) = make_uint2(w[0], w[1]);
+      scales[at / KV4_BLOCK] = (uint8_t)byte;
     }
     if (bad) report_status(a.status, LLAMA_ERR_RANGE);
+   }
   }
 
-  const int q_units = a.H * per_head;
-  for (int u0 = threadIdx.x; u0 < a.rows * q_units; u0 += KW_THREADS * KW_UNITS) {
+  const int q_units = a.H * per_head, q_rows = KW_THREADS / a.q_lanes;
+  for (int u = threadIdx.x & (a.q_lanes - 1); u < q_units; u += a.q_lanes) {
+   const int head = u / per_head, e = u % per_head * V;
+   const T *const q_first = qkv + ((size_t)t0 * heads + head) * a.D + e;
+   T *const out = q_out + ((size_t)t0 * a.H + head) * a.D + e;
+   for (int r0 = threadIdx.x / a.q_lanes; r0 < a.rows; r0 += KW_UNITS * q_rows) {
     Vec16<T> x[KW_UNITS], y[KW_UNITS];
     float4 cs[KW_UNITS][V / 2];
     int pos[KW_UNITS];
     size_t at[KW_UNITS];
 #pragma unroll
     for (int k = 0; k < KW_UNITS; ++k) {
-      const int uu = u0 + k * KW_THREADS;
-      pos[k] = -2;
-      if (uu >= a.rows * q_units) continue;
-      const int row = uu / q_units, u = uu % q_units;
-      pos[k] = s_pos[row];
+      const int row = r0 + k * q_rows;
+      pos[k] = row < a.rows ? s_pos[row] : -2;
       if (pos[k] == -2) continue;
-      const int head = u / per_head, e = u % per_head * V;
-      const T *src = qkv + ((size_t)(t0 + row) * heads + head) * a.D + e;
-      at[k] = ((size_t)(t0 + row) * a.H + head) * a.D + e;
+      const T *src = q_first + (size_t)row * (heads * a.D);
+      at[k] = (size_t)row * (a.H * a.D);
       x[k].raw = ld_once_after_wait(src);
       y[k].raw = ld_once_after_wait(src + a.D / 2);
       if (pos[k] >= 0) {
@@ -188,9 +204,10 @@ __global__ void __launch_bounds__(KW_THREADS, KW_CTAS)
           }
         }
       }
-      store16(q_out + at[k], p);
-      store16(q_out + at[k] + a.D / 2, q);
+      store16(out + at[k], p);
+      store16(out + at[k] + a.D / 2, q);
     }
+   }
   }
 }
 
@@ -199,12 +216,14 @@ struct KrArgs {
   PackedView b;
   const uint8_t *k, *v;
   int G, D, rows, word_log2;  // words of eight elements of a head: 1 << word_log2
+  int lanes;
   int *status;
 };
 
 template <typename T>
 __global__ void __launch_bounds__(KW_THREADS) kv4_read_kernel(T *k_out, T *v_out, const __grid_constant__ KrArgs a) {
-  __shared__ int s_pos[KW_ROWS], s_page[KW_ROWS];
+  __shared__ int s_pos[KW_ROWS];
+  __shared__ long long s_page[KW_ROWS];
   const int t0 = (int)blockIdx.x * a.rows;
   allow_dependents_launch();
   grid_dependency_wait();
@@ -213,27 +232,32 @@ __global__ void __launch_bounds__(KW_THREADS) kv4_read_kernel(T *k_out, T *v_out
   find_rows(a.pv, a.b, t0, a.rows, INT_MAX, false, s_pos, s_page, a.status);
   __syncthreads();
   const int head_units = a.G << a.word_log2, units = 2 * head_units;  // of a row: k's, then v's
-  for (int u0 = threadIdx.x; u0 < a.rows * units; u0 += KW_THREADS * KR_UNITS) {
+  const int slot_mask = (1 << a.pv.page_log2) - 1, step = KW_THREADS / a.lanes;
+  for (int u = threadIdx.x & (a.lanes - 1); u < units; u += a.lanes) {
+   const bool value = u >= head_units;
+   T *const out = value ? v_out : k_out;
+   if (out == nullptr) continue;
+   const int g = (value ? u - head_units : u) >> a.word_log2, e = u & ((1 << a.word_log2) - 1);
+   const Kv4Row first = kv4_row(value ? a.v : a.k, a.pv, 0, g, a.D, 0);
+   const uint8_t *const codes = first.codes + 4 * e, *const scales = first.scales + e / 2;
+   T *const dst0 = out + ((size_t)t0 * a.G + g) * a.D + e * 8;
+   for (int r0 = threadIdx.x / a.lanes; r0 < a.rows; r0 += KR_UNITS * step) {
     uint32_t w[KR_UNITS], byte[KR_UNITS];
     T *dst[KR_UNITS];
 #pragma unroll
     for (int i = 0; i < KR_UNITS; ++i) {
-      const int uu = u0 + i * KW_THREADS;
+      const int row = r0 + i * step;
       dst[i] = nullptr;
       w[i] = 0x88888888u;  // zeros
       byte[i] = 0;
-      if (uu >= a.rows * units) continue;
-      const int row = uu / units, u = uu % units;
-      if (s_pos[row] == -2) continue;
-      const bool value = u >= head_units;
-      T *out = value ? v_out : k_out;
-      if (out == nullptr) continue;
-      const int g = (value ? u - head_units : u) >> a.word_log2, e = u & ((1 << a.word_log2) - 1);
-      dst[i] = out + ((size_t)(t0 + row) * a.G + g) * a.D + e * 8;
-      if (s_page[row] < 0) continue;
-      const Kv4Row r = kv4_row(value ? a.v : a.k, a.pv, s_page[row], g, a.D, s_pos[row] & ((1 << a.pv.page_log2) - 1));
-      w[i] = (uint32_t)ld_after_wait(reinterpret_cast<const int *>(r.codes) + e);
-      asm volatile("ld.global.u8 %0, [%1];" : "=r"(byte[i]) : "l"(r.scales + e / 2));
+      const int pos = row < a.rows ? s_pos[row] : -2;
+      if (pos == -2) continue;
+      dst[i] = dst0 + (size_t)row * (a.G * a.D);
+      const long long page = s_page[row];
+      if (page < 0) continue;
+      const int slot = pos & slot_mask;
+      w[i] = (uint32_t)ld_after_wait(reinterpret_cast<const int *>(codes + page + slot * kv4_code_bytes(a.D)));
+      asm volatile("ld.global.u8 %0, [%1];" : "=r"(byte[i]) : "l"(scales + page + slot * kv4_scale_bytes(a.D)));
     }
 #pragma unroll
     for (int i = 0; i < KR_UNITS; ++i) {
@@ -246,15 +270,22 @@ __global__ void __launch_bounds__(KW_THREADS) kv4_read_kernel(T *k_out, T *v_out
         reinterpret_cast<float4 *>(dst[i])[1] = kv4_four(w[i], 1, s);
       }
     }
+   }
   }
 }
 
-// Rows of a CTA: one where rows are few, else enough that a thread has several units to move.
-int rows_of(int n_tokens) {
+// Rows of a CTA: one where rows are few, else enough that a thread has several to go through.
+int rows_of(int n_tokens, int most) {
   const int sms = sm_count();
   int rows = 1;
-  while (rows < KW_ROWS && n_tokens / (2 * rows) >= 4 * sms) rows *= 2;
+  while (rows < most && n_tokens / (2 * rows) >= 4 * sms) rows *= 2;
   return rows;
+}
+// Threads side by side in a row of `units`.
+int lanes_of(int units) {
+  int n = 1;
+  while (n < KW_THREADS && n < units) n *= 2;
+  return n;
 }
 
 }  // namespace
@@ -273,7 +304,9 @@ cudaError_t launch_rope_kv4(const T *qkv, T *q_out, uint8_t *k, uint8_t *v, cons
   a.D = D;
   a.halves = halves;
   a.status = status;
-  a.rows = rows_of(b.n_tokens);
+  a.rows = rows_of(b.n_tokens, KW_MOST);
+  a.q_lanes = lanes_of(H * (D / (2 * Vec16<T>::N)));
+  a.kv_lanes = lanes_of(2 * G * (D == 16 ? 1 : D / 32));
   count_launch();
   return launch_pdl(D == 16 ? rope_kv4_kernel<T, 16> : rope_kv4_kernel<T, 32>,
                     dim3((unsigned)((b.n_tokens + a.rows - 1) / a.rows)), dim3(KW_THREADS), 0, st, qkv, q_out, k, v, a);
@@ -292,7 +325,8 @@ cudaError_t launch_kv4_read(const uint8_t *k, const uint8_t *v, T *k_out, T *v_o
   for (a.word_log2 = 0; 8 << a.word_log2 < D; ++a.word_log2) {
   }
   a.status = status;
-  a.rows = rows_of(b.n_tokens);
+  a.rows = rows_of(b.n_tokens, KR_MOST);
+  a.lanes = lanes_of(2 * G * D / 8);
   count_launch();
   return launch_pdl(kv4_read_kernel<T>, dim3((unsigned)((b.n_tokens + a.rows - 1) / a.rows)), dim3(KW_THREADS), 0, st,
                     k_out, v_out, a);

@@ -29,6 +29,12 @@ namespace {
 constexpr int VD_THREADS = 256;
 constexpr int VD_WARPS = VD_THREADS / 32;
 constexpr int VD_VECS = 4;          // 16-byte vectors of a thread in flight
+// CTAs of an SM, and CTAs for an SM that the parts aim at: 265 MB in 47 us, 0.82 of the measured
+// rate (4 and 16: 48; rows left in L2 for the drawing, by loads that do not say that they
+// are the last: 74 to 77 us in all for 71).
+constexpr int VD_CTAS = 6, VD_AIM = 32;
+constexpr int VD_PREFETCH = 32;     // pieces that a CTA asks for
+constexpr int VD_RACE = 2;          // of each of a race's rows
 constexpr int VD_MAX_PARTS = 32;    // of a row: a lane each when they are added up
 constexpr int VD_MIN_PART = 4096;   // logits of a part, at least
 constexpr int VD_MAX_CLUSTER = 8;
@@ -170,10 +176,9 @@ __device__ __forceinline__ void scan_part(const T *x, int V, int part, int parts
 }
 
 template <typename T>
-__global__ void __launch_bounds__(VD_THREADS, 4) verify_rows_kernel(const __grid_constant__ VdArgs a) {
+__global__ void __launch_bounds__(VD_THREADS, VD_CTAS) verify_rows_kernel(const __grid_constant__ VdArgs a) {
   __shared__ float s_m[VD_WARPS], s_z[VD_WARPS];
   __shared__ int s_id[VD_WARPS];
-  __shared__ int s_seq;
   allow_dependents_launch();
   grid_dependency_wait();
   const int part = blockIdx.x % a.parts, side = blockIdx.x / a.parts % 2, row = blockIdx.x / a.parts / 2;
@@ -182,12 +187,7 @@ __global__ void __launch_bounds__(VD_THREADS, 4) verify_rows_kernel(const __grid
   b.q_offsets = a.q_offsets;
   b.n_seqs = a.n_seqs;
   b.n_tokens = a.n_rows;
-  if (warp == 0) {
-    const int i = find_seq(b, row);
-    if (lane == 0) s_seq = i;
-  }
-  __syncthreads();
-  const int seq = s_seq;
+  const int seq = find_seq(b, row);  // (every warp for itself)
   if (seq < 0) return;
   int first, n;
   rows_of(a, seq, first, n);
@@ -251,22 +251,16 @@ __device__ __forceinline__ VdPart row_sum(const VdArgs &a, int row, int side, fl
 }
 __device__ __forceinline__ bool row_ok(float z) { return z > 0.f && z <= FLT_MAX; }
 
-// The best so far of a race; all: of the one without the draft's share, which counts where
-// nothing is left of the other.
+// The best so far of a race; of equals the lowest id.
 struct VdBest {
-  float score, all;
-  int id, all_id;
-  __device__ __forceinline__ void join(float s, int i, float s_all, int i_all) {
+  float score;
+  int id;
+  __device__ __forceinline__ void join(float s, int i) {
     if (s > score || (s == score && i < id)) {
       score = s;
       id = i;
     }
-    if (s_all > all || (s_all == all && i_all < all_id)) {
-      all = s_all;
-      all_id = i_all;
-    }
   }
-  __device__ __forceinline__ int drawn() const { return score > 0.f ? id : all > 0.f ? all_id : -1; }
 };
 
 template <typename T>
@@ -275,7 +269,6 @@ __global__ void __launch_bounds__(VD_THREADS) verify_draw_kernel(const __grid_co
   __shared__ float s_m[2][MOST], s_z[2][MOST];
   __shared__ int s_id[MOST];
   __shared__ bool s_keep[MOST];
-  __shared__ double s_lp[MOST];  // ln p of each draft
   __shared__ VdBest s_best[VD_WARPS];
   __shared__ VdBest s_cta[VD_MAX_CLUSTER];  // of the cluster's first CTA: every CTA's
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
@@ -291,8 +284,16 @@ __global__ void __launch_bounds__(VD_THREADS) verify_draw_kernel(const __grid_co
   int kept = 0, token = -1;
   if (fine && n > 0) {  // the same in every CTA of the cluster
     const bool greedy = t == 0.f;
+    if (!greedy && threadIdx.x < VD_PREFETCH) {
+      // this CTA's share of the noise, which does not wait for the decisions, into L2
+      const int ids = (a.V + VD_PREFETCH * a.cluster - 1) / (VD_PREFETCH * a.cluster);
+      const int from = (rank * VD_PREFETCH + (int)threadIdx.x) * ids, to = min(a.V, from + ids);
+      const uintptr_t p = reinterpret_cast<uintptr_t>(a.noise + (size_t)seq * a.noise_stride);
+      const uintptr_t b0 = (p + 4 * (uintptr_t)from + 15) & ~uintptr_t(15), b1 = (p + 4 * (uintptr_t)max(from, to)) & ~uintptr_t(15);
+      if (b1 > b0)
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(b0), "r"((uint32_t)(b1 - b0)) : "memory");
+    }
     const float c = greedy ? VD_LOG2E : VD_LOG2E / t;
-    const double per_t = greedy ? 1.0 : 1.0 / (double)t;
     for (int k = warp; k < n; k += VD_WARPS) {
       const VdPart p = row_sum(a, first + k, 0, c);
       const bool has_draft = a.draft != nullptr && !greedy && k + 1 < n;
@@ -307,25 +308,29 @@ __global__ void __launch_bounds__(VD_THREADS) verify_draw_kernel(const __grid_co
         if (k + 1 < n) {
           const int x = ld_after_wait(a.tokens + first + k + 1);
           bool keep = false;
-          double lp = 0.0;
           if (x < 0 || x >= a.V) {
             if (rank == 0) report_status(a.status, LLAMA_ERR_RANGE);
           } else if (row_ok(p.z)) {
-            const T *row = reinterpret_cast<const T *>(a.target) + (size_t)(first + k) * a.target_stride;
-            lp = ((double)ld_logit<T>(row + x) - (double)p.m) * per_t - log((double)p.z);
             if (greedy) {
               keep = x == p.id;
             } else {
-              double lq = 0.0;
+              // p / q = e^((x - m) / T - (y - m_q) / T) z_q / z, the exponent in fp64 and what its
+              // fp32 part leaves of it as a factor
+              const T *row = reinterpret_cast<const T *>(a.target) + (size_t)(first + k) * a.target_stride;
+              double d = (double)ld_logit<T>(row + x) - (double)p.m;
+              double z = p.z;
               if (s_z[1][k] > 0.f) {
                 const T *drow = reinterpret_cast<const T *>(a.draft) + (size_t)seq * a.seq_stride + (size_t)k * a.step_stride;
-                lq = ((double)ld_logit<T>(drow + x) - (double)q.m) * per_t - log((double)q.z);
+                d -= (double)ld_logit<T>(drow + x) - (double)q.m;
+                z /= q.z;
               }
-              keep = (double)ld_float_after_wait(a.uniforms + (size_t)seq * a.max_drafts + k) < exp(lp - lq);
+              d /= (double)t;
+              const float hi = (float)d, lo = (float)(d - (double)hi);
+              const double ratio = (double)expf(hi) * (fabsf(hi) <= FLT_MAX ? 1.0 + (double)lo : 1.0);
+              keep = (double)ld_float_after_wait(a.uniforms + (size_t)seq * a.max_drafts + k) * z < ratio;
             }
           }
           s_keep[k] = keep;
-          s_lp[k] = lp;
         }
       }
     }
@@ -343,116 +348,129 @@ __global__ void __launch_bounds__(VD_THREADS) verify_draw_kernel(const __grid_co
                         : nullptr;
       const int banned = refused && !both ? ld_after_wait(a.tokens + first + kept + 1) : -1;
       const float m = s_m[0][kept], mq = s_m[1][kept], inv = 1.f / z, inv_q = both ? 1.f / s_z[1][kept] : 0.f;
-      VdBest best{0.f, 0.f, INT_MAX, INT_MAX};
-      auto race = [&](float fx, float fy, float e, int id) {
-        if (!(e > 0.f)) return;
+      VdBest best{0.f, INT_MAX};
+      // What cannot beat the best so far is found without a division: `bar` is a little below it.
+      float bar = 0.f;
+      auto race = [&](float fx, float fy, float e, int id, bool residual) {
         const float p = ptx::ex2_approx((fx - m) * c) * inv;
         float w = p;
-        if (both) w = fmaxf(p - ptx::ex2_approx((fy - mq) * c) * inv_q, 0.f);
-        if (id == banned) w = 0.f;
-        // (0 does not win: ids start behind every other)
-        const float s = w / e, s_all = p / e;
-        if (s > best.score) {
-          best.score = s;
-          best.id = id;
-        }
-        if (s_all > best.all) {
-          best.all = s_all;
-          best.all_id = id;
+        if (residual && both) w = p - ptx::ex2_approx((fy - mq) * c) * inv_q;
+        if (residual && id == banned) w = 0.f;
+        if (w > bar * e && e > 0.f) {  // (0 does not win: ids start behind every other)
+          const float s = w / e;
+          if (s > best.score) {
+            best.score = s;
+            best.id = id;
+            bar = s * (1.f - 0x1p-21f);
+          }
         }
       };
       constexpr int N = Vec16<T>::N;
       const bool whole = ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(noise) |
                            reinterpret_cast<uintptr_t>(y)) & 15) == 0;
       const int stride = a.cluster * VD_THREADS, me = rank * VD_THREADS + (int)threadIdx.x;
-      int done = 0;  // ids below are searched by whole vectors
-      if (whole) {
-        const int n_vec = a.V / N;
-        done = n_vec * N;
-        for (int v = me; v < n_vec; v += 2 * stride) {
-          Vec16<T> fx[2], fy[2];
-          float4 e[2][N / 4];
+      auto search = [&](bool residual) {
+        int done = 0;  // ids below are searched by whole vectors
+        if (whole) {
+          const int n_vec = a.V / N;
+          done = n_vec * N;
+          for (int v = me; v < n_vec; v += VD_RACE * stride) {
+            Vec16<T> fx[VD_RACE], fy[VD_RACE];
+            float4 e[VD_RACE][N / 4];
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const int at = v + k * stride;
-            if (at >= n_vec) continue;
-            fx[k] = load16<T>(x + (size_t)at * N);
-            if (both) fy[k] = load16<T>(y + (size_t)at * N);
+            for (int k = 0; k < VD_RACE; ++k) {
+              const int at = v + k * stride;
+              if (at >= n_vec) continue;
+              fx[k].raw = ld_once_after_wait(x + (size_t)at * N);
+              if (both) fy[k].raw = ld_once_after_wait(y + (size_t)at * N);
 #pragma unroll
-            for (int i = 0; i < N / 4; ++i) {
-              const uint4 u = ld_once_after_wait(noise + (size_t)at * N + 4 * i);
-              e[k][i] = *reinterpret_cast<const float4 *>(&u);
+              for (int i = 0; i < N / 4; ++i) {
+                const uint4 u = ld_once_after_wait(noise + (size_t)at * N + 4 * i);
+                e[k][i] = *reinterpret_cast<const float4 *>(&u);
+              }
+            }
+#pragma unroll
+            for (int k = 0; k < VD_RACE; ++k) {
+              const int at = v + k * stride;
+              if (at >= n_vec) continue;
+#pragma unroll
+              for (int i = 0; i < N; ++i)
+                race(fx[k].get(i), both ? fy[k].get(i) : 0.f, reinterpret_cast<const float *>(e[k])[i], at * N + i, residual);
             }
           }
+        }
+        for (int v = done + me; v < a.V; v += 8 * stride) {
+          float fx[8], fy[8], e[8];
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
+          for (int k = 0; k < 8; ++k) {
             const int at = v + k * stride;
-            if (at >= n_vec) continue;
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-              race(fx[k].get(i), both ? fy[k].get(i) : 0.f, reinterpret_cast<const float *>(e[k])[i], at * N + i);
+            e[k] = 0.f;
+            if (at >= a.V) continue;
+            fx[k] = ld_logit<T>(x + at);
+            fy[k] = both ? ld_logit<T>(y + at) : 0.f;
+            e[k] = ld_float_after_wait(noise + at);
           }
-        }
-      }
-      for (int v = done + me; v < a.V; v += 4 * stride) {
-        float fx[4], fy[4], e[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int at = v + k * stride;
-          e[k] = 0.f;
-          if (at >= a.V) continue;
-          fx[k] = ld_logit<T>(x + at);
-          fy[k] = both ? ld_logit<T>(y + at) : 0.f;
-          e[k] = ld_float_after_wait(noise + at);
+          for (int k = 0; k < 8; ++k)
+            if (e[k] > 0.f) race(fx[k], fy[k], e[k], v + k * stride, residual);
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          if (e[k] > 0.f) race(fx[k], fy[k], e[k], v + k * stride);
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        const float s = __shfl_xor_sync(0xffffffffu, best.score, o), sa = __shfl_xor_sync(0xffffffffu, best.all, o);
-        const int i = __shfl_xor_sync(0xffffffffu, best.id, o), ia = __shfl_xor_sync(0xffffffffu, best.all_id, o);
-        best.join(s, i, sa, ia);
-      }
-      if (lane == 0) s_best[warp] = best;
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        for (int w = 1; w < VD_WARPS; ++w) best.join(s_best[w].score, s_best[w].id, s_best[w].all, s_best[w].all_id);
-        // into the first CTA's array, through distributed shared memory
-        uint32_t dst = ptx::smem_u32(&s_cta[rank]);
-        if (a.cluster > 1) dst = ptx::mapa_shared(dst, 0);
-        if (a.cluster > 1) {
+        for (int o = 16; o > 0; o >>= 1) {
+          const float s = __shfl_xor_sync(0xffffffffu, best.score, o);
+          const int i = __shfl_xor_sync(0xffffffffu, best.id, o);
+          best.join(s, i);
+        }
+        if (lane == 0) s_best[warp] = best;
+        __syncthreads();
+        if (threadIdx.x == 0)
+          for (int w = 1; w < VD_WARPS; ++w) best.join(s_best[w].score, s_best[w].id);
+        __syncthreads();
+      };
+      // the CTA's best into the first CTA's array, through distributed shared memory
+      auto meet = [&] {
+        if (a.cluster > 1) ptx::cluster_sync();
+        else __syncthreads();
+      };
+      auto publish = [&] {
+        if (threadIdx.x == 0) {
+          uint32_t dst = ptx::smem_u32(&s_cta[rank]);
+          if (a.cluster > 1) dst = ptx::mapa_shared(dst, 0);
           ptx::st_cluster_u32(dst, __float_as_uint(best.score));
-          ptx::st_cluster_u32(dst + 4, __float_as_uint(best.all));
-          ptx::st_cluster_u32(dst + 8, (uint32_t)best.id);
-          ptx::st_cluster_u32(dst + 12, (uint32_t)best.all_id);
-        } else {
-          s_cta[0] = best;
+          ptx::st_cluster_u32(dst + 4, (uint32_t)best.id);
         }
+        meet();
+      };
+      search(true);
+      publish();
+      if (refused) {  // (in every CTA of the cluster alike)
+        float top = 0.f;
+        for (int k = 0; k < a.cluster; ++k) {
+          uint32_t src = ptx::smem_u32(&s_cta[k]);
+          if (a.cluster > 1) src = ptx::mapa_shared(src, 0);
+          top = fmaxf(top, ptx::ld_cluster_f32(src));
+        }
+        meet();
+        if (top == 0.f) {  // nothing of p - q is left: from p
+          search(false);
+          publish();
+        }
+      }
+      if (rank == 0) {
+        VdBest all = s_cta[0];
+        for (int k = 1; k < a.cluster; ++k) all.join(s_cta[k].score, s_cta[k].id);
+        token = all.score > 0.f ? all.id : -1;
       }
     }
   }
-  if (a.cluster > 1) ptx::cluster_sync();
   if (rank != 0) return;
-  __syncthreads();
-  const bool drawing = fine && n > 0 && t != 0.f && row_ok(s_z[0][kept]);
-  if (drawing) {
-    VdBest best = s_cta[0];
-    for (int k = 1; k < a.cluster; ++k) best.join(s_cta[k].score, s_cta[k].id, s_cta[k].all, s_cta[k].all_id);
-    token = best.drawn();
-  }
   for (int k = threadIdx.x; k < width; k += VD_THREADS) {
     int x = -1;
     float lp = 0.f;
-    if (k < kept) {
-      x = ld_after_wait(a.tokens + first + k + 1);
-      lp = (float)s_lp[k];
-    } else if (k == kept && token >= 0) {
-      x = token;
-      const T *row = reinterpret_cast<const T *>(a.target) + (size_t)(first + kept) * a.target_stride;
-      lp = (float)(((double)ld_logit<T>(row + x) - (double)s_m[0][kept]) * (t == 0.f ? 1.0 : 1.0 / (double)t) -
-                   log((double)s_z[0][kept]));
+    if (k < kept) x = ld_after_wait(a.tokens + first + k + 1);
+    else if (k == kept) x = token;
+    if (x >= 0 && a.logprobs != nullptr) {
+      const T *row = reinterpret_cast<const T *>(a.target) + (size_t)(first + k) * a.target_stride;
+      lp = (ld_logit<T>(row + x) - s_m[0][k]) / (t == 0.f ? 1.f : t) - logf(s_z[0][k]);
     }
     a.out_tokens[(size_t)seq * width + k] = x;
     if (a.logprobs != nullptr) a.logprobs[(size_t)seq * width + k] = lp;
@@ -463,7 +481,7 @@ __global__ void __launch_bounds__(VD_THREADS) verify_draw_kernel(const __grid_co
 // Parts of a row: enough CTAs to fill the GPU several times over, none with less than
 // VD_MIN_PART logits.
 int parts_of(int n_rows, int V) {
-  const long long aim = 16LL * sm_count(), want = (aim + 2LL * n_rows - 1) / (2LL * n_rows);
+  const long long aim = (long long)VD_AIM * sm_count(), want = (aim + 2LL * n_rows - 1) / (2LL * n_rows);
   const int most = V / VD_MIN_PART < VD_MAX_PARTS ? V / VD_MIN_PART : VD_MAX_PARTS;
   return want < most ? (int)want : most > 1 ? most : 1;
 }
