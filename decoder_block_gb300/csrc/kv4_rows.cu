@@ -62,7 +62,8 @@ struct KdLayout {
   static constexpr int RING = STAGES * STAGE > PART ? STAGES * STAGE : PART;  // of a warp; its last part at the end
   static constexpr int OFF_PART = WARPS * RING;   // of each warp, its first
   static constexpr int OFF_META = OFF_PART + WARPS * PART;
-  static constexpr int OFF_SUMS = OFF_META + WARPS * 2 * 16;
+  static constexpr int OFF_CHAINS = OFF_META + WARPS * 2 * 16;
+  static constexpr int OFF_SUMS = OFF_CHAINS + WARPS * 2 * 32;
   // tiles before sequence i: of one item with a row each, else of its items for one KV head
   static constexpr int OFF_FIRST = OFF_SUMS + 128;
   static int bytes(int n_seqs) { return OFF_FIRST + (n_seqs + 1) * 4; }
@@ -90,6 +91,13 @@ struct KdArgs {
 struct KdMeta {
   int seq, unit;  // seq -1: none
   int j0, j1;
+};
+
+// Pieces of one item, in order, and what their join needs to know of it.
+struct KdChain {
+  unsigned pieces;
+  int first, g, r0, nr, before;
+  int part;  // of the workspace: 0, 1; -1: the whole item is there
 };
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -143,6 +151,16 @@ __device__ __forceinline__ SeqSpan kd_span(const KdArgs &a, int i) {
   return SeqSpan{i, 1, checked_len(ld_after_wait(a.b.kv_lens + i), a.b.max_kv_len, a.pv)};
 }
 __device__ __forceinline__ int kd_tiles(int keys) { return (keys + KD_KEYS - 1) / KD_KEYS; }
+
+// Token and head in the group of an item's row, without a division for each: the item's first
+// row has been divided, and what is left is small (fp32 is exact to half a step there).
+struct KdRows {
+  int token0, head0;
+  float inv;
+  __device__ __forceinline__ KdRows(int r0, int r) : token0(r0 / r), head0(r0 - r0 / r * r), inv(1.f / (float)r) {}
+  __device__ __forceinline__ int token(int h) const { return token0 + (int)(((float)(head0 + h) + 0.5f) * inv); }
+  __device__ __forceinline__ int head(int h, int r) const { return head0 + h - (token(h) - token0) * r; }
+};
 
 // A place in the row of tiles.  A unit is a KV head and a block of 8 NB rows.
 template <int NB>
@@ -198,6 +216,8 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_rows_kerne
   int *first = reinterpret_cast<int *>(smem + L::OFF_FIRST);
   int *sums = reinterpret_cast<int *>(smem + L::OFF_SUMS);
   KdMeta *meta = reinterpret_cast<KdMeta *>(smem + L::OFF_META);
+  KdChain *chains = reinterpret_cast<KdChain *>(smem + L::OFF_CHAINS);
+  static_assert(sizeof(KdChain) <= 32, "a chain fits its place");
   const uint32_t ring = s0 + warp * L::RING;
   allow_dependents_launch();
   if (lane < 2) meta[warp * 2 + lane].seq = -1;
@@ -301,9 +321,10 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_rows_kerne
       // the item's queries, a line each: they are loaded when its first tile is there
       const int r0 = ahead.sub * (8 * NB), nr = min(8 * NB, ahead.s.count * a.r - r0);
       constexpr int LINES = D >= 64 ? D / 64 : 1;
+      const KdRows rows(r0, a.r);
       for (int i = lane; i < nr * LINES; i += 32) {
-        const int R = r0 + i / LINES;
-        const bf16 *row = a.q + ((size_t)(ahead.s.first + R / a.r) * a.H + ahead.g * a.r + R % a.r) * D;
+        const int h = i / LINES;
+        const bf16 *row = a.q + ((size_t)(ahead.s.first + rows.token(h)) * a.H + ahead.g * a.r + rows.head(h, a.r)) * D;
         asm volatile("prefetch.global.L1 [%0];" ::"l"(row + i % LINES * 64));
       }
       from_s = (lane < 16 ? a.k : a.v) + block + (L::RB << a.pv.page_log2) + s_lane % L::SB * 16;
@@ -375,14 +396,15 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_rows_kerne
       const int j1 = min(n_tiles, j0 + todo - done);
       const int r0 = at.sub * (8 * NB), nr = min(8 * NB, at.s.count * a.r - r0);
       const int before = at.s.kv_len - at.s.count + 1;  // keys that the sequence's first new token sees
-      // row R of the sequence in q and o
-      auto row_at = [&](int R) { return (size_t)(at.s.first + R / a.r) * a.H + g * a.r + R % a.r; };
+      const KdRows rows(r0, a.r);
+      // row h of the item in q and o
+      auto row_at = [&](int h) { return (size_t)(at.s.first + rows.token(h)) * a.H + g * a.r + rows.head(h, a.r); };
       uint32_t qf[NB][STEPS][2];
       int sees[NB][2];  // keys that this thread's columns of S^T see
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         const int h = b * 8 + gi;
-        const int *src = reinterpret_cast<const int *>(a.q + row_at(r0 + min(h, nr - 1)) * D + ti * (D / 4));
+        const int *src = reinterpret_cast<const int *>(a.q + row_at(min(h, nr - 1)) * D + ti * (D / 4));
 #pragma unroll
         for (int s = 0; s < STEPS; ++s) {
           if constexpr (STEPS >= 2) {
@@ -399,9 +421,9 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_rows_kerne
           }
         }
 #pragma unroll
-        for (int e = 0; e < 2; ++e) sees[b][e] = before + (r0 + min(b * 8 + ti * 2 + e, nr - 1)) / a.r;
+        for (int e = 0; e < 2; ++e) sees[b][e] = before + rows.token(min(b * 8 + ti * 2 + e, nr - 1));
       }
-      const int all_see = before + r0 / a.r;
+      const int all_see = before + rows.token0;
       float acc[NB][STEPS][4], m[NB][2], l[NB][2];
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
@@ -421,46 +443,46 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_rows_kerne
         const uint32_t sk = ring + use * L::STAGE, sv = sk + L::HALF;
         // scores: keys gi and gi + 8 of both halves of the tile
         float sc[2][NB][4];
+        uint32_t w[4][KW];
+        Kv4Scale sa[4], sb[4];
 #pragma unroll
-        for (int mb = 0; mb < 2; ++mb) {
+        for (int e = 0; e < 4; ++e) {
+          const int row = e * 8 + gi;
+          const uint32_t scales = sk + KD_KEYS * L::RB + row * L::SB;
+          if constexpr (D >= 32) ld_words<KW>(sk + row * L::RB + ti * (D / 8), w[e]);
+          else ld_words<KW>(sk + row * L::RB + ti / 2 * 4, w[e]);
+          if constexpr (D == 16) w[e][0] >>= 8 * (ti & 1);
+          if constexpr (D == 128) {
+            uint16_t x;
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(scales + ti * 2));
+            sa[e] = kv4_scales((uint32_t)x & 255);
+            sb[e] = kv4_scales((uint32_t)x >> 8);
+          } else {
+            sa[e] = kv4_scales(ld_byte(scales + (D == 64 ? ti : D == 32 ? ti / 2 : 0)));
+            sb[e] = sa[e];
+          }
+        }
+#pragma unroll
+        for (int mb = 0; mb < 2; ++mb)
 #pragma unroll
           for (int b = 0; b < NB; ++b)
 #pragma unroll
             for (int e = 0; e < 4; ++e) sc[mb][b][e] = 0.f;
-          uint32_t w[2][KW];
-          Kv4Scale sa[2], sb[2];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int row = mb * 16 + e * 8 + gi;
-            const uint32_t scales = sk + KD_KEYS * L::RB + row * L::SB;
-            if constexpr (D >= 32) ld_words<KW>(sk + row * L::RB + ti * (D / 8), w[e]);
-            else ld_words<KW>(sk + row * L::RB + ti / 2 * 4, w[e]);
-            if constexpr (D == 16) w[e][0] >>= 8 * (ti & 1);
-            if constexpr (D == 128) {
-              uint16_t x;
-              asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(scales + ti * 2));
-              sa[e] = kv4_scales((uint32_t)x & 255);
-              sb[e] = kv4_scales((uint32_t)x >> 8);
-            } else {
-              sa[e] = kv4_scales(ld_byte(scales + (D == 64 ? ti : D == 32 ? ti / 2 : 0)));
-              sb[e] = sa[e];
-            }
-          }
+        for (int s = 0; s < STEPS; ++s)
 #pragma unroll
-          for (int s = 0; s < STEPS; ++s) {
-            // elements 4 s .. 4 s + 3 of the thread's; 16 of them share a scale
+          for (int mb = 0; mb < 2; ++mb) {
             uint32_t f[4];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const uint32_t word = w[e][s / 2];
-              const Kv4Scale &k = s < 4 ? sa[e] : sb[e];
+              const uint32_t word = w[2 * mb + e][s / 2];
+              const Kv4Scale &k = s < 4 ? sa[2 * mb + e] : sb[2 * mb + e];
               f[e] = s % 2 == 0 ? kv4_pair<0>(word, k) : kv4_pair<2>(word, k);
               f[2 + e] = s % 2 == 0 ? kv4_pair<1>(word, k) : kv4_pair<3>(word, k);
             }
 #pragma unroll
             for (int b = 0; b < NB; ++b) mma16816(sc[mb][b], f, qf[b][s][0], qf[b][s][1]);
           }
-        }
         if ((j + 1) * KD_KEYS > all_see) {
           const int key = j * KD_KEYS + gi;
 #pragma unroll
@@ -572,7 +594,7 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_rows_kerne
             const int h = b * 8 + ti * 2 + e;
             if (h >= nr || sees[b][e] <= 0) continue;
             const float inv = KD_VALUE / l[b][e];  // scores of NaN or -inf alone: NaN
-            uint32_t *dst = reinterpret_cast<uint32_t *>(a.o + row_at(r0 + h) * D + gi * (D / 8));
+            uint32_t *dst = reinterpret_cast<uint32_t *>(a.o + row_at(h) * D + gi * (D / 8));
 #pragma unroll
             for (int i = 0; i < STEPS; ++i) dst[i] = kd_pack2(acc[b][i][e] * inv, acc[b][i][e + 2] * inv);
           }
@@ -588,13 +610,14 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_rows_kerne
         for (int b = 0; b < NB; ++b)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int h = b * 8 + ti * 2 + e;
+            // in the order of the fragments: a warp's stores are whole
 #pragma unroll
             for (int i = 0; i < STEPS; ++i)
-              *reinterpret_cast<float2 *>(p + h * D + gi * (D / 8) + 2 * i) = make_float2(acc[b][i][e], acc[b][i][e + 2]);
+              *reinterpret_cast<float2 *>(p + ((b * 2 + e) * STEPS + i) * 64 + lane * 2) =
+                  make_float2(acc[b][i][e], acc[b][i][e + 2]);
             if (gi == 0) {
-              p[8 * NB * D + h] = m[b][e];
-              p[8 * NB * (D + 1) + h] = l[b][e];
+              p[8 * NB * D + b * 8 + ti * 2 + e] = m[b][e];
+              p[8 * NB * (D + 1) + b * 8 + ti * 2 + e] = l[b][e];
             }
           }
         if (lane == 0) meta[warp * 2 + which] = KdMeta{seq, unit, j0, j1};
@@ -620,68 +643,78 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_rows_kerne
   const int prev_seq = __shfl_sync(0xffffffffu, mine.seq, prev), prev_unit = __shfl_sync(0xffffffffu, mine.unit, prev);
   const bool joined = prev != lane && prev_seq == mine.seq && prev_unit == mine.unit;
   const unsigned starts = __ballot_sync(0xffffffffu, mine.seq >= 0 && !joined);
-  // A warp for each chain and row: a lane for each piece's m and l, then for each two columns.
-  const int rows = a.b.q_offsets != nullptr ? 8 * NB : min(8 * NB, a.r);
-  for (int u = warp; u < __popc(starts) * rows; u += L::WARPS) {
-    const int c = __fns(starts, 0, u / rows + 1), h = u % rows;
-    const unsigned later = starts & ~((2u << c) - 1u);
-    const unsigned chain = there & (later != 0 ? (1u << (__ffs(later) - 1)) - 1u : 0xffffffffu) & ~((1u << c) - 1u);
-    const int head_j0 = __shfl_sync(0xffffffffu, mine.j0, c), end = __shfl_sync(0xffffffffu, mine.j1, 31 - __clz(chain));
+  if (warp == 0 && (starts >> lane & 1)) {  // a lane for each chain
+    const unsigned later = starts & ~((2u << lane) - 1u);
+    const unsigned chain = there & (later != 0 ? (1u << (__ffs(later) - 1)) - 1u : 0xffffffffu) & ~((1u << lane) - 1u);
     KdCursor<NB> it;
-    it.set(a, __shfl_sync(0xffffffffu, mine.seq, c), __shfl_sync(0xffffffffu, mine.unit, c), 0);
-    const int R = it.sub * (8 * NB) + h, i = R / a.r;
-    if (R >= it.s.count * a.r) continue;
-    const bool whole = head_j0 == 0 && end == it.n, in = chain >> lane & 1;
+    it.set(a, mine.seq, mine.unit, 0);
+    const int end = meta[31 - __clz(chain)].j1;
+    KdChain k;
+    k.pieces = chain;
+    k.first = it.s.first;
+    k.g = it.g;
+    k.r0 = it.sub * (8 * NB);
+    k.nr = min(8 * NB, it.s.count * a.r - k.r0);
+    k.before = it.s.kv_len - it.s.count + 1;
+    k.part = mine.j0 == 0 && end == it.n ? -1 : mine.j0 == 0 ? 1 : 0;
+    chains[__popc(starts & ((1u << lane) - 1u))] = k;
+    if (a.spans != nullptr && later == 0) {  // the CTA's last item: it may begin it and not end it
+      const long long item_end = (long long)first[it.seq] * a.times + (long long)(it.unit + 1) * it.n;
+      const int c1 = (int)min((item_end - 1) / each, (long long)gridDim.x - 1);
+      a.spans[blockIdx.x] = k.part == 1 ? make_int4(it.seq, it.unit, c1, 0) : make_int4(-1, 0, 0, 0);
+    }
+  }
+  if (a.spans != nullptr && starts == 0 && threadIdx.x == 0) a.spans[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  __syncthreads();
+  // A warp for each chain and row: a lane for each piece's m and l, then for each two columns.
+  const int most_rows = a.b.q_offsets != nullptr ? 8 * NB : min(8 * NB, a.r);
+  for (int u = warp; u < __popc(starts) * most_rows; u += L::WARPS) {
+    const KdChain &k = chains[u / most_rows];
+    const int h = u % most_rows;
+    if (h >= k.nr) continue;
+    const unsigned chain = k.pieces;
+    const bool in = chain >> lane & 1;
     const float m = in ? piece(lane)[8 * NB * D + h] : -FLT_MAX, top = warp_max(m);
     const float f = in ? ptx::ex2_approx(m - top) : 0.f;
     const float l = warp_sum(in ? f * piece(lane)[8 * NB * (D + 1) + h] : 0.f);
-    float2 x[D > 64 ? D / 64 : 1];
+    // columns c (D / 8) + 2 i of c = lane % 8, i = lane / 8 and every fourth from there
+    constexpr int MINE = STEPS > 4 ? STEPS / 4 : 1;
+    const int c = lane & 7, i0 = lane / 8;
+    const int from = ((h / 8 * 2 + (h & 1)) * STEPS + i0) * 64 + (c * 4 + (h & 7) / 2) * 2;
+    float2 x[MINE];
 #pragma unroll
-    for (int e = 0; e < (D > 64 ? D / 64 : 1); ++e) x[e] = make_float2(0.f, 0.f);
+    for (int e = 0; e < MINE; ++e) x[e] = make_float2(0.f, 0.f);
     for (unsigned left = chain; left != 0; left &= left - 1) {
       const int s = __ffs(left) - 1;
-      const float g = __shfl_sync(0xffffffffu, f, s);
-      const float *p = piece(s) + h * D + 2 * lane;
-      if (2 * lane < D) {
+      const float w = __shfl_sync(0xffffffffu, f, s);
+      const float *p = piece(s) + from;
+      if (i0 < STEPS) {
 #pragma unroll
-        for (int e = 0; e < (D > 64 ? D / 64 : 1); ++e) {
-          const float2 v = *reinterpret_cast<const float2 *>(p + 64 * e);
-          x[e].x = fmaf(g, v.x, x[e].x);
-          x[e].y = fmaf(g, v.y, x[e].y);
+        for (int e = 0; e < MINE; ++e) {
+          const float2 v = *reinterpret_cast<const float2 *>(p + e * 256);
+          x[e].x = fmaf(w, v.x, x[e].x);
+          x[e].y = fmaf(w, v.y, x[e].y);
         }
       }
     }
-    if (2 * lane >= D) continue;
-    if (!whole) {
-      float *out = a.part + ((size_t)blockIdx.x * 2 + (head_j0 == 0 ? 1 : 0)) * (8 * NB * (D + 2));
+    if (i0 >= STEPS) continue;
+    const int column = c * (D / 8) + 2 * i0;
+    if (k.part >= 0) {
+      float *out = a.part + ((size_t)blockIdx.x * 2 + k.part) * (8 * NB * (D + 2));
 #pragma unroll
-      for (int e = 0; e < (D > 64 ? D / 64 : 1); ++e)
-        *reinterpret_cast<float2 *>(out + h * D + 64 * e + 2 * lane) = x[e];
+      for (int e = 0; e < MINE; ++e) *reinterpret_cast<float2 *>(out + h * D + column + 8 * e) = x[e];
       if (lane == 0) {
         out[8 * NB * D + h] = top;
         out[8 * NB * (D + 1) + h] = l;
       }
-    } else if (it.s.kv_len - it.s.count + i >= 0) {
+    } else {
+      const int i = (k.r0 + h) / a.r;
+      if (k.before + i <= 0) continue;
       const float inv = KD_VALUE / l;
-      bf16 *dst = a.o + ((size_t)(it.s.first + i) * a.H + it.g * a.r + R % a.r) * D + 2 * lane;
+      bf16 *dst = a.o + ((size_t)(k.first + i) * a.H + k.g * a.r + (k.r0 + h - i * a.r)) * D + column;
 #pragma unroll
-      for (int e = 0; e < (D > 64 ? D / 64 : 1); ++e)
-        *reinterpret_cast<uint32_t *>(dst + 64 * e) = kd_pack2(x[e].x * inv, x[e].y * inv);
+      for (int e = 0; e < MINE; ++e) *reinterpret_cast<uint32_t *>(dst + 8 * e) = kd_pack2(x[e].x * inv, x[e].y * inv);
     }
-  }
-  if (a.spans != nullptr && warp == 0) {  // the item that this CTA begins and does not end is its last one
-    int4 span = make_int4(-1, 0, 0, 0);
-    if (starts != 0) {
-      const int c = 31 - __clz(starts);
-      KdCursor<NB> it;
-      it.set(a, __shfl_sync(0xffffffffu, mine.seq, c), __shfl_sync(0xffffffffu, mine.unit, c), 0);
-      const int j0 = __shfl_sync(0xffffffffu, mine.j0, c), end = __shfl_sync(0xffffffffu, mine.j1, 31 - __clz(there));
-      if (j0 == 0 && end < it.n) {
-        const long long item_end = (long long)first[it.seq] * a.times + (long long)(it.unit + 1) * it.n;
-        span = make_int4(it.seq, it.unit, (int)min((item_end - 1) / each, (long long)gridDim.x - 1), 0);
-      }
-    }
-    if (lane == 0) a.spans[blockIdx.x] = span;
   }
 }
 
