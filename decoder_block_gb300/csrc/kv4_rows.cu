@@ -62,8 +62,7 @@ struct KdLayout {
   static constexpr int RING = STAGES * STAGE > PART ? STAGES * STAGE : PART;  // of a warp; its last part at the end
   static constexpr int OFF_PART = WARPS * RING;   // of each warp, its first
   static constexpr int OFF_META = OFF_PART + WARPS * PART;
-  static constexpr int OFF_CHAINS = OFF_META + WARPS * 2 * 16;
-  static constexpr int OFF_SUMS = OFF_CHAINS + WARPS * 2 * 32;
+  static constexpr int OFF_SUMS = OFF_META + WARPS * 2 * 48;
   // tiles before sequence i: of one item with a row each, else of its items for one KV head
   static constexpr int OFF_FIRST = OFF_SUMS + 128;
   static int bytes(int n_seqs) { return OFF_FIRST + (n_seqs + 1) * 4; }
@@ -87,17 +86,80 @@ struct KdArgs {
   int *status;
 };
 
+__device__ __forceinline__ uint32_t kd_pack2(float a, float b) {
+  __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<uint32_t *>(&h);
+}
+// N words side by side.
+template <int N>
+__device__ __forceinline__ void kd_store(uint32_t *dst, const uint32_t (&w)[N]) {
+  if constexpr (N >= 4) {
+#pragma unroll
+    for (int i = 0; i < N; i += 4) *reinterpret_cast<uint4 *>(dst + i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+  } else if constexpr (N == 2) {
+    *reinterpret_cast<uint2 *>(dst) = make_uint2(w[0], w[1]);
+  } else {
+    dst[0] = w[0];
+  }
+}
 // A piece of an item that a warp leaves for its CTA to join.
-struct KdMeta {
+struct __align__(16) KdMeta {
   int seq, unit;  // seq -1: none
-  int j0, j1;
+  int j0, j1, n;  // its key tiles, and all of the item's
+  int first, count, kv_len;  // of the sequence
+  int g, r0;
+  int pad[2];
 };
 
-// Pieces of one item, in order, and what their join needs to know of it.
-struct KdChain {
-  unsigned pieces;
+// An item as its join has it: its rows in o, and the keys that the sequence's first token sees.
+struct KdOut {
   int first, g, r0, nr, before;
-  int part;  // of the workspace: 0, 1; -1: the whole item is there
+  __device__ __forceinline__ KdOut(const KdArgs &a, int first_, int count, int kv_len, int g_, int r0_, int most)
+      : first(first_), g(g_), r0(r0_), nr(min(most, count * a.r - r0_)), before(kv_len - count + 1) {}
+};
+
+// Sums of a fragment's columns -- steps i of rows 8 b + 2 ti + e, a float2 of each lane -- over
+// the pieces piece(0) .. piece(n - 1), in that order.  SPLIT: warps that share the steps.
+template <int D, int NB, int SPLIT>
+struct KdSum {
+  static constexpr int STEPS = D / 16 / SPLIT;
+  int i0;  // the first of the steps
+  float2 x[STEPS];
+  float top = -FLT_MAX, l = 0.f;
+  template <typename F>
+  __device__ __forceinline__ KdSum(int be, int part, int n, F &&piece) : i0(part * STEPS) {
+    const int lane = threadIdx.x & 31, h = be / 2 * 8 + (lane & 3) * 2 + (be & 1);
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) x[i] = make_float2(0.f, 0.f);
+#pragma unroll 16
+    for (int s = 0; s < n; ++s) top = fmaxf(top, piece(s)[8 * NB * D + h]);
+#pragma unroll(SPLIT > 1 ? 8 : 4)
+    for (int s = 0; s < n; ++s) {
+      const float *p = piece(s);
+      const float f = ptx::ex2_approx(p[8 * NB * D + h] - top);
+      l = fmaf(f, p[8 * NB * (D + 1) + h], l);
+#pragma unroll
+      for (int i = 0; i < STEPS; ++i) {
+        const float2 v = *reinterpret_cast<const float2 *>(p + (be * (D / 16) + i0 + i) * 64 + lane * 2);
+        x[i].x = fmaf(f, v.x, x[i].x);
+        x[i].y = fmaf(f, v.y, x[i].y);
+      }
+    }
+  }
+  // The rows' outputs: a lane has D / 8 columns of its own.
+  __device__ __forceinline__ void store(const KdArgs &a, const KdOut &k, int be) const {
+    const int lane = threadIdx.x & 31, h = be / 2 * 8 + (lane & 3) * 2 + (be & 1);
+    if (h >= k.nr) return;
+    const int i = (k.r0 + h) / a.r;
+    if (k.before + i <= 0) return;  // it sees nothing
+    const float inv = KD_VALUE / l;
+    uint32_t *dst = reinterpret_cast<uint32_t *>(
+        a.o + ((size_t)(k.first + i) * a.H + k.g * a.r + (k.r0 + h - i * a.r)) * D + lane / 4 * (D / 8) + 2 * i0);
+    uint32_t w[STEPS];
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) w[i] = kd_pack2(x[i].x * inv, x[i].y * inv);
+    kd_store<STEPS>(dst, w);
+  }
 };
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -114,10 +176,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
-}
-__device__ __forceinline__ uint32_t kd_pack2(float a, float b) {
-  __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<uint32_t *>(&h);
 }
 __device__ __forceinline__ uint32_t kd_pack_half2(float a, float b) {
   __half2 h = __floats2half2_rn(a, b);
@@ -185,9 +243,15 @@ struct KdCursor {
       if ((long long)first[mid] * a.times <= at) lo = mid;
       else hi = mid;
     }
-    set(a, lo, 0, 0);
     const long long rest = at - (long long)first[lo] * a.times;
-    set(a, lo, (int)(rest / n), (int)(rest % n));
+    set(a, lo, 0, 0);
+    // (a 64-bit division takes some hundred cycles)
+    const int u = rest <= 0x7fffffffLL ? (int)rest / n : (int)(rest / n);
+    const int subs = units / a.G;
+    unit = u;
+    g = u / subs;
+    sub = u - g * subs;
+    j = (int)(rest - (long long)u * n);
   }
   __device__ __forceinline__ bool next(const KdArgs &a, const int *first) {  // true: it is another item's
     if (++j < n || a.direct) return false;
@@ -216,8 +280,7 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_rows_kerne
   int *first = reinterpret_cast<int *>(smem + L::OFF_FIRST);
   int *sums = reinterpret_cast<int *>(smem + L::OFF_SUMS);
   KdMeta *meta = reinterpret_cast<KdMeta *>(smem + L::OFF_META);
-  KdChain *chains = reinterpret_cast<KdChain *>(smem + L::OFF_CHAINS);
-  static_assert(sizeof(KdChain) <= 32, "a chain fits its place");
+  static_assert(sizeof(KdMeta) == 48, "a piece's place");
   const uint32_t ring = s0 + warp * L::RING;
   allow_dependents_launch();
   if (lane < 2) meta[warp * 2 + lane].seq = -1;
@@ -594,9 +657,10 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_rows_kerne
             const int h = b * 8 + ti * 2 + e;
             if (h >= nr || sees[b][e] <= 0) continue;
             const float inv = KD_VALUE / l[b][e];  // scores of NaN or -inf alone: NaN
-            uint32_t *dst = reinterpret_cast<uint32_t *>(a.o + row_at(h) * D + gi * (D / 8));
+            uint32_t w[STEPS];
 #pragma unroll
-            for (int i = 0; i < STEPS; ++i) dst[i] = kd_pack2(acc[b][i][e] * inv, acc[b][i][e + 2] * inv);
+            for (int i = 0; i < STEPS; ++i) w[i] = kd_pack2(acc[b][i][e] * inv, acc[b][i][e + 2] * inv);
+            kd_store<STEPS>(reinterpret_cast<uint32_t *>(a.o + row_at(h) * D + gi * (D / 8)), w);
           }
       } else {
         // the last piece goes over this warp's tiles, which are all used up
@@ -620,7 +684,9 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_rows_kerne
               p[8 * NB * (D + 1) + b * 8 + ti * 2 + e] = l[b][e];
             }
           }
-        if (lane == 0) meta[warp * 2 + which] = KdMeta{seq, unit, j0, j1};
+        if (lane == 0)
+          meta[warp * 2 + which] =
+              KdMeta{seq, unit, j0, j1, n_tiles, at.s.first, at.s.count, at.s.kv_len, g, r0, {0, 0}};
       }
       at.next(a, first);
     }
@@ -635,118 +701,76 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_rows_kerne
   auto piece = [&](int s) {
     return reinterpret_cast<const float *>(smem + (s & 1 ? s / 2 * L::RING : L::OFF_PART + s / 2 * L::PART));
   };
-  KdMeta mine = {-1, 0, 0, 0};
-  if (lane < 2 * L::WARPS) mine = meta[lane];
-  const unsigned there = __ballot_sync(0xffffffffu, mine.seq >= 0);
+  int my_seq = -1, my_unit = 0;
+  if (lane < 2 * L::WARPS) {
+    my_seq = meta[lane].seq;
+    my_unit = meta[lane].unit;
+  }
+  const unsigned there = __ballot_sync(0xffffffffu, my_seq >= 0);
   const unsigned below = there & ((1u << lane) - 1u);
   const int prev = below != 0 ? 31 - __clz(below) : lane;
-  const int prev_seq = __shfl_sync(0xffffffffu, mine.seq, prev), prev_unit = __shfl_sync(0xffffffffu, mine.unit, prev);
-  const bool joined = prev != lane && prev_seq == mine.seq && prev_unit == mine.unit;
-  const unsigned starts = __ballot_sync(0xffffffffu, mine.seq >= 0 && !joined);
-  if (warp == 0 && (starts >> lane & 1)) {  // a lane for each chain
-    const unsigned later = starts & ~((2u << lane) - 1u);
-    const unsigned chain = there & (later != 0 ? (1u << (__ffs(later) - 1)) - 1u : 0xffffffffu) & ~((1u << lane) - 1u);
-    KdCursor<NB> it;
-    it.set(a, mine.seq, mine.unit, 0);
-    const int end = meta[31 - __clz(chain)].j1;
-    KdChain k;
-    k.pieces = chain;
-    k.first = it.s.first;
-    k.g = it.g;
-    k.r0 = it.sub * (8 * NB);
-    k.nr = min(8 * NB, it.s.count * a.r - k.r0);
-    k.before = it.s.kv_len - it.s.count + 1;
-    k.part = mine.j0 == 0 && end == it.n ? -1 : mine.j0 == 0 ? 1 : 0;
-    chains[__popc(starts & ((1u << lane) - 1u))] = k;
-    if (a.spans != nullptr && later == 0) {  // the CTA's last item: it may begin it and not end it
-      const long long item_end = (long long)first[it.seq] * a.times + (long long)(it.unit + 1) * it.n;
-      const int c1 = (int)min((item_end - 1) / each, (long long)gridDim.x - 1);
-      a.spans[blockIdx.x] = k.part == 1 ? make_int4(it.seq, it.unit, c1, 0) : make_int4(-1, 0, 0, 0);
+  const int prev_seq = __shfl_sync(0xffffffffu, my_seq, prev), prev_unit = __shfl_sync(0xffffffffu, my_unit, prev);
+  const bool joined = prev != lane && prev_seq == my_seq && prev_unit == my_unit;
+  unsigned starts = __ballot_sync(0xffffffffu, my_seq >= 0 && !joined);
+  if (a.spans != nullptr && threadIdx.x == 0) {  // the CTA's last item: it may begin it and not end it
+    int4 span = make_int4(-1, 0, 0, 0);
+    if (starts != 0) {
+      const KdMeta &x = meta[31 - __clz(starts)];
+      if (x.j0 == 0 && meta[31 - __clz(there)].j1 < x.n) {
+        const long long item_end = (long long)first[x.seq] * a.times + (long long)(x.unit + 1) * x.n;
+        span = make_int4(x.seq, x.unit, (int)min((item_end - 1) / each, (long long)gridDim.x - 1), 0);
+      }
     }
+    a.spans[blockIdx.x] = span;
   }
-  if (a.spans != nullptr && starts == 0 && threadIdx.x == 0) a.spans[blockIdx.x] = make_int4(-1, 0, 0, 0);
-  __syncthreads();
-  // A warp for each chain and row: a lane for each piece's m and l, then for each two columns.
-  const int most_rows = a.b.q_offsets != nullptr ? 8 * NB : min(8 * NB, a.r);
-  for (int u = warp; u < __popc(starts) * most_rows; u += L::WARPS) {
-    const KdChain &k = chains[u / most_rows];
-    const int h = u % most_rows;
-    if (h >= k.nr) continue;
-    const unsigned chain = k.pieces;
-    const bool in = chain >> lane & 1;
-    const float m = in ? piece(lane)[8 * NB * D + h] : -FLT_MAX, top = warp_max(m);
-    const float f = in ? ptx::ex2_approx(m - top) : 0.f;
-    const float l = warp_sum(in ? f * piece(lane)[8 * NB * (D + 1) + h] : 0.f);
-    // columns c (D / 8) + 2 i of c = lane % 8, i = lane / 8 and every fourth from there
-    constexpr int MINE = STEPS > 4 ? STEPS / 4 : 1;
-    const int c = lane & 7, i0 = lane / 8;
-    const int from = ((h / 8 * 2 + (h & 1)) * STEPS + i0) * 64 + (c * 4 + (h & 7) / 2) * 2;
-    float2 x[MINE];
-#pragma unroll
-    for (int e = 0; e < MINE; ++e) x[e] = make_float2(0.f, 0.f);
-    for (unsigned left = chain; left != 0; left &= left - 1) {
-      const int s = __ffs(left) - 1;
-      const float w = __shfl_sync(0xffffffffu, f, s);
-      const float *p = piece(s) + from;
-      if (i0 < STEPS) {
-#pragma unroll
-        for (int e = 0; e < MINE; ++e) {
-          const float2 v = *reinterpret_cast<const float2 *>(p + e * 256);
-          x[e].x = fmaf(w, v.x, x[e].x);
-          x[e].y = fmaf(w, v.y, x[e].y);
-        }
+  // A warp for each chain and two blocks' worth of fragments (rows 8 b + e, + 2, + 4, + 6).
+  int u = 0;
+  while (starts != 0) {
+    const int c = __ffs(starts) - 1;
+    starts &= starts - 1;
+    const unsigned chain = there & (starts != 0 ? (1u << (__ffs(starts) - 1)) - 1u : 0xffffffffu) & ~((1u << c) - 1u);
+    const KdMeta &x = meta[c];
+    const KdOut k(a, x.first, x.count, x.kv_len, x.g, x.r0, 8 * NB);
+    const bool whole = x.j0 == 0 && meta[31 - __clz(chain)].j1 == x.n;
+    float *out = whole ? nullptr : a.part + ((size_t)blockIdx.x * 2 + (x.j0 == 0 ? 1 : 0)) * (8 * NB * (D + 2));
+    for (int be = 0; be < 2 * NB; ++be) {
+      if (be / 2 * 8 + (be & 1) >= k.nr) continue;  // no rows
+      if (u++ % L::WARPS != warp) continue;
+      // (behind its first piece a chain goes on with the first one of each warp that follows)
+      const KdSum<D, NB, 1> sum(be, 0, __popc(chain), [&](int s) { return piece(s == 0 ? c : (c / 2 + s) * 2); });
+      if (whole) {
+        sum.store(a, k, be);
+        continue;
       }
-    }
-    if (i0 >= STEPS) continue;
-    const int column = c * (D / 8) + 2 * i0;
-    if (k.part >= 0) {
-      float *out = a.part + ((size_t)blockIdx.x * 2 + k.part) * (8 * NB * (D + 2));
 #pragma unroll
-      for (int e = 0; e < MINE; ++e) *reinterpret_cast<float2 *>(out + h * D + column + 8 * e) = x[e];
-      if (lane == 0) {
-        out[8 * NB * D + h] = top;
-        out[8 * NB * (D + 1) + h] = l;
+      for (int i = 0; i < STEPS; ++i)
+        *reinterpret_cast<float2 *>(out + (be * STEPS + i) * 64 + lane * 2) = sum.x[i];
+      if (gi == 0) {
+        const int h = be / 2 * 8 + ti * 2 + (be & 1);
+        out[8 * NB * D + h] = sum.top;
+        out[8 * NB * (D + 1) + h] = sum.l;
       }
-    } else {
-      const int i = (k.r0 + h) / a.r;
-      if (k.before + i <= 0) continue;
-      const float inv = KD_VALUE / l;
-      bf16 *dst = a.o + ((size_t)(k.first + i) * a.H + k.g * a.r + (k.r0 + h - i * a.r)) * D + column;
-#pragma unroll
-      for (int e = 0; e < MINE; ++e) *reinterpret_cast<uint32_t *>(dst + 8 * e) = kd_pack2(x[e].x * inv, x[e].y * inv);
     }
   }
 }
 
-// Joins the parts of the items that several CTAs had: a CTA of D / 2 threads for each CTA that
-// may have begun one, and row.
+// Joins the parts of the items that several CTAs had: KD_JOIN warps for each CTA that may have
+// begun one and fragment.
+template <int D>
+constexpr int KD_JOIN = D >= 64 ? 4 : D / 16;
 template <int D, int NB>
-__global__ void __launch_bounds__(D / 2) kv4_rows_join_kernel(const __grid_constant__ KdArgs a) {
+__global__ void __launch_bounds__(64 * NB * KD_JOIN<D>) kv4_rows_join_kernel(const __grid_constant__ KdArgs a) {
   grid_dependency_wait();
-  const int c0 = blockIdx.x, h = blockIdx.y;
+  const int c0 = blockIdx.x, be = threadIdx.x / 32 / KD_JOIN<D>, part = threadIdx.x / 32 % KD_JOIN<D>;
   const int4 span = ld_after_wait(a.spans + c0);
   if (span.x < 0) return;
   KdCursor<NB> it;
   it.set(a, span.x, span.y, 0);
-  const int R = it.sub * (8 * NB) + h, i = R / a.r;
-  if (R >= it.s.count * a.r || it.s.kv_len - it.s.count + i < 0) return;
-  auto part = [&](int c) { return a.part + ((size_t)c * 2 + (c == c0 ? 1 : 0)) * (8 * NB * (D + 2)); };
-  const int d = threadIdx.x * 2;
-  float m = -FLT_MAX, l = 0.f, x = 0.f, y = 0.f;
-#pragma unroll 4
-  for (int c = c0; c <= span.z; ++c) m = fmaxf(m, part(c)[8 * NB * D + h]);
-#pragma unroll 4
-  for (int c = c0; c <= span.z; ++c) {
-    const float *p = part(c);
-    const float f = ptx::ex2_approx(p[8 * NB * D + h] - m);
-    const float2 v = *reinterpret_cast<const float2 *>(p + h * D + d);
-    l = fmaf(f, p[8 * NB * (D + 1) + h], l);
-    x = fmaf(f, v.x, x);
-    y = fmaf(f, v.y, y);
-  }
-  const float inv = KD_VALUE / l;
-  *reinterpret_cast<uint32_t *>(a.o + ((size_t)(it.s.first + i) * a.H + it.g * a.r + R % a.r) * D + d) =
-      kd_pack2(x * inv, y * inv);
+  const KdOut k(a, it.s.first, it.s.count, it.s.kv_len, it.g, it.sub * (8 * NB), 8 * NB);
+  const KdSum<D, NB, KD_JOIN<D>> sum(be, part, span.z - c0 + 1, [&](int s) {
+    return a.part + ((size_t)(c0 + s) * 2 + (s == 0 ? 1 : 0)) * (8 * NB * (D + 2));
+  });
+  sum.store(a, k, be);
 }
 
 // Form and grid of a call; rows: of a sequence and KV head, on average.
@@ -783,7 +807,7 @@ cudaError_t launch(KdArgs a, const KdPlan &p, cudaStream_t st) {
       launch_pdl(kv4_rows_kernel<D, NB>, dim3((unsigned)p.ctas), dim3(L::WARPS * 32), L::bytes(a.b.n_seqs), st, a);
   if (r != cudaSuccess || p.direct) return r;
   count_launch();
-  return launch_pdl(kv4_rows_join_kernel<D, NB>, dim3((unsigned)(p.ctas - 1), (unsigned)(a.b.q_offsets != nullptr || a.r > 8 * NB ? 8 * NB : a.r)), dim3(D / 2), 0, st, a);
+  return launch_pdl(kv4_rows_join_kernel<D, NB>, dim3((unsigned)(p.ctas - 1)), dim3(64 * NB * KD_JOIN<D>), 0, st, a);
 }
 
 // Tiles of a KV head's items over all sequences, at most.
