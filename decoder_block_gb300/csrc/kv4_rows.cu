@@ -6,7 +6,7 @@
 // in one pass over the keys, the running maximum m and the sum in fp32.
 //
 // The cache is read once, and a byte of it is nearly two elements: what has to be kept small
-// is the work per element.  A warp takes 32 keys at a time for 8, 16 or 24 rows (head of the
+// is the work per element.  A warp takes 64 or 32 keys at a time for 8, 16 or 24 rows (head of the
 // group, token) of a sequence; codes go from shared memory into registers and from there
 // straight into the operands of mma.sync, keys and columns of the values on its 16-row side:
 //   S^T[16 keys x 8 rows] = K Q^T,     O^T[16 columns x 8 rows] += V^T P^T.
@@ -38,26 +38,28 @@
 namespace llama {
 namespace {
 
-constexpr int KD_KEYS = 32;  // keys of a warp's tile
+// Keys of a warp's tile: as many as the registers have room for, what is done once a tile is a
+// third of a tile of 32 keys.
+constexpr int kd_keys(int NB) { return NB == 1 ? 64 : 32; }
 constexpr float KD_RESCALE = 8.0f;  // log2 units: the running maximum is raised when it grows by > 2^8
 // Weights are fp16 for their product with V: 2^7 times what they are, so that the largest,
 // 2^15, has room above, and what is less than 2^-31 of the running maximum's, not 2^-24, is
 // lost (120000 keys of such weights: 2^-14 of the sum).
 constexpr float KD_WEIGHT = 7.0f;
 constexpr float KD_VALUE = 2.0f;  // V's operand is half of V
-// Key tiles of a CTA's item in the direct form, at most.
-constexpr int KD_DIRECT_TILES = 64;
+// Keys of a CTA's item in the direct form, at most.
+constexpr int KD_DIRECT_KEYS = 2048;
 constexpr int KD_MAX_NB = 3;
 constexpr int KD_LEAST = 4;  // tiles of a CTA's run, at least: a warp on each scheduler
 
 // NB: blocks of 8 rows of an item.
 template <int D, int NB>
 struct KdLayout {
-  static constexpr int WARPS = NB == 1 ? 16 : 8;
+  static constexpr int WARPS = 8, KEYS = kd_keys(NB);
   static constexpr int RB = kv4_code_bytes(D), SB = kv4_scale_bytes(D);
-  static constexpr int HALF = KD_KEYS * (RB + SB), STAGE = 2 * HALF;  // K, then V: codes, then scales
+  static constexpr int HALF = KEYS * (RB + SB), STAGE = 2 * HALF;  // K, then V: codes, then scales
   static constexpr int PART = 8 * NB * (D + 2) * 4;  // (O, m, l) of an item
-  static constexpr int FIT = (NB == 1 ? 9216 : 13824) / STAGE;
+  static constexpr int FIT = (NB == 1 ? 18432 : 13824) / STAGE;
   static constexpr int STAGES = FIT < 8 ? FIT : 8;
   static constexpr int RING = STAGES * STAGE > PART ? STAGES * STAGE : PART;  // of a warp; its last part at the end
   static constexpr int OFF_PART = WARPS * RING;   // of each warp, its first
@@ -208,7 +210,8 @@ __device__ __forceinline__ SeqSpan kd_span(const KdArgs &a, int i) {
   if (a.b.q_offsets != nullptr) return seq_span(a.b, a.pv, i);
   return SeqSpan{i, 1, checked_len(ld_after_wait(a.b.kv_lens + i), a.b.max_kv_len, a.pv)};
 }
-__device__ __forceinline__ int kd_tiles(int keys) { return (keys + KD_KEYS - 1) / KD_KEYS; }
+template <int NB>
+__host__ __device__ __forceinline__ int kd_tiles(int keys) { return (keys + kd_keys(NB) - 1) / kd_keys(NB); }
 
 // Token and head in the group of an item's row, without a division for each: the item's first
 // row has been divided, and what is left is small (fp32 is exact to half a step there).
@@ -228,7 +231,7 @@ struct KdCursor {
   __device__ __forceinline__ void set(const KdArgs &a, int i, int u, int at) {
     seq = i;
     s = kd_span(a, i);
-    n = kd_tiles(s.kv_len);
+    n = kd_tiles<NB>(s.kv_len);
     const int subs = (s.count * a.r + 8 * NB - 1) / (8 * NB);
     units = a.G * subs;
     unit = u;
@@ -273,7 +276,7 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_rows_kerne
   constexpr int THREADS = L::WARPS * 32;
   constexpr int KW = D / 32 > 0 ? D / 32 : 1;  // words of a key's codes that a thread takes (of 8 elements)
   constexpr int VW = D / 64 > 0 ? D / 64 : 1;  // of a value's
-  constexpr int STEPS = D / 16;
+  constexpr int STEPS = D / 16, MB = L::KEYS / 16;
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, gi = lane / 4, ti = lane & 3;
   const uint32_t s0 = ptx::smem_u32(smem);
@@ -304,7 +307,7 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_rows_kerne
       return;
     }
   } else {
-    // (4096 sequences: 8 or 16 each)
+    // (4096 sequences: 16 each)
     const int per = (a.b.n_seqs + THREADS - 1) / THREADS;
     auto add = [&](int x, int y) { return (int)min((unsigned)x + (unsigned)y, (unsigned)a.most); };
     int mine = 0;
@@ -317,7 +320,7 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_rows_kerne
         if (a.b.q_offsets != nullptr) check_seq(a.b, a.pv, i, a.status);
         else if (ld_after_wait(a.b.kv_lens + i) != s.kv_len) report_status(a.status, LLAMA_ERR_RANGE);
       }
-      int n = kd_tiles(s.kv_len);
+      int n = kd_tiles<NB>(s.kv_len);
       if (a.b.q_offsets != nullptr) n = min((long long)n * ((s.count * a.r + 8 * NB - 1) / (8 * NB)), (long long)a.most);
       blind |= s.kv_len < s.count;
       first[i] = n;
@@ -363,19 +366,27 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_rows_kerne
     if (a.direct) at.j = w0;
     else at.seek(a, first, begin + w0);
     // ------------------------------------------------------------ copies ---
-    // A tile's rows are two runs of 16, which no page splits; a run behind the last key is given
-    // the first one's rows, which may be read, and its scores are replaced.  Every lane knows
-    // the page ids and adds to pointers of its own (by bulk copies, whose operands have to be
-    // made uniform, a tile took 893 instructions for the 838 of lanes asking one another).
+    // A tile's rows are runs of 16, which no page splits; a run behind the last key is given the
+    // first one's rows, which may be read, and its scores are replaced.  Every lane knows the
+    // page ids and adds to pointers of its own (by bulk copies, whose operands have to be made
+    // uniform, a tile of 32 keys took 893 instructions for the 838 of lanes asking one another
+    // and the 823 of this).
     KdCursor<NB> ahead = at;  // the tile whose pages are known and that is copied next
-    int left = todo, fill = 0, id0 = 0, id1 = 0;
+    constexpr int RUNS = L::KEYS / 16;
+    constexpr int CHUNK = L::RB < 16 ? L::RB : 16;             // bytes of a lane's copy
+    constexpr int COPIES = D >= 64 ? L::RB / 32 : 1;           // of 32 lanes for a run; D < 64: for two
+    constexpr int S_PIECES = L::KEYS * L::SB / 16;             // of 16 bytes: K's scales, and V's
+    constexpr int S_COPIES = S_PIECES > 16 ? S_PIECES / 16 : 1;
+    int left = todo, fill = 0, id[RUNS], slot[RUNS], s_id = 0, s_slot = 0;
+#pragma unroll
+    for (int r = 0; r < RUNS; ++r) id[r] = slot[r] = 0;
     const int rows_mask = (1 << a.pv.page_log2) - 1;
-    const bool narrow = a.pv.page_log2 == 4;
+    const bool wide = 1 << a.pv.page_log2 >= L::KEYS;  // a tile lies in one page
     const uint32_t stride = (uint32_t)a.pv.page_stride;
-    constexpr int CHUNK = L::RB < 16 ? L::RB : 16;   // bytes of a lane's copy
-    constexpr int COPIES = D >= 64 ? L::RB / 32 : 1;  // of 32 lanes for a run; D < 64: for both runs
-    const int s_lane = lane % 16, s_half = s_lane / L::SB & 1;  // scales: K's by lanes 0 .., V's by lanes 16 ..
-    const uint8_t *from_k, *from_v, *from_s;
+    // scales: pieces lane + 32 i, K's first; S_PIECES is 32 at most, then i says K or V
+    const int s_piece = lane % S_PIECES, s_run = s_piece / L::SB;
+    const bool s_mine = lane < 2 * S_PIECES;
+    const uint8_t *from_k, *from_v, *from_s[S_COPIES];
     auto aim = [&] {  // this lane's bytes of page 0
       const int block = kv4_block_bytes(1 << a.pv.page_log2, D) * ahead.g;
       const int off = D >= 64 ? lane * 16 : lane % 16 * CHUNK;
@@ -390,54 +401,78 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_rows_kerne
         const bf16 *row = a.q + ((size_t)(ahead.s.first + rows.token(h)) * a.H + ahead.g * a.r + rows.head(h, a.r)) * D;
         asm volatile("prefetch.global.L1 [%0];" ::"l"(row + i % LINES * 64));
       }
-      from_s = (lane < 16 ? a.k : a.v) + block + (L::RB << a.pv.page_log2) + s_lane % L::SB * 16;
+#pragma unroll
+      for (int i = 0; i < S_COPIES; ++i)
+        from_s[i] = ((S_COPIES > 1 ? i : lane / S_PIECES) == 0 ? a.k : a.v) + block + (L::RB << a.pv.page_log2) +
+                    s_piece % L::SB * 16;
     };
     auto look_up = [&] {
       if (left <= 0) return;
-      const int p = ahead.j * KD_KEYS;
-      const int *table = a.pv.table + (size_t)ahead.seq * a.pv.table_stride + (p >> a.pv.page_log2);
-      id0 = id1 = ld_after_wait(table);
-      if (narrow && p + 16 < ahead.s.kv_len) id1 = ld_after_wait(table + 1);
+      const int p = ahead.j * L::KEYS;
+      const int *table = a.pv.table + (size_t)ahead.seq * a.pv.table_stride;
+      id[0] = ld_after_wait(table + (p >> a.pv.page_log2));
+      slot[0] = p & rows_mask;
+      if (wide) {
+        s_id = id[0];
+        s_slot = slot[0] + s_run * 16;
+        return;
+      }
+#pragma unroll
+      for (int r = 1; r < RUNS; ++r) {
+        const int pr = p + 16 * r < ahead.s.kv_len ? p + 16 * r : p;
+        id[r] = ld_after_wait(table + (pr >> a.pv.page_log2));
+        slot[r] = pr & rows_mask;
+      }
+      const int ps = p + 16 * s_run < ahead.s.kv_len ? p + 16 * s_run : p;
+      s_id = ld_after_wait(table + (ps >> a.pv.page_log2));
+      s_slot = ps & rows_mask;
     };
     auto request = [&] {
       if (left > 0) {
-        const uint32_t stage = ring + fill * L::STAGE;
-        const int slot0 = ahead.j * KD_KEYS & rows_mask, slot1 = narrow ? 0 : slot0 + 16;
-        const bool bad0 = (unsigned)id0 >= (unsigned)a.pv.n_pages, bad1 = (unsigned)id1 >= (unsigned)a.pv.n_pages;
-        auto copies = [&](auto checked) {
-          constexpr bool CHECKED = decltype(checked)::value;  // a page may be out of range: one of zeros
-          auto run = [&](const uint8_t *from, uint32_t to, int h) {
-            const uint8_t *p = from + (uint64_t)(uint32_t)(h ? id1 : id0) * stride + (h ? slot1 : slot0) * L::RB;
-#pragma unroll
-            for (int i = 0; i < COPIES; ++i) {
-              if (CHECKED && (h ? bad1 : bad0)) {
-                asm volatile("st.shared.v2.u32 [%0], {%1, %1};" ::"r"(to + i * 512), "r"(0x88888888u) : "memory");
-                if (CHUNK == 16)
-                  asm volatile("st.shared.v2.u32 [%0], {%1, %1};" ::"r"(to + i * 512 + 8), "r"(0x88888888u) : "memory");
-              } else {
-                copy_async<CHUNK>(to + i * 512, p + i * 512);
-              }
-            }
-          };
+        const uint32_t stage = ring + fill * L::STAGE, to = stage + lane * CHUNK;
+        bool bad = (unsigned)id[0] >= (unsigned)a.pv.n_pages;  // a page is out of range
+        if (wide && !bad) {
 #pragma unroll
           for (int which = 0; which < 2; ++which) {
-            const uint32_t to = stage + which * L::HALF + lane * CHUNK;
-            if constexpr (D >= 64) {
-              run(which ? from_v : from_k, to, 0);
-              run(which ? from_v : from_k, to + 16 * L::RB, 1);
-            } else {
-              run(which ? from_v : from_k, to, lane / 16);
-            }
+            // (with D < 64 lanes 16 .. have another row in each of their runs)
+            const uint8_t *p = (which ? from_v : from_k) + (uint64_t)(uint32_t)id[0] * stride + slot[0] * L::RB +
+                               (D >= 64 ? 0 : lane / 16 * 16 * L::RB);
+#pragma unroll
+            for (int i = 0; i < L::KEYS * L::RB / (32 * CHUNK); ++i)
+              copy_async<CHUNK>(to + which * L::HALF + i * 32 * CHUNK, p + i * 32 * CHUNK);
           }
-          if (s_lane < 2 * L::SB && !(CHECKED && (s_half ? bad1 : bad0)))
-            copy_async<16>(stage + (lane < 16 ? 0 : L::HALF) + KD_KEYS * L::RB + s_lane * 16,
-                           from_s + (uint64_t)(uint32_t)(s_half ? id1 : id0) * stride + (s_half ? slot1 : slot0) * L::SB);
-        };
-        if (!bad0 && !bad1) {
-          copies(std::false_type());
         } else {
-          if (lane == 0) report_status(a.status, LLAMA_ERR_RANGE);
-          copies(std::true_type());
+          if (!wide)
+#pragma unroll
+            for (int r = 1; r < RUNS; ++r) bad |= (unsigned)id[r] >= (unsigned)a.pv.n_pages;
+          if (bad && lane == 0) report_status(a.status, LLAMA_ERR_RANGE);
+#pragma unroll
+          for (int which = 0; which < 2; ++which)
+#pragma unroll
+            for (int r = 0; r < RUNS; r += D >= 64 ? 1 : 2) {
+              const int in = wide ? 0 : r, r1 = D >= 64 ? in : wide ? 0 : r + 1;
+              const int my_id = D >= 64 || lane < 16 ? id[in] : id[r1];
+              const int my_slot = (D >= 64 || lane < 16 ? slot[in] : slot[r1]) + (wide ? (r + (D >= 64 ? 0 : lane / 16)) * 16 : 0);
+              const uint8_t *p = (which ? from_v : from_k) + (uint64_t)(uint32_t)my_id * stride + my_slot * L::RB;
+              const uint32_t dst = to + which * L::HALF + r * 16 * L::RB;
+#pragma unroll
+              for (int i = 0; i < COPIES; ++i) {
+                if ((unsigned)my_id < (unsigned)a.pv.n_pages) {
+                  copy_async<CHUNK>(dst + i * 512, p + i * 512);
+                } else {  // zeros
+                  asm volatile("st.shared.v2.u32 [%0], {%1, %1};" ::"r"(dst + i * 512), "r"(0x88888888u) : "memory");
+                  if (CHUNK == 16)
+                    asm volatile("st.shared.v2.u32 [%0], {%1, %1};" ::"r"(dst + i * 512 + 8), "r"(0x88888888u) : "memory");
+                }
+              }
+            }
+        }
+        if (s_mine && (unsigned)s_id < (unsigned)a.pv.n_pages) {
+          const uint64_t off = (uint64_t)(uint32_t)s_id * stride + (uint32_t)(s_slot * L::SB);
+#pragma unroll
+          for (int i = 0; i < S_COPIES; ++i)
+            copy_async<16>(stage + (S_COPIES > 1 ? i : lane / S_PIECES) * L::HALF + L::KEYS * L::RB + s_piece * 16,
+                           from_s[i] + off);
         }
         if (ahead.next(a, first)) aim();
         --left;
@@ -504,14 +539,22 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_rows_kerne
         asm volatile("cp.async.wait_group %0;" ::"n"(L::STAGES - 1) : "memory");
         __syncwarp();
         const uint32_t sk = ring + use * L::STAGE, sv = sk + L::HALF;
-        // scores: keys gi and gi + 8 of both halves of the tile
-        float sc[2][NB][4];
+        // scores: keys gi and gi + 8 of every 16, 32 keys at a time
+        float sc[MB][NB][4];
+#pragma unroll
+        for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[mb][b][e] = 0.f;
+#pragma unroll
+        for (int m0 = 0; m0 < MB; m0 += 2) {
         uint32_t w[4][KW];
         Kv4Scale sa[4], sb[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int row = e * 8 + gi;
-          const uint32_t scales = sk + KD_KEYS * L::RB + row * L::SB;
+          const int row = m0 * 16 + e * 8 + gi;
+          const uint32_t scales = sk + L::KEYS * L::RB + row * L::SB;
           if constexpr (D >= 32) ld_words<KW>(sk + row * L::RB + ti * (D / 8), w[e]);
           else ld_words<KW>(sk + row * L::RB + ti / 2 * 4, w[e]);
           if constexpr (D == 16) w[e][0] >>= 8 * (ti & 1);
@@ -526,12 +569,6 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_rows_kerne
           }
         }
 #pragma unroll
-        for (int mb = 0; mb < 2; ++mb)
-#pragma unroll
-          for (int b = 0; b < NB; ++b)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sc[mb][b][e] = 0.f;
-#pragma unroll
         for (int s = 0; s < STEPS; ++s)
 #pragma unroll
           for (int mb = 0; mb < 2; ++mb) {
@@ -544,12 +581,13 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_rows_kerne
               f[2 + e] = s % 2 == 0 ? kv4_pair<1>(word, k) : kv4_pair<3>(word, k);
             }
 #pragma unroll
-            for (int b = 0; b < NB; ++b) mma16816(sc[mb][b], f, qf[b][s][0], qf[b][s][1]);
+            for (int b = 0; b < NB; ++b) mma16816(sc[m0 + mb][b], f, qf[b][s][0], qf[b][s][1]);
           }
-        if ((j + 1) * KD_KEYS > all_see) {
-          const int key = j * KD_KEYS + gi;
+        }
+        if ((j + 1) * L::KEYS > all_see) {
+          const int key = j * L::KEYS + gi;
 #pragma unroll
-          for (int mb = 0; mb < 2; ++mb)
+          for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
             for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -557,14 +595,17 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_rows_kerne
                 if (key + mb * 16 + (e / 2) * 8 >= sees[b][e & 1]) sc[mb][b][e] = -INFINITY;
         }
         // weights: rows 8 b + 2 ti and the next
-        uint32_t pf[2][NB][2];
+        uint32_t pf[MB][NB][2];
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
           float mx[2];
           bool need = false;
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            mx[e] = fmaxf(fmaxf(sc[0][b][e], sc[0][b][e + 2]), fmaxf(sc[1][b][e], sc[1][b][e + 2])) * a.scale_log2;
+            mx[e] = fmaxf(sc[0][b][e], sc[0][b][e + 2]);
+#pragma unroll
+            for (int mb = 1; mb < MB; ++mb) mx[e] = fmaxf(mx[e], fmaxf(sc[mb][b][e], sc[mb][b][e + 2]));
+            mx[e] *= a.scale_log2;
             need |= mx[e] > m[b][e] + KD_RESCALE;
           }
           if (__any_sync(0xffffffffu, need)) {
@@ -584,7 +625,7 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_rows_kerne
           }
           const float less[2] = {KD_WEIGHT - m[b][0], KD_WEIGHT - m[b][1]};
 #pragma unroll
-          for (int mb = 0; mb < 2; ++mb) {
+          for (int mb = 0; mb < MB; ++mb) {
             float p[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -597,7 +638,7 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_rows_kerne
         }
         // outputs: columns gi (D / 8) .. of the values, keys 2 ti, 2 ti + 1, and 8 more
 #pragma unroll
-        for (int mb = 0; mb < 2; ++mb) {
+        for (int mb = 0; mb < MB; ++mb) {
           uint32_t even[2][VW], odd[2][VW];
           Kv4Half sv2[2];
 #pragma unroll
@@ -607,7 +648,7 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_rows_kerne
             const uint32_t from = sv + row * L::RB + (D >= 64 ? gi * (D / 16) : D == 32 ? gi / 2 * 4 : gi / 4 * 4);
             ld_words<VW>(from, x);
             ld_words<VW>(from + L::RB, y);
-            const uint32_t scales = sv + KD_KEYS * L::RB + row * L::SB + gi * L::SB / 8;
+            const uint32_t scales = sv + L::KEYS * L::RB + row * L::SB + gi * L::SB / 8;
             sv2[e] = kv4_halves(ld_byte(scales), ld_byte(scales + L::SB));
 #pragma unroll
             for (int w = 0; w < VW; ++w) {
@@ -784,7 +825,7 @@ KdPlan plan_of(const PackedView &b, long long rows, int H, int G, int D, bool de
   const int sms = sm_count();
   p.nb = rows <= 8 ? 1 : rows <= 16 || decode ? 2 : KD_MAX_NB;
   const long long items = (long long)b.n_seqs * G * ((H / G + 8 * p.nb - 1) / (8 * p.nb));
-  p.direct = decode && (b.max_kv_len + KD_KEYS - 1) / KD_KEYS <= KD_DIRECT_TILES && items <= sms;
+  p.direct = decode && b.max_kv_len <= KD_DIRECT_KEYS && items <= sms;
   p.ctas = p.direct ? (int)items : sms > 2 ? sms : 2;
   if (!p.direct) {
     p.off_part = ((size_t)p.ctas * 16 + 127) / 128 * 128;
@@ -812,7 +853,7 @@ cudaError_t launch(KdArgs a, const KdPlan &p, cudaStream_t st) {
 
 // Tiles of a KV head's items over all sequences, at most.
 long long most_tiles(const PackedView &b, int H, int G) {
-  return (long long)((b.max_kv_len + KD_KEYS - 1) / KD_KEYS) * ((long long)b.n_tokens * (H / G) / 8 + b.n_seqs);
+  return (long long)kd_tiles<2>(b.max_kv_len) * ((long long)b.n_tokens * (H / G) / 8 + b.n_seqs);
 }
 
 cudaError_t launch_rows(const bf16 *q, const uint8_t *k, const uint8_t *v, bf16 *o, const PagedView &pv,
