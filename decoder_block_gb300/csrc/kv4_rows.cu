@@ -50,6 +50,7 @@ constexpr float KD_VALUE = 2.0f;  // V's operand is half of V
 // Keys of a CTA's item in the direct form, at most.
 constexpr int KD_DIRECT_KEYS = 2048;
 constexpr int KD_MAX_NB = 3;
+constexpr int KD_ROUNDS = 10, KD_FEW_KEYS = 384;  // of packed calls: see kv4_rows_fit
 constexpr int KD_LEAST = 4;  // tiles of a CTA's run, at least: a warp on each scheduler
 
 // NB: blocks of 8 rows of an item.
@@ -915,9 +916,17 @@ cudaError_t launch_kv4_decode(const bf16 *q, const uint8_t *k, const uint8_t *v,
   return launch_rows(q, k, v, o, pv, b, H, G, D, workspace, plan_of(b, H / G, H, G, D, true), status, st);
 }
 
-// Few rows: what tcgen05's 128-row tiles would mostly pad.  (The counts of tiles are ints.)
+// Few rows, which tcgen05's 128-row tiles would mostly pad: those of one item on average, or
+// of so many that the warps take KD_ROUNDS of their tiles each at the longest length (64
+// sequences of 20 rows behind 2200 keys, 8 KV heads: 77 us for 104; 26 of 73 rows behind up to
+// 3300 keys, one KV head: 20 for 31; at 15 rounds 17 for 24, but 30 for 25).  Not over a few
+// keys, where tcgen05 takes a single kernel (up to 236 keys 9 us for 13, up to 400 keys 11.5
+// for 11).  (The counts of tiles are ints.)
 bool kv4_rows_fit(const PackedView &b, int H, int G) {
-  return rows_of(b, H, G) <= KV4_FEW_ROWS && most_tiles(b, H, G) <= 0x7fffffffLL;
+  const long long tiles = (long long)G * kd_tiles<KD_MAX_NB>(b.max_kv_len) *
+                          ((long long)b.n_tokens * (H / G) / (8 * KD_MAX_NB) + b.n_seqs);
+  return b.max_kv_len > KD_FEW_KEYS && most_tiles(b, H, G) <= 0x7fffffffLL &&
+         (rows_of(b, H, G) <= 8 * KD_MAX_NB || tiles <= (long long)KD_ROUNDS * sm_count() * 8);
 }
 size_t kv4_rows_workspace_bytes(const PackedView &b, int H, int G, int D) {
   return plan_of(b, rows_of(b, H, G), H, G, D, false).bytes;

@@ -103,7 +103,6 @@ cudaError_t launch_paged_decode_tc(const bf16 *q, const bf16 *k, const bf16 *v, 
                                    void *workspace, int *status, cudaStream_t st);
 
 // Packed attention of few rows a sequence over pages held in 4 bits (kv4_rows.cu), where it fits.
-constexpr int KV4_FEW_ROWS = 24;  // rows (token, head) of a sequence and KV head, at most on average
 bool kv4_rows_fit(const PackedView &b, int H, int G);
 size_t kv4_rows_workspace_bytes(const PackedView &b, int H, int G, int D);
 cudaError_t launch_kv4_rows(const bf16 *q, const uint8_t *k, const uint8_t *v, bf16 *o, const PagedView &pv,

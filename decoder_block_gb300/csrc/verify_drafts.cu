@@ -19,6 +19,7 @@
 #include <float.h>
 #include <limits.h>
 #include <math.h>
+#include <string.h>
 
 #include "paged_kernels.h"
 #include "ptx.cuh"
@@ -251,6 +252,44 @@ __device__ __forceinline__ VdPart row_sum(const VdArgs &a, int row, int side, fl
 }
 __device__ __forceinline__ bool row_ok(float z) { return z > 0.f && z <= FLT_MAX; }
 
+// N elements side by side, whatever their alignment (bytes, 16 at most): rows of an odd
+// vocabulary begin anywhere, and differently in each array.
+template <typename E, int N>
+__device__ __forceinline__ void load_group(const E *p, int align, E (&x)[N]) {
+  static_assert(N * sizeof(E) % 16 == 0, "whole vectors");
+  constexpr int WORDS = N * (int)sizeof(E) / 4;
+  uint32_t w[WORDS];
+  if (align >= 16) {
+#pragma unroll
+    for (int i = 0; i < WORDS; i += 4) {
+      const uint4 v = ld_once_after_wait(reinterpret_cast<const char *>(p) + 4 * i);
+      w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
+    }
+  } else if (align == 8) {
+#pragma unroll
+    for (int i = 0; i < WORDS; i += 2)
+      asm volatile("ld.global.cs.v2.u32 {%0, %1}, [%2];"
+                   : "=r"(w[i]), "=r"(w[i + 1])
+                   : "l"(reinterpret_cast<const char *>(p) + 4 * i));
+  } else if (align == 4) {
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) w[i] = (uint32_t)ld_after_wait(reinterpret_cast<const int *>(p) + i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) {
+      uint16_t a, b;
+      asm volatile("ld.global.u16 %0, [%1];" : "=h"(a) : "l"(reinterpret_cast<const char *>(p) + 4 * i));
+      asm volatile("ld.global.u16 %0, [%1];" : "=h"(b) : "l"(reinterpret_cast<const char *>(p) + 4 * i + 2));
+      w[i] = (uint32_t)a | (uint32_t)b << 16;
+    }
+  }
+  memcpy(x, w, sizeof(w));
+}
+__device__ __forceinline__ int align_of(const void *p) {
+  const uint32_t low = (uint32_t)reinterpret_cast<uintptr_t>(p) | 16u;
+  return (int)(low & (0u - low));
+}
+
 // The best so far of a race; of equals the lowest id.
 struct VdBest {
   float score;
@@ -366,54 +405,33 @@ __global__ void __launch_bounds__(VD_THREADS) verify_draw_kernel(const __grid_co
         }
       };
       constexpr int N = Vec16<T>::N;
-      const bool whole = ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(noise) |
-                           reinterpret_cast<uintptr_t>(y)) & 15) == 0;
+      const int ax = align_of(x), ay = both ? align_of(y) : 16, ae = align_of(noise);
       const int stride = a.cluster * VD_THREADS, me = rank * VD_THREADS + (int)threadIdx.x;
       auto search = [&](bool residual) {
-        int done = 0;  // ids below are searched by whole vectors
-        if (whole) {
-          const int n_vec = a.V / N;
-          done = n_vec * N;
-          for (int v = me; v < n_vec; v += VD_RACE * stride) {
-            Vec16<T> fx[VD_RACE], fy[VD_RACE];
-            float4 e[VD_RACE][N / 4];
+        const int groups = a.V / N;
+        for (int v = me; v < groups; v += VD_RACE * stride) {
+          T fx[VD_RACE][N], fy[VD_RACE][N];
+          float e[VD_RACE][N];
 #pragma unroll
-            for (int k = 0; k < VD_RACE; ++k) {
-              const int at = v + k * stride;
-              if (at >= n_vec) continue;
-              fx[k].raw = ld_once_after_wait(x + (size_t)at * N);
-              if (both) fy[k].raw = ld_once_after_wait(y + (size_t)at * N);
-#pragma unroll
-              for (int i = 0; i < N / 4; ++i) {
-                const uint4 u = ld_once_after_wait(noise + (size_t)at * N + 4 * i);
-                e[k][i] = *reinterpret_cast<const float4 *>(&u);
-              }
-            }
-#pragma unroll
-            for (int k = 0; k < VD_RACE; ++k) {
-              const int at = v + k * stride;
-              if (at >= n_vec) continue;
-#pragma unroll
-              for (int i = 0; i < N; ++i)
-                race(fx[k].get(i), both ? fy[k].get(i) : 0.f, reinterpret_cast<const float *>(e[k])[i], at * N + i, residual);
-            }
-          }
-        }
-        for (int v = done + me; v < a.V; v += 8 * stride) {
-          float fx[8], fy[8], e[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
+          for (int k = 0; k < VD_RACE; ++k) {
             const int at = v + k * stride;
-            e[k] = 0.f;
-            if (at >= a.V) continue;
-            fx[k] = ld_logit<T>(x + at);
-            fy[k] = both ? ld_logit<T>(y + at) : 0.f;
-            e[k] = ld_float_after_wait(noise + at);
+            if (at >= groups) continue;
+            load_group(x + (size_t)at * N, ax, fx[k]);
+            if (both) load_group(y + (size_t)at * N, ay, fy[k]);
+            load_group(noise + (size_t)at * N, ae, e[k]);
           }
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (e[k] > 0.f) race(fx[k], fy[k], e[k], v + k * stride, residual);
+          for (int k = 0; k < VD_RACE; ++k) {
+            const int at = v + k * stride;
+            if (at >= groups) continue;
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+              race(to_f32<T>(fx[k][i]), both ? to_f32<T>(fy[k][i]) : 0.f, e[k][i], at * N + i, residual);
+          }
         }
+        const int at = groups * N + me;  // what is left of the row
+        if (at < a.V)
+          race(ld_logit<T>(x + at), both ? ld_logit<T>(y + at) : 0.f, ld_float_after_wait(noise + at), at, residual);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
           const float s = __shfl_xor_sync(0xffffffffu, best.score, o);
