@@ -905,6 +905,12 @@ long long rows_of(const PackedView &b, int H, int G) {
 
 }  // namespace
 
+// A CTA's tiles are counted in an int.
+bool kv4_decode_fits(int n_seqs, int max_kv_len, int H, int G) {
+  const long long subs = (H / G + 15) / 16;
+  return (long long)n_seqs * max_kv_len <= (1LL << 42) / (G * subs);
+}
+
 size_t kv4_decode_workspace_bytes(int n_seqs, int max_kv_len, int H, int G, int D) {
   return plan_of(decode_view(nullptr, n_seqs, max_kv_len), H / G, H, G, D, true).bytes;
 }
@@ -926,6 +932,7 @@ bool kv4_rows_fit(const PackedView &b, int H, int G) {
   const long long tiles = (long long)G * kd_tiles<KD_MAX_NB>(b.max_kv_len) *
                           ((long long)b.n_tokens * (H / G) / (8 * KD_MAX_NB) + b.n_seqs);
   return b.max_kv_len > KD_FEW_KEYS && most_tiles(b, H, G) <= 0x7fffffffLL &&
+         most_tiles(b, H, G) * G <= (1LL << 30) * sm_count() &&
          (rows_of(b, H, G) <= 8 * KD_MAX_NB || tiles <= (long long)KD_ROUNDS * sm_count() * 8);
 }
 size_t kv4_rows_workspace_bytes(const PackedView &b, int H, int G, int D) {

@@ -109,6 +109,7 @@ cudaError_t launch_kv4_rows(const bf16 *q, const uint8_t *k, const uint8_t *v, b
                             const PackedView &b, int H, int G, int D, void *workspace, int *status, cudaStream_t st);
 
 // Decode attention over pages held in 4 bits, q and o bf16 (kv4_rows.cu).
+bool kv4_decode_fits(int n_seqs, int max_kv_len, int H, int G);
 size_t kv4_decode_workspace_bytes(int n_seqs, int max_kv_len, int H, int G, int D);
 cudaError_t launch_kv4_decode(const bf16 *q, const uint8_t *k, const uint8_t *v, bf16 *o, const PagedView &pv,
                               const int *kv_lens, int n_seqs, int max_kv_len, int H, int G, int D, void *workspace,

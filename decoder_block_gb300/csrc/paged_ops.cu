@@ -156,6 +156,7 @@ llama_status check_decode(int32_t dtype, int32_t pages, const void *q, const lla
   if (!dtype_ok(dtype) || kv == nullptr || n_seqs < 0 || max_kv_len < 0) return LLAMA_ERR_INVALID_ARG;
   llama_status s = check_heads(H, G, D);
   if (s == LLAMA_OK && (n_seqs > LLAMA_PACKED_MAX_SEQS || max_kv_len > LLAMA_PACKED_MAX_KV)) s = LLAMA_ERR_UNSUPPORTED;
+  if (s == LLAMA_OK && pages == KV4_PAGES && !kv4_decode_fits(n_seqs, max_kv_len, H, G)) s = LLAMA_ERR_UNSUPPORTED;
   if (s == LLAMA_OK) s = view_of(kv, pages, G, D, pv);
   if (s != LLAMA_OK) return s;
   if (n_seqs == 0) return LLAMA_OK;
@@ -331,6 +332,7 @@ llama_status llama_op_attention_paged_decode(int32_t dtype, const void *q, const
 
 size_t llama_op_attention_paged_decode_kv4_workspace_bytes(int32_t dtype, int32_t n_seqs, int32_t max_kv_len,
                                                            int32_t H, int32_t G, int32_t D) {
+  if (decode_sizes_ok(n_seqs, max_kv_len, H, G, D) && !kv4_decode_fits(n_seqs, max_kv_len, H, G)) return 0;
   if (dtype != LLAMA_BF16 || !decode_sizes_ok(n_seqs, max_kv_len, H, G, D))
     return llama_op_attention_paged_decode_workspace_bytes(dtype, n_seqs, max_kv_len, H, G, D);
   return kv4_decode_workspace_bytes(n_seqs, max_kv_len, H, G, D);

@@ -29,6 +29,7 @@ namespace {
 
 constexpr int VD_THREADS = 256;
 constexpr int VD_WARPS = VD_THREADS / 32;
+constexpr int VD_MOST_THREADS = 1024;  // of a CTA that draws
 constexpr int VD_VECS = 4;          // 16-byte vectors of a thread in flight
 // CTAs of an SM, and CTAs for an SM that the parts aim at: 265 MB in 47 us, 0.82 of the measured
 // rate (4 and 16: 48; rows left in L2 for the drawing, by loads that do not say that they
@@ -38,6 +39,7 @@ constexpr int VD_PREFETCH = 32;     // pieces that a CTA asks for
 constexpr int VD_RACE = 2;          // of each of a race's rows
 constexpr int VD_MAX_PARTS = 32;    // of a row: a lane each when they are added up
 constexpr int VD_MIN_PART = 4096;   // logits of a part, at least
+constexpr int VD_MIN_RACE = 1024;   // ids of a CTA of a cluster, at least
 constexpr int VD_MAX_CLUSTER = 8;
 constexpr float VD_LOG2E = 1.4426950408889634f;
 
@@ -303,14 +305,14 @@ struct VdBest {
 };
 
 template <typename T>
-__global__ void __launch_bounds__(VD_THREADS) verify_draw_kernel(const __grid_constant__ VdArgs a) {
+__global__ void __launch_bounds__(VD_MOST_THREADS) verify_draw_kernel(const __grid_constant__ VdArgs a) {
   constexpr int MOST = LLAMA_MAX_DRAFTS + 1;
   __shared__ float s_m[2][MOST], s_z[2][MOST];
   __shared__ int s_id[MOST];
   __shared__ bool s_keep[MOST];
-  __shared__ VdBest s_best[VD_WARPS];
+  __shared__ VdBest s_best[VD_MOST_THREADS / 32];
   __shared__ VdBest s_cta[VD_MAX_CLUSTER];  // of the cluster's first CTA: every CTA's
-  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, threads = blockDim.x, warps = threads / 32;
   const int seq = blockIdx.x / a.cluster, rank = blockIdx.x % a.cluster;
   if (a.cluster > 1) ptx::cluster_sync();  // every CTA runs: the first one's shared memory may be written
   grid_dependency_wait();
@@ -325,15 +327,15 @@ __global__ void __launch_bounds__(VD_THREADS) verify_draw_kernel(const __grid_co
     const bool greedy = t == 0.f;
     if (!greedy && threadIdx.x < VD_PREFETCH) {
       // this CTA's share of the noise, which does not wait for the decisions, into L2
-      const int ids = (a.V + VD_PREFETCH * a.cluster - 1) / (VD_PREFETCH * a.cluster);
-      const int from = (rank * VD_PREFETCH + (int)threadIdx.x) * ids, to = min(a.V, from + ids);
+      const long long ids = ((long long)a.V + VD_PREFETCH * a.cluster - 1) / (VD_PREFETCH * a.cluster);
+      const long long from = (rank * VD_PREFETCH + (int)threadIdx.x) * ids, to = min((long long)a.V, from + ids);
       const uintptr_t p = reinterpret_cast<uintptr_t>(a.noise + (size_t)seq * a.noise_stride);
       const uintptr_t b0 = (p + 4 * (uintptr_t)from + 15) & ~uintptr_t(15), b1 = (p + 4 * (uintptr_t)max(from, to)) & ~uintptr_t(15);
       if (b1 > b0)
         asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(b0), "r"((uint32_t)(b1 - b0)) : "memory");
     }
     const float c = greedy ? VD_LOG2E : VD_LOG2E / t;
-    for (int k = warp; k < n; k += VD_WARPS) {
+    for (int k = warp; k < n; k += warps) {
       const VdPart p = row_sum(a, first + k, 0, c);
       const bool has_draft = a.draft != nullptr && !greedy && k + 1 < n;
       VdPart q{0.f, 0.f, 0, 0};
@@ -378,7 +380,8 @@ __global__ void __launch_bounds__(VD_THREADS) verify_draw_kernel(const __grid_co
     const bool refused = kept + 1 < n;
     const float z = s_z[0][kept];
     if (greedy) {
-      token = row_ok(z) ? s_id[kept] : -1;
+      // (offsets that descend may leave rows that no CTA has summed: any id may stand there)
+      token = row_ok(z) && (unsigned)s_id[kept] < (unsigned)a.V ? s_id[kept] : -1;
     } else if (row_ok(z)) {
       const T *x = reinterpret_cast<const T *>(a.target) + (size_t)(first + kept) * a.target_stride;
       const float *noise = a.noise + (size_t)seq * a.noise_stride;
@@ -406,7 +409,7 @@ __global__ void __launch_bounds__(VD_THREADS) verify_draw_kernel(const __grid_co
       };
       constexpr int N = Vec16<T>::N;
       const int ax = align_of(x), ay = both ? align_of(y) : 16, ae = align_of(noise);
-      const int stride = a.cluster * VD_THREADS, me = rank * VD_THREADS + (int)threadIdx.x;
+      const int stride = a.cluster * threads, me = rank * threads + (int)threadIdx.x;
       auto search = [&](bool residual) {
         const int groups = a.V / N;
         for (int v = me; v < groups; v += VD_RACE * stride) {
@@ -441,7 +444,7 @@ __global__ void __launch_bounds__(VD_THREADS) verify_draw_kernel(const __grid_co
         if (lane == 0) s_best[warp] = best;
         __syncthreads();
         if (threadIdx.x == 0)
-          for (int w = 1; w < VD_WARPS; ++w) best.join(s_best[w].score, s_best[w].id);
+          for (int w = 1; w < warps; ++w) best.join(s_best[w].score, s_best[w].id);
         __syncthreads();
       };
       // the CTA's best into the first CTA's array, through distributed shared memory
@@ -481,7 +484,7 @@ __global__ void __launch_bounds__(VD_THREADS) verify_draw_kernel(const __grid_co
     }
   }
   if (rank != 0) return;
-  for (int k = threadIdx.x; k < width; k += VD_THREADS) {
+  for (int k = threadIdx.x; k < width; k += threads) {
     int x = -1;
     float lp = 0.f;
     if (k < kept) x = ld_after_wait(a.tokens + first + k + 1);
@@ -543,9 +546,9 @@ cudaError_t launch_verify_drafts(const T *target, long long target_stride, const
                                      dim3(VD_THREADS), 0, st, a);
     if (e != cudaSuccess) return e;
   }
-  // clusters as large as keep every SM at work, a CTA not below VD_MIN_PART ids
+  // clusters as large as keep every SM at work, a CTA not below VD_MIN_RACE ids
   a.cluster = 1;
-  while (a.cluster < VD_MAX_CLUSTER && 2LL * a.cluster * b.n_seqs <= 4LL * sm_count() && V / (2 * a.cluster) >= VD_MIN_PART)
+  while (a.cluster < VD_MAX_CLUSTER && 2LL * a.cluster * b.n_seqs <= 4LL * sm_count() && V / (2 * a.cluster) >= VD_MIN_RACE)
     a.cluster *= 2;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -555,7 +558,10 @@ cudaError_t launch_verify_drafts(const T *target, long long target_stride, const
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(b.n_seqs * a.cluster));
-  cfg.blockDim = dim3(VD_THREADS);
+  // few sequences: as many loads in flight as an SM has room for (two of 125880 ids 25 -> 21 us)
+  cfg.blockDim = dim3(a.cluster == VD_MAX_CLUSTER && b.n_seqs * a.cluster <= sm_count() && V >= VD_MOST_THREADS * VD_MAX_CLUSTER * 8
+                          ? VD_MOST_THREADS
+                          : VD_THREADS);
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = a.cluster > 1 ? 2 : 1;

@@ -276,6 +276,13 @@ def test_bad_inputs_are_reported(lb):
     d = c.run(lb)
     assert d.out[0].tolist() == [-1, -1, -1] and d.out[1].tolist() == [-1, -1, -1]
     assert int(d.status[0]) == lb.LLAMA_ERR_RANGE
+    for greedy in (True, False):  # rows that no part of the sums has seen
+        c = Drafts("bo2", "f32", 5000, [2, 2, 2], [1.0], greedy=greedy)
+        c.offsets = np.array([0, 3, 1, 4], np.int32)
+        d = c.run(lb, ws=torch().randint(0, 256, (1 << 16,), dtype=torch().uint8, device="cuda"))
+        assert int(d.status[0]) == lb.LLAMA_ERR_RANGE
+        assert d.out[1].tolist() == [-1, -1, -1]
+        assert int(d.out.max()) < 5000 and int(d.out.min()) >= -1
 
 
 def test_any_alignment(lb):
