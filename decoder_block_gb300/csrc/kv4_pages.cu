@@ -18,15 +18,14 @@ namespace {
 
 constexpr int KW_THREADS = 256;
 constexpr int KW_CTAS = 3;   // CTAs of an SM
-constexpr int KW_ROWS = 16;  // rows of a CTA, at most
+constexpr int KW_ROWS = 8;   // places for a CTA's rows
 constexpr int KW_UNITS = 2;  // rows of a thread in flight
 constexpr int KR_UNITS = 4;
-#ifndef KW_MOST
-#define KW_MOST 4
-#endif
-#ifndef KR_MOST
-#define KR_MOST 8
-#endif
+// Rows of a CTA at most, written and read: finding their places is shared, but the last CTAs are
+// longer.  (8192 rows of 4096 + 2 * 1024 bf16 written: 92, 61, 52, 54 and 54 us at 1, 2, 4, 8 and
+// 16; 40000 rows of 2 * 1024 read: 100, 63, 46, 41 and 41.  Asking for the rows to be written
+// before their places are known gains nothing: 53.)
+constexpr int KW_MOST = 4, KR_MOST = 8;
 
 struct KwArgs {
   PagedView pv;
@@ -95,119 +94,120 @@ __global__ void __launch_bounds__(KW_THREADS, KW_CTAS)
   // Keys and values first: theirs is the longer way.
   const int kv_units = 2 * a.G * (a.D / N), kv_rows = KW_THREADS / a.kv_lanes;
   for (int u = threadIdx.x & (a.kv_lanes - 1); u < kv_units; u += a.kv_lanes) {
-   const int head = u / (a.D / N), e = u % (a.D / N) * (N / 2);  // elements e .., and those D / 2 further
-   const bool key = head < a.G;
-   uint8_t *const block = (key ? kc : vc) + (long long)(key ? head : head - a.G) * kv4_block_bytes(1 << a.pv.page_log2, a.D);
-   const T *const first = qkv + ((size_t)t0 * heads + a.H + head) * a.D;
-   for (int row = threadIdx.x / a.kv_lanes; row < a.rows; row += kv_rows) {
-    const int pos = s_pos[row];
-    const long long page = s_page[row];
-    if (pos < 0 || page < 0) continue;
-    const T *src = first + (size_t)row * (heads * a.D);
-    float x[N];
+    const int head = u / (a.D / N), e = u % (a.D / N) * (N / 2);  // elements e .., and those D / 2 further
+    const bool key = head < a.G;
+    uint8_t *const block =
+        (key ? kc : vc) + (long long)(key ? head : head - a.G) * kv4_block_bytes(1 << a.pv.page_log2, a.D);
+    const T *const first = qkv + ((size_t)t0 * heads + a.H + head) * a.D;
+    for (int row = threadIdx.x / a.kv_lanes; row < a.rows; row += kv_rows) {
+      const int pos = s_pos[row];
+      const long long page = s_page[row];
+      if (pos < 0 || page < 0) continue;
+      const T *src = first + (size_t)row * (heads * a.D);
+      float x[N];
 #pragma unroll
-    for (int j = 0; j < N; j += V) {
-      Vec16<T> v;
-      v.raw = ld_once_after_wait(src + (j < N / 2 ? e + j : a.D / 2 + e + j - N / 2));
+      for (int j = 0; j < N; j += V) {
+        Vec16<T> v;
+        v.raw = ld_once_after_wait(src + (j < N / 2 ? e + j : a.D / 2 + e + j - N / 2));
 #pragma unroll
-      for (int k = 0; k < V; ++k) x[j + k] = v.get(k);
-    }
-    if (key && a.halves) {
-      const float4 *c = reinterpret_cast<const float4 *>(angles(pos, e));
-#pragma unroll
-      for (int j = 0; j < N / 2; j += 2) {
-        const float4 f = __ldg(c + j / 2);
-        turn(x[j], x[N / 2 + j], make_float2(f.x, f.y), x[j], x[N / 2 + j]);
-        turn(x[j + 1], x[N / 2 + j + 1], make_float2(f.z, f.w), x[j + 1], x[N / 2 + j + 1]);
+        for (int k = 0; k < V; ++k) x[j + k] = v.get(k);
       }
-    } else if (key) {
+      if (key && a.halves) {
+        const float4 *c = reinterpret_cast<const float4 *>(angles(pos, e));
 #pragma unroll
-      for (int j = 0; j < N; j += 4) {
-        const float4 f = __ldg(reinterpret_cast<const float4 *>(
-            angles(pos, j < N / 2 ? (e + j) / 2 : (a.D / 2 + e + j - N / 2) / 2)));
-        turn(x[j], x[j + 1], make_float2(f.x, f.y), x[j], x[j + 1]);
-        turn(x[j + 2], x[j + 3], make_float2(f.z, f.w), x[j + 2], x[j + 3]);
+        for (int j = 0; j < N / 2; j += 2) {
+          const float4 f = __ldg(c + j / 2);
+          turn(x[j], x[N / 2 + j], make_float2(f.x, f.y), x[j], x[N / 2 + j]);
+          turn(x[j + 1], x[N / 2 + j + 1], make_float2(f.z, f.w), x[j + 1], x[N / 2 + j + 1]);
+        }
+      } else if (key) {
+#pragma unroll
+        for (int j = 0; j < N; j += 4) {
+          const float4 f = __ldg(reinterpret_cast<const float4 *>(
+              angles(pos, j < N / 2 ? (e + j) / 2 : (a.D / 2 + e + j - N / 2) / 2)));
+          turn(x[j], x[j + 1], make_float2(f.x, f.y), x[j], x[j + 1]);
+          turn(x[j + 2], x[j + 3], make_float2(f.z, f.w), x[j + 2], x[j + 3]);
+        }
       }
-    }
-    const int slot = pos & ((1 << a.pv.page_log2) - 1);
-    uint8_t *codes = block + page + slot * kv4_code_bytes(a.D);
-    uint8_t *scales = block + page + (kv4_code_bytes(a.D) << a.pv.page_log2) + slot * kv4_scale_bytes(a.D);
-    bool bad = false;
-    // blocks of 16: at e and, with N = 32, at e + D / 2
+      const int slot = pos & ((1 << a.pv.page_log2) - 1);
+      uint8_t *codes = block + page + slot * kv4_code_bytes(a.D);
+      uint8_t *scales = block + page + (kv4_code_bytes(a.D) << a.pv.page_log2) + slot * kv4_scale_bytes(a.D);
+      bool bad = false;
+      // blocks of 16: at e and, with N = 32, at e + D / 2
 #pragma unroll
-    for (int j = 0; j < N / KV4_BLOCK; ++j) {
-      const int at = N == 32 ? e + j * (a.D / 2) : 0;
-      uint32_t w[2];
-      const uint32_t byte = kv4_quantise(reinterpret_cast<float(&)[KV4_BLOCK]>(x[j * KV4_BLOCK]), w, bad);
-      *reinterpret_cast<uint2 *>(codes + at / 2) = make_uint2(w[0], w[1]);
-      scales[at / KV4_BLOCK] = (uint8_t)byte;
+      for (int j = 0; j < N / KV4_BLOCK; ++j) {
+        const int at = N == 32 ? e + j * (a.D / 2) : 0;
+        uint32_t w[2];
+        const uint32_t byte = kv4_quantise(reinterpret_cast<float(&)[KV4_BLOCK]>(x[j * KV4_BLOCK]), w, bad);
+        *reinterpret_cast<uint2 *>(codes + at / 2) = make_uint2(w[0], w[1]);
+        scales[at / KV4_BLOCK] = (uint8_t)byte;
+      }
+      if (bad) report_status(a.status, LLAMA_ERR_RANGE);
     }
-    if (bad) report_status(a.status, LLAMA_ERR_RANGE);
-   }
   }
 
   const int q_units = a.H * per_head, q_rows = KW_THREADS / a.q_lanes;
   for (int u = threadIdx.x & (a.q_lanes - 1); u < q_units; u += a.q_lanes) {
-   const int head = u / per_head, e = u % per_head * V;
-   const T *const q_first = qkv + ((size_t)t0 * heads + head) * a.D + e;
-   T *const out = q_out + ((size_t)t0 * a.H + head) * a.D + e;
-   for (int r0 = threadIdx.x / a.q_lanes; r0 < a.rows; r0 += KW_UNITS * q_rows) {
-    Vec16<T> x[KW_UNITS], y[KW_UNITS];
-    float4 cs[KW_UNITS][V / 2];
-    int pos[KW_UNITS];
-    size_t at[KW_UNITS];
+    const int head = u / per_head, e = u % per_head * V;
+    const T *const q_first = qkv + ((size_t)t0 * heads + head) * a.D + e;
+    T *const out = q_out + ((size_t)t0 * a.H + head) * a.D + e;
+    for (int r0 = threadIdx.x / a.q_lanes; r0 < a.rows; r0 += KW_UNITS * q_rows) {
+      Vec16<T> x[KW_UNITS], y[KW_UNITS];
+      float4 cs[KW_UNITS][V / 2];
+      int pos[KW_UNITS];
+      size_t at[KW_UNITS];
 #pragma unroll
-    for (int k = 0; k < KW_UNITS; ++k) {
-      const int row = r0 + k * q_rows;
-      pos[k] = row < a.rows ? s_pos[row] : -2;
-      if (pos[k] == -2) continue;
-      const T *src = q_first + (size_t)row * (heads * a.D);
-      at[k] = (size_t)row * (a.H * a.D);
-      x[k].raw = ld_once_after_wait(src);
-      y[k].raw = ld_once_after_wait(src + a.D / 2);
-      if (pos[k] >= 0) {
-        // the unit's V pairs: (e + j, e + j + D/2); or (e + 2j, e + 2j + 1), then those D/2 further
-        const float4 *c = reinterpret_cast<const float4 *>(angles(pos[k], a.halves ? e : e / 2));
-        const float4 *c2 = a.halves ? c + V / 4 : c + a.D / 8;
+      for (int k = 0; k < KW_UNITS; ++k) {
+        const int row = r0 + k * q_rows;
+        pos[k] = row < a.rows ? s_pos[row] : -2;
+        if (pos[k] == -2) continue;
+        const T *src = q_first + (size_t)row * (heads * a.D);
+        at[k] = (size_t)row * (a.H * a.D);
+        x[k].raw = ld_once_after_wait(src);
+        y[k].raw = ld_once_after_wait(src + a.D / 2);
+        if (pos[k] >= 0) {
+          // the unit's V pairs: (e + j, e + j + D/2); or (e + 2j, e + 2j + 1), then those D/2 further
+          const float4 *c = reinterpret_cast<const float4 *>(angles(pos[k], a.halves ? e : e / 2));
+          const float4 *c2 = a.halves ? c + V / 4 : c + a.D / 8;
 #pragma unroll
-        for (int j = 0; j < V / 4; ++j) {
-          cs[k][j] = __ldg(c + j);
-          cs[k][V / 4 + j] = __ldg(c2 + j);
+          for (int j = 0; j < V / 4; ++j) {
+            cs[k][j] = __ldg(c + j);
+            cs[k][V / 4 + j] = __ldg(c2 + j);
+          }
         }
       }
-    }
 #pragma unroll
-    for (int k = 0; k < KW_UNITS; ++k) {
-      if (pos[k] == -2) continue;
-      Vec16<T> p, q;
-      if (pos[k] < 0) {
-        p.raw = q.raw = make_uint4(0, 0, 0, 0);
-      } else {
-        const float2 *c = reinterpret_cast<const float2 *>(cs[k]);
-        float f, g;
-        if (a.halves) {
-#pragma unroll
-          for (int j = 0; j < V; ++j) {
-            turn(x[k].get(j), y[k].get(j), c[j], f, g);
-            p.set(j, f);
-            q.set(j, g);
-          }
+      for (int k = 0; k < KW_UNITS; ++k) {
+        if (pos[k] == -2) continue;
+        Vec16<T> p, q;
+        if (pos[k] < 0) {
+          p.raw = q.raw = make_uint4(0, 0, 0, 0);
         } else {
+          const float2 *c = reinterpret_cast<const float2 *>(cs[k]);
+          float f, g;
+          if (a.halves) {
 #pragma unroll
-          for (int j = 0; j < V / 2; ++j) {
-            turn(x[k].get(2 * j), x[k].get(2 * j + 1), c[j], f, g);
-            p.set(2 * j, f);
-            p.set(2 * j + 1, g);
-            turn(y[k].get(2 * j), y[k].get(2 * j + 1), c[V / 2 + j], f, g);
-            q.set(2 * j, f);
-            q.set(2 * j + 1, g);
+            for (int j = 0; j < V; ++j) {
+              turn(x[k].get(j), y[k].get(j), c[j], f, g);
+              p.set(j, f);
+              q.set(j, g);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < V / 2; ++j) {
+              turn(x[k].get(2 * j), x[k].get(2 * j + 1), c[j], f, g);
+              p.set(2 * j, f);
+              p.set(2 * j + 1, g);
+              turn(y[k].get(2 * j), y[k].get(2 * j + 1), c[V / 2 + j], f, g);
+              q.set(2 * j, f);
+              q.set(2 * j + 1, g);
+            }
           }
         }
+        store16(out + at[k], p);
+        store16(out + at[k] + a.D / 2, q);
       }
-      store16(out + at[k], p);
-      store16(out + at[k] + a.D / 2, q);
     }
-   }
   }
 }
 
@@ -234,43 +234,43 @@ __global__ void __launch_bounds__(KW_THREADS) kv4_read_kernel(T *k_out, T *v_out
   const int head_units = a.G << a.word_log2, units = 2 * head_units;  // of a row: k's, then v's
   const int slot_mask = (1 << a.pv.page_log2) - 1, step = KW_THREADS / a.lanes;
   for (int u = threadIdx.x & (a.lanes - 1); u < units; u += a.lanes) {
-   const bool value = u >= head_units;
-   T *const out = value ? v_out : k_out;
-   if (out == nullptr) continue;
-   const int g = (value ? u - head_units : u) >> a.word_log2, e = u & ((1 << a.word_log2) - 1);
-   const Kv4Row first = kv4_row(value ? a.v : a.k, a.pv, 0, g, a.D, 0);
-   const uint8_t *const codes = first.codes + 4 * e, *const scales = first.scales + e / 2;
-   T *const dst0 = out + ((size_t)t0 * a.G + g) * a.D + e * 8;
-   for (int r0 = threadIdx.x / a.lanes; r0 < a.rows; r0 += KR_UNITS * step) {
-    uint32_t w[KR_UNITS], byte[KR_UNITS];
-    T *dst[KR_UNITS];
+    const bool value = u >= head_units;
+    T *const out = value ? v_out : k_out;
+    if (out == nullptr) continue;
+    const int g = (value ? u - head_units : u) >> a.word_log2, e = u & ((1 << a.word_log2) - 1);
+    const Kv4Row first = kv4_row(value ? a.v : a.k, a.pv, 0, g, a.D, 0);
+    const uint8_t *const codes = first.codes + 4 * e, *const scales = first.scales + e / 2;
+    T *const dst0 = out + ((size_t)t0 * a.G + g) * a.D + e * 8;
+    for (int r0 = threadIdx.x / a.lanes; r0 < a.rows; r0 += KR_UNITS * step) {
+      uint32_t w[KR_UNITS], byte[KR_UNITS];
+      T *dst[KR_UNITS];
 #pragma unroll
-    for (int i = 0; i < KR_UNITS; ++i) {
-      const int row = r0 + i * step;
-      dst[i] = nullptr;
-      w[i] = 0x88888888u;  // zeros
-      byte[i] = 0;
-      const int pos = row < a.rows ? s_pos[row] : -2;
-      if (pos == -2) continue;
-      dst[i] = dst0 + (size_t)row * (a.G * a.D);
-      const long long page = s_page[row];
-      if (page < 0) continue;
-      const int slot = pos & slot_mask;
-      w[i] = (uint32_t)ld_after_wait(reinterpret_cast<const int *>(codes + page + slot * kv4_code_bytes(a.D)));
-      asm volatile("ld.global.u8 %0, [%1];" : "=r"(byte[i]) : "l"(scales + page + slot * kv4_scale_bytes(a.D)));
-    }
+      for (int i = 0; i < KR_UNITS; ++i) {
+        const int row = r0 + i * step;
+        dst[i] = nullptr;
+        w[i] = 0x88888888u;  // zeros
+        byte[i] = 0;
+        const int pos = row < a.rows ? s_pos[row] : -2;
+        if (pos == -2) continue;
+        dst[i] = dst0 + (size_t)row * (a.G * a.D);
+        const long long page = s_page[row];
+        if (page < 0) continue;
+        const int slot = pos & slot_mask;
+        w[i] = (uint32_t)ld_after_wait(reinterpret_cast<const int *>(codes + page + slot * kv4_code_bytes(a.D)));
+        asm volatile("ld.global.u8 %0, [%1];" : "=r"(byte[i]) : "l"(scales + page + slot * kv4_scale_bytes(a.D)));
+      }
 #pragma unroll
-    for (int i = 0; i < KR_UNITS; ++i) {
-      if (dst[i] == nullptr) continue;
-      if constexpr (sizeof(T) == 2) {
-        *reinterpret_cast<uint4 *>(dst[i]) = kv4_eight(w[i], kv4_scales(byte[i]));
-      } else {
-        const float s = kv4_scale(byte[i]);
-        reinterpret_cast<float4 *>(dst[i])[0] = kv4_four(w[i], 0, s);
-        reinterpret_cast<float4 *>(dst[i])[1] = kv4_four(w[i], 1, s);
+      for (int i = 0; i < KR_UNITS; ++i) {
+        if (dst[i] == nullptr) continue;
+        if constexpr (sizeof(T) == 2) {
+          *reinterpret_cast<uint4 *>(dst[i]) = kv4_eight(w[i], kv4_scales(byte[i]));
+        } else {
+          const float s = kv4_scale(byte[i]);
+          reinterpret_cast<float4 *>(dst[i])[0] = kv4_four(w[i], 0, s);
+          reinterpret_cast<float4 *>(dst[i])[1] = kv4_four(w[i], 1, s);
+        }
       }
     }
-   }
   }
 }
 
