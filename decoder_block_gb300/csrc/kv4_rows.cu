@@ -41,6 +41,11 @@ namespace {
 // Keys of a warp's tile: as many as the registers have room for, what is done once a tile is a
 // third of a tile of 32 keys.
 constexpr int kd_keys(int NB) { return NB == 1 ? 64 : 32; }
+// Places before an item's first tile in the row that is dealt out: an item's beginning and end
+// (its queries, its output) take as long as 64 keys.  (64 sequences of 253 to 4096 keys, 8 KV
+// heads of 4 rows: 43.7, 41.2, 42.6 us with 0, 1, 2 tiles of 64 keys; of 20 rows, tiles of 32:
+// 75.5, 72.7, 71.4, 71.8 with 0, 1, 2, 3.)
+constexpr int kd_start(int NB) { return 64 / kd_keys(NB); }
 constexpr float KD_RESCALE = 8.0f;  // log2 units: the running maximum is raised when it grows by > 2^8
 // Weights are fp16 for their product with V: 2^7 times what they are, so that the largest,
 // 2^15, has room above, and what is less than 2^-31 of the running maximum's, not 2^-24, is
@@ -51,6 +56,7 @@ constexpr float KD_VALUE = 2.0f;  // V's operand is half of V
 constexpr int KD_DIRECT_KEYS = 2048;
 constexpr int KD_MAX_NB = 3;
 constexpr int KD_ROUNDS = 10, KD_FEW_KEYS = 384;  // of packed calls: see kv4_rows_fit
+constexpr int KD_BATCH = 2;  // pieces that a join within a CTA reads at a time
 constexpr int KD_LEAST = 4;  // tiles of a CTA's run, at least: a warp on each scheduler
 
 // NB: blocks of 8 rows of an item.
@@ -85,7 +91,7 @@ struct KdArgs {
   int direct;
   float scale_log2;
   float *part;  // [CTA][2][8 NB][D + 2]
-  int4 *spans;  // of each CTA: sequence, unit and last CTA of the item that it begins and leaves (-1: none)
+  int4 *spans;  // of each CTA, the item that it begins and leaves: two, its last CTA (-1: none) and as KdOut has it
   int *status;
 };
 
@@ -122,8 +128,9 @@ struct KdOut {
 };
 
 // Sums of a fragment's columns -- steps i of rows 8 b + 2 ti + e, a float2 of each lane -- over
-// the pieces piece(0) .. piece(n - 1), in that order.  SPLIT: warps that share the steps.
-template <int D, int NB, int SPLIT>
+// the pieces piece(0) .. piece(n - 1), in that order, BATCH of them read at a time.  SPLIT:
+// warps that share the steps.
+template <int D, int NB, int SPLIT, int BATCH>
 struct KdSum {
   static constexpr int STEPS = D / 16 / SPLIT;
   int i0;  // the first of the steps
@@ -134,18 +141,45 @@ struct KdSum {
     const int lane = threadIdx.x & 31, h = be / 2 * 8 + (lane & 3) * 2 + (be & 1);
 #pragma unroll
     for (int i = 0; i < STEPS; ++i) x[i] = make_float2(0.f, 0.f);
-#pragma unroll 16
-    for (int s = 0; s < n; ++s) top = fmaxf(top, piece(s)[8 * NB * D + h]);
-#pragma unroll(SPLIT > 1 ? 8 : 4)
-    for (int s = 0; s < n; ++s) {
-      const float *p = piece(s);
-      const float f = ptx::ex2_approx(p[8 * NB * D + h] - top);
-      l = fmaf(f, p[8 * NB * (D + 1) + h], l);
+#pragma unroll 1
+    for (int s = 0; s < n; s += BATCH) {
+      float m[BATCH], w[BATCH];
+      float2 v[BATCH][STEPS];
+#pragma unroll
+      for (int k = 0; k < BATCH; ++k) {
+        m[k] = -FLT_MAX;
+        w[k] = 0.f;
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) v[k][i] = make_float2(0.f, 0.f);
+        if (s + k < n) {
+          const float *p = piece(s + k);
+          m[k] = p[8 * NB * D + h];
+          w[k] = p[8 * NB * (D + 1) + h];
+#pragma unroll
+          for (int i = 0; i < STEPS; ++i)
+            v[k][i] = *reinterpret_cast<const float2 *>(p + (be * (D / 16) + i0 + i) * 64 + lane * 2);
+        }
+      }
+      float up = top;
+#pragma unroll
+      for (int k = 0; k < BATCH; ++k) up = fmaxf(up, m[k]);
+      const float less = ptx::ex2_approx(top - up);
+      top = up;
+      l *= less;
 #pragma unroll
       for (int i = 0; i < STEPS; ++i) {
-        const float2 v = *reinterpret_cast<const float2 *>(p + (be * (D / 16) + i0 + i) * 64 + lane * 2);
-        x[i].x = fmaf(f, v.x, x[i].x);
-        x[i].y = fmaf(f, v.y, x[i].y);
+        x[i].x *= less;
+        x[i].y *= less;
+      }
+#pragma unroll
+      for (int k = 0; k < BATCH; ++k) {
+        const float f = ptx::ex2_approx(m[k] - up);
+        l = fmaf(f, w[k], l);
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) {
+          x[i].x = fmaf(f, v[k][i].x, x[i].x);
+          x[i].y = fmaf(f, v[k][i].y, x[i].y);
+        }
       }
     }
   }
@@ -250,12 +284,12 @@ struct KdCursor {
     const long long rest = at - (long long)first[lo] * a.times;
     set(a, lo, 0, 0);
     // (a 64-bit division takes some hundred cycles)
-    const int u = rest <= 0x7fffffffLL ? (int)rest / n : (int)(rest / n);
+    const int slots = n + kd_start(NB), u = rest <= 0x7fffffffLL ? (int)rest / slots : (int)(rest / slots);
     const int subs = units / a.G;
     unit = u;
     g = u / subs;
     sub = u - g * subs;
-    j = (int)(rest - (long long)u * n);
+    j = (int)(rest - (long long)u * slots) - kd_start(NB);
   }
   __device__ __forceinline__ bool next(const KdArgs &a, const int *first) {  // true: it is another item's
     if (++j < n || a.direct) return false;
@@ -266,7 +300,7 @@ struct KdCursor {
       }
       if (i == a.b.n_seqs) return false;  // the end of the row
     }
-    set(a, i, u, 0);
+    set(a, i, u, -kd_start(NB));
     return true;
   }
 };
@@ -322,6 +356,7 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_rows_kerne
         else if (ld_after_wait(a.b.kv_lens + i) != s.kv_len) report_status(a.status, LLAMA_ERR_RANGE);
       }
       int n = kd_tiles<NB>(s.kv_len);
+      if (n > 0) n += kd_start(NB);
       if (a.b.q_offsets != nullptr) n = min((long long)n * ((s.count * a.r + 8 * NB - 1) / (8 * NB)), (long long)a.most);
       blind |= s.kv_len < s.count;
       first[i] = n;
@@ -428,6 +463,11 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_rows_kerne
       s_id = ld_after_wait(table + (ps >> a.pv.page_log2));
       s_slot = ps & rows_mask;
     };
+    auto to_tile = [](KdCursor<NB> &c, int rest) {  // over the places before an item's first tile
+      const int step = min(max(-c.j, 0), rest);
+      c.j += step;
+      return step;
+    };
     auto request = [&] {
       if (left > 0) {
         const uint32_t stage = ring + fill * L::STAGE, to = stage + lane * CHUNK;
@@ -453,7 +493,8 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_rows_kerne
             for (int r = 0; r < RUNS; r += D >= 64 ? 1 : 2) {
               const int in = wide ? 0 : r, r1 = D >= 64 ? in : wide ? 0 : r + 1;
               const int my_id = D >= 64 || lane < 16 ? id[in] : id[r1];
-              const int my_slot = (D >= 64 || lane < 16 ? slot[in] : slot[r1]) + (wide ? (r + (D >= 64 ? 0 : lane / 16)) * 16 : 0);
+              const int my_slot = (D >= 64 || lane < 16 ? slot[in] : slot[r1]) +
+                                  (wide ? (r + (D >= 64 ? 0 : lane / 16)) * 16 : 0);
               const uint8_t *p = (which ? from_v : from_k) + (uint64_t)(uint32_t)my_id * stride + my_slot * L::RB;
               const uint32_t dst = to + which * L::HALF + r * 16 * L::RB;
 #pragma unroll
@@ -475,12 +516,16 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_rows_kerne
             copy_async<16>(stage + (S_COPIES > 1 ? i : lane / S_PIECES) * L::HALF + L::KEYS * L::RB + s_piece * 16,
                            from_s[i] + off);
         }
-        if (ahead.next(a, first)) aim();
         --left;
+        if (ahead.next(a, first)) {
+          aim();
+          left -= to_tile(ahead, left);
+        }
         fill = fill + 1 == L::STAGES ? 0 : fill + 1;
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
     };
+    left -= to_tile(ahead, left);
     aim();
     look_up();
 #pragma unroll 1
@@ -489,7 +534,7 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_rows_kerne
       look_up();
     }
     int done = 0, use = 0;
-    while (done < todo) {
+    while ((done += to_tile(at, todo - done)) < todo) {
       // ----------------------------------------------------------- a piece ---
       const int seq = at.seq, unit = at.unit, j0 = at.j, n_tiles = at.n, g = at.g;
       const int j1 = min(n_tiles, j0 + todo - done);
@@ -550,40 +595,40 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_rows_kerne
             for (int e = 0; e < 4; ++e) sc[mb][b][e] = 0.f;
 #pragma unroll
         for (int m0 = 0; m0 < MB; m0 += 2) {
-        uint32_t w[4][KW];
-        Kv4Scale sa[4], sb[4];
+          uint32_t w[4][KW];
+          Kv4Scale sa[4], sb[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int row = m0 * 16 + e * 8 + gi;
-          const uint32_t scales = sk + L::KEYS * L::RB + row * L::SB;
-          if constexpr (D >= 32) ld_words<KW>(sk + row * L::RB + ti * (D / 8), w[e]);
-          else ld_words<KW>(sk + row * L::RB + ti / 2 * 4, w[e]);
-          if constexpr (D == 16) w[e][0] >>= 8 * (ti & 1);
-          if constexpr (D == 128) {
-            uint16_t x;
-            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(scales + ti * 2));
-            sa[e] = kv4_scales((uint32_t)x & 255);
-            sb[e] = kv4_scales((uint32_t)x >> 8);
-          } else {
-            sa[e] = kv4_scales(ld_byte(scales + (D == 64 ? ti : D == 32 ? ti / 2 : 0)));
-            sb[e] = sa[e];
-          }
-        }
-#pragma unroll
-        for (int s = 0; s < STEPS; ++s)
-#pragma unroll
-          for (int mb = 0; mb < 2; ++mb) {
-            uint32_t f[4];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              const uint32_t word = w[2 * mb + e][s / 2];
-              const Kv4Scale &k = s < 4 ? sa[2 * mb + e] : sb[2 * mb + e];
-              f[e] = s % 2 == 0 ? kv4_pair<0>(word, k) : kv4_pair<2>(word, k);
-              f[2 + e] = s % 2 == 0 ? kv4_pair<1>(word, k) : kv4_pair<3>(word, k);
+          for (int e = 0; e < 4; ++e) {
+            const int row = m0 * 16 + e * 8 + gi;
+            const uint32_t scales = sk + L::KEYS * L::RB + row * L::SB;
+            if constexpr (D >= 32) ld_words<KW>(sk + row * L::RB + ti * (D / 8), w[e]);
+            else ld_words<KW>(sk + row * L::RB + ti / 2 * 4, w[e]);
+            if constexpr (D == 16) w[e][0] >>= 8 * (ti & 1);
+            if constexpr (D == 128) {
+              uint16_t x;
+              asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(scales + ti * 2));
+              sa[e] = kv4_scales((uint32_t)x & 255);
+              sb[e] = kv4_scales((uint32_t)x >> 8);
+            } else {
+              sa[e] = kv4_scales(ld_byte(scales + (D == 64 ? ti : D == 32 ? ti / 2 : 0)));
+              sb[e] = sa[e];
             }
-#pragma unroll
-            for (int b = 0; b < NB; ++b) mma16816(sc[m0 + mb][b], f, qf[b][s][0], qf[b][s][1]);
           }
+#pragma unroll
+          for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+            for (int mb = 0; mb < 2; ++mb) {
+              uint32_t f[4];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const uint32_t word = w[2 * mb + e][s / 2];
+                const Kv4Scale &k = s < 4 ? sa[2 * mb + e] : sb[2 * mb + e];
+                f[e] = s % 2 == 0 ? kv4_pair<0>(word, k) : kv4_pair<2>(word, k);
+                f[2 + e] = s % 2 == 0 ? kv4_pair<1>(word, k) : kv4_pair<3>(word, k);
+              }
+#pragma unroll
+              for (int b = 0; b < NB; ++b) mma16816(sc[m0 + mb][b], f, qf[b][s][0], qf[b][s][1]);
+            }
         }
         if ((j + 1) * L::KEYS > all_see) {
           const int key = j * L::KEYS + gi;
@@ -755,15 +800,17 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_rows_kerne
   const bool joined = prev != lane && prev_seq == my_seq && prev_unit == my_unit;
   unsigned starts = __ballot_sync(0xffffffffu, my_seq >= 0 && !joined);
   if (a.spans != nullptr && threadIdx.x == 0) {  // the CTA's last item: it may begin it and not end it
-    int4 span = make_int4(-1, 0, 0, 0);
+    int4 span = make_int4(-1, 0, 0, 0), item = span;
     if (starts != 0) {
       const KdMeta &x = meta[31 - __clz(starts)];
       if (x.j0 == 0 && meta[31 - __clz(there)].j1 < x.n) {
-        const long long item_end = (long long)first[x.seq] * a.times + (long long)(x.unit + 1) * x.n;
-        span = make_int4(x.seq, x.unit, (int)min((item_end - 1) / each, (long long)gridDim.x - 1), 0);
+        const long long item_end = (long long)first[x.seq] * a.times + (long long)(x.unit + 1) * (x.n + kd_start(NB));
+        span = make_int4((int)min((item_end - 1) / each, (long long)gridDim.x - 1), x.first, x.count, x.kv_len);
+        item = make_int4(x.g, x.r0, 0, 0);
       }
     }
-    a.spans[blockIdx.x] = span;
+    a.spans[2 * blockIdx.x] = span;
+    a.spans[2 * blockIdx.x + 1] = item;
   }
   // A warp for each chain and two blocks' worth of fragments (rows 8 b + e, + 2, + 4, + 6).
   int u = 0;
@@ -779,7 +826,7 @@ __global__ void __launch_bounds__(KdLayout<D, NB>::WARPS * 32, 1) kv4_rows_kerne
       if (be / 2 * 8 + (be & 1) >= k.nr) continue;  // no rows
       if (u++ % L::WARPS != warp) continue;
       // (behind its first piece a chain goes on with the first one of each warp that follows)
-      const KdSum<D, NB, 1> sum(be, 0, __popc(chain), [&](int s) { return piece(s == 0 ? c : (c / 2 + s) * 2); });
+      const KdSum<D, NB, 1, KD_BATCH> sum(be, 0, __popc(chain), [&](int s) { return piece(s == 0 ? c : (c / 2 + s) * 2); });
       if (whole) {
         sum.store(a, k, be);
         continue;
@@ -804,12 +851,10 @@ template <int D, int NB>
 __global__ void __launch_bounds__(64 * NB * KD_JOIN<D>) kv4_rows_join_kernel(const __grid_constant__ KdArgs a) {
   grid_dependency_wait();
   const int c0 = blockIdx.x, be = threadIdx.x / 32 / KD_JOIN<D>, part = threadIdx.x / 32 % KD_JOIN<D>;
-  const int4 span = ld_after_wait(a.spans + c0);
+  const int4 span = ld_after_wait(a.spans + 2 * c0), item = ld_after_wait(a.spans + 2 * c0 + 1);
   if (span.x < 0) return;
-  KdCursor<NB> it;
-  it.set(a, span.x, span.y, 0);
-  const KdOut k(a, it.s.first, it.s.count, it.s.kv_len, it.g, it.sub * (8 * NB), 8 * NB);
-  const KdSum<D, NB, KD_JOIN<D>> sum(be, part, span.z - c0 + 1, [&](int s) {
+  const KdOut k(a, span.y, span.z, span.w, item.x, item.y, 8 * NB);
+  const KdSum<D, NB, KD_JOIN<D>, NB == 1 ? 16 : 8> sum(be, part, span.x - c0 + 1, [&](int s) {
     return a.part + ((size_t)(c0 + s) * 2 + (s == 0 ? 1 : 0)) * (8 * NB * (D + 2));
   });
   sum.store(a, k, be);
@@ -829,7 +874,7 @@ KdPlan plan_of(const PackedView &b, long long rows, int H, int G, int D, bool de
   p.direct = decode && b.max_kv_len <= KD_DIRECT_KEYS && items <= sms;
   p.ctas = p.direct ? (int)items : sms > 2 ? sms : 2;
   if (!p.direct) {
-    p.off_part = ((size_t)p.ctas * 16 + 127) / 128 * 128;
+    p.off_part = ((size_t)p.ctas * 32 + 127) / 128 * 128;
     p.bytes = p.off_part + (size_t)p.ctas * 2 * 8 * p.nb * (D + 2) * 4;
   }
   return p;
@@ -854,7 +899,7 @@ cudaError_t launch(KdArgs a, const KdPlan &p, cudaStream_t st) {
 
 // Tiles of a KV head's items over all sequences, at most.
 long long most_tiles(const PackedView &b, int H, int G) {
-  return (long long)kd_tiles<2>(b.max_kv_len) * ((long long)b.n_tokens * (H / G) / 8 + b.n_seqs);
+  return (long long)(kd_tiles<2>(b.max_kv_len) + kd_start(2)) * ((long long)b.n_tokens * (H / G) / 8 + b.n_seqs);
 }
 
 cudaError_t launch_rows(const bf16 *q, const uint8_t *k, const uint8_t *v, bf16 *o, const PagedView &pv,
@@ -905,10 +950,11 @@ long long rows_of(const PackedView &b, int H, int G) {
 
 }  // namespace
 
-// A CTA's tiles are counted in an int.
+// The tiles of a KV head, and those of a CTA, are counted in ints.
 bool kv4_decode_fits(int n_seqs, int max_kv_len, int H, int G) {
   const long long subs = (H / G + 15) / 16;
-  return (long long)n_seqs * max_kv_len <= (1LL << 42) / (G * subs);
+  const long long keys = (long long)n_seqs * max_kv_len;
+  return keys <= 1LL << 35 && keys <= (1LL << 42) / (G * subs);
 }
 
 size_t kv4_decode_workspace_bytes(int n_seqs, int max_kv_len, int H, int G, int D) {

@@ -294,8 +294,8 @@ llama_status llama_op_attention_packed_kv4(int32_t dtype, const void *q, const l
                                            llama_stream stream);
 
 /* llama_op_attention_paged_decode over 4-bit pages; dtype is that of q and o.
- * LLAMA_ERR_UNSUPPORTED also where n_seqs * max_kv_len * G * ceil(H / G / 16) is
- * above 2^42. */
+ * LLAMA_ERR_UNSUPPORTED also where n_seqs * max_kv_len is above 2^35, or its
+ * product with G * ceil(H / G / 16) above 2^42. */
 size_t llama_op_attention_paged_decode_kv4_workspace_bytes(int32_t dtype, int32_t n_seqs, int32_t max_kv_len,
                                                            int32_t H, int32_t G, int32_t D);
 llama_status llama_op_attention_paged_decode_kv4(int32_t dtype, const void *q, const llama_paged_kv_cache *kv,

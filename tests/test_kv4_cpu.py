@@ -108,9 +108,10 @@ def test_refusals(lb, host):
     assert _calls(lb, bf, ok_kv, ok_b, host, 4, 2, 64, layout=2)[0] == inv
     assert _calls(lb, bf, ok_kv, ok_b, host, 4, 2, 64, table_max=0)[0] == inv
     # more tiles than a kernel counts
-    many = (bf, host, ok_kv, host, 4096, 1 << 23, host, 65535, 65535, 64, host, 1 << 40)
-    assert lb.llama_op_attention_paged_decode_kv4(*many) == uns
-    assert lb.llama_op_attention_paged_decode_kv4_workspace_bytes(bf, 4096, 1 << 23, 65535, 65535, 64) == 0
+    for n, heads in ((1 << 23, 65535), (1 << 24, 1)):
+        many = (bf, host, ok_kv, host, 4096, n, host, heads, heads, 64, host, 1 << 40)
+        assert lb.llama_op_attention_paged_decode_kv4(*many) == uns
+        assert lb.llama_op_attention_paged_decode_kv4_workspace_bytes(bf, 4096, n, heads, heads, 64) == 0
     # nothing to do: nothing is looked at
     assert _calls(lb, bf, _cache(lb), _batch(lb, n_seqs=0), None, 4, 2, 64) == [lb.LLAMA_OK] * 4
     assert _calls(lb, bf, _cache(lb), _batch(lb, n_tokens=0), None, 4, 2, 64)[:3] == [lb.LLAMA_OK] * 3
