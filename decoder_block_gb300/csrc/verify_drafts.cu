@@ -35,11 +35,13 @@ constexpr int VD_VECS = 4;          // 16-byte vectors of a thread in flight
 // rate (4 and 16: 48; rows left in L2 for the drawing, by loads that do not say that they
 // are the last: 74 to 77 us in all for 71).
 constexpr int VD_CTAS = 6, VD_AIM = 32;
-constexpr int VD_PREFETCH = 32;     // pieces that a CTA asks for
 constexpr int VD_RACE = 2;          // of each of a race's rows
 constexpr int VD_MAX_PARTS = 32;    // of a row: a lane each when they are added up
 constexpr int VD_MIN_PART = 4096;   // logits of a part, at least
-constexpr int VD_MIN_RACE = 1024;   // ids of a CTA of a cluster, at least
+// Ids of a CTA of a cluster, at least: while SMs are idle, and above that.  (6 and 3 sequences of
+// 22085 and 12828 ids: 15.8 and 13.9 us at 1024, 15.8 and 14.5 at 2048, 16.9 and 16.1 at 4096, 20.9 and
+// 17.5 at 8192; 197 sequences of 2833: 19.0 at 1024, 17.6 at 2048.)
+constexpr int VD_MIN_RACE = 1024, VD_MIN_RACE_BUSY = 4096;
 constexpr int VD_MAX_CLUSTER = 8;
 constexpr float VD_LOG2E = 1.4426950408889634f;
 
@@ -232,14 +234,18 @@ __global__ void __launch_bounds__(VD_THREADS, VD_CTAS) verify_rows_kernel(const 
 }
 
 // ------------------------------------------------------------------ draw ---
-// A row's (m, z, id), from its parts, in every lane.
-__device__ __forceinline__ VdPart row_sum(const VdArgs &a, int row, int side, float c) {
+// This lane's part of a row.
+__device__ __forceinline__ VdPart load_part(const VdArgs &a, int row, int side, bool there = true) {
   const int lane = threadIdx.x & 31;
   VdPart p{-FLT_MAX, 0.f, INT_MAX, 0};
-  if (lane < a.parts) {
+  if (there && lane < a.parts) {
     const int4 v = ld_after_wait(reinterpret_cast<const int4 *>(a.part + ((size_t)row * 2 + side) * a.parts + lane));
     p = VdPart{__int_as_float(v.x), __int_as_float(v.y), v.z, 0};
   }
+  return p;
+}
+// The row's (m, z, id), from the lanes' parts, in every lane.
+__device__ __forceinline__ VdPart sum_parts(VdPart p, float c) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     const float om = __shfl_xor_sync(0xffffffffu, p.m, o), oz = __shfl_xor_sync(0xffffffffu, p.z, o);
@@ -311,7 +317,7 @@ __global__ void __launch_bounds__(VD_MOST_THREADS) verify_draw_kernel(const __gr
   __shared__ int s_id[MOST];
   __shared__ bool s_keep[MOST];
   __shared__ VdBest s_best[VD_MOST_THREADS / 32];
-  __shared__ VdBest s_cta[VD_MAX_CLUSTER];  // of the cluster's first CTA: every CTA's
+  __shared__ VdBest s_cta[2][VD_MAX_CLUSTER];  // every CTA's, of each search
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, threads = blockDim.x, warps = threads / 32;
   const int seq = blockIdx.x / a.cluster, rank = blockIdx.x % a.cluster;
   if (a.cluster > 1) ptx::cluster_sync();  // every CTA runs: the first one's shared memory may be written
@@ -325,31 +331,44 @@ __global__ void __launch_bounds__(VD_MOST_THREADS) verify_draw_kernel(const __gr
   int kept = 0, token = -1;
   if (fine && n > 0) {  // the same in every CTA of the cluster
     const bool greedy = t == 0.f;
-    if (!greedy && threadIdx.x < VD_PREFETCH) {
-      // this CTA's share of the noise, which does not wait for the decisions, into L2
-      const long long ids = ((long long)a.V + VD_PREFETCH * a.cluster - 1) / (VD_PREFETCH * a.cluster);
-      const long long from = (rank * VD_PREFETCH + (int)threadIdx.x) * ids, to = min((long long)a.V, from + ids);
+    const float c = greedy ? VD_LOG2E : VD_LOG2E / t;
+    // This CTA's share of the noise, which does not wait for the decisions, into L2, a piece for each
+    // lane; behind the loads that the decisions wait for.
+    auto ask_for_noise = [&] {
+      const long long ids = ((long long)a.V + 32 * a.cluster - 1) / (32 * a.cluster);
+      const long long from = (rank * 32 + lane) * ids, to = min((long long)a.V, from + ids);
       const uintptr_t p = reinterpret_cast<uintptr_t>(a.noise + (size_t)seq * a.noise_stride);
-      const uintptr_t b0 = (p + 4 * (uintptr_t)from + 15) & ~uintptr_t(15), b1 = (p + 4 * (uintptr_t)max(from, to)) & ~uintptr_t(15);
+      const uintptr_t b0 = (p + 4 * (uintptr_t)from + 15) & ~uintptr_t(15);
+      const uintptr_t b1 = (p + 4 * (uintptr_t)max(from, to)) & ~uintptr_t(15);
       if (b1 > b0)
         asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(b0), "r"((uint32_t)(b1 - b0)) : "memory");
-    }
-    const float c = greedy ? VD_LOG2E : VD_LOG2E / t;
+    };
+    // (loads first, as far as they are known: each takes about as long as all else here)
     for (int k = warp; k < n; k += warps) {
-      const VdPart p = row_sum(a, first + k, 0, c);
-      const bool has_draft = a.draft != nullptr && !greedy && k + 1 < n;
-      VdPart q{0.f, 0.f, 0, 0};
-      if (has_draft) q = row_sum(a, first + k, 1, c);
+      const bool has_draft = a.draft != nullptr && !greedy && k + 1 < n, random = k + 1 < n && !greedy;
+      const int x = k + 1 < n ? ld_after_wait(a.tokens + first + k + 1) : 0;
+      const float u = random ? ld_float_after_wait(a.uniforms + (size_t)seq * a.max_drafts + k) : 0.f;
+      VdPart p = load_part(a, first + k, 0), q = load_part(a, first + k, 1, has_draft);
+      const bool in = x >= 0 && x < a.V;
+      float fx = 0.f, fy = 0.f;
+      if (random && in) {
+        fx = ld_logit<T>(reinterpret_cast<const T *>(a.target) + (size_t)(first + k) * a.target_stride + x);
+        if (has_draft)
+          fy = ld_logit<T>(reinterpret_cast<const T *>(a.draft) + (size_t)seq * a.seq_stride + (size_t)k * a.step_stride + x);
+      }
+      if (!greedy && k == 0) ask_for_noise();
+      p = sum_parts(p, c);
+      if (has_draft) q = sum_parts(q, c);
       if (lane == 0) {
         s_m[0][k] = p.m;
         s_z[0][k] = p.z;
         s_m[1][k] = q.m;
-        s_z[1][k] = has_draft && row_ok(q.z) ? q.z : 0.f;  // 0: the draft was certain
+        const float zq = has_draft && row_ok(q.z) ? q.z : 0.f;  // 0: the draft was certain
+        s_z[1][k] = zq;
         s_id[k] = p.id;
         if (k + 1 < n) {
-          const int x = ld_after_wait(a.tokens + first + k + 1);
           bool keep = false;
-          if (x < 0 || x >= a.V) {
+          if (!in) {
             if (rank == 0) report_status(a.status, LLAMA_ERR_RANGE);
           } else if (row_ok(p.z)) {
             if (greedy) {
@@ -357,18 +376,15 @@ __global__ void __launch_bounds__(VD_MOST_THREADS) verify_draw_kernel(const __gr
             } else {
               // p / q = e^((x - m) / T - (y - m_q) / T) z_q / z, the exponent in fp64 and what its
               // fp32 part leaves of it as a factor
-              const T *row = reinterpret_cast<const T *>(a.target) + (size_t)(first + k) * a.target_stride;
-              double d = (double)ld_logit<T>(row + x) - (double)p.m;
-              double z = p.z;
-              if (s_z[1][k] > 0.f) {
-                const T *drow = reinterpret_cast<const T *>(a.draft) + (size_t)seq * a.seq_stride + (size_t)k * a.step_stride;
-                d -= (double)ld_logit<T>(drow + x) - (double)q.m;
-                z /= q.z;
+              double d = (double)fx - (double)p.m, z = p.z;
+              if (zq > 0.f) {
+                d -= (double)fy - (double)q.m;
+                z /= zq;
               }
               d /= (double)t;
               const float hi = (float)d, lo = (float)(d - (double)hi);
               const double ratio = (double)expf(hi) * (fabsf(hi) <= FLT_MAX ? 1.0 + (double)lo : 1.0);
-              keep = (double)ld_float_after_wait(a.uniforms + (size_t)seq * a.max_drafts + k) * z < ratio;
+              keep = (double)u * z < ratio;
             }
           }
           s_keep[k] = keep;
@@ -390,7 +406,7 @@ __global__ void __launch_bounds__(VD_MOST_THREADS) verify_draw_kernel(const __gr
                         : nullptr;
       const int banned = refused && !both ? ld_after_wait(a.tokens + first + kept + 1) : -1;
       const float m = s_m[0][kept], mq = s_m[1][kept], inv = 1.f / z, inv_q = both ? 1.f / s_z[1][kept] : 0.f;
-      VdBest best{0.f, INT_MAX};
+      VdBest best{0.f, INT_MAX};  // in the end the CTA's, in its first warp
       // What cannot beat the best so far is found without a division: `bar` is a little below it.
       float bar = 0.f;
       auto race = [&](float fx, float fy, float e, int id, bool residual) {
@@ -443,42 +459,42 @@ __global__ void __launch_bounds__(VD_MOST_THREADS) verify_draw_kernel(const __gr
         }
         if (lane == 0) s_best[warp] = best;
         __syncthreads();
-        if (threadIdx.x == 0)
-          for (int w = 1; w < warps; ++w) best.join(s_best[w].score, s_best[w].id);
-        __syncthreads();
+        if (warp == 0) {
+          best = s_best[lane < warps ? lane : 0];
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) {
+            const float s = __shfl_xor_sync(0xffffffffu, best.score, o);
+            const int i = __shfl_xor_sync(0xffffffffu, best.id, o);
+            best.join(s, i);
+          }
+        }
+        __syncthreads();  // (the next search writes there again)
       };
-      // the CTA's best into the first CTA's array, through distributed shared memory
-      auto meet = [&] {
-        if (a.cluster > 1) ptx::cluster_sync();
-        else __syncthreads();
-      };
-      auto publish = [&] {
-        if (threadIdx.x == 0) {
-          uint32_t dst = ptx::smem_u32(&s_cta[rank]);
-          if (a.cluster > 1) dst = ptx::mapa_shared(dst, 0);
+      // the CTA's best into every CTA's array, through distributed shared memory
+      auto publish = [&](int which) {
+        if (threadIdx.x < a.cluster) {
+          uint32_t dst = ptx::smem_u32(&s_cta[which][rank]);
+          if (a.cluster > 1) dst = ptx::mapa_shared(dst, threadIdx.x);
           ptx::st_cluster_u32(dst, __float_as_uint(best.score));
           ptx::st_cluster_u32(dst + 4, (uint32_t)best.id);
         }
-        meet();
+        if (a.cluster > 1) ptx::cluster_sync();
+        else __syncthreads();
       };
       search(true);
-      publish();
+      publish(0);
+      int last = 0;
       if (refused) {  // (in every CTA of the cluster alike)
         float top = 0.f;
-        for (int k = 0; k < a.cluster; ++k) {
-          uint32_t src = ptx::smem_u32(&s_cta[k]);
-          if (a.cluster > 1) src = ptx::mapa_shared(src, 0);
-          top = fmaxf(top, ptx::ld_cluster_f32(src));
-        }
-        meet();
+        for (int k = 0; k < a.cluster; ++k) top = fmaxf(top, s_cta[0][k].score);
         if (top == 0.f) {  // nothing of p - q is left: from p
           search(false);
-          publish();
+          publish(last = 1);
         }
       }
       if (rank == 0) {
-        VdBest all = s_cta[0];
-        for (int k = 1; k < a.cluster; ++k) all.join(s_cta[k].score, s_cta[k].id);
+        VdBest all = s_cta[last][0];
+        for (int k = 1; k < a.cluster; ++k) all.join(s_cta[last][k].score, s_cta[last][k].id);
         token = all.score > 0.f ? all.id : -1;
       }
     }
@@ -546,10 +562,12 @@ cudaError_t launch_verify_drafts(const T *target, long long target_stride, const
                                      dim3(VD_THREADS), 0, st, a);
     if (e != cudaSuccess) return e;
   }
-  // clusters as large as keep every SM at work, a CTA not below VD_MIN_RACE ids
   a.cluster = 1;
-  while (a.cluster < VD_MAX_CLUSTER && 2LL * a.cluster * b.n_seqs <= 4LL * sm_count() && V / (2 * a.cluster) >= VD_MIN_RACE)
-    a.cluster *= 2;
+  for (int c = 2; c <= VD_MAX_CLUSTER; c *= 2) {
+    const long long ctas = (long long)c * b.n_seqs;
+    if (ctas > 4 * sm_count() || V / c < (ctas <= sm_count() ? VD_MIN_RACE : VD_MIN_RACE_BUSY)) break;
+    a.cluster = c;
+  }
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -559,9 +577,8 @@ cudaError_t launch_verify_drafts(const T *target, long long target_stride, const
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(b.n_seqs * a.cluster));
   // few sequences: as many loads in flight as an SM has room for (two of 125880 ids 25 -> 21 us)
-  cfg.blockDim = dim3(a.cluster == VD_MAX_CLUSTER && b.n_seqs * a.cluster <= sm_count() && V >= VD_MOST_THREADS * VD_MAX_CLUSTER * 8
-                          ? VD_MOST_THREADS
-                          : VD_THREADS);
+  const bool few = a.cluster == VD_MAX_CLUSTER && b.n_seqs * a.cluster <= sm_count();
+  cfg.blockDim = dim3(few && V >= VD_MOST_THREADS * VD_MAX_CLUSTER * 8 ? VD_MOST_THREADS : VD_THREADS);
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = a.cluster > 1 ? 2 : 1;
