@@ -29,7 +29,7 @@ namespace {
 
 constexpr int VD_THREADS = 256;
 constexpr int VD_WARPS = VD_THREADS / 32;
-constexpr int VD_MOST_THREADS = 1024;  // of a CTA that draws
+constexpr int VD_MOST_THREADS = 768;  // of a CTA that draws
 constexpr int VD_VECS = 4;          // 16-byte vectors of a thread in flight
 // CTAs of an SM, and CTAs for an SM that the parts aim at: 265 MB in 47 us, 0.82 of the measured
 // rate (4 and 16: 48; rows left in L2 for the drawing, by loads that do not say that they
@@ -576,9 +576,14 @@ cudaError_t launch_verify_drafts(const T *target, long long target_stride, const
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(b.n_seqs * a.cluster));
-  // few sequences: as many loads in flight as an SM has room for (two of 125880 ids 25 -> 21 us)
-  const bool few = a.cluster == VD_MAX_CLUSTER && b.n_seqs * a.cluster <= sm_count();
-  cfg.blockDim = dim3(few && V >= VD_MOST_THREADS * VD_MAX_CLUSTER * 8 ? VD_MOST_THREADS : VD_THREADS);
+  // few sequences: a thread for each vector (8 sequences of 35468 ids 17.0 -> 15.4 us, 3 of 12828
+  // 13.2 -> 12.4; 1024 threads, where a row has as many: two sequences of 49152 12.0 for 11.5)
+  const int vectors = V / (a.cluster * (16 / (int)sizeof(T)));
+  int threads = VD_THREADS;
+  if (b.noise != nullptr && b.n_seqs * a.cluster <= sm_count()) {
+    while (threads < vectors && threads < VD_MOST_THREADS) threads += VD_THREADS;
+  }
+  cfg.blockDim = dim3((unsigned)threads);
   cfg.stream = st;
   cfg.attrs = attr;
   cfg.numAttrs = a.cluster > 1 ? 2 : 1;
