@@ -26,6 +26,12 @@
 // and what begins or ends inside the CTA's run goes to the workspace, where a second kernel
 // joins it, in order.  With short sequences (direct: one token each) a CTA takes one item
 // instead, and there is no second kernel.
+//
+// Measured, D = 128 and 8 KV heads of four: 64 sequences of 253 to 4096 keys 41.5 us, of which
+// about 11 are the kernels' beginnings and joins; between, 5.3 TB/s (0.78 of the copy rate),
+// instructions issued in two cycles of three.  One sequence of 120001 keys 40.5 us.  64
+// sequences of five rows 71.5 us: three times the products on the same unpacked numbers,
+// bound by their latency (255 registers leave two warps to a scheduler).
 #include <cuda_fp16.h>
 #include <float.h>
 
@@ -971,15 +977,19 @@ cudaError_t launch_kv4_decode(const bf16 *q, const uint8_t *k, const uint8_t *v,
 // Few rows, which tcgen05's 128-row tiles would mostly pad: those of one item on average, or
 // of so many that the warps take KD_ROUNDS of their tiles each at the longest length (64
 // sequences of 20 rows behind 2200 keys, 8 KV heads: 77 us for 104; 26 of 73 rows behind up to
-// 3300 keys, one KV head: 20 for 31; at 15 rounds 17 for 24, but 30 for 25).  Not over a few
-// keys, where tcgen05 takes a single kernel (up to 236 keys 9 us for 13, up to 400 keys 11.5
-// for 11).  (The counts of tiles are ints.)
+// 3300 keys, one KV head: 20 for 31; at 15 rounds 17 for 24, but 30 for 25).  Over a few keys
+// tcgen05 takes a single kernel, and is better while its items are fewer than its CTAs (5 rows
+// behind 300 keys, 90 items 9.3 us for 10.3, 150 items 13.3 for 9.2; 64 sequences of 5 on 8 KV
+// heads 33.5 for 23.6, 1000 of 2 behind 10 keys 202 for 37) or have more rows (100 sequences of
+// 60 behind 300 keys, 3 KV heads 19 for 23).  (The counts of tiles are ints.)
 bool kv4_rows_fit(const PackedView &b, int H, int G) {
+  const long long most = most_tiles(b, H, G);
+  if (most > 0x7fffffffLL || most * G > (1LL << 30) * sm_count()) return false;
+  const bool few_keys = b.max_kv_len <= KD_FEW_KEYS;
+  if (rows_of(b, H, G) <= 8 * KD_MAX_NB) return !few_keys || 3LL * b.n_seqs * G > 2LL * sm_count();
   const long long tiles = (long long)G * kd_tiles<KD_MAX_NB>(b.max_kv_len) *
                           ((long long)b.n_tokens * (H / G) / (8 * KD_MAX_NB) + b.n_seqs);
-  return b.max_kv_len > KD_FEW_KEYS && most_tiles(b, H, G) <= 0x7fffffffLL &&
-         most_tiles(b, H, G) * G <= (1LL << 30) * sm_count() &&
-         (rows_of(b, H, G) <= 8 * KD_MAX_NB || tiles <= (long long)KD_ROUNDS * sm_count() * 8);
+  return !few_keys && tiles <= (long long)KD_ROUNDS * sm_count() * 8;
 }
 size_t kv4_rows_workspace_bytes(const PackedView &b, int H, int G, int D) {
   return plan_of(b, rows_of(b, H, G), H, G, D, false).bytes;

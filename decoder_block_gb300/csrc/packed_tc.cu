@@ -1,7 +1,8 @@
 // Causal grouped-query attention of a packed batch over cache pages, bf16, on
 // tcgen05 tensor cores ("The Evolving Transformer 04 · LLaMA", §05 GQA; "Full Llama 3
 // transformer block", How it works: keys j <= position).  d_head 64 or 128; 16 and 32
-// run as 64, their tiles filled up with zeros by the copies.  For token t at position p and its KV head's keys and values
+// run as 64, their tiles filled up with zeros by the copies.  For token t at position p
+// and its KV head's keys and values
 //   o = sum_{j<=p} 2^(x_j - m) v_j / sum_{j<=p} 2^(x_j - m),  x_j = q.k_j log2(e) / sqrt(D),
 // in one pass over the keys with the running maximum m and sum in fp32.
 //
@@ -30,13 +31,17 @@
 //     outlast the rest (few query rows against many keys) it splits their keys
 //     into pieces; a piece leaves fp32 (O, m, l) per row in the workspace, and a
 //     third kernel joins them in piece order, so results do not depend on timing.
-// Pages held in 4 bits: the four loading warps copy a tile's codes and scales into shared
-// memory a stage ahead, and write the 16-bit numbers that they stand for where the copies
+// Pages held in 4 bits (kv4.cuh): the loading warps copy a tile's codes and scales into shared
+// memory ahead of time, and write the 16-bit numbers that they stand for where the copies
 // above would have put them: keys as bf16, as the queries are, and values as fp16 (half
-// of each, kv4.cuh), as the weights then are: an eighth of bf16's rounding.
+// of each), as the weights then are: an eighth of bf16's rounding.  A tile's 32768 elements
+// are unpacked by four warps beside the eight of the softmax, and that bounds it: S = 8192
+// takes 453 us (0.63 of the burst rate) for 364 to 389 over bf16 pages; 406 with the
+// numbers stored as they come, 395 with nothing stored.  Where sequences have few rows an
+// item is one query tile, eight warps unpack and three tiles are on their way.
 // Every wait is bounded (llama_op_set_wait_budget).  A CTA that gives up records
 // LLAMA_ERR_DEVICE_TIMEOUT and leaves once its copies, MMAs and tensor memory stores in
-// flight are done; the four loading warps each arm the bytes they are about to ask for.
+// flight are done; the loading warps each arm the bytes they are about to ask for.
 #include <cudaTypedefs.h>
 #include <cuda_fp16.h>
 #include <float.h>
@@ -1427,7 +1432,9 @@ cudaError_t launch_packed_tc(const bf16 *q, const bf16 *k, const bf16 *v, bf16 *
 
 namespace {
 // Query tiles of an item over 4-bit pages: one where the sequences' rows are few on average
-// (drafts, single tokens): eight warps then unpack, with more tiles on their way.
+// (and kv4_rows.cu does not take them): eight warps then unpack, with more tiles on their way
+// (128 sequences of 30 rows behind 2000 keys, 8 KV heads of four: 190 us for 232 with two; 64 of
+// 20 behind 300 keys 36.5 for 39.6).
 int kv4_tiles(const PackedView &b, int H, int G) {
   return (long long)b.n_tokens * (H / G) <= 128LL * b.n_seqs ? 1 : 2;
 }

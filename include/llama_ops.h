@@ -242,7 +242,8 @@ llama_status llama_op_attention_paged_decode(int32_t dtype, const void *q, const
  * Pages: a llama_paged_kv_cache whose k and v are pools of bytes,
  * [n_pages][n_kv_heads][llama_kv4_block_bytes(page_size, d_head)], with
  * page_stride in bytes (0: dense; otherwise a multiple of 16, at least
- * n_kv_heads blocks; below 2^32, LLAMA_ERR_UNSUPPORTED otherwise).  A block, the rows of one page and KV head, is
+ * n_kv_heads blocks; below 2^32, LLAMA_ERR_UNSUPPORTED otherwise).  A block, the
+ * rows of one page and KV head, is
  *     page_size rows of d_head / 2 bytes: the codes, and behind them
  *     page_size rows of d_head / 16 bytes: the scales.
  * Eight elements 8w .. 8w + 7 of a row are the four bytes of a little-endian

@@ -27,6 +27,8 @@ def lb():
     ("one_query_tile_in_pieces", [20, 20, 20], [3000, 500, 5000], FAR),
     ("one_query_tile", [20] * 24, [30 + 14 * i for i in range(24)], None),
     ("rows_of_many_items", [40, 9], [1500, 700], None),
+    ("many_of_few_keys", [1 + i % 5 for i in range(120)], [5 + (37 * i) % 300 for i in range(120)], None),
+    ("few_of_few_keys", [1 + i % 5 for i in range(7)], [5 + (37 * i) % 300 for i in range(7)], None),
 ])
 def test_packed(lb, H, G, D, name, q_lens, kv_lens, max_kv):
     p = Kv4Problem(f"pp/{name}{D}", "bf16", H, G, D, 32, q_lens, kv_lens, pad=2)
