@@ -132,9 +132,9 @@ __device__ __forceinline__ float4 kv4_four(uint32_t w, int half, float scale) {
                      (float)((int)(w >> 4 & 15) - 8) * scale, (float)((int)(w >> 20 & 15) - 8) * scale);
 }
 
-__device__ __forceinline__ float max_nan_abs(float a, float b) {  // NaN when either is
+__device__ __forceinline__ float max_nan_abs(float a, float b, float c) {  // of magnitudes; NaN when one is
   float d;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(fabsf(b)));
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
 // A block of 16 values: its scale byte and codes (two words).  `bad` is set for a NaN, which is
@@ -150,7 +150,7 @@ __device__ __forceinline__ float max_nan_abs(float a, float b) {  // NaN when ei
 __device__ __forceinline__ uint32_t kv4_quantise(float (&x)[KV4_BLOCK], uint32_t (&words)[2], bool &bad) {
   float most = 0.f;
 #pragma unroll
-  for (int e = 0; e < KV4_BLOCK; ++e) most = max_nan_abs(most, x[e]);
+  for (int e = 0; e < KV4_BLOCK; e += 2) most = max_nan_abs(most, x[e], x[e + 1]);
   if (!(most <= KV4_MOST)) {
     bad = true;
     most = 0.f;

@@ -11,7 +11,7 @@
 //          found without asking another thread.
 //   read   a thread turns four bytes of codes into eight elements.
 // What bounds them is a CTA's chain of look-up, load, arithmetic and store: 8192 rows of
-// 4096 + 2 * 1024 bf16 are written in 39 us (4.5 TB/s, 0.66 of the copy rate) and read back
+// 4096 + 2 * 1024 bf16 are written in 38 us (4.7 TB/s, 0.69 of the copy rate) and read back
 // in 13; 39778 rows of 2 * 1024 are read from memory in 41 (5.1 TB/s, 0.74).
 #include "kv4.cuh"
 #include "paged_kernels.h"
@@ -26,7 +26,7 @@ constexpr int KW_UNITS = 2;  // rows of a thread in flight
 constexpr int KR_UNITS = 4;
 // Rows of a CTA at most, written and read: finding their places is shared, but the last CTAs are
 // longer.  (8192 rows of 4096 + 2 * 1024 bf16 written: 92, 61, 52, 54 and 54 us at 1, 2, 4, 8 and
-// 16; 40000 rows of 2 * 1024 read: 100, 63, 46, 41 and 41.  Asking for the rows to be written
+// 16, with less arithmetic 51 and 53 at 4 and 8; 40000 rows of 2 * 1024 read: 100, 63, 46, 41 and 41.  Asking for the rows to be written
 // before their places are known gains nothing: 53.)
 constexpr int KW_MOST = 4, KR_MOST = 8;
 
@@ -38,6 +38,7 @@ struct KwArgs {
   int H, G, D, rows;  // rows of a CTA
   int halves;
   int q_lanes, kv_lanes;  // threads side by side in a row (powers of two)
+  int q_log2, kv_log2;    // units of a head: 1 << these
   int *status;
 };
 
@@ -75,6 +76,14 @@ __device__ __forceinline__ void turn(float a, float b, float2 c, float &p, float
   q = __fadd_rn(__fmul_rn(a, c.y), __fmul_rn(b, c.x));
 }
 
+__device__ __forceinline__ void set_two(Vec16<float> &v, int i, float a, float b) {
+  v.set(i, a);
+  v.set(i + 1, b);
+}
+__device__ __forceinline__ void set_two(Vec16<bf16> &v, int i, float a, float b) {
+  reinterpret_cast<__nv_bfloat162 *>(&v.raw)[i / 2] = __floats2bfloat162_rn(a, b);
+}
+
 // N: elements of a thread's unit of keys and values, 32, or 16 where a head has no more.
 template <typename T, int N>
 __global__ void __launch_bounds__(KW_THREADS, KW_CTAS)
@@ -83,7 +92,7 @@ __global__ void __launch_bounds__(KW_THREADS, KW_CTAS)
   __shared__ int s_pos[KW_ROWS];
   __shared__ long long s_page[KW_ROWS];
   const int t0 = (int)blockIdx.x * a.rows;
-  const int heads = a.H + 2 * a.G, per_head = a.D / (2 * V);
+  const int heads = a.H + 2 * a.G;
   allow_dependents_launch();
   grid_dependency_wait();
   if (blockIdx.x == 0)
@@ -95,9 +104,10 @@ __global__ void __launch_bounds__(KW_THREADS, KW_CTAS)
   auto angles = [&](int pos, int at) { return a.table + (size_t)pos * (a.D / 2) + at; };
 
   // Keys and values first: theirs is the longer way.
-  const int kv_units = 2 * a.G * (a.D / N), kv_rows = KW_THREADS / a.kv_lanes;
+  const int kv_units = 2 * a.G << a.kv_log2, kv_rows = KW_THREADS / a.kv_lanes;
   for (int u = threadIdx.x & (a.kv_lanes - 1); u < kv_units; u += a.kv_lanes) {
-    const int head = u / (a.D / N), e = u % (a.D / N) * (N / 2);  // elements e .., and those D / 2 further
+    // elements e .., and those D / 2 further
+    const int head = u >> a.kv_log2, e = (u & ((1 << a.kv_log2) - 1)) * (N / 2);
     const bool key = head < a.G;
     uint8_t *const block =
         (key ? kc : vc) + (long long)(key ? head : head - a.G) * kv4_block_bytes(1 << a.pv.page_log2, a.D);
@@ -149,9 +159,9 @@ __global__ void __launch_bounds__(KW_THREADS, KW_CTAS)
     }
   }
 
-  const int q_units = a.H * per_head, q_rows = KW_THREADS / a.q_lanes;
+  const int q_units = a.H << a.q_log2, q_rows = KW_THREADS / a.q_lanes;
   for (int u = threadIdx.x & (a.q_lanes - 1); u < q_units; u += a.q_lanes) {
-    const int head = u / per_head, e = u % per_head * V;
+    const int head = u >> a.q_log2, e = (u & ((1 << a.q_log2) - 1)) * V;
     const T *const q_first = qkv + ((size_t)t0 * heads + head) * a.D + e;
     T *const out = q_out + ((size_t)t0 * a.H + head) * a.D + e;
     for (int r0 = threadIdx.x / a.q_lanes; r0 < a.rows; r0 += KW_UNITS * q_rows) {
@@ -187,24 +197,18 @@ __global__ void __launch_bounds__(KW_THREADS, KW_CTAS)
           p.raw = q.raw = make_uint4(0, 0, 0, 0);
         } else {
           const float2 *c = reinterpret_cast<const float2 *>(cs[k]);
-          float f, g;
-          if (a.halves) {
+          float f, g, f2, g2;
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
+          for (int j = 0; j < V; j += 2) {
+            if (a.halves) {
               turn(x[k].get(j), y[k].get(j), c[j], f, g);
-              p.set(j, f);
-              q.set(j, g);
+              turn(x[k].get(j + 1), y[k].get(j + 1), c[j + 1], f2, g2);
+            } else {
+              turn(x[k].get(j), x[k].get(j + 1), c[j / 2], f, f2);
+              turn(y[k].get(j), y[k].get(j + 1), c[V / 2 + j / 2], g, g2);
             }
-          } else {
-#pragma unroll
-            for (int j = 0; j < V / 2; ++j) {
-              turn(x[k].get(2 * j), x[k].get(2 * j + 1), c[j], f, g);
-              p.set(2 * j, f);
-              p.set(2 * j + 1, g);
-              turn(y[k].get(2 * j), y[k].get(2 * j + 1), c[V / 2 + j], f, g);
-              q.set(2 * j, f);
-              q.set(2 * j + 1, g);
-            }
+            set_two(p, j, f, f2);
+            set_two(q, j, g, g2);
           }
         }
         store16(out + at[k], p);
@@ -284,6 +288,11 @@ int rows_of(int n_tokens, int most) {
   while (rows < most && n_tokens / (2 * rows) >= 4 * sms) rows *= 2;
   return rows;
 }
+int log2_of(int n) {  // of a power of two
+  int k = 0;
+  while (1 << k < n) ++k;
+  return k;
+}
 // Threads side by side in a row of `units`.
 int lanes_of(int units) {
   int n = 1;
@@ -308,8 +317,10 @@ cudaError_t launch_rope_kv4(const T *qkv, T *q_out, uint8_t *k, uint8_t *v, cons
   a.halves = halves;
   a.status = status;
   a.rows = rows_of(b.n_tokens, KW_MOST);
-  a.q_lanes = lanes_of(H * (D / (2 * Vec16<T>::N)));
-  a.kv_lanes = lanes_of(2 * G * (D == 16 ? 1 : D / 32));
+  a.q_log2 = log2_of(D / (2 * Vec16<T>::N));
+  a.kv_log2 = log2_of(D == 16 ? 1 : D / 32);
+  a.q_lanes = lanes_of(H << a.q_log2);
+  a.kv_lanes = lanes_of(2 * G << a.kv_log2);
   count_launch();
   return launch_pdl(D == 16 ? rope_kv4_kernel<T, 16> : rope_kv4_kernel<T, 32>,
                     dim3((unsigned)((b.n_tokens + a.rows - 1) / a.rows)), dim3(KW_THREADS), 0, st, qkv, q_out, k, v, a);
@@ -325,8 +336,7 @@ cudaError_t launch_kv4_read(const uint8_t *k, const uint8_t *v, T *k_out, T *v_o
   a.v = v;
   a.G = G;
   a.D = D;
-  for (a.word_log2 = 0; 8 << a.word_log2 < D; ++a.word_log2) {
-  }
+  a.word_log2 = log2_of(D / 8);
   a.status = status;
   a.rows = rows_of(b.n_tokens, KR_MOST);
   a.lanes = lanes_of(2 * G * D / 8);
