@@ -36,7 +36,7 @@
 // above would have put them: keys as bf16, as the queries are, and values as fp16 (half
 // of each), as the weights then are: an eighth of bf16's rounding.  A tile's 32768 elements
 // are unpacked by four warps beside the eight of the softmax, and that bounds it: S = 8192
-// takes 453 us (0.63 of the burst rate) for 364 to 389 over bf16 pages; 406 with the
+// takes 449 us (0.63 of the burst rate) for 364 to 389 over bf16 pages; 406 with the
 // numbers stored as they come, 395 with nothing stored.  Where sequences have few rows an
 // item is one query tile, eight warps unpack and three tiles are on their way.
 // Every wait is bounded (llama_op_set_wait_budget).  A CTA that gives up records
@@ -521,8 +521,16 @@ struct Unpacker {
     for (int i = 0; i < ROUNDS; ++i) {
       const int row = (i * LANES + lane % LANES) / PER_ROW, col = (i * LANES + lane % LANES) % PER_ROW;
       if constexpr (CHUNK == 16) {
-        r.codes[i] = ld_shared16(from + row * RB + col * 16);
+        const uint32_t at = from + row * RB + col * 16;
         r.scales[i] = ld_shared_u16(from + S::ROWS + row * SB + col * 2);
+        if constexpr (W == 128) {  // in the order in which they are stored
+          const uint32_t turn = (lane & 2) * 4;
+          const uint2 c = ld_shared8(at + turn), d = ld_shared8(at + (turn ^ 8));
+          r.codes[i] = make_uint4(c.x, c.y, d.x, d.y);
+          r.scales[i] = __byte_perm(r.scales[i], 0, turn ? 0x4401 : 0x4410);
+        } else {
+          r.codes[i] = ld_shared16(at);
+        }
       } else {
         const uint2 c = ld_shared8(from + row * RB);
         r.codes[i] = make_uint4(c.x, c.y, 0, 0);
@@ -537,17 +545,8 @@ struct Unpacker {
     for (int i = 0; i < ROUNDS; ++i) {
       const int row = warp * WR + (i * LANES + lane) / PER_ROW, col = (i * LANES + lane) % PER_ROW;
       const bool turned = W == 128 && col >= 2;
-      uint32_t w[4] = {r.codes[i].x, r.codes[i].y, r.codes[i].z, r.codes[i].w};
-      uint32_t s0 = r.scales[i] & 255u, s1 = r.scales[i] >> 8;
-      if (W == 128) {
-        const uint32_t x = w[0], y = w[1], s = s0;
-        w[0] = turned ? w[2] : w[0];
-        w[1] = turned ? w[3] : w[1];
-        w[2] = turned ? x : w[2];
-        w[3] = turned ? y : w[3];
-        s0 = turned ? s1 : s0;
-        s1 = turned ? s : s1;
-      }
+      const uint32_t w[4] = {r.codes[i].x, r.codes[i].y, r.codes[i].z, r.codes[i].w};
+      const uint32_t s0 = r.scales[i] & 255u, s1 = r.scales[i] >> 8;
       const uint32_t base = tile + (W == 128 ? col / 2 * L::ATOM : 0) + row * 128;
       const int c0 = W == 128 ? col % 2 * 4 : col * 4;
       Kv4Scale ks[2];
