@@ -45,8 +45,9 @@ namespace llama {
 namespace {
 
 // Keys of a warp's tile: as many as the registers have room for, what is done once a tile is a
-// third of a tile of 32 keys.
-constexpr int kd_keys(int NB) { return NB == 1 ? 64 : 32; }
+// third of a tile of 32 keys.  (64 sequences of one and of three rows, four heads to a group: 45 and
+// 51.6 us at 64 keys, 47 and 55.5 at 32.)
+constexpr int kd_keys(int NB) { return NB <= 2 ? 64 : 32; }
 // Places before an item's first tile in the row that is dealt out: an item's beginning and end
 // (its queries, its output) take as long as 64 keys.  (64 sequences of 253 to 4096 keys, 8 KV
 // heads of 4 rows: 43.7, 41.2, 42.6 us with 0, 1, 2 tiles of 64 keys; of 20 rows, tiles of 32:
@@ -72,7 +73,7 @@ struct KdLayout {
   static constexpr int RB = kv4_code_bytes(D), SB = kv4_scale_bytes(D);
   static constexpr int HALF = KEYS * (RB + SB), STAGE = 2 * HALF;  // K, then V: codes, then scales
   static constexpr int PART = 8 * NB * (D + 2) * 4;  // (O, m, l) of an item
-  static constexpr int FIT = (NB == 1 ? 18432 : 13824) / STAGE;
+  static constexpr int FIT = (NB <= 2 ? 18432 : 13824) / STAGE;
   static constexpr int STAGES = FIT < 8 ? FIT : 8;
   static constexpr int RING = STAGES * STAGE > PART ? STAGES * STAGE : PART;  // of a warp; its last part at the end
   static constexpr int OFF_PART = WARPS * RING;   // of each warp, its first
@@ -83,6 +84,7 @@ struct KdLayout {
   static int bytes(int n_seqs) { return OFF_FIRST + (n_seqs + 1) * 4; }
 };
 static_assert(KdLayout<128, 1>::OFF_FIRST + (LLAMA_PACKED_MAX_SEQS + 1) * 4 <= 227 * 1024, "fits an SM");
+static_assert(KdLayout<128, 2>::OFF_FIRST + (LLAMA_PACKED_MAX_SEQS + 1) * 4 <= 227 * 1024, "fits an SM");
 static_assert(KdLayout<128, 3>::OFF_FIRST + (LLAMA_PACKED_MAX_SEQS + 1) * 4 <= 227 * 1024, "fits an SM");
 
 struct KdArgs {
@@ -905,7 +907,7 @@ cudaError_t launch(KdArgs a, const KdPlan &p, cudaStream_t st) {
 
 // Tiles of a KV head's items over all sequences, at most.
 long long most_tiles(const PackedView &b, int H, int G) {
-  return (long long)(kd_tiles<2>(b.max_kv_len) + kd_start(2)) * ((long long)b.n_tokens * (H / G) / 8 + b.n_seqs);
+  return (long long)(kd_tiles<KD_MAX_NB>(b.max_kv_len) + kd_start(KD_MAX_NB)) * ((long long)b.n_tokens * (H / G) / 8 + b.n_seqs);
 }
 
 cudaError_t launch_rows(const bf16 *q, const uint8_t *k, const uint8_t *v, bf16 *o, const PagedView &pv,
