@@ -350,7 +350,7 @@ llama_status llama_op_token_logprobs(int32_t dtype, const void *logits, int64_t 
  *
  * Sequence i owns rows [q_offsets[i], q_offsets[i + 1]): one more than it has
  * drafts, at most max_drafts + 1, or none (an empty slot).  tokens [n_rows] holds
- * the token at each row, so that row r's logits judge the draft tokens[r + 1]: draft
+ * the token at each row, so that row r's logits decide on tokens[r + 1]: draft
  * j of sequence i (from 0) is tokens[q_offsets[i] + 1 + j].  Rows behind the last
  * sequence are not read.
  * temperatures: fp32 [n_seqs] (NULL: all 1); probabilities are those of the logits
