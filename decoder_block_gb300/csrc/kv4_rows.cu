@@ -59,8 +59,11 @@ constexpr float KD_RESCALE = 8.0f;  // log2 units: the running maximum is raised
 // lost (120000 keys of such weights: 2^-14 of the sum).
 constexpr float KD_WEIGHT = 7.0f;
 constexpr float KD_VALUE = 2.0f;  // V's operand is half of V
-// Keys of a CTA's item in the direct form, at most.
-constexpr int KD_DIRECT_KEYS = 2048;
+// Keys of a CTA's item in the direct form, at most; elements of them where the items leave three
+// of four SMs idle.  (Direct / planned, D = 128, 8 KV heads: one sequence of 1000 keys 8.6 / 8.9 us,
+// of 1500 10.7 / 9.1; four of 1500 11.2 / 10.2; 16 of 1000 9.1 / 12.9, of 2048 14.5 / 18.3.  D = 64,
+// 3 KV heads: four of 1500 7.9 / 8.5, of 2048 9.1 / 8.7; 16 of 2048 9.2 / 9.8.)
+constexpr int KD_DIRECT_KEYS = 2048, KD_DIRECT_FEW = 1024 * 128;
 constexpr int KD_MAX_NB = 3;
 constexpr int KD_ROUNDS = 10, KD_FEW_KEYS = 384;  // of packed calls: see kv4_rows_fit
 constexpr int KD_BATCH = 2;  // pieces that a join within a CTA reads at a time
@@ -879,7 +882,8 @@ KdPlan plan_of(const PackedView &b, long long rows, int H, int G, int D, bool de
   const int sms = sm_count();
   p.nb = rows <= 8 ? 1 : rows <= 16 || decode ? 2 : KD_MAX_NB;
   const long long items = (long long)b.n_seqs * G * ((H / G + 8 * p.nb - 1) / (8 * p.nb));
-  p.direct = decode && b.max_kv_len <= KD_DIRECT_KEYS && items <= sms;
+  p.direct = decode && b.max_kv_len <= KD_DIRECT_KEYS && items <= sms &&
+             (4 * items > sms || b.max_kv_len * D <= KD_DIRECT_FEW);
   p.ctas = p.direct ? (int)items : sms > 2 ? sms : 2;
   if (!p.direct) {
     p.off_part = ((size_t)p.ctas * 32 + 127) / 128 * 128;

@@ -50,6 +50,17 @@ def test_decode_of_many_sequences(lb, n):
         p.check(to_f64(d.o), f"{n} {max_kv}")
 
 
+@pytest.mark.parametrize("H,G,D", [(32, 8, 128), (18, 6, 64), (12, 6, 16)])
+@pytest.mark.parametrize("longest", [1024, 1025, 2048, 2049])
+def test_decode_either_side_of_the_forms_limits(lb, H, G, D, longest):
+    for n in (2, 16):  # items for few SMs, and for most of them
+        lens = [longest - 97 * i if 97 * i < longest else 0 for i in range(n)]
+        p = Kv4Problem(f"lim{longest}{n}{D}", "bf16", H, G, D, 64, [1] * n, lens)
+        d = run_decode(lb, p)
+        torch().cuda.synchronize()
+        p.check(to_f64(d.o), f"{n} {longest}")
+
+
 def test_packed_of_many_sequences(lb):
     n = 4096
     lens = [5 + i % 40 for i in range(n)]
