@@ -34,7 +34,7 @@ constexpr int VD_THREADS = 256;
 constexpr int VD_WARPS = VD_THREADS / 32;
 constexpr int VD_MOST_THREADS = 768;  // of a CTA that draws
 constexpr int VD_VECS = 4;          // 16-byte vectors of a thread in flight
-// CTAs of an SM, and CTAs for an SM that the parts aim at: 265 MB in 47 us, 0.82 of the measured
+// CTAs of an SM, and CTAs for an SM that the parts aim at: 265 MB in 47 us by itself, 0.82 of the measured
 // rate (4 and 16: 48; rows left in L2 for the drawing, by loads that do not say that they
 // are the last: 74 to 77 us in all for 71).
 constexpr int VD_CTAS = 6, VD_AIM = 32;
