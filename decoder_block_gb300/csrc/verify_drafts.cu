@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(VD_MOST_THREADS) verify_draw_kernel(const __gr
   __shared__ int s_id[MOST];
   __shared__ bool s_keep[MOST];
   __shared__ VdBest s_best[VD_MOST_THREADS / 32];
-  __shared__ VdBest s_cta[2][VD_MAX_CLUSTER];  // every CTA's, of each search
+  __shared__ VdBest s_cta[3][VD_MAX_CLUSTER];  // every CTA's, of each search
   const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, threads = blockDim.x, warps = threads / 32;
   const int seq = blockIdx.x / a.cluster, rank = blockIdx.x % a.cluster;
   if (a.cluster > 1) ptx::cluster_sync();  // every CTA runs: the first one's shared memory may be written
@@ -454,6 +454,9 @@ __global__ void __launch_bounds__(VD_MOST_THREADS) verify_draw_kernel(const __gr
         const int at = groups * N + me;  // what is left of the row
         if (at < a.V)
           race(ld_logit<T>(x + at), both ? ld_logit<T>(y + at) : 0.f, ld_float_after_wait(noise + at), at, residual);
+      };
+      // the CTA's best into every CTA's array, through distributed shared memory
+      auto publish = [&](int which) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
           const float s = __shfl_xor_sync(0xffffffffu, best.score, o);
@@ -472,9 +475,6 @@ __global__ void __launch_bounds__(VD_MOST_THREADS) verify_draw_kernel(const __gr
           }
         }
         __syncthreads();  // (the next search writes there again)
-      };
-      // the CTA's best into every CTA's array, through distributed shared memory
-      auto publish = [&](int which) {
         if (threadIdx.x < a.cluster) {
           uint32_t dst = ptx::smem_u32(&s_cta[which][rank]);
           if (a.cluster > 1) dst = ptx::mapa_shared(dst, threadIdx.x);
@@ -488,11 +488,22 @@ __global__ void __launch_bounds__(VD_MOST_THREADS) verify_draw_kernel(const __gr
       publish(0);
       int last = 0;
       if (refused) {  // (in every CTA of the cluster alike)
-        float top = 0.f;
-        for (int k = 0; k < a.cluster; ++k) top = fmaxf(top, s_cta[0][k].score);
-        if (top == 0.f) {  // nothing of p - q is left: from p
-          search(false);
-          publish(last = 1);
+        auto nobody_won = [&](int which) {
+          float top = 0.f;
+          for (int k = 0; k < a.cluster; ++k) top = fmaxf(top, s_cta[which][k].score);
+          return top == 0.f;
+        };
+        // Either p - q is 0 everywhere, and the token is drawn from p, or no id that it leaves may be
+        // drawn, and there is no token: a race without the noise tells.  (Rare: an id at a time, in
+        // few registers.)
+#pragma unroll 1
+        for (int which = 1; which <= 2 && nobody_won(which - 1); ++which) {
+#pragma unroll 1
+          for (int at = me; at < a.V; at += stride)
+            race(ld_logit<T>(x + at), both ? ld_logit<T>(y + at) : 0.f,
+                 which == 1 ? 1.f : ld_float_after_wait(noise + at), at, which == 1);
+          publish(which);
+          last = which == 2 ? 2 : 0;
         }
       }
       if (rank == 0) {

@@ -386,7 +386,8 @@ typedef struct {
  *   in place of the first that is not kept, a token is drawn from
  *   max(p - q, 0) (a certain draft: p without x), from p where that is 0 everywhere;
  *   behind drafts that were all kept, a token is drawn from p at the last row;
- *   drawn from w: the id of the largest w[v] / noise[i][v], the lowest among equals.
+ *   drawn from w: the id of the largest w[v] / noise[i][v], the lowest among equals;
+ *   where every id that w leaves is one that is never drawn, no token (-1).
  * Greedy: a draft is kept while it is the id of the largest logit (the lowest id
  * among equals), and the token behind is that id.
  *   out_tokens [n_seqs][max_drafts + 1]: the kept drafts, the token drawn, then -1

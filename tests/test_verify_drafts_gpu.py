@@ -260,6 +260,50 @@ def test_noise_that_is_not_above_zero_is_never_drawn(lb):
     assert d.out.cpu().numpy().ravel().tolist() == [-1, -1, -1]
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [64, 40001])  # a CTA a sequence, a cluster a sequence
+@pytest.mark.parametrize("model", [True, False])
+def test_a_residual_whose_ids_have_no_noise_draws_nothing(lb, model, V, dtype):
+    """max(p - q, 0) is above 0 at ids that may not be drawn, and 0 elsewhere: no token, and not one from p, which
+    has weight at the refused draft and at every id that the draft's q covers."""
+    c = Drafts("rn", dtype, V, [1, 1, 1, 2], [1.0], model=model)
+    x = 6
+    high = np.arange(V) % 2 == 1   # p > q there
+    for i in range(c.n):
+        for j in range(c.drafts[i]):
+            c.target[c.offsets[i] + j] = store(np.where(high, 1.0, -1.0).astype(np.float32), dtype)
+            c.draft[i, j] = store(np.where(high, -1.0, 1.0).astype(np.float32), dtype)
+            c.tokens[c.offsets[i] + 1 + j] = x
+    c.uniforms[:] = 0.9            # p[x] / q[x] = e^-2
+    left = high if model else np.arange(V) != x
+    for i, bad in enumerate((0.0, -1.0, np.nan)):
+        c.noise[i, left] = bad
+    c.noise[3, left] = 0.0
+    c.noise[3, V - 3 if (V - 3) % 2 else V - 4] = 2.0  # one that may be drawn
+    d = c.run(lb)
+    c.check(d)
+    assert d.out[:3].max() == -1 and int(d.out[3, 0]) >= V - 4
+
+
+@pytest.mark.parametrize("V", [64, 40001])
+def test_an_empty_residual_is_drawn_from_p(lb, V):
+    """The other side: p <= q at every id and q has more there, so that p - q is 0 and the token comes from p, among the
+    ids whose noise lets it."""
+    c = Drafts("er", "f32", V, [1, 1, 1], [1.0])
+    c.uniforms[:] = 0.5
+    for i in range(3):
+        r = c.offsets[i]
+        c.tokens[r + 1] = 11
+        c.target[r] = -np.inf
+        c.draft[i, 0] = -np.inf
+        c.target[r, [40, V - 2]] = 1.0     # p = q = 1 / 2 at both; the draft, 11, has neither
+        c.draft[i, 0, [40, V - 2]] = 5.0
+    c.noise[:, 40], c.noise[:, V - 2] = [1.0, 2.0, 0.0], [2.0, 1.0, 0.0]
+    d = c.run(lb)
+    c.check(d)
+    assert d.out[:, 0].tolist() == [40, V - 2, -1]
+
+
 def test_bad_inputs_are_reported(lb):
     c = Drafts("bad", "f32", 300, [2, 2, 1], [1.0])
     c.tokens[1] = 300
