@@ -7,6 +7,11 @@
 // is v with probability w_v / sum w.  No running sum is needed for it, so nothing depends
 // on the order in which a row's parts are added up, and its parts can be searched apart.
 //
+// How near p / q is: an exponent (x - m) log2(e) / T has four roundings, 2^-22 of its size, which
+// is log2 V at most on average over a row's weights; p / q is off by ln 2 log2(V) 2^-22 (2.8e-6 for
+// 128256 ids), 2^-22 for each exponential and 2^-24 for each of a thread's additions.  Measured over
+// 4099 to 200003 ids: 6.5e-7 at most.
+//
 // Every logit has to be read once, and that bounds it.  Two kernels:
 //   rows   a CTA takes a part of a row, target's or draft's, and leaves its maximum m,
 //          sum of e^((x - m) / T) and, for greedy sequences, the id of m;

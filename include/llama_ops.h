@@ -394,7 +394,8 @@ typedef struct {
  *   n_accepted [n_seqs]: drafts kept
  *   logprobs   [n_seqs][max_drafts + 1]: ln p of each token of out_tokens, at the
  *              sequence's temperature (greedy: 1), 0 beside a -1; may be NULL
- * p and q are summed in fp32, in parts; u < p / q is decided to about 2^-21 of p / q.
+ * p and q are summed in fp32, in parts; u < p / q is decided to about 1e-5 of p / q
+ * (rows of up to 2^18 ids; 6.5e-7 at most where it was measured).
  * A logit of -inf has probability 0.  A row that holds a NaN or +inf, or nothing but
  * -inf, keeps no draft and draws no token (-1, logprob 0).  Nor does an empty slot,
  * and neither does a sequence whose offsets or row count are out of range or whose

@@ -391,6 +391,47 @@ def test_tokens_follow_the_target(lb):
     assert ((seen - n * p) ** 2 / (n * p)).sum() < 40.5
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("size,temp", [(0.2, 1.0), (2.5, 1.0), (2.5, 0.1), (2.5, 3.0)])
+def test_decisions_near_the_ratio(lb, dtype, size, temp):
+    """u within a few 1e-5 of p / q on both sides of it, over a wide vocabulary, flat and steep."""
+    V, n = 128256, 16
+    c = Drafts("near", dtype, V, [1] * n, [temp])
+    rng = np.random.default_rng(5)
+    row = (rng.standard_normal(V) * size).astype(np.float32)
+    c.target[:] = store(row, dtype)
+    c.draft[:] = store(row + (rng.standard_normal(V) * 0.2 * size * temp).astype(np.float32), dtype)
+    p, q = (np.exp((y - y.max()) / temp) for y in (synth.as_f64(c.target)[0], synth.as_f64(c.draft)[0, 0]))
+    ratio = (p / p.sum()) / (q / q.sum())
+    at = np.flatnonzero((ratio > 0.3) & (ratio < 0.9) & (p > 0))
+    off = np.concatenate([np.linspace(-4e-5, -1.1e-5, n // 2), np.linspace(1.1e-5, 4e-5, n // 2)])
+    for i in range(n):
+        x = at[(i * 977) % len(at)]
+        c.tokens[c.offsets[i] + 1] = x
+        c.uniforms[i, 0] = ratio[x] * (1 + off[i])
+    d = c.run(lb)
+    assert d.acc.cpu().numpy().tolist() == [1] * (n // 2) + [0] * (n // 2)
+    c.check(d)
+
+
+@pytest.mark.parametrize("V,temp", [(4099, 0.3), (128256, 0.1), (128256, 0.7), (200003, 0.9)])
+def test_decisions_on_certain_drafts_near_p(lb, V, temp):
+    """Half of the probability on the draft and the rest flat: every weight of the rest has the same rounded argument,
+    so that their errors add up."""
+    n = 8
+    c = Drafts("near2", "f32", V, [1] * n, [temp], model=False)
+    temp, x = float(np.float32(temp)), 77
+    c.target[:] = 0.0
+    c.target[:, x] = np.float32(temp * np.log(V - 1) * 1.01)
+    c.tokens[1::2] = x
+    y = synth.as_f64(c.target)[0] / temp
+    p = 1 / np.exp(y - y.max()).sum()
+    c.uniforms[:, 0] = p * (1 + np.concatenate([np.linspace(-4e-5, -1.1e-5, n // 2), np.linspace(1.1e-5, 4e-5, n // 2)]))
+    d = c.run(lb)
+    assert d.acc.cpu().numpy().tolist() == [1] * (n // 2) + [0] * (n // 2)
+    c.check(d)
+
+
 def test_a_speculative_step(lb):
     """Write, attention over the 4-bit pages, logits, verification, one after another on one stream: greedy drafts that
     the step itself would choose are all kept, and a wrong one ends them."""
