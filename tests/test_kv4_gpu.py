@@ -150,6 +150,47 @@ def test_write_positions_and_pages_out_of_range(lb):
     t.cuda.synchronize()
 
 
+@pytest.mark.parametrize("halves", [False, True])
+@pytest.mark.parametrize("dtype,H,G,D,page", [("bf16", 4, 2, 128, 16), ("bf16", 2, 1, 64, 32), ("f32", 3, 3, 16, 16)])
+def test_write_stores_the_rows_in_range_and_no_other_byte(lb, dtype, H, G, D, page, halves):
+    """Rows before their sequence's start, positions behind the table, page ids out of range at a first and at a later
+    page, beside rows that are fine, some of them in the same sequences: both pools byte for byte, q_out bit for bit."""
+    c = WriteCase(f"wr{dtype}{D}", dtype, H, G, D, page, [5, 4, 3, 2 * page + 3, page + 9, 2],
+                  [3, 40, 3, 3 * page, 3 * page - 5, 1], halves, pad=2)
+    p, limit = c.p, 3 * page - 2
+    c.table = _table(limit, D)     # the fourth sequence's last two positions are behind it
+    p.table[2, 0] = -1
+    p.table[3, 1] = p.n_pages      # the middle page: rows before and behind it are stored
+    p.table[4, 2] = 0x7fffffff
+    q, pools = np.full((p.T, H, D), 7.0, F32), [x.copy() for x in p.pools]
+    stored = 0
+    for i, (n, L) in enumerate(zip(p.q_lens, p.kv_lens)):
+        for t in range(n):
+            row, pos = p.offsets[i] + t, L - n + t
+            if not 0 <= pos < limit:
+                q[row] = 0.0
+                continue
+            rot = _rotate(c.x[row:row + 1, :H + G], c.table[pos:pos + 1], halves)[0]
+            q[row] = rot[:H]
+            at = int(p.table[i, pos // page])
+            if not 0 <= at < p.n_pages:
+                continue
+            stored += 1
+            for pool, new in zip(pools, (rot[H:], c.x[row, H + G:])):
+                codes, byte = quantise(new)
+                block, s = pool[at], pos % page
+                block[:, s * D // 2:(s + 1) * D // 2] = pack(codes)
+                block[:, page * D // 2:].reshape(G, page, D // 16)[:, s] = byte
+    assert page < stored < int(p.offsets[-1]) - 8
+    d = c.run(lb)
+    for name, got, want in zip("kv", (d.k, d.v), pools):
+        bad = np.nonzero(got.cpu().numpy() != want)
+        assert not len(bad[0]), f"{name}: {len(bad[0])} bytes differ, first {[int(b[0]) for b in bad]}"
+    want = store(q, dtype)
+    assert np.array_equal(to_host_bits(d.q_out).view(want.dtype), want)
+    assert int(d.status[0]) == lb.LLAMA_ERR_RANGE
+
+
 @pytest.mark.parametrize("dtype,H,G,D,page", SHAPES)
 @pytest.mark.parametrize("q_lens,kv_lens,pad", [([300, 0, 17], [300, 9, 17], 5), ([4, 30], [100, 20], 0), ([1], [77], 2),
                                                 ([900, 800], [900, 2000], 0)])
@@ -227,6 +268,19 @@ def test_packed(lb, dtype, H, G, D, name, q_lens, kv_lens, max_kv):
     torch().cuda.synchronize()
     p.check(to_f64(d.o), name)
     assert int(d.status[0]) == 0
+
+
+@pytest.mark.parametrize("H,G,D,page", [(4, 1, 128, 32), (3, 1, 64, 16)])
+def test_long_caches(lb, H, G, D, page):
+    """One token and a few drafts behind more than 100000 keys, beside a short sequence, and a prompt of 3000 rows."""
+    for q_lens, kv_lens in (([1, 1], [100003, 40]), ([3, 1], [100003, 40]), ([3001], [3100])):
+        p = Kv4Problem(f"long{D}{len(q_lens)}{q_lens[0]}", "bf16", H, G, D, page, q_lens, kv_lens)
+        runs = [run_packed] + ([run_decode] if max(q_lens) == 1 else [])
+        for run in runs:
+            d = run(lb, p)
+            torch().cuda.synchronize()
+            p.check(to_f64(d.o), str(q_lens))
+            assert int(d.status[0]) == 0
 
 
 @pytest.mark.parametrize("run", [run_packed, run_decode])

@@ -391,6 +391,39 @@ def test_tokens_follow_the_target(lb):
     assert ((seen - n * p) ** 2 / (n * p)).sum() < 40.5
 
 
+def _follows(p, seen):
+    """Chi-squared over 8 tokens: the 1e-6 quantile of 7 degrees of freedom is 40.5."""
+    p = np.exp(p.astype(np.float64))
+    p /= p.sum()
+    n = len(seen)
+    count = np.bincount(seen, minlength=8)
+    return ((count - n * p) ** 2 / (n * p)).sum() < 40.5
+
+
+def test_tokens_follow_the_target_where_drafts_are_certain(lb):
+    """Looked-up drafts, one token for every sequence: what comes out at the first place is distributed as p."""
+    V, n = 8, 4096
+    c = Drafts("chc", "f32", V, [1] * n, [1.0], model=False)
+    c.target[:] = np.array([0.3, -1, 0.8, 0, -0.4, 1.2, -2, 0.1], np.float32)
+    for x in (5, 6):
+        c.tokens[1::2] = x
+        assert _follows(c.target[0], c.run(lb).out[:, 0].cpu().numpy())
+
+
+def test_the_token_behind_kept_drafts_follows_the_target(lb):
+    """Drafts that are all kept (u = 0): the token behind is distributed as p of the last row, at the temperature."""
+    V, n = 8, 4096
+    for model in (True, False):
+        c = Drafts("chb", "f32", V, [1] * n, [0.5], model=model)
+        c.target[1::2] = np.array([0.3, -1, 0.8, 0, -0.4, 0.7, -0.5, 0.1], np.float32)
+        c.tokens[1::2] = c.tokens[1::2] % V
+        c.target[0::2], c.draft[:] = 0.0, 0.0
+        c.uniforms[:] = 0.0
+        d = c.run(lb)
+        assert d.acc.cpu().numpy().min() == 1
+        assert _follows(2 * c.target[1], d.out[:, 1].cpu().numpy())
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("size,temp", [(0.2, 1.0), (2.5, 1.0), (2.5, 0.1), (2.5, 3.0)])
 def test_decisions_near_the_ratio(lb, dtype, size, temp):
