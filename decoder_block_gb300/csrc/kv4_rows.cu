@@ -34,6 +34,7 @@
 // bound by their latency (255 registers leave two warps to a scheduler).
 #include <cuda_fp16.h>
 #include <float.h>
+#include <limits.h>
 
 #include <type_traits>
 
@@ -66,6 +67,7 @@ constexpr float KD_VALUE = 2.0f;  // V's operand is half of V
 constexpr int KD_DIRECT_KEYS = 2048, KD_DIRECT_FEW = 1024 * 128;
 constexpr int KD_MAX_NB = 3;
 constexpr int KD_ROUNDS = 10, KD_FEW_KEYS = 384;  // of packed calls: see kv4_rows_fit
+constexpr int KD_FEW_ROWS = 48, KD_MIXED_ROUNDS = 48;  // see kv4_rows_few
 constexpr int KD_BATCH = 2;  // pieces that a join within a CTA reads at a time
 constexpr int KD_LEAST = 4;  // tiles of a CTA's run, at least: a warp on each scheduler
 
@@ -97,6 +99,7 @@ struct KdArgs {
   PagedView pv;
   PackedView b;  // q_offsets null: one row of q and o per sequence
   int H, G, r;   // r: heads of a group
+  int few;       // tokens of a sequence that this kernel takes; those of others are another's
   int times;     // items of a sequence for each of the tiles that `first` counts
   int most;      // tiles that `first` may count: offsets that descend make sequences overlap
   int direct;
@@ -251,9 +254,13 @@ __device__ __forceinline__ uint32_t ld_byte(uint32_t at) {
   return v;
 }
 
-// The rows and keys of a sequence as its items have them; no rows where they are out of range.
+// The rows and keys of a sequence as its items have them; no rows where they are out of range
+// or another kernel's.
 __device__ __forceinline__ SeqSpan kd_span(const KdArgs &a, int i) {
-  if (a.b.q_offsets != nullptr) return seq_span(a.b, a.pv, i);
+  if (a.b.q_offsets != nullptr) {
+    const SeqSpan s = seq_span(a.b, a.pv, i);
+    return s.count <= a.few ? s : SeqSpan{s.first, 0, 0};
+  }
   return SeqSpan{i, 1, checked_len(ld_after_wait(a.b.kv_lens + i), a.b.max_kv_len, a.pv)};
 }
 template <int NB>
@@ -915,8 +922,8 @@ long long most_tiles(const PackedView &b, int H, int G) {
 }
 
 cudaError_t launch_rows(const bf16 *q, const uint8_t *k, const uint8_t *v, bf16 *o, const PagedView &pv,
-                        const PackedView &b, int H, int G, int D, void *workspace, const KdPlan &p, int *status,
-                        cudaStream_t st) {
+                        const PackedView &b, int H, int G, int D, int few, void *workspace, const KdPlan &p,
+                        int *status, cudaStream_t st) {
   KdArgs a;
   a.q = q;
   a.k = k;
@@ -927,6 +934,7 @@ cudaError_t launch_rows(const bf16 *q, const uint8_t *k, const uint8_t *v, bf16 
   a.H = H;
   a.G = G;
   a.r = H / G;
+  a.few = few;
   a.direct = p.direct;
   a.times = b.q_offsets != nullptr ? G : G * ((a.r + 8 * p.nb - 1) / (8 * p.nb));
   a.most = b.q_offsets != nullptr ? (int)most_tiles(b, H, G) : 0x7fffffff;
@@ -977,7 +985,7 @@ cudaError_t launch_kv4_decode(const bf16 *q, const uint8_t *k, const uint8_t *v,
                               const int *kv_lens, int n_seqs, int max_kv_len, int H, int G, int D, void *workspace,
                               int *status, cudaStream_t st) {
   const PackedView b = decode_view(kv_lens, n_seqs, max_kv_len);
-  return launch_rows(q, k, v, o, pv, b, H, G, D, workspace, plan_of(b, H / G, H, G, D, true), status, st);
+  return launch_rows(q, k, v, o, pv, b, H, G, D, INT_MAX, workspace, plan_of(b, H / G, H, G, D, true), status, st);
 }
 
 // Few rows, which tcgen05's 128-row tiles would mostly pad: those of one item on average, or
@@ -997,12 +1005,31 @@ bool kv4_rows_fit(const PackedView &b, int H, int G) {
                           ((long long)b.n_tokens * (H / G) / (8 * KD_MAX_NB) + b.n_seqs);
   return !few_keys && tiles <= (long long)KD_ROUNDS * sm_count() * 8;
 }
+// The average says nothing of a prompt among single tokens, whose keys would be unpacked again for
+// every 24 of its rows.  Where one sequence may bring so many that a warp has KD_MIXED_ROUNDS of
+// their tiles, at the longest length, sequences of more than KD_FEW_ROWS rows are left to tcgen05
+// (64 sequences of 40 rows: 128 us here, 110 there).  8 KV heads of four, single tokens and a
+// prompt, all here / shared out: 255 behind up to 300 keys and 1024 behind 6000 490 / 175 us, 1000
+// behind 500 and 1000 behind 6000 825 / 224, at 62 rounds (128 and 512 behind 3000) 165 / 108, at 55
+// (64 and 256 behind 6000) 123 / 79; at 24 (64 and 300 behind 2000) 64 / 52.  Where there is no
+// such sequence the other's three kernels cost 4 to 10 us: 256 sequences of five rows behind up to
+// 4096 keys (145 rounds) 253 / 263, 64 of them (36) 69 / 80.
+int kv4_rows_few(const PackedView &b, int H, int G) {
+  const long long rows = ((long long)b.n_tokens - b.n_seqs + 1) * (H / G);
+  const int few = H / G < KD_FEW_ROWS ? KD_FEW_ROWS / (H / G) : 1;
+  if (rows <= KD_FEW_ROWS) return INT_MAX;
+  const long long tiles =
+      (long long)G * kd_tiles<KD_MAX_NB>(b.max_kv_len) * ((rows + 8 * KD_MAX_NB - 1) / (8 * KD_MAX_NB));
+  return tiles > (long long)KD_MIXED_ROUNDS * sm_count() * 8 ? few : INT_MAX;
+}
 size_t kv4_rows_workspace_bytes(const PackedView &b, int H, int G, int D) {
   return plan_of(b, rows_of(b, H, G), H, G, D, false).bytes;
 }
 cudaError_t launch_kv4_rows(const bf16 *q, const uint8_t *k, const uint8_t *v, bf16 *o, const PagedView &pv,
-                            const PackedView &b, int H, int G, int D, void *workspace, int *status, cudaStream_t st) {
-  return launch_rows(q, k, v, o, pv, b, H, G, D, workspace, plan_of(b, rows_of(b, H, G), H, G, D, false), status, st);
+                            const PackedView &b, int H, int G, int D, int few, void *workspace, int *status,
+                            cudaStream_t st) {
+  return launch_rows(q, k, v, o, pv, b, H, G, D, few, workspace, plan_of(b, rows_of(b, H, G), H, G, D, false), status,
+                     st);
 }
 
 }  // namespace llama

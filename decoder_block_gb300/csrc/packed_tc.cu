@@ -45,6 +45,7 @@
 #include <cudaTypedefs.h>
 #include <cuda_fp16.h>
 #include <float.h>
+#include <limits.h>
 
 #include "kv4.cuh"
 #include "paged_kernels.h"
@@ -211,8 +212,8 @@ __device__ __forceinline__ int item_end(const PtItem &it, int Mq, int t) {
 // keeps those of its first blocks, so a batch of up to 4096 blocks is looked up once.
 constexpr int PT_KEEP = 4;
 
-__global__ void __launch_bounds__(PT_PLAN_THREADS) packed_plan_kernel(PagedView pv, PackedView b, int units, int Bq,
-                                                                      int sms, int max_blocks, int max_entries,
+__global__ void __launch_bounds__(PT_PLAN_THREADS) packed_plan_kernel(PagedView pv, PackedView b, int few, int units,
+                                                                      int Bq, int sms, int max_blocks, int max_entries,
                                                                       PtPlan *plan, PtEntry *entries, PtSplit *splits,
                                                                       int *status) {
   __shared__ int first_blk[LLAMA_PACKED_MAX_SEQS + 1];  // blocks before sequence i
@@ -238,7 +239,7 @@ __global__ void __launch_bounds__(PT_PLAN_THREADS) packed_plan_kernel(PagedView 
     if (i < b.n_seqs) {
       check_seq(b, pv, i, status);
       const SeqSpan s = seq_span(b, pv, i);
-      n = (s.count + Bq - 1) / Bq;
+      n = s.count > few ? (s.count + Bq - 1) / Bq : 0;  // (those of few tokens are another kernel's)
       if (i0 == 0) seqs[tid] = s;
     }
     const int end = add_counts(base, cta_scan(n, warp_sums));
@@ -247,6 +248,10 @@ __global__ void __launch_bounds__(PT_PLAN_THREADS) packed_plan_kernel(PagedView 
     __syncthreads();
     base = warp_sums[0];
     __syncthreads();
+  }
+  if (base == 0) {  // (a mixed batch without long sequences: what follows takes 3 us)
+    if (tid == 0) *plan = PtPlan{};
+    return;
   }
   // (more blocks than well-formed offsets can make: see add_counts)
   const int n_blk = min(base, max_blocks);
@@ -1312,8 +1317,8 @@ struct PtSizes {
   size_t off_entries = 0, off_splits = 0, off_part = 0, bytes = 0;
 };
 
-// tiles_of_item: query tiles of an item.
-PtSizes packed_sizes(const PackedView &b, int H, int G, int D, int sms, int tiles_of_item) {
+// tiles_of_item: query tiles of an item.  planned: not direct, however few the items.
+PtSizes packed_sizes(const PackedView &b, int H, int G, int D, int sms, int tiles_of_item, bool planned = false) {
   PtSizes z;
   const int r = H / G;
   z.rb = r < 128 ? r : 128;
@@ -1327,7 +1332,7 @@ PtSizes packed_sizes(const PackedView &b, int H, int G, int D, int sms, int tile
   // the idle SMs (planned / direct: 8B-shaped, 512 tokens behind 600 29 / 21 us, 1100
   // behind 900 39 / 33, but three tokens, the longest behind 1900, 20 / 28).
   const long long items = z.max_blocks * z.units, tiles = (b.max_kv_len + PT_KEYS - 1) / PT_KEYS;
-  if (items <= sms && tiles <= 16 && tiles * (sms - items) <= 8LL * sms) return z;
+  if (!planned && items <= sms && tiles <= 16 && tiles * (sms - items) <= 8LL * sms) return z;
   // Split items: none where no sequence is long enough (no share is below PT_MIN_PIECE) or
   // every SM has an item anyway; see the planner.
   z.max_slots = b.max_kv_len > (PT_MIN_PIECE + PT_SPLIT_COST) * PT_KEYS && z.units < sms ? 2 * sms / z.units : 0;
@@ -1341,10 +1346,11 @@ PtSizes packed_sizes(const PackedView &b, int H, int G, int D, int sms, int tile
   return z;
 }
 
-// k, v: bf16 pages, or with W > 0 pages held in 4 bits, of heads of width W.
+// k, v: bf16 pages, or with W > 0 pages held in 4 bits, of heads of width W.  few: sequences of up
+// to so many tokens are left out (0: none is).
 template <int D, int W, int QT>
 cudaError_t launch_tc(const bf16 *q, const void *k, const void *v, bf16 *o, const PagedView &pv, const PackedView &b,
-                      int H, int G, int width, void *workspace, int *status, cudaStream_t st) {
+                      int H, int G, int width, int few, void *workspace, int *status, cudaStream_t st) {
   constexpr int BYTES = PtShared<D, W, QT>::BYTES, ISSUERS = W > 0 ? PtShared<D, W, QT>::WARPS : 4;
   static PerContextOnce attr;
   cudaError_t e = attr.run([] {
@@ -1357,7 +1363,7 @@ cudaError_t launch_tc(const bf16 *q, const void *k, const void *v, bf16 *o, cons
   });
   if (e != cudaSuccess) return e;
   const int sms = sm_count();
-  const PtSizes z = packed_sizes(b, H, G, D, sms, QT);
+  const PtSizes z = packed_sizes(b, H, G, D, sms, QT, few > 0);
   PtArgs a;
   a.o = o;
   a.pv = pv;
@@ -1403,7 +1409,7 @@ cudaError_t launch_tc(const bf16 *q, const void *k, const void *v, bf16 *o, cons
   PtSplit *splits = reinterpret_cast<PtSplit *>(w + z.off_splits);
   a.part = reinterpret_cast<float *>(w + z.off_part);
   count_launch();
-  e = launch_pdl(packed_plan_kernel, dim3(1), dim3(PT_PLAN_THREADS), 0, st, pv, b, z.units, a.Bq, sms,
+  e = launch_pdl(packed_plan_kernel, dim3(1), dim3(PT_PLAN_THREADS), 0, st, pv, b, few, z.units, a.Bq, sms,
                  (int)z.max_blocks, (int)z.max_entries, a.plan, a.entries, splits, status);
   if (e != cudaSuccess) return e;
   const long long items = z.max_entries * z.units;
@@ -1425,8 +1431,8 @@ size_t packed_tc_workspace_bytes(const PackedView &b, int H, int G, int D) {
 
 cudaError_t launch_packed_tc(const bf16 *q, const bf16 *k, const bf16 *v, bf16 *o, const PagedView &pv,
                              const PackedView &b, int H, int G, int D, void *workspace, int *status, cudaStream_t st) {
-  if (D == 128) return launch_tc<128, 0, 2>(q, k, v, o, pv, b, H, G, D, workspace, status, st);
-  return launch_tc<64, 0, 2>(q, k, v, o, pv, b, H, G, D, workspace, status, st);
+  if (D == 128) return launch_tc<128, 0, 2>(q, k, v, o, pv, b, H, G, D, 0, workspace, status, st);
+  return launch_tc<64, 0, 2>(q, k, v, o, pv, b, H, G, D, 0, workspace, status, st);
 }
 
 namespace {
@@ -1439,27 +1445,41 @@ int kv4_tiles(const PackedView &b, int H, int G) {
 }
 template <int QT>
 cudaError_t launch_kv4(const bf16 *q, const uint8_t *k, const uint8_t *v, bf16 *o, const PagedView &pv,
-                       const PackedView &b, int H, int G, int D, void *workspace, int *status, cudaStream_t st) {
+                       const PackedView &b, int H, int G, int D, int few, void *workspace, int *status,
+                       cudaStream_t st) {
   switch (D) {
-    case 16: return launch_tc<64, 16, QT>(q, k, v, o, pv, b, H, G, D, workspace, status, st);
-    case 32: return launch_tc<64, 32, QT>(q, k, v, o, pv, b, H, G, D, workspace, status, st);
-    case 64: return launch_tc<64, 64, QT>(q, k, v, o, pv, b, H, G, D, workspace, status, st);
-    case 128: return launch_tc<128, 128, QT>(q, k, v, o, pv, b, H, G, D, workspace, status, st);
+    case 16: return launch_tc<64, 16, QT>(q, k, v, o, pv, b, H, G, D, few, workspace, status, st);
+    case 32: return launch_tc<64, 32, QT>(q, k, v, o, pv, b, H, G, D, few, workspace, status, st);
+    case 64: return launch_tc<64, 64, QT>(q, k, v, o, pv, b, H, G, D, few, workspace, status, st);
+    case 128: return launch_tc<128, 128, QT>(q, k, v, o, pv, b, H, G, D, few, workspace, status, st);
   }
   return cudaErrorInvalidValue;
+}
+// Where the kernel of few rows leaves long sequences to this one, each has a part of the workspace.
+size_t rows_part_bytes(const PackedView &b, int H, int G, int D) {
+  return (kv4_rows_workspace_bytes(b, H, G, D) + 127) / 128 * 128;
 }
 }  // namespace
 
 size_t packed_kv4_workspace_bytes(const PackedView &b, int H, int G, int D) {
-  if (kv4_rows_fit(b, H, G)) return kv4_rows_workspace_bytes(b, H, G, D);
-  return packed_sizes(b, H, G, D < 64 ? 64 : D, sm_count(), kv4_tiles(b, H, G)).bytes;
+  const int width = D < 64 ? 64 : D;
+  if (!kv4_rows_fit(b, H, G)) return packed_sizes(b, H, G, width, sm_count(), kv4_tiles(b, H, G)).bytes;
+  if (kv4_rows_few(b, H, G) == INT_MAX) return kv4_rows_workspace_bytes(b, H, G, D);
+  return rows_part_bytes(b, H, G, D) + packed_sizes(b, H, G, width, sm_count(), 2, true).bytes;
 }
 
 cudaError_t launch_packed_kv4(const bf16 *q, const uint8_t *k, const uint8_t *v, bf16 *o, const PagedView &pv,
                               const PackedView &b, int H, int G, int D, void *workspace, int *status, cudaStream_t st) {
-  if (kv4_rows_fit(b, H, G)) return launch_kv4_rows(q, k, v, o, pv, b, H, G, D, workspace, status, st);
-  return kv4_tiles(b, H, G) == 1 ? launch_kv4<1>(q, k, v, o, pv, b, H, G, D, workspace, status, st)
-                                 : launch_kv4<2>(q, k, v, o, pv, b, H, G, D, workspace, status, st);
+  if (!kv4_rows_fit(b, H, G))
+    return kv4_tiles(b, H, G) == 1 ? launch_kv4<1>(q, k, v, o, pv, b, H, G, D, 0, workspace, status, st)
+                                   : launch_kv4<2>(q, k, v, o, pv, b, H, G, D, 0, workspace, status, st);
+  const int few = kv4_rows_few(b, H, G);
+  if (few != INT_MAX) {
+    const cudaError_t e = launch_kv4<2>(q, k, v, o, pv, b, H, G, D, few,
+                                        reinterpret_cast<char *>(workspace) + rows_part_bytes(b, H, G, D), status, st);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_kv4_rows(q, k, v, o, pv, b, H, G, D, few, workspace, status, st);
 }
 
 }  // namespace llama

@@ -104,9 +104,13 @@ cudaError_t launch_paged_decode_tc(const bf16 *q, const bf16 *k, const bf16 *v, 
 
 // Packed attention of few rows a sequence over pages held in 4 bits (kv4_rows.cu), where it fits.
 bool kv4_rows_fit(const PackedView &b, int H, int G);
+// Tokens of a sequence that it is to take where it fits: sequences of more are left to packed_tc.cu
+// (INT_MAX: all are few).
+int kv4_rows_few(const PackedView &b, int H, int G);
 size_t kv4_rows_workspace_bytes(const PackedView &b, int H, int G, int D);
 cudaError_t launch_kv4_rows(const bf16 *q, const uint8_t *k, const uint8_t *v, bf16 *o, const PagedView &pv,
-                            const PackedView &b, int H, int G, int D, void *workspace, int *status, cudaStream_t st);
+                            const PackedView &b, int H, int G, int D, int few, void *workspace, int *status,
+                            cudaStream_t st);
 
 // Decode attention over pages held in 4 bits, q and o bf16 (kv4_rows.cu).
 bool kv4_decode_fits(int n_seqs, int max_kv_len, int H, int G);
