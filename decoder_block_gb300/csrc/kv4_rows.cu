@@ -67,7 +67,7 @@ constexpr float KD_VALUE = 2.0f;  // V's operand is half of V
 constexpr int KD_DIRECT_KEYS = 2048, KD_DIRECT_FEW = 1024 * 128;
 constexpr int KD_MAX_NB = 3;
 constexpr int KD_ROUNDS = 10, KD_FEW_KEYS = 384;  // of packed calls: see kv4_rows_fit
-constexpr int KD_FEW_ROWS = 48, KD_MIXED_ROUNDS = 48;  // see kv4_rows_few
+constexpr int KD_FEW_ROWS = 48, KD_MIXED_ROUNDS = 96;  // see kv4_rows_few
 constexpr int KD_BATCH = 2;  // pieces that a join within a CTA reads at a time
 constexpr int KD_LEAST = 4;  // tiles of a CTA's run, at least: a warp on each scheduler
 
@@ -1009,11 +1009,12 @@ bool kv4_rows_fit(const PackedView &b, int H, int G) {
 // every 24 of its rows.  Where one sequence may bring so many that a warp has KD_MIXED_ROUNDS of
 // their tiles, at the longest length, sequences of more than KD_FEW_ROWS rows are left to tcgen05
 // (64 sequences of 40 rows: 128 us here, 110 there).  8 KV heads of four, single tokens and a
-// prompt, all here / shared out: 255 behind up to 300 keys and 1024 behind 6000 490 / 175 us, 1000
-// behind 500 and 1000 behind 6000 825 / 224, at 62 rounds (128 and 512 behind 3000) 165 / 108, at 55
-// (64 and 256 behind 6000) 123 / 79; at 24 (64 and 300 behind 2000) 64 / 52.  Where there is no
-// such sequence the other's three kernels cost 4 to 10 us: 256 sequences of five rows behind up to
-// 4096 keys (145 rounds) 253 / 263, 64 of them (36) 69 / 80.
+// prompt, all here / shared out: 255 behind up to 300 keys and 1024 behind 6000 490 / 181 us, 500
+// behind 100 and 2000 behind 100 318 / 94.  Where there is no such sequence the other's three
+// kernels cost 5 to 7 us: 64 sequences of five rows behind 300 keys 24 / 29, behind 2000 66 / 73, 256
+// behind up to 4096 236 / 243.  Below the limit batches stay here, mixed ones for longer than they
+// had to (128 and 512 behind 3000, 62 rounds, 164 / 111; 64 and 300 behind 8000, 86 rounds, 176 / 104),
+// the drafts of 64 users under a bound of 8192 keys (72 rounds) without those kernels.
 int kv4_rows_few(const PackedView &b, int H, int G) {
   const long long rows = ((long long)b.n_tokens - b.n_seqs + 1) * (H / G);
   const int few = H / G < KD_FEW_ROWS ? KD_FEW_ROWS / (H / G) : 1;

@@ -151,6 +151,7 @@ struct PtArgs {
   const uint8_t *kc, *vc;  // pools of 4-bit blocks
   int *status;
   long long wait_cycles;  // a wait's budget
+  bool maybe_none;        // there may be no entry: short sequences are another kernel's
 };
 
 __device__ __forceinline__ uint32_t pt_pack_half2(float a, float b) {
@@ -582,6 +583,11 @@ __global__ void __launch_bounds__(64 + QT * 128 + ISSUERS * 32, 1)
   using L = PtLayout<D, QT>;
   constexpr int ATOMS = D / 64;
   constexpr int SOFT = 4 * QT, FIRST_ISSUER = 2 + SOFT;  // softmax warps from 2 on, issuers behind them
+  if (W > 0 && a.maybe_none) {  // before the rest is set up: 1 us
+    allow_dependents_launch();
+    grid_dependency_wait();
+    if (*reinterpret_cast<volatile int *>(&a.plan->n_entries) == 0) return;
+  }
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::OFF_BAR);
@@ -1385,6 +1391,7 @@ cudaError_t launch_tc(const bf16 *q, const void *k, const void *v, bf16 *o, cons
   a.vc = W > 0 ? (const uint8_t *)v : nullptr;
   a.status = status;
   a.wait_cycles = op_wait_cycles();
+  a.maybe_none = few > 0;
   CUtensorMap mq, mk, mv;
   if (!make_heads_map(&mq, q, b.n_tokens, H, width, a.rb, a.Mq)) return cudaErrorInvalidValue;
   if (W > 0) {
@@ -1418,7 +1425,7 @@ cudaError_t launch_tc(const bf16 *q, const void *k, const void *v, bf16 *o, cons
                  mk, mv, a);
   if (e != cudaSuccess || z.max_split == 0) return e;
   count_launch();
-  const long long joins = (long long)z.max_split * z.units * 4 * QT, ctas = (long long)JOIN_CTAS * sms;
+  const long long joins = (long long)z.max_split * z.units * 4 * QT, ctas = (long long)(few > 0 ? 1 : JOIN_CTAS) * sms;  // (4: 2 us more without any)
   return launch_pdl(packed_join_kernel<D, QT>, dim3((unsigned)(joins < ctas ? joins : ctas)), dim3(D / JOIN_COLS * 32), 0,
                     st, a, (const PtSplit *)splits);
 }
