@@ -4,8 +4,11 @@
 // The scale's byte is the top of an fp32 or bf16 number -- three bits of mantissa under
 // an exponent that starts at -20 -- so that it turns into one with an add and a shift,
 // reaches from 2^-20 to 3840 without a factor per tensor, and a code times it has seven
-// significant bits: bf16 holds every value exactly.  Equal steps lose less of such
-// blocks than fp4's do (normal values: an error of 0.093 of their RMS for 0.095 to 0.100).
+// significant bits: bf16 holds every value exactly.  Equal steps lose less of such blocks than
+// fp4's do (normal values: an error of 0.0929 of their RMS, for 0.0942 with a scale that is exactly
+// a sixth of the largest and 0.1004 with one of these).  The smallest scale that reaches the
+// largest value is found without trying: the best of it and the next four smaller ones, which cut
+// the largest off, would lose 0.0828.
 #pragma once
 
 #include <stdint.h>

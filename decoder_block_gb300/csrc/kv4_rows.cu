@@ -14,9 +14,10 @@
 // leaves every thread whole words of codes.  Two codes become two 16-bit numbers with a
 // shift, a masked or and an fma (kv4.cuh): K bf16 as Q is, V fp16, and P^T, which comes from
 // S^T by movmatrix, fp16 too.  V's products run over keys, so the words of two keys are
-// interleaved first, half a word at a time.  (tcgen05 takes its operands from shared memory:
-// the 16-bit numbers written there and read back are four times the codes, and its 128 rows
-// are mostly padding here: 64 sequences of 5 rows on 8 KV heads 104 us with it.)
+// interleaved first, half a word at a time.  (With the rows on tcgen05's side of 128, as in
+// packed_tc.cu, the 16-bit numbers go through shared memory, four times the codes, and the side is
+// mostly padding: 64 sequences of 5 rows on 8 KV heads 104 us.  Keys on that side, from tensor
+// memory for one of the two products, were not tried.)
 // Each warp copies its own tiles into its own shared memory, a few tiles ahead, and waits
 // for nothing but those copies.
 //
@@ -30,8 +31,10 @@
 // Measured, D = 128 and 8 KV heads of four: 64 sequences of 253 to 4096 keys 41.5 us, of which
 // about 11 are the kernels' beginnings and joins; between, 5.3 TB/s (0.78 of the copy rate),
 // instructions issued in two cycles of three.  One sequence of 120001 keys 40.5 us.  64
-// sequences of five rows 71.5 us: three times the products on the same unpacked numbers,
-// bound by their latency (255 registers leave two warps to a scheduler).
+// sequences of five rows 71 us: three times the products on the same unpacked numbers,
+// bound by their latency (255 registers, with 64 bytes of them spilled, leave two warps to a
+// scheduler).  The page ids of a tile are looked up by an index of run time, which puts them in
+// 16 to 32 bytes of local memory in every form.
 #include <cuda_fp16.h>
 #include <float.h>
 #include <limits.h>
@@ -46,8 +49,8 @@ namespace llama {
 namespace {
 
 // Keys of a warp's tile: as many as the registers have room for, what is done once a tile is a
-// third of a tile of 32 keys.  (64 sequences of one and of three rows, four heads to a group: 45 and
-// 51.6 us at 64 keys, 47 and 55.5 at 32.)
+// third of a tile of 32 keys.  (64 sequences of one and of three rows, four heads to a group: 41.6
+// and 51.6 us at 64 keys, 46.7 and 55.6 at 32.)
 constexpr int kd_keys(int NB) { return NB <= 2 ? 64 : 32; }
 // Places before an item's first tile in the row that is dealt out: an item's beginning and end
 // (its queries, its output) take as long as 64 keys.  (64 sequences of 253 to 4096 keys, 8 KV

@@ -19,8 +19,8 @@
 //          takes the decisions, and searches a part of the one row (with its draft's and
 //          the noise) that the next token is drawn from.  The CTAs meet through
 //          distributed shared memory.
-// 64 sequences of four drafts over 128256 ids (fp32, with a draft's logits): 69.6 us, 44 of them
-// the rows kernel at 6.1 TB/s (0.9 of the copy rate); in the draw kernel the decisions take
+// 64 sequences of four drafts over 128256 ids (fp32, with a draft's logits): 69.5 to 72 us, 43 of
+// them the rows kernel at 6.2 TB/s (0.91 of the copy rate); in the draw kernel the decisions take
 // 3 us, the search the rest.
 // Rows behind the first refused draft are summed in vain: knowing it first would take a
 // chain of kernels as long as the drafts, each too small to fill the GPU.
@@ -39,9 +39,10 @@ constexpr int VD_THREADS = 256;
 constexpr int VD_WARPS = VD_THREADS / 32;
 constexpr int VD_MOST_THREADS = 768;  // of a CTA that draws
 constexpr int VD_VECS = 4;          // 16-byte vectors of a thread in flight
-// CTAs of an SM, and CTAs for an SM that the parts aim at: 265 MB in 47 us by itself, 0.82 of the measured
-// rate (4 and 16: 48; rows left in L2 for the drawing, by loads that do not say that they
-// are the last: 74 to 77 us in all for 71).
+// CTAs of an SM, and CTAs for an SM that the parts aim at: 265 MB in 42.9 us by itself, 0.91 of the
+// measured rate (4 and 32: 45.2, 6 and 16: 43.5, 4 and 16: 43.5; rows left in L2 for the drawing, by
+// loads that do not say that they are the last: 74 to 77 us in all for 71).  With bf16 logits 40
+// registers spill 28 bytes: 64 x 4 drafts 62 us.
 constexpr int VD_CTAS = 6, VD_AIM = 32;
 constexpr int VD_RACE = 2;          // of each of a race's rows
 constexpr int VD_MAX_PARTS = 32;    // of a row: a lane each when they are added up

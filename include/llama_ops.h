@@ -254,7 +254,10 @@ llama_status llama_op_attention_paged_decode(int32_t dtype, const void *q, const
  * such value is a bf16 (seven significant bits at most), and every byte is a
  * valid code or scale.
  * A page id outside [0, n_pages) reads as a page of zeros, is not written, and
- * records LLAMA_ERR_RANGE. */
+ * records LLAMA_ERR_RANGE.
+ * What it costs: normal keys and values are off by 0.093 of their RMS (bf16: 0.0017),
+ * and attention over them by about 0.13 of its output's, more where columns of
+ * the keys differ in size. */
 
 /* Bytes of one page's rows of one KV head: page_size * (d_head / 2 + d_head / 16);
  * 0 for a page size or head width that is not supported. */
@@ -359,8 +362,10 @@ llama_status llama_op_token_logprobs(int32_t dtype, const void *logits, int64_t 
  * uniforms: fp32 [n_seqs][max_drafts], one in [0, 1) for every draft.
  * noise: fp32 [n_seqs][V], rows noise_stride elements apart (>= V): independent
  * exponential variates (-ln of a uniform); an id whose variate is not above 0 (or
- * is NaN) is never drawn.  uniforms and noise may both be NULL: every sequence is
- * then decoded greedily, whatever the temperatures. */
+ * is NaN) is never drawn.  They are the caller's to make, V for every sequence and
+ * step (33 MB for 64 sequences of 128256; rows of greedy sequences are not read).
+ * uniforms and noise may both be NULL: every sequence is then decoded greedily,
+ * whatever the temperatures. */
 #define LLAMA_MAX_DRAFTS 64
 typedef struct {
     const int32_t *q_offsets;
